@@ -9,6 +9,7 @@ missing, every call raises; there is no CPU fallback.
     C = sg.matmul(A, B)                      # FP32-accurate
     C = sg.matmul(A, B, mode=sg.MODE_TF32)   # explicit 1xTF32
     C = sg.matmul(A, B, mode="3xfp16")       # scaled FP16 pieces (bound in the C header)
+    W = sg.q4_quantize(B); C = sg.q4_matmul(A[:4].contiguous(), W)  # 4-bit weights (q4.py)
 """
 
 from __future__ import annotations
@@ -52,8 +53,21 @@ PROBE_FFMA2 = 1
 PROBE_TF32_MMA = 2
 PROBE_F16_MMA = 3
 
+# the 4-bit operators live in q4.py, which needs torch; it is loaded at the first use of one
+_Q4_NAMES = ("Q4Matrix", "MoeLayer", "q4_quantize", "q4_pack", "q4_dequantize", "q4_matmul",
+             "Q4_ZEROS", "Q4_SCALE_FP16", "MOE_MAX_TOKENS")
+
 _lock = threading.Lock()
 _lib = None
+
+
+def __getattr__(name: str):
+    if name in _Q4_NAMES:
+        from . import q4
+        for n in _Q4_NAMES:
+            globals()[n] = getattr(q4, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 class SgemmError(RuntimeError):
@@ -116,6 +130,19 @@ def lib() -> ctypes.CDLL:
             L.sgemm_tc_clock_mhz.restype = i
             L.sgemm_simt_clock_mhz.argtypes = [vp, ctypes.POINTER(ctypes.c_double)]
             L.sgemm_simt_clock_mhz.restype = i
+            ll = ctypes.c_longlong
+            L.sgemm_q4_bytes.argtypes = [vp]
+            L.sgemm_q4_bytes.restype = ll
+            L.sgemm_q4_quantize.argtypes = [vp, i, i, vp, vp]
+            L.sgemm_q4_quantize.restype = i
+            L.sgemm_q4_pack.argtypes = [vp, vp, vp, i, vp, vp]
+            L.sgemm_q4_pack.restype = i
+            L.sgemm_q4_dequantize.argtypes = [vp, vp, vp]
+            L.sgemm_q4_dequantize.restype = i
+            L.sgemm_q4_matmul.argtypes = [vp, i, ll, i, vp, vp, ll, vp]
+            L.sgemm_q4_matmul.restype = i
+            L.sgemm_moe.argtypes = [vp, vp, ll, i, vp, vp, ll, vp, vp, vp]
+            L.sgemm_moe.restype = i
             _lib = L
     return _lib
 

@@ -20,6 +20,34 @@ struct DeviceInfo {
     bool usable = false;
 };
 
+// The current device's facts, or null when it is not a usable sm_103 device (sgemm_api.cu).
+const DeviceInfo* current_device(int* dev_out);
+// The library's stream-ordered memory pool of a device, created at its first use.
+cudaError_t pool_for(int dev, cudaMemPool_t* out);
+
+// Stream-ordered scratch from the library pool, released on the same stream.
+struct Scratch {
+    void* ptr = nullptr;
+    cudaStream_t stream = nullptr;
+    cudaError_t alloc(int dev, size_t bytes, cudaStream_t s) {
+        cudaMemPool_t pool;
+        cudaError_t err = pool_for(dev, &pool);
+        if (err != cudaSuccess) return err;
+        stream = s;
+        return cudaMallocFromPoolAsync(&ptr, bytes, pool, s);
+    }
+    ~Scratch() {
+        if (ptr) cudaFreeAsync(ptr, stream);
+    }
+};
+
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+inline bool ranges_overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
+    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+    return a0 < b0 + b_bytes && b0 < a0 + a_bytes;
+}
+
 // Records the caller's timing events around the main kernel of one call.
 struct KernelTimer {
     cudaEvent_t start = nullptr;

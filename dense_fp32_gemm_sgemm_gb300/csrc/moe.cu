@@ -1,0 +1,264 @@
+// A mixture-of-experts layer for a few tokens (definition in sgemm.h): router, choice of
+// experts, gated pair of 4-bit products and the 4-bit product back, summed over a token's
+// experts.
+#include "internal.cuh"
+#include "q4.cuh"
+
+namespace sgemm {
+namespace {
+
+constexpr int kMoeMaxT = 64;
+constexpr int kMoeMaxDim = 16384;
+constexpr int kMoeMaxE = 256;
+constexpr int kMoeMaxTop = 16;
+
+constexpr int WARPS = 8;
+
+struct MoeArgs {
+    const void* x;
+    size_t ldx;
+    const void* router;
+    int router_dtype, dtype, T, D, F, E, top, renormalize;
+    const uint8_t* live;
+    int* ids;        // T x top, -1 for a token that is not live
+    float* weights;  // T x top
+    float* hidden;   // T x top x F
+    void* y;
+    size_t ldy;
+};
+
+__global__ void __launch_bounds__(WARPS * 32) moe_router_kernel(MoeArgs a) {
+    __shared__ float logit[kMoeMaxE];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int t = blockIdx.x;
+    for (int e = warp; e < a.E; e += WARPS) {
+        float s = 0.0f;
+        for (int d = lane; d < a.D; d += 32)
+            s = fmaf(load_as_float(a.x, a.dtype, t * a.ldx + d),
+                     load_as_float(a.router, a.router_dtype, size_t(e) * a.D + d), s);
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (lane == 0) logit[e] = s == s ? s : -INFINITY;
+    }
+    __syncthreads();
+    if (warp != 0) return;
+    const bool live = !a.live || a.live[t];
+    float biggest = -INFINITY;
+    for (int e = lane; e < a.E; e += 32) biggest = fmaxf(biggest, logit[e]);
+    for (int o = 16; o > 0; o >>= 1)
+        biggest = fmaxf(biggest, __shfl_xor_sync(0xffffffffu, biggest, o));
+    float sum = 0.0f;
+    uint32_t taken = 0;  // bit i: expert lane + 32 i
+    for (int e = lane; e < a.E; e += 32)
+        sum += logit[e] == biggest ? 1.0f : expf(logit[e] - biggest);
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    float chosen = 0.0f;
+    for (int j = 0; j < a.top; ++j) {
+        float best = -INFINITY;
+        int at = kMoeMaxE;
+        for (int i = 0; lane + 32 * i < a.E; ++i)
+            if (!((taken >> i) & 1) && (logit[lane + 32 * i] > best || at == kMoeMaxE)) {
+                best = logit[lane + 32 * i];
+                at = lane + 32 * i;
+            }
+        for (int o = 16; o > 0; o >>= 1) {
+            const float other = __shfl_xor_sync(0xffffffffu, best, o);
+            const int other_at = __shfl_xor_sync(0xffffffffu, at, o);
+            if (other_at < kMoeMaxE &&
+                (at == kMoeMaxE || other > best || (other == best && other_at < at))) {
+                best = other;
+                at = other_at;
+            }
+        }
+        if ((at & 31) == lane) taken |= 1u << (at >> 5);
+        chosen += best == biggest ? 1.0f : expf(best - biggest);
+    }
+    // the chosen experts in ascending order
+    int slot = 0;
+    for (int i = 0; 32 * i < a.E; ++i) {
+        const uint32_t mask = __ballot_sync(0xffffffffu, (taken >> i) & 1);
+        if ((taken >> i) & 1) {
+            const int e = lane + 32 * i;
+            const int at = t * a.top + slot + __popc(mask & ((1u << lane) - 1));
+            const float p = logit[e] == biggest ? 1.0f : expf(logit[e] - biggest);
+            a.ids[at] = live ? e : -1;
+            a.weights[at] = live ? p / (a.renormalize ? chosen : sum) : 0.0f;
+        }
+        slot += __popc(mask);
+    }
+}
+
+__device__ __forceinline__ uint4 piece_of(const void* src, int dtype, size_t at, int n, int N, int p) {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        float piece[3];
+        split_pieces<3>(n + i < N ? load_as_float(src, dtype, at + n + i) : 0.0f, piece);
+        v[i] = piece[p];
+    }
+    return make_uint4(pack_pieces(v[0], v[1]), pack_pieces(v[2], v[3]), pack_pieces(v[4], v[5]),
+                      pack_pieces(v[6], v[7]));
+}
+
+// Adds the CTA's share of strip . src[at .. at + N) to total.
+template <int GROUP>
+__device__ __forceinline__ void strip_product(const uint8_t* strip, const Q4Geom& geom,
+                                              const void* src, int dtype, size_t at, int pieces,
+                                              float (&total)[1][4]) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, c = lane & 3;
+    for (int ch = warp; ch < geom.chunks; ch += WARPS) {
+        const uint8_t* chunk = strip + size_t(ch) * geom.chunk_bytes;
+        const uint4 w0 = __ldg(reinterpret_cast<const uint4*>(chunk) + lane);
+        const uint4 w1 = __ldg(reinterpret_cast<const uint4*>(chunk + 512) + lane);
+        const uint32_t words[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+        q4_chunk<1, GROUP>(
+            words, chunk + kQ4CodeBytes, geom.zeros, geom.fp16, lane,
+            [&](int b, int) {
+                if (r >= pieces) return make_uint4(0, 0, 0, 0);
+                return piece_of(src, dtype, at, ch * kQ4ChunkN + 32 * b + 8 * c, geom.N, r);
+            },
+            total);
+    }
+}
+
+__device__ __forceinline__ void strip_product(const uint8_t* strip, const Q4Geom& geom,
+                                              const void* src, int dtype, size_t at, int pieces,
+                                              float (&total)[1][4]) {
+    if (geom.group == 32)
+        strip_product<32>(strip, geom, src, dtype, at, pieces, total);
+    else if (geom.group == 64)
+        strip_product<64>(strip, geom, src, dtype, at, pieces, total);
+    else
+        strip_product<128>(strip, geom, src, dtype, at, pieces, total);
+}
+
+__device__ __forceinline__ void put(float (&red)[8][17], const float (&total)[1][4]) {
+    const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) red[2 * c + (i & 1)][r + 8 * (i >> 1)] = total[0][i];
+}
+
+__device__ __forceinline__ float gathered(const float (&red)[WARPS][8][17], int pieces, int col) {
+    float s = 0.0f;
+    for (int w = 0; w < WARPS; ++w)
+        for (int p = 0; p < pieces; ++p) s += red[w][p][col];
+    return s;
+}
+
+__global__ void __launch_bounds__(WARPS * 32)
+    moe_hidden_kernel(MoeArgs a, const uint8_t* gate, const uint8_t* up, Q4Geom geom, int pieces) {
+    __shared__ float red[2][WARPS][8][17];
+    const int slot = blockIdx.y, t = slot / a.top, strip = blockIdx.x;
+    const int e = a.ids[slot];
+    if (e < 0) return;
+    const size_t at = e * geom.matrix_bytes() + strip * geom.strip_bytes();
+    float total[1][4] = {};
+    strip_product(gate + at, geom, a.x, a.dtype, t * a.ldx, pieces, total);
+    put(red[0][threadIdx.x >> 5], total);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) total[0][i] = 0.0f;
+    strip_product(up + at, geom, a.x, a.dtype, t * a.ldx, pieces, total);
+    put(red[1][threadIdx.x >> 5], total);
+    __syncthreads();
+    const int col = threadIdx.x, f = strip * kQ4StripK + col;
+    if (col < kQ4StripK && f < geom.K) {
+        const float g = gathered(red[0], pieces, col), u = gathered(red[1], pieces, col);
+        a.hidden[size_t(slot) * a.F + f] = g / (1.0f + expf(-g)) * u * a.weights[slot];
+    }
+}
+
+__global__ void __launch_bounds__(WARPS * 32)
+    moe_down_kernel(MoeArgs a, const uint8_t* down, Q4Geom geom, int pieces) {
+    __shared__ float red[WARPS][8][17];
+    const int t = blockIdx.y, strip = blockIdx.x;
+    float total[1][4] = {};
+    for (int j = 0; j < a.top; ++j) {
+        const int slot = t * a.top + j, e = a.ids[slot];
+        if (e < 0) continue;
+        strip_product(down + e * geom.matrix_bytes() + strip * geom.strip_bytes(), geom, a.hidden,
+                      SGEMM_FLOAT32, size_t(slot) * a.F, pieces, total);
+    }
+    put(red[threadIdx.x >> 5], total);
+    __syncthreads();
+    const int col = threadIdx.x, d = strip * kQ4StripK + col;
+    if (col < kQ4StripK && d < geom.K)
+        store_from_float(a.y, a.dtype, t * a.ldy + d, gathered(red, pieces, col));
+}
+
+bool stack_fits(const sgemm_q4& w, int E, int N, int K) {
+    return q4_valid(&w) && w.data && aligned16(w.data) && w.count == E && w.N == N && w.K == K;
+}
+
+}  // namespace
+}  // namespace sgemm
+
+using namespace sgemm;
+
+extern "C" int sgemm_moe(const sgemm_moe_layer* layer, const void* x, long long ldx, int T,
+                         const unsigned char* live, void* y, long long ldy, int* ids,
+                         float* weights, void* stream) {
+    if (!layer || !layer->router || !dtype_valid(layer->dtype) || !dtype_valid(layer->router_dtype))
+        return SGEMM_ERR_ARG;
+    const sgemm_moe_layer& m = *layer;
+    if (m.D < 1 || m.D > kMoeMaxDim || m.F < 1 || m.F > kMoeMaxDim || m.E < 1 || m.E > kMoeMaxE ||
+        m.top_k < 1 || m.top_k > kMoeMaxTop || m.top_k > m.E)
+        return SGEMM_ERR_ARG;
+    if (!stack_fits(m.gate, m.E, m.D, m.F) || !stack_fits(m.up, m.E, m.D, m.F) ||
+        !stack_fits(m.down, m.E, m.F, m.D) || m.gate.group != m.up.group ||
+        m.gate.flags != m.up.flags)
+        return SGEMM_ERR_ARG;
+    if (T < 0 || T > kMoeMaxT || ldx < m.D || ldy < m.D || ldx > (1ll << 40) || ldy > (1ll << 40))
+        return SGEMM_ERR_ARG;
+    if (T == 0) return SGEMM_OK;
+    if (!x || !y) return SGEMM_ERR_ARG;
+    const size_t size = dtype_bytes(m.dtype), side = size_t(T) * m.top_k * 4;
+    const struct { const void* p; size_t bytes; } outs[3] = {
+        {y, (size_t(T - 1) * ldy + m.D) * size}, {ids, ids ? side : 0}, {weights, weights ? side : 0}};
+    const struct { const void* p; size_t bytes; } ins[6] = {
+        {x, (size_t(T - 1) * ldx + m.D) * size},
+        {m.router, size_t(m.E) * m.D * dtype_bytes(m.router_dtype)},
+        {live, live ? size_t(T) : 0},
+        {m.gate.data, q4_bytes(m.gate)}, {m.up.data, q4_bytes(m.up)}, {m.down.data, q4_bytes(m.down)}};
+    for (int i = 0; i < 3; ++i) {
+        if (!outs[i].bytes) continue;
+        for (const auto& in : ins)
+            if (in.bytes && ranges_overlap(outs[i].p, outs[i].bytes, in.p, in.bytes))
+                return SGEMM_ERR_OVERLAP;
+        for (int j = 0; j < i; ++j)
+            if (outs[j].bytes && ranges_overlap(outs[i].p, outs[i].bytes, outs[j].p, outs[j].bytes))
+                return SGEMM_ERR_OVERLAP;
+    }
+    int dev = -1;
+    if (!current_device(&dev)) return SGEMM_ERR_NO_DEVICE;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const size_t slots = size_t(T) * m.top_k;
+    Scratch ws;
+    if (ws.alloc(dev, slots * 8 + slots * m.F * sizeof(float), s) != cudaSuccess)
+        return SGEMM_ERR_CUDA;
+    MoeArgs a;
+    a.x = x;
+    a.ldx = ldx;
+    a.router = m.router;
+    a.router_dtype = m.router_dtype;
+    a.dtype = m.dtype;
+    a.T = T;
+    a.D = m.D;
+    a.F = m.F;
+    a.E = m.E;
+    a.top = m.top_k;
+    a.renormalize = m.renormalize;
+    a.live = live;
+    a.ids = ids ? ids : static_cast<int*>(ws.ptr);
+    a.weights = weights ? weights : static_cast<float*>(ws.ptr) + slots;
+    a.hidden = static_cast<float*>(ws.ptr) + 2 * slots;
+    a.y = y;
+    a.ldy = ldy;
+    const Q4Geom g = q4_geom(m.gate), gd = q4_geom(m.down);
+    moe_router_kernel<<<T, WARPS * 32, 0, s>>>(a);
+    moe_hidden_kernel<<<dim3(g.strips, int(slots)), WARPS * 32, 0, s>>>(
+        a, static_cast<const uint8_t*>(m.gate.data), static_cast<const uint8_t*>(m.up.data), g,
+        pieces_of(m.dtype));
+    moe_down_kernel<<<dim3(gd.strips, T), WARPS * 32, 0, s>>>(
+        a, static_cast<const uint8_t*>(m.down.data), gd, m.dtype == SGEMM_FLOAT32 ? 3 : 2);
+    count_launch(3);
+    return cudaGetLastError() == cudaSuccess ? SGEMM_OK : SGEMM_ERR_CUDA;
+}

@@ -1,0 +1,198 @@
+// The packed 4-bit format and the inner product on it, shared by the packing kernels
+// (q4_pack.cu), the few-row product (q4_matmul.cu) and the expert layer (moe.cu).
+//
+// The product runs on the warp-level matrix instruction m16n8k16 with the weights as its
+// 16 x 16 operand: 16 columns of B by 16 steps of n, so that one 32-bit word of a lane
+// holds exactly its 8 codes of one instruction. With M of a few rows the bytes of B are
+// the cost (2 M operations for half a byte), and this form turns codes into operands in
+// registers, without a trip through shared or tensor memory.
+//
+// A chunk is 16 columns x 128 n. Lane l = 4 r + c of a warp works on columns r and r + 8
+// of the 16; in the 32-n block b of the chunk it multiplies n = 32 b + 8 c .. + 7, four of
+// them in each of two instructions t = 0, 1 (the n order inside an instruction is free as
+// long as both operands agree, and 8 consecutive n let a lane load its part of A as one
+// 16-byte word). Word (b, t) of a lane holds, with n0 = 32 b + 8 c + 4 t, in nibbles 0..7:
+//   q(r, n0)  q(r+8, n0)  q(r, n0+2)  q(r+8, n0+2)  q(r, n0+1)  q(r+8, n0+1)  q(r, n0+3)  q(r+8, n0+3)
+// so that nibbles j and j + 4 (one mask of the word shifted right by 4 j) are the operand's
+// register j. A chunk in memory: 2 x 512 bytes of codes (16 bytes a lane: words 0..3, then
+// 4..7), then for each of its groups 16 scales, then for each group 16 zero-point bytes if
+// any, both in the order r = 0: columns 0, 8; r = 1: columns 1, 9; ...
+// A strip is the chunks of 16 columns, n ascending; strips follow one another.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+#include "sgemm.h"
+
+namespace sgemm {
+
+constexpr int kQ4ChunkN = 128;
+constexpr int kQ4StripK = 16;
+constexpr int kQ4CodeBytes = 1024;  // codes of a chunk
+
+struct Q4Geom {
+    int N, K;
+    int chunks;       // of a strip
+    int strips;       // of a matrix
+    int group;        // 32, 64 or 128
+    int zeros;        // 1: groups have zero points
+    int fp16;         // 1: scales are float16
+    int chunk_bytes;  // codes, scales, zero points
+    __host__ __device__ size_t strip_bytes() const { return size_t(chunks) * chunk_bytes; }
+    __host__ __device__ size_t matrix_bytes() const { return strips * strip_bytes(); }
+};
+
+inline Q4Geom q4_geom(const sgemm_q4& w) {
+    Q4Geom g;
+    g.N = w.N;
+    g.K = w.K;
+    g.chunks = (w.N + kQ4ChunkN - 1) / kQ4ChunkN;
+    g.strips = (w.K + kQ4StripK - 1) / kQ4StripK;
+    g.group = w.group;
+    g.zeros = (w.flags & SGEMM_Q4_ZEROS) != 0;
+    g.fp16 = (w.flags & SGEMM_Q4_SCALE_FP16) != 0;
+    g.chunk_bytes = kQ4CodeBytes + (kQ4ChunkN / w.group) * (32 + 16 * g.zeros);
+    return g;
+}
+
+// The descriptor's limits (its data pointer is not looked at).
+inline bool q4_valid(const sgemm_q4* w) {
+    return w && w->count >= 1 && w->count <= 4096 && w->N >= 1 && w->N <= 65536 && w->K >= 1 &&
+           w->K <= (1 << 20) && (w->group == 32 || w->group == 64 || w->group == 128) &&
+           (w->flags & ~(SGEMM_Q4_ZEROS | SGEMM_Q4_SCALE_FP16)) == 0;
+}
+inline size_t q4_bytes(const sgemm_q4& w) { return size_t(w.count) * q4_geom(w).matrix_bytes(); }
+
+inline int dtype_bytes(int dtype) { return dtype == SGEMM_FLOAT32 ? 4 : 2; }
+inline bool dtype_valid(int dtype) { return dtype >= SGEMM_FLOAT32 && dtype <= SGEMM_FLOAT16; }
+
+// bfloat16 pieces that a value of this type is split into, exactly: 8 of the significant
+// bits each, of 8, 11 and 24.
+__host__ __device__ constexpr int pieces_of(int dtype) {
+    return dtype == SGEMM_FLOAT32 ? 3 : dtype == SGEMM_FLOAT16 ? 2 : 1;
+}
+
+// ---- device side -----------------------------------------------------------------------
+
+__device__ __forceinline__ float load_as_float(const void* p, int dtype, size_t i) {
+    if (dtype == SGEMM_FLOAT32) return static_cast<const float*>(p)[i];
+    if (dtype == SGEMM_BFLOAT16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+    return __half2float(static_cast<const __half*>(p)[i]);
+}
+__device__ __forceinline__ void store_from_float(void* p, int dtype, size_t i, float v) {
+    if (dtype == SGEMM_FLOAT32)
+        static_cast<float*>(p)[i] = v;
+    else if (dtype == SGEMM_BFLOAT16)
+        static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+    else
+        static_cast<__half*>(p)[i] = __float2half_rn(v);
+}
+
+// Splits x into pieces whose sum it is: each takes the leading 8 significant bits of what
+// is left by truncation, so no piece overflows and the remainder is exact. An infinity or
+// NaN is its own first piece and leaves nothing (a difference of infinities would turn it
+// into NaN).
+template <int P>
+__device__ __forceinline__ void split_pieces(float x, float (&piece)[P]) {
+    const bool finite = fabsf(x) <= 3.402823466e38f;
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+        const float hi =
+            finite ? __uint_as_float(__float_as_uint(x) & 0xffff0000u) : (p == 0 ? x : 0.0f);
+        piece[p] = hi;
+        x -= hi;
+    }
+}
+// Two such pieces (their low 16 bits are zero) as a pair of bfloat16.
+__device__ __forceinline__ uint32_t pack_pieces(float lo, float hi) {
+    return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
+}
+
+// Register j of the 16 x 16 operand: (q - z) in bfloat16 from nibbles j and j + 4 of the
+// word. 0x4300 | q is the bfloat16 128 + q; subtracting the pair 128 + z is exact.
+__device__ __forceinline__ uint32_t q4_operand(uint32_t shifted_word, uint32_t base) {
+    uint32_t v = (shifted_word & 0x000f000fu) | 0x43004300u;
+    const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v),
+                                     *reinterpret_cast<const __nv_bfloat162*>(&base));
+    return *reinterpret_cast<const uint32_t*>(&d);
+}
+
+// D (16 x 8, FP32) = A (16 x 16) . B (16 x 8) + D.
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+    asm(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7},"
+        " {%8, %9}, {%0, %1, %2, %3};\n"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// A lane's two scales (columns r and r + 8) from the pair of 16-bit values.
+__device__ __forceinline__ void q4_scales(uint32_t pair, int fp16, float& lo, float& hi) {
+    if (fp16) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&pair));
+        lo = f.x;
+        hi = f.y;
+    } else {
+        lo = __uint_as_float(pair << 16);
+        hi = __uint_as_float(pair & 0xffff0000u);
+    }
+}
+
+// One chunk of one strip times NT tiles of 8 columns of A^T (a column is a bfloat16 piece of
+// a row of A): total[nt][0..3] += columns (r, 2c), (r, 2c + 1), (r + 8, 2c), (r + 8, 2c + 1)
+// of the 16 x 8 product. words: the lane's 8 words of codes; side: the chunk's scales and
+// zero points; A(b, nt): the lane's 8 consecutive bfloat16 of 32-n block b for column
+// 8 nt + r of the tile, as a uint4. Each group is summed on its own as an integer product
+// and scaled in FP32, so no weight is rounded.
+template <int NT, int GROUP, class LoadA>
+__device__ __forceinline__ void q4_chunk(const uint32_t (&words)[8], const uint8_t* side, int zeros,
+                                         int fp16, int lane, LoadA&& A, float (&total)[NT][4]) {
+    constexpr int BLOCKS = GROUP / 32, GROUPS = kQ4ChunkN / GROUP;
+    const int r = lane >> 2;
+#pragma unroll
+    for (int g = 0; g < GROUPS; ++g) {
+        const uint32_t pair = *reinterpret_cast<const uint32_t*>(side + g * 32 + r * 4);
+        uint32_t z = 0x0808u;
+        if (zeros)
+            z = *reinterpret_cast<const uint16_t*>(side + GROUPS * 32 + g * 16 + r * 2);
+        const uint32_t base0 = 0x43004300u | (z & 0xffu) * 0x00010001u;
+        const uint32_t base1 = 0x43004300u | (z >> 8) * 0x00010001u;
+        float acc[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[nt][i] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < BLOCKS; ++k) {
+            const int b = g * BLOCKS + k;
+            uint4 x[NT];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) x[nt] = A(b, nt);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const uint32_t w = words[2 * b + t];
+                const uint32_t a[4] = {q4_operand(w, base0), q4_operand(w >> 4, base1),
+                                       q4_operand(w >> 8, base0), q4_operand(w >> 12, base1)};
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                    mma_bf16(acc[nt], a, t == 0 ? x[nt].x : x[nt].z, t == 0 ? x[nt].y : x[nt].w);
+            }
+        }
+        float s0, s1;
+        q4_scales(pair, fp16, s0, s1);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            total[nt][0] = fmaf(s0, acc[nt][0], total[nt][0]);
+            total[nt][1] = fmaf(s0, acc[nt][1], total[nt][1]);
+            total[nt][2] = fmaf(s1, acc[nt][2], total[nt][2]);
+            total[nt][3] = fmaf(s1, acc[nt][3], total[nt][3]);
+        }
+    }
+}
+
+}  // namespace sgemm

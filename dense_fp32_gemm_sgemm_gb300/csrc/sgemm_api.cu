@@ -64,6 +64,8 @@ void init_device(int dev) {
     d.usable = true;
 }
 
+}  // namespace
+
 const DeviceInfo* current_device(int* dev_out) {
     int dev = -1;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
@@ -96,28 +98,7 @@ cudaError_t pool_for(int dev, cudaMemPool_t* out) {
     return pool_err[dev];
 }
 
-// Stream-ordered scratch from the library pool, released on the same stream.
-struct Scratch {
-    void* ptr = nullptr;
-    cudaStream_t stream = nullptr;
-    cudaError_t alloc(int dev, size_t bytes, cudaStream_t s) {
-        cudaMemPool_t pool;
-        cudaError_t err = pool_for(dev, &pool);
-        if (err != cudaSuccess) return err;
-        stream = s;
-        return cudaMallocFromPoolAsync(&ptr, bytes, pool, s);
-    }
-    ~Scratch() {
-        if (ptr) cudaFreeAsync(ptr, stream);
-    }
-};
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-bool ranges_overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
-    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-    return a0 < b0 + b_bytes && b0 < a0 + a_bytes;
-}
+namespace {
 
 int check_args(const float* A, const float* B, const float* C, int M, int N, int K, int mode) {
     if (M < 1 || N < 1 || K < 1 || M > kMaxDim || N > kMaxDim || K > kMaxDim) return SGEMM_ERR_ARG;
@@ -483,7 +464,7 @@ const char* sgemm_status_string(int status) {
         case SGEMM_OK:
             return "ok";
         case SGEMM_ERR_ARG:
-            return "invalid argument (dimension outside [1, 8192], null pointer or bad mode)";
+            return "invalid argument (dimension out of range, null pointer or bad mode)";
         case SGEMM_ERR_OVERLAP:
             return "output C overlaps input A or B";
         case SGEMM_ERR_CUDA:

@@ -1698,8 +1698,6 @@ size_t round_halves(size_t n) { return (n + 127) / 128 * 128; }  // 256-byte pla
 size_t round_floats(size_t n) { return (n + 63) / 64 * 64; }  // 256-byte plane starts
 int pad4(int n) { return (n + 3) / 4 * 4; }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 // Fixed-order sum of the split parts: for each of the `split_tiles` tiles (tile index
 // full_tiles + r in grouped order), C = sum over part = 0 .. splits-1 of its block row
 // part * split_tiles + r of the partial plane (256 columns per row).

@@ -300,6 +300,145 @@ SGEMM_API int sgemm_release_pool(void);
  */
 SGEMM_API int solve_row_noalloc(const float* A, const float* B, float* C, int N, int K, void* stream);
 
+/* ==== 4-bit weights ==================================================================
+ *
+ * A packed matrix holds the N x K operand B of a product in 4 bits an element, or a
+ * stack of `count` such matrices (one for each expert of a layer, say). The n range is
+ * cut into groups of 32, 64 or 128 (the last one may be shorter); each group of each
+ * column k has a 16-bit scale s and, with SGEMM_Q4_ZEROS, a zero point z in 0 .. 15:
+ *
+ *     B[n][k] = s[n / group][k] * (q[n][k] - z[n / group][k]),   q in 0 .. 15,
+ *
+ * with z = 8 when the matrix has no zero points. Every such value is exact in FP32.
+ *
+ * sgemm_q4 describes one: `data` is a device buffer of sgemm_q4_bytes(w) bytes, 16-byte
+ * aligned, owned by the caller and written by sgemm_q4_quantize or sgemm_q4_pack. Its
+ * layout is the library's own: for every 16 columns, chunks of 128 n, each chunk its
+ * codes in the order in which the lanes of a warp multiply them, then its scales and zero
+ * points. Elements past N or K are held as zeros. The struct itself is read during the
+ * call only.
+ *
+ * 1 <= count <= 4096, 1 <= N <= 65536, 1 <= K <= 1048576, group 32, 64 or 128.
+ * The common rules at the top hold here too, with these limits in place of 8192. The
+ * finite-input rule: an infinity or NaN in A reaches the rows of C that it belongs to,
+ * as it would in FP32 arithmetic, and no others.
+ */
+typedef struct sgemm_q4 {
+    void* data;
+    int count;
+    int N;
+    int K;
+    int group;
+    int flags; /* SGEMM_Q4_* */
+} sgemm_q4;
+
+#define SGEMM_Q4_ZEROS 1      /* the groups have zero points */
+#define SGEMM_Q4_SCALE_FP16 2 /* scales are float16 (else bfloat16) */
+
+/* element types of the 4-bit entry points */
+#define SGEMM_FLOAT32 0
+#define SGEMM_BFLOAT16 1
+#define SGEMM_FLOAT16 2
+
+/* sgemm_q4_bytes - size in bytes of the packed buffer of *w (its data is ignored), or
+ * SGEMM_ERR_ARG. Host-only. */
+SGEMM_API long long sgemm_q4_bytes(const sgemm_q4* w);
+
+/*
+ * sgemm_q4_quantize - rounds B to 4 bits into w->data. B is a device array of `count`
+ * matrices one behind the other, each N x K row-major, or K x N with `transposed` (a
+ * matrix that is stored with one row for each output); `dtype` is its element type. No
+ * alignment is required. For each group, with all arithmetic in FP32 and rounding to
+ * nearest even:
+ *   without zero points: s = bf16(max|B| / 7), q = 8 + clamp(round(B / s), -8, 7);
+ *   with them: hi = max(B, 0), lo = min(B, 0), s = bf16(hi / 15 - lo / 15),
+ *              z = clamp(round(-lo / s), 0, 15), q = clamp(round(B / s) + z, 0, 15);
+ * a group whose s is zero is held as zeros. Scales are bfloat16, whose range is FP32's:
+ * SGEMM_Q4_SCALE_FP16 gives SGEMM_ERR_UNSUPPORTED. B must be finite; what a group with an
+ * infinity or NaN is held as is unspecified. B must not overlap w->data. One launch.
+ */
+SGEMM_API int sgemm_q4_quantize(const void* B, int dtype, int transposed, const sgemm_q4* w,
+                                void* stream);
+
+/*
+ * sgemm_q4_pack - lays out weights that are quantised already. codes: count x N x K bytes,
+ * of which the low four bits count; scales: count x ceil(N / group) x K, bfloat16 or, with
+ * SGEMM_Q4_SCALE_FP16, float16; zeros: the same shape in bytes, values above 15 taken as
+ * 15 (with SGEMM_Q4_ZEROS; null and unused without). With `transposed` they are
+ * count x K x N and count x K x ceil(N / group). All are device arrays. One launch.
+ */
+SGEMM_API int sgemm_q4_pack(const unsigned char* codes, const void* scales,
+                            const unsigned char* zeros, int transposed, const sgemm_q4* w,
+                            void* stream);
+
+/* sgemm_q4_dequantize - writes the values of *w as count x N x K row-major float32 to B
+ * (device), exactly. With solve_ex it serves products of many rows, where a 4-bit
+ * weight's bytes no longer are the cost. One launch. */
+SGEMM_API int sgemm_q4_dequantize(const sgemm_q4* w, float* B, void* stream);
+
+/*
+ * sgemm_q4_matmul - C[M x K] = A[M x N] . B with the 4-bit B of *w (count 1), for few rows:
+ * the cost is reading B's codes once. A and C are device arrays of element type `dtype`
+ * (SGEMM_FLOAT32, SGEMM_BFLOAT16 or SGEMM_FLOAT16), row-major with row pitches lda >= N
+ * and ldc >= K in elements. 0 <= M <= 65536; M = 0 enqueues nothing.
+ *
+ * Neither A nor the weights are rounded: A is multiplied as one, two or three bfloat16
+ * pieces (bfloat16, float16, float32) whose sum it is, the weights as the integers q - z;
+ * sums are FP32, the scales are applied to each group's sum in FP32, and C is rounded
+ * once. The order of summation depends on the sizes alone, so results are bitwise
+ * reproducible. Elements of C's rows past K are not touched. C must not overlap A or w->data.
+ */
+SGEMM_API int sgemm_q4_matmul(const void* A, int dtype, long long lda, int M, const sgemm_q4* w,
+                              void* C, long long ldc, void* stream);
+
+/* ==== mixture of experts for a few tokens ============================================
+ *
+ * A layer of E experts, each a gated pair of products: gate and up are stacks of E
+ * matrices D x F, down is a stack of E matrices F x D, all 4-bit; router is E x D,
+ * row-major, of type router_dtype, with the input's type `dtype`. The struct is read
+ * during the call only.
+ */
+typedef struct sgemm_moe_layer {
+    const void* router;
+    int router_dtype; /* SGEMM_FLOAT32, SGEMM_BFLOAT16 or SGEMM_FLOAT16 */
+    int dtype;        /* type of x and y */
+    int D;
+    int F;
+    int E;
+    int top_k;
+    int renormalize; /* nonzero: the chosen experts' weights are made to sum to one */
+    sgemm_q4 gate;
+    sgemm_q4 up;
+    sgemm_q4 down;
+} sgemm_moe_layer;
+
+/*
+ * sgemm_moe - the layer for T tokens x (T x D, row pitch ldx elements) into y (T x D, row
+ * pitch ldy):
+ *
+ *     l = router . x[t];  p = softmax(l) over the E experts;
+ *     S = the top_k experts with the largest l, the lowest index first among equals;
+ *     c_e = p_e, or p_e / sum over S of p with `renormalize`;
+ *     y[t] = sum over e in S of c_e * (silu(x[t] . gate_e) * (x[t] . up_e)) . down_e.
+ *
+ * live (T bytes, or null for all): a token whose byte is zero picks no expert, so that no
+ * weights are read for it; its row of y is zeros. ids (T x top_k, int) and weights
+ * (T x top_k, float) may be null; they get each token's experts in ascending order and
+ * their c_e, and -1 and 0 for a token that is not live. A NaN logit counts as the
+ * smallest value, so that ids stay in range.
+ *
+ * 0 <= T <= 64 (T = 0 enqueues nothing), 1 <= D, F <= 16384, 1 <= E <= 256,
+ * 1 <= top_k <= min(E, 16); gate and up have the same group and flags. Arithmetic as for
+ * sgemm_q4_matmul; the hidden values are kept in FP32 and multiplied as two bfloat16
+ * pieces (16 significant bits), three for float32 inputs (all 24). Results are bitwise
+ * reproducible. Every expert that some live token picked is read once, the others not at
+ * all. y, ids and weights must not overlap the inputs or each other. Workspace comes from
+ * the library's pool; the call can be captured into a CUDA graph.
+ */
+SGEMM_API int sgemm_moe(const sgemm_moe_layer* layer, const void* x, long long ldx, int T,
+                        const unsigned char* live, void* y, long long ldy, int* ids,
+                        float* weights, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
