@@ -103,15 +103,12 @@ __device__ __forceinline__ uint4 piece_of(const void* src, int dtype, size_t at,
 template <int GROUP>
 __device__ __forceinline__ void strip_product(const uint8_t* strip, const Q4Geom& geom,
                                               const void* src, int dtype, size_t at, int pieces,
-                                              float (&total)[1][4]) {
+                                              float (&total)[1][1][4]) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, c = lane & 3;
     for (int ch = warp; ch < geom.chunks; ch += WARPS) {
         const uint8_t* chunk = strip + size_t(ch) * geom.chunk_bytes;
-        const uint4 w0 = __ldg(reinterpret_cast<const uint4*>(chunk) + lane);
-        const uint4 w1 = __ldg(reinterpret_cast<const uint4*>(chunk + 512) + lane);
-        const uint32_t words[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-        q4_chunk<1, GROUP>(
-            words, chunk + kQ4CodeBytes, geom.zeros, geom.fp16, lane,
+        q4_chunk<1, 1, GROUP>(
+            [&](int) { return chunk; }, geom.zeros, geom.fp16, lane,
             [&](int b, int) {
                 if (r >= pieces) return make_uint4(0, 0, 0, 0);
                 return piece_of(src, dtype, at, ch * kQ4ChunkN + 32 * b + 8 * c, geom.N, r);
@@ -122,7 +119,7 @@ __device__ __forceinline__ void strip_product(const uint8_t* strip, const Q4Geom
 
 __device__ __forceinline__ void strip_product(const uint8_t* strip, const Q4Geom& geom,
                                               const void* src, int dtype, size_t at, int pieces,
-                                              float (&total)[1][4]) {
+                                              float (&total)[1][1][4]) {
     if (geom.group == 32)
         strip_product<32>(strip, geom, src, dtype, at, pieces, total);
     else if (geom.group == 64)
@@ -131,10 +128,10 @@ __device__ __forceinline__ void strip_product(const uint8_t* strip, const Q4Geom
         strip_product<128>(strip, geom, src, dtype, at, pieces, total);
 }
 
-__device__ __forceinline__ void put(float (&red)[8][17], const float (&total)[1][4]) {
+__device__ __forceinline__ void put(float (&red)[8][17], const float (&total)[1][1][4]) {
     const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) red[2 * c + (i & 1)][r + 8 * (i >> 1)] = total[0][i];
+    for (int i = 0; i < 4; ++i) red[2 * c + (i & 1)][r + 8 * (i >> 1)] = total[0][0][i];
 }
 
 __device__ __forceinline__ float gathered(const float (&red)[WARPS][8][17], int pieces, int col) {
@@ -151,11 +148,11 @@ __global__ void __launch_bounds__(WARPS * 32)
     const int e = a.ids[slot];
     if (e < 0) return;
     const size_t at = e * geom.matrix_bytes() + strip * geom.strip_bytes();
-    float total[1][4] = {};
+    float total[1][1][4] = {};
     strip_product(gate + at, geom, a.x, a.dtype, t * a.ldx, pieces, total);
     put(red[0][threadIdx.x >> 5], total);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) total[0][i] = 0.0f;
+    for (int i = 0; i < 4; ++i) total[0][0][i] = 0.0f;
     strip_product(up + at, geom, a.x, a.dtype, t * a.ldx, pieces, total);
     put(red[1][threadIdx.x >> 5], total);
     __syncthreads();
@@ -170,7 +167,7 @@ __global__ void __launch_bounds__(WARPS * 32)
     moe_down_kernel(MoeArgs a, const uint8_t* down, Q4Geom geom, int pieces) {
     __shared__ float red[WARPS][8][17];
     const int t = blockIdx.y, strip = blockIdx.x;
-    float total[1][4] = {};
+    float total[1][1][4] = {};
     for (int j = 0; j < a.top; ++j) {
         const int slot = t * a.top + j, e = a.ids[slot];
         if (e < 0) continue;

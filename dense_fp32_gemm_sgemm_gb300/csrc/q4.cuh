@@ -26,6 +26,7 @@
 #include <cstddef>
 #include <cstdint>
 
+#include "ptx.cuh"
 #include "sgemm.h"
 
 namespace sgemm {
@@ -143,56 +144,129 @@ __device__ __forceinline__ void q4_scales(uint32_t pair, int fp16, float& lo, fl
     }
 }
 
-// One chunk of one strip times NT tiles of 8 columns of A^T (a column is a bfloat16 piece of
-// a row of A): total[nt][0..3] += columns (r, 2c), (r, 2c + 1), (r + 8, 2c), (r + 8, 2c + 1)
-// of the 16 x 8 product. words: the lane's 8 words of codes; side: the chunk's scales and
-// zero points; A(b, nt): the lane's 8 consecutive bfloat16 of 32-n block b for column
-// 8 nt + r of the tile, as a uint4. Each group is summed on its own as an integer product
-// and scaled in FP32, so no weight is rounded.
-template <int NT, int GROUP, class LoadA>
-__device__ __forceinline__ void q4_chunk(const uint32_t (&words)[8], const uint8_t* side, int zeros,
-                                         int fp16, int lane, LoadA&& A, float (&total)[NT][4]) {
+// One chunk of MT strips times NT tiles of 8 columns of A^T (a column is a bfloat16 piece of
+// a row of A): total[m][nt][0..3] += columns (r, 2c), (r, 2c + 1), (r + 8, 2c), (r + 8, 2c + 1)
+// of the 16 x 8 products. chunk(m): the chunk of strip m in shared memory; A(b, nt): the
+// lane's 8 consecutive bfloat16 of 32-n block b for column 8 nt + r, as a uint4. Each group
+// is summed on its own as an integer product and scaled in FP32, so no weight is rounded.
+template <int MT, int NT, int GROUP, class Chunk, class LoadA>
+__device__ __forceinline__ void q4_chunk(Chunk&& chunk, int zeros, int fp16, int lane, LoadA&& A,
+                                         float (&total)[MT][NT][4]) {
     constexpr int BLOCKS = GROUP / 32, GROUPS = kQ4ChunkN / GROUP;
     const int r = lane >> 2;
+    uint4 word[MT];  // of half a chunk: blocks 2 h and 2 h + 1, two instructions each
 #pragma unroll
     for (int g = 0; g < GROUPS; ++g) {
-        const uint32_t pair = *reinterpret_cast<const uint32_t*>(side + g * 32 + r * 4);
-        uint32_t z = 0x0808u;
-        if (zeros)
-            z = *reinterpret_cast<const uint16_t*>(side + GROUPS * 32 + g * 16 + r * 2);
-        const uint32_t base0 = 0x43004300u | (z & 0xffu) * 0x00010001u;
-        const uint32_t base1 = 0x43004300u | (z >> 8) * 0x00010001u;
-        float acc[NT][4];
+        uint32_t base0[MT], base1[MT], pair[MT];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int m = 0; m < MT; ++m) {
+            const uint8_t* side = chunk(m) + kQ4CodeBytes;
+            pair[m] = *reinterpret_cast<const uint32_t*>(side + g * 32 + r * 4);
+            uint32_t z = 0x0808u;
+            if (zeros) z = *reinterpret_cast<const uint16_t*>(side + GROUPS * 32 + g * 16 + r * 2);
+            base0[m] = 0x43004300u | (z & 0xffu) * 0x00010001u;
+            base1[m] = 0x43004300u | (z >> 8) * 0x00010001u;
+        }
+        float acc[MT][NT][4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[nt][i] = 0.0f;
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[m][nt][i] = 0.0f;
 #pragma unroll
         for (int k = 0; k < BLOCKS; ++k) {
             const int b = g * BLOCKS + k;
+            if (b % 2 == 0) {
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+                    word[m] = reinterpret_cast<const uint4*>(chunk(m) + (b / 2) * 512)[lane];
+            }
             uint4 x[NT];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) x[nt] = A(b, nt);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                const uint32_t w = words[2 * b + t];
-                const uint32_t a[4] = {q4_operand(w, base0), q4_operand(w >> 4, base1),
-                                       q4_operand(w >> 8, base0), q4_operand(w >> 12, base1)};
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    mma_bf16(acc[nt], a, t == 0 ? x[nt].x : x[nt].z, t == 0 ? x[nt].y : x[nt].w);
+                for (int m = 0; m < MT; ++m) {
+                    const uint32_t w = b % 2 == 0 ? (t == 0 ? word[m].x : word[m].y)
+                                                  : (t == 0 ? word[m].z : word[m].w);
+                    const uint32_t a[4] = {q4_operand(w, base0[m]), q4_operand(w >> 4, base1[m]),
+                                           q4_operand(w >> 8, base0[m]),
+                                           q4_operand(w >> 12, base1[m])};
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        mma_bf16(acc[m][nt], a, t == 0 ? x[nt].x : x[nt].z,
+                                 t == 0 ? x[nt].y : x[nt].w);
+                }
             }
         }
-        float s0, s1;
-        q4_scales(pair, fp16, s0, s1);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            total[nt][0] = fmaf(s0, acc[nt][0], total[nt][0]);
-            total[nt][1] = fmaf(s0, acc[nt][1], total[nt][1]);
-            total[nt][2] = fmaf(s1, acc[nt][2], total[nt][2]);
-            total[nt][3] = fmaf(s1, acc[nt][3], total[nt][3]);
+        for (int m = 0; m < MT; ++m) {
+            float s0, s1;
+            q4_scales(pair[m], fp16, s0, s1);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                total[m][nt][0] = fmaf(s0, acc[m][nt][0], total[m][nt][0]);
+                total[m][nt][1] = fmaf(s0, acc[m][nt][1], total[m][nt][1]);
+                total[m][nt][2] = fmaf(s1, acc[m][nt][2], total[m][nt][2]);
+                total[m][nt][3] = fmaf(s1, acc[m][nt][3], total[m][nt][3]);
+            }
         }
     }
+}
+
+// Copies a chunk (chunk_bytes: a multiple of 16, at most kQ4MaxChunk) of each of MT strips to
+// a warp's stage in shared memory, asynchronously: 16 bytes a lane and step.
+constexpr int kQ4MaxChunk = kQ4CodeBytes + 4 * 48;
+template <int MT>
+__device__ __forceinline__ void q4_fetch(uint32_t stage, const uint8_t* const (&src)[MT],
+                                         int chunk_bytes, int lane) {
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+        const uint32_t dst = stage + m * kQ4MaxChunk + lane * 16;
+        const uint8_t* from = src[m] + lane * 16;
+        ptx::cp_async_16(dst, from, true);
+        ptx::cp_async_16(dst + 512, from + 512, true);
+        if (kQ4CodeBytes + lane * 16 < chunk_bytes) ptx::cp_async_16(dst + 1024, from + 1024, true);
+    }
+}
+
+// The lane's 8 consecutive values src[at + n .. + 8) as P pieces, zeros from N on. vec: rows
+// start on 16-byte boundaries (and n is a multiple of 8).
+template <int P, class T>
+__device__ __forceinline__ void load_split8(const T* row, int n, int N, bool vec,
+                                            uint4 (&out)[P]) {
+    float v[8];
+    if (vec && n + 8 <= N) {
+        if constexpr (sizeof(T) == 4) {
+            const float4 a = *reinterpret_cast<const float4*>(row + n);
+            const float4 b = *reinterpret_cast<const float4*>(row + n + 4);
+            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+        } else {
+            const uint4 a = *reinterpret_cast<const uint4*>(row + n);
+            if constexpr (P == 1) {
+                out[0] = a;
+                return;
+            }
+            const T* e = reinterpret_cast<const T*>(&a);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = float(e[i]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = n + i < N ? float(row[n + i]) : 0.0f;
+    }
+    float piece[8][P];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) split_pieces<P>(v[i], piece[i]);
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+        out[p] = make_uint4(pack_pieces(piece[0][p], piece[1][p]),
+                            pack_pieces(piece[2][p], piece[3][p]),
+                            pack_pieces(piece[4][p], piece[5][p]),
+                            pack_pieces(piece[6][p], piece[7][p]));
 }
 
 }  // namespace sgemm

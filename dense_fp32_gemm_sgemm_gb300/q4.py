@@ -62,20 +62,27 @@ def _rows(t, name: str, cols: int) -> int:
     return pitch if rows > 1 else max(pitch, cols)
 
 
-def _launch(fn, what, tensors, device, stream, *args):
+# The current stream's handle and the current device without the public calls' wrapping,
+# which costs a small product's call as much as its launch.
+_current_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _launch(fn, what, tensors, index, stream, *args):
     """Calls a library function with a stream as its last argument, on the tensors' device.
     Tensors used on a stream other than the current one are marked as in use there."""
     if stream is None:
-        handle = torch.cuda.current_stream(device).cuda_stream
+        handle = _current_handle(index)
     else:
         handle = stream.cuda_stream
         for t in tensors:
             if t is not None:
                 t.record_stream(stream)
-    if device.index == torch.cuda.current_device():
+    if index == _current_device():
         rc = fn(*args, handle)
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(index):
             rc = fn(*args, handle)
     if rc != OK:
         raise SgemmError(rc, what)
@@ -98,6 +105,7 @@ class Q4Matrix:
             raise SgemmError(int(size), f"4-bit matrix {count} x {N} x {K}, group {group}")
         self.data = torch.empty(size, dtype=torch.uint8, device=device)
         self.device = self.data.device
+        self.index = self.device.index
         self._c.data = self.data.data_ptr()
 
     @property
@@ -129,7 +137,7 @@ def q4_quantize(B, group: int = 128, zeros: bool = False, transposed: bool = Fal
     _cuda_tensor(B, "B")
     code = _dtype_code(B, "B")
     W = _packed_for(B, "B", group, zeros, False, transposed)
-    _launch(lib().sgemm_q4_quantize, "sgemm_q4_quantize", (B, W.data), B.device, stream,
+    _launch(lib().sgemm_q4_quantize, "sgemm_q4_quantize", (B, W.data), W.index, stream,
             B.data_ptr(), code, int(transposed), W._ref)
     return W
 
@@ -155,7 +163,7 @@ def q4_pack(codes, scales, zeros=None, group: int = 128, transposed: bool = Fals
                 t.device != codes.device:
             raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)} and type "
                              f"{' or '.join(map(str, kinds))} on {codes.device}")
-    _launch(lib().sgemm_q4_pack, "sgemm_q4_pack", (codes, scales, zeros, W.data), codes.device,
+    _launch(lib().sgemm_q4_pack, "sgemm_q4_pack", (codes, scales, zeros, W.data), W.index,
             stream, codes.data_ptr(), scales.data_ptr(),
             None if zeros is None else zeros.data_ptr(), int(transposed), W._ref)
     return W
@@ -173,7 +181,7 @@ def q4_dequantize(W: Q4Matrix, out=None, stream=None):
                 or out.device != W.device:
             raise ValueError(f"out must be a contiguous float32 tensor of shape {W.shape} on "
                              f"{W.device}")
-    _launch(lib().sgemm_q4_dequantize, "sgemm_q4_dequantize", (W.data, out), W.device, stream,
+    _launch(lib().sgemm_q4_dequantize, "sgemm_q4_dequantize", (W.data, out), W.index, stream,
             W._ref, out.data_ptr())
     return out
 
@@ -199,7 +207,7 @@ def q4_matmul(A, W: Q4Matrix, out=None, stream=None):
         if out.dtype != A.dtype or out.shape[0] != M or out.device != A.device:
             raise ValueError(f"out must be {M} x {W.K} of type {A.dtype} on {A.device}")
         ldc = _rows(out, "out", W.K)
-    _launch(lib().sgemm_q4_matmul, "sgemm_q4_matmul", (A, W.data, out), A.device, stream,
+    _launch(lib().sgemm_q4_matmul, "sgemm_q4_matmul", (A, W.data, out), W.index, stream,
             A.data_ptr(), code, lda, M, W._ref, out.data_ptr(), ldc)
     return out
 
@@ -238,6 +246,7 @@ class MoeLayer:
         if self.dtype not in _DTYPES:
             raise ValueError(f"dtype must be float32, bfloat16 or float16, not {self.dtype}")
         self.E, self.D, self.F, self.device = E, D, F, router.device
+        self.index = self.device.index
         self._c = _Moe(router.data_ptr(), _dtype_code(router, "router"), _DTYPES[self.dtype], D, F,
                        E, self.top_k, int(self.renormalize), gate._c, up._c, down._c)
         self._ref = ctypes.byref(self._c)
@@ -267,7 +276,7 @@ class MoeLayer:
         weights = torch.empty((T, self.top_k), dtype=torch.float32, device=x.device)
         _launch(lib().sgemm_moe, "sgemm_moe",
                 (x, live, out, ids, weights, self.router, self.gate.data, self.up.data,
-                 self.down.data), x.device, stream, self._ref, x.data_ptr(), ldx, T,
+                 self.down.data), self.index, stream, self._ref, x.data_ptr(), ldx, T,
                 None if live is None else live.data_ptr(), out.data_ptr(), ldy, ids.data_ptr(),
                 weights.data_ptr())
         return out, ids, weights
