@@ -107,13 +107,22 @@ __device__ __forceinline__ void strip_product(const uint8_t* strip, const Q4Geom
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, c = lane & 3;
     for (int ch = warp; ch < geom.chunks; ch += WARPS) {
         const uint8_t* chunk = strip + size_t(ch) * geom.chunk_bytes;
-        q4_chunk<1, 1, GROUP>(
-            [&](int) { return chunk; }, geom.zeros, geom.fp16, lane,
-            [&](int b, int) {
-                if (r >= pieces) return make_uint4(0, 0, 0, 0);
-                return piece_of(src, dtype, at, ch * kQ4ChunkN + 32 * b + 8 * c, geom.N, r);
-            },
-            total);
+        __shared__ uint4 xw[WARPS][4][32];  // [block][lane]
+        for (int b = 0; b < 4; ++b)
+            xw[threadIdx.x >> 5][b][lane] =
+                r < pieces ? piece_of(src, dtype, at, ch * kQ4ChunkN + 32 * b + 8 * c, geom.N, r)
+                           : make_uint4(0, 0, 0, 0);
+        __syncwarp();
+        // blocks of a lane's column are 64 bytes apart there, 512 here
+        __shared__ uint4 xc[WARPS][8][16];
+        for (int b = 0; b < 4; ++b) xc[threadIdx.x >> 5][r][4 * b + c] = xw[threadIdx.x >> 5][b][lane];
+        __syncwarp();
+        const uint8_t* x = reinterpret_cast<const uint8_t*>(&xc[threadIdx.x >> 5][r][c]);
+        if (geom.zeros)
+            q4_chunk_centred<GROUP, true>(chunk, x, geom.fp16, lane, total[0][0]);
+        else
+            q4_chunk_centred<GROUP, false>(chunk, x, geom.fp16, lane, total[0][0]);
+        __syncwarp();
     }
 }
 

@@ -68,7 +68,7 @@ inline bool q4_valid(const sgemm_q4* w) {
 }
 inline size_t q4_bytes(const sgemm_q4& w) { return size_t(w.count) * q4_geom(w).matrix_bytes(); }
 
-inline int dtype_bytes(int dtype) { return dtype == SGEMM_FLOAT32 ? 4 : 2; }
+__host__ __device__ constexpr int dtype_bytes(int dtype) { return dtype == SGEMM_FLOAT32 ? 4 : 2; }
 inline bool dtype_valid(int dtype) { return dtype >= SGEMM_FLOAT32 && dtype <= SGEMM_FLOAT16; }
 
 // bfloat16 pieces that a value of this type is split into, exactly: 8 of the significant
@@ -113,10 +113,40 @@ __device__ __forceinline__ uint32_t pack_pieces(float lo, float hi) {
     return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
 }
 
-// Register j of the 16 x 16 operand: (q - z) in bfloat16 from nibbles j and j + 4 of the
-// word. 0x4300 | q is the bfloat16 128 + q; subtracting the pair 128 + z is exact.
-__device__ __forceinline__ uint32_t q4_operand(uint32_t shifted_word, uint32_t base) {
-    uint32_t v = (shifted_word & 0x000f000fu) | 0x43004300u;
+// Two forms of the weight operand, register j from nibbles j and j + 4 of a word:
+//
+//  * Plain (five instructions for eight weights). The bfloat16 with the bit pattern of an
+//    integer I in 0 .. 255 is I * 2^-133 exactly: its subnormals and its first binade lie on
+//    one line, and the matrix instruction takes subnormal operands as they are. So one mask
+//    makes an operand: q from the low nibble of each half of the word, 16 q from the next
+//    one (columns r + 8, whose sums are scaled by 1/16 afterwards), and one shift by 8 gives
+//    the other two. The columns of A^T are staged times 2^96 to bring the products back into
+//    FP32's range, and a group's sum is (sum of q x) - z (sum of x), the second sum taken
+//    once when the columns are staged.
+//  * Centred (eleven): 0x4300 | q is the bfloat16 128 + q, and subtracting 128 + z leaves
+//    q - z. Works for every x; taken where a staged value is an infinity, a NaN or outside
+//    [2^-64, 2^24), where the scaled product could leave FP32's range.
+constexpr float kQ4Low = 0x1p-64f, kQ4High = 0x1p24f;
+constexpr float kQ4Scale = 0x1p96f;
+constexpr float kQ4Unscale = 0x1p37f;      // 2^133 / 2^96
+constexpr float kQ4Unscale16 = 0x1p33f;    // and of 16 q
+
+// Whether x must be multiplied in the centred form.
+__device__ __forceinline__ bool q4_special(float x) {
+    const float a = fabsf(x);
+    return !(a < kQ4High) || (a < kQ4Low && a != 0.0f);
+}
+
+// 0x000f000f in a register that the compiler does not see through: with two constants it
+// would split the and-or of the centred form into two instructions.
+__device__ __forceinline__ uint32_t q4_mask() {
+    uint32_t m;
+    asm("mov.b32 %0, 0x000f000f;" : "=r"(m));
+    return m;
+}
+__device__ __forceinline__ uint32_t q4_centred(uint32_t shifted_word, uint32_t mask, uint32_t base) {
+    uint32_t v;
+    asm("lop3.b32 %0, %1, %2, 0x43004300, 0xea;" : "=r"(v) : "r"(shifted_word), "r"(mask));
     const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v),
                                      *reinterpret_cast<const __nv_bfloat162*>(&base));
     return *reinterpret_cast<const uint32_t*>(&d);
@@ -130,6 +160,15 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
         " {%8, %9}, {%0, %1, %2, %3};\n"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// D (16 x 8, FP32) = A (16 x 16) . B (16 x 8).
+__device__ __forceinline__ void mma_bf16_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                               uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7},"
+        " {%8, %9}, {%10, %10, %10, %10};\n"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
 // A lane's two scales (columns r and r + 8) from the pair of 16-bit values.
@@ -147,33 +186,28 @@ __device__ __forceinline__ void q4_scales(uint32_t pair, int fp16, float& lo, fl
 // One chunk of MT strips times NT tiles of 8 columns of A^T (a column is a bfloat16 piece of
 // a row of A): total[m][nt][0..3] += columns (r, 2c), (r, 2c + 1), (r + 8, 2c), (r + 8, 2c + 1)
 // of the 16 x 8 products. chunk(m): the chunk of strip m in shared memory; A(b, nt): the
-// lane's 8 consecutive bfloat16 of 32-n block b for column 8 nt + r, as a uint4. Each group
-// is summed on its own as an integer product and scaled in FP32, so no weight is rounded.
-template <int MT, int NT, int GROUP, class Chunk, class LoadA>
-__device__ __forceinline__ void q4_chunk(Chunk&& chunk, int zeros, int fp16, int lane, LoadA&& A,
+// lane's 8 consecutive bfloat16 of 32-n block b for column 8 nt + r, as a uint4; in the plain
+// form scaled, and sum(g, nt) the pair of -(sum of x) over group g of the chunk for columns
+// 8 nt + 2 c and + 1, times 8 without zero points. Each group's product is a sum of integers
+// times x, and its scale is applied in FP32, so no weight is rounded.
+template <int MT, int NT, int GROUP, bool ZEROS, class Chunk, class LoadA, class Sum>
+__device__ __forceinline__ void q4_chunk(Chunk&& chunk, int fp16, int lane, LoadA&& A, Sum&& sum,
                                          float (&total)[MT][NT][4]) {
     constexpr int BLOCKS = GROUP / 32, GROUPS = kQ4ChunkN / GROUP;
     const int r = lane >> 2;
     uint4 word[MT];  // of half a chunk: blocks 2 h and 2 h + 1, two instructions each
 #pragma unroll
     for (int g = 0; g < GROUPS; ++g) {
-        uint32_t base0[MT], base1[MT], pair[MT];
+        uint32_t pair[MT], zero[MT];
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
             const uint8_t* side = chunk(m) + kQ4CodeBytes;
             pair[m] = *reinterpret_cast<const uint32_t*>(side + g * 32 + r * 4);
-            uint32_t z = 0x0808u;
-            if (zeros) z = *reinterpret_cast<const uint16_t*>(side + GROUPS * 32 + g * 16 + r * 2);
-            base0[m] = 0x43004300u | (z & 0xffu) * 0x00010001u;
-            base1[m] = 0x43004300u | (z >> 8) * 0x00010001u;
+            zero[m] = 0;
+            if constexpr (ZEROS)
+                zero[m] = *reinterpret_cast<const uint16_t*>(side + GROUPS * 32 + g * 16 + r * 2);
         }
         float acc[MT][NT][4];
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[m][nt][i] = 0.0f;
 #pragma unroll
         for (int k = 0; k < BLOCKS; ++k) {
             const int b = g * BLOCKS + k;
@@ -191,14 +225,34 @@ __device__ __forceinline__ void q4_chunk(Chunk&& chunk, int zeros, int fp16, int
                 for (int m = 0; m < MT; ++m) {
                     const uint32_t w = b % 2 == 0 ? (t == 0 ? word[m].x : word[m].y)
                                                   : (t == 0 ? word[m].z : word[m].w);
-                    const uint32_t a[4] = {q4_operand(w, base0[m]), q4_operand(w >> 4, base1[m]),
-                                           q4_operand(w >> 8, base0[m]),
-                                           q4_operand(w >> 12, base1[m])};
+                    const uint32_t a[4] = {w & 0x000f000fu, w & 0x00f000f0u,
+                                           (w >> 8) & 0x000f000fu, (w >> 8) & 0x00f000f0u};
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        mma_bf16(acc[m][nt], a, t == 0 ? x[nt].x : x[nt].z,
-                                 t == 0 ? x[nt].y : x[nt].w);
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const uint32_t b0 = t == 0 ? x[nt].x : x[nt].z;
+                        const uint32_t b1 = t == 0 ? x[nt].y : x[nt].w;
+                        if (k == 0 && t == 0)
+                            mma_bf16_first(acc[m][nt], a, b0, b1);
+                        else
+                            mma_bf16(acc[m][nt], a, b0, b1);
+                    }
                 }
+            }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const float2 xs = sum(g, nt);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                float z0 = 1.0f, z1 = 1.0f;
+                if constexpr (ZEROS) {  // 0x4300 | z is the upper half of the float 128 + z
+                    z0 = __uint_as_float(__byte_perm(zero[m], 0x43u, 0x4055)) - 128.0f;
+                    z1 = __uint_as_float(__byte_perm(zero[m], 0x43u, 0x4155)) - 128.0f;
+                }
+                acc[m][nt][0] = fmaf(acc[m][nt][0], kQ4Unscale, z0 * xs.x);
+                acc[m][nt][1] = fmaf(acc[m][nt][1], kQ4Unscale, z0 * xs.y);
+                acc[m][nt][2] = fmaf(acc[m][nt][2], kQ4Unscale16, z1 * xs.x);
+                acc[m][nt][3] = fmaf(acc[m][nt][3], kQ4Unscale16, z1 * xs.y);
             }
         }
 #pragma unroll
@@ -216,57 +270,108 @@ __device__ __forceinline__ void q4_chunk(Chunk&& chunk, int zeros, int fp16, int
     }
 }
 
-// Copies a chunk (chunk_bytes: a multiple of 16, at most kQ4MaxChunk) of each of MT strips to
-// a warp's stage in shared memory, asynchronously: 16 bytes a lane and step.
-constexpr int kQ4MaxChunk = kQ4CodeBytes + 4 * 48;
-template <int MT>
-__device__ __forceinline__ void q4_fetch(uint32_t stage, const uint8_t* const (&src)[MT],
-                                         int chunk_bytes, int lane) {
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        const uint32_t dst = stage + m * kQ4MaxChunk + lane * 16;
-        const uint8_t* from = src[m] + lane * 16;
-        ptx::cp_async_16(dst, from, true);
-        ptx::cp_async_16(dst + 512, from + 512, true);
-        if (kQ4CodeBytes + lane * 16 < chunk_bytes) ptx::cp_async_16(dst + 1024, from + 1024, true);
+// One chunk of one strip times a tile of 8 columns in the centred form, added to total. x: the
+// lane's word of block 0 of its column, as it is; a block is 64 bytes. Rarely run, so kept
+// small rather than unrolled.
+template <int GROUP, bool ZEROS>
+__device__ __forceinline__ void q4_chunk_centred(const uint8_t* chunk, const uint8_t* x, int fp16,
+                                                 int lane, float (&total)[4]) {
+    constexpr int BLOCKS = GROUP / 32, GROUPS = kQ4ChunkN / GROUP;
+    const int r = lane >> 2;
+    const uint32_t mask = q4_mask();
+    const uint8_t* side = chunk + kQ4CodeBytes;
+#pragma unroll 1
+    for (int g = 0; g < GROUPS; ++g) {
+        uint32_t z = 0x0808u;
+        if constexpr (ZEROS)
+            z = *reinterpret_cast<const uint16_t*>(side + GROUPS * 32 + g * 16 + r * 2);
+        const uint32_t base0 = __byte_perm(z, 0x43u, 0x4040), base1 = __byte_perm(z, 0x43u, 0x4141);
+        float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+        for (int i = 0; i < 2 * BLOCKS; ++i) {
+            const int b = g * BLOCKS + i / 2;
+            const uint32_t w = *reinterpret_cast<const uint32_t*>(chunk + (b / 2) * 512 + lane * 16 +
+                                                                  (b & 1) * 8 + (i & 1) * 4);
+            const uint2 xb = *reinterpret_cast<const uint2*>(x + b * 64 + (i & 1) * 8);
+            const uint32_t a[4] = {q4_centred(w, mask, base0), q4_centred(w >> 4, mask, base1),
+                                   q4_centred(w >> 8, mask, base0),
+                                   q4_centred(w >> 12, mask, base1)};
+            mma_bf16(acc, a, xb.x, xb.y);
+        }
+        float s0, s1;
+        q4_scales(reinterpret_cast<const uint32_t*>(side + g * 32)[r], fp16, s0, s1);
+        total[0] = fmaf(s0, acc[0], total[0]);
+        total[1] = fmaf(s0, acc[1], total[1]);
+        total[2] = fmaf(s1, acc[2], total[2]);
+        total[3] = fmaf(s1, acc[3], total[3]);
     }
 }
 
-// The lane's 8 consecutive values src[at + n .. + 8) as P pieces, zeros from N on. vec: rows
-// start on 16-byte boundaries (and n is a multiple of 8).
-template <int P, class T>
-__device__ __forceinline__ void load_split8(const T* row, int n, int N, bool vec,
-                                            uint4 (&out)[P]) {
-    float v[8];
+// Copies `bytes` (a multiple of 16, at most kQ4MaxChunk) of a chunk to shared memory,
+// asynchronously: 16 bytes a lane and step.
+constexpr int kQ4MaxChunk = kQ4CodeBytes + 4 * 48;
+__device__ __forceinline__ void q4_fetch(uint32_t dst, const uint8_t* src, bool tail) {
+    ptx::cp_async_16(dst, src, true);
+    ptx::cp_async_16(dst + 512, src + 512, true);
+    if (tail) ptx::cp_async_16(dst + 1024, src + 1024, true);
+}
+
+// 8 consecutive values of a row as they lie in memory.
+template <class T>
+struct Raw8 {
+    uint4 v[sizeof(T) / 2];
+};
+// row[n .. n + 8), zeros from N on. vec: rows start on 16-byte boundaries (n is a multiple
+// of 8).
+template <class T>
+__device__ __forceinline__ Raw8<T> load_raw8(const T* row, int n, int N, bool vec) {
+    Raw8<T> raw;
     if (vec && n + 8 <= N) {
-        if constexpr (sizeof(T) == 4) {
-            const float4 a = *reinterpret_cast<const float4*>(row + n);
-            const float4 b = *reinterpret_cast<const float4*>(row + n + 4);
-            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-        } else {
-            const uint4 a = *reinterpret_cast<const uint4*>(row + n);
-            if constexpr (P == 1) {
-                out[0] = a;
-                return;
-            }
-            const T* e = reinterpret_cast<const T*>(&a);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = float(e[i]);
-        }
+        for (int i = 0; i < int(sizeof(T) / 2); ++i)
+            raw.v[i] = reinterpret_cast<const uint4*>(row + n)[i];
     } else {
+        T e[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = n + i < N ? float(row[n + i]) : 0.0f;
+        for (int i = 0; i < 8; ++i) e[i] = n + i < N ? row[n + i] : T(0.0f);
+        raw = *reinterpret_cast<const Raw8<T>*>(e);
     }
+    return raw;
+}
+// The P pieces of 8 values, times `scale` (a power of two); sets `special` where the plain
+// form cannot take one of them.
+template <int P, class T>
+__device__ __forceinline__ void split_raw8(const Raw8<T>& raw, float scale, bool& special,
+                                           uint4 (&out)[P]) {
+    const T* e = reinterpret_cast<const T*>(&raw);
     float piece[8][P];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) split_pieces<P>(v[i], piece[i]);
+    for (int i = 0; i < 8; ++i) {
+        const float x = float(e[i]);
+        special |= q4_special(x);
+        split_pieces<P>(x, piece[i]);
+#pragma unroll
+        for (int p = 0; p < P; ++p) piece[i][p] *= scale;
+    }
 #pragma unroll
     for (int p = 0; p < P; ++p)
         out[p] = make_uint4(pack_pieces(piece[0][p], piece[1][p]),
                             pack_pieces(piece[2][p], piece[3][p]),
                             pack_pieces(piece[4][p], piece[5][p]),
                             pack_pieces(piece[6][p], piece[7][p]));
+}
+// The sum of 32 staged values (4 words), added pairwise along a fixed order.
+__device__ __forceinline__ float sum_staged32(const uint4* words) {
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint4 w = words[i];
+        const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            s += __uint_as_float(v[j] << 16) + __uint_as_float(v[j] & 0xffff0000u);
+    }
+    return s;
 }
 
 }  // namespace sgemm

@@ -16,20 +16,29 @@
 namespace sgemm {
 namespace {
 
-constexpr int WARPS = 8;
-constexpr int THREADS = WARPS * 32;
-constexpr int DEPTH = 6;         // stages of a warp's ring
-constexpr int SMEM_LIMIT = 227 * 1024;
-constexpr int SMEM_HALF = 113 * 1024;  // two CTAs on an SM
+constexpr int SMEM_LIMIT = 227 * 1024;  // of a CTA
+constexpr int SMEM_SM = 228 * 1024;     // of an SM; 1 KB of each CTA's share is the system's
+
+// Warps of a CTA: 8, or 16 where the columns of one CTA leave no room for a second.
+template <int NT>
+constexpr int max_warps() { return NT == 1 ? 8 : 16; }
+
+template <int NT>
+constexpr int min_blocks() { return NT == 1 ? 2 : 1; }
+
+// Stages of a warp's ring: with 16 warps on an SM about 70 KB are in flight, twice what
+// covers HBM's latency at its full rate.
+template <int MT>
+constexpr int depth() { return 4; }
 
 struct Plan {
-    int cluster;       // CTAs that split n
-    int wn;            // warps of a CTA that split n
-    int chunks;        // of a CTA's n range
-    int window;        // chunks whose columns are staged at a time (a multiple of wn, or all)
-    int groups;        // of WARPS / wn * MT strips
-    int clusters;      // launched
-    int staged;        // columns that a CTA stages
+    int warps;    // of a CTA
+    int cluster;  // CTAs that split n
+    int wn;       // warps of a CTA that split n
+    int chunks;   // of a CTA's n range
+    int groups;   // of warps / wn * MT strips
+    int clusters; // launched
+    int staged;   // columns that a CTA stages
     int smem;
 };
 
@@ -42,111 +51,214 @@ struct Args {
     void* C;
     size_t ldc;
     Plan plan;
-    bool vec;          // rows of A start on 16-byte boundaries
+    bool vec;  // rows of A start on 16-byte boundaries
 };
 
 // Bytes of a column of `chunks` chunks in shared memory: 64 bytes more than a multiple of
 // 256, so that the 8 lanes of a 16-byte load phase (4 words of two columns) meet no bank twice.
 __host__ __device__ constexpr int column_pitch(int chunks) { return chunks * kQ4ChunkN * 2 + 64; }
-// Floats of a CTA's part of a group's sums when a cluster shares it: [row][column of C].
-__host__ __device__ constexpr int part_floats(int mt, int nt) {
-    return WARPS * mt * kQ4StripK * nt * 8;
-}
 // Floats of the sums of one group: [wn][strip][column][16], a column's 16 padded to 17.
-__host__ __device__ constexpr int red_floats(int mt, int nt) { return WARPS * mt * nt * 8 * 17; }
+__host__ __device__ constexpr int red_floats(int warps, int mt, int columns) {
+    return warps * mt * columns * 17;
+}
+// Floats of the staged columns' sums over each group of n.
+__host__ __device__ constexpr int xsum_floats(int chunks, int group, int nt) {
+    return chunks * (kQ4ChunkN / group) * nt * 8;
+}
+// Floats of a CTA's part of a group's sums when a cluster shares it: [row][column of C].
+__host__ __device__ constexpr int part_floats(int warps, int mt, int columns) {
+    return warps * mt * kQ4StripK * columns;
+}
 
-template <int MT, int NT, int GROUP>
-__global__ void __launch_bounds__(THREADS, 2) q4_matmul_kernel(const Args args) {
+// What a CTA stages of the columns: rows of A from row0 on, n from n0 on, `units` of 8 values.
+struct Staging {
+    const void* A;
+    size_t lda;
+    int dtype, rows, n0, N, units, threads, pitch;
+    bool vec;
+    uint8_t* xs;
+};
+
+// Writes the pieces of the rows, times scale, to their columns; true where the plain form
+// cannot take one of the thread's values.
+template <int P, class T>
+__device__ __noinline__ bool stage_rows(const Staging& s, float scale) {
+    constexpr int AHEAD = 4;  // loads in flight
+    const T* A = static_cast<const T*>(s.A);
+    const int items = s.units * s.rows, threads = s.threads;
+    int row = 0, u = threadIdx.x;
+    bool special = false;
+    for (int i = threadIdx.x; i < items; i += AHEAD * threads) {
+        Raw8<T> raw[AHEAD];
+        int at[AHEAD];
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) {
+            at[j] = -1;
+            if (i + j * threads < items) {
+                while (u >= s.units) {
+                    u -= s.units;
+                    ++row;
+                }
+                at[j] = row * P * s.pitch + u * 16;
+                raw[j] = load_raw8(A + row * s.lda, s.n0 + u * 8, s.N, s.vec);
+                u += threads;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j)
+            if (at[j] >= 0) {
+                uint4 piece[P];
+                split_raw8<P>(raw[j], scale, special, piece);
+#pragma unroll
+                for (int p = 0; p < P; ++p)
+                    *reinterpret_cast<uint4*>(s.xs + at[j] + p * s.pitch) = piece[p];
+            }
+    }
+    return special;
+}
+
+__device__ __forceinline__ bool stage_any(const Staging& s, float scale) {
+    if (s.dtype == SGEMM_BFLOAT16) return stage_rows<1, __nv_bfloat16>(s, scale);
+    if (s.dtype == SGEMM_FLOAT16) return stage_rows<2, __half>(s, scale);
+    return stage_rows<3, float>(s, scale);
+}
+
+// Stages the columns, scaled for the plain form, and factor times their sums over each group
+// of 32 << log_blocks n at xsum[group][column] (sum_pitch floats a group); true where the plain
+// form cannot take one of the values, and then the columns are staged as they are.
+__device__ __noinline__ bool stage_columns(const Staging& s, int columns, int log_blocks, float factor,
+                                           float* xsum, int sum_pitch) {
+    if (__syncthreads_or(stage_any(s, kQ4Scale))) {
+        stage_any(s, 1.0f);
+        __syncthreads();
+        return true;
+    }
+    // a thread sums 32 n; the 1, 2 or 4 threads of a group are neighbours in a warp
+    const int blocks = s.units / 4;  // a multiple of 4
+    int col = 0, block = threadIdx.x;
+    for (int i = threadIdx.x; i < (blocks * columns + 31) / 32 * 32; i += s.threads) {
+        while (block >= blocks) {
+            block -= blocks;
+            ++col;
+        }
+        float v = 0.0f;
+        if (col < columns)
+            v = sum_staged32(reinterpret_cast<const uint4*>(s.xs + col * s.pitch + block * 64));
+        for (int o = 0; o < log_blocks; ++o) v += __shfl_xor_sync(0xffffffffu, v, 1 << o);
+        if (col < columns && (block & ((1 << log_blocks) - 1)) == 0)
+            xsum[(block >> log_blocks) * sum_pitch + col] = v * factor;
+        block += s.threads;
+    }
+    __syncthreads();
+    return false;
+}
+
+// Where a CTA's shared memory holds what, in bytes; `columns`: those that it stages.
+struct Offsets {
+    int ring, red, xsum, part, end;
+};
+__host__ __device__ constexpr Offsets offsets(int warps, int mt, int depth, int chunk_bytes,
+                                              int columns, int chunks, int group, int nt,
+                                              bool cluster) {
+    Offsets o{};
+    o.ring = columns * column_pitch(chunks);
+    o.red = o.ring + warps * depth * mt * chunk_bytes;
+    o.xsum = o.red + 2 * red_floats(warps, mt, columns) * 4;
+    o.part = o.xsum + xsum_floats(chunks, group, nt) * 4;
+    o.end = o.part + (cluster ? 2 * part_floats(warps, mt, columns) * 4 : 0);
+    return o;
+}
+
+template <int MT, int NT, int GROUP, bool ZEROS>
+__global__ void __launch_bounds__(max_warps<NT>() * 32, min_blocks<NT>())
+    q4_matmul_kernel(const Args args) {
     extern __shared__ __align__(128) uint8_t smem[];
-    constexpr int STAGE = MT * kQ4MaxChunk;
+    constexpr int DEPTH = depth<MT>();
     const Plan& plan = args.plan;
     const Q4Geom& geom = args.geom;
+    const int threads = plan.warps * 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int r = lane >> 2, c = lane & 3;
-    const int wn = warp % plan.wn, wm = warp / plan.wn;
-    const int strips_per_group = WARPS / plan.wn * MT;
+    const int wn = warp & (plan.wn - 1), wm = warp / plan.wn;
+    const int strips_per_group = plan.warps / plan.wn * MT;  // a power of two
     const int rank = plan.cluster > 1 ? int(ptx::cluster_ctarank()) : 0;
     const int first_group = blockIdx.x / plan.cluster;
     const int chunk0 = rank * plan.chunks;
     const int chunks = max(0, min(plan.chunks, geom.chunks - chunk0));
-    // this launch row's share of the rows of A
     const int pieces = args.pieces, most_rows = NT * 8 / pieces;
     const int row0 = blockIdx.y * most_rows;
     const int rows = min(most_rows, args.M - row0), columns = rows * pieces;
 
-    const int pitch = column_pitch(plan.window);
+    const int pitch = column_pitch(plan.chunks);
+    const int chunk_bytes = geom.chunk_bytes, stage_bytes = MT * chunk_bytes;
     uint8_t* xs = smem;
-    uint8_t* ring = xs + plan.staged * pitch + warp * DEPTH * STAGE;
-    float* red = reinterpret_cast<float*>(xs + plan.staged * pitch + WARPS * DEPTH * STAGE);
-    float* part = red + 2 * red_floats(MT, NT);  // only with a cluster
-    const uint32_t ring_u32 = ptx::smem_u32(ring);
+    const Offsets at = offsets(plan.warps, MT, DEPTH, chunk_bytes, plan.staged, plan.chunks, GROUP,
+                               NT, plan.cluster > 1);
+    uint8_t* ring = smem + at.ring + warp * DEPTH * stage_bytes;
+    float* red = reinterpret_cast<float*>(smem + at.red);
+    float* xsum = reinterpret_cast<float*>(smem + at.xsum);  // [group of n][column]
+    float* part = reinterpret_cast<float*>(smem + at.part);  // only with a cluster
 
-    // the warp's sequence: for each of the CTA's groups, chunks wn, wn + WN, ... of the range
-    int fetch_group = first_group, fetch_chunk = wn;
-    auto fetch = [&](int stage) {
-        if (fetch_group < plan.groups && wn < chunks) {
-            const uint8_t* src[MT];
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                // past the last strip: the last one again, its sums are not used
-                const int strip =
-                    min(fetch_group * strips_per_group + wm * MT + m, geom.strips - 1);
-                src[m] = args.data + strip * geom.strip_bytes() +
-                         size_t(chunk0 + fetch_chunk) * geom.chunk_bytes;
-            }
-            q4_fetch<MT>(ring_u32 + stage * STAGE, src, geom.chunk_bytes, lane);
-            fetch_chunk += plan.wn;
-            if (fetch_chunk >= chunks) {
-                fetch_chunk = wn;
-                fetch_group += plan.clusters;
+    // The warp's sequence: for each of the CTA's groups, chunks wn, wn + WN, ... of the range.
+    // Strips past the last one are not fetched; what is computed for them is not used.
+    const int my_chunks = wn < chunks ? (chunks - wn + plan.wn - 1) / plan.wn : 0;
+    const bool tail = kQ4CodeBytes + lane * 16 < chunk_bytes;
+    const uint32_t step = plan.wn * chunk_bytes;
+    const int strip_step = plan.clusters * strips_per_group;
+    const size_t wrap = size_t(strip_step) * geom.strip_bytes() - size_t(my_chunks) * step;
+    int fetch_strip = my_chunks > 0 ? first_group * strips_per_group + wm * MT : geom.strips;
+    const uint8_t* fetch_from = args.data + size_t(fetch_strip) * geom.strip_bytes() +
+                                size_t(chunk0 + wn) * chunk_bytes + lane * 16;
+    int fetch_left = my_chunks;
+    uint32_t fetch_to = ptx::smem_u32(ring) + lane * 16;
+    const uint32_t fetch_end = fetch_to + DEPTH * stage_bytes;
+    auto fetch = [&]() {
+        if (fetch_strip < geom.strips) {
+            q4_fetch(fetch_to, fetch_from, tail);
+            if (MT == 2 && fetch_strip + 1 < geom.strips)
+                q4_fetch(fetch_to + chunk_bytes, fetch_from + geom.strip_bytes(), tail);
+            fetch_from += step;
+            if (--fetch_left == 0) {
+                fetch_left = my_chunks;
+                fetch_from += wrap;
+                fetch_strip += strip_step;
             }
         }
         ptx::cp_async_commit();
+        fetch_to += stage_bytes;
+        if (fetch_to == fetch_end) fetch_to -= DEPTH * stage_bytes;
     };
 #pragma unroll
-    for (int i = 0; i < DEPTH - 1; ++i) fetch(i);
+    for (int i = 0; i < DEPTH - 1; ++i) fetch();
 
-    auto stage_columns = [&](int from) {
-        const int units = min(plan.window, chunks - from) * (kQ4ChunkN / 8);
-        const int n0 = (chunk0 + from) * kQ4ChunkN;
-        for (int i = threadIdx.x; i < units * rows; i += THREADS) {
-            const int row = i / units, u = i - row * units;
-            const size_t at = (row0 + row) * args.lda;
-            uint8_t* dst = xs + row * pieces * pitch + u * 16;
-            if (args.dtype == SGEMM_BFLOAT16) {
-                uint4 piece[1];
-                load_split8<1>(static_cast<const __nv_bfloat16*>(args.A) + at, n0 + u * 8, geom.N,
-                               args.vec, piece);
-                *reinterpret_cast<uint4*>(dst) = piece[0];
-            } else if (args.dtype == SGEMM_FLOAT16) {
-                uint4 piece[2];
-                load_split8<2>(static_cast<const __half*>(args.A) + at, n0 + u * 8, geom.N,
-                               args.vec, piece);
-                *reinterpret_cast<uint4*>(dst) = piece[0];
-                *reinterpret_cast<uint4*>(dst + pitch) = piece[1];
-            } else {
-                uint4 piece[3];
-                load_split8<3>(static_cast<const float*>(args.A) + at, n0 + u * 8, geom.N, args.vec,
-                               piece);
+    Staging st;
+    st.A = static_cast<const uint8_t*>(args.A) + row0 * args.lda * dtype_bytes(args.dtype);
+    st.lda = args.lda;
+    st.dtype = args.dtype;
+    st.rows = rows;
+    st.n0 = chunk0 * kQ4ChunkN;
+    st.N = geom.N;
+    st.units = chunks * (kQ4ChunkN / 8);
+    st.threads = threads;
+    st.pitch = pitch;
+    st.vec = args.vec;
+    st.xs = xs;
+    const bool special = stage_columns(st, columns, GROUP == 32 ? 0 : GROUP == 64 ? 1 : 2,
+                                       (ZEROS ? -1.0f : -8.0f) / kQ4Scale, xsum, NT * 8);
+
+    // a lane's words of column 8 nt + r in the warp's first chunk; columns that do not exist
+    // repeat the last one, and their sums are not used
+    uint32_t xcol[NT];
 #pragma unroll
-                for (int p = 0; p < 3; ++p)
-                    *reinterpret_cast<uint4*>(dst + p * pitch) = piece[p];
-            }
-        }
-    };
-    const bool whole = plan.window >= plan.chunks;
-    if (whole) {
-        stage_columns(0);
-        __syncthreads();
-    }
+    for (int nt = 0; nt < NT; ++nt)
+        xcol[nt] = min(nt * 8 + r, columns - 1) * pitch + c * 16 + wn * (kQ4ChunkN * 2);
+    const float* sums0 = xsum + wn * (kQ4ChunkN / GROUP) * (NT * 8) + 2 * c;
 
-    // a lane's words of column 8 nt + r; columns that do not exist repeat the last one, and
-    // their sums are not used
-    const uint8_t* xcol[NT];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) xcol[nt] = xs + min(nt * 8 + r, columns - 1) * pitch + c * 16;
-
-    int stage = 0, buffer = 0;
+    const uint8_t* stage = ring;
+    const uint8_t* const ring_end = ring + DEPTH * stage_bytes;
+    const int width_log = __ffs(strips_per_group * kQ4StripK) - 1;
+    const int cells = rows << width_log;
+    int buffer = 0;
     for (int group = first_group; group < plan.groups; group += plan.clusters) {
         float total[MT][NT][4];
 #pragma unroll
@@ -155,68 +267,92 @@ __global__ void __launch_bounds__(THREADS, 2) q4_matmul_kernel(const Args args) 
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) total[m][nt][i] = 0.0f;
-        for (int from = 0; from < chunks; from += plan.window) {
-            if (!whole) {
-                __syncthreads();
-                stage_columns(from);
-                __syncthreads();
-            }
-            const int to = min(chunks, from + plan.window);
-            for (int ch = from + wn; ch < to; ch += plan.wn) {
+        const uint8_t* x = xs;
+        const float* sums = sums0;
+        auto next = [&]() {
+            x += plan.wn * (kQ4ChunkN * 2);
+            sums += plan.wn * (kQ4ChunkN / GROUP) * (NT * 8);
+            stage += stage_bytes;
+            if (stage == ring_end) stage = ring;
+        };
+        if (special) {
+#pragma unroll 1
+            for (int i = 0; i < my_chunks; ++i, next()) {
                 ptx::cp_async_wait<DEPTH - 2>();
                 __syncwarp();
-                fetch(stage == 0 ? DEPTH - 1 : stage - 1);
-                const uint8_t* codes = ring + stage * STAGE;
-                const int x_at = (ch - from) * kQ4ChunkN * 2;
-                q4_chunk<MT, NT, GROUP>(
-                    [&](int m) { return codes + m * kQ4MaxChunk; }, geom.zeros, geom.fp16, lane,
+                fetch();
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        q4_chunk_centred<GROUP, ZEROS>(stage + m * chunk_bytes, x + xcol[nt],
+                                                       geom.fp16, lane, total[m][nt]);
+            }
+        } else {
+#pragma unroll 1
+            for (int i = 0; i < my_chunks; ++i, next()) {
+                ptx::cp_async_wait<DEPTH - 2>();
+                __syncwarp();
+                fetch();
+                q4_chunk<MT, NT, GROUP, ZEROS>(
+                    [&](int m) { return stage + m * chunk_bytes; }, geom.fp16, lane,
                     [&](int b, int nt) {
-                        return *reinterpret_cast<const uint4*>(xcol[nt] + x_at + b * 64);
+                        return *reinterpret_cast<const uint4*>(x + xcol[nt] + b * 64);
+                    },
+                    [&](int g, int nt) {
+                        return *reinterpret_cast<const float2*>(sums + g * (NT * 8) + nt * 8);
                     },
                     total);
-                stage = stage == DEPTH - 1 ? 0 : stage + 1;
             }
         }
-        // sums over the warps that split n, in their order
-        float* mine = red + buffer * red_floats(MT, NT) + (wn * strips_per_group + wm * MT) * NT * 8 * 17;
+        // Sums over the warps that split n, in their order. Two buffers in turn: a warp is
+        // back at one of them only after the barrier that follows the other's use.
+        float* reds = red + buffer * red_floats(plan.warps, MT, plan.staged);
+        float* mine = reds + (wn * strips_per_group + wm * MT) * columns * 17 + r;
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int i = 0; i < 2; ++i) {
+                const int col = nt * 8 + 2 * c + i;
+                if (col >= columns) continue;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    mine[((m * NT + nt) * 8 + 2 * c + (i & 1)) * 17 + r + 8 * (i >> 1)] =
-                        total[m][nt][i];
-        __syncthreads();
-        const float* sums = red + buffer * red_floats(MT, NT);
-        const int width = strips_per_group * kQ4StripK, cells = width * rows;
-        const int k0 = group * width;
-        for (int i = threadIdx.x; i < cells; i += THREADS) {
-            const int row = i / width, col = i - row * width;
-            const float* at = sums + ((col / kQ4StripK) * NT * 8 + row * pieces) * 17 + col % kQ4StripK;
-            float s = 0.0f;
-            for (int w = 0; w < plan.wn; ++w) {
-                for (int p = 0; p < pieces; ++p) s += at[p * 17];
-                at += strips_per_group * NT * 8 * 17;
+                for (int m = 0; m < MT; ++m) {
+                    mine[(m * columns + col) * 17] = total[m][nt][i];
+                    mine[(m * columns + col) * 17 + 8] = total[m][nt][i + 2];
+                }
             }
+        __syncthreads();
+        const int k0 = group << width_log;
+        const int wn_stride = strips_per_group * columns * 17;
+        float* shared_sums = part + buffer * part_floats(plan.warps, MT, plan.staged);
+        auto put = [&](int i, float v) {
+            const int row = i >> width_log, k = k0 + i - (row << width_log);
+            if (k < geom.K) store_from_float(args.C, args.dtype, (row0 + row) * args.ldc + k, v);
+        };
+        for (int i = threadIdx.x; i < cells; i += threads) {
+            const int row = i >> width_log, col = i - (row << width_log);
+            const float* from =
+                reds + ((col / kQ4StripK) * columns + row * pieces) * 17 + col % kQ4StripK;
+            float s = 0.0f;
+            for (int p = 0; p < pieces; ++p, from += 17)
+#pragma unroll 8
+                for (int w = 0; w < plan.wn; ++w) s += from[w * wn_stride];
             if (plan.cluster > 1)
-                part[buffer * part_floats(MT, NT) + i] = s;
-            else if (k0 + col < geom.K)
-                store_from_float(args.C, args.dtype, (row0 + row) * args.ldc + k0 + col, s);
+                shared_sums[i] = s;
+            else
+                put(i, s);
         }
         if (plan.cluster > 1) {
             ptx::cluster_sync();
             // each CTA adds the ranges' sums of its share of the cells, in rank order
             const int share = (cells + plan.cluster - 1) / plan.cluster;
-            const uint32_t base =
-                ptx::smem_u32(part + buffer * part_floats(MT, NT));
+            const uint32_t base = ptx::smem_u32(shared_sums);
             for (int i = rank * share + threadIdx.x; i < min(cells, (rank + 1) * share);
-                 i += THREADS) {
+                 i += threads) {
                 float s = 0.0f;
                 for (int q = 0; q < plan.cluster; ++q)
                     s += ptx::ld_shared_cluster_f32(ptx::mapa_shared(base + i * 4, q));
-                const int row = i / width, col = i - row * width;
-                if (k0 + col < geom.K) store_from_float(args.C, args.dtype, (row0 + row) * args.ldc + k0 + col, s);
+                put(i, s);
             }
         }
         buffer ^= 1;
@@ -226,60 +362,91 @@ __global__ void __launch_bounds__(THREADS, 2) q4_matmul_kernel(const Args args) 
     if (plan.cluster > 1) ptx::cluster_sync();
 }
 
-// The split of an N x K product with this many columns on sm_count SMs, for kernels with MT
-// and NT: the cluster size and warp split whose slowest SM is done first. A chunk costs an
-// SM about 45 cycles at the HBM rate; exchanging sums some hundreds a group.
-Plan make_plan(const Q4Geom& g, int columns, int mt, int nt, int sm_count, double* cost_out) {
+constexpr double kNoPlan = 1e30;
+
+// Clusters of this size that the device holds at once, `resident` CTAs an SM.
+template <auto KERNEL>
+int resident_clusters(int cluster, int resident, int threads, int sm_count) {
+    if (cluster == 1) return sm_count * resident;
+    constexpr int kDevices = 64;
+    static std::atomic<int> known[kDevices][3][3];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) dev = 0;
+    std::atomic<int>& slot = known[dev][cluster == 2 ? 0 : cluster == 4 ? 1 : 2][resident - 1];
+    int n = slot.load(std::memory_order_relaxed);
+    if (n > 0) return n;
+    cudaLaunchConfig_t config = {};
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = cluster;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    config.gridDim = dim3(sm_count / cluster * cluster * resident);
+    config.blockDim = dim3(threads);
+    config.dynamicSmemBytes = resident == 1 ? SMEM_LIMIT : SMEM_SM / resident - 1024;
+    config.attrs = &attr;
+    config.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, KERNEL, &config) != cudaSuccess || n < 1) {
+        cudaGetLastError();
+        n = sm_count * resident / cluster;
+        if (n < 1) n = 1;
+    }
+    slot.store(n, std::memory_order_relaxed);
+    return n;
+}
+
+// The split of an N x K product with this many columns: the warps, cluster size and warp split
+// whose slowest SM is done first.
+template <int MT, int NT, int GROUP, bool ZEROS>
+Plan make_plan(const Q4Geom& g, int columns, int sm_count, double* cost_out) {
+    constexpr int DEPTH = depth<MT>();
     Plan best{};
-    double best_cost = 1e30;
-    for (int cluster = 1; cluster <= 4; cluster *= 2) {
-        if (cluster > 1 && g.chunks < 2 * cluster) break;
-        for (int wn = WARPS; wn >= 1; wn /= 2) {
-            Plan p;
-            p.cluster = cluster;
-            p.wn = wn;
-            p.chunks = (g.chunks + cluster - 1) / cluster;
-            if (wn > 1 && wn > p.chunks) continue;
-            const int fixed = WARPS * DEPTH * mt * kQ4MaxChunk + 2 * red_floats(mt, nt) * 4 +
-                              (cluster > 1 ? 2 * part_floats(mt, nt) * 4 : 0);
-            p.staged = columns;
-            p.window = p.chunks;
-            int smem = fixed + columns * column_pitch(p.window);
-            if (smem > SMEM_LIMIT) {
-                p.window = ((SMEM_LIMIT - fixed) / columns - 64) / (kQ4ChunkN * 2) / wn * wn;
-                if (p.window < wn) continue;
-                smem = fixed + columns * column_pitch(p.window);
-            }
-            p.smem = smem;
-            const int resident = smem <= SMEM_HALF ? 2 : 1;
-            const int strips = WARPS / wn * mt;
-            p.groups = (g.strips + strips - 1) / strips;
-            const int slots = sm_count * resident / cluster;
-            p.clusters = p.groups < slots ? p.groups : slots;
-            const int rounds = (p.groups + p.clusters - 1) / p.clusters;
-            const int units = (p.chunks + wn - 1) / wn * mt;  // of a warp and group
-            const int busy = (p.clusters * cluster + sm_count - 1) / sm_count;
-            const double windows = double((p.chunks + p.window - 1) / p.window);
-            const double cost = rounds * (busy * WARPS * units * 45.0 + 300.0 +
-                                          (cluster > 1 ? 400.0 : 0.0) +
-                                          (windows > 1 ? windows * 1500.0 : 0.0));
-            if (cost < best_cost) {
-                best_cost = cost;
-                best = p;
+    double best_cost = kNoPlan;
+    for (int warps = 8; warps <= max_warps<NT>(); warps *= 2)
+        for (int cluster = 1; cluster <= 8; cluster *= 2) {
+            if (cluster > 1 && g.chunks < 2 * cluster) break;
+            for (int wn = warps; wn >= 1; wn /= 2) {
+                Plan p;
+                p.warps = warps;
+                p.cluster = cluster;
+                p.wn = wn;
+                p.chunks = (g.chunks + cluster - 1) / cluster;
+                if (wn > 1 && wn > p.chunks) continue;
+                p.staged = columns;
+                p.smem = offsets(warps, MT, DEPTH, g.chunk_bytes, columns, p.chunks, GROUP, NT,
+                                 cluster > 1)
+                             .end;
+                if (p.smem > SMEM_LIMIT) continue;
+                int resident = 1;
+                while (resident < (16 / warps) &&
+                       (p.smem + 1024) * (resident + 1) <= SMEM_SM)
+                    ++resident;
+                const int strips = warps / wn * MT;
+                p.groups = (g.strips + strips - 1) / strips;
+                const int slots = resident_clusters<q4_matmul_kernel<MT, NT, GROUP, ZEROS>>(
+                    cluster, resident, warps * 32, sm_count);
+                p.clusters = p.groups < slots ? p.groups : slots;
+                const int rounds = (p.groups + p.clusters - 1) / p.clusters;
+                const int units = (p.chunks + wn - 1) / wn * MT;  // of a warp and group
+                const int busy = (p.clusters * cluster + sm_count - 1) / sm_count;
+                const double chunk_cost = busy * warps >= 24 ? 42.0 : busy * warps > 8 ? 45.0 : 70.0;
+                const double stage = busy * 3.0 * columns * p.chunks + 1500.0;
+                const double cost = stage + rounds * (busy * warps * units * chunk_cost + 400.0 +
+                                              (cluster > 1 ? 500.0 : 0.0));
+                if (cost < best_cost) {
+                    best_cost = cost;
+                    best = p;
+                }
             }
         }
-    }
     *cost_out = best_cost;
     return best;
 }
 
-template <int MT, int NT, int GROUP>
+template <int MT, int NT, int GROUP, bool ZEROS>
 cudaError_t launch_kernel(const Args& args, int launch_rows, cudaStream_t stream) {
-    const cudaError_t err = set_smem_limit_once<q4_matmul_kernel<MT, NT, GROUP>>(SMEM_LIMIT);
-    if (err != cudaSuccess) return err;
     cudaLaunchConfig_t config = {};
     config.gridDim = dim3(args.plan.clusters * args.plan.cluster, launch_rows);
-    config.blockDim = dim3(THREADS);
+    config.blockDim = dim3(args.plan.warps * 32);
     config.dynamicSmemBytes = args.plan.smem;
     config.stream = stream;
     cudaLaunchAttribute attr;
@@ -290,26 +457,36 @@ cudaError_t launch_kernel(const Args& args, int launch_rows, cudaStream_t stream
     config.attrs = &attr;
     config.numAttrs = args.plan.cluster > 1 ? 1 : 0;
     count_launch();
-    return cudaLaunchKernelEx(&config, q4_matmul_kernel<MT, NT, GROUP>, args);
+    return cudaLaunchKernelEx(&config, q4_matmul_kernel<MT, NT, GROUP, ZEROS>, args);
 }
 
-template <int NT>
-cudaError_t launch(Args args, int sm_count, cudaStream_t stream) {
+template <int NT, int GROUP, bool ZEROS>
+cudaError_t launch_group(Args args, int sm_count, cudaStream_t stream) {
+    cudaError_t err = set_smem_limit_once<q4_matmul_kernel<1, NT, GROUP, ZEROS>>(SMEM_LIMIT);
+    if (err == cudaSuccess)
+        err = set_smem_limit_once<q4_matmul_kernel<2, NT, GROUP, ZEROS>>(SMEM_LIMIT);
+    if (err != cudaSuccess) return err;
     const int most_rows = NT * 8 / args.pieces;
     const int launch_rows = (args.M + most_rows - 1) / most_rows;
     const int columns = (args.M < most_rows ? args.M : most_rows) * args.pieces;
     double one, two;
-    const Plan p1 = make_plan(args.geom, columns, 1, NT, sm_count, &one);
-    const Plan p2 = make_plan(args.geom, columns, 2, NT, sm_count, &two);
-    const bool pair = two <= one;
-    args.plan = pair ? p2 : p1;
-    switch (args.geom.group * 2 + (pair ? 1 : 0)) {
-        case 64: return launch_kernel<1, NT, 32>(args, launch_rows, stream);
-        case 65: return launch_kernel<2, NT, 32>(args, launch_rows, stream);
-        case 128: return launch_kernel<1, NT, 64>(args, launch_rows, stream);
-        case 129: return launch_kernel<2, NT, 64>(args, launch_rows, stream);
-        case 256: return launch_kernel<1, NT, 128>(args, launch_rows, stream);
-        default: return launch_kernel<2, NT, 128>(args, launch_rows, stream);
+    args.plan = make_plan<1, NT, GROUP, ZEROS>(args.geom, columns, sm_count, &one);
+    const Plan pair = make_plan<2, NT, GROUP, ZEROS>(args.geom, columns, sm_count, &two);
+    if (one >= kNoPlan && two >= kNoPlan) return cudaErrorInvalidConfiguration;
+    if (one < two) return launch_kernel<1, NT, GROUP, ZEROS>(args, launch_rows, stream);
+    args.plan = pair;
+    return launch_kernel<2, NT, GROUP, ZEROS>(args, launch_rows, stream);
+}
+
+template <int NT>
+cudaError_t launch(const Args& args, int sm_count, cudaStream_t stream) {
+    switch (args.geom.group + args.geom.zeros) {
+        case 32: return launch_group<NT, 32, false>(args, sm_count, stream);
+        case 33: return launch_group<NT, 32, true>(args, sm_count, stream);
+        case 64: return launch_group<NT, 64, false>(args, sm_count, stream);
+        case 65: return launch_group<NT, 64, true>(args, sm_count, stream);
+        case 128: return launch_group<NT, 128, false>(args, sm_count, stream);
+        default: return launch_group<NT, 128, true>(args, sm_count, stream);
     }
 }
 
@@ -347,9 +524,11 @@ extern "C" int sgemm_q4_matmul(const void* A, int dtype, long long lda, int M, c
     args.ldc = size_t(ldc);
     args.vec = aligned16(A) && size_t(lda) * size % 16 == 0;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    // few enough columns at a time that a cluster's shared memory holds them (8 always fit)
     const int columns = M * args.pieces;
-    const cudaError_t err = columns <= 8    ? launch<1>(args, info->sm_count, s)
-                            : columns <= 16 ? launch<2>(args, info->sm_count, s)
-                                            : launch<4>(args, info->sm_count, s);
+    cudaError_t err = cudaErrorInvalidConfiguration;
+    if (columns > 16) err = launch<4>(args, info->sm_count, s);
+    if (columns > 8 && err == cudaErrorInvalidConfiguration) err = launch<2>(args, info->sm_count, s);
+    if (err == cudaErrorInvalidConfiguration) err = launch<1>(args, info->sm_count, s);
     return err == cudaSuccess ? SGEMM_OK : SGEMM_ERR_CUDA;
 }
