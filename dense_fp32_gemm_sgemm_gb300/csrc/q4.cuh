@@ -338,11 +338,11 @@ __device__ __forceinline__ Raw8<T> load_raw8(const T* row, int n, int N, bool ve
     }
     return raw;
 }
-// The P pieces of 8 values, times `scale` (a power of two); sets `special` where the plain
+// The P pieces of 8 values, times `scale` (a power of two), and their sums; sets `special` where the plain
 // form cannot take one of them.
 template <int P, class T>
 __device__ __forceinline__ void split_raw8(const Raw8<T>& raw, float scale, bool& special,
-                                           uint4 (&out)[P]) {
+                                           uint4 (&out)[P], float (&sum)[P]) {
     const T* e = reinterpret_cast<const T*>(&raw);
     float piece[8][P];
 #pragma unroll
@@ -351,7 +351,10 @@ __device__ __forceinline__ void split_raw8(const Raw8<T>& raw, float scale, bool
         special |= q4_special(x);
         split_pieces<P>(x, piece[i]);
 #pragma unroll
-        for (int p = 0; p < P; ++p) piece[i][p] *= scale;
+        for (int p = 0; p < P; ++p) {
+            sum[p] += piece[i][p];
+            piece[i][p] *= scale;
+        }
     }
 #pragma unroll
     for (int p = 0; p < P; ++p)
@@ -360,18 +363,4 @@ __device__ __forceinline__ void split_raw8(const Raw8<T>& raw, float scale, bool
                             pack_pieces(piece[4][p], piece[5][p]),
                             pack_pieces(piece[6][p], piece[7][p]));
 }
-// The sum of 32 staged values (4 words), added pairwise along a fixed order.
-__device__ __forceinline__ float sum_staged32(const uint4* words) {
-    float s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint4 w = words[i];
-        const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            s += __uint_as_float(v[j] << 16) + __uint_as_float(v[j] & 0xffff0000u);
-    }
-    return s;
-}
-
 }  // namespace sgemm

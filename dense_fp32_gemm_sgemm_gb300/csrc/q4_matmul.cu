@@ -29,9 +29,10 @@ constexpr int min_blocks() { return NT == 1 ? 2 : 1; }
 // Stages of a warp's ring: with 16 warps on an SM about 70 KB are in flight, twice what
 // covers HBM's latency at its full rate.
 template <int MT>
-constexpr int depth() { return 4; }
+constexpr int depth() { return MT == 4 ? 3 : 4; }
 
 struct Plan {
+    int mt;       // strips that a warp takes at a time
     int warps;    // of a CTA
     int cluster;  // CTAs that split n
     int wn;       // warps of a CTA that split n
@@ -70,49 +71,70 @@ __host__ __device__ constexpr int part_floats(int warps, int mt, int columns) {
     return warps * mt * kQ4StripK * columns;
 }
 
-// What a CTA stages of the columns: rows of A from row0 on, n from n0 on, `units` of 8 values.
+// What a CTA stages of the columns: rows of A, n from n0 on, `units` of 8 values (a multiple
+// of 16), and factor times their sums over each group of 8 << log_units values.
 struct Staging {
     const void* A;
     size_t lda;
     int dtype, rows, n0, N, units, threads, pitch;
     bool vec;
     uint8_t* xs;
+    float* xsum;  // [group][column], sum_pitch floats a group
+    int sum_pitch, log_units;
+    float factor;
 };
 
-// Writes the pieces of the rows, times scale, to their columns; true where the plain form
-// cannot take one of the thread's values.
+// Writes the pieces of the rows, times scale, to their columns, and their sums; true where
+// the plain form cannot take one of the thread's values. A group's units lie in neighbouring
+// lanes of a warp, so that shuffles add them.
 template <int P, class T>
 __device__ __noinline__ bool stage_rows(const Staging& s, float scale) {
     constexpr int AHEAD = 4;  // loads in flight
     const T* A = static_cast<const T*>(s.A);
     const int items = s.units * s.rows, threads = s.threads;
+    const int group_mask = (1 << s.log_units) - 1;
     int row = 0, u = threadIdx.x;
     bool special = false;
-    for (int i = threadIdx.x; i < items; i += AHEAD * threads) {
+    for (int i = threadIdx.x; i - int(threadIdx.x & 31) < items; i += AHEAD * threads) {
         Raw8<T> raw[AHEAD];
-        int at[AHEAD];
+        int rows_[AHEAD], units_[AHEAD];
 #pragma unroll
         for (int j = 0; j < AHEAD; ++j) {
-            at[j] = -1;
+            rows_[j] = -1;
             if (i + j * threads < items) {
                 while (u >= s.units) {
                     u -= s.units;
                     ++row;
                 }
-                at[j] = row * P * s.pitch + u * 16;
+                rows_[j] = row;
+                units_[j] = u;
                 raw[j] = load_raw8(A + row * s.lda, s.n0 + u * 8, s.N, s.vec);
                 u += threads;
             }
         }
 #pragma unroll
-        for (int j = 0; j < AHEAD; ++j)
-            if (at[j] >= 0) {
+        for (int j = 0; j < AHEAD; ++j) {
+            float sum[P];
+#pragma unroll
+            for (int p = 0; p < P; ++p) sum[p] = 0.0f;
+            if (rows_[j] >= 0) {
                 uint4 piece[P];
-                split_raw8<P>(raw[j], scale, special, piece);
+                split_raw8<P>(raw[j], scale, special, piece, sum);
 #pragma unroll
                 for (int p = 0; p < P; ++p)
-                    *reinterpret_cast<uint4*>(s.xs + at[j] + p * s.pitch) = piece[p];
+                    *reinterpret_cast<uint4*>(s.xs + (rows_[j] * P + p) * s.pitch + units_[j] * 16) =
+                        piece[p];
             }
+            if (i - int(threadIdx.x & 31) + j * threads >= items) continue;  // warp-uniform
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+                for (int o = 1; o <= group_mask; o *= 2)
+                    sum[p] += __shfl_xor_sync(0xffffffffu, sum[p], o);
+                if (rows_[j] >= 0 && (units_[j] & group_mask) == 0)
+                    s.xsum[(units_[j] >> s.log_units) * s.sum_pitch + rows_[j] * P + p] =
+                        sum[p] * s.factor;
+            }
+        }
     }
     return special;
 }
@@ -123,34 +145,13 @@ __device__ __forceinline__ bool stage_any(const Staging& s, float scale) {
     return stage_rows<3, float>(s, scale);
 }
 
-// Stages the columns, scaled for the plain form, and factor times their sums over each group
-// of 32 << log_blocks n at xsum[group][column] (sum_pitch floats a group); true where the plain
-// form cannot take one of the values, and then the columns are staged as they are.
-__device__ __noinline__ bool stage_columns(const Staging& s, int columns, int log_blocks, float factor,
-                                           float* xsum, int sum_pitch) {
-    if (__syncthreads_or(stage_any(s, kQ4Scale))) {
-        stage_any(s, 1.0f);
-        __syncthreads();
-        return true;
-    }
-    // a thread sums 32 n; the 1, 2 or 4 threads of a group are neighbours in a warp
-    const int blocks = s.units / 4;  // a multiple of 4
-    int col = 0, block = threadIdx.x;
-    for (int i = threadIdx.x; i < (blocks * columns + 31) / 32 * 32; i += s.threads) {
-        while (block >= blocks) {
-            block -= blocks;
-            ++col;
-        }
-        float v = 0.0f;
-        if (col < columns)
-            v = sum_staged32(reinterpret_cast<const uint4*>(s.xs + col * s.pitch + block * 64));
-        for (int o = 0; o < log_blocks; ++o) v += __shfl_xor_sync(0xffffffffu, v, 1 << o);
-        if (col < columns && (block & ((1 << log_blocks) - 1)) == 0)
-            xsum[(block >> log_blocks) * sum_pitch + col] = v * factor;
-        block += s.threads;
-    }
+// Stages the columns, scaled for the plain form; true where that form cannot take one of the
+// values, and then they are staged as they are.
+__device__ __noinline__ bool stage_columns(const Staging& s) {
+    if (!__syncthreads_or(stage_any(s, kQ4Scale))) return false;
+    stage_any(s, 1.0f);
     __syncthreads();
-    return false;
+    return true;
 }
 
 // Where a CTA's shared memory holds what, in bytes; `columns`: those that it stages.
@@ -163,7 +164,7 @@ __host__ __device__ constexpr Offsets offsets(int warps, int mt, int depth, int 
     Offsets o{};
     o.ring = columns * column_pitch(chunks);
     o.red = o.ring + warps * depth * mt * chunk_bytes;
-    o.xsum = o.red + 2 * red_floats(warps, mt, columns) * 4;
+    o.xsum = o.red + red_floats(warps, mt, columns) * 4;
     o.part = o.xsum + xsum_floats(chunks, group, nt) * 4;
     o.end = o.part + (cluster ? 2 * part_floats(warps, mt, columns) * 4 : 0);
     return o;
@@ -215,8 +216,10 @@ __global__ void __launch_bounds__(max_warps<NT>() * 32, min_blocks<NT>())
     auto fetch = [&]() {
         if (fetch_strip < geom.strips) {
             q4_fetch(fetch_to, fetch_from, tail);
-            if (MT == 2 && fetch_strip + 1 < geom.strips)
-                q4_fetch(fetch_to + chunk_bytes, fetch_from + geom.strip_bytes(), tail);
+#pragma unroll
+            for (int m = 1; m < MT; ++m)
+                if (fetch_strip + m < geom.strips)
+                    q4_fetch(fetch_to + m * chunk_bytes, fetch_from + m * geom.strip_bytes(), tail);
             fetch_from += step;
             if (--fetch_left == 0) {
                 fetch_left = my_chunks;
@@ -228,6 +231,10 @@ __global__ void __launch_bounds__(max_warps<NT>() * 32, min_blocks<NT>())
         fetch_to += stage_bytes;
         if (fetch_to == fetch_end) fetch_to -= DEPTH * stage_bytes;
     };
+    // Nothing in global memory is touched before the kernels ahead in the stream are done; the
+    // next one may take its place on SMs as they come free.
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
 #pragma unroll
     for (int i = 0; i < DEPTH - 1; ++i) fetch();
 
@@ -243,8 +250,11 @@ __global__ void __launch_bounds__(max_warps<NT>() * 32, min_blocks<NT>())
     st.pitch = pitch;
     st.vec = args.vec;
     st.xs = xs;
-    const bool special = stage_columns(st, columns, GROUP == 32 ? 0 : GROUP == 64 ? 1 : 2,
-                                       (ZEROS ? -1.0f : -8.0f) / kQ4Scale, xsum, NT * 8);
+    st.xsum = xsum;
+    st.sum_pitch = NT * 8;
+    st.log_units = GROUP == 32 ? 2 : GROUP == 64 ? 3 : 4;
+    st.factor = ZEROS ? -1.0f : -8.0f;
+    const bool special = stage_columns(st);
 
     // a lane's words of column 8 nt + r in the warp's first chunk; columns that do not exist
     // repeat the last one, and their sums are not used
@@ -305,10 +315,9 @@ __global__ void __launch_bounds__(max_warps<NT>() * 32, min_blocks<NT>())
                     total);
             }
         }
-        // Sums over the warps that split n, in their order. Two buffers in turn: a warp is
-        // back at one of them only after the barrier that follows the other's use.
-        float* reds = red + buffer * red_floats(plan.warps, MT, plan.staged);
-        float* mine = reds + (wn * strips_per_group + wm * MT) * columns * 17 + r;
+        // Sums over the warps that split n, in their order
+        if (group != first_group) __syncthreads();
+        float* mine = red + (wn * strips_per_group + wm * MT) * columns * 17 + r;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -332,7 +341,7 @@ __global__ void __launch_bounds__(max_warps<NT>() * 32, min_blocks<NT>())
         for (int i = threadIdx.x; i < cells; i += threads) {
             const int row = i >> width_log, col = i - (row << width_log);
             const float* from =
-                reds + ((col / kQ4StripK) * columns + row * pieces) * 17 + col % kQ4StripK;
+                red + ((col / kQ4StripK) * columns + row * pieces) * 17 + col % kQ4StripK;
             float s = 0.0f;
             for (int p = 0; p < pieces; ++p, from += 17)
 #pragma unroll 8
@@ -397,15 +406,15 @@ int resident_clusters(int cluster, int resident, int threads, int sm_count) {
 // The split of an N x K product with this many columns: the warps, cluster size and warp split
 // whose slowest SM is done first.
 template <int MT, int NT, int GROUP, bool ZEROS>
-Plan make_plan(const Q4Geom& g, int columns, int sm_count, double* cost_out) {
+void make_plan(const Q4Geom& g, int columns, int sm_count, double* best_cost, Plan* best) {
     constexpr int DEPTH = depth<MT>();
-    Plan best{};
-    double best_cost = kNoPlan;
+    if (set_smem_limit_once<q4_matmul_kernel<MT, NT, GROUP, ZEROS>>(SMEM_LIMIT) != cudaSuccess) return;
     for (int warps = 8; warps <= max_warps<NT>(); warps *= 2)
         for (int cluster = 1; cluster <= 8; cluster *= 2) {
             if (cluster > 1 && g.chunks < 2 * cluster) break;
             for (int wn = warps; wn >= 1; wn /= 2) {
                 Plan p;
+                p.mt = MT;
                 p.warps = warps;
                 p.cluster = cluster;
                 p.wn = wn;
@@ -428,18 +437,16 @@ Plan make_plan(const Q4Geom& g, int columns, int sm_count, double* cost_out) {
                 const int rounds = (p.groups + p.clusters - 1) / p.clusters;
                 const int units = (p.chunks + wn - 1) / wn * MT;  // of a warp and group
                 const int busy = (p.clusters * cluster + sm_count - 1) / sm_count;
-                const double chunk_cost = busy * warps >= 24 ? 42.0 : busy * warps > 8 ? 45.0 : 70.0;
+                const double chunk_cost = busy * warps > 8 ? 45.0 : 70.0;
                 const double stage = busy * 3.0 * columns * p.chunks + 1500.0;
-                const double cost = stage + rounds * (busy * warps * units * chunk_cost + 400.0 +
-                                              (cluster > 1 ? 500.0 : 0.0));
-                if (cost < best_cost) {
-                    best_cost = cost;
-                    best = p;
+                const double cost = stage + rounds * (busy * warps * units * chunk_cost + 300.0 +
+                                              (wn - 1) * MT * 60.0 + (cluster > 1 ? 500.0 : 0.0));
+                if (cost < *best_cost) {
+                    *best_cost = cost;
+                    *best = p;
                 }
             }
         }
-    *cost_out = best_cost;
-    return best;
 }
 
 template <int MT, int NT, int GROUP, bool ZEROS>
@@ -449,32 +456,36 @@ cudaError_t launch_kernel(const Args& args, int launch_rows, cudaStream_t stream
     config.blockDim = dim3(args.plan.warps * 32);
     config.dynamicSmemBytes = args.plan.smem;
     config.stream = stream;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = args.plan.cluster;
-    attr.val.clusterDim.y = 1;
-    attr.val.clusterDim.z = 1;
-    config.attrs = &attr;
-    config.numAttrs = args.plan.cluster > 1 ? 1 : 0;
+    cudaLaunchAttribute attrs[2];
+    attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[0].val.programmaticStreamSerializationAllowed = 1;
+    attrs[1].id = cudaLaunchAttributeClusterDimension;
+    attrs[1].val.clusterDim.x = args.plan.cluster;
+    attrs[1].val.clusterDim.y = 1;
+    attrs[1].val.clusterDim.z = 1;
+    config.attrs = attrs;
+    config.numAttrs = args.plan.cluster > 1 ? 2 : 1;
     count_launch();
     return cudaLaunchKernelEx(&config, q4_matmul_kernel<MT, NT, GROUP, ZEROS>, args);
 }
 
 template <int NT, int GROUP, bool ZEROS>
 cudaError_t launch_group(Args args, int sm_count, cudaStream_t stream) {
-    cudaError_t err = set_smem_limit_once<q4_matmul_kernel<1, NT, GROUP, ZEROS>>(SMEM_LIMIT);
-    if (err == cudaSuccess)
-        err = set_smem_limit_once<q4_matmul_kernel<2, NT, GROUP, ZEROS>>(SMEM_LIMIT);
-    if (err != cudaSuccess) return err;
     const int most_rows = NT * 8 / args.pieces;
     const int launch_rows = (args.M + most_rows - 1) / most_rows;
     const int columns = (args.M < most_rows ? args.M : most_rows) * args.pieces;
-    double one, two;
-    args.plan = make_plan<1, NT, GROUP, ZEROS>(args.geom, columns, sm_count, &one);
-    const Plan pair = make_plan<2, NT, GROUP, ZEROS>(args.geom, columns, sm_count, &two);
-    if (one >= kNoPlan && two >= kNoPlan) return cudaErrorInvalidConfiguration;
-    if (one < two) return launch_kernel<1, NT, GROUP, ZEROS>(args, launch_rows, stream);
-    args.plan = pair;
+    // one strip a warp only where a product is small: its columns' words serve once
+    constexpr int LEAST = NT == 1 ? 1 : 2, MOST = NT == 4 ? 2 : 4;
+    double cost = kNoPlan;
+    args.plan = Plan{};
+    if constexpr (LEAST <= 1) make_plan<1, NT, GROUP, ZEROS>(args.geom, columns, sm_count, &cost, &args.plan);
+    make_plan<2, NT, GROUP, ZEROS>(args.geom, columns, sm_count, &cost, &args.plan);
+    if constexpr (MOST >= 4) make_plan<4, NT, GROUP, ZEROS>(args.geom, columns, sm_count, &cost, &args.plan);
+    if (cost >= kNoPlan) return cudaErrorInvalidConfiguration;
+    if constexpr (LEAST <= 1)
+        if (args.plan.mt == 1) return launch_kernel<1, NT, GROUP, ZEROS>(args, launch_rows, stream);
+    if constexpr (MOST >= 4)
+        if (args.plan.mt == 4) return launch_kernel<4, NT, GROUP, ZEROS>(args, launch_rows, stream);
     return launch_kernel<2, NT, GROUP, ZEROS>(args, launch_rows, stream);
 }
 
