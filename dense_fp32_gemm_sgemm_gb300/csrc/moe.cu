@@ -87,107 +87,59 @@ __global__ void __launch_bounds__(WARPS * 32) moe_router_kernel(MoeArgs a) {
     }
 }
 
-__device__ __forceinline__ uint4 piece_of(const void* src, int dtype, size_t at, int n, int N, int p) {
-    float v[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        float piece[3];
-        split_pieces<3>(n + i < N ? load_as_float(src, dtype, at + n + i) : 0.0f, piece);
-        v[i] = piece[p];
+// Adds column `col` of a tile times src[at .. at + N) (FP32 or 16-bit values).
+__device__ float column_product(const uint8_t* tile, const Q4Geom& geom, int col, const void* src,
+                                int dtype, size_t at) {
+    float total = 0.0f;
+    const int groups = kQ4UnitN / geom.group;
+    for (int u = 0; u < geom.units; ++u) {
+        const uint8_t* unit = tile + size_t(u) * geom.unit_bytes;
+        for (int g = 0; g < groups; ++g) {
+            float z = 8.0f;
+            if (geom.zeros) z = unit[kQ4CodeBytes + groups * kQ4UnitK * 2 + g * kQ4UnitK + col];
+            float acc = 0.0f;
+            for (int i = g * geom.group / 8; i < (g + 1) * geom.group / 8; ++i) {
+                const uint32_t w =
+                    reinterpret_cast<const uint32_t*>(unit)[(i / 4 * kQ4UnitK + col) * 4 + i % 4];
+                for (int e = 0; e < 8; ++e) {
+                    const int n = u * kQ4UnitN + 8 * i + e;
+                    if (n < geom.N)
+                        acc = fmaf(float((w >> (4 * ((e >> 1) + 4 * (e & 1)))) & 15) - z,
+                                   load_as_float(src, dtype, at + n), acc);
+                }
+            }
+            total = fmaf(q4_scale(reinterpret_cast<const uint16_t*>(unit + kQ4CodeBytes)[g * kQ4UnitK +
+                                                                                        col],
+                                  geom.fp16),
+                         acc, total);
+        }
     }
-    return make_uint4(pack_pieces(v[0], v[1]), pack_pieces(v[2], v[3]), pack_pieces(v[4], v[5]),
-                      pack_pieces(v[6], v[7]));
+    return total;
 }
 
-// Adds the CTA's share of strip . src[at .. at + N) to total.
-template <int GROUP>
-__device__ __forceinline__ void strip_product(const uint8_t* strip, const Q4Geom& geom,
-                                              const void* src, int dtype, size_t at, int pieces,
-                                              float (&total)[1][1][4]) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, c = lane & 3;
-    for (int ch = warp; ch < geom.chunks; ch += WARPS) {
-        const uint8_t* chunk = strip + size_t(ch) * geom.chunk_bytes;
-        __shared__ uint4 xw[WARPS][4][32];  // [block][lane]
-        for (int b = 0; b < 4; ++b)
-            xw[threadIdx.x >> 5][b][lane] =
-                r < pieces ? piece_of(src, dtype, at, ch * kQ4ChunkN + 32 * b + 8 * c, geom.N, r)
-                           : make_uint4(0, 0, 0, 0);
-        __syncwarp();
-        // blocks of a lane's column are 64 bytes apart there, 512 here
-        __shared__ uint4 xc[WARPS][8][16];
-        for (int b = 0; b < 4; ++b) xc[threadIdx.x >> 5][r][4 * b + c] = xw[threadIdx.x >> 5][b][lane];
-        __syncwarp();
-        const uint8_t* x = reinterpret_cast<const uint8_t*>(&xc[threadIdx.x >> 5][r][c]);
-        if (geom.zeros)
-            q4_chunk_centred<GROUP, true>(chunk, x, geom.fp16, lane, total[0][0]);
-        else
-            q4_chunk_centred<GROUP, false>(chunk, x, geom.fp16, lane, total[0][0]);
-        __syncwarp();
-    }
+__global__ void __launch_bounds__(kQ4UnitK)
+    moe_hidden_kernel(MoeArgs a, const uint8_t* gate, const uint8_t* up, Q4Geom geom) {
+    const int slot = blockIdx.y, t = slot / a.top, col = threadIdx.x;
+    const int e = a.ids[slot], f = blockIdx.x * kQ4UnitK + col;
+    if (e < 0 || f >= geom.K) return;
+    const size_t at = e * geom.matrix_bytes() + blockIdx.x * geom.tile_bytes();
+    const float g = column_product(gate + at, geom, col, a.x, a.dtype, t * a.ldx);
+    const float u = column_product(up + at, geom, col, a.x, a.dtype, t * a.ldx);
+    a.hidden[size_t(slot) * a.F + f] = g / (1.0f + expf(-g)) * u * a.weights[slot];
 }
 
-__device__ __forceinline__ void strip_product(const uint8_t* strip, const Q4Geom& geom,
-                                              const void* src, int dtype, size_t at, int pieces,
-                                              float (&total)[1][1][4]) {
-    if (geom.group == 32)
-        strip_product<32>(strip, geom, src, dtype, at, pieces, total);
-    else if (geom.group == 64)
-        strip_product<64>(strip, geom, src, dtype, at, pieces, total);
-    else
-        strip_product<128>(strip, geom, src, dtype, at, pieces, total);
-}
-
-__device__ __forceinline__ void put(float (&red)[8][17], const float (&total)[1][1][4]) {
-    const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) red[2 * c + (i & 1)][r + 8 * (i >> 1)] = total[0][0][i];
-}
-
-__device__ __forceinline__ float gathered(const float (&red)[WARPS][8][17], int pieces, int col) {
-    float s = 0.0f;
-    for (int w = 0; w < WARPS; ++w)
-        for (int p = 0; p < pieces; ++p) s += red[w][p][col];
-    return s;
-}
-
-__global__ void __launch_bounds__(WARPS * 32)
-    moe_hidden_kernel(MoeArgs a, const uint8_t* gate, const uint8_t* up, Q4Geom geom, int pieces) {
-    __shared__ float red[2][WARPS][8][17];
-    const int slot = blockIdx.y, t = slot / a.top, strip = blockIdx.x;
-    const int e = a.ids[slot];
-    if (e < 0) return;
-    const size_t at = e * geom.matrix_bytes() + strip * geom.strip_bytes();
-    float total[1][1][4] = {};
-    strip_product(gate + at, geom, a.x, a.dtype, t * a.ldx, pieces, total);
-    put(red[0][threadIdx.x >> 5], total);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) total[0][0][i] = 0.0f;
-    strip_product(up + at, geom, a.x, a.dtype, t * a.ldx, pieces, total);
-    put(red[1][threadIdx.x >> 5], total);
-    __syncthreads();
-    const int col = threadIdx.x, f = strip * kQ4StripK + col;
-    if (col < kQ4StripK && f < geom.K) {
-        const float g = gathered(red[0], pieces, col), u = gathered(red[1], pieces, col);
-        a.hidden[size_t(slot) * a.F + f] = g / (1.0f + expf(-g)) * u * a.weights[slot];
-    }
-}
-
-__global__ void __launch_bounds__(WARPS * 32)
-    moe_down_kernel(MoeArgs a, const uint8_t* down, Q4Geom geom, int pieces) {
-    __shared__ float red[WARPS][8][17];
-    const int t = blockIdx.y, strip = blockIdx.x;
-    float total[1][1][4] = {};
+__global__ void __launch_bounds__(kQ4UnitK)
+    moe_down_kernel(MoeArgs a, const uint8_t* down, Q4Geom geom) {
+    const int t = blockIdx.y, col = threadIdx.x, d = blockIdx.x * kQ4UnitK + col;
+    if (d >= geom.K) return;
+    float v = 0.0f;
     for (int j = 0; j < a.top; ++j) {
         const int slot = t * a.top + j, e = a.ids[slot];
-        if (e < 0) continue;
-        strip_product(down + e * geom.matrix_bytes() + strip * geom.strip_bytes(), geom, a.hidden,
-                      SGEMM_FLOAT32, size_t(slot) * a.F, pieces, total);
+        if (e >= 0)
+            v += column_product(down + e * geom.matrix_bytes() + blockIdx.x * geom.tile_bytes(), geom,
+                                col, a.hidden, SGEMM_FLOAT32, size_t(slot) * a.F);
     }
-    put(red[threadIdx.x >> 5], total);
-    __syncthreads();
-    const int col = threadIdx.x, d = strip * kQ4StripK + col;
-    if (col < kQ4StripK && d < geom.K)
-        store_from_float(a.y, a.dtype, t * a.ldy + d, gathered(red, pieces, col));
+    store_from_float(a.y, a.dtype, t * a.ldy + d, v);
 }
 
 bool stack_fits(const sgemm_q4& w, int E, int N, int K) {
@@ -260,11 +212,10 @@ extern "C" int sgemm_moe(const sgemm_moe_layer* layer, const void* x, long long 
     a.ldy = ldy;
     const Q4Geom g = q4_geom(m.gate), gd = q4_geom(m.down);
     moe_router_kernel<<<T, WARPS * 32, 0, s>>>(a);
-    moe_hidden_kernel<<<dim3(g.strips, int(slots)), WARPS * 32, 0, s>>>(
-        a, static_cast<const uint8_t*>(m.gate.data), static_cast<const uint8_t*>(m.up.data), g,
-        pieces_of(m.dtype));
-    moe_down_kernel<<<dim3(gd.strips, T), WARPS * 32, 0, s>>>(
-        a, static_cast<const uint8_t*>(m.down.data), gd, m.dtype == SGEMM_FLOAT32 ? 3 : 2);
+    moe_hidden_kernel<<<dim3(g.tiles, int(slots)), kQ4UnitK, 0, s>>>(
+        a, static_cast<const uint8_t*>(m.gate.data), static_cast<const uint8_t*>(m.up.data), g);
+    moe_down_kernel<<<dim3(gd.tiles, T), kQ4UnitK, 0, s>>>(
+        a, static_cast<const uint8_t*>(m.down.data), gd);
     count_launch(3);
     return cudaGetLastError() == cudaSuccess ? SGEMM_OK : SGEMM_ERR_CUDA;
 }

@@ -2,10 +2,9 @@
 // that are quantised already, and dequantisation to FP32 (definitions in sgemm.h, layout in
 // q4.cuh).
 //
-// All three move a tile of 128 n x 64 columns (one chunk of four strips) through shared
-// memory, because a lane's codes run along n while a dense matrix is contiguous along k (or,
-// transposed, the other way round): global memory is read and written in whole lines on
-// both sides.
+// All three move a tile of 128 n x 64 columns (half a unit) through shared memory, because a
+// column's codes run along n while a dense matrix is contiguous along k (or, transposed, the
+// other way round): global memory is read and written in whole lines on both sides.
 #include "internal.cuh"
 #include "q4.cuh"
 
@@ -13,34 +12,43 @@ namespace sgemm {
 namespace {
 
 constexpr int TILE_K = 64;
-constexpr int TILE_STRIPS = TILE_K / kQ4StripK;
 constexpr int PITCH = TILE_K + 1;  // column and row walks of the tile are free of conflicts
 constexpr int THREADS = 256;
 
 enum class Source { values, codes };
 
-// Position of a strip's column among its 16 scales.
-__device__ __forceinline__ int side_pos(int col) { return (col & 7) * 2 + (col >> 3); }
+// The nibble of a word that holds the e-th of its 8 codes.
+__device__ constexpr int nibble_of(int e) { return (e >> 1) + 4 * (e & 1); }
+
+// The unit that a CTA works on, and its first column there.
+__device__ __forceinline__ uint8_t* unit_at(uint8_t* data, const Q4Geom& geom) {
+    return data + size_t(blockIdx.z) * geom.matrix_bytes() +
+           (blockIdx.x / (kQ4UnitK / TILE_K)) * geom.tile_bytes() +
+           size_t(blockIdx.y) * geom.unit_bytes;
+}
+__device__ __forceinline__ int first_column() {
+    return int(blockIdx.x) % (kQ4UnitK / TILE_K) * TILE_K;
+}
 
 template <Source SOURCE>
 __global__ void __launch_bounds__(THREADS)
     q4_pack_kernel(const void* __restrict__ src, int dtype, bool transposed,
                    const uint16_t* __restrict__ scales, const uint8_t* __restrict__ zeros,
                    uint8_t* __restrict__ out, Q4Geom geom) {
-    __shared__ float tile[kQ4ChunkN][PITCH];
+    __shared__ float tile[kQ4UnitN][PITCH];
     __shared__ float lo_s[4][TILE_K], hi_s[4][TILE_K];  // of 32 n each
     __shared__ float scale_s[4][TILE_K];                // of a group each
     __shared__ float zero_s[4][TILE_K];
     const int tid = threadIdx.x;
-    const int n0 = blockIdx.y * kQ4ChunkN, k0 = blockIdx.x * TILE_K;
+    const int n0 = blockIdx.y * kQ4UnitN, k0 = blockIdx.x * TILE_K;
     const int N = geom.N, K = geom.K;
     const size_t mat = size_t(blockIdx.z) * N * K;
-    const int blocks = geom.group / 32, groups = kQ4ChunkN / geom.group;
+    const int blocks = geom.group / 32, groups = kQ4UnitN / geom.group;
 
 #pragma unroll 8
-    for (int i = 0; i < kQ4ChunkN * TILE_K / THREADS; ++i) {
-        const int n = transposed ? tid % kQ4ChunkN : tid / TILE_K + i * (THREADS / TILE_K);
-        const int k = transposed ? tid / kQ4ChunkN + i * (THREADS / kQ4ChunkN) : tid % TILE_K;
+    for (int i = 0; i < kQ4UnitN * TILE_K / THREADS; ++i) {
+        const int n = transposed ? tid % kQ4UnitN : tid / TILE_K + i * (THREADS / TILE_K);
+        const int k = transposed ? tid / kQ4UnitN + i * (THREADS / kQ4UnitN) : tid % TILE_K;
         float v = 0.0f;
         if (n0 + n < N && k0 + k < K) {
             const size_t at =
@@ -98,23 +106,14 @@ __global__ void __launch_bounds__(THREADS)
             }
             zero_s[part][k] = z;
         }
-        const int strip = blockIdx.x * TILE_STRIPS + k / kQ4StripK;
-        if (strip < geom.strips) {
-            uint8_t* chunk = out + size_t(blockIdx.z) * geom.matrix_bytes() +
-                             strip * geom.strip_bytes() + size_t(blockIdx.y) * geom.chunk_bytes;
-            const int pos = side_pos(k % kQ4StripK);
-            reinterpret_cast<uint16_t*>(chunk + kQ4CodeBytes + part * 32)[pos] = bits;
-            if (geom.zeros) chunk[kQ4CodeBytes + groups * 32 + part * 16 + pos] = uint8_t(z);
-        }
+        uint8_t* unit = unit_at(out, geom);
+        const int at = part * kQ4UnitK + first_column() + k;
+        reinterpret_cast<uint16_t*>(unit + kQ4CodeBytes)[at] = bits;
+        if (geom.zeros) unit[kQ4CodeBytes + groups * kQ4UnitK * 2 + at] = uint8_t(z);
     }
     __syncthreads();
 
-    // one 16-byte word of codes a thread: strip, half of the chunk, lane
-    const int lane = tid & 31, half = (tid >> 5) & 1, st = tid >> 6;
-    const int strip = blockIdx.x * TILE_STRIPS + st;
-    if (strip >= geom.strips) return;
-    const int r = lane >> 2, c = lane & 3;
-    const int col[2] = {st * kQ4StripK + r, st * kQ4StripK + r + 8};
+    // 16 bytes of codes a thread: part is the block of 32 n
     auto code = [&](int n, int kk) -> uint32_t {
         const int g = n / geom.group;
         const float z = zero_s[g][kk];
@@ -131,72 +130,51 @@ __global__ void __launch_bounds__(THREADS)
     uint32_t word[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int n = (2 * half + i / 2) * 32 + 8 * c + 4 * (i & 1);
         uint32_t w = 0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            // nibbles 0..3: n, n (r + 8), n + 2, n + 2 (r + 8); 4..7: the same of n + 1
-            const int step = (e & 2) + (e >> 2);
-            w |= code(n + step, col[e & 1]) << (4 * e);
-        }
+        for (int e = 0; e < 8; ++e) w |= code(part * 32 + 8 * i + e, k) << (4 * nibble_of(e));
         word[i] = w;
     }
-    uint8_t* chunk = out + size_t(blockIdx.z) * geom.matrix_bytes() + strip * geom.strip_bytes() +
-                     size_t(blockIdx.y) * geom.chunk_bytes;
-    reinterpret_cast<uint4*>(chunk + half * 512)[lane] =
+    reinterpret_cast<uint4*>(unit_at(out, geom))[part * kQ4UnitK + first_column() + k] =
         make_uint4(word[0], word[1], word[2], word[3]);
 }
 
 __global__ void __launch_bounds__(THREADS)
     q4_dequantize_kernel(const uint8_t* __restrict__ data, float* __restrict__ B, Q4Geom geom) {
-    __shared__ float tile[kQ4ChunkN][PITCH];
+    __shared__ float tile[kQ4UnitN][PITCH];
     const int tid = threadIdx.x;
-    const int n0 = blockIdx.y * kQ4ChunkN, k0 = blockIdx.x * TILE_K;
+    const int n0 = blockIdx.y * kQ4UnitN, k0 = blockIdx.x * TILE_K;
     const int N = geom.N, K = geom.K;
-    const int lane = tid & 31, half = (tid >> 5) & 1, st = tid >> 6;
-    const int strip = blockIdx.x * TILE_STRIPS + st;
-    if (strip < geom.strips) {
-        const uint8_t* chunk = data + size_t(blockIdx.z) * geom.matrix_bytes() +
-                               strip * geom.strip_bytes() + size_t(blockIdx.y) * geom.chunk_bytes;
-        const uint4 w4 = __ldcs(reinterpret_cast<const uint4*>(chunk + half * 512) + lane);
+    const int k = tid % TILE_K, part = tid / TILE_K;
+    {
+        const uint8_t* unit = unit_at(const_cast<uint8_t*>(data), geom);
+        const int col = first_column() + k, g = part * 32 / geom.group;
+        const int groups = kQ4UnitN / geom.group;
+        const uint4 w4 = __ldcs(reinterpret_cast<const uint4*>(unit) + part * kQ4UnitK + col);
         const uint32_t word[4] = {w4.x, w4.y, w4.z, w4.w};
-        const int r = lane >> 2, c = lane & 3;
-        const int groups = kQ4ChunkN / geom.group;
+        const float s = q4_scale(
+            reinterpret_cast<const uint16_t*>(unit + kQ4CodeBytes)[g * kQ4UnitK + col], geom.fp16);
+        const int z =
+            geom.zeros ? unit[kQ4CodeBytes + groups * kQ4UnitK * 2 + g * kQ4UnitK + col] : 8;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int n = (2 * half + i / 2) * 32 + 8 * c + 4 * (i & 1);
-            const int g = n / geom.group;
-            float s0, s1;
-            q4_scales(reinterpret_cast<const uint32_t*>(chunk + kQ4CodeBytes + g * 32)[r], geom.fp16,
-                      s0, s1);
-            int z0 = 8, z1 = 8;
-            if (geom.zeros) {
-                const uint8_t* z = chunk + kQ4CodeBytes + groups * 32 + g * 16 + r * 2;
-                z0 = z[0];
-                z1 = z[1];
-            }
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int step = (e & 2) + (e >> 2);
-                const int q = (word[i] >> (4 * e)) & 15;
-                tile[n + step][st * kQ4StripK + r + 8 * (e & 1)] =
-                    (e & 1) ? s1 * float(q - z1) : s0 * float(q - z0);
-            }
-        }
+            for (int e = 0; e < 8; ++e)
+                tile[part * 32 + 8 * i + e][k] =
+                    s * float(int((word[i] >> (4 * nibble_of(e))) & 15) - z);
     }
     __syncthreads();
     float* out = B + size_t(blockIdx.z) * N * K;
-    const int k = tid % TILE_K;
     if (k0 + k >= K) return;
 #pragma unroll 8
-    for (int i = 0; i < kQ4ChunkN * TILE_K / THREADS; ++i) {
+    for (int i = 0; i < kQ4UnitN * TILE_K / THREADS; ++i) {
         const int n = tid / TILE_K + i * (THREADS / TILE_K);
         if (n0 + n < N) __stcs(out + size_t(n0 + n) * K + k0 + k, tile[n][k]);
     }
 }
 
 dim3 tile_grid(const Q4Geom& g, int count) {
-    return dim3((g.K + TILE_K - 1) / TILE_K, g.chunks, count);
+    return dim3(g.tiles * (kQ4UnitK / TILE_K), g.units, count);
 }
 
 // Checks shared by the three entry points; SGEMM_OK or an error.
@@ -225,6 +203,7 @@ int sgemm_q4_quantize(const void* B, int dtype, int transposed, const sgemm_q4* 
     if (w->flags & SGEMM_Q4_SCALE_FP16) return SGEMM_ERR_UNSUPPORTED;
     const size_t dense = size_t(w->count) * w->N * w->K * dtype_bytes(dtype);
     if (ranges_overlap(w->data, q4_bytes(*w), B, dense)) return SGEMM_ERR_OVERLAP;
+    if (!aligned_to(B, dtype_bytes(dtype))) return SGEMM_ERR_ARG;
     if (!current_device(nullptr)) return SGEMM_ERR_NO_DEVICE;
     const Q4Geom g = q4_geom(*w);
     q4_pack_kernel<Source::values>
@@ -246,6 +225,7 @@ int sgemm_q4_pack(const unsigned char* codes, const void* scales, const unsigned
         ranges_overlap(w->data, bytes, scales, 2 * side) ||
         ((w->flags & SGEMM_Q4_ZEROS) && ranges_overlap(w->data, bytes, zeros, side)))
         return SGEMM_ERR_OVERLAP;
+    if (!aligned_to(scales, 2)) return SGEMM_ERR_ARG;
     if (!current_device(nullptr)) return SGEMM_ERR_NO_DEVICE;
     q4_pack_kernel<Source::codes>
         <<<tile_grid(g, w->count), THREADS, 0, static_cast<cudaStream_t>(stream)>>>(
@@ -260,6 +240,7 @@ int sgemm_q4_dequantize(const sgemm_q4* w, float* B, void* stream) {
     if (rc != SGEMM_OK) return rc;
     const size_t dense = size_t(w->count) * w->N * w->K * sizeof(float);
     if (ranges_overlap(B, dense, w->data, q4_bytes(*w))) return SGEMM_ERR_OVERLAP;
+    if (!aligned_to(B, sizeof(float))) return SGEMM_ERR_ARG;
     if (!current_device(nullptr)) return SGEMM_ERR_NO_DEVICE;
     const Q4Geom g = q4_geom(*w);
     q4_dequantize_kernel<<<tile_grid(g, w->count), THREADS, 0, static_cast<cudaStream_t>(stream)>>>(

@@ -68,6 +68,7 @@
 
 #include "internal.cuh"
 #include "ptx.cuh"
+#include "wait.cuh"
 
 namespace sgemm {
 namespace {
@@ -91,7 +92,6 @@ constexpr int NUM_BARS = 2 * MAX_STAGES + 4 + 1;
 constexpr int STAGING_FIXED = 8;
 constexpr int STAGING_BYTES = 32 * 32 * 4;
 constexpr int SMEM_BYTES = RING_BYTES + STAGING_FIXED * STAGING_BYTES + 256 + 1024;
-constexpr unsigned long long WAIT_LIMIT_NS = 4000000000ull;
 // tile-accumulator kernel: TMA warp, MMA warp, 4 epilogue warps (per CTA)
 constexpr int THREADS_TILE = 192;
 constexpr int EPI_WARPS_TILE = 4;
@@ -183,32 +183,6 @@ __device__ __forceinline__ void clock_mark(int end) {
     if (blockIdx.x == 0) {
         g_clock_record[2 * end] = global_ns();
         g_clock_record[2 * end + 1] = clock64();
-    }
-}
-
-// Waits for the barrier phase of the given parity (acquire at cluster scope when
-// `cluster` is set: the barrier is signalled from the peer CTA). Returns false if the
-// wait ran out of time (then it raises the abort flag and the device error word) or if
-// another role of this CTA already aborted.
-__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                           int* err,
-                                           unsigned long long limit_ns = WAIT_LIMIT_NS,
-                                           bool cluster = false) {
-    auto probe = [&]() {
-        return cluster ? ptx::mbar_try_wait_cluster(bar, parity) : ptx::mbar_try_wait(bar, parity);
-    };
-    if (probe()) return true;
-    const unsigned long long t0 = global_ns();
-    while (true) {
-#pragma unroll 1
-        for (int i = 0; i < 32; ++i)
-            if (probe()) return true;
-        if (*abort_flag) return false;
-        if (global_ns() - t0 > limit_ns) {
-            *abort_flag = 1;
-            atomicExch(err, kErrWaitTimeout);
-            return false;
-        }
     }
 }
 

@@ -44,8 +44,8 @@ def q4(data=W_DATA, count=1, N=256, K=64, group=64, flags=0):
     (128, 16, 128, 0, 1), (129, 17, 128, 0, 1), (1, 1, 32, 1, 1), (4096, 4096, 64, 3, 2),
     (65536, 1 << 20, 32, 1, 1)])
 def test_packed_bytes(L, N, K, group, flags, count):
-    chunk = 1024 + 128 // group * (32 + (16 if flags & 1 else 0))
-    want = count * -(-K // 16) * -(-N // 128) * chunk
+    unit = 8192 + 128 // group * 128 * (3 if flags & 1 else 2)
+    want = count * -(-K // 128) * -(-N // 128) * unit
     assert L.sgemm_q4_bytes(ctypes.byref(q4(None, count, N, K, group, flags))) == want
 
 
