@@ -7,21 +7,22 @@
 // moe_expert_kernel: every CTA builds the same lists of the picked experts' tokens, cut into tiles
 // of so many tokens that an expert's weights are read once for each tile. Then the CTAs take work
 // items in order from a counter:
-//   first items: one tile x 16 hidden values: the strips of gate and up, n = D split over the
-//     CTA's warps; h = silu(g) u times the token's weight goes to scratch as bfloat16 pieces;
-//   then items: 32 columns of the output x a part of the tiles: two strips of down, with the
-//     (tile, n = F) chunks of all the part's experts dealt out to the warps in turn. Each warp
-//     adds its sums to a slab of its own, [token][32], and the slabs are added in warp order; the
-//     last part of a column block to finish adds the parts in their order.
-// An item of the second kind needs all of the first kind. Those have been taken before it, by CTAs
-// that are running and wait for nothing, so its wait ends whatever the number of CTAs that are
+//   first items: one tile x some strips of 16 hidden values, gate and up; h = silu(g) u times
+//     the token's weight goes to scratch as bfloat16 pieces;
+//   second items: one tile x some pairs of strips of the output: the rows of h times down go to
+//     scratch in FP32, one row for each token and expert;
+//   sum items: 32 columns of the output, each token's rows added in the order of its experts.
+// So a token's result does not depend on which other tokens there are. An item that needs earlier
+// ones waits for a count of them. Those have been taken before it, by CTAs that are running and
+// wait for still earlier ones at most, so every wait ends whatever the number of CTAs that are
 // resident. Meanwhile each warp's ring of cp.async stages already fills with the item's weights:
-// HBM stays busy across items and across the wait.
+// HBM stays busy across items and across the waits.
 //
 // The inner product is that of q4_warp.cuh, on chunk pairs (gate and up, or two strips of down), so
 // that a column's words serve two strips. The sums of x that zero points take come from one more
 // matrix instruction on a constant operand (z's place taken by 8, or by 1 and multiplied by z
 // afterwards): hidden values of a group come from several CTAs, so they cannot be summed beforehand.
+#include <cmath>
 #include <type_traits>
 
 #include "internal.cuh"
@@ -40,9 +41,7 @@ constexpr int ROUTE_CTAS = 8;  // of a token
 constexpr int ROUTE_THREADS = 256;
 
 constexpr int DEPTH = 4;        // stages of a warp's ring, a pair of chunks each
-constexpr int MAX_WARPS = 16;
-constexpr int MAX_PARTS = 16;
-constexpr int SMEM_SM = 228 * 1024;
+constexpr int WARPS = 8, THREADS = WARPS * 32;
 constexpr int SMEM_LIMIT = 227 * 1024;
 
 struct MoeArgs {
@@ -61,8 +60,8 @@ struct MoeArgs {
     uint16_t* hp;      // pieces of the hidden values: [token and slot][piece][F padded]
     int* x_special;    // [token]: nonzero where the plain form cannot take some value
     int* h_special;    // [token and slot]
-    int* counters;     // 0: next item, 1: finished first items, 2 ..: parts done of a column block
-    float* parts;      // [part][token][D]
+    int* counters;     // 0: next item, 1: first items done, 2 ..: second items done of a group
+    float* z;          // [token and slot][D]
     int* err;
 };
 
@@ -73,45 +72,42 @@ struct Stack {
 
 // How the expert kernel cuts its work.
 struct MoePlan {
-    int warps;
-    int capacity;   // tokens of a tile
-    int x_pieces, x_columns;  // pieces of a token of x, and columns that they take
-    int h_pieces, h_columns;  // and of a hidden row
-    int blocks;     // column blocks of 32 of the output
-    int parts;      // at most, of the tiles of a column block
+    int capacity;                 // tokens of a tile
+    int x_pieces, x_columns_log;  // pieces of a token of x, and the columns that they take
+    int h_pieces, h_columns_log;  // and of a hidden row
+    int max_columns;              // of a tile
+    int wn1, wn2;                 // warps that split n in first and second items
+    int pairs;                    // pairs of strips of the output
     int chunk, smem;
 };
 
 // ---- routing ---------------------------------------------------------------------------
 
+// The lane's part of x . w: octets lane, lane + 32, ... of [from, to).
 template <class T, class R>
-__device__ __forceinline__ float dot(const T* x, const R* w, int D, bool vec, int lane) {
+__device__ __forceinline__ float dot(const T* x, const R* w, int from, int to, int D, bool vec,
+                                     int lane) {
+    constexpr int AHEAD = 4;  // octets in flight
     float s = 0.0f;
-    if (vec && D % 8 == 0) {
-#pragma unroll 4
-        for (int d = lane * 8; d < D; d += 256) {
-            const Raw8<T> a = load_raw8(x, d, D, true);
-            const Raw8<R> b = load_raw8(w, d, D, true);
-            const T* p = reinterpret_cast<const T*>(&a);
-            const R* q = reinterpret_cast<const R*>(&b);
+    for (int u = from + lane; u < to; u += 32 * AHEAD) {
+        Raw8<T> p[AHEAD];
+        Raw8<R> q[AHEAD];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) s = fmaf(float(p[i]), float(q[i]), s);
-        }
-    } else {
-        for (int d = lane; d < D; d += 32) s = fmaf(float(x[d]), float(w[d]), s);
+        for (int j = 0; j < AHEAD; ++j)
+            if (u + 32 * j < to) {
+                p[j] = load_raw8(x, (u + 32 * j) * 8, D, vec);
+                q[j] = load_raw8(w, (u + 32 * j) * 8, D, vec);
+            }
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j)
+            if (u + 32 * j < to) {
+                const T* a = reinterpret_cast<const T*>(&p[j]);
+                const R* b = reinterpret_cast<const R*>(&q[j]);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) s = fmaf(float(a[i]), float(b[i]), s);
+            }
     }
     return s;
-}
-
-template <class T>
-__device__ __forceinline__ float router_dot(const MoeArgs& a, int t, int e, int lane) {
-    const T* x = static_cast<const T*>(a.x) + t * a.ldx;
-    const size_t at = size_t(e) * a.D;
-    if (a.router_dtype == SGEMM_FLOAT32)
-        return dot(x, static_cast<const float*>(a.router) + at, a.D, a.vec, lane);
-    if (a.router_dtype == SGEMM_BFLOAT16)
-        return dot(x, static_cast<const __nv_bfloat16*>(a.router) + at, a.D, a.vec, lane);
-    return dot(x, static_cast<const __half*>(a.router) + at, a.D, a.vec, lane);
 }
 
 // This CTA's share of the token's octets as pieces; true where the plain form cannot take one.
@@ -140,60 +136,55 @@ __device__ __forceinline__ bool write_pieces(const MoeArgs& a, int t, int rank, 
     return magnitudes.special<T>();
 }
 
-// The top experts of a token's logits (shared memory, one warp) in ascending order, and their
-// weights.
-__device__ __forceinline__ void choose(const MoeArgs& a, const float* logit, int t, int lane) {
-    float biggest = -INFINITY;
-    for (int e = lane; e < a.E; e += 32) biggest = fmaxf(biggest, logit[e]);
+// The top experts of a token's logits in ascending order, and their weights; all threads of the
+// CTA, a thread an expert. An expert is among them if fewer than `top` others go before it: a
+// larger logit, or an equal one and a lower index.
+__device__ __forceinline__ void choose(const MoeArgs& a, const float* logit, int t) {
+    __shared__ float part[3][ROUTE_THREADS / 32];
+    __shared__ int count[ROUTE_THREADS / 32];
+    const int e = threadIdx.x, lane = e & 31, warp = e >> 5;
+    const float mine = e < a.E ? logit[e] : -INFINITY;
+    float biggest = mine;
     for (int o = 16; o > 0; o >>= 1)
         biggest = fmaxf(biggest, __shfl_xor_sync(0xffffffffu, biggest, o));
+    if (lane == 0) part[0][warp] = biggest;
+    int before = 0;
+    if (e < a.E)
+#pragma unroll 8
+        for (int i = 0; i < a.E; ++i) before += logit[i] > mine || (logit[i] == mine && i < e);
+    const bool chosen = e < a.E && before < a.top;
+    __syncthreads();
+    for (int w = 0; w < ROUTE_THREADS / 32; ++w) biggest = fmaxf(biggest, part[0][w]);
     // an infinite logit shares the weight with its equals, and so do logits that are all -infinity
-    auto power = [&](float l) { return l == biggest ? 1.0f : expf(l - biggest); };
-    float sum = 0.0f;
-    for (int e = lane; e < a.E; e += 32) sum += power(logit[e]);
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    uint32_t taken = 0;  // bit i: expert lane + 32 i
-    float chosen = 0.0f;
-    for (int j = 0; j < a.top; ++j) {
-        float best = -INFINITY;
-        int at = kMoeMaxE;
-        for (int i = 0; lane + 32 * i < a.E; ++i) {
-            const float l = logit[lane + 32 * i];
-            if (!((taken >> i) & 1) && (l > best || at == kMoeMaxE)) {
-                best = l;
-                at = lane + 32 * i;
-            }
-        }
-        for (int o = 16; o > 0; o >>= 1) {
-            const float other = __shfl_xor_sync(0xffffffffu, best, o);
-            const int other_at = __shfl_xor_sync(0xffffffffu, at, o);
-            if (other_at < kMoeMaxE &&
-                (at == kMoeMaxE || other > best || (other == best && other_at < at))) {
-                best = other;
-                at = other_at;
-            }
-        }
-        if ((at & 31) == lane) taken |= 1u << (at >> 5);
-        chosen += power(best);
+    const float power = e < a.E ? (mine == biggest ? 1.0f : expf(mine - biggest)) : 0.0f;
+    float all = power, some = chosen ? power : 0.0f;
+    for (int o = 16; o > 0; o >>= 1) {
+        all += __shfl_xor_sync(0xffffffffu, all, o);
+        some += __shfl_xor_sync(0xffffffffu, some, o);
     }
-    int slot = 0;
-    for (int i = 0; 32 * i < a.E; ++i) {
-        const bool mine = (taken >> i) & 1;
-        const uint32_t mask = __ballot_sync(0xffffffffu, mine);
-        if (mine) {
-            const int at = t * a.top + slot + __popc(mask & ((1u << lane) - 1));
-            a.ids[at] = lane + 32 * i;
-            a.weights[at] = power(logit[lane + 32 * i]) / (a.renormalize ? chosen : sum);
-        }
-        slot += __popc(mask);
+    const uint32_t mask = __ballot_sync(0xffffffffu, chosen);
+    if (lane == 0) {
+        part[1][warp] = all;
+        part[2][warp] = some;
+        count[warp] = __popc(mask);
+    }
+    __syncthreads();
+    float total = 0.0f;
+    for (int w = 0; w < ROUTE_THREADS / 32; ++w) total += part[a.renormalize ? 2 : 1][w];
+    int slot = __popc(mask & ((1u << lane) - 1));
+    for (int w = 0; w < warp; ++w) slot += count[w];
+    if (chosen) {
+        a.ids[t * a.top + slot] = e;
+        a.weights[t * a.top + slot] = power / total;
     }
 }
 
+template <class T, class R>
 __global__ void __launch_bounds__(ROUTE_THREADS) moe_route_kernel(const MoeArgs a, int counters,
                                                                   int padded) {
-    __shared__ float mine[kMoeMaxE / ROUTE_CTAS];
-    __shared__ float logit[kMoeMaxE];
-    __shared__ float special_s;
+    __shared__ float mine[ROUTE_THREADS / 32];
+    __shared__ float logit[kMoeMaxE];          // of the first CTA
+    __shared__ int special_of[ROUTE_CTAS];     // and there, each CTA's
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int rank = int(ptx::cluster_ctarank()), t = blockIdx.y;
     ptx::griddep_launch_dependents();
@@ -203,22 +194,6 @@ __global__ void __launch_bounds__(ROUTE_THREADS) moe_route_kernel(const MoeArgs 
              i += ROUTE_CTAS * ROUTE_THREADS)
             a.counters[i] = 0;
     const bool live = !a.live || a.live[t];  // the same in the whole cluster
-    bool special = false;
-    if (live) {
-        for (int i = warp; rank + ROUTE_CTAS * i < a.E; i += ROUTE_THREADS / 32) {
-            const int e = rank + ROUTE_CTAS * i;
-            float s = a.dtype == SGEMM_FLOAT32    ? router_dot<float>(a, t, e, lane)
-                      : a.dtype == SGEMM_BFLOAT16 ? router_dot<__nv_bfloat16>(a, t, e, lane)
-                                                  : router_dot<__half>(a, t, e, lane);
-            for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-            if (lane == 0) mine[i] = s == s ? s : -INFINITY;
-        }
-        special = a.dtype == SGEMM_FLOAT32    ? write_pieces<float>(a, t, rank, padded)
-                  : a.dtype == SGEMM_BFLOAT16 ? write_pieces<__nv_bfloat16>(a, t, rank, padded)
-                                              : write_pieces<__half>(a, t, rank, padded);
-    }
-    special = __syncthreads_or(special);
-    if (threadIdx.x == 0) special_s = special ? 1.0f : 0.0f;
     if (!live) {
         if (rank == 0 && threadIdx.x < a.top) {
             a.ids[t * a.top + threadIdx.x] = -1;
@@ -226,44 +201,87 @@ __global__ void __launch_bounds__(ROUTE_THREADS) moe_route_kernel(const MoeArgs 
         }
         return;
     }
-    ptx::cluster_sync();
-    if (rank == 0) {
-        for (int e = threadIdx.x; e < a.E; e += ROUTE_THREADS)
-            logit[e] = ptx::ld_shared_cluster_f32(
-                ptx::mapa_shared(ptx::smem_u32(mine + e / ROUTE_CTAS), e % ROUTE_CTAS));
-        if (threadIdx.x < a.top) a.h_special[t * a.top + threadIdx.x] = 0;
-        float any = 0.0f;
-        if (threadIdx.x == 0) {
-            for (int q = 0; q < ROUTE_CTAS; ++q)
-                any += ptx::ld_shared_cluster_f32(ptx::mapa_shared(ptx::smem_u32(&special_s), q));
-            a.x_special[t] = any > 0.0f;
+    // Experts rank, rank + 8, ...: 8 / SPLIT of them at a time, each by SPLIT warps, so that few
+    // experts still use all warps.
+    const int experts = (a.E - rank + ROUTE_CTAS - 1) / ROUTE_CTAS;  // of this CTA
+    const int split = experts >= 8 ? 1 : experts >= 4 ? 2 : experts >= 2 ? 4 : 8;
+    const int octets = (a.D + 7) / 8, per = (octets + split - 1) / split;
+    ptx::cluster_sync();  // the first CTA is there for what is stored to it
+    for (int i0 = 0; i0 < experts; i0 += 8 / split) {
+        const int i = i0 + warp / split, part = warp % split;
+        float s = 0.0f;
+        if (i < experts) {
+            const int e = rank + ROUTE_CTAS * i, from = part * per, to = min(octets, from + per);
+            s = dot(static_cast<const T*>(a.x) + t * a.ldx,
+                    static_cast<const R*>(a.router) + size_t(e) * a.D, from, to, a.D, a.vec, lane);
         }
-        __syncthreads();
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (split > 1) {
+            if (lane == 0) mine[warp] = s;
+            __syncthreads();
+            s = 0.0f;
+            for (int w = 0; w < split; ++w) s += mine[warp / split * split + w];
+            __syncthreads();
+        }
+        if (lane == 0 && part == 0 && i < experts)
+            ptx::st_shared_cluster_f32(
+                ptx::mapa_shared(ptx::smem_u32(logit + rank + ROUTE_CTAS * i), 0),
+                s == s ? s : -INFINITY);
     }
-    ptx::cluster_sync();  // the others' shared memory has been read
-    if (rank == 0 && warp == 0) choose(a, logit, t, lane);
+    const bool special = __syncthreads_or(write_pieces<T>(a, t, rank, padded));
+    if (threadIdx.x == 0)
+        ptx::st_shared_cluster_f32(ptx::mapa_shared(ptx::smem_u32(special_of + rank), 0),
+                                   __int_as_float(special));
+    ptx::cluster_sync();
+    if (rank != 0) return;
+    choose(a, logit, t);
+    if (threadIdx.x < a.top) a.h_special[t * a.top + threadIdx.x] = 0;
+    if (threadIdx.x == 0) {
+        int any = 0;
+        for (int q = 0; q < ROUTE_CTAS; ++q) any |= special_of[q];
+        a.x_special[t] = any;
+    }
 }
 
 // ---- experts -------------------------------------------------------------------------------
 
 // Where the expert kernel's shared memory holds what, in bytes.
 struct MoeOffsets {
-    int tiles;    // int4 each: expert, first member, members, special
+    int tiles;    // int4 each: expert, first member, members, whether the centred form is wanted
     int members;  // token and slot, by expert
-    int sums;     // first items: [warp][gate, up][column][17]; second: [warp][token][32]
+    int sums;     // [wn][strips or pairs][2][column][17]
+    int masks;    // in the same place before: [expert][form][2], and [expert]
     int ring;
     int end;
 };
-__host__ __device__ constexpr MoeOffsets moe_offsets(int warps, int T, int max_columns, int chunk,
-                                                     int tiles, int slots) {
+__host__ __device__ constexpr MoeOffsets moe_offsets(int max_columns, int chunk, int tiles, int slots,
+                                                     int E) {
     MoeOffsets o{};
     o.tiles = 0;
     o.members = tiles * 16;
     o.sums = (o.members + slots * 2 + 15) / 16 * 16;
-    const int first = warps * 2 * max_columns * 17 * 4, second = warps * T * 32 * 4;
-    o.ring = o.sums + (((first > second ? first : second) + 15) / 16) * 16;
-    o.end = o.ring + warps * DEPTH * 2 * chunk;
+    o.masks = o.sums;
+    int most = WARPS * 2 * max_columns * 17 * 4;
+    if (most < E * 20) most = E * 20;
+    o.ring = o.sums + (most + 15) / 16 * 16;
+    o.end = o.ring + WARPS * DEPTH * 2 * chunk;
     return o;
+}
+
+// Waits until other CTAs have counted up to `count`; all threads of the CTA. Bounded: when it gives
+// up, the rest is computed from what the scratch holds.
+__device__ __forceinline__ void wait_count(const int* counter, int count, volatile int* abort_flag,
+                                           int* err) {
+    if (threadIdx.x == 0 && !*abort_flag) {
+        const unsigned long long t0 = ptx::globaltimer_ns();
+        while (ptx::ld_acquire_gpu(counter) < count)
+            if (ptx::globaltimer_ns() - t0 > WAIT_LIMIT_NS) {
+                *abort_flag = 1;
+                atomicExch(err, kErrWaitTimeout);
+                break;
+            }
+    }
+    __syncthreads();
 }
 
 // Tiles of the picked experts' tokens: an expert has at most two that are not full.
@@ -271,71 +289,52 @@ __host__ __device__ constexpr int most_tiles(int E, int slots, int capacity) {
     return slots / capacity + 2 * (E < slots ? E : slots);
 }
 
-// One pair of chunks (strips m = 0, 1 at stage and stage + chunk) times NT tiles of 8 columns, added
-// to total as in q4_chunk. col[nt]: the lane's column 8 nt + r at the unit, plus 8 c values; its
-// pieces are as they are and scaled here. The group size and zero points are the stack's.
-template <int NT, bool CENTRED>
+// One pair of chunks (at stage and stage + chunk) times NT tiles of 8 columns, added to total as in
+// q4_chunk. x[b][nt]: the lane's 8 values of block b of column 8 nt + r, as they are. GROUP 0:
+// the stack's own group size and zero points.
+template <int NT, int GROUP, bool ZEROS>
 __device__ __forceinline__ void chunk_pair(const uint8_t* stage, int chunk, const Q4Geom& geom, int lane,
-                                           const uint16_t* const (&col)[NT], float (&total)[2][NT][4]) {
-    constexpr int AHEAD = NT == 4 ? 1 : 4;  // blocks whose columns are loaded ahead
+                                           const uint4 (&x)[4][NT], float (&total)[2][NT][4]) {
     const int r = lane >> 2;
-    const int blocks = geom.group / 32, groups = kQ4UnitN / geom.group;
+    const int blocks = GROUP ? GROUP / 32 : geom.group / 32;
+    const int groups = GROUP ? kQ4UnitN / (GROUP ? GROUP : 32) : kQ4UnitN / geom.group;
+    const bool zeros = GROUP ? ZEROS : geom.zeros != 0;
     const __nv_bfloat162 scale = __float2bfloat162_rn(kQ4Scale);
     const __nv_bfloat162 scale16 = __float2bfloat162_rn(kQ4Scale16);
-    const uint32_t one = geom.zeros ? 0x00010001u : 0x00080008u;
+    const uint32_t one = zeros ? 0x00010001u : 0x00080008u;
     const uint32_t ones[4] = {one, one, one << 4, one << 4};
-    uint4 x[AHEAD][NT];
-    auto load = [&](int b) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-            x[b % AHEAD][nt] = *reinterpret_cast<const uint4*>(col[nt] + b * 32);
-    };
-#pragma unroll
-    for (int b = 0; b < AHEAD; ++b) load(b);
     float acc[2][NT][4], sum[NT][4];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[0][nt][i] = acc[1][nt][i] = sum[nt][i] = 0.0f;
     int left = blocks;  // of the group
+    bool first = true;
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
+        if (GROUP ? b % blocks == 0 : first) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[0][nt][i] = acc[1][nt][i] = sum[nt][i] = 0.0f;
+            first = false;
+        }
         uint32_t xs[NT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const uint4 v = x[b % AHEAD][nt];
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            const uint32_t w[4] = {x[b][nt].x, x[b][nt].y, x[b][nt].z, x[b][nt].w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                xs[nt][i] = w[i];
-                if constexpr (!CENTRED) {
-                    const __nv_bfloat162 s = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]),
-                                                     (i & 1) ? scale16 : scale);
-                    xs[nt][i] = *reinterpret_cast<const uint32_t*>(&s);
-                }
+                const __nv_bfloat162 s = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]),
+                                                 (i & 1) ? scale16 : scale);
+                xs[nt][i] = *reinterpret_cast<const uint32_t*>(&s);
             }
+            mma_bf16(sum[nt], ones, xs[nt][0], xs[nt][1]);
+            mma_bf16(sum[nt], ones, xs[nt][2], xs[nt][3]);
         }
-        if (AHEAD == 1 && b < 3) load(b + 1);
-        const int g = b / blocks;
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
             const uint32_t* codes =
                 reinterpret_cast<const uint32_t*>(stage + m * chunk + b * 256) + lane;
             uint32_t lo[4], hi[4];
-            if constexpr (CENTRED) {
-                uint32_t z0 = 8, z1 = 8;
-                if (geom.zeros) {
-                    const uint8_t* z = stage + m * chunk + kQ4ChunkCodes + groups * kQ4StripK * 2 +
-                                       g * kQ4StripK + r;
-                    z0 = z[0];
-                    z1 = z[8];
-                }
-                q4_centred(codes[0], 0x43004300u | z0 * 0x00010001u, lo);
-                q4_centred(codes[32], 0x43004300u | z1 * 0x00010001u, hi);
-            } else {
-                q4_plain(codes[0], lo);
-                q4_plain(codes[32], hi);
-            }
+            q4_plain(codes[0], lo);
+            q4_plain(codes[32], hi);
             const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]};
             const uint32_t a1[4] = {lo[2], hi[2], lo[3], hi[3]};
 #pragma unroll
@@ -344,22 +343,17 @@ __device__ __forceinline__ void chunk_pair(const uint8_t* stage, int chunk, cons
                 mma_bf16(acc[m][nt], a1, xs[nt][2], xs[nt][3]);
             }
         }
-        if constexpr (!CENTRED) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                mma_bf16(sum[nt], ones, xs[nt][0], xs[nt][1]);
-                mma_bf16(sum[nt], ones, xs[nt][2], xs[nt][3]);
-            }
-        }
-        if (--left > 0) continue;
+        if (GROUP ? (b + 1) % blocks != 0 : --left > 0) continue;
         left = blocks;
+        first = true;
+        const int g = b / blocks;
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
             const uint8_t* side = stage + m * chunk + kQ4ChunkCodes;
             const uint16_t* scales = reinterpret_cast<const uint16_t*>(side) + g * kQ4StripK + r;
             const float s0 = q4_scale(scales[0], geom.fp16), s1 = q4_scale(scales[8], geom.fp16);
             float z0 = 1.0f, z1 = 1.0f;
-            if (!CENTRED && geom.zeros) {  // 0x4300 | z is the upper half of the float 128 + z
+            if (zeros) {  // 0x4300 | z is the upper half of the float 128 + z
                 const uint8_t* z = side + groups * kQ4StripK * 2 + g * kQ4StripK + r;
                 z0 = __uint_as_float(0x43000000u | uint32_t(z[0]) << 16) - 128.0f;
                 z1 = __uint_as_float(0x43000000u | uint32_t(z[8]) << 16) - 128.0f;
@@ -368,165 +362,198 @@ __device__ __forceinline__ void chunk_pair(const uint8_t* stage, int chunk, cons
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float s = i < 2 ? s0 : s1, z = i < 2 ? z0 : z1;
-                    float v = acc[m][nt][i];
                     // the sums are alike in all rows of the constant operand
-                    if constexpr (!CENTRED) v = fmaf(-z, sum[nt][i & 1], v) * kQ4Unscale;
-                    total[m][nt][i] = fmaf(s, v, total[m][nt][i]);
-                    acc[m][nt][i] = 0.0f;
+                    const float v =
+                        fmaf(i < 2 ? -z0 : -z1, sum[nt][i & 1], acc[m][nt][i]) * kQ4Unscale;
+                    total[m][nt][i] = fmaf(i < 2 ? s0 : s1, v, total[m][nt][i]);
                 }
         }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) sum[nt][i] = 0.0f;
     }
 }
-
-// Adds up a warp's columns of a tile, column by column: NT as few as hold `columns`.
-template <class Body>
-__device__ __forceinline__ void by_tiles(int columns, bool special, Body&& body) {
-    if (columns <= 8) {
-        if (special)
-            body(std::integral_constant<int, 1>(), std::true_type());
-        else
-            body(std::integral_constant<int, 1>(), std::false_type());
-    } else if (columns <= 16) {
-        if (special)
-            body(std::integral_constant<int, 2>(), std::true_type());
-        else
-            body(std::integral_constant<int, 2>(), std::false_type());
-    } else {
-        if (special)
-            body(std::integral_constant<int, 4>(), std::true_type());
-        else
-            body(std::integral_constant<int, 4>(), std::false_type());
-    }
+// The same in the centred form. Rarely run, so kept small rather than unrolled.
+template <int NT>
+__device__ __forceinline__ void chunk_pair_centred(const uint8_t* stage, int chunk, const Q4Geom& geom,
+                                                   int lane, const uint16_t* const (&col)[NT],
+                                                   float (&total)[2][NT][4]) {
+    const int r = lane >> 2;
+    const int blocks = geom.group / 32, groups = kQ4UnitN / geom.group;
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const uint8_t* side = stage + m * chunk + kQ4ChunkCodes;
+            float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            int left = blocks, g = 0;
+#pragma unroll 1
+            for (int b = 0; b < 4; ++b) {
+                uint32_t z0 = 8, z1 = 8;
+                if (geom.zeros) {
+                    const uint8_t* z = side + groups * kQ4StripK * 2 + g * kQ4StripK + r;
+                    z0 = z[0];
+                    z1 = z[8];
+                }
+                const uint32_t* codes =
+                    reinterpret_cast<const uint32_t*>(stage + m * chunk + b * 256) + lane;
+                const uint4 x = *reinterpret_cast<const uint4*>(col[nt] + b * 32);
+                uint32_t lo[4], hi[4];
+                q4_centred(codes[0], 0x43004300u | z0 * 0x00010001u, lo);
+                q4_centred(codes[32], 0x43004300u | z1 * 0x00010001u, hi);
+                const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]};
+                const uint32_t a1[4] = {lo[2], hi[2], lo[3], hi[3]};
+                mma_bf16(acc, a0, x.x, x.y);
+                mma_bf16(acc, a1, x.z, x.w);
+                if (--left > 0) continue;
+                left = blocks;
+                const uint16_t* scales = reinterpret_cast<const uint16_t*>(side) + g * kQ4StripK + r;
+                const float s0 = q4_scale(scales[0], geom.fp16);
+                const float s1 = q4_scale(scales[8], geom.fp16);
+                total[m][nt][0] = fmaf(s0, acc[0], total[m][nt][0]);
+                total[m][nt][1] = fmaf(s0, acc[1], total[m][nt][1]);
+                total[m][nt][2] = fmaf(s1, acc[2], total[m][nt][2]);
+                total[m][nt][3] = fmaf(s1, acc[3], total[m][nt][3]);
+                acc[0] = acc[1] = acc[2] = acc[3] = 0.0f;
+                ++g;
+            }
+        }
 }
 
-__global__ void __launch_bounds__(MAX_WARPS * 32, 1)
+// NT_MOST: tiles of 8 columns that a tile of tokens may take.
+template <int NT_MOST, int GROUP, bool ZEROS>
+__global__ void __launch_bounds__(THREADS, 2)
     moe_expert_kernel(const MoeArgs a, const Stack gate, const Stack up, const Stack down,
                       const MoePlan plan) {
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int scan_s[MAX_WARPS], tiles_s, item_s[2], last_s;
+    __shared__ int scan_s[WARPS], tiles_s, item_s[2];
     __shared__ volatile int abort_s;
-    const int warps = plan.warps, threads = warps * 32;
+    constexpr int warps = WARPS, threads = THREADS;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane >> 2, c = lane & 3;
     const int slots = a.T * a.top;
     const int max_tiles = most_tiles(a.E, slots, plan.capacity);
-    const int max_columns = plan.capacity * max(plan.x_columns, plan.h_columns);
-    const MoeOffsets at = moe_offsets(warps, a.T, max_columns, plan.chunk, max_tiles, slots);
+    const MoeOffsets at =
+        moe_offsets(plan.max_columns, plan.chunk, max_tiles, slots, a.E);
     int4* tile_s = reinterpret_cast<int4*>(smem + at.tiles);
     uint16_t* member_s = reinterpret_cast<uint16_t*>(smem + at.members);
     float* sums = reinterpret_cast<float*>(smem + at.sums);
     uint8_t* ring = smem + at.ring + warp * DEPTH * 2 * plan.chunk;
+    // phase 1: wm1 strips of wn1 warps each; phase 2: wm2 pairs of strips of wn2 warps each
+    const int wn1 = warp % plan.wn1, wm1 = warp / plan.wn1, strips_item = warps / plan.wn1;
+    const int wn2 = warp % plan.wn2, wm2 = warp / plan.wn2, pairs_item = warps / plan.wn2;
 
     if (tid == 0) abort_s = 0;
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
+    int claimed = 0, claimed2 = 0;
+    if (tid == 0) {
+        claimed = atomicAdd(a.counters, 1);
+        claimed2 = atomicAdd(a.counters, 1);
+    }
 
-    // The tokens of each expert, in order, in tiles; the same in every CTA. The slots' experts are
-    // put where the sums will be.
+    // The tokens of each expert, in order, in tiles; the same in every CTA. Tokens that want the
+    // centred form have tiles of their own, so that they change nothing for the others. A token
+    // picks an expert once, so an expert's tokens are a 64-bit mask (one for each form).
     {
-        int* id_s = reinterpret_cast<int*>(sums);
-        // an expert's number, and beside it whether the token wants the centred form: such tokens
-        // have tiles of their own, so that they change nothing for the others
+        uint32_t* mask_s = reinterpret_cast<uint32_t*>(smem + at.masks);  // [expert][form][2]
+        int* first_s = reinterpret_cast<int*>(mask_s + 4 * a.E);          // [expert]
+        for (int i = tid; i < 4 * a.E; i += threads) mask_s[i] = 0;
+        __syncthreads();
         for (int i = tid; i < slots; i += threads) {
-            const int e = a.ids[i];
-            id_s[i] = e < 0 ? -1 : 2 * e + (a.x_special[i / a.top] != 0);
+            const int e = a.ids[i], t = i / a.top;
+            const int form = a.x_special[t] != 0;
+            if (e >= 0) atomicOr(mask_s + 4 * e + 2 * form + (t >> 5), 1u << (t & 31));
         }
         __syncthreads();
-        int count = 0, plain = 0;
-        if (tid < a.E)
-            for (int i = 0; i < slots; ++i) {
-                count += id_s[i] >> 1 == tid;
-                plain += id_s[i] == 2 * tid;
-            }
+        int plain = 0, centred = 0;
+        if (tid < a.E) {
+            plain = __popc(mask_s[4 * tid]) + __popc(mask_s[4 * tid + 1]);
+            centred = __popc(mask_s[4 * tid + 2]) + __popc(mask_s[4 * tid + 3]);
+        }
         const int plain_tiles = (plain + plan.capacity - 1) / plan.capacity;
-        const int my_tiles = plain_tiles + (count - plain + plan.capacity - 1) / plan.capacity;
+        const int my_tiles = plain_tiles + (centred + plan.capacity - 1) / plan.capacity;
         // tiles and members before this expert's: a scan over the threads
-        int scan = my_tiles << 16 | count;
+        const int own = my_tiles << 16 | (plain + centred);
+        int scan = own;
         for (int o = 1; o < 32; o *= 2) {
             const int v = __shfl_up_sync(0xffffffffu, scan, o);
             if (lane >= o) scan += v;
         }
         if (lane == 31) scan_s[warp] = scan;
         __syncthreads();
-        int before = scan - (my_tiles << 16 | count);
+        int before = scan - own;
         for (int w = 0; w < warp; ++w) before += scan_s[w];
         const int first_tile = before >> 16, first = before & 0xffff;
-        if (tid < a.E && count > 0) {
-            int n = first, special = first + plain;
-            for (int i = 0; i < slots; ++i)
-                if (id_s[i] >> 1 == tid) member_s[(id_s[i] & 1) ? special++ : n++] = uint16_t(i);
+        if (tid < a.E) {
+            first_s[tid] = first;
             for (int k = 0; k < my_tiles; ++k) {
-                const bool centred = k >= plain_tiles;
-                const int from = (centred ? k - plain_tiles : k) * plan.capacity;
+                const bool other = k >= plain_tiles;
+                const int from = (other ? k - plain_tiles : k) * plan.capacity;
                 int4 tile;
                 tile.x = tid;
-                tile.y = first + (centred ? plain : 0) + from;
-                tile.z = min(plan.capacity, (centred ? count - plain : plain) - from);
-                tile.w = centred;
+                tile.y = first + (other ? plain : 0) + from;
+                tile.z = min(plan.capacity, (other ? centred : plain) - from);
+                tile.w = other;
                 tile_s[first_tile + k] = tile;
             }
         }
-        if (tid == threads - 1) tiles_s = (before + (my_tiles << 16 | count)) >> 16;
+        if (tid == threads - 1) tiles_s = (before + own) >> 16;
         if (tid == 0) {
-            item_s[0] = atomicAdd(a.counters, 1);
-            item_s[1] = atomicAdd(a.counters, 1);
+            item_s[0] = claimed;
+            item_s[1] = claimed2;
+        }
+        __syncthreads();
+        for (int i = tid; i < slots; i += threads) {
+            const int e = a.ids[i], t = i / a.top;
+            if (e < 0) continue;
+            const uint32_t* mask = mask_s + 4 * e;
+            const bool other = (mask[2 + (t >> 5)] >> (t & 31)) & 1;
+            const uint32_t* own_mask = mask + (other ? 2 : 0);
+            int n = first_s[e] + __popc(own_mask[t >> 5] & ((1u << (t & 31)) - 1));
+            if (t >= 32) n += __popc(own_mask[0]);
+            if (other) n += __popc(mask[0]) + __popc(mask[1]);
+            member_s[n] = uint16_t(i);
         }
         __syncthreads();
     }
     const int tiles = tiles_s;
     const int strips = (a.F + kQ4StripK - 1) / kQ4StripK;
-    const int parts = max(1, min(plan.parts, tiles));
-    const int first_items = tiles * strips, items = first_items + plan.blocks * parts;
+    const int strip_groups = (strips + strips_item - 1) / strips_item;
+    const int pair_groups = (plan.pairs + pairs_item - 1) / pairs_item;
+    const int first_items = tiles * strip_groups, second_items = tiles * pair_groups;
+    const int items = first_items + second_items + plan.pairs;
     const int x_padded = gate.geom.units * kQ4UnitN, h_padded = down.geom.units * kQ4UnitN;
 
-    // Where an item's chunks are: first items: strip `strip` of gate and up of the tile's expert,
-    // units warp, warp + warps, ...; second items: strips 2 block and + 1 of down, tiles from .. to,
-    // (tile, unit) pairs warp, warp + warps, ... of them.
+    // Where a warp is in an item. kind 0: strip `strip` of gate and up of the tile's expert, units
+    // wn1, wn1 + wn1's count, ...; 1: strips `strip` and + 1 of down, units wn2, ...; 2: nothing to
+    // fetch.
     struct Walk {
-        int kind;  // 0, 1; 2: nothing
-        int tile, to, unit, strip;
+        int kind, strip, tile, unit, left;
     };
     auto walk = [&](int item) {
         Walk w;
+        w.kind = 2;
+        w.strip = w.tile = w.unit = w.left = 0;
         if (item < first_items) {
             w.kind = 0;
-            w.tile = item / strips;
-            w.strip = item - w.tile * strips;
-            w.to = w.tile + 1;
-            w.unit = warp;
-        } else if (item < items) {
-            const int i = item - first_items, block = i / parts, part = i - block * parts;
+            w.tile = item / strip_groups;
+            w.strip = (item - w.tile * strip_groups) * strips_item + wm1;
+            w.unit = wn1;
+            if (w.strip < strips) w.left = (gate.geom.units - wn1 + plan.wn1 - 1) / plan.wn1;
+        } else if (item < first_items + second_items) {
+            item -= first_items;
             w.kind = 1;
-            w.strip = 2 * block;
-            w.tile = part * tiles / parts;
-            w.to = (part + 1) * tiles / parts;
-            w.unit = warp;
-            while (w.unit >= down.geom.units && w.tile < w.to) {
-                w.unit -= down.geom.units;
-                ++w.tile;
-            }
-        } else {
-            w.kind = 2;
-            w.tile = w.to = w.unit = w.strip = 0;
+            w.tile = item / pair_groups;
+            const int pair = (item - w.tile * pair_groups) * pairs_item + wm2;
+            w.strip = 2 * pair;
+            w.unit = wn2;
+            if (pair < plan.pairs) w.left = (down.geom.units - wn2 + plan.wn2 - 1) / plan.wn2;
         }
         return w;
     };
-    auto done = [&](const Walk& w) {
-        return w.kind == 0 ? w.unit >= gate.geom.units : w.tile >= w.to;
-    };
     auto advance = [&](Walk& w) {
-        w.unit += warps;
-        if (w.kind == 1)
-            while (w.unit >= down.geom.units && w.tile < w.to) {
-                w.unit -= down.geom.units;
-                ++w.tile;
-            }
+        --w.left;
+        w.unit += w.kind == 0 ? plan.wn1 : plan.wn2;
     };
 
+    // ---- the ring
     const uint32_t ring_u32 = ptx::smem_u32(ring);
     uint32_t fetch_to = ring_u32;
     const int stage_bytes = 2 * plan.chunk;
@@ -542,26 +569,35 @@ __global__ void __launch_bounds__(MAX_WARPS * 32, 1)
         return s;
     };
     const Q4Side side1 = side_of(gate.geom), side2 = side_of(down.geom);
+    const ptrdiff_t gate_to_up = up.data - gate.data;
     int next_item = item_s[1];
-    Walk f = walk(item_s[0]);
     int f_on = 0;   // the walk is in the current item (0), the next (1) or through both (2)
     int ahead = 0;  // stages fetched and not used up
+    const uint8_t* f_from = nullptr;  // the unit that the walk is at
+    Walk f = walk(item_s[0]);
+    auto locate = [&]() {
+        if (f.left == 0) return;
+        const Stack& stack = f.kind == 0 ? gate : down;
+        f_from = stack.data + tile_s[f.tile].x * stack.geom.matrix_bytes() +
+                 size_t(f.strip / kQ4StripsOfTile) * stack.geom.tile_bytes() +
+                 size_t(f.unit) * stack.geom.unit_bytes;
+    };
     auto fetch = [&]() -> bool {
-        while (f_on < 2 && done(f))
-            if (++f_on == 1) f = walk(next_item);
-        if (f_on == 2) return false;
-        const int e = tile_s[f.tile].x, in_tile = f.strip % kQ4StripsOfTile;
+        while (f.left == 0) {
+            if (f_on == 2) return false;
+            if (++f_on == 2) return false;
+            f = walk(next_item);
+            locate();
+        }
+        const int in_tile = f.strip % kQ4StripsOfTile;
         if (f.kind == 0) {
-            const size_t from = e * gate.geom.matrix_bytes() +
-                                size_t(f.strip / kQ4StripsOfTile) * gate.geom.tile_bytes() +
-                                size_t(f.unit) * gate.geom.unit_bytes;
-            q4_fetch<1>(fetch_to, plan.chunk, gate.data + from, in_tile, 1, lane, side1);
-            q4_fetch<1>(fetch_to + plan.chunk, plan.chunk, up.data + from, in_tile, 1, lane, side1);
+            q4_fetch<1>(fetch_to, plan.chunk, f_from, in_tile, 1, lane, side1);
+            q4_fetch<1>(fetch_to + plan.chunk, plan.chunk, f_from + gate_to_up, in_tile, 1, lane,
+                        side1);
+            f_from += size_t(plan.wn1) * gate.geom.unit_bytes;
         } else {
-            const size_t from = e * down.geom.matrix_bytes() +
-                                size_t(f.strip / kQ4StripsOfTile) * down.geom.tile_bytes() +
-                                size_t(f.unit) * down.geom.unit_bytes;
-            q4_fetch<2>(fetch_to, plan.chunk, down.data + from, in_tile, 2, lane, side2);
+            q4_fetch<2>(fetch_to, plan.chunk, f_from, in_tile, 2, lane, side2);
+            f_from += size_t(plan.wn2) * down.geom.unit_bytes;
         }
         ptx::cp_async_commit();
         advance(f);
@@ -580,88 +616,124 @@ __global__ void __launch_bounds__(MAX_WARPS * 32, 1)
             default: ptx::cp_async_wait<DEPTH - 1>(); break;
         }
         __syncwarp();
+#pragma unroll 1
         while (ahead < DEPTH && fetch()) {
         }
     };
-    while (ahead < DEPTH && fetch()) {
-    }
     const uint8_t* stage = ring;
     auto release = [&]() {
         --ahead;
         stage += stage_bytes;
         if (stage == ring + DEPTH * stage_bytes) stage = ring;
     };
+    locate();
+#pragma unroll 1
+    while (ahead < DEPTH && fetch()) {
+    }
 
+    // Multiplies the warp's pairs of an item with the columns of its tile of tokens (row(m, p) is
+    // piece p of its m-th token's row) and puts the sums to [wn][strip or pair][2][column][17].
+    const int pitch = plan.max_columns * 17;
+    auto product = [&](const int4& tile, const Q4Geom& geom, int pieces, int columns_log, int place,
+                       auto&& row, Walk& w) {
+        const int columns = tile.z << columns_log;
+        auto run = [&](auto nt_) {
+            constexpr int NT = decltype(nt_)::value;
+            // columns that do not exist repeat the first, and their sums are not used
+            const uint16_t* col[NT];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const int j = nt * 8 + r, m = j >> columns_log, p = j - (m << columns_log);
+                const bool is = m < tile.z && p < pieces;
+                col[nt] = row(is ? m : 0, is ? p : 0) + c * 8;
+            }
+            float total[2][NT][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) total[0][nt][i] = total[1][nt][i] = 0.0f;
+#pragma unroll 1
+            while (w.left > 0) {
+                const uint16_t* here[NT];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) here[nt] = col[nt] + w.unit * kQ4UnitN;
+                advance(w);
+                if (tile.w) {
+                    acquire();
+                    chunk_pair_centred<NT>(stage, plan.chunk, geom, lane, here, total);
+                } else {
+                    // all four blocks' words at once, while the stage is waited for
+                    uint4 x[4][NT];
+#pragma unroll
+                    for (int b = 0; b < 4; ++b)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            x[b][nt] = *reinterpret_cast<const uint4*>(here[nt] + b * 32);
+                    acquire();
+                    chunk_pair<NT, GROUP, ZEROS>(stage, plan.chunk, geom, lane, x, total);
+                }
+                release();
+            }
+            float* mine = sums + place * 2 * pitch + r;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int j = nt * 8 + 2 * c + i;
+                    if (j < columns)
+#pragma unroll
+                        for (int m = 0; m < 2; ++m) {
+                            mine[m * pitch + j * 17] = total[m][nt][i];
+                            mine[m * pitch + j * 17 + 8] = total[m][nt][i + 2];
+                        }
+                }
+        };
+        if (NT_MOST == 1 || columns <= 8)
+            run(std::integral_constant<int, 1>());
+        else
+            run(std::integral_constant<int, NT_MOST>());
+    };
+
+    // ---- the items
     bool hidden_ready = false;
     int item = item_s[0];
     while (item < items) {
         __syncthreads();  // the sums and item_s are free again
-        int claimed = 0;  // the item after the next
-        if (tid == 0) claimed = atomicAdd(a.counters, 1);
+        if (tid == 0) claimed = atomicAdd(a.counters, 1);  // the item after the next
         Walk w = walk(item);
-        if (w.kind == 0) {
+        if (item < first_items) {
             const int4 tile = tile_s[w.tile];
-            const int columns = tile.z * plan.x_columns;
-            by_tiles(columns, tile.w != 0, [&](auto nt_, auto centred) {
-                constexpr int NT = decltype(nt_)::value;
-                constexpr bool CENTRED = decltype(centred)::value;
-                // columns that do not exist repeat the first, and their sums are not used
-                const uint16_t* col[NT];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const int j = nt * 8 + r, m = j / plan.x_columns, p = j - m * plan.x_columns;
-                    const bool is = m < tile.z && p < plan.x_pieces;
-                    const int token = member_s[tile.y + (is ? m : 0)] / a.top;
-                    col[nt] = a.xp + (size_t(token) * plan.x_pieces + (is ? p : 0)) * x_padded + c * 8;
-                }
-                float total[2][NT][4];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) total[0][nt][i] = total[1][nt][i] = 0.0f;
-#pragma unroll 1
-                for (; !done(w); advance(w)) {
-                    acquire();
-                    const uint16_t* here[NT];
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) here[nt] = col[nt] + w.unit * kQ4UnitN;
-                    chunk_pair<NT, CENTRED>(stage, plan.chunk, gate.geom, lane, here, total);
-                    release();
-                }
-                float* mine = sums + warp * 2 * max_columns * 17 + r;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int j = nt * 8 + 2 * c + i;
-                        if (j < columns)
-#pragma unroll
-                            for (int m = 0; m < 2; ++m) {
-                                mine[(m * max_columns + j) * 17] = total[m][nt][i];
-                                mine[(m * max_columns + j) * 17 + 8] = total[m][nt][i + 2];
-                            }
-                    }
-            });
+            product(
+                tile, gate.geom, plan.x_pieces, plan.x_columns_log, wn1 * strips_item + wm1,
+                [&](int m, int p) {
+                    const int token = member_s[tile.y + m] / a.top;
+                    return a.xp + (size_t(token) * plan.x_pieces + p) * x_padded;
+                },
+                w);
             __syncthreads();
-            for (int i = tid; i < tile.z * kQ4StripK; i += threads) {
-                const int m = i / kQ4StripK, k = i % kQ4StripK, f_at = w.strip * kQ4StripK + k;
+            const int strip0 = (item - w.tile * strip_groups) * strips_item;
+            const int width = strips_item * kQ4StripK;
+            for (int i = tid; i < tile.z * width; i += threads) {
+                const int m = i / width, k = i - m * width;
+                const int f_at = strip0 * kQ4StripK + k;
+                if (f_at >= strips * kQ4StripK) continue;
                 float g = 0.0f, u = 0.0f;
                 for (int p = 0; p < plan.x_pieces; ++p) {
-                    const float* from = sums + (m * plan.x_columns + p) * 17 + k;
-                    for (int q = 0; q < warps; ++q) {
-                        g += from[q * 2 * max_columns * 17];
-                        u += from[(q * 2 + 1) * max_columns * 17];
+                    const float* from = sums + (k / kQ4StripK) * 2 * pitch +
+                                        ((m << plan.x_columns_log) + p) * 17 + k % kQ4StripK;
+#pragma unroll 4
+                    for (int q = 0; q < plan.wn1; ++q) {
+                        g += from[q * strips_item * 2 * pitch];
+                        u += from[q * strips_item * 2 * pitch + pitch];
                     }
                 }
                 const int slot = member_s[tile.y + m];
-                const float h =
-                    f_at < a.F ? g / (1.0f + expf(-g)) * u * a.weights[slot] : 0.0f;
+                const float h = f_at < a.F ? g / (1.0f + expf(-g)) * u * a.weights[slot] : 0.0f;
                 float piece[3];
                 split_pieces<3>(h, piece);
-                if (plan.h_pieces == 2 && fabsf(h) < 1e38f) {
+                if (plan.h_pieces == 2 && fabsf(h) < 1e38f)
                     // the second piece rounded to nearest: 2^-16 of the value at most
                     piece[1] = __bfloat162float(__float2bfloat16_rn(h - piece[0]));
-                }
                 Magnitudes magnitude;
                 magnitude.add(__float_as_uint(h));
                 if (magnitude.special<float>()) atomicOr(a.h_special + slot, 1);
@@ -670,134 +742,165 @@ __global__ void __launch_bounds__(MAX_WARPS * 32, 1)
                         uint16_t(__float_as_uint(piece[p]) >> 16);
             }
             // past F: down's weights are zero there, but not whatever the scratch holds
-            if (w.strip == strips - 1) {
-                const int from = strips * kQ4StripK, width = h_padded - from;
-                for (int i = tid; i < tile.z * plan.h_pieces * width; i += threads) {
-                    const int row = i / width, m = row / plan.h_pieces;
-                    a.hp[(size_t(member_s[tile.y + m]) * plan.h_pieces + row % plan.h_pieces) *
+            if (strip0 + strips_item >= strips) {
+                const int from = strips * kQ4StripK, rest = h_padded - from;
+                for (int i = tid; i < tile.z * plan.h_pieces * rest; i += threads) {
+                    const int line = i / rest, m = line / plan.h_pieces;
+                    a.hp[(size_t(member_s[tile.y + m]) * plan.h_pieces + line % plan.h_pieces) *
                              h_padded +
-                         from + i % width] = 0;
+                         from + i % rest] = 0;
                 }
             }
             __syncthreads();
             if (tid == 0) ptx::red_release_gpu_add(a.counters + 1, 1);
-        } else {
+        } else if (item < first_items + second_items) {
             if (!hidden_ready) {
-                // bounded; when it gives up, the rest is computed from what the scratch holds
-                if (tid == 0) {
-                    const unsigned long long t0 = ptx::globaltimer_ns();
-                    while (ptx::ld_acquire_gpu(a.counters + 1) < first_items && !abort_s)
-                        if (ptx::globaltimer_ns() - t0 > WAIT_LIMIT_NS) {
-                            abort_s = 1;
-                            atomicExch(a.err, kErrWaitTimeout);
-                        }
+                wait_count(a.counters + 1, first_items, &abort_s, a.err);
+                // tiles with a hidden value that the plain form cannot take
+                for (int k = tid; k < tiles; k += threads) {
+                    const int4 tile = tile_s[k];
+                    int special = 0;
+                    for (int i = 0; i < tile.z; ++i)
+                        special |= __ldcg(a.h_special + member_s[tile.y + i]);
+                    tile_s[k].w = special;
                 }
                 __syncthreads();
-                __threadfence();
                 hidden_ready = true;
             }
-            float* slab = sums + warp * a.T * 32;
-            for (int i = lane; i < a.T * 32; i += 32) slab[i] = 0.0f;
-            __syncwarp();
-            while (!done(w)) {
-                const int4 tile = tile_s[w.tile];
-                const int columns = tile.z * plan.h_columns;
-                int special = 0;
-                for (int i = lane; i < tile.z; i += 32) special |= a.h_special[member_s[tile.y + i]];
-                special = __any_sync(0xffffffffu, special);
-                by_tiles(columns, special != 0, [&](auto nt_, auto centred) {
-                    constexpr int NT = decltype(nt_)::value;
-                    constexpr bool CENTRED = decltype(centred)::value;
-                    const uint16_t* col[NT];
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        const int j = nt * 8 + r, m = j / plan.h_columns, p = j - m * plan.h_columns;
-                        const bool is = m < tile.z && p < plan.h_pieces;
-                        const int slot = member_s[tile.y + (is ? m : 0)];
-                        col[nt] =
-                            a.hp + (size_t(slot) * plan.h_pieces + (is ? p : 0)) * h_padded + c * 8;
-                    }
-                    float total[2][NT][4];
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) total[0][nt][i] = total[1][nt][i] = 0.0f;
-                    const int this_tile = w.tile;
-#pragma unroll 1
-                    for (; !done(w) && w.tile == this_tile; advance(w)) {
-                        acquire();
-                        const uint16_t* here[NT];
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) here[nt] = col[nt] + w.unit * kQ4UnitN;
-                        chunk_pair<NT, CENTRED>(stage, plan.chunk, down.geom, lane, here, total);
-                        release();
-                    }
-                    // a token's pieces: two columns of this lane, or these and the first of the
-                    // next lane's
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        const int j = nt * 8 + 2 * c, m = j / plan.h_columns;
-                        const int token = m < tile.z ? member_s[tile.y + m] / a.top : 0;
-#pragma unroll
-                        for (int h = 0; h < 2; ++h)
-#pragma unroll
-                            for (int i = 0; i < 4; i += 2) {
-                                float v = total[h][nt][i] + total[h][nt][i + 1];
-                                if (plan.h_columns == 4) {
-                                    const float third =
-                                        __shfl_down_sync(0xffffffffu, total[h][nt][i], 1);
-                                    v += third;
-                                    if (c & 1) continue;
-                                }
-                                if (m < tile.z) slab[token * 32 + h * 16 + r + 4 * i] += v;
-                            }
-                    }
-                    __syncwarp();
-                });
+            const int4 tile = tile_s[w.tile];
+            product(
+                tile, down.geom, plan.h_pieces, plan.h_columns_log, wn2 * pairs_item + wm2,
+                [&](int m, int p) {
+                    return a.hp + (size_t(member_s[tile.y + m]) * plan.h_pieces + p) * h_padded;
+                },
+                w);
+            __syncthreads();
+            const int group = item - first_items - w.tile * pair_groups;
+            const int width = pairs_item * 32;
+            for (int i = tid; i < tile.z * width; i += threads) {
+                const int m = i / width, k = i - m * width, d = group * width + k;
+                if (d >= a.D) continue;
+                float v = 0.0f;
+                for (int p = 0; p < plan.h_pieces; ++p) {
+                    const float* from = sums + (k / kQ4StripK) * pitch +
+                                        ((m << plan.h_columns_log) + p) * 17 + k % kQ4StripK;
+#pragma unroll 4
+                    for (int q = 0; q < plan.wn2; ++q) v += from[q * pairs_item * 2 * pitch];
+                }
+                a.z[size_t(member_s[tile.y + m]) * a.D + d] = v;
             }
             __syncthreads();
-            const int i2 = item - first_items, block = i2 / parts, part = i2 - block * parts;
-            auto put = [&](int t, int d, float v) {
-                if (d < a.D) store_from_float(a.y, a.dtype, t * a.ldy + d, v);
-            };
+            if (tid == 0) ptx::red_release_gpu_add(a.counters + 2 + group, 1);
+        } else {
+            // 32 columns of the output: each token's rows in the order of its experts
+            const int pair = item - first_items - second_items;
+            wait_count(a.counters + 2 + pair / pairs_item, tiles, &abort_s, a.err);
             for (int i = tid; i < a.T * 32; i += threads) {
+                const int t = i / 32, d = pair * 32 + i % 32;
+                if (d >= a.D) continue;
                 float v = 0.0f;
-                for (int q = 0; q < warps; ++q) v += sums[q * a.T * 32 + i];
-                const int t = i / 32, d = block * 32 + i % 32;
-                if (parts == 1)
-                    put(t, d, v);
-                else if (d < a.D)
-                    a.parts[(size_t(part) * a.T + t) * a.D + d] = v;
-            }
-            if (parts > 1) {
-                __syncthreads();
-                if (tid == 0) {
-                    __threadfence();
-                    last_s = atomicAdd(a.counters + 2 + block, 1) == parts - 1;
-                    __threadfence();
-                }
-                __syncthreads();
-                if (last_s)
-                    for (int i = tid; i < a.T * 32; i += threads) {
-                        const int t = i / 32, d = block * 32 + i % 32;
-                        if (d >= a.D) continue;
-                        float v = 0.0f;
-                        for (int q = 0; q < parts; ++q)
-                            v += __ldcg(a.parts + (size_t(q) * a.T + t) * a.D + d);
-                        put(t, d, v);
-                    }
+                if (a.ids[t * a.top] >= 0)
+#pragma unroll 4
+                    for (int j = 0; j < a.top; ++j)
+                        v += __ldcg(a.z + size_t(t * a.top + j) * a.D + d);
+                store_from_float(a.y, a.dtype, t * a.ldy + d, v);
             }
         }
         if (tid == 0) item_s[0] = claimed;
         __syncthreads();
         item = next_item;
         next_item = item_s[0];
-        if (f_on == 0)  // the walk is through the item that was
+        if (f_on == 0) {  // the walk is through the item that was
             f = walk(item);
-        else if (--f_on == 1)  // and through the one that is
+            locate();
+        } else if (--f_on == 1) {  // and through the one that is
             f = walk(next_item);
+            locate();
+        }
     }
     ptx::cp_async_wait<0>();
+}
+
+template <class T>
+cudaError_t launch_route(const cudaLaunchConfig_t& config, const MoeArgs& a, int counters, int padded) {
+    if (a.router_dtype == SGEMM_FLOAT32)
+        return cudaLaunchKernelEx(&config, moe_route_kernel<T, float>, a, counters, padded);
+    if (a.router_dtype == SGEMM_BFLOAT16)
+        return cudaLaunchKernelEx(&config, moe_route_kernel<T, __nv_bfloat16>, a, counters, padded);
+    return cudaLaunchKernelEx(&config, moe_route_kernel<T, __half>, a, counters, padded);
+}
+
+template <int NT_MOST, int GROUP, bool ZEROS>
+cudaError_t launch_expert_kernel(const cudaLaunchConfig_t& config, const MoeArgs& a, const Stack& gate,
+                                 const Stack& up, const Stack& down, const MoePlan& plan) {
+    constexpr auto kernel = moe_expert_kernel<NT_MOST, GROUP, ZEROS>;
+    const cudaError_t err = set_smem_limit_once<kernel>(SMEM_LIMIT - 2048);
+    if (err != cudaSuccess) return err;
+    count_launch();
+    return cudaLaunchKernelEx(&config, kernel, a, gate, up, down, plan);
+}
+
+// The stacks' group size and zero points are known to the kernel where they are the same.
+template <int NT_MOST>
+cudaError_t launch_experts(const cudaLaunchConfig_t& config, const MoeArgs& a, const Stack& gate,
+                           const Stack& up, const Stack& down, const MoePlan& plan) {
+    if (gate.geom.group != down.geom.group || gate.geom.zeros != down.geom.zeros)
+        return launch_expert_kernel<NT_MOST, 0, false>(config, a, gate, up, down, plan);
+    switch (gate.geom.group + gate.geom.zeros) {
+        case 32: return launch_expert_kernel<NT_MOST, 32, false>(config, a, gate, up, down, plan);
+        case 33: return launch_expert_kernel<NT_MOST, 32, true>(config, a, gate, up, down, plan);
+        case 64: return launch_expert_kernel<NT_MOST, 64, false>(config, a, gate, up, down, plan);
+        case 65: return launch_expert_kernel<NT_MOST, 64, true>(config, a, gate, up, down, plan);
+        case 128: return launch_expert_kernel<NT_MOST, 128, false>(config, a, gate, up, down, plan);
+        default: return launch_expert_kernel<NT_MOST, 128, true>(config, a, gate, up, down, plan);
+    }
+}
+
+// How many warps split n, so that the CTAs are done first with `tiles` times `strips` pieces of
+// work of `units` chunk pairs each; an item costs some pairs besides.
+int choose_split(double tiles, int strips, int units, int ctas) {
+    constexpr double FIXED = 4.0;
+    double best_cost = 1e30;
+    int best = 1;
+    for (int wn = 1; wn <= WARPS; wn *= 2) {
+        if (wn > 1 && wn > units) break;
+        const int groups = (strips + WARPS / wn - 1) / (WARPS / wn);
+        const double rounds = std::ceil(tiles * groups / ctas);
+        const double cost = rounds * ((units + wn - 1) / wn + FIXED + 0.25 * wn);
+        if (cost < best_cost) {
+            best_cost = cost;
+            best = wn;
+        }
+    }
+    return best;
+}
+
+MoePlan make_plan(const sgemm_moe_layer& m, const Q4Geom& g, const Q4Geom& gd, int T, int sm_count) {
+    MoePlan p;
+    const int slots = T * m.top_k;
+    p.x_pieces = pieces_of(m.dtype);
+    p.x_columns_log = m.dtype == SGEMM_FLOAT32 ? 2 : p.x_pieces - 1;
+    // the hidden values: all 24 significant bits for float32, 16 for the 16-bit types
+    p.h_pieces = m.dtype == SGEMM_FLOAT32 ? 3 : 2;
+    p.h_columns_log = m.dtype == SGEMM_FLOAT32 ? 2 : 1;
+    // 16 columns at most: with 32, the matrix instructions take twice as long as reading the
+    // weights again from L2 for a second tile
+    p.capacity = 16 >> p.h_columns_log;
+    if (p.capacity > T) p.capacity = T;
+    p.max_columns = p.capacity << (p.x_columns_log > p.h_columns_log ? p.x_columns_log : p.h_columns_log);
+    const int chunk1 = q4_chunk_bytes(g.group, g.zeros), chunk2 = q4_chunk_bytes(gd.group, gd.zeros);
+    p.chunk = chunk1 > chunk2 ? chunk1 : chunk2;
+    p.smem = moe_offsets(p.max_columns, p.chunk, most_tiles(m.E, slots, p.capacity), slots, m.E).end;
+    p.pairs = (m.D + 31) / 32;
+    // tiles, about, if tokens picked experts at random
+    double missed = 1.0;
+    for (int t = 0; t < T; ++t) missed *= 1.0 - double(m.top_k) / m.E;
+    double tiles = m.E * (1.0 - missed);
+    if (tiles < double(slots) / p.capacity) tiles = double(slots) / p.capacity;
+    const int ctas = 2 * sm_count;
+    p.wn1 = choose_split(tiles, (m.F + kQ4StripK - 1) / kQ4StripK, g.units, ctas);
+    p.wn2 = choose_split(tiles, p.pairs, gd.units, ctas);
+    return p;
 }
 
 bool stack_fits(const sgemm_q4& w, int E, int N, int K) {
@@ -850,41 +953,12 @@ extern "C" int sgemm_moe(const sgemm_moe_layer* layer, const void* x, long long 
     int dev = -1;
     const DeviceInfo* info = current_device(&dev);
     if (!info) return SGEMM_ERR_NO_DEVICE;
-    if (set_smem_limit_once<moe_expert_kernel>(SMEM_LIMIT - 2048) != cudaSuccess)
-        return SGEMM_ERR_CUDA;
-
     const Q4Geom g = q4_geom(m.gate), gd = q4_geom(m.down);
     const int slots = T * m.top_k;
-    MoePlan plan;
-    plan.x_pieces = pieces_of(m.dtype);
-    plan.x_columns = m.dtype == SGEMM_FLOAT32 ? 4 : plan.x_pieces;
-    // the hidden values: all 24 significant bits for float32, 16 for the 16-bit types
-    plan.h_pieces = m.dtype == SGEMM_FLOAT32 ? 3 : 2;
-    plan.h_columns = m.dtype == SGEMM_FLOAT32 ? 4 : 2;
-    plan.capacity = 32 / plan.h_columns;  // 32 columns at most
-    if (plan.capacity > T) plan.capacity = T;
-    const int chunk1 = q4_chunk_bytes(g.group, g.zeros), chunk2 = q4_chunk_bytes(gd.group, gd.zeros);
-    plan.chunk = chunk1 > chunk2 ? chunk1 : chunk2;
-    const int max_columns =
-        plan.capacity * (plan.x_columns > plan.h_columns ? plan.x_columns : plan.h_columns);
-    const int max_tiles = most_tiles(m.E, slots, plan.capacity);
-    // two CTAs of 8 warps on an SM while their slabs leave room for it, else one of 12
-    int resident = 2;
-    plan.warps = 8;
-    plan.smem = moe_offsets(8, T, max_columns, plan.chunk, max_tiles, slots).end;
-    if ((plan.smem + 2048) * 2 > SMEM_SM) {
-        resident = 1;
-        plan.warps = 12;
-        plan.smem = moe_offsets(12, T, max_columns, plan.chunk, max_tiles, slots).end;
-    }
-    const int ctas = info->sm_count * resident;
-    plan.blocks = (m.D + 31) / 32;
-    plan.parts = (2 * ctas + plan.blocks - 1) / plan.blocks;
-    if (plan.parts > MAX_PARTS) plan.parts = MAX_PARTS;
-    if (plan.parts > max_tiles) plan.parts = max_tiles;
+    const MoePlan plan = make_plan(m, g, gd, T, info->sm_count);
 
     const int x_padded = g.units * kQ4UnitN, h_padded = gd.units * kQ4UnitN;
-    const int counters = 2 + plan.blocks;
+    const int counters = 2 + plan.pairs;
     size_t bytes = 0;
     auto take = [&](size_t n) {
         const size_t at = bytes;
@@ -895,7 +969,7 @@ extern "C" int sgemm_moe(const sgemm_moe_layer* layer, const void* x, long long 
     const size_t at_hp = take(size_t(slots) * plan.h_pieces * h_padded * 2);
     const size_t at_xs = take(size_t(T) * 4), at_hs = take(size_t(slots) * 4);
     const size_t at_counters = take(size_t(counters) * 4);
-    const size_t at_parts = take(plan.parts > 1 ? size_t(plan.parts) * T * m.D * 4 : 0);
+    const size_t at_z = take(size_t(slots) * m.D * 4);
     const size_t at_ids = take(ids ? 0 : side), at_weights = take(weights ? 0 : side);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     Scratch ws;
@@ -926,7 +1000,7 @@ extern "C" int sgemm_moe(const sgemm_moe_layer* layer, const void* x, long long 
     a.x_special = reinterpret_cast<int*>(base + at_xs);
     a.h_special = reinterpret_cast<int*>(base + at_hs);
     a.counters = reinterpret_cast<int*>(base + at_counters);
-    a.parts = reinterpret_cast<float*>(base + at_parts);
+    a.z = reinterpret_cast<float*>(base + at_z);
     a.err = info->error_word;
 
     cudaLaunchAttribute attrs[2];
@@ -942,17 +1016,21 @@ extern "C" int sgemm_moe(const sgemm_moe_layer* layer, const void* x, long long 
     config.gridDim = dim3(ROUTE_CTAS, T);
     config.blockDim = dim3(ROUTE_THREADS);
     config.numAttrs = 2;
-    cudaError_t err = cudaLaunchKernelEx(&config, moe_route_kernel, a, counters, x_padded);
+    cudaError_t err = m.dtype == SGEMM_FLOAT32    ? launch_route<float>(config, a, counters, x_padded)
+                      : m.dtype == SGEMM_BFLOAT16 ? launch_route<__nv_bfloat16>(config, a, counters, x_padded)
+                                                  : launch_route<__half>(config, a, counters, x_padded);
     if (err != cudaSuccess) return SGEMM_ERR_CUDA;
     count_launch();
-    config.gridDim = dim3(ctas);
-    config.blockDim = dim3(plan.warps * 32);
+    config.gridDim = dim3(2 * info->sm_count);
+    config.blockDim = dim3(THREADS);
     config.dynamicSmemBytes = plan.smem;
     config.numAttrs = 1;
     const Stack gate{static_cast<const uint8_t*>(m.gate.data), g};
     const Stack up{static_cast<const uint8_t*>(m.up.data), g};
     const Stack down{static_cast<const uint8_t*>(m.down.data), gd};
-    err = cudaLaunchKernelEx(&config, moe_expert_kernel, a, gate, up, down, plan);
-    count_launch();
+    if (plan.max_columns <= 8)
+        err = launch_experts<1>(config, a, gate, up, down, plan);
+    else
+        err = launch_experts<2>(config, a, gate, up, down, plan);
     return err == cudaSuccess ? SGEMM_OK : SGEMM_ERR_CUDA;
 }
