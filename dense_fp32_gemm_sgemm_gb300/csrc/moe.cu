@@ -38,7 +38,7 @@ constexpr int kMoeMaxE = 256;
 constexpr int kMoeMaxTop = 16;
 
 constexpr int ROUTE_CTAS = 8;  // of a token
-constexpr int ROUTE_THREADS = 256;
+constexpr int ROUTE_THREADS = 512, ROUTE_WARPS = ROUTE_THREADS / 32;
 
 constexpr int DEPTH = 4;        // stages of a warp's ring, a pair of chunks each
 constexpr int WARPS = 8, THREADS = WARPS * 32;
@@ -87,7 +87,7 @@ struct MoePlan {
 template <class T, class R>
 __device__ __forceinline__ float dot(const T* x, const R* w, int from, int to, int D, bool vec,
                                      int lane) {
-    constexpr int AHEAD = 4;  // octets in flight
+    constexpr int AHEAD = sizeof(T) + sizeof(R) > 4 ? 4 : 8;  // octets in flight
     float s = 0.0f;
     for (int u = from + lane; u < to; u += 32 * AHEAD) {
         Raw8<T> p[AHEAD];
@@ -140,8 +140,8 @@ __device__ __forceinline__ bool write_pieces(const MoeArgs& a, int t, int rank, 
 // CTA, a thread an expert. An expert is among them if fewer than `top` others go before it: a
 // larger logit, or an equal one and a lower index.
 __device__ __forceinline__ void choose(const MoeArgs& a, const float* logit, int t) {
-    __shared__ float part[3][ROUTE_THREADS / 32];
-    __shared__ int count[ROUTE_THREADS / 32];
+    __shared__ float part[3][ROUTE_WARPS];
+    __shared__ int count[ROUTE_WARPS];
     const int e = threadIdx.x, lane = e & 31, warp = e >> 5;
     const float mine = e < a.E ? logit[e] : -INFINITY;
     float biggest = mine;
@@ -154,7 +154,7 @@ __device__ __forceinline__ void choose(const MoeArgs& a, const float* logit, int
         for (int i = 0; i < a.E; ++i) before += logit[i] > mine || (logit[i] == mine && i < e);
     const bool chosen = e < a.E && before < a.top;
     __syncthreads();
-    for (int w = 0; w < ROUTE_THREADS / 32; ++w) biggest = fmaxf(biggest, part[0][w]);
+    for (int w = 0; w < ROUTE_WARPS; ++w) biggest = fmaxf(biggest, part[0][w]);
     // an infinite logit shares the weight with its equals, and so do logits that are all -infinity
     const float power = e < a.E ? (mine == biggest ? 1.0f : expf(mine - biggest)) : 0.0f;
     float all = power, some = chosen ? power : 0.0f;
@@ -170,7 +170,7 @@ __device__ __forceinline__ void choose(const MoeArgs& a, const float* logit, int
     }
     __syncthreads();
     float total = 0.0f;
-    for (int w = 0; w < ROUTE_THREADS / 32; ++w) total += part[a.renormalize ? 2 : 1][w];
+    for (int w = 0; w < ROUTE_WARPS; ++w) total += part[a.renormalize ? 2 : 1][w];
     int slot = __popc(mask & ((1u << lane) - 1));
     for (int w = 0; w < warp; ++w) slot += count[w];
     if (chosen) {
@@ -182,7 +182,7 @@ __device__ __forceinline__ void choose(const MoeArgs& a, const float* logit, int
 template <class T, class R>
 __global__ void __launch_bounds__(ROUTE_THREADS) moe_route_kernel(const MoeArgs a, int counters,
                                                                   int padded) {
-    __shared__ float mine[ROUTE_THREADS / 32];
+    __shared__ float mine[ROUTE_WARPS];
     __shared__ float logit[kMoeMaxE];          // of the first CTA
     __shared__ int special_of[ROUTE_CTAS];     // and there, each CTA's
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -201,13 +201,13 @@ __global__ void __launch_bounds__(ROUTE_THREADS) moe_route_kernel(const MoeArgs 
         }
         return;
     }
-    // Experts rank, rank + 8, ...: 8 / SPLIT of them at a time, each by SPLIT warps, so that few
-    // experts still use all warps.
+    // Experts rank, rank + 8, ...: so many warps for each that all have work.
     const int experts = (a.E - rank + ROUTE_CTAS - 1) / ROUTE_CTAS;  // of this CTA
-    const int split = experts >= 8 ? 1 : experts >= 4 ? 2 : experts >= 2 ? 4 : 8;
+    int split = 1;
+    while (split < ROUTE_WARPS && experts * split * 2 <= ROUTE_WARPS) split *= 2;
     const int octets = (a.D + 7) / 8, per = (octets + split - 1) / split;
     ptx::cluster_sync();  // the first CTA is there for what is stored to it
-    for (int i0 = 0; i0 < experts; i0 += 8 / split) {
+    for (int i0 = 0; i0 < experts; i0 += ROUTE_WARPS / split) {
         const int i = i0 + warp / split, part = warp % split;
         float s = 0.0f;
         if (i < experts) {
@@ -423,7 +423,9 @@ __global__ void __launch_bounds__(THREADS, 2)
     moe_expert_kernel(const MoeArgs a, const Stack gate, const Stack up, const Stack down,
                       const MoePlan plan) {
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int scan_s[WARPS], tiles_s, item_s[2];
+    __shared__ int scan_s[WARPS], tiles_s, item_s;
+    // the item after the current one, -1 while it is not known; two places in turn
+    __shared__ volatile int next_s[2];
     __shared__ volatile int abort_s;
     constexpr int warps = WARPS, threads = THREADS;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane >> 2, c = lane & 3;
@@ -442,11 +444,8 @@ __global__ void __launch_bounds__(THREADS, 2)
     if (tid == 0) abort_s = 0;
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
-    int claimed = 0, claimed2 = 0;
-    if (tid == 0) {
-        claimed = atomicAdd(a.counters, 1);
-        claimed2 = atomicAdd(a.counters, 1);
-    }
+    int claimed = 0;
+    if (tid == 0) claimed = atomicAdd(a.counters, 1);
 
     // The tokens of each expert, in order, in tiles; the same in every CTA. Tokens that want the
     // centred form have tiles of their own, so that they change nothing for the others. A token
@@ -496,8 +495,8 @@ __global__ void __launch_bounds__(THREADS, 2)
         }
         if (tid == threads - 1) tiles_s = (before + own) >> 16;
         if (tid == 0) {
-            item_s[0] = claimed;
-            item_s[1] = claimed2;
+            item_s = claimed;
+            next_s[0] = next_s[1] = -1;
         }
         __syncthreads();
         for (int i = tid; i < slots; i += threads) {
@@ -561,46 +560,63 @@ __global__ void __launch_bounds__(THREADS, 2)
     auto side_of = [&](const Q4Geom& g) {
         const int groups = kQ4UnitN / g.group;
         Q4Side s;
-        const bool zero = lane >= 2 * groups;
+        const bool zero = lane >= 2 * groups;  // zero points
         s.step = zero ? kQ4StripK : kQ4StripK * 2;
         s.from = kQ4CodeBytes + (zero ? groups * kQ4UnitK * 2 + (lane - 2 * groups) * kQ4UnitK
                                       : (lane >> 1) * kQ4UnitK * 2 + (lane & 1) * 16);
         s.any = lane < (2 + g.zeros) * groups;
         return s;
     };
-    const Q4Side side1 = side_of(gate.geom), side2 = side_of(down.geom);
     const ptrdiff_t gate_to_up = up.data - gate.data;
-    int next_item = item_s[1];
-    int f_on = 0;   // the walk is in the current item (0), the next (1) or through both (2)
+    int turn = 0;   // of next_s
+    int claim_at = 0;  // units left when the next item is claimed
+    int f_on = 0;   // the walk is in the current item (0) or the next (1)
     int ahead = 0;  // stages fetched and not used up
-    const uint8_t* f_from = nullptr;  // the unit that the walk is at
-    Walk f = walk(item_s[0]);
+    Walk f = walk(item_s);
+    // where the lane's next codes and scales or zero points are; from there to the second strip's,
+    // and to the next unit's
+    const uint8_t *f_codes = nullptr, *f_rest = nullptr;
+    ptrdiff_t f_codes2 = 0, f_rest2 = 0;
+    size_t f_step = 0;
+    bool f_any = false;
     auto locate = [&]() {
         if (f.left == 0) return;
         const Stack& stack = f.kind == 0 ? gate : down;
-        f_from = stack.data + tile_s[f.tile].x * stack.geom.matrix_bytes() +
-                 size_t(f.strip / kQ4StripsOfTile) * stack.geom.tile_bytes() +
-                 size_t(f.unit) * stack.geom.unit_bytes;
+        const int in_tile = f.strip % kQ4StripsOfTile;
+        const Q4Side side = side_of(stack.geom);
+        const uint8_t* unit = stack.data + tile_s[f.tile].x * stack.geom.matrix_bytes() +
+                              size_t(f.strip / kQ4StripsOfTile) * stack.geom.tile_bytes() +
+                              size_t(f.unit) * stack.geom.unit_bytes;
+        f_codes = unit + (lane >> 4) * (kQ4UnitK * 16) + (in_tile * kQ4StripK + (lane & 15)) * 16;
+        f_rest = unit + side.from + in_tile * side.step;
+        f_codes2 = f.kind == 0 ? gate_to_up : kQ4StripK * 16;
+        f_rest2 = f.kind == 0 ? gate_to_up : side.step;
+        f_step = size_t(f.kind == 0 ? plan.wn1 : plan.wn2) * stack.geom.unit_bytes;
+        f_any = side.any;
     };
     auto fetch = [&]() -> bool {
-        while (f.left == 0) {
-            if (f_on == 2) return false;
-            if (++f_on == 2) return false;
-            f = walk(next_item);
+        if (f.left == 0) {
+            if (f_on == 1) return false;
+            const int next = __shfl_sync(0xffffffffu, next_s[turn], 0);
+            if (next < 0) return false;
+            f = walk(next);
             locate();
+            f_on = 1;
+            if (f.left == 0) return false;
         }
-        const int in_tile = f.strip % kQ4StripsOfTile;
-        if (f.kind == 0) {
-            q4_fetch<1>(fetch_to, plan.chunk, f_from, in_tile, 1, lane, side1);
-            q4_fetch<1>(fetch_to + plan.chunk, plan.chunk, f_from + gate_to_up, in_tile, 1, lane,
-                        side1);
-            f_from += size_t(plan.wn1) * gate.geom.unit_bytes;
-        } else {
-            q4_fetch<2>(fetch_to, plan.chunk, f_from, in_tile, 2, lane, side2);
-            f_from += size_t(plan.wn2) * down.geom.unit_bytes;
+        const uint32_t to = fetch_to + lane * 16;
+        ptx::cp_async_16(to, f_codes, true);
+        ptx::cp_async_16(to + 512, f_codes + 2 * kQ4UnitK * 16, true);
+        ptx::cp_async_16(to + plan.chunk, f_codes + f_codes2, true);
+        ptx::cp_async_16(to + plan.chunk + 512, f_codes + f_codes2 + 2 * kQ4UnitK * 16, true);
+        if (f_any) {
+            ptx::cp_async_16(to + kQ4ChunkCodes, f_rest, true);
+            ptx::cp_async_16(to + plan.chunk + kQ4ChunkCodes, f_rest + f_rest2, true);
         }
         ptx::cp_async_commit();
-        advance(f);
+        f_codes += f_step;
+        f_rest += f_step;
+        --f.left;
         ++ahead;
         fetch_to += stage_bytes;
         if (fetch_to == ring_u32 + DEPTH * stage_bytes) fetch_to = ring_u32;
@@ -616,9 +632,7 @@ __global__ void __launch_bounds__(THREADS, 2)
             default: ptx::cp_async_wait<DEPTH - 1>(); break;
         }
         __syncwarp();
-#pragma unroll 1
-        while (ahead < DEPTH && fetch()) {
-        }
+        if (ahead < DEPTH && fetch() && ahead < DEPTH) fetch();
     };
     const uint8_t* stage = ring;
     auto release = [&]() {
@@ -630,6 +644,16 @@ __global__ void __launch_bounds__(THREADS, 2)
 #pragma unroll 1
     while (ahead < DEPTH && fetch()) {
     }
+
+    // The first thread's claim of the next item: none or through (0), wanted (1), asked for (2).
+    int claim = 0, ticket = 0;
+    auto claim_step = [&]() {
+        if (claim == 1)
+            ticket = atomicAdd(a.counters, 1);
+        else if (claim == 2)
+            next_s[turn] = ticket;
+        claim = claim == 1 ? 2 : 0;
+    };
 
     // Multiplies the warp's pairs of an item with the columns of its tile of tokens (row(m, p) is
     // piece p of its m-th token's row) and puts the sums to [wn][strip or pair][2][column][17].
@@ -654,6 +678,7 @@ __global__ void __launch_bounds__(THREADS, 2)
                 for (int i = 0; i < 4; ++i) total[0][nt][i] = total[1][nt][i] = 0.0f;
 #pragma unroll 1
             while (w.left > 0) {
+                if (warp == 0 && w.left <= claim_at) claim_step();
                 const uint16_t* here[NT];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) here[nt] = col[nt] + w.unit * kQ4UnitN;
@@ -696,11 +721,18 @@ __global__ void __launch_bounds__(THREADS, 2)
 
     // ---- the items
     bool hidden_ready = false;
-    int item = item_s[0];
+    int item = item_s;
     while (item < items) {
-        __syncthreads();  // the sums and item_s are free again
-        if (tid == 0) claimed = atomicAdd(a.counters, 1);  // the item after the next
+        // The next item is claimed when the first warp is near this one's end, not before: where
+        // there is about one item for each CTA, none should hold two. Far from the end of a phase
+        // it may be claimed at once.
+        claim = tid == 0;
+        const int phase_end = item < first_items ? first_items : first_items + second_items;
+        claim_at = item + 3 * int(gridDim.x) < phase_end ? INT_MAX : DEPTH + 1;
         Walk w = walk(item);
+#pragma unroll 1
+        while (ahead < DEPTH && fetch()) {
+        }
         if (item < first_items) {
             const int4 tile = tile_s[w.tile];
             product(
@@ -806,17 +838,18 @@ __global__ void __launch_bounds__(THREADS, 2)
                 store_from_float(a.y, a.dtype, t * a.ldy + d, v);
             }
         }
-        if (tid == 0) item_s[0] = claimed;
+        // all have read the other place since they took this item from it
+        if (tid == 0) next_s[turn ^ 1] = -1;
+        if (claim == 1) claim_step();
+        if (claim == 2) claim_step();
         __syncthreads();
-        item = next_item;
-        next_item = item_s[0];
+        item = next_s[turn];
+        turn ^= 1;
         if (f_on == 0) {  // the walk is through the item that was
             f = walk(item);
             locate();
-        } else if (--f_on == 1) {  // and through the one that is
-            f = walk(next_item);
-            locate();
         }
+        f_on = 0;
     }
     ptx::cp_async_wait<0>();
 }
