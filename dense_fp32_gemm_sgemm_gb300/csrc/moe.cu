@@ -40,7 +40,9 @@ constexpr int kMoeMaxTop = 16;
 constexpr int ROUTE_CTAS = 8;  // of a token
 constexpr int ROUTE_THREADS = 512, ROUTE_WARPS = ROUTE_THREADS / 32;
 
-constexpr int DEPTH = 4;        // stages of a warp's ring, a pair of chunks each
+constexpr int SET = 4;          // chunks that a warp multiplies with the same columns
+constexpr int DEPTH = 2;        // stages of a warp's ring, a set of chunks each
+constexpr int SUM_COLUMNS = 32;  // of a sum item
 constexpr int WARPS = 8, THREADS = WARPS * 32;
 constexpr int SMEM_LIMIT = 227 * 1024;
 
@@ -56,8 +58,11 @@ struct MoeArgs {
     size_t ldy;
     bool vec;  // rows of x and the router start on 16-byte boundaries
     // scratch
-    uint16_t* xp;      // pieces of x as bfloat16: [token][piece][D padded to units]
-    uint16_t* hp;      // pieces of the hidden values: [token and slot][piece][F padded]
+    // pieces as bfloat16, first staged for the plain form, then, x_form and h_form further, as they
+    // are for the centred form
+    uint16_t* xp;      // of x: [token][piece][D padded to units]
+    uint16_t* hp;      // of the hidden values: [token and slot][piece][F padded]
+    size_t x_form, h_form;
     int* x_special;    // [token]: nonzero where the plain form cannot take some value
     int* h_special;    // [token and slot]
     int* counters;     // 0: next item, 1: first items done, 2 ..: second items done of a group
@@ -77,7 +82,7 @@ struct MoePlan {
     int h_pieces, h_columns_log;  // and of a hidden row
     int max_columns;              // of a tile
     int wn1, wn2;                 // warps that split n in first and second items
-    int pairs;                    // pairs of strips of the output
+    int sets1, sets2;             // sets of a tile's hidden values (32) and of the output (64)
     int chunk, smem;
 };
 
@@ -119,19 +124,16 @@ __device__ __forceinline__ bool write_pieces(const MoeArgs& a, int t, int rank, 
     const int octets = padded / 8;
     for (int u = rank * ROUTE_THREADS + threadIdx.x; u < octets; u += ROUTE_CTAS * ROUTE_THREADS) {
         const Raw8<T> raw = load_raw8(x, u * 8, a.D, a.vec);
-        const uint32_t* words = reinterpret_cast<const uint32_t*>(&raw);
+        uint4 plain[P], centred[P];
+        float sums[P];  // not used: they are taken with the product
+        split_plain<P>(raw, magnitudes, plain, sums);
+        split_centred<P>(raw, centred);
 #pragma unroll
-        for (int i = 0; i < int(sizeof(T)) * 2; ++i) {
-            if constexpr (sizeof(T) == 4)
-                magnitudes.add(words[i]);
-            else
-                magnitudes.add2(words[i]);
+        for (int p = 0; p < P; ++p) {
+            uint16_t* to = a.xp + (size_t(t) * P + p) * padded;
+            reinterpret_cast<uint4*>(to)[u] = plain[p];
+            reinterpret_cast<uint4*>(to + a.x_form)[u] = centred[p];
         }
-        uint4 piece[P];
-        split_centred<P>(raw, piece);
-#pragma unroll
-        for (int p = 0; p < P; ++p)
-            reinterpret_cast<uint4*>(a.xp + (size_t(t) * P + p) * padded)[u] = piece[p];
     }
     return magnitudes.special<T>();
 }
@@ -249,7 +251,7 @@ __global__ void __launch_bounds__(ROUTE_THREADS) moe_route_kernel(const MoeArgs 
 struct MoeOffsets {
     int tiles;    // int4 each: expert, first member, members, whether the centred form is wanted
     int members;  // token and slot, by expert
-    int sums;     // [wn][strips or pairs][2][column][17]
+    int sums;     // [wn][set][chunk][column][17]
     int masks;    // in the same place before: [expert][form][2], and [expert]
     int ring;
     int end;
@@ -261,10 +263,10 @@ __host__ __device__ constexpr MoeOffsets moe_offsets(int max_columns, int chunk,
     o.members = tiles * 16;
     o.sums = (o.members + slots * 2 + 15) / 16 * 16;
     o.masks = o.sums;
-    int most = WARPS * 2 * max_columns * 17 * 4;
+    int most = WARPS * SET * max_columns * 17 * 4;
     if (most < E * 20) most = E * 20;
     o.ring = o.sums + (most + 15) / 16 * 16;
-    o.end = o.ring + WARPS * DEPTH * 2 * chunk;
+    o.end = o.ring + WARPS * DEPTH * SET * chunk;
     return o;
 }
 
@@ -289,66 +291,62 @@ __host__ __device__ constexpr int most_tiles(int E, int slots, int capacity) {
     return slots / capacity + 2 * (E < slots ? E : slots);
 }
 
-// One pair of chunks (at stage and stage + chunk) times NT tiles of 8 columns, added to total as in
-// q4_chunk. x[b][nt]: the lane's 8 values of block b of column 8 nt + r, as they are. GROUP 0:
-// the stack's own group size and zero points.
-template <int NT, int GROUP, bool ZEROS>
-__device__ __forceinline__ void chunk_pair(const uint8_t* stage, int chunk, const Q4Geom& geom, int lane,
-                                           const uint4 (&x)[4][NT], float (&total)[2][NT][4]) {
+// MT chunks (at stage, stage + chunk, ...) times NT tiles of 8 columns, added to total as in
+// q4_chunk. x(b, nt): the lane's 8 values of block b of column 8 nt + r, staged for the plain form.
+// GROUP 0: the stack's own group size and zero points.
+template <int MT, int NT, int GROUP, bool ZEROS, class X>
+__device__ __forceinline__ void chunk_set(const uint8_t* stage, int chunk, const Q4Geom& geom, int lane,
+                                          X&& x, float (*total)[NT][4]) {
     const int r = lane >> 2;
     const int blocks = GROUP ? GROUP / 32 : geom.group / 32;
     const int groups = GROUP ? kQ4UnitN / (GROUP ? GROUP : 32) : kQ4UnitN / geom.group;
     const bool zeros = GROUP ? ZEROS : geom.zeros != 0;
-    const __nv_bfloat162 scale = __float2bfloat162_rn(kQ4Scale);
-    const __nv_bfloat162 scale16 = __float2bfloat162_rn(kQ4Scale16);
     const uint32_t one = zeros ? 0x00010001u : 0x00080008u;
     const uint32_t ones[4] = {one, one, one << 4, one << 4};
-    float acc[2][NT][4], sum[NT][4];
-    int left = blocks;  // of the group
-    bool first = true;
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-        if (GROUP ? b % blocks == 0 : first) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[0][nt][i] = acc[1][nt][i] = sum[nt][i] = 0.0f;
-            first = false;
-        }
-        uint32_t xs[NT][4];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const uint32_t w[4] = {x[b][nt].x, x[b][nt].y, x[b][nt].z, x[b][nt].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const __nv_bfloat162 s = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]),
-                                                 (i & 1) ? scale16 : scale);
-                xs[nt][i] = *reinterpret_cast<const uint32_t*>(&s);
-            }
-            mma_bf16(sum[nt], ones, xs[nt][0], xs[nt][1]);
-            mma_bf16(sum[nt], ones, xs[nt][2], xs[nt][3]);
-        }
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-            const uint32_t* codes =
-                reinterpret_cast<const uint32_t*>(stage + m * chunk + b * 256) + lane;
-            uint32_t lo[4], hi[4];
-            q4_plain(codes[0], lo);
-            q4_plain(codes[32], hi);
-            const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]};
-            const uint32_t a1[4] = {lo[2], hi[2], lo[3], hi[3]};
+    constexpr int BLOCKS = GROUP ? GROUP / 32 : 1;
+#pragma unroll(NT == 1 && GROUP ? 4 : 1)
+    for (int g = 0; g < groups; ++g) {
+        float acc[MT][NT][4], sum[NT][4];
+        auto block = [&](int b, bool first) {
+            uint4 v[NT];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                mma_bf16(acc[m][nt], a0, xs[nt][0], xs[nt][1]);
-                mma_bf16(acc[m][nt], a1, xs[nt][2], xs[nt][3]);
+                v[nt] = x(b, nt);
+                if (first)
+                    mma_bf16_first(sum[nt], ones, v[nt].x, v[nt].y);
+                else
+                    mma_bf16(sum[nt], ones, v[nt].x, v[nt].y);
+                mma_bf16(sum[nt], ones, v[nt].z, v[nt].w);
             }
-        }
-        if (GROUP ? (b + 1) % blocks != 0 : --left > 0) continue;
-        left = blocks;
-        first = true;
-        const int g = b / blocks;
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
+            for (int m = 0; m < MT; ++m) {
+                const uint32_t* codes =
+                    reinterpret_cast<const uint32_t*>(stage + m * chunk + b * 256) + lane;
+                uint32_t lo[4], hi[4];
+                q4_plain(codes[0], lo);
+                q4_plain(codes[32], hi);
+                const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]};
+                const uint32_t a1[4] = {lo[2], hi[2], lo[3], hi[3]};
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    if (first)
+                        mma_bf16_first(acc[m][nt], a0, v[nt].x, v[nt].y);
+                    else
+                        mma_bf16(acc[m][nt], a0, v[nt].x, v[nt].y);
+                    mma_bf16(acc[m][nt], a1, v[nt].z, v[nt].w);
+                }
+            }
+        };
+        if constexpr (GROUP != 0) {
+#pragma unroll
+            for (int k = 0; k < BLOCKS; ++k) block(g * BLOCKS + k, k == 0);
+        } else {
+            block(g * blocks, true);
+#pragma unroll 1
+            for (int k = 1; k < blocks; ++k) block(g * blocks + k, false);
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
             const uint8_t* side = stage + m * chunk + kQ4ChunkCodes;
             const uint16_t* scales = reinterpret_cast<const uint16_t*>(side) + g * kQ4StripK + r;
             const float s0 = q4_scale(scales[0], geom.fp16), s1 = q4_scale(scales[8], geom.fp16);
@@ -363,22 +361,22 @@ __device__ __forceinline__ void chunk_pair(const uint8_t* stage, int chunk, cons
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     // the sums are alike in all rows of the constant operand
-                    const float v =
+                    const float d =
                         fmaf(i < 2 ? -z0 : -z1, sum[nt][i & 1], acc[m][nt][i]) * kQ4Unscale;
-                    total[m][nt][i] = fmaf(i < 2 ? s0 : s1, v, total[m][nt][i]);
+                    total[m][nt][i] = fmaf(i < 2 ? s0 : s1, d, total[m][nt][i]);
                 }
         }
     }
 }
 // The same in the centred form. Rarely run, so kept small rather than unrolled.
 template <int NT>
-__device__ __forceinline__ void chunk_pair_centred(const uint8_t* stage, int chunk, const Q4Geom& geom,
-                                                   int lane, const uint16_t* const (&col)[NT],
-                                                   float (&total)[2][NT][4]) {
+__device__ __forceinline__ void chunk_set_centred(const uint8_t* stage, int chunk, const Q4Geom& geom,
+                                                  int lane, const uint16_t* const (&col)[NT],
+                                                  float (&total)[SET][NT][4]) {
     const int r = lane >> 2;
     const int blocks = geom.group / 32, groups = kQ4UnitN / geom.group;
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
+    for (int m = 0; m < SET; ++m)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const uint8_t* side = stage + m * chunk + kQ4ChunkCodes;
@@ -436,10 +434,10 @@ __global__ void __launch_bounds__(THREADS, 2)
     int4* tile_s = reinterpret_cast<int4*>(smem + at.tiles);
     uint16_t* member_s = reinterpret_cast<uint16_t*>(smem + at.members);
     float* sums = reinterpret_cast<float*>(smem + at.sums);
-    uint8_t* ring = smem + at.ring + warp * DEPTH * 2 * plan.chunk;
-    // phase 1: wm1 strips of wn1 warps each; phase 2: wm2 pairs of strips of wn2 warps each
-    const int wn1 = warp % plan.wn1, wm1 = warp / plan.wn1, strips_item = warps / plan.wn1;
-    const int wn2 = warp % plan.wn2, wm2 = warp / plan.wn2, pairs_item = warps / plan.wn2;
+    uint8_t* ring = smem + at.ring + warp * DEPTH * SET * plan.chunk;
+    // first items: wm1 sets of wn1 warps each; second items: wm2 sets of wn2 warps each
+    const int wn1 = warp % plan.wn1, wm1 = warp / plan.wn1, sets1_item = warps / plan.wn1;
+    const int wn2 = warp % plan.wn2, wm2 = warp / plan.wn2, sets2_item = warps / plan.wn2;
 
     if (tid == 0) abort_s = 0;
     ptx::griddep_launch_dependents();
@@ -513,16 +511,15 @@ __global__ void __launch_bounds__(THREADS, 2)
         __syncthreads();
     }
     const int tiles = tiles_s;
-    const int strips = (a.F + kQ4StripK - 1) / kQ4StripK;
-    const int strip_groups = (strips + strips_item - 1) / strips_item;
-    const int pair_groups = (plan.pairs + pairs_item - 1) / pairs_item;
-    const int first_items = tiles * strip_groups, second_items = tiles * pair_groups;
-    const int items = first_items + second_items + plan.pairs;
+    const int groups1 = (plan.sets1 + sets1_item - 1) / sets1_item;
+    const int groups2 = (plan.sets2 + sets2_item - 1) / sets2_item;
+    const int first_items = tiles * groups1, second_items = tiles * groups2;
+    const int items = first_items + second_items + (a.D + SUM_COLUMNS - 1) / SUM_COLUMNS;
     const int x_padded = gate.geom.units * kQ4UnitN, h_padded = down.geom.units * kQ4UnitN;
 
-    // Where a warp is in an item. kind 0: strip `strip` of gate and up of the tile's expert, units
-    // wn1, wn1 + wn1's count, ...; 1: strips `strip` and + 1 of down, units wn2, ...; 2: nothing to
-    // fetch.
+    // Where a warp is in an item. kind 0: strips `strip` and + 1 of gate and up of the tile's
+    // expert, units wn1, wn1 + plan.wn1, ...; 1: strips `strip` .. + 3 of down, units wn2, ...;
+    // 2: nothing to fetch. The packed columns are a multiple of eight strips.
     struct Walk {
         int kind, strip, tile, unit, left;
     };
@@ -532,18 +529,19 @@ __global__ void __launch_bounds__(THREADS, 2)
         w.strip = w.tile = w.unit = w.left = 0;
         if (item < first_items) {
             w.kind = 0;
-            w.tile = item / strip_groups;
-            w.strip = (item - w.tile * strip_groups) * strips_item + wm1;
+            w.tile = item / groups1;
+            const int set = (item - w.tile * groups1) * sets1_item + wm1;
+            w.strip = 2 * set;
             w.unit = wn1;
-            if (w.strip < strips) w.left = (gate.geom.units - wn1 + plan.wn1 - 1) / plan.wn1;
+            if (set < plan.sets1) w.left = (gate.geom.units - wn1 + plan.wn1 - 1) / plan.wn1;
         } else if (item < first_items + second_items) {
             item -= first_items;
             w.kind = 1;
-            w.tile = item / pair_groups;
-            const int pair = (item - w.tile * pair_groups) * pairs_item + wm2;
-            w.strip = 2 * pair;
+            w.tile = item / groups2;
+            const int set = (item - w.tile * groups2) * sets2_item + wm2;
+            w.strip = 4 * set;
             w.unit = wn2;
-            if (pair < plan.pairs) w.left = (down.geom.units - wn2 + plan.wn2 - 1) / plan.wn2;
+            if (set < plan.sets2) w.left = (down.geom.units - wn2 + plan.wn2 - 1) / plan.wn2;
         }
         return w;
     };
@@ -555,7 +553,7 @@ __global__ void __launch_bounds__(THREADS, 2)
     // ---- the ring
     const uint32_t ring_u32 = ptx::smem_u32(ring);
     uint32_t fetch_to = ring_u32;
-    const int stage_bytes = 2 * plan.chunk;
+    const int stage_bytes = SET * plan.chunk;
     // what a lane copies besides codes, for the gate and up stacks and for down
     auto side_of = [&](const Q4Geom& g) {
         const int groups = kQ4UnitN / g.group;
@@ -573,10 +571,11 @@ __global__ void __launch_bounds__(THREADS, 2)
     int f_on = 0;   // the walk is in the current item (0) or the next (1)
     int ahead = 0;  // stages fetched and not used up
     Walk f = walk(item_s);
-    // where the lane's next codes and scales or zero points are; from there to the second strip's,
-    // and to the next unit's
+    // where the lane's next codes and scales or zero points are; from there to the second chunk's
+    // (the fourth's is as far from the third's), to the third's, and to the next unit's
     const uint8_t *f_codes = nullptr, *f_rest = nullptr;
     ptrdiff_t f_codes2 = 0, f_rest2 = 0;
+    int f_codes3 = 0, f_rest3 = 0;
     size_t f_step = 0;
     bool f_any = false;
     auto locate = [&]() {
@@ -591,6 +590,8 @@ __global__ void __launch_bounds__(THREADS, 2)
         f_rest = unit + side.from + in_tile * side.step;
         f_codes2 = f.kind == 0 ? gate_to_up : kQ4StripK * 16;
         f_rest2 = f.kind == 0 ? gate_to_up : side.step;
+        f_codes3 = (f.kind + 1) * (kQ4StripK * 16);
+        f_rest3 = (f.kind + 1) * side.step;
         f_step = size_t(f.kind == 0 ? plan.wn1 : plan.wn2) * stack.geom.unit_bytes;
         f_any = side.any;
     };
@@ -604,14 +605,22 @@ __global__ void __launch_bounds__(THREADS, 2)
             f_on = 1;
             if (f.left == 0) return false;
         }
-        const uint32_t to = fetch_to + lane * 16;
-        ptx::cp_async_16(to, f_codes, true);
-        ptx::cp_async_16(to + 512, f_codes + 2 * kQ4UnitK * 16, true);
-        ptx::cp_async_16(to + plan.chunk, f_codes + f_codes2, true);
-        ptx::cp_async_16(to + plan.chunk + 512, f_codes + f_codes2 + 2 * kQ4UnitK * 16, true);
-        if (f_any) {
-            ptx::cp_async_16(to + kQ4ChunkCodes, f_rest, true);
-            ptx::cp_async_16(to + plan.chunk + kQ4ChunkCodes, f_rest + f_rest2, true);
+        uint32_t to = fetch_to + lane * 16;
+        const uint8_t *codes = f_codes, *rest = f_rest;
+#pragma unroll
+        for (int m = 0; m < SET; m += 2) {
+            const uint32_t to2 = to + plan.chunk;
+            ptx::cp_async_16(to, codes, true);
+            ptx::cp_async_16(to + 512, codes + 2 * kQ4UnitK * 16, true);
+            ptx::cp_async_16(to2, codes + f_codes2, true);
+            ptx::cp_async_16(to2 + 512, codes + f_codes2 + 2 * kQ4UnitK * 16, true);
+            if (f_any) {
+                ptx::cp_async_16(to + kQ4ChunkCodes, rest, true);
+                ptx::cp_async_16(to2 + kQ4ChunkCodes, rest + f_rest2, true);
+            }
+            to = to2 + plan.chunk;
+            codes += f_codes3;
+            rest += f_rest3;
         }
         ptx::cp_async_commit();
         f_codes += f_step;
@@ -622,17 +631,16 @@ __global__ void __launch_bounds__(THREADS, 2)
         if (fetch_to == ring_u32 + DEPTH * stage_bytes) fetch_to = ring_u32;
         return true;
     };
-    // Waits for the oldest stage and fills up the ring again; the stage used before it is free.
+    // Fills up the ring again, the stage used before being free, and waits for the oldest.
+    static_assert(DEPTH == 2, "the waits");
     auto acquire = [&]() {
-        if (ahead == 0) fetch();
-        switch (ahead) {
-            case 1: ptx::cp_async_wait<0>(); break;
-            case 2: ptx::cp_async_wait<1>(); break;
-            case 3: ptx::cp_async_wait<2>(); break;
-            default: ptx::cp_async_wait<DEPTH - 1>(); break;
-        }
         __syncwarp();
         if (ahead < DEPTH && fetch() && ahead < DEPTH) fetch();
+        if (ahead == DEPTH)
+            ptx::cp_async_wait<DEPTH - 1>();
+        else
+            ptx::cp_async_wait<0>();
+        __syncwarp();
     };
     const uint8_t* stage = ring;
     auto release = [&]() {
@@ -655,8 +663,8 @@ __global__ void __launch_bounds__(THREADS, 2)
         claim = claim == 1 ? 2 : 0;
     };
 
-    // Multiplies the warp's pairs of an item with the columns of its tile of tokens (row(m, p) is
-    // piece p of its m-th token's row) and puts the sums to [wn][strip or pair][2][column][17].
+    // Multiplies the warp's set of an item with the columns of its tile of tokens (row(m, p) is
+    // piece p of its m-th token's row) and puts the sums to [wn][set][chunk][column][17].
     const int pitch = plan.max_columns * 17;
     auto product = [&](const int4& tile, const Q4Geom& geom, int pieces, int columns_log, int place,
                        auto&& row, Walk& w) {
@@ -671,11 +679,13 @@ __global__ void __launch_bounds__(THREADS, 2)
                 const bool is = m < tile.z && p < pieces;
                 col[nt] = row(is ? m : 0, is ? p : 0) + c * 8;
             }
-            float total[2][NT][4];
+            float total[SET][NT][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int m = 0; m < SET; ++m)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) total[0][nt][i] = total[1][nt][i] = 0.0f;
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) total[m][nt][i] = 0.0f;
 #pragma unroll 1
             while (w.left > 0) {
                 if (warp == 0 && w.left <= claim_at) claim_step();
@@ -685,21 +695,34 @@ __global__ void __launch_bounds__(THREADS, 2)
                 advance(w);
                 if (tile.w) {
                     acquire();
-                    chunk_pair_centred<NT>(stage, plan.chunk, geom, lane, here, total);
+                    chunk_set_centred<NT>(stage, plan.chunk, geom, lane, here, total);
                 } else {
-                    // all four blocks' words at once, while the stage is waited for
-                    uint4 x[4][NT];
+                    if constexpr (NT == 1 && GROUP != 0) {
+                        // all four blocks' words at once, while the stage is waited for
+                        uint4 x[4];
 #pragma unroll
-                    for (int b = 0; b < 4; ++b)
+                        for (int b = 0; b < 4; ++b)
+                            x[b] = *reinterpret_cast<const uint4*>(here[0] + b * 32);
+                        acquire();
+                        chunk_set<SET, 1, GROUP, ZEROS>(
+                            stage, plan.chunk, geom, lane, [&](int b, int) { return x[b]; }, total);
+                    } else {
+                        // with 16 columns, registers for two chunks at a time and no words ahead
+                        constexpr int MT = NT == 1 ? SET : 2;
+                        acquire();
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            x[b][nt] = *reinterpret_cast<const uint4*>(here[nt] + b * 32);
-                    acquire();
-                    chunk_pair<NT, GROUP, ZEROS>(stage, plan.chunk, geom, lane, x, total);
+                        for (int m = 0; m < SET; m += MT)
+                            chunk_set<MT, NT, GROUP, ZEROS>(
+                                stage + m * plan.chunk, plan.chunk, geom, lane,
+                                [&](int b, int nt) {
+                                    return *reinterpret_cast<const uint4*>(here[nt] + b * 32);
+                                },
+                                total + m);
+                    }
                 }
                 release();
             }
-            float* mine = sums + place * 2 * pitch + r;
+            float* mine = sums + place * SET * pitch + r;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -707,7 +730,7 @@ __global__ void __launch_bounds__(THREADS, 2)
                     const int j = nt * 8 + 2 * c + i;
                     if (j < columns)
 #pragma unroll
-                        for (int m = 0; m < 2; ++m) {
+                        for (int m = 0; m < SET; ++m) {
                             mine[m * pitch + j * 17] = total[m][nt][i];
                             mine[m * pitch + j * 17 + 8] = total[m][nt][i + 2];
                         }
@@ -736,27 +759,27 @@ __global__ void __launch_bounds__(THREADS, 2)
         if (item < first_items) {
             const int4 tile = tile_s[w.tile];
             product(
-                tile, gate.geom, plan.x_pieces, plan.x_columns_log, wn1 * strips_item + wm1,
+                tile, gate.geom, plan.x_pieces, plan.x_columns_log, wn1 * sets1_item + wm1,
                 [&](int m, int p) {
                     const int token = member_s[tile.y + m] / a.top;
-                    return a.xp + (size_t(token) * plan.x_pieces + p) * x_padded;
+                    return a.xp + (tile.w ? a.x_form : 0) +
+                           (size_t(token) * plan.x_pieces + p) * x_padded;
                 },
                 w);
             __syncthreads();
-            const int strip0 = (item - w.tile * strip_groups) * strips_item;
-            const int width = strips_item * kQ4StripK;
+            const int width = sets1_item * 32, f0 = (item - w.tile * groups1) * width;
             for (int i = tid; i < tile.z * width; i += threads) {
                 const int m = i / width, k = i - m * width;
-                const int f_at = strip0 * kQ4StripK + k;
-                if (f_at >= strips * kQ4StripK) continue;
+                const int f_at = f0 + k;
+                if (f_at >= plan.sets1 * 32) continue;
                 float g = 0.0f, u = 0.0f;
                 for (int p = 0; p < plan.x_pieces; ++p) {
-                    const float* from = sums + (k / kQ4StripK) * 2 * pitch +
+                    const float* from = sums + (k / kQ4StripK) * 2 * pitch +  // two of a set
                                         ((m << plan.x_columns_log) + p) * 17 + k % kQ4StripK;
 #pragma unroll 4
                     for (int q = 0; q < plan.wn1; ++q) {
-                        g += from[q * strips_item * 2 * pitch];
-                        u += from[q * strips_item * 2 * pitch + pitch];
+                        g += from[q * sets1_item * SET * pitch];
+                        u += from[q * sets1_item * SET * pitch + pitch];
                     }
                 }
                 const int slot = member_s[tile.y + m];
@@ -769,18 +792,23 @@ __global__ void __launch_bounds__(THREADS, 2)
                 Magnitudes magnitude;
                 magnitude.add(__float_as_uint(h));
                 if (magnitude.special<float>()) atomicOr(a.h_special + slot, 1);
-                for (int p = 0; p < plan.h_pieces; ++p)
-                    a.hp[(size_t(slot) * plan.h_pieces + p) * h_padded + f_at] =
-                        uint16_t(__float_as_uint(piece[p]) >> 16);
+                const float scale = (f_at & 2) ? kQ4Scale16 : kQ4Scale;  // by place, as in x
+                for (int p = 0; p < plan.h_pieces; ++p) {
+                    uint16_t* to = a.hp + (size_t(slot) * plan.h_pieces + p) * h_padded + f_at;
+                    to[0] = uint16_t(__float_as_uint(piece[p] * scale) >> 16);
+                    to[a.h_form] = uint16_t(__float_as_uint(piece[p]) >> 16);
+                }
             }
             // past F: down's weights are zero there, but not whatever the scratch holds
-            if (strip0 + strips_item >= strips) {
-                const int from = strips * kQ4StripK, rest = h_padded - from;
+            if (f0 + width >= plan.sets1 * 32) {
+                const int from = plan.sets1 * 32, rest = h_padded - from;
                 for (int i = tid; i < tile.z * plan.h_pieces * rest; i += threads) {
                     const int line = i / rest, m = line / plan.h_pieces;
-                    a.hp[(size_t(member_s[tile.y + m]) * plan.h_pieces + line % plan.h_pieces) *
-                             h_padded +
-                         from + i % rest] = 0;
+                    uint16_t* to = a.hp +
+                                   (size_t(member_s[tile.y + m]) * plan.h_pieces +
+                                    line % plan.h_pieces) * h_padded +
+                                   from + i % rest;
+                    to[0] = to[a.h_form] = 0;
                 }
             }
             __syncthreads();
@@ -801,14 +829,15 @@ __global__ void __launch_bounds__(THREADS, 2)
             }
             const int4 tile = tile_s[w.tile];
             product(
-                tile, down.geom, plan.h_pieces, plan.h_columns_log, wn2 * pairs_item + wm2,
+                tile, down.geom, plan.h_pieces, plan.h_columns_log, wn2 * sets2_item + wm2,
                 [&](int m, int p) {
-                    return a.hp + (size_t(member_s[tile.y + m]) * plan.h_pieces + p) * h_padded;
+                    return a.hp + (tile.w ? a.h_form : 0) +
+                           (size_t(member_s[tile.y + m]) * plan.h_pieces + p) * h_padded;
                 },
                 w);
             __syncthreads();
-            const int group = item - first_items - w.tile * pair_groups;
-            const int width = pairs_item * 32;
+            const int group = item - first_items - w.tile * groups2;
+            const int width = sets2_item * 64;
             for (int i = tid; i < tile.z * width; i += threads) {
                 const int m = i / width, k = i - m * width, d = group * width + k;
                 if (d >= a.D) continue;
@@ -817,18 +846,18 @@ __global__ void __launch_bounds__(THREADS, 2)
                     const float* from = sums + (k / kQ4StripK) * pitch +
                                         ((m << plan.h_columns_log) + p) * 17 + k % kQ4StripK;
 #pragma unroll 4
-                    for (int q = 0; q < plan.wn2; ++q) v += from[q * pairs_item * 2 * pitch];
+                    for (int q = 0; q < plan.wn2; ++q) v += from[q * sets2_item * SET * pitch];
                 }
                 a.z[size_t(member_s[tile.y + m]) * a.D + d] = v;
             }
             __syncthreads();
             if (tid == 0) ptx::red_release_gpu_add(a.counters + 2 + group, 1);
         } else {
-            // 32 columns of the output: each token's rows in the order of its experts
-            const int pair = item - first_items - second_items;
-            wait_count(a.counters + 2 + pair / pairs_item, tiles, &abort_s, a.err);
-            for (int i = tid; i < a.T * 32; i += threads) {
-                const int t = i / 32, d = pair * 32 + i % 32;
+            // some columns of the output: each token's rows in the order of its experts
+            const int d0 = (item - first_items - second_items) * SUM_COLUMNS;
+            wait_count(a.counters + 2 + d0 / (64 * sets2_item), tiles, &abort_s, a.err);
+            for (int i = tid; i < a.T * SUM_COLUMNS; i += threads) {
+                const int t = i / SUM_COLUMNS, d = d0 + i % SUM_COLUMNS;
                 if (d >= a.D) continue;
                 float v = 0.0f;
                 if (a.ids[t * a.top] >= 0)
@@ -889,17 +918,17 @@ cudaError_t launch_experts(const cudaLaunchConfig_t& config, const MoeArgs& a, c
     }
 }
 
-// How many warps split n, so that the CTAs are done first with `tiles` times `strips` pieces of
-// work of `units` chunk pairs each; an item costs some pairs besides.
-int choose_split(double tiles, int strips, int units, int ctas) {
-    constexpr double FIXED = 4.0;
+// How many warps split n, so that the CTAs are done first with `tiles` times `sets` pieces of
+// work of `units` chunk sets each; an item costs some sets besides.
+int choose_split(double tiles, int sets, int units, int ctas) {
+    constexpr double FIXED = 2.0;
     double best_cost = 1e30;
     int best = 1;
     for (int wn = 1; wn <= WARPS; wn *= 2) {
         if (wn > 1 && wn > units) break;
-        const int groups = (strips + WARPS / wn - 1) / (WARPS / wn);
+        const int groups = (sets + WARPS / wn - 1) / (WARPS / wn);
         const double rounds = std::ceil(tiles * groups / ctas);
-        const double cost = rounds * ((units + wn - 1) / wn + FIXED + 0.25 * wn);
+        const double cost = rounds * ((units + wn - 1) / wn + FIXED + 0.125 * wn);
         if (cost < best_cost) {
             best_cost = cost;
             best = wn;
@@ -924,15 +953,16 @@ MoePlan make_plan(const sgemm_moe_layer& m, const Q4Geom& g, const Q4Geom& gd, i
     const int chunk1 = q4_chunk_bytes(g.group, g.zeros), chunk2 = q4_chunk_bytes(gd.group, gd.zeros);
     p.chunk = chunk1 > chunk2 ? chunk1 : chunk2;
     p.smem = moe_offsets(p.max_columns, p.chunk, most_tiles(m.E, slots, p.capacity), slots, m.E).end;
-    p.pairs = (m.D + 31) / 32;
+    p.sets1 = (m.F + 31) / 32;
+    p.sets2 = (m.D + 63) / 64;
     // tiles, about, if tokens picked experts at random
     double missed = 1.0;
     for (int t = 0; t < T; ++t) missed *= 1.0 - double(m.top_k) / m.E;
     double tiles = m.E * (1.0 - missed);
     if (tiles < double(slots) / p.capacity) tiles = double(slots) / p.capacity;
     const int ctas = 2 * sm_count;
-    p.wn1 = choose_split(tiles, (m.F + kQ4StripK - 1) / kQ4StripK, g.units, ctas);
-    p.wn2 = choose_split(tiles, p.pairs, gd.units, ctas);
+    p.wn1 = choose_split(tiles, p.sets1, g.units, ctas);
+    p.wn2 = choose_split(tiles, p.sets2, gd.units, ctas);
     return p;
 }
 
@@ -991,15 +1021,15 @@ extern "C" int sgemm_moe(const sgemm_moe_layer* layer, const void* x, long long 
     const MoePlan plan = make_plan(m, g, gd, T, info->sm_count);
 
     const int x_padded = g.units * kQ4UnitN, h_padded = gd.units * kQ4UnitN;
-    const int counters = 2 + plan.pairs;
+    const int counters = 2 + plan.sets2;
     size_t bytes = 0;
     auto take = [&](size_t n) {
         const size_t at = bytes;
         bytes += (n + 255) / 256 * 256;
         return at;
     };
-    const size_t at_xp = take(size_t(T) * plan.x_pieces * x_padded * 2);
-    const size_t at_hp = take(size_t(slots) * plan.h_pieces * h_padded * 2);
+    const size_t at_xp = take(size_t(T) * plan.x_pieces * x_padded * 4);
+    const size_t at_hp = take(size_t(slots) * plan.h_pieces * h_padded * 4);
     const size_t at_xs = take(size_t(T) * 4), at_hs = take(size_t(slots) * 4);
     const size_t at_counters = take(size_t(counters) * 4);
     const size_t at_z = take(size_t(slots) * m.D * 4);
@@ -1030,6 +1060,8 @@ extern "C" int sgemm_moe(const sgemm_moe_layer* layer, const void* x, long long 
             size_t(m.D) * router_size % 16 == 0;
     a.xp = reinterpret_cast<uint16_t*>(base + at_xp);
     a.hp = reinterpret_cast<uint16_t*>(base + at_hp);
+    a.x_form = size_t(T) * plan.x_pieces * x_padded;
+    a.h_form = size_t(slots) * plan.h_pieces * h_padded;
     a.x_special = reinterpret_cast<int*>(base + at_xs);
     a.h_special = reinterpret_cast<int*>(base + at_hs);
     a.counters = reinterpret_cast<int*>(base + at_counters);
