@@ -42,7 +42,7 @@ constexpr int ROUTE_THREADS = 512, ROUTE_WARPS = ROUTE_THREADS / 32;
 
 constexpr int SET = 4;          // chunks that a warp multiplies with the same columns
 constexpr int DEPTH = 2;        // stages of a warp's ring, a set of chunks each
-constexpr int SUM_COLUMNS = 32;  // of a sum item
+constexpr int SUM_COLUMNS = 32, SUM_TOKENS = 16;  // of a sum item
 constexpr int WARPS = 8, THREADS = WARPS * 32;
 constexpr int SMEM_LIMIT = 227 * 1024;
 
@@ -65,7 +65,9 @@ struct MoeArgs {
     size_t x_form, h_form;
     int* x_special;    // [token]: nonzero where the plain form cannot take some value
     int* h_special;    // [token and slot]
-    int* counters;     // 0: next item, 1: first items done, 2 ..: second items done of a group
+    // 0: next item, 1: first items done, 2: whether some h_special is set, 3 ..: second items done
+    // of a group
+    int* counters;
     float* z;          // [token and slot][D]
     int* err;
 };
@@ -82,6 +84,8 @@ struct MoePlan {
     int h_pieces, h_columns_log;  // and of a hidden row
     int max_columns;              // of a tile
     int wn1, wn2;                 // warps that split n in first and second items
+    int step1, step2;             // bytes from a warp's unit to its next
+    ptrdiff_t gate_to_up;
     int sets1, sets2;             // sets of a tile's hidden values (32) and of the output (64)
     int chunk, smem;
 };
@@ -418,7 +422,7 @@ __device__ __forceinline__ void chunk_set_centred(const uint8_t* stage, int chun
 // NT_MOST: tiles of 8 columns that a tile of tokens may take.
 template <int NT_MOST, int GROUP, bool ZEROS>
 __global__ void __launch_bounds__(THREADS, 2)
-    moe_expert_kernel(const MoeArgs a, const Stack gate, const Stack up, const Stack down,
+    moe_expert_kernel(const MoeArgs a, const Stack gate, const Stack down,
                       const MoePlan plan) {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int scan_s[WARPS], tiles_s, item_s;
@@ -514,7 +518,9 @@ __global__ void __launch_bounds__(THREADS, 2)
     const int groups1 = (plan.sets1 + sets1_item - 1) / sets1_item;
     const int groups2 = (plan.sets2 + sets2_item - 1) / sets2_item;
     const int first_items = tiles * groups1, second_items = tiles * groups2;
-    const int items = first_items + second_items + (a.D + SUM_COLUMNS - 1) / SUM_COLUMNS;
+    const int sum_columns = (a.D + SUM_COLUMNS - 1) / SUM_COLUMNS;
+    const int items = first_items + second_items +
+                      sum_columns * ((a.T + SUM_TOKENS - 1) / SUM_TOKENS);
     const int x_padded = gate.geom.units * kQ4UnitN, h_padded = down.geom.units * kQ4UnitN;
 
     // Where a warp is in an item. kind 0: strips `strip` and + 1 of gate and up of the tile's
@@ -565,18 +571,15 @@ __global__ void __launch_bounds__(THREADS, 2)
         s.any = lane < (2 + g.zeros) * groups;
         return s;
     };
-    const ptrdiff_t gate_to_up = up.data - gate.data;
     int turn = 0;   // of next_s
     int claim_at = 0;  // units left when the next item is claimed
     int f_on = 0;   // the walk is in the current item (0) or the next (1)
     int ahead = 0;  // stages fetched and not used up
     Walk f = walk(item_s);
-    // where the lane's next codes and scales or zero points are; from there to the second chunk's
-    // (the fourth's is as far from the third's), to the third's, and to the next unit's
+    // where the lane's next codes and scales or zero points are, and the latter's step to the next
+    // strip
     const uint8_t *f_codes = nullptr, *f_rest = nullptr;
-    ptrdiff_t f_codes2 = 0, f_rest2 = 0;
-    int f_codes3 = 0, f_rest3 = 0;
-    size_t f_step = 0;
+    int f_side = 0;
     bool f_any = false;
     auto locate = [&]() {
         if (f.left == 0) return;
@@ -588,11 +591,7 @@ __global__ void __launch_bounds__(THREADS, 2)
                               size_t(f.unit) * stack.geom.unit_bytes;
         f_codes = unit + (lane >> 4) * (kQ4UnitK * 16) + (in_tile * kQ4StripK + (lane & 15)) * 16;
         f_rest = unit + side.from + in_tile * side.step;
-        f_codes2 = f.kind == 0 ? gate_to_up : kQ4StripK * 16;
-        f_rest2 = f.kind == 0 ? gate_to_up : side.step;
-        f_codes3 = (f.kind + 1) * (kQ4StripK * 16);
-        f_rest3 = (f.kind + 1) * side.step;
-        f_step = size_t(f.kind == 0 ? plan.wn1 : plan.wn2) * stack.geom.unit_bytes;
+        f_side = side.step;
         f_any = side.any;
     };
     auto fetch = [&]() -> bool {
@@ -607,24 +606,31 @@ __global__ void __launch_bounds__(THREADS, 2)
         }
         uint32_t to = fetch_to + lane * 16;
         const uint8_t *codes = f_codes, *rest = f_rest;
+        // from a chunk to the second (as from the third to the fourth), and to the third
+        const bool second = f.kind != 0;
+        const ptrdiff_t codes2 = second ? kQ4StripK * 16 : plan.gate_to_up;
+        const ptrdiff_t rest2 = second ? f_side : plan.gate_to_up;
+        const int codes3 = second ? 2 * kQ4StripK * 16 : kQ4StripK * 16;
+        const int rest3 = second ? 2 * f_side : f_side;
 #pragma unroll
         for (int m = 0; m < SET; m += 2) {
             const uint32_t to2 = to + plan.chunk;
             ptx::cp_async_16(to, codes, true);
             ptx::cp_async_16(to + 512, codes + 2 * kQ4UnitK * 16, true);
-            ptx::cp_async_16(to2, codes + f_codes2, true);
-            ptx::cp_async_16(to2 + 512, codes + f_codes2 + 2 * kQ4UnitK * 16, true);
+            ptx::cp_async_16(to2, codes + codes2, true);
+            ptx::cp_async_16(to2 + 512, codes + codes2 + 2 * kQ4UnitK * 16, true);
             if (f_any) {
                 ptx::cp_async_16(to + kQ4ChunkCodes, rest, true);
-                ptx::cp_async_16(to2 + kQ4ChunkCodes, rest + f_rest2, true);
+                ptx::cp_async_16(to2 + kQ4ChunkCodes, rest + rest2, true);
             }
             to = to2 + plan.chunk;
-            codes += f_codes3;
-            rest += f_rest3;
+            codes += codes3;
+            rest += rest3;
         }
         ptx::cp_async_commit();
-        f_codes += f_step;
-        f_rest += f_step;
+        const int step = second ? plan.step2 : plan.step1;
+        f_codes += step;
+        f_rest += step;
         --f.left;
         ++ahead;
         fetch_to += stage_bytes;
@@ -663,11 +669,19 @@ __global__ void __launch_bounds__(THREADS, 2)
         claim = claim == 1 ? 2 : 0;
     };
 
-    // Multiplies the warp's set of an item with the columns of its tile of tokens (row(m, p) is
-    // piece p of its m-th token's row) and puts the sums to [wn][set][chunk][column][17].
+    // Multiplies the warp's set of an item with the columns of its tile of tokens and puts the sums
+    // to [wn][set][chunk][column][17]. One copy of this code serves both kinds of items: it is most
+    // of the kernel, and where there are few items its instructions come from far.
     const int pitch = plan.max_columns * 17;
-    auto product = [&](const int4& tile, const Q4Geom& geom, int pieces, int columns_log, int place,
-                       auto&& row, Walk& w) {
+    auto product = [&](const int4& tile, Walk& w) {
+        const bool second = w.kind != 0;
+        const Q4Geom& geom = second ? down.geom : gate.geom;
+        const int pieces = second ? plan.h_pieces : plan.x_pieces;
+        const int columns_log = second ? plan.h_columns_log : plan.x_columns_log;
+        const int padded = second ? h_padded : x_padded, per_row = second ? 1 : a.top;
+        const int place = second ? wn2 * sets2_item + wm2 : wn1 * sets1_item + wm1;
+        const uint16_t* rows = second ? a.hp + (tile.w ? a.h_form : 0)
+                                      : a.xp + (tile.w ? a.x_form : 0);
         const int columns = tile.z << columns_log;
         auto run = [&](auto nt_) {
             constexpr int NT = decltype(nt_)::value;
@@ -677,7 +691,8 @@ __global__ void __launch_bounds__(THREADS, 2)
             for (int nt = 0; nt < NT; ++nt) {
                 const int j = nt * 8 + r, m = j >> columns_log, p = j - (m << columns_log);
                 const bool is = m < tile.z && p < pieces;
-                col[nt] = row(is ? m : 0, is ? p : 0) + c * 8;
+                const int row = member_s[tile.y + (is ? m : 0)] / per_row;
+                col[nt] = rows + (size_t(row) * pieces + (is ? p : 0)) * padded + c * 8;
             }
             float total[SET][NT][4];
 #pragma unroll
@@ -756,17 +771,28 @@ __global__ void __launch_bounds__(THREADS, 2)
 #pragma unroll 1
         while (ahead < DEPTH && fetch()) {
         }
-        if (item < first_items) {
-            const int4 tile = tile_s[w.tile];
-            product(
-                tile, gate.geom, plan.x_pieces, plan.x_columns_log, wn1 * sets1_item + wm1,
-                [&](int m, int p) {
-                    const int token = member_s[tile.y + m] / a.top;
-                    return a.xp + (tile.w ? a.x_form : 0) +
-                           (size_t(token) * plan.x_pieces + p) * x_padded;
-                },
-                w);
+        if (item >= first_items && item < first_items + second_items && !hidden_ready) {
+            wait_count(a.counters + 1, first_items, &abort_s, a.err);
+            // tiles with a hidden value that the plain form cannot take
+            const bool some = __ldcg(a.counters + 2) != 0;
+            for (int k = tid; k < tiles; k += threads) {
+                const int4 tile = tile_s[k];
+                int special = 0;
+                if (some)
+                    for (int i = 0; i < tile.z; ++i)
+                        special |= __ldcg(a.h_special + member_s[tile.y + i]);
+                tile_s[k].w = special;
+            }
             __syncthreads();
+            hidden_ready = true;
+        }
+        int4 tile = make_int4(0, 0, 0, 0);
+        if (item < first_items + second_items) {
+            tile = tile_s[w.tile];
+            product(tile, w);
+            __syncthreads();
+        }
+        if (item < first_items) {
             const int width = sets1_item * 32, f0 = (item - w.tile * groups1) * width;
             for (int i = tid; i < tile.z * width; i += threads) {
                 const int m = i / width, k = i - m * width;
@@ -791,7 +817,10 @@ __global__ void __launch_bounds__(THREADS, 2)
                     piece[1] = __bfloat162float(__float2bfloat16_rn(h - piece[0]));
                 Magnitudes magnitude;
                 magnitude.add(__float_as_uint(h));
-                if (magnitude.special<float>()) atomicOr(a.h_special + slot, 1);
+                if (magnitude.special<float>()) {
+                    a.h_special[slot] = 1;
+                    a.counters[2] = 1;
+                }
                 const float scale = (f_at & 2) ? kQ4Scale16 : kQ4Scale;  // by place, as in x
                 for (int p = 0; p < plan.h_pieces; ++p) {
                     uint16_t* to = a.hp + (size_t(slot) * plan.h_pieces + p) * h_padded + f_at;
@@ -814,28 +843,6 @@ __global__ void __launch_bounds__(THREADS, 2)
             __syncthreads();
             if (tid == 0) ptx::red_release_gpu_add(a.counters + 1, 1);
         } else if (item < first_items + second_items) {
-            if (!hidden_ready) {
-                wait_count(a.counters + 1, first_items, &abort_s, a.err);
-                // tiles with a hidden value that the plain form cannot take
-                for (int k = tid; k < tiles; k += threads) {
-                    const int4 tile = tile_s[k];
-                    int special = 0;
-                    for (int i = 0; i < tile.z; ++i)
-                        special |= __ldcg(a.h_special + member_s[tile.y + i]);
-                    tile_s[k].w = special;
-                }
-                __syncthreads();
-                hidden_ready = true;
-            }
-            const int4 tile = tile_s[w.tile];
-            product(
-                tile, down.geom, plan.h_pieces, plan.h_columns_log, wn2 * sets2_item + wm2,
-                [&](int m, int p) {
-                    return a.hp + (tile.w ? a.h_form : 0) +
-                           (size_t(member_s[tile.y + m]) * plan.h_pieces + p) * h_padded;
-                },
-                w);
-            __syncthreads();
             const int group = item - first_items - w.tile * groups2;
             const int width = sets2_item * 64;
             for (int i = tid; i < tile.z * width; i += threads) {
@@ -851,19 +858,26 @@ __global__ void __launch_bounds__(THREADS, 2)
                 a.z[size_t(member_s[tile.y + m]) * a.D + d] = v;
             }
             __syncthreads();
-            if (tid == 0) ptx::red_release_gpu_add(a.counters + 2 + group, 1);
+            if (tid == 0) ptx::red_release_gpu_add(a.counters + 3 + group, 1);
         } else {
-            // some columns of the output: each token's rows in the order of its experts
-            const int d0 = (item - first_items - second_items) * SUM_COLUMNS;
-            wait_count(a.counters + 2 + d0 / (64 * sets2_item), tiles, &abort_s, a.err);
-            for (int i = tid; i < a.T * SUM_COLUMNS; i += threads) {
-                const int t = i / SUM_COLUMNS, d = d0 + i % SUM_COLUMNS;
-                if (d >= a.D) continue;
+            // some columns of some tokens' output: their rows in the order of the experts
+            const int at = item - first_items - second_items;
+            const int d0 = at % sum_columns * SUM_COLUMNS, t0 = at / sum_columns * SUM_TOKENS;
+            wait_count(a.counters + 3 + d0 / (64 * sets2_item), tiles, &abort_s, a.err);
+            for (int i = tid; i < SUM_TOKENS * SUM_COLUMNS; i += threads) {
+                const int t = t0 + i / SUM_COLUMNS, d = d0 + i % SUM_COLUMNS;
+                if (t >= a.T || d >= a.D) continue;
                 float v = 0.0f;
                 if (a.ids[t * a.top] >= 0)
-#pragma unroll 4
-                    for (int j = 0; j < a.top; ++j)
-                        v += __ldcg(a.z + size_t(t * a.top + j) * a.D + d);
+                    for (int j0 = 0; j0 < a.top; j0 += 8) {
+                        float z[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            z[j] = j0 + j < a.top ? __ldcg(a.z + size_t(t * a.top + j0 + j) * a.D + d)
+                                                  : 0.0f;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) v += z[j];
+                    }
                 store_from_float(a.y, a.dtype, t * a.ldy + d, v);
             }
         }
@@ -894,27 +908,27 @@ cudaError_t launch_route(const cudaLaunchConfig_t& config, const MoeArgs& a, int
 
 template <int NT_MOST, int GROUP, bool ZEROS>
 cudaError_t launch_expert_kernel(const cudaLaunchConfig_t& config, const MoeArgs& a, const Stack& gate,
-                                 const Stack& up, const Stack& down, const MoePlan& plan) {
+                                 const Stack& down, const MoePlan& plan) {
     constexpr auto kernel = moe_expert_kernel<NT_MOST, GROUP, ZEROS>;
     const cudaError_t err = set_smem_limit_once<kernel>(SMEM_LIMIT - 2048);
     if (err != cudaSuccess) return err;
     count_launch();
-    return cudaLaunchKernelEx(&config, kernel, a, gate, up, down, plan);
+    return cudaLaunchKernelEx(&config, kernel, a, gate, down, plan);
 }
 
 // The stacks' group size and zero points are known to the kernel where they are the same.
 template <int NT_MOST>
 cudaError_t launch_experts(const cudaLaunchConfig_t& config, const MoeArgs& a, const Stack& gate,
-                           const Stack& up, const Stack& down, const MoePlan& plan) {
+                           const Stack& down, const MoePlan& plan) {
     if (gate.geom.group != down.geom.group || gate.geom.zeros != down.geom.zeros)
-        return launch_expert_kernel<NT_MOST, 0, false>(config, a, gate, up, down, plan);
+        return launch_expert_kernel<NT_MOST, 0, false>(config, a, gate, down, plan);
     switch (gate.geom.group + gate.geom.zeros) {
-        case 32: return launch_expert_kernel<NT_MOST, 32, false>(config, a, gate, up, down, plan);
-        case 33: return launch_expert_kernel<NT_MOST, 32, true>(config, a, gate, up, down, plan);
-        case 64: return launch_expert_kernel<NT_MOST, 64, false>(config, a, gate, up, down, plan);
-        case 65: return launch_expert_kernel<NT_MOST, 64, true>(config, a, gate, up, down, plan);
-        case 128: return launch_expert_kernel<NT_MOST, 128, false>(config, a, gate, up, down, plan);
-        default: return launch_expert_kernel<NT_MOST, 128, true>(config, a, gate, up, down, plan);
+        case 32: return launch_expert_kernel<NT_MOST, 32, false>(config, a, gate, down, plan);
+        case 33: return launch_expert_kernel<NT_MOST, 32, true>(config, a, gate, down, plan);
+        case 64: return launch_expert_kernel<NT_MOST, 64, false>(config, a, gate, down, plan);
+        case 65: return launch_expert_kernel<NT_MOST, 64, true>(config, a, gate, down, plan);
+        case 128: return launch_expert_kernel<NT_MOST, 128, false>(config, a, gate, down, plan);
+        default: return launch_expert_kernel<NT_MOST, 128, true>(config, a, gate, down, plan);
     }
 }
 
@@ -963,6 +977,9 @@ MoePlan make_plan(const sgemm_moe_layer& m, const Q4Geom& g, const Q4Geom& gd, i
     const int ctas = 2 * sm_count;
     p.wn1 = choose_split(tiles, p.sets1, g.units, ctas);
     p.wn2 = choose_split(tiles, p.sets2, gd.units, ctas);
+    p.step1 = p.wn1 * g.unit_bytes;
+    p.step2 = p.wn2 * gd.unit_bytes;
+    p.gate_to_up = static_cast<const uint8_t*>(m.up.data) - static_cast<const uint8_t*>(m.gate.data);
     return p;
 }
 
@@ -1021,7 +1038,7 @@ extern "C" int sgemm_moe(const sgemm_moe_layer* layer, const void* x, long long 
     const MoePlan plan = make_plan(m, g, gd, T, info->sm_count);
 
     const int x_padded = g.units * kQ4UnitN, h_padded = gd.units * kQ4UnitN;
-    const int counters = 2 + plan.sets2;
+    const int counters = 3 + plan.sets2;
     size_t bytes = 0;
     auto take = [&](size_t n) {
         const size_t at = bytes;
@@ -1091,11 +1108,10 @@ extern "C" int sgemm_moe(const sgemm_moe_layer* layer, const void* x, long long 
     config.dynamicSmemBytes = plan.smem;
     config.numAttrs = 1;
     const Stack gate{static_cast<const uint8_t*>(m.gate.data), g};
-    const Stack up{static_cast<const uint8_t*>(m.up.data), g};
     const Stack down{static_cast<const uint8_t*>(m.down.data), gd};
     if (plan.max_columns <= 8)
-        err = launch_experts<1>(config, a, gate, up, down, plan);
+        err = launch_experts<1>(config, a, gate, down, plan);
     else
-        err = launch_experts<2>(config, a, gate, up, down, plan);
+        err = launch_experts<2>(config, a, gate, down, plan);
     return err == cudaSuccess ? SGEMM_OK : SGEMM_ERR_CUDA;
 }
