@@ -440,10 +440,34 @@ __global__ void __launch_bounds__(THREADS, 2)
     float* sums = reinterpret_cast<float*>(smem + at.sums);
     uint8_t* ring = smem + at.ring + warp * DEPTH * SET * plan.chunk;
     // first items: wm1 sets of wn1 warps each; second items: wm2 sets of wn2 warps each
-    const int wn1 = warp % plan.wn1, wm1 = warp / plan.wn1, sets1_item = warps / plan.wn1;
-    const int wn2 = warp % plan.wn2, wm2 = warp / plan.wn2, sets2_item = warps / plan.wn2;
+    const int wn1 = warp & (plan.wn1 - 1), wm1 = warp / plan.wn1, sets1_item = warps / plan.wn1;
+    const int wn2 = warp & (plan.wn2 - 1), wm2 = warp / plan.wn2, sets2_item = warps / plan.wn2;
 
-    if (tid == 0) abort_s = 0;
+    // what does not depend on the routing, while that runs
+    const int groups1 = (plan.sets1 + sets1_item - 1) / sets1_item;
+    const int groups2 = (plan.sets2 + sets2_item - 1) / sets2_item;
+    const int sum_columns = (a.D + SUM_COLUMNS - 1) / SUM_COLUMNS;
+    const int x_padded = gate.geom.units * kQ4UnitN, h_padded = down.geom.units * kQ4UnitN;
+    // what a lane copies besides codes, for the gate and up stacks and for down
+    auto side_of = [&](const Q4Geom& g) {
+        const int groups = kQ4UnitN / g.group;
+        Q4Side s;
+        const bool zero = lane >= 2 * groups;  // zero points
+        s.step = zero ? kQ4StripK : kQ4StripK * 2;
+        s.from = kQ4CodeBytes + (zero ? groups * kQ4UnitK * 2 + (lane - 2 * groups) * kQ4UnitK
+                                      : (lane >> 1) * kQ4UnitK * 2 + (lane & 1) * 16);
+        s.any = lane < (2 + g.zeros) * groups;
+        return s;
+    };
+    // [expert][form][2], and [expert]
+    uint32_t* mask_s = reinterpret_cast<uint32_t*>(smem + at.masks);
+    int* first_s = reinterpret_cast<int*>(mask_s + 4 * a.E);
+    for (int i = tid; i < 4 * a.E; i += threads) mask_s[i] = 0;
+    if (tid == 0) {
+        abort_s = 0;
+        next_s[0] = next_s[1] = -1;
+    }
+    __syncthreads();
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
     int claimed = 0;
@@ -453,10 +477,6 @@ __global__ void __launch_bounds__(THREADS, 2)
     // centred form have tiles of their own, so that they change nothing for the others. A token
     // picks an expert once, so an expert's tokens are a 64-bit mask (one for each form).
     {
-        uint32_t* mask_s = reinterpret_cast<uint32_t*>(smem + at.masks);  // [expert][form][2]
-        int* first_s = reinterpret_cast<int*>(mask_s + 4 * a.E);          // [expert]
-        for (int i = tid; i < 4 * a.E; i += threads) mask_s[i] = 0;
-        __syncthreads();
         for (int i = tid; i < slots; i += threads) {
             const int e = a.ids[i], t = i / a.top;
             const int form = a.x_special[t] != 0;
@@ -496,10 +516,7 @@ __global__ void __launch_bounds__(THREADS, 2)
             }
         }
         if (tid == threads - 1) tiles_s = (before + own) >> 16;
-        if (tid == 0) {
-            item_s = claimed;
-            next_s[0] = next_s[1] = -1;
-        }
+        if (tid == 0) item_s = claimed;
         __syncthreads();
         for (int i = tid; i < slots; i += threads) {
             const int e = a.ids[i], t = i / a.top;
@@ -515,13 +532,9 @@ __global__ void __launch_bounds__(THREADS, 2)
         __syncthreads();
     }
     const int tiles = tiles_s;
-    const int groups1 = (plan.sets1 + sets1_item - 1) / sets1_item;
-    const int groups2 = (plan.sets2 + sets2_item - 1) / sets2_item;
     const int first_items = tiles * groups1, second_items = tiles * groups2;
-    const int sum_columns = (a.D + SUM_COLUMNS - 1) / SUM_COLUMNS;
     const int items = first_items + second_items +
                       sum_columns * ((a.T + SUM_TOKENS - 1) / SUM_TOKENS);
-    const int x_padded = gate.geom.units * kQ4UnitN, h_padded = down.geom.units * kQ4UnitN;
 
     // Where a warp is in an item. kind 0: strips `strip` and + 1 of gate and up of the tile's
     // expert, units wn1, wn1 + plan.wn1, ...; 1: strips `strip` .. + 3 of down, units wn2, ...;
@@ -560,17 +573,6 @@ __global__ void __launch_bounds__(THREADS, 2)
     const uint32_t ring_u32 = ptx::smem_u32(ring);
     uint32_t fetch_to = ring_u32;
     const int stage_bytes = SET * plan.chunk;
-    // what a lane copies besides codes, for the gate and up stacks and for down
-    auto side_of = [&](const Q4Geom& g) {
-        const int groups = kQ4UnitN / g.group;
-        Q4Side s;
-        const bool zero = lane >= 2 * groups;  // zero points
-        s.step = zero ? kQ4StripK : kQ4StripK * 2;
-        s.from = kQ4CodeBytes + (zero ? groups * kQ4UnitK * 2 + (lane - 2 * groups) * kQ4UnitK
-                                      : (lane >> 1) * kQ4UnitK * 2 + (lane & 1) * 16);
-        s.any = lane < (2 + g.zeros) * groups;
-        return s;
-    };
     int turn = 0;   // of next_s
     int claim_at = 0;  // units left when the next item is claimed
     int f_on = 0;   // the walk is in the current item (0) or the next (1)
