@@ -2,9 +2,12 @@
 // that are quantised already, and dequantisation to FP32 (definitions in sgemm.h, layout in
 // q4.cuh).
 //
-// All three move a tile of 128 n x 64 columns (half a unit) through shared memory, because a
-// column's codes run along n while a dense matrix is contiguous along k (or, transposed, the
-// other way round): global memory is read and written in whole lines on both sides.
+// All three are bound by memory: the dense matrix once, and the packed one. A thread of the
+// quantisation owns 32 n of two columns, in registers, which is what 16 bytes of codes hold; a
+// warp's loads run along the matrix' rows. Groups of 64 and 128 n meet in shared memory for their
+// extremes only. From a transposed matrix, a lane reads its columns' n itself, in whole aligned
+// 16 bytes whatever the row's alignment. Dequantisation holds 32 n of four columns a thread and
+// writes rows.
 #include "internal.cuh"
 #include "q4.cuh"
 
@@ -15,12 +18,10 @@ constexpr int TILE_K = 64;
 constexpr int PITCH = TILE_K + 1;  // column and row walks of the tile are free of conflicts
 constexpr int THREADS = 256;
 
-enum class Source { values, codes };
-
 // The nibble of a word that holds the e-th of its 8 codes.
 __device__ constexpr int nibble_of(int e) { return (e >> 1) + 4 * (e & 1); }
 
-// The unit that a CTA works on, and its first column there.
+// The unit that a CTA of the layout kernel works on, and its first column there.
 __device__ __forceinline__ uint8_t* unit_at(uint8_t* data, const Q4Geom& geom) {
     return data + size_t(blockIdx.z) * geom.matrix_bytes() +
            (blockIdx.x / (kQ4UnitK / TILE_K)) * geom.tile_bytes() +
@@ -30,146 +31,315 @@ __device__ __forceinline__ int first_column() {
     return int(blockIdx.x) % (kQ4UnitK / TILE_K) * TILE_K;
 }
 
-template <Source SOURCE>
+// A tile of 128 n x 64 columns (half a unit) through shared memory: global memory is read and
+// written in whole lines on both sides.
 __global__ void __launch_bounds__(THREADS)
-    q4_pack_kernel(const void* __restrict__ src, int dtype, bool transposed,
+    q4_pack_kernel(const uint8_t* __restrict__ src, bool transposed,
                    const uint16_t* __restrict__ scales, const uint8_t* __restrict__ zeros,
                    uint8_t* __restrict__ out, Q4Geom geom) {
-    __shared__ float tile[kQ4UnitN][PITCH];
-    __shared__ float lo_s[4][TILE_K], hi_s[4][TILE_K];  // of 32 n each
-    __shared__ float scale_s[4][TILE_K];                // of a group each
-    __shared__ float zero_s[4][TILE_K];
+    __shared__ uint8_t tile[kQ4UnitN][PITCH];
+    __shared__ uint8_t zero_s[4][TILE_K];  // of a group each
     const int tid = threadIdx.x;
     const int n0 = blockIdx.y * kQ4UnitN, k0 = blockIdx.x * TILE_K;
     const int N = geom.N, K = geom.K;
     const size_t mat = size_t(blockIdx.z) * N * K;
-    const int blocks = geom.group / 32, groups = kQ4UnitN / geom.group;
+    const int groups = kQ4UnitN / geom.group;
 
 #pragma unroll 8
     for (int i = 0; i < kQ4UnitN * TILE_K / THREADS; ++i) {
         const int n = transposed ? tid % kQ4UnitN : tid / TILE_K + i * (THREADS / TILE_K);
         const int k = transposed ? tid / kQ4UnitN + i * (THREADS / kQ4UnitN) : tid % TILE_K;
-        float v = 0.0f;
-        if (n0 + n < N && k0 + k < K) {
-            const size_t at =
-                mat + (transposed ? size_t(k0 + k) * N + n0 + n : size_t(n0 + n) * K + k0 + k);
-            if constexpr (SOURCE == Source::values)
-                v = load_as_float(src, dtype, at);
-            else
-                v = float(static_cast<const uint8_t*>(src)[at] & 15);
-        }
-        tile[n][k] = v;
+        uint8_t v = 0;
+        if (n0 + n < N && k0 + k < K)
+            v = src[mat + (transposed ? size_t(k0 + k) * N + n0 + n : size_t(n0 + n) * K + k0 + k)];
+        tile[n][k] = v & 15;
     }
-    __syncthreads();
-
     const int k = tid % TILE_K, part = tid / TILE_K;
-    if constexpr (SOURCE == Source::values) {
-        float lo = 0.0f, hi = 0.0f;
-#pragma unroll 8
-        for (int i = 0; i < 32; ++i) {
-            const float v = tile[part * 32 + i][k];
-            lo = fminf(lo, v);
-            hi = fmaxf(hi, v);
-        }
-        lo_s[part][k] = lo;
-        hi_s[part][k] = hi;
-        __syncthreads();
-    }
     if (part < groups) {
-        float s = 0.0f, z = geom.zeros ? 0.0f : 8.0f;
-        if constexpr (SOURCE == Source::values) {
-            float lo = 0.0f, hi = 0.0f;
-            for (int b = part * blocks; b < (part + 1) * blocks; ++b) {
-                lo = fminf(lo, lo_s[b][k]);
-                hi = fmaxf(hi, hi_s[b][k]);
-            }
-            s = geom.zeros ? __fsub_rn(__fdiv_rn(hi, 15.0f), __fdiv_rn(lo, 15.0f))
-                           : __fdiv_rn(fmaxf(hi, -lo), 7.0f);
-            s = __bfloat162float(__float2bfloat16_rn(s));
-            if (geom.zeros && s > 0.0f)
-                z = fminf(fmaxf(rintf(__fdiv_rn(-lo, s)), 0.0f), 15.0f);
-            scale_s[part][k] = s;
-            zero_s[part][k] = z;
-        }
-        const int group = (n0 + part * geom.group) / geom.group;
+        const int group = n0 / geom.group + part;
         const int all_groups = (N + geom.group - 1) / geom.group;
         uint16_t bits = 0;
-        if constexpr (SOURCE == Source::values) {
-            bits = uint16_t(__float_as_uint(s) >> 16);
-        } else {
-            if (group < all_groups && k0 + k < K) {
-                const size_t at = size_t(blockIdx.z) * all_groups * K +
-                                  (transposed ? size_t(k0 + k) * all_groups + group
-                                              : size_t(group) * K + k0 + k);
-                bits = scales[at];
-                if (geom.zeros) z = fminf(float(zeros[at]), 15.0f);
-            }
-            zero_s[part][k] = z;
+        uint8_t z = geom.zeros ? 0 : 8;
+        if (group < all_groups && k0 + k < K) {
+            const size_t at = size_t(blockIdx.z) * all_groups * K +
+                              (transposed ? size_t(k0 + k) * all_groups + group
+                                          : size_t(group) * K + k0 + k);
+            bits = scales[at];
+            if (geom.zeros) z = zeros[at] < 15 ? zeros[at] : 15;
         }
+        zero_s[part][k] = z;
         uint8_t* unit = unit_at(out, geom);
         const int at = part * kQ4UnitK + first_column() + k;
         reinterpret_cast<uint16_t*>(unit + kQ4CodeBytes)[at] = bits;
-        if (geom.zeros) unit[kQ4CodeBytes + groups * kQ4UnitK * 2 + at] = uint8_t(z);
+        if (geom.zeros) unit[kQ4CodeBytes + groups * kQ4UnitK * 2 + at] = z;
     }
     __syncthreads();
 
     // 16 bytes of codes a thread: part is the block of 32 n
-    auto code = [&](int n, int kk) -> uint32_t {
-        const int g = n / geom.group;
-        const float z = zero_s[g][kk];
-        if (n0 + n >= N || k0 + kk >= K) return uint32_t(z);
-        if constexpr (SOURCE == Source::codes) return uint32_t(tile[n][kk]);
-        const float s = scale_s[g][kk];
-        const float low = geom.zeros ? 0.0f : -8.0f, high = geom.zeros ? 15.0f : 7.0f;
-        if (!(s > 0.0f)) return uint32_t(z);
-        float q = rintf(__fdiv_rn(tile[n][kk], s));
-        if (geom.zeros) q += z;
-        q = fminf(fmaxf(q, low), high);
-        return uint32_t(int(geom.zeros ? q : q + 8.0f));
-    };
+    const uint32_t z = zero_s[part * 32 / geom.group][k];
     uint32_t word[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         uint32_t w = 0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w |= code(part * 32 + 8 * i + e, k) << (4 * nibble_of(e));
+        for (int e = 0; e < 8; ++e) {
+            const int n = part * 32 + 8 * i + e;
+            const uint32_t code = n0 + n < N && k0 + k < K ? tile[n][k] : z;
+            w |= code << (4 * nibble_of(e));
+        }
         word[i] = w;
     }
     reinterpret_cast<uint4*>(unit_at(out, geom))[part * kQ4UnitK + first_column() + k] =
         make_uint4(word[0], word[1], word[2], word[3]);
 }
 
+// The code of v by the definition, as it is written down. z: 8 without zero points.
+__device__ __forceinline__ uint32_t code_of(float v, float s, float z, bool zeros) {
+    if (!(s > 0.0f)) return uint32_t(z);
+    float q = rintf(__fdiv_rn(v, s));
+    if (zeros) q += z;
+    q = fminf(fmaxf(q, zeros ? 0.0f : -8.0f), zeros ? 15.0f : 7.0f);
+    return uint32_t(int(zeros ? q : q + 8.0f));
+}
+__device__ __noinline__ uint32_t word_of(const float* v, float s, float z, bool zeros) {
+    uint32_t w = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w |= code_of(v[e], s, z, zeros) << (4 * nibble_of(e));
+    return w;
+}
+
+// 8 codes of a word. The definition divides and rounds to nearest even. v times the rounded
+// reciprocal lies within 15.1 * 2^-23 < 2e-6 of the rounded quotient (two roundings against one),
+// so wherever it is less than 0.4999 from an integer, that integer is the definition's too. The
+// product is rounded by adding 1.5 * 2^23, in one instruction; the sum's low bits are the code.
+// Else, and for scales whose reciprocal is not a normal number, the word is made by the
+// definition.
+__device__ __forceinline__ uint32_t quick_word(const float (&v)[8], float s, float r, float z,
+                                               bool zeros) {
+    constexpr float ROUND = 12582912.0f;
+    constexpr uint32_t BITS = 0x4b400000u;  // ROUND's
+    bool ok = s >= 0x1p-100f && s <= 0x1p100f;
+    uint32_t w = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float u = __fmaf_rn(v[e], r, ROUND);
+        const float off = __fmaf_rn(v[e], r, -__fsub_rn(u, ROUND));
+        ok = ok && fabsf(off) < 0.4999f;  // false for NaN
+        // without zero points no quotient passes 7 * (1 + 2^-8), so none is clipped
+        const int code = int(__float_as_uint(u) - BITS) + int(z);
+        w += uint32_t(zeros ? min(max(code, 0), 15) : code) << (4 * nibble_of(e));
+    }
+    return ok ? w : word_of(v, s, z, zeros);
+}
+
+template <class T>
+__device__ __forceinline__ float as_float(T v) { return float(v); }
+
+// v[i] = row[n0 + i], zeros from N on. Aligned 16-byte loads cover the 32 values, and are shifted
+// into place; those that reach beyond [begin, end) of the matrix are read value by value.
+template <class T>
+__device__ __forceinline__ void load_along(const T* row, int n0, int N, const char* begin,
+                                           const char* end, float (&v)[32]) {
+    constexpr int CHUNKS = 32 * int(sizeof(T)) / 16 + 1;
+    const char* from = reinterpret_cast<const char*>(row + n0);
+    const int shift = int(reinterpret_cast<uintptr_t>(from) & 15);
+    const char* at = from - shift;
+    const char* stop = reinterpret_cast<const char*>(row + N);  // nothing after is wanted
+    if (n0 + 32 > N || at < begin || at + CHUNKS * 16 > end) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = n0 + i < N ? as_float(row[n0 + i]) : 0.0f;
+        return;
+    }
+    uint32_t w[CHUNKS * 4];
+#pragma unroll
+    for (int i = 0; i < CHUNKS; ++i) {
+        uint4 c = make_uint4(0, 0, 0, 0);
+        if (at + i * 16 < stop) c = *reinterpret_cast<const uint4*>(at + i * 16);
+        w[4 * i] = c.x;
+        w[4 * i + 1] = c.y;
+        w[4 * i + 2] = c.z;
+        w[4 * i + 3] = c.w;
+    }
+    constexpr int WORDS = 32 * int(sizeof(T)) / 4;
+#pragma unroll
+    for (int i = 0; i < WORDS + 2; ++i) w[i] = (shift & 8) ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < WORDS + 1; ++i) w[i] = (shift & 4) ? w[i + 1] : w[i];
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(w[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) {
+            const uint32_t pair = __funnelshift_r(w[i], w[i + 1], (shift & 2) * 8);
+            const T* half = reinterpret_cast<const T*>(&pair);
+            v[2 * i] = as_float(half[0]);
+            v[2 * i + 1] = as_float(half[1]);
+        }
+    }
+}
+
+template <class T, bool TRANSPOSED, bool ZEROS>
+__global__ void __launch_bounds__(THREADS, 2)
+    q4_quantize_kernel(const T* __restrict__ src, size_t values, uint8_t* __restrict__ out,
+                       Q4Geom geom) {
+    __shared__ float lo_s[4][kQ4UnitK], hi_s[4][kQ4UnitK];  // of 32 n each
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int block = warp >> 1, first = (warp & 1) * 64 + lane;  // columns first and first + 32
+    const int n0 = blockIdx.y * kQ4UnitN + block * 32, k0 = blockIdx.x * kQ4UnitK;
+    const int N = geom.N, K = geom.K;
+    const T* mat = src + size_t(blockIdx.z) * N * K;
+
+    float v[2][32];
+    if constexpr (TRANSPOSED) {
+        const char* begin = reinterpret_cast<const char*>(src);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int k = k0 + first + 32 * j;
+            load_along(mat + size_t(k) * N, n0, k < K ? N : 0, begin, begin + values * sizeof(T),
+                       v[j]);
+        }
+    } else if (n0 + 32 <= N && k0 + kQ4UnitK <= K) {
+        const T* from = mat + size_t(n0) * K + k0 + first;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) v[j][i] = as_float(__ldcs(from + size_t(i) * K + 32 * j));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int k = k0 + first + 32 * j;
+                v[j][i] = n0 + i < N && k < K ? as_float(mat[size_t(n0 + i) * K + k]) : 0.0f;
+            }
+    }
+    float lo[2] = {0.0f, 0.0f}, hi[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            lo[j] = fminf(lo[j], v[j][i]);
+            hi[j] = fmaxf(hi[j], v[j][i]);
+        }
+    const int blocks = geom.group / 32, g = block / blocks;
+    if (blocks > 1) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            lo_s[block][first + 32 * j] = lo[j];
+            hi_s[block][first + 32 * j] = hi[j];
+        }
+        __syncthreads();
+        for (int b = g * blocks; b < (g + 1) * blocks; ++b)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                lo[j] = fminf(lo[j], lo_s[b][first + 32 * j]);
+                hi[j] = fmaxf(hi[j], hi_s[b][first + 32 * j]);
+            }
+    }
+    uint8_t* unit = out + size_t(blockIdx.z) * geom.matrix_bytes() +
+                    blockIdx.x * geom.tile_bytes() + size_t(blockIdx.y) * geom.unit_bytes;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int column = first + 32 * j;
+        float s = ZEROS ? __fsub_rn(__fdiv_rn(hi[j], 15.0f), __fdiv_rn(lo[j], 15.0f))
+                        : __fdiv_rn(fmaxf(hi[j], -lo[j]), 7.0f);
+        s = __bfloat162float(__float2bfloat16_rn(s));
+        float z = ZEROS ? 0.0f : 8.0f;
+        if (ZEROS && s > 0.0f) z = fminf(fmaxf(rintf(__fdiv_rn(-lo[j], s)), 0.0f), 15.0f);
+        if (block % blocks == 0) {
+            const int at = g * kQ4UnitK + column;
+            reinterpret_cast<uint16_t*>(unit + kQ4CodeBytes)[at] =
+                uint16_t(__float_as_uint(s) >> 16);
+            if (ZEROS)
+                unit[kQ4CodeBytes + kQ4UnitN / geom.group * kQ4UnitK * 2 + at] = uint8_t(z);
+        }
+        uint32_t word[4];
+        if (s > 0.0f) {
+            const float r = __fdiv_rn(1.0f, s);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float v8[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v8[e] = v[j][8 * i + e];
+                word[i] = quick_word(v8, s, r, z, ZEROS);
+            }
+        } else {
+            word[0] = word[1] = word[2] = word[3] = uint32_t(z) * 0x11111111u;
+        }
+        reinterpret_cast<uint4*>(unit)[block * kQ4UnitK + column] =
+            make_uint4(word[0], word[1], word[2], word[3]);
+    }
+}
+
+// Rows of 16-byte multiples are written 16 bytes at a time (VEC: a thread's four columns are
+// neighbours), others 4 (a thread's columns are 32 apart).
+template <bool VEC>
 __global__ void __launch_bounds__(THREADS)
     q4_dequantize_kernel(const uint8_t* __restrict__ data, float* __restrict__ B, Q4Geom geom) {
-    __shared__ float tile[kQ4UnitN][PITCH];
-    const int tid = threadIdx.x;
-    const int n0 = blockIdx.y * kQ4UnitN, k0 = blockIdx.x * TILE_K;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int y = blockIdx.y * 2 + (warp >> 2), block = warp & 3;
+    const int n0 = y * kQ4UnitN + block * 32, k0 = blockIdx.x * kQ4UnitK;
     const int N = geom.N, K = geom.K;
-    const int k = tid % TILE_K, part = tid / TILE_K;
-    {
-        const uint8_t* unit = unit_at(const_cast<uint8_t*>(data), geom);
-        const int col = first_column() + k, g = part * 32 / geom.group;
-        const int groups = kQ4UnitN / geom.group;
-        const uint4 w4 = __ldcs(reinterpret_cast<const uint4*>(unit) + part * kQ4UnitK + col);
-        const uint32_t word[4] = {w4.x, w4.y, w4.z, w4.w};
-        const float s = q4_scale(
-            reinterpret_cast<const uint16_t*>(unit + kQ4CodeBytes)[g * kQ4UnitK + col], geom.fp16);
-        const int z =
-            geom.zeros ? unit[kQ4CodeBytes + groups * kQ4UnitK * 2 + g * kQ4UnitK + col] : 8;
+    if (n0 >= N) return;
+    const uint8_t* unit = data + size_t(blockIdx.z) * geom.matrix_bytes() +
+                          blockIdx.x * geom.tile_bytes() + size_t(y) * geom.unit_bytes;
+    const int g = block * 32 / geom.group;
+    const uint16_t* scales = reinterpret_cast<const uint16_t*>(unit + kQ4CodeBytes) + g * kQ4UnitK;
+    const uint8_t* zeros = unit + kQ4CodeBytes + kQ4UnitN / geom.group * kQ4UnitK * 2 + g * kQ4UnitK;
+    uint32_t word[4][4];
+    float s[4], z[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                tile[part * 32 + 8 * i + e][k] =
-                    s * float(int((word[i] >> (4 * nibble_of(e))) & 15) - z);
+    for (int j = 0; j < 4; ++j) {
+        const int column = VEC ? lane * 4 + j : lane + 32 * j;
+        const uint4 w = __ldcs(reinterpret_cast<const uint4*>(unit) + block * kQ4UnitK + column);
+        word[j][0] = w.x;
+        word[j][1] = w.y;
+        word[j][2] = w.z;
+        word[j][3] = w.w;
+        s[j] = q4_scale(scales[column], geom.fp16);
+        // 2^23 + code less 2^23 + z: the difference is exact
+        z[j] = 8388608.0f + (geom.zeros ? float(zeros[column]) : 8.0f);
     }
-    __syncthreads();
-    float* out = B + size_t(blockIdx.z) * N * K;
-    if (k0 + k >= K) return;
-#pragma unroll 8
-    for (int i = 0; i < kQ4UnitN * TILE_K / THREADS; ++i) {
-        const int n = tid / TILE_K + i * (THREADS / TILE_K);
-        if (n0 + n < N) __stcs(out + size_t(n0 + n) * K + k0 + k, tile[n][k]);
+    float* row = B + (size_t(blockIdx.z) * N + n0) * K + k0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if (n0 + 8 * i + e >= N) return;
+            float f[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t code = (word[j][i] >> (4 * nibble_of(e))) & 15u;
+                f[j] = s[j] * (__uint_as_float(0x4b000000u | code) - z[j]);
+            }
+            if (VEC) {
+                if (k0 + lane * 4 < K)
+                    __stcs(reinterpret_cast<float4*>(row) + lane, make_float4(f[0], f[1], f[2], f[3]));
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (k0 + lane + 32 * j < K) __stcs(row + lane + 32 * j, f[j]);
+            }
+            row += K;
+        }
+}
+
+template <class T>
+void launch_quantize(const void* B, bool transposed, size_t values, uint8_t* out, const Q4Geom& g,
+                     int count, cudaStream_t stream) {
+    const dim3 grid(g.tiles, g.units, count);
+    const T* src = static_cast<const T*>(B);
+    if (transposed) {
+        if (g.zeros)
+            q4_quantize_kernel<T, true, true><<<grid, THREADS, 0, stream>>>(src, values, out, g);
+        else
+            q4_quantize_kernel<T, true, false><<<grid, THREADS, 0, stream>>>(src, values, out, g);
+    } else {
+        if (g.zeros)
+            q4_quantize_kernel<T, false, true><<<grid, THREADS, 0, stream>>>(src, values, out, g);
+        else
+            q4_quantize_kernel<T, false, false><<<grid, THREADS, 0, stream>>>(src, values, out, g);
     }
 }
 
@@ -206,9 +376,15 @@ int sgemm_q4_quantize(const void* B, int dtype, int transposed, const sgemm_q4* 
     if (!aligned_to(B, dtype_bytes(dtype))) return SGEMM_ERR_ARG;
     if (!current_device(nullptr)) return SGEMM_ERR_NO_DEVICE;
     const Q4Geom g = q4_geom(*w);
-    q4_pack_kernel<Source::values>
-        <<<tile_grid(g, w->count), THREADS, 0, static_cast<cudaStream_t>(stream)>>>(
-            B, dtype, transposed != 0, nullptr, nullptr, static_cast<uint8_t*>(w->data), g);
+    const size_t values = size_t(w->count) * w->N * w->K;
+    uint8_t* out = static_cast<uint8_t*>(w->data);
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (dtype == SGEMM_FLOAT32)
+        launch_quantize<float>(B, transposed != 0, values, out, g, w->count, s);
+    else if (dtype == SGEMM_BFLOAT16)
+        launch_quantize<__nv_bfloat16>(B, transposed != 0, values, out, g, w->count, s);
+    else
+        launch_quantize<__half>(B, transposed != 0, values, out, g, w->count, s);
     count_launch();
     return cudaGetLastError() == cudaSuccess ? SGEMM_OK : SGEMM_ERR_CUDA;
 }
@@ -227,10 +403,9 @@ int sgemm_q4_pack(const unsigned char* codes, const void* scales, const unsigned
         return SGEMM_ERR_OVERLAP;
     if (!aligned_to(scales, 2)) return SGEMM_ERR_ARG;
     if (!current_device(nullptr)) return SGEMM_ERR_NO_DEVICE;
-    q4_pack_kernel<Source::codes>
-        <<<tile_grid(g, w->count), THREADS, 0, static_cast<cudaStream_t>(stream)>>>(
-            codes, 0, transposed != 0, static_cast<const uint16_t*>(scales), zeros,
-            static_cast<uint8_t*>(w->data), g);
+    q4_pack_kernel<<<tile_grid(g, w->count), THREADS, 0, static_cast<cudaStream_t>(stream)>>>(
+        codes, transposed != 0, static_cast<const uint16_t*>(scales), zeros,
+        static_cast<uint8_t*>(w->data), g);
     count_launch();
     return cudaGetLastError() == cudaSuccess ? SGEMM_OK : SGEMM_ERR_CUDA;
 }
@@ -243,8 +418,13 @@ int sgemm_q4_dequantize(const sgemm_q4* w, float* B, void* stream) {
     if (!aligned_to(B, sizeof(float))) return SGEMM_ERR_ARG;
     if (!current_device(nullptr)) return SGEMM_ERR_NO_DEVICE;
     const Q4Geom g = q4_geom(*w);
-    q4_dequantize_kernel<<<tile_grid(g, w->count), THREADS, 0, static_cast<cudaStream_t>(stream)>>>(
-        static_cast<const uint8_t*>(w->data), B, g);
+    const dim3 grid(g.tiles, (g.units + 1) / 2, w->count);
+    const uint8_t* data = static_cast<const uint8_t*>(w->data);
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (w->K % 4 == 0 && aligned16(B))
+        q4_dequantize_kernel<true><<<grid, THREADS, 0, s>>>(data, B, g);
+    else
+        q4_dequantize_kernel<false><<<grid, THREADS, 0, s>>>(data, B, g);
     count_launch();
     return cudaGetLastError() == cudaSuccess ? SGEMM_OK : SGEMM_ERR_CUDA;
 }
