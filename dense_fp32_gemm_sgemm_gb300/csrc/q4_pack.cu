@@ -108,28 +108,33 @@ __device__ __noinline__ uint32_t word_of(const float* v, float s, float z, bool 
     return w;
 }
 
-// 8 codes of a word. The definition divides and rounds to nearest even. v times the rounded
-// reciprocal lies within 15.1 * 2^-23 < 2e-6 of the rounded quotient (two roundings against one),
-// so wherever it is less than 0.4999 from an integer, that integer is the definition's too. The
-// product is rounded by adding 1.5 * 2^23, in one instruction; the sum's low bits are the code.
-// Else, and for scales whose reciprocal is not a normal number, the word is made by the
-// definition.
-__device__ __forceinline__ uint32_t quick_word(const float (&v)[8], float s, float r, float z,
-                                               bool zeros) {
-    constexpr float ROUND = 12582912.0f;
-    constexpr uint32_t BITS = 0x4b400000u;  // ROUND's
+// 8 codes of a word. The definition divides and rounds to nearest, ties to even. v times the
+// rounded reciprocal is within 15.1 * 2^-23 of the quotient; rounding it to a grid of 2^-14 first
+// (by adding 768) puts ties, which quotients of short numbers often are, back where they belong,
+// and a quotient that this moves across a tie leaves a remainder of more than s / 2. The remainder
+// v - s q is exact (8 by 5 bits, and no larger than v), so where it is no more than s / 2, q is
+// the definition's: the rounded quotient is a tie only if the quotient is, since neighbours of
+// s (q + 1/2) in 24 bits are further off than half a place of the quotient. Else, for NaN, and
+// for scales far from one, the word is made by the definition.
+template <bool ZEROS>
+__device__ __forceinline__ uint32_t quick_word(const float (&v)[8], float s, float r, float z) {
+    constexpr float GRID = 768.0f, ROUND = 12582912.0f;  // 1.5 * 2^9, 1.5 * 2^23
+    constexpr uint32_t BITS = 0x4b400000u;               // ROUND's
+    const float half = 0.5f * s;
     bool ok = s >= 0x1p-100f && s <= 0x1p100f;
     uint32_t w = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        const float u = __fmaf_rn(v[e], r, ROUND);
-        const float off = __fmaf_rn(v[e], r, -__fsub_rn(u, ROUND));
-        ok = ok && fabsf(off) < 0.4999f;  // false for NaN
-        // without zero points no quotient passes 7 * (1 + 2^-8), so none is clipped
-        const int code = int(__float_as_uint(u) - BITS) + int(z);
-        w += uint32_t(zeros ? min(max(code, 0), 15) : code) << (4 * nibble_of(e));
+        const float u = __fadd_rn(__fmaf_rn(v[e], r, GRID), ROUND - GRID);
+        const float rest = __fmaf_rn(-s, __fsub_rn(u, ROUND), v[e]);
+        ok = ok && fabsf(rest) <= half;
+        uint32_t code = __float_as_uint(u);
+        if (ZEROS) code = uint32_t(min(max(int(code - BITS) + int(z), 0), 15));
+        w += code << (4 * nibble_of(e));
     }
-    return ok ? w : word_of(v, s, z, zeros);
+    // without zero points no quotient passes 7 * (1 + 2^-8), so none is clipped
+    if (!ZEROS) w += (8u - BITS) * 0x11111111u;
+    return ok ? w : word_of(v, s, z, ZEROS);
 }
 
 template <class T>
@@ -262,7 +267,7 @@ __global__ void __launch_bounds__(THREADS, 2)
                 float v8[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) v8[e] = v[j][8 * i + e];
-                word[i] = quick_word(v8, s, r, z, ZEROS);
+                word[i] = quick_word<ZEROS>(v8, s, r, z);
             }
         } else {
             word[0] = word[1] = word[2] = word[3] = uint32_t(z) * 0x11111111u;
