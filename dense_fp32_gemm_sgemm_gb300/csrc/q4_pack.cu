@@ -18,6 +18,9 @@ constexpr int TILE_K = 64;
 constexpr int PITCH = TILE_K + 1;  // column and row walks of the tile are free of conflicts
 constexpr int THREADS = 256;
 
+// Quantisation: 32 n of so many columns a thread
+constexpr int Q_COLS = 1, Q_WIDTH = 32 * Q_COLS, Q_THREADS = 128, Q_CTAS = 7;
+
 // The nibble of a word that holds the e-th of its 8 codes.
 __device__ constexpr int nibble_of(int e) { return (e >> 1) + 4 * (e & 1); }
 
@@ -120,21 +123,20 @@ template <bool ZEROS>
 __device__ __forceinline__ uint32_t quick_word(const float (&v)[8], float s, float r, float z) {
     constexpr float GRID = 768.0f, ROUND = 12582912.0f;  // 1.5 * 2^9, 1.5 * 2^23
     constexpr uint32_t BITS = 0x4b400000u;               // ROUND's
-    const float half = 0.5f * s;
-    bool ok = s >= 0x1p-100f && s <= 0x1p100f;
+    float most = 0.0f;  // of the remainders; NaN if one is
     uint32_t w = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         const float u = __fadd_rn(__fmaf_rn(v[e], r, GRID), ROUND - GRID);
         const float rest = __fmaf_rn(-s, __fsub_rn(u, ROUND), v[e]);
-        ok = ok && fabsf(rest) <= half;
+        asm("max.NaN.f32 %0, %0, %1;" : "+f"(most) : "f"(fabsf(rest)));
         uint32_t code = __float_as_uint(u);
         if (ZEROS) code = uint32_t(min(max(int(code - BITS) + int(z), 0), 15));
         w += code << (4 * nibble_of(e));
     }
     // without zero points no quotient passes 7 * (1 + 2^-8), so none is clipped
     if (!ZEROS) w += (8u - BITS) * 0x11111111u;
-    return ok ? w : word_of(v, s, z, ZEROS);
+    return s >= 0x1p-100f && s <= 0x1p100f && most <= 0.5f * s ? w : word_of(v, s, z, ZEROS);
 }
 
 template <class T>
@@ -185,43 +187,45 @@ __device__ __forceinline__ void load_along(const T* row, int n0, int N, const ch
 }
 
 template <class T, bool TRANSPOSED, bool ZEROS>
-__global__ void __launch_bounds__(THREADS, 2)
+__global__ void __launch_bounds__(Q_THREADS, Q_CTAS)
     q4_quantize_kernel(const T* __restrict__ src, size_t values, uint8_t* __restrict__ out,
                        Q4Geom geom) {
-    __shared__ float lo_s[4][kQ4UnitK], hi_s[4][kQ4UnitK];  // of 32 n each
+    __shared__ float lo_s[4][Q_WIDTH], hi_s[4][Q_WIDTH];  // of 32 n each
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int block = warp >> 1, first = (warp & 1) * 64 + lane;  // columns first and first + 32
-    const int n0 = blockIdx.y * kQ4UnitN + block * 32, k0 = blockIdx.x * kQ4UnitK;
+    const int block = warp;  // of 32 n
+    const int n0 = blockIdx.y * kQ4UnitN + block * 32, k0 = blockIdx.x * Q_WIDTH;
     const int N = geom.N, K = geom.K;
     const T* mat = src + size_t(blockIdx.z) * N * K;
 
-    float v[2][32];
+    float v[Q_COLS][32];
     if constexpr (TRANSPOSED) {
         const char* begin = reinterpret_cast<const char*>(src);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int k = k0 + first + 32 * j;
+        for (int j = 0; j < Q_COLS; ++j) {
+            const int k = k0 + lane + 32 * j;
             load_along(mat + size_t(k) * N, n0, k < K ? N : 0, begin, begin + values * sizeof(T),
                        v[j]);
         }
-    } else if (n0 + 32 <= N && k0 + kQ4UnitK <= K) {
-        const T* from = mat + size_t(n0) * K + k0 + first;
+    } else if (n0 + 32 <= N && k0 + Q_WIDTH <= K) {
+        // the CTA's corner and a 32-bit offset: one addition a load
+        const T* corner = mat + size_t(blockIdx.y) * kQ4UnitN * K + k0;
+        const uint32_t at = uint32_t(block * 32) * K + lane;
 #pragma unroll
         for (int i = 0; i < 32; ++i)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) v[j][i] = as_float(__ldcs(from + size_t(i) * K + 32 * j));
+            for (int j = 0; j < Q_COLS; ++j) v[j][i] = as_float(__ldcs(corner + (at + uint32_t(i) * K + 32 * j)));
     } else {
 #pragma unroll
         for (int i = 0; i < 32; ++i)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int k = k0 + first + 32 * j;
+            for (int j = 0; j < Q_COLS; ++j) {
+                const int k = k0 + lane + 32 * j;
                 v[j][i] = n0 + i < N && k < K ? as_float(mat[size_t(n0 + i) * K + k]) : 0.0f;
             }
     }
-    float lo[2] = {0.0f, 0.0f}, hi[2] = {0.0f, 0.0f};
+    float lo[Q_COLS] = {}, hi[Q_COLS] = {};
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < Q_COLS; ++j)
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
             lo[j] = fminf(lo[j], v[j][i]);
@@ -230,23 +234,23 @@ __global__ void __launch_bounds__(THREADS, 2)
     const int blocks = geom.group / 32, g = block / blocks;
     if (blocks > 1) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            lo_s[block][first + 32 * j] = lo[j];
-            hi_s[block][first + 32 * j] = hi[j];
+        for (int j = 0; j < Q_COLS; ++j) {
+            lo_s[block][lane + 32 * j] = lo[j];
+            hi_s[block][lane + 32 * j] = hi[j];
         }
         __syncthreads();
         for (int b = g * blocks; b < (g + 1) * blocks; ++b)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                lo[j] = fminf(lo[j], lo_s[b][first + 32 * j]);
-                hi[j] = fmaxf(hi[j], hi_s[b][first + 32 * j]);
+            for (int j = 0; j < Q_COLS; ++j) {
+                lo[j] = fminf(lo[j], lo_s[b][lane + 32 * j]);
+                hi[j] = fmaxf(hi[j], hi_s[b][lane + 32 * j]);
             }
     }
     uint8_t* unit = out + size_t(blockIdx.z) * geom.matrix_bytes() +
-                    blockIdx.x * geom.tile_bytes() + size_t(blockIdx.y) * geom.unit_bytes;
+                    k0 / kQ4UnitK * geom.tile_bytes() + size_t(blockIdx.y) * geom.unit_bytes;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const int column = first + 32 * j;
+    for (int j = 0; j < Q_COLS; ++j) {
+        const int column = k0 % kQ4UnitK + lane + 32 * j;
         float s = ZEROS ? __fsub_rn(__fdiv_rn(hi[j], 15.0f), __fdiv_rn(lo[j], 15.0f))
                         : __fdiv_rn(fmaxf(hi[j], -lo[j]), 7.0f);
         s = __bfloat162float(__float2bfloat16_rn(s));
@@ -333,18 +337,18 @@ __global__ void __launch_bounds__(THREADS)
 template <class T>
 void launch_quantize(const void* B, bool transposed, size_t values, uint8_t* out, const Q4Geom& g,
                      int count, cudaStream_t stream) {
-    const dim3 grid(g.tiles, g.units, count);
+    const dim3 grid(g.tiles * (kQ4UnitK / Q_WIDTH), g.units, count);
     const T* src = static_cast<const T*>(B);
     if (transposed) {
         if (g.zeros)
-            q4_quantize_kernel<T, true, true><<<grid, THREADS, 0, stream>>>(src, values, out, g);
+            q4_quantize_kernel<T, true, true><<<grid, Q_THREADS, 0, stream>>>(src, values, out, g);
         else
-            q4_quantize_kernel<T, true, false><<<grid, THREADS, 0, stream>>>(src, values, out, g);
+            q4_quantize_kernel<T, true, false><<<grid, Q_THREADS, 0, stream>>>(src, values, out, g);
     } else {
         if (g.zeros)
-            q4_quantize_kernel<T, false, true><<<grid, THREADS, 0, stream>>>(src, values, out, g);
+            q4_quantize_kernel<T, false, true><<<grid, Q_THREADS, 0, stream>>>(src, values, out, g);
         else
-            q4_quantize_kernel<T, false, false><<<grid, THREADS, 0, stream>>>(src, values, out, g);
+            q4_quantize_kernel<T, false, false><<<grid, Q_THREADS, 0, stream>>>(src, values, out, g);
     }
 }
 
