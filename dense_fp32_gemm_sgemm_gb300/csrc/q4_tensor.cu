@@ -291,6 +291,13 @@ __global__ void __launch_bounds__(THREADS, 1) q4_matmul_kernel(const Q4Product a
                 base[g] = 0x43004300u | z * 0x00010001u;
                 zero[g] = __uint_as_float(base[g] & 0xffff0000u) - 128.0f;
             }
+            __syncwarp();  // all lanes have read
+            if (lane == 0) ptx::mbar_arrive(empty(q_slot));
+            q_slot += 2;
+            if (q_slot >= plan.ring) {
+                q_slot -= plan.ring;
+                ++q_use;
+            }
         };
         auto operand = [&](int k) {
             if (wg + 2 * k >= total_units) return;
@@ -323,15 +330,7 @@ __global__ void __launch_bounds__(THREADS, 1) q4_matmul_kernel(const Q4Product a
             ptx::tmem_st_wait();
             ptx::tc_fence_before();
             __syncwarp();
-            if (lane == 0) {
-                ptx::mbar_arrive(empty(q_slot));
-                ptx::mbar_arrive(a_full(wg, k & 1));
-            }
-            q_slot += 2;
-            if (q_slot >= plan.ring) {
-                q_slot -= plan.ring;
-                ++q_use;
-            }
+            if (lane == 0) ptx::mbar_arrive(a_full(wg, k & 1));
         };
 
         float total[COLUMNS];
@@ -522,6 +521,7 @@ bool make_plan(const Q4Geom& g, int sm_count, Plan* best) {
         p.ring = (SMEM_LIMIT - STATIC - fixed) / g.unit_bytes;
         if (fixed > SMEM_LIMIT - STATIC || p.ring < 4) continue;
         if (p.ring > MAX_RING) p.ring = MAX_RING;
+        p.ring &= ~1;  // so that a slot's units are all one warpgroup's, which meets its phases in order
         p.smem = offsets<COLUMNS, GROUP>(p.units, p.ring, g.unit_bytes).end;
         const int slots = resident_clusters<q4_matmul_kernel<COLUMNS, GROUP, ZEROS>>(cluster, sm_count);
         p.clusters = g.tiles < slots ? g.tiles : slots;
