@@ -40,6 +40,7 @@ struct Staging {
     float* xsum;  // [group][column], sum_pitch floats a group
     int sum_pitch, log_octets;
     float factor;
+    int turn, turns;  // this CTA's number among those that stage the same rows
 };
 
 // Writes the pieces of the rows to their columns, and their sums (zeros for the centred form);
@@ -51,25 +52,28 @@ __device__ __noinline__ bool stage_rows(const Staging s, bool plain) {
     constexpr int AHEAD = 4;  // loads in flight
     constexpr int COLS = P == 3 ? 4 : P;  // of a row
     const T* A = static_cast<const T*>(s.A);
-    const int items = s.octets * s.rows;
+    // Warps take 32 octets at a time, of all rows in order, and each CTA starts elsewhere: lines that
+    // all of them want at once, and that L2 does not hold, come some three times as slowly.
+    const int items = s.octets * s.rows, lane = threadIdx.x & 31, warps = s.threads / 32;
+    const int bundles = (items + 31) / 32;
+    const int start = int(uint64_t(uint32_t(bundles)) * s.turn / s.turns);
+    const uint32_t reciprocal = 0xffffffffu / uint32_t(max(s.octets, 1)) + 1;  // items * octets < 2^32
     const int group_mask = (1 << s.log_octets) - 1;
-    int row = 0, u = threadIdx.x;
     Magnitudes magnitudes;
-    for (int i = threadIdx.x; i - int(threadIdx.x & 31) < items; i += AHEAD * s.threads) {
+    for (int i = threadIdx.x / 32; i < bundles; i += AHEAD * warps) {
         Raw8<T> raw[AHEAD];
         int rows[AHEAD], octets[AHEAD];
 #pragma unroll
         for (int j = 0; j < AHEAD; ++j) {
             rows[j] = -1;
-            if (i + j * s.threads < items) {
-                while (u >= s.octets) {
-                    u -= s.octets;
-                    ++row;
-                }
+            int bundle = i + j * warps + start;
+            if (bundle >= bundles) bundle -= bundles;
+            const int item = bundle * 32 + lane;
+            if (i + j * warps < bundles && item < items) {
+                const int row = int(__umulhi(uint32_t(item), reciprocal));
                 rows[j] = row;
-                octets[j] = u;
-                raw[j] = load_raw8(A + row * s.lda, s.n0 + u * 8, s.N, s.vec);
-                u += s.threads;
+                octets[j] = item - row * s.octets;
+                raw[j] = load_raw8(A + row * s.lda, s.n0 + octets[j] * 8, s.N, s.vec);
             }
         }
 #pragma unroll
@@ -89,7 +93,7 @@ __device__ __noinline__ bool stage_rows(const Staging s, bool plain) {
                                               (rows[j] * COLS + p) * s.column_stride) =
                         piece[p];
             }
-            if (i - int(threadIdx.x & 31) + j * s.threads >= items) continue;  // warp-uniform
+            if (i + j * warps >= bundles) continue;  // the same in the whole warp
 #pragma unroll
             for (int p = 0; p < P; ++p) {
                 for (int o = 1; o <= group_mask; o *= 2)

@@ -208,6 +208,8 @@ __global__ void __launch_bounds__(THREADS, 1) q4_matmul_kernel(const Q4Product a
     st.sum_pitch = COLUMNS;
     st.log_octets = GROUP == 32 ? 2 : GROUP == 64 ? 3 : 4;
     st.factor = ZEROS ? -1.0f : -8.0f;
+    st.turn = first_tile;
+    st.turns = plan.clusters;
     const bool special = stage_columns(st);
 
     if (warp == WARP_PRODUCER) {

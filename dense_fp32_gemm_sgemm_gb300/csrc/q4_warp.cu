@@ -143,6 +143,8 @@ __global__ void __launch_bounds__(THREADS, MOST_RESIDENT)
     st.sum_pitch = COLUMNS;
     st.log_octets = GROUP == 32 ? 2 : GROUP == 64 ? 3 : 4;
     st.factor = ZEROS ? -1.0f : -8.0f;
+    st.turn = first_group;
+    st.turns = plan.clusters;
     const bool special = stage_columns(st);
 
     // a lane's words of column r in the warp's first unit; columns that do not exist repeat the
