@@ -28,9 +28,10 @@
 namespace sgemm {
 namespace {
 
-constexpr int WARP_PRODUCER = 0, WARP_MMA = 1, WARP_OUTPUT = 3, WARP_GROUPS = 4;  // two MMA warps
-constexpr int WARPS = 12, THREADS = WARPS * 32;
-constexpr int OUTPUT_THREADS = (WARP_GROUPS - WARP_OUTPUT) * 32;
+// two MMA warps, eight of the warpgroups, four output warps
+constexpr int WARP_PRODUCER = 0, WARP_MMA = 1, WARP_SIGNAL = 3, WARP_GROUPS = 4, WARP_OUTPUT = 12;
+constexpr int WARPS = 16, THREADS = WARPS * 32;
+constexpr int OUTPUT_WARPS = WARPS - WARP_OUTPUT, OUTPUT_THREADS = OUTPUT_WARPS * 32;
 constexpr int MAX_RING = 20;
 constexpr int SMEM_LIMIT = 227 * 1024;
 constexpr int TMEM_COLUMNS = 512;  // two warpgroups' pairs of operand and accumulator buffers
@@ -58,15 +59,15 @@ struct Shape {
 
 // Where a CTA's shared memory holds what, in bytes.
 struct Offsets {
-    int ring, xsum, recv, bars, end;
+    int ring, xsum, send, bars, end;
 };
 template <int COLUMNS, int GROUP>
 __host__ __device__ constexpr Offsets offsets(int units, int ring, int unit_bytes) {
     Offsets o{};
     o.ring = units * (kQ4UnitN / 8) * Shape<COLUMNS>::STRIDE;
     o.xsum = o.ring + ring * unit_bytes;
-    o.recv = o.xsum + units * (kQ4UnitN / GROUP) * COLUMNS * 4;
-    o.bars = o.recv + 2 * 2 * kQ4UnitK * COLUMNS * 4;
+    o.send = o.xsum + units * (kQ4UnitN / GROUP) * COLUMNS * 4;
+    o.bars = o.send + 2 * 2 * kQ4UnitK * COLUMNS * 4;
     o.end = o.bars + 8 * (2 * MAX_RING + 20);
     return o;
 }
@@ -122,7 +123,8 @@ __global__ void __launch_bounds__(THREADS, 1) q4_matmul_kernel(const Q4Product a
     auto a_full = [&](int wg, int b) { return bar0 + 8u * (2 * MAX_RING + 2 * wg + b); };
     auto d_full = [&](int wg, int b) { return bar0 + 8u * (2 * MAX_RING + 4 + 2 * wg + b); };
     auto d_empty = [&](int wg, int b) { return bar0 + 8u * (2 * MAX_RING + 8 + 2 * wg + b); };
-    auto recv_full = [&](int b) { return bar0 + 8u * (2 * MAX_RING + 12 + b); };
+    auto send_full = [&](int b) { return bar0 + 8u * (2 * MAX_RING + 12 + b); };
+    auto peers_full = [&](int b) { return bar0 + 8u * (2 * MAX_RING + 18 + b); };
     auto credit = [&](int b) { return bar0 + 8u * (2 * MAX_RING + 14 + b); };
     auto drained = [&](int wg) { return bar0 + 8u * (2 * MAX_RING + 16 + wg); };
     // Bounded. When a wait gives up, the abort flag makes all later ones return at once: every
@@ -146,9 +148,9 @@ __global__ void __launch_bounds__(THREADS, 1) q4_matmul_kernel(const Q4Product a
                 ptx::mbar_init(d_empty(wg, b), 4);
             }
         for (int b = 0; b < 2; ++b) {
-            // each warp of each warpgroup signals each owner of some of its 32 rows once
-            ptx::mbar_init(recv_full(b), plan.cluster * 2 * max(1, slice / 32));
-            ptx::mbar_init(credit(b), plan.cluster);
+            ptx::mbar_init(send_full(b), 8);  // the warps of the warpgroups
+            ptx::mbar_init(peers_full(b), plan.cluster);
+            ptx::mbar_init(credit(b), plan.cluster * OUTPUT_WARPS);
         }
         for (int wg = 0; wg < 2; ++wg) ptx::mbar_init(drained(wg), 1);
         abort_s = 0;
@@ -220,7 +222,7 @@ __global__ void __launch_bounds__(THREADS, 1) q4_matmul_kernel(const Q4Product a
                 fetch();
             }
         __syncwarp();
-    } else if (warp < WARP_OUTPUT) {
+    } else if (warp < WARP_SIGNAL) {
         constexpr uint32_t idesc = idesc_bf16(S::N);
         const uint32_t xs = ptx::smem_u32(smem);
         const int wg = warp - WARP_MMA;
@@ -257,7 +259,18 @@ __global__ void __launch_bounds__(THREADS, 1) q4_matmul_kernel(const Q4Product a
             ptx::mma_commit(drained(wg));
             wait_drained(drained(wg), 0);
         }
-    } else if (warp >= WARP_GROUPS) {
+    } else if (warp == WARP_SIGNAL) {
+        // Tells the owners that this CTA's totals are there. An arrival on another CTA's barrier
+        // that releases what was written here takes some 1500 cycles, which the warpgroups would
+        // otherwise spend on each tile.
+        if (plan.cluster > 1)
+            for (int i = 0; i < tiles; ++i) {
+                wait(send_full(i & 1), i >> 1);
+                if (lane < plan.cluster)
+                    ptx::mbar_arrive_cluster(ptx::mapa_shared(peers_full(i & 1), lane));
+            }
+        __syncwarp();
+    } else if (warp < WARP_OUTPUT) {
         auto work = [&](auto centred) {
         constexpr bool CENTRED = decltype(centred)::value;
         const int wg = (warp - WARP_GROUPS) >> 2;
@@ -383,33 +396,18 @@ __global__ void __launch_bounds__(THREADS, 1) q4_matmul_kernel(const Q4Product a
                 }
                 operand(k + 2);
             }
-            // push the totals to the owner of this row of the tile: [source][4 columns][row]
+            // the totals: [warpgroup][4 columns][row]; the owners of the rows fetch them
             const int buffer = i & 1;
             wait(credit(buffer), (i >> 1) + 1, plan.cluster > 1);
-            const int owner = row / slice, local = row - owner * slice;
-            const int source = buffer * 2 * plan.cluster + rank * 2 + wg;
-            const int to = (source * (COLUMNS / 4) * slice + local) * 16;
-            if (plan.cluster == 1) {
-                float4* mine = reinterpret_cast<float4*>(smem + at.recv + to);
+            float4* mine = reinterpret_cast<float4*>(smem + at.send) +
+                           (buffer * 2 + wg) * (COLUMNS / 4) * kQ4UnitK + row;
 #pragma unroll
-                for (int q = 0; q < COLUMNS / 4; ++q)
-                    if (q < quads)
-                        mine[q * slice] = make_float4(total[4 * q], total[4 * q + 1],
-                                                      total[4 * q + 2], total[4 * q + 3]);
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(recv_full(buffer));
-            } else {
-                const uint32_t theirs = ptx::mapa_shared(ptx::smem_u32(smem + at.recv), owner) + to;
-#pragma unroll
-                for (int q = 0; q < COLUMNS / 4; ++q)
-                    if (q < quads)
-                        ptx::st_shared_cluster_v4(theirs + q * slice * 16, total[4 * q],
-                                                  total[4 * q + 1], total[4 * q + 2],
-                                                  total[4 * q + 3]);
-                __syncwarp();  // the arrival below releases the whole warp's stores
-                if (lane % min(slice, 32) == 0)
-                    ptx::mbar_arrive_cluster(ptx::mapa_shared(recv_full(buffer), owner));
-            }
+            for (int q = 0; q < COLUMNS / 4; ++q)
+                if (q < quads)
+                    mine[q * kQ4UnitK] = make_float4(total[4 * q], total[4 * q + 1],
+                                                     total[4 * q + 2], total[4 * q + 3]);
+            __syncwarp();  // the arrival below releases the whole warp's stores
+            if (lane == 0) ptx::mbar_arrive(send_full(buffer));
         }
         };
         if (special)
@@ -417,25 +415,33 @@ __global__ void __launch_bounds__(THREADS, 1) q4_matmul_kernel(const Q4Product a
         else
             work(std::false_type());
     } else {
-        // output warps: the sources' sums of this CTA's slice of each tile, in rank order
+        // output warps: the totals of this CTA's slice of each tile, in rank order
         const int id = threadIdx.x - WARP_OUTPUT * 32;
-        const int sources = 2 * plan.cluster, slice_log = __ffs(slice) - 1;
+        const int slice_log = __ffs(slice) - 1;
+        const bool alone = plan.cluster == 1;
         for (int i = 0; i < tiles; ++i) {
             const int buffer = i & 1;
-            wait(recv_full(buffer), i >> 1, plan.cluster > 1);
+            wait(alone ? send_full(buffer) : peers_full(buffer), i >> 1, !alone);
             const int k0 = (first_tile + i * plan.clusters) * kQ4UnitK + rank * slice;
-            const float4* from = reinterpret_cast<const float4*>(smem + at.recv) +
-                                 buffer * sources * (COLUMNS / 4) * slice;
+            const uint32_t from = ptx::smem_u32(smem + at.send) +
+                                  (buffer * 2 * (COLUMNS / 4) * kQ4UnitK + rank * slice) * 16;
             for (int cell = id; cell < quads << slice_log; cell += OUTPUT_THREADS) {
-                const int q = cell >> slice_log, k = k0 + cell - (q << slice_log);
+                const int q = cell >> slice_log, local = cell - (q << slice_log), k = k0 + local;
                 float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
-                for (int src = 0; src < sources; ++src) {
-                    const float4 x = from[src * (COLUMNS / 4) * slice + cell];
-                    v.x += x.x;
-                    v.y += x.y;
-                    v.z += x.z;
-                    v.w += x.w;
+                for (int src = 0; src < plan.cluster; ++src) {
+                    const uint32_t theirs = alone ? from : ptx::mapa_shared(from, src);
+#pragma unroll
+                    for (int wg = 0; wg < 2; ++wg) {
+                        const uint32_t there =
+                            theirs + ((wg * (COLUMNS / 4) + q) * kQ4UnitK + local) * 16;
+                        const float4 x =
+                            alone ? ptx::ld_shared_v4(there) : ptx::ld_shared_cluster_v4(there);
+                        v.x += x.x;
+                        v.y += x.y;
+                        v.z += x.z;
+                        v.w += x.w;
+                    }
                 }
                 if (k >= geom.K) continue;
                 size_t to = row0 * args.ldc + k;
