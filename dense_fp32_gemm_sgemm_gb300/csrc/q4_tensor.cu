@@ -15,10 +15,16 @@
 //    registers. With two units of each warpgroup in flight the round trip through tensor
 //    memory (about 700 cycles) is hidden.
 // The columns are staged in shared memory once for all the tiles of a CTA. Where the tiles alone
-// would not fill the GPU, or the columns not fit, the CTAs of a cluster split n; each thread
-// pushes its totals to the CTA that owns its part of the tile through distributed shared
-// memory, and two output warps there add them in a fixed order and write C: one launch, no
+// would not fill the GPU, or the columns not fit, the CTAs of a cluster split n. Each CTA then
+// owns a part of the tile's columns of C; its output warps fetch all CTAs' totals of that part
+// through distributed shared memory, add them in a fixed order and write C: one launch, no
 // workspace, no atomics.
+//
+// What bounds it: the instructions of a unit in two warpgroups, some 600 cycles an SM against the
+// 365 that its bytes take at HBM's rate. 16 x 8192 by 65536 columns, group 128: 74 us (3.7 TB/s);
+// 16 x 8192 by 6144, group 64: 18.0 us; 64 x 8192 by 65536 (two launches' worth of rows in one
+// grid, each reading the weights): 215 us. Four warpgroups with one unit each in flight measured
+// 91, 26 and 216 us, short of registers.
 #include <atomic>
 #include <type_traits>
 
@@ -272,143 +278,143 @@ __global__ void __launch_bounds__(THREADS, 1) q4_matmul_kernel(const Q4Product a
         __syncwarp();
     } else if (warp < WARP_OUTPUT) {
         auto work = [&](auto centred) {
-        constexpr bool CENTRED = decltype(centred)::value;
-        const int wg = (warp - WARP_GROUPS) >> 2;
-        const int row = (warp & 3) * 32 + lane;  // of the tile, and lane of tensor memory
-        const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
-        constexpr float unscale = CENTRED ? 1.0f : kQ4Unscale;
-        float scale0[GROUPS], scale1[GROUPS];  // of the unit in buffer 0 and 1
-        float zero0[GROUPS], zero1[GROUPS];
+            constexpr bool CENTRED = decltype(centred)::value;
+            const int wg = (warp - WARP_GROUPS) >> 2;
+            const int row = (warp & 3) * 32 + lane;  // of the tile, and lane of tensor memory
+            const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
+            constexpr float unscale = CENTRED ? 1.0f : kQ4Unscale;
+            float scale0[GROUPS], scale1[GROUPS];  // of the unit in buffer 0 and 1
+            float zero0[GROUPS], zero1[GROUPS];
 #pragma unroll
-        for (int g = 0; g < GROUPS; ++g) scale0[g] = scale1[g] = zero0[g] = zero1[g] = 1.0f;
+            for (int g = 0; g < GROUPS; ++g) scale0[g] = scale1[g] = zero0[g] = zero1[g] = 1.0f;
 
-        // Unit number k of this warpgroup's (sequence number wg + 2 k): read() takes its codes,
-        // scales and zero points into registers, operand() turns them into operand words.
-        int q_slot = wg, q_use = 0;
-        uint4 w[4];
-        float scale[GROUPS], zero[GROUPS];
-        uint32_t base[GROUPS];
-        auto read = [&](int k) {
-            if (wg + 2 * k >= total_units) return;
-            wait(full(q_slot), q_use);
-            const uint8_t* unit = ring + q_slot * geom.unit_bytes;
+            // Unit number k of this warpgroup's (sequence number wg + 2 k): read() takes its codes,
+            // scales and zero points into registers, operand() turns them into operand words.
+            int q_slot = wg, q_use = 0;
+            uint4 w[4];
+            float scale[GROUPS], zero[GROUPS];
+            uint32_t base[GROUPS];
+            auto read = [&](int k) {
+                if (wg + 2 * k >= total_units) return;
+                wait(full(q_slot), q_use);
+                const uint8_t* unit = ring + q_slot * geom.unit_bytes;
 #pragma unroll
-            for (int b = 0; b < 4; ++b)
-                w[b] = reinterpret_cast<const uint4*>(unit)[b * kQ4UnitK + row];
+                for (int b = 0; b < 4; ++b)
+                    w[b] = reinterpret_cast<const uint4*>(unit)[b * kQ4UnitK + row];
 #pragma unroll
-            for (int g = 0; g < GROUPS; ++g) {
-                scale[g] = q4_scale(
-                    reinterpret_cast<const uint16_t*>(unit + kQ4CodeBytes)[g * kQ4UnitK + row],
-                    geom.fp16);
-                uint32_t z = 8;
-                if constexpr (ZEROS)
-                    z = unit[kQ4CodeBytes + GROUPS * kQ4UnitK * 2 + g * kQ4UnitK + row];
-                base[g] = 0x43004300u | z * 0x00010001u;
-                zero[g] = __uint_as_float(base[g] & 0xffff0000u) - 128.0f;
-            }
-            __syncwarp();  // all lanes have read
-            if (lane == 0) ptx::mbar_arrive(empty(q_slot));
-            q_slot += 2;
-            if (q_slot >= plan.ring) {
-                q_slot -= plan.ring;
-                ++q_use;
-            }
-        };
-        auto operand = [&](int k) {
-            if (wg + 2 * k >= total_units) return;
-            const uint32_t a = tmem + lanes + uint32_t(wg * 2 + (k & 1)) * TMEM_SLOT;
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                const uint32_t word[4] = {w[b].x, w[b].y, w[b].z, w[b].w};
-                uint32_t r[16];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t o[4];
-                    if constexpr (CENTRED)
-                        q4_centred(word[i], base[b * 32 / GROUP], o);
-                    else
-                        q4_plain(word[i], o);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) r[4 * i + j] = o[j];
+                for (int g = 0; g < GROUPS; ++g) {
+                    scale[g] = q4_scale(
+                        reinterpret_cast<const uint16_t*>(unit + kQ4CodeBytes)[g * kQ4UnitK + row],
+                        geom.fp16);
+                    uint32_t z = 8;
+                    if constexpr (ZEROS)
+                        z = unit[kQ4CodeBytes + GROUPS * kQ4UnitK * 2 + g * kQ4UnitK + row];
+                    base[g] = 0x43004300u | z * 0x00010001u;
+                    zero[g] = __uint_as_float(base[g] & 0xffff0000u) - 128.0f;
                 }
-                ptx::tmem_st_16(a + b * 16, r);
-            }
-#pragma unroll
-            for (int g = 0; g < GROUPS; ++g) {
-                scale0[g] = k & 1 ? scale0[g] : scale[g];
-                scale1[g] = k & 1 ? scale[g] : scale1[g];
-                if constexpr (ZEROS) {
-                    zero0[g] = k & 1 ? zero0[g] : zero[g];
-                    zero1[g] = k & 1 ? zero[g] : zero1[g];
+                __syncwarp();  // all lanes have read
+                if (lane == 0) ptx::mbar_arrive(empty(q_slot));
+                q_slot += 2;
+                if (q_slot >= plan.ring) {
+                    q_slot -= plan.ring;
+                    ++q_use;
                 }
-            }
-            ptx::tmem_st_wait();
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(a_full(wg, k & 1));
-        };
+            };
+            auto operand = [&](int k) {
+                if (wg + 2 * k >= total_units) return;
+                const uint32_t a = tmem + lanes + uint32_t(wg * 2 + (k & 1)) * TMEM_SLOT;
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    const uint32_t word[4] = {w[b].x, w[b].y, w[b].z, w[b].w};
+                    uint32_t r[16];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t o[4];
+                        if constexpr (CENTRED)
+                            q4_centred(word[i], base[b * 32 / GROUP], o);
+                        else
+                            q4_plain(word[i], o);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) r[4 * i + j] = o[j];
+                    }
+                    ptx::tmem_st_16(a + b * 16, r);
+                }
+#pragma unroll
+                for (int g = 0; g < GROUPS; ++g) {
+                    scale0[g] = k & 1 ? scale0[g] : scale[g];
+                    scale1[g] = k & 1 ? scale[g] : scale1[g];
+                    if constexpr (ZEROS) {
+                        zero0[g] = k & 1 ? zero0[g] : zero[g];
+                        zero1[g] = k & 1 ? zero[g] : zero1[g];
+                    }
+                }
+                ptx::tmem_st_wait();
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(a_full(wg, k & 1));
+            };
 
-        float total[COLUMNS];
-        read(0);
-        operand(0);
-        read(1);
-        operand(1);
-        int k = 0;
-        for (int i = 0; i < tiles; ++i) {
+            float total[COLUMNS];
+            read(0);
+            operand(0);
+            read(1);
+            operand(1);
+            int k = 0;
+            for (int i = 0; i < tiles; ++i) {
 #pragma unroll
-            for (int j = 0; j < COLUMNS; ++j) total[j] = 0.0f;
-            for (int in_tile = wg ^ (i * units & 1); in_tile < units; in_tile += 2, ++k) {
-                read(k + 2);
+                for (int j = 0; j < COLUMNS; ++j) total[j] = 0.0f;
+                for (int in_tile = wg ^ (i * units & 1); in_tile < units; in_tile += 2, ++k) {
+                    read(k + 2);
 #pragma unroll
-                for (int step = 0; step < STEPS; ++step) {
-                    const int use = k * STEPS + step;
-                    wait(d_full(wg, use & 1), use >> 1);
-                    ptx::tc_fence_after();
-                    const uint32_t d = tmem + lanes + uint32_t(4 + wg * 2 + (use & 1)) * TMEM_SLOT;
-                    constexpr int READ = COLUMNS < 16 ? COLUMNS : 16;
+                    for (int step = 0; step < STEPS; ++step) {
+                        const int use = k * STEPS + step;
+                        wait(d_full(wg, use & 1), use >> 1);
+                        ptx::tc_fence_after();
+                        const uint32_t d = tmem + lanes + uint32_t(4 + wg * 2 + (use & 1)) * TMEM_SLOT;
+                        constexpr int READ = COLUMNS < 16 ? COLUMNS : 16;
 #pragma unroll
-                    for (int g = 0; g < GROUPS_SLOT; ++g) {
-                        const int gg = step * GROUPS_SLOT + g;
-                        const float s = k & 1 ? scale1[gg] : scale0[gg];
-                        const float z = k & 1 ? zero1[gg] : zero0[gg];
-                        const float4* xs4 = reinterpret_cast<const float4*>(
-                            xsum + (in_tile * GROUPS + gg) * COLUMNS);
+                        for (int g = 0; g < GROUPS_SLOT; ++g) {
+                            const int gg = step * GROUPS_SLOT + g;
+                            const float s = k & 1 ? scale1[gg] : scale0[gg];
+                            const float z = k & 1 ? zero1[gg] : zero0[gg];
+                            const float4* xs4 = reinterpret_cast<const float4*>(
+                                xsum + (in_tile * GROUPS + gg) * COLUMNS);
 #pragma unroll
-                        for (int c0 = 0; c0 < COLUMNS; c0 += READ) {
-                            float acc[READ];
-                            ptx::tmem_ld<READ>(d + g * S::N + c0, acc);
+                            for (int c0 = 0; c0 < COLUMNS; c0 += READ) {
+                                float acc[READ];
+                                ptx::tmem_ld<READ>(d + g * S::N + c0, acc);
 #pragma unroll
-                            for (int c = 0; c < READ; c += 4) {
-                                const float4 x4 = xs4[(c0 + c) / 4];
-                                const float x[4] = {x4.x, x4.y, x4.z, x4.w};
+                                for (int c = 0; c < READ; c += 4) {
+                                    const float4 x4 = xs4[(c0 + c) / 4];
+                                    const float x[4] = {x4.x, x4.y, x4.z, x4.w};
 #pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    const float t =
-                                        fmaf(acc[c + e], unscale, ZEROS ? z * x[e] : x[e]);
-                                    total[c0 + c + e] = fmaf(s, t, total[c0 + c + e]);
+                                    for (int e = 0; e < 4; ++e) {
+                                        const float t =
+                                            fmaf(acc[c + e], unscale, ZEROS ? z * x[e] : x[e]);
+                                        total[c0 + c + e] = fmaf(s, t, total[c0 + c + e]);
+                                    }
                                 }
                             }
                         }
+                        ptx::tc_fence_before();
+                        __syncwarp();
+                        if (STEPS > 1 && lane == 0) ptx::mbar_arrive(d_empty(wg, use & 1));
                     }
-                    ptx::tc_fence_before();
-                    __syncwarp();
-                    if (STEPS > 1 && lane == 0) ptx::mbar_arrive(d_empty(wg, use & 1));
+                    operand(k + 2);
                 }
-                operand(k + 2);
-            }
-            // the totals: [warpgroup][4 columns][row]; the owners of the rows fetch them
-            const int buffer = i & 1;
-            wait(credit(buffer), (i >> 1) + 1, plan.cluster > 1);
-            float4* mine = reinterpret_cast<float4*>(smem + at.send) +
-                           (buffer * 2 + wg) * (COLUMNS / 4) * kQ4UnitK + row;
+                // the totals: [warpgroup][4 columns][row]; the owners of the rows fetch them
+                const int buffer = i & 1;
+                wait(credit(buffer), (i >> 1) + 1, plan.cluster > 1);
+                float4* mine = reinterpret_cast<float4*>(smem + at.send) +
+                               (buffer * 2 + wg) * (COLUMNS / 4) * kQ4UnitK + row;
 #pragma unroll
-            for (int q = 0; q < COLUMNS / 4; ++q)
-                if (q < quads)
-                    mine[q * kQ4UnitK] = make_float4(total[4 * q], total[4 * q + 1],
-                                                     total[4 * q + 2], total[4 * q + 3]);
-            __syncwarp();  // the arrival below releases the whole warp's stores
-            if (lane == 0) ptx::mbar_arrive(send_full(buffer));
-        }
+                for (int q = 0; q < COLUMNS / 4; ++q)
+                    if (q < quads)
+                        mine[q * kQ4UnitK] = make_float4(total[4 * q], total[4 * q + 1],
+                                                         total[4 * q + 2], total[4 * q + 3]);
+                __syncwarp();  // the arrival below releases the whole warp's stores
+                if (lane == 0) ptx::mbar_arrive(send_full(buffer));
+            }
         };
         if (special)
             work(std::true_type());
@@ -513,9 +519,10 @@ int resident_clusters(int cluster, int sm_count) {
 }
 
 // The split of the product: the cluster size whose slowest SM is done first. In cycles: a
-// unit takes an SM 250, or what its bytes take of HBM's rate (3500 a cycle) when all that are
-// busy share it; a launch's set-up and its tail do not depend on the split, a cluster's exchange
-// costs some hundreds.
+// unit takes an SM 600, or what its bytes take of HBM's rate (3500 a cycle) when all that are
+// busy share it; a cluster's exchange 1500 a tile; staging 28 a column and unit. Larger clusters
+// stage less each but exchange more, and of 8 only 15 are resident: 16 rows of 4096 by 14336
+// columns take 19.8, 17.6, 16.6 and 21.1 us with clusters of 1, 2, 4 and 8.
 template <int COLUMNS, int GROUP, bool ZEROS>
 bool make_plan(const Q4Geom& g, int sm_count, Plan* best) {
     constexpr int STATIC = 1024;  // statically allocated shared memory and the system's
@@ -536,8 +543,8 @@ bool make_plan(const Q4Geom& g, int sm_count, Plan* best) {
         const int rounds = (g.tiles + p.clusters - 1) / p.clusters;
         const double shared = double(g.unit_bytes) * p.clusters * cluster / 3500.0;
         const double cost =
-            rounds * (p.units * (shared > 300.0 ? shared : 300.0) + (cluster > 1 ? 500.0 : 200.0)) +
-            10.0 * COLUMNS * p.units;
+            rounds * (p.units * (shared > 600.0 ? shared : 600.0) + (cluster > 1 ? 1500.0 : 200.0)) +
+            28.0 * COLUMNS * p.units;
         if (cost < best_cost) {
             best_cost = cost;
             *best = p;
