@@ -2,26 +2,35 @@
 // reading the weights of the experts that some token picked, once.
 //
 // moe_route_kernel: a cluster of 8 CTAs a token shares the router's rows, writes the token as
-// bfloat16 pieces, and its first CTA chooses the experts.
+// bfloat16 pieces (staged for the plain form of the weights and, once more, as they are for the
+// centred form), and its first CTA chooses the experts.
 //
 // moe_expert_kernel: every CTA builds the same lists of the picked experts' tokens, cut into tiles
 // of so many tokens that an expert's weights are read once for each tile. Then the CTAs take work
 // items in order from a counter:
-//   first items: one tile x some strips of 16 hidden values, gate and up; h = silu(g) u times
+//   first items: one tile x some sets of 32 hidden values, gate and up; h = silu(g) u times
 //     the token's weight goes to scratch as bfloat16 pieces;
-//   second items: one tile x some pairs of strips of the output: the rows of h times down go to
+//   second items: one tile x some sets of 64 columns of the output: the rows of h times down go to
 //     scratch in FP32, one row for each token and expert;
-//   sum items: 32 columns of the output, each token's rows added in the order of its experts.
+//   sum items: 32 columns of 16 tokens' output, each token's rows added in the order of its experts.
 // So a token's result does not depend on which other tokens there are. An item that needs earlier
 // ones waits for a count of them. Those have been taken before it, by CTAs that are running and
 // wait for still earlier ones at most, so every wait ends whatever the number of CTAs that are
 // resident. Meanwhile each warp's ring of cp.async stages already fills with the item's weights:
 // HBM stays busy across items and across the waits.
 //
-// The inner product is that of q4_warp.cuh, on chunk pairs (gate and up, or two strips of down), so
-// that a column's words serve two strips. The sums of x that zero points take come from one more
-// matrix instruction on a constant operand (z's place taken by 8, or by 1 and multiplied by z
-// afterwards): hidden values of a group come from several CTAs, so they cannot be summed beforehand.
+// The inner product is that of q4_warp.cuh, on sets of four chunks (two strips of gate and of up, or
+// four of down), so that a column's words serve four strips (two gave 428 us instead of 338 at the
+// largest case below). The sums of x that zero points take are kept beside the pieces, for each 32 n
+// (a group's hidden values may come from several CTAs, but 32 of them come from one). Taken by one
+// more matrix instruction on a constant operand, whose sums are truncated, they more than doubled the
+// error of float32 layers with zero points (5.8e-7 instead of 2.4e-7 of the result's norm).
+//
+// Measured, experts of 4096 x 2048, 8 of 64 picked, group 128, bfloat16: one token 43 us (its
+// weights take 15.6 at HBM's rate), 64 tokens 350 us (124). 8 experts of 512 x 512, one token: 17 us.
+// What bounds it: with few items, latencies, a third of them for instructions that come from far
+// (routing 6 us, lists 2, each phase 4 and its products); with many, the instructions of a set, some
+// 400 for one tile of columns, at 16 warps an SM.
 #include <cmath>
 #include <type_traits>
 
@@ -63,6 +72,9 @@ struct MoeArgs {
     uint16_t* xp;      // of x: [token][piece][D padded to units]
     uint16_t* hp;      // of the hidden values: [token and slot][piece][F padded]
     size_t x_form, h_form;
+    // sums of 32 values of each piece, times -8 or, where the weights have zero points, -1
+    float *x_sum, *h_sum;
+    float x_factor, h_factor;
     int* x_special;    // [token]: nonzero where the plain form cannot take some value
     int* h_special;    // [token and slot]
     // 0: next item, 1: first items done, 2: whether some h_special is set, 3 ..: second items done
@@ -125,18 +137,31 @@ __device__ __forceinline__ bool write_pieces(const MoeArgs& a, int t, int rank, 
     constexpr int P = pieces_of_type<T>();
     const T* x = static_cast<const T*>(a.x) + t * a.ldx;
     Magnitudes magnitudes;
-    const int octets = padded / 8;
-    for (int u = rank * ROUTE_THREADS + threadIdx.x; u < octets; u += ROUTE_CTAS * ROUTE_THREADS) {
-        const Raw8<T> raw = load_raw8(x, u * 8, a.D, a.vec);
-        uint4 plain[P], centred[P];
-        float sums[P];  // not used: they are taken with the product
-        split_plain<P>(raw, magnitudes, plain, sums);
-        split_centred<P>(raw, centred);
+    const int octets = padded / 8, lane = threadIdx.x & 31;
+    for (int first = rank * ROUTE_THREADS + threadIdx.x - lane; first < octets;
+         first += ROUTE_CTAS * ROUTE_THREADS) {
+        const int u = first + lane;  // octets are a multiple of four
+        float sums[P];
+#pragma unroll
+        for (int p = 0; p < P; ++p) sums[p] = 0.0f;
+        if (u < octets) {
+            const Raw8<T> raw = load_raw8(x, u * 8, a.D, a.vec);
+            uint4 plain[P], centred[P];
+            split_plain<P>(raw, magnitudes, plain, sums);
+            split_centred<P>(raw, centred);
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+                uint16_t* to = a.xp + (size_t(t) * P + p) * padded;
+                reinterpret_cast<uint4*>(to)[u] = plain[p];
+                reinterpret_cast<uint4*>(to + a.x_form)[u] = centred[p];
+            }
+        }
 #pragma unroll
         for (int p = 0; p < P; ++p) {
-            uint16_t* to = a.xp + (size_t(t) * P + p) * padded;
-            reinterpret_cast<uint4*>(to)[u] = plain[p];
-            reinterpret_cast<uint4*>(to + a.x_form)[u] = centred[p];
+            sums[p] += __shfl_xor_sync(0xffffffffu, sums[p], 1);
+            sums[p] += __shfl_xor_sync(0xffffffffu, sums[p], 2);
+            if (u < octets && lane % 4 == 0)
+                a.x_sum[(size_t(t) * P + p) * (padded / 32) + u / 4] = sums[p] * a.x_factor;
         }
     }
     return magnitudes.special<T>();
@@ -296,32 +321,24 @@ __host__ __device__ constexpr int most_tiles(int E, int slots, int capacity) {
 }
 
 // MT chunks (at stage, stage + chunk, ...) times NT tiles of 8 columns, added to total as in
-// q4_chunk. x(b, nt): the lane's 8 values of block b of column 8 nt + r, staged for the plain form.
+// q4_chunk. x(b, nt): the lane's 8 values of block b of column 8 nt + r, staged for the plain form;
+// sum(g, nt): the kept sums over group g of columns 8 nt + 2 c and + 1.
 // GROUP 0: the stack's own group size and zero points.
-template <int MT, int NT, int GROUP, bool ZEROS, class X>
+template <int MT, int NT, int GROUP, bool ZEROS, class X, class Sum>
 __device__ __forceinline__ void chunk_set(const uint8_t* stage, int chunk, const Q4Geom& geom, int lane,
-                                          X&& x, float (*total)[NT][4]) {
+                                          X&& x, Sum&& sum, float (*total)[NT][4]) {
     const int r = lane >> 2;
     const int blocks = GROUP ? GROUP / 32 : geom.group / 32;
     const int groups = GROUP ? kQ4UnitN / (GROUP ? GROUP : 32) : kQ4UnitN / geom.group;
     const bool zeros = GROUP ? ZEROS : geom.zeros != 0;
-    const uint32_t one = zeros ? 0x00010001u : 0x00080008u;
-    const uint32_t ones[4] = {one, one, one << 4, one << 4};
     constexpr int BLOCKS = GROUP ? GROUP / 32 : 1;
 #pragma unroll(NT == 1 && GROUP ? 4 : 1)
     for (int g = 0; g < groups; ++g) {
-        float acc[MT][NT][4], sum[NT][4];
+        float acc[MT][NT][4];
         auto block = [&](int b, bool first) {
             uint4 v[NT];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                v[nt] = x(b, nt);
-                if (first)
-                    mma_bf16_first(sum[nt], ones, v[nt].x, v[nt].y);
-                else
-                    mma_bf16(sum[nt], ones, v[nt].x, v[nt].y);
-                mma_bf16(sum[nt], ones, v[nt].z, v[nt].w);
-            }
+            for (int nt = 0; nt < NT; ++nt) v[nt] = x(b, nt);
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
                 const uint32_t* codes =
@@ -349,6 +366,9 @@ __device__ __forceinline__ void chunk_set(const uint8_t* stage, int chunk, const
 #pragma unroll 1
             for (int k = 1; k < blocks; ++k) block(g * blocks + k, false);
         }
+        float2 xs[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) xs[nt] = sum(g, nt);
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
             const uint8_t* side = stage + m * chunk + kQ4ChunkCodes;
@@ -364,13 +384,22 @@ __device__ __forceinline__ void chunk_set(const uint8_t* stage, int chunk, const
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    // the sums are alike in all rows of the constant operand
-                    const float d =
-                        fmaf(i < 2 ? -z0 : -z1, sum[nt][i & 1], acc[m][nt][i]) * kQ4Unscale;
+                    const float d = fmaf(acc[m][nt][i], kQ4Unscale,
+                                         (i < 2 ? z0 : z1) * (i & 1 ? xs[nt].y : xs[nt].x));
                     total[m][nt][i] = fmaf(i < 2 ? s0 : s1, d, total[m][nt][i]);
                 }
         }
     }
+}
+// A group's sum of the kept sums of a unit's four blocks of 32 n.
+template <int GROUP>
+__device__ __forceinline__ float group_sum(const float* block, int g, int group) {
+    if constexpr (GROUP == 32) return block[g];
+    if constexpr (GROUP == 64) return block[2 * g] + block[2 * g + 1];
+    if constexpr (GROUP == 128) return (block[0] + block[1]) + (block[2] + block[3]);
+    float s = 0.0f;
+    for (int k = 0; k < group / 32; ++k) s += block[g * (group / 32) + k];
+    return s;
 }
 // The same in the centred form. Rarely run, so kept small rather than unrolled.
 template <int NT>
@@ -682,6 +711,7 @@ __global__ void __launch_bounds__(THREADS, 2)
         const int columns_log = second ? plan.h_columns_log : plan.x_columns_log;
         const int padded = second ? h_padded : x_padded, per_row = second ? 1 : a.top;
         const int place = second ? wn2 * sets2_item + wm2 : wn1 * sets1_item + wm1;
+        const float* sum_rows = second ? a.h_sum : a.x_sum;
         const uint16_t* rows = second ? a.hp + (tile.w ? a.h_form : 0)
                                       : a.xp + (tile.w ? a.x_form : 0);
         const int columns = tile.z << columns_log;
@@ -689,12 +719,19 @@ __global__ void __launch_bounds__(THREADS, 2)
             constexpr int NT = decltype(nt_)::value;
             // columns that do not exist repeat the first, and their sums are not used
             const uint16_t* col[NT];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const int j = nt * 8 + r, m = j >> columns_log, p = j - (m << columns_log);
+            uint32_t sum_at[NT][2];  // of columns 2 c and 2 c + 1, in their units' first block
+            auto row_of = [&](int j) {
+                const int m = j >> columns_log, p = j - (m << columns_log);
                 const bool is = m < tile.z && p < pieces;
                 const int row = member_s[tile.y + (is ? m : 0)] / per_row;
-                col[nt] = rows + (size_t(row) * pieces + (is ? p : 0)) * padded + c * 8;
+                return uint32_t(row * pieces + (is ? p : 0));
+            };
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                col[nt] = rows + size_t(row_of(nt * 8 + r)) * padded + c * 8;
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    sum_at[nt][i] = row_of(nt * 8 + 2 * c + i) * uint32_t(padded / 32);
             }
             float total[SET][NT][4];
 #pragma unroll
@@ -709,6 +746,7 @@ __global__ void __launch_bounds__(THREADS, 2)
                 const uint16_t* here[NT];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) here[nt] = col[nt] + w.unit * kQ4UnitN;
+                const float* here_sum = sum_rows + w.unit * (kQ4UnitN / 32);
                 advance(w);
                 if (tile.w) {
                     acquire();
@@ -720,9 +758,19 @@ __global__ void __launch_bounds__(THREADS, 2)
 #pragma unroll
                         for (int b = 0; b < 4; ++b)
                             x[b] = *reinterpret_cast<const uint4*>(here[0] + b * 32);
+                        __align__(16) float block[2][4];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            *reinterpret_cast<float4*>(block[i]) =
+                                *reinterpret_cast<const float4*>(here_sum + sum_at[0][i]);
                         acquire();
                         chunk_set<SET, 1, GROUP, ZEROS>(
-                            stage, plan.chunk, geom, lane, [&](int b, int) { return x[b]; }, total);
+                            stage, plan.chunk, geom, lane, [&](int b, int) { return x[b]; },
+                            [&](int g, int) {
+                                return make_float2(group_sum<GROUP>(block[0], g, GROUP),
+                                                   group_sum<GROUP>(block[1], g, GROUP));
+                            },
+                            total);
                     } else {
                         // with 16 columns, registers for two chunks at a time and no words ahead
                         constexpr int MT = NT == 1 ? SET : 2;
@@ -733,6 +781,11 @@ __global__ void __launch_bounds__(THREADS, 2)
                                 stage + m * plan.chunk, plan.chunk, geom, lane,
                                 [&](int b, int nt) {
                                     return *reinterpret_cast<const uint4*>(here[nt] + b * 32);
+                                },
+                                [&](int g, int nt) {
+                                    return make_float2(
+                                        group_sum<GROUP>(here_sum + sum_at[nt][0], g, geom.group),
+                                        group_sum<GROUP>(here_sum + sum_at[nt][1], g, geom.group));
                                 },
                                 total + m);
                     }
@@ -825,6 +878,11 @@ __global__ void __launch_bounds__(THREADS, 2)
                 }
                 const float scale = (f_at & 2) ? kQ4Scale16 : kQ4Scale;  // by place, as in x
                 for (int p = 0; p < plan.h_pieces; ++p) {
+                    float sum = piece[p];  // a warp's 32 values are one token's
+                    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                    if (lane == 0)
+                        a.h_sum[(size_t(slot) * plan.h_pieces + p) * (h_padded / 32) + f_at / 32] =
+                            sum * a.h_factor;
                     uint16_t* to = a.hp + (size_t(slot) * plan.h_pieces + p) * h_padded + f_at;
                     to[0] = uint16_t(__float_as_uint(piece[p] * scale) >> 16);
                     to[a.h_form] = uint16_t(__float_as_uint(piece[p]) >> 16);
@@ -840,6 +898,10 @@ __global__ void __launch_bounds__(THREADS, 2)
                                     line % plan.h_pieces) * h_padded +
                                    from + i % rest;
                     to[0] = to[a.h_form] = 0;
+                    if (i % rest % 32 == 0)
+                        a.h_sum[(size_t(member_s[tile.y + m]) * plan.h_pieces +
+                                 line % plan.h_pieces) * (h_padded / 32) +
+                                (from + i % rest) / 32] = 0.0f;
                 }
             }
             __syncthreads();
@@ -1052,6 +1114,8 @@ extern "C" int sgemm_moe(const sgemm_moe_layer* layer, const void* x, long long 
     const size_t at_xs = take(size_t(T) * 4), at_hs = take(size_t(slots) * 4);
     const size_t at_counters = take(size_t(counters) * 4);
     const size_t at_z = take(size_t(slots) * m.D * 4);
+    const size_t at_xsum = take(size_t(T) * plan.x_pieces * (x_padded / 32) * 4);
+    const size_t at_hsum = take(size_t(slots) * plan.h_pieces * (h_padded / 32) * 4);
     const size_t at_ids = take(ids ? 0 : side), at_weights = take(weights ? 0 : side);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     Scratch ws;
@@ -1079,6 +1143,10 @@ extern "C" int sgemm_moe(const sgemm_moe_layer* layer, const void* x, long long 
             size_t(m.D) * router_size % 16 == 0;
     a.xp = reinterpret_cast<uint16_t*>(base + at_xp);
     a.hp = reinterpret_cast<uint16_t*>(base + at_hp);
+    a.x_sum = reinterpret_cast<float*>(base + at_xsum);
+    a.h_sum = reinterpret_cast<float*>(base + at_hsum);
+    a.x_factor = g.zeros ? -1.0f : -8.0f;
+    a.h_factor = gd.zeros ? -1.0f : -8.0f;
     a.x_form = size_t(T) * plan.x_pieces * x_padded;
     a.h_form = size_t(slots) * plan.h_pieces * h_padded;
     a.x_special = reinterpret_cast<int*>(base + at_xs);

@@ -313,10 +313,12 @@ SGEMM_API int solve_row_noalloc(const float* A, const float* B, float* C, int N,
  *
  * sgemm_q4 describes one: `data` is a device buffer of sgemm_q4_bytes(w) bytes, 16-byte
  * aligned, owned by the caller and written by sgemm_q4_quantize or sgemm_q4_pack. Its
- * layout is the library's own: for every 16 columns, chunks of 128 n, each chunk its
- * codes in the order in which the lanes of a warp multiply them, then its scales and zero
- * points. Elements past N or K are held as zeros. The struct itself is read during the
- * call only.
+ * layout is the library's own: for every 128 columns, units of 128 n, each unit its codes
+ * (16 bytes for 32 n of a column), then its scales and zero points. Elements past N or K
+ * are held as zeros. The struct itself is read during the call only.
+ *
+ * Pointers of these entry points are aligned to their element type, else SGEMM_ERR_ARG; no
+ * more than that is required, except of `data`.
  *
  * 1 <= count <= 4096, 1 <= N <= 65536, 1 <= K <= 1048576, group 32, 64 or 128.
  * The common rules at the top hold here too, with these limits in place of 8192. The
@@ -383,10 +385,13 @@ SGEMM_API int sgemm_q4_dequantize(const sgemm_q4* w, float* B, void* stream);
  * and ldc >= K in elements. 0 <= M <= 65536; M = 0 enqueues nothing.
  *
  * Neither A nor the weights are rounded: A is multiplied as one, two or three bfloat16
- * pieces (bfloat16, float16, float32) whose sum it is, the weights as the integers q - z;
- * sums are FP32, the scales are applied to each group's sum in FP32, and C is rounded
- * once. The order of summation depends on the sizes alone, so results are bitwise
+ * pieces (bfloat16, float16, float32) whose sum it is, the weights as the integers q, and
+ * z times the group's sum of A is subtracted; where a row has an infinity, a NaN or a value
+ * outside [2^-64, 2^24), the rows that are staged with it are multiplied by the integers
+ * q - z instead. Sums are FP32, the scales are applied to each group's sum in FP32, and C is
+ * rounded once. The order of summation depends on the sizes alone, so results are bitwise
  * reproducible. Elements of C's rows past K are not touched. C must not overlap A or w->data.
+ * One launch, no workspace; the call can be captured into a CUDA graph.
  */
 SGEMM_API int sgemm_q4_matmul(const void* A, int dtype, long long lda, int M, const sgemm_q4* w,
                               void* C, long long ldc, void* stream);
@@ -431,9 +436,11 @@ typedef struct sgemm_moe_layer {
  * 1 <= top_k <= min(E, 16); gate and up have the same group and flags. Arithmetic as for
  * sgemm_q4_matmul; the hidden values are kept in FP32 and multiplied as two bfloat16
  * pieces (16 significant bits), three for float32 inputs (all 24). Results are bitwise
- * reproducible. Every expert that some live token picked is read once, the others not at
- * all. y, ids and weights must not overlap the inputs or each other. Workspace comes from
- * the library's pool; the call can be captured into a CUDA graph.
+ * reproducible, and a token's do not depend on the other tokens, as long as T is the same
+ * (T decides how sums are split). An expert that live tokens picked is read once for every
+ * 8 of them (4 for float32), the others not at all. y, ids and weights must not overlap the
+ * inputs or each other. Two launches; workspace comes from the library's pool; the call can
+ * be captured into a CUDA graph.
  */
 SGEMM_API int sgemm_moe(const sgemm_moe_layer* layer, const void* x, long long ldx, int T,
                         const unsigned char* live, void* y, long long ldy, int* ids,
