@@ -2,12 +2,15 @@
 // that are quantised already, and dequantisation to FP32 (definitions in sgemm.h, layout in
 // q4.cuh).
 //
-// All three are bound by memory: the dense matrix once, and the packed one. A thread of the
-// quantisation owns 32 n of two columns, in registers, which is what 16 bytes of codes hold; a
+// All three have to read the dense matrix once and write the packed one, or the reverse. A thread of
+// the quantisation owns 32 n of a column, in registers, which is what 16 bytes of codes hold; a
 // warp's loads run along the matrix' rows. Groups of 64 and 128 n meet in shared memory for their
-// extremes only. From a transposed matrix, a lane reads its columns' n itself, in whole aligned
-// 16 bytes whatever the row's alignment. Dequantisation holds 32 n of four columns a thread and
-// writes rows.
+// extremes only. From a transposed matrix, a lane reads its column's n itself, in whole aligned
+// 16 bytes whatever the row's alignment. Two columns a thread measured 71 us where one takes 62
+// (fewer warps to hide the loads). Dequantisation holds 32 n of four columns a thread and writes rows.
+//
+// Measured at 8192 x 8192, group 128: quantisation 62 us from float32 (4.9 TB/s) and 56 from bfloat16,
+// which is bound by some 20 instructions an element; dequantisation 48 us (6.2 TB/s, 93 % of a copy).
 #include "internal.cuh"
 #include "q4.cuh"
 

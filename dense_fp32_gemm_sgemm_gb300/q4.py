@@ -53,10 +53,12 @@ def _dtype_code(t, name: str) -> int:
 
 def _rows(t, name: str, cols: int) -> int:
     """The row pitch of a 2-D tensor whose rows are contiguous and do not overlap."""
-    if t.dim() != 2 or t.shape[1] != cols:
-        raise ValueError(f"{name} must be 2-D with {cols} columns, not {tuple(t.shape)}")
-    rows, pitch = t.shape[0], t.stride(0)
-    if (cols > 1 and t.stride(1) != 1) or (rows > 1 and pitch < cols):
+    shape = t.shape
+    if len(shape) != 2 or shape[1] != cols:
+        raise ValueError(f"{name} must be 2-D with {cols} columns, not {tuple(shape)}")
+    rows = shape[0]
+    pitch, step = t.stride()
+    if (cols > 1 and step != 1) or (rows > 1 and pitch < cols):
         raise ValueError(f"{name} must have contiguous rows that do not overlap "
                          f"(strides {t.stride()})")
     return pitch if rows > 1 else max(pitch, cols)
@@ -74,6 +76,11 @@ def _launch(fn, what, tensors, index, stream, *args):
     Tensors used on a stream other than the current one are marked as in use there."""
     if stream is None:
         handle = _current_handle(index)
+        if index == _current_device():
+            rc = fn(*args, handle)
+            if rc != OK:
+                raise SgemmError(rc, what)
+            return
     else:
         handle = stream.cuda_stream
         for t in tensors:
@@ -197,10 +204,10 @@ def q4_matmul(A, W: Q4Matrix, out=None, stream=None):
     code = _dtype_code(A, "A")
     lda = _rows(A, "A", W.N)
     M = A.shape[0]
-    if A.device != W.device:
+    if A.get_device() != W.index:
         raise ValueError(f"A is on {A.device}, W on {W.device}")
     if out is None:
-        out = torch.empty((M, W.K), dtype=A.dtype, device=A.device)
+        out = torch.empty((M, W.K), dtype=A.dtype, device=W.device)
         ldc = W.K
     else:
         _cuda_tensor(out, "out")
@@ -253,7 +260,7 @@ class MoeLayer:
 
     def __call__(self, x, live=None, out=None, stream=None):
         _cuda_tensor(x, "x")
-        if x.dtype != self.dtype or x.device != self.device:
+        if x.dtype is not self.dtype or x.get_device() != self.index:
             raise ValueError(f"x must be {self.dtype} on {self.device}")
         ldx = _rows(x, "x", self.D)
         T = x.shape[0]
@@ -265,15 +272,15 @@ class MoeLayer:
                     not live.is_contiguous() or live.device != self.device:
                 raise ValueError(f"live must be {T} bool or uint8 values on {self.device}")
         if out is None:
-            out = torch.empty((T, self.D), dtype=x.dtype, device=x.device)
+            out = torch.empty((T, self.D), dtype=self.dtype, device=self.device)
             ldy = self.D
         else:
             _cuda_tensor(out, "out")
             if out.dtype != x.dtype or out.shape[0] != T or out.device != x.device:
                 raise ValueError(f"out must be {T} x {self.D} of type {x.dtype} on {x.device}")
             ldy = _rows(out, "out", self.D)
-        ids = torch.empty((T, self.top_k), dtype=torch.int32, device=x.device)
-        weights = torch.empty((T, self.top_k), dtype=torch.float32, device=x.device)
+        ids = torch.empty((T, self.top_k), dtype=torch.int32, device=self.device)
+        weights = torch.empty((T, self.top_k), dtype=torch.float32, device=self.device)
         _launch(lib().sgemm_moe, "sgemm_moe",
                 (x, live, out, ids, weights, self.router, self.gate.data, self.up.data,
                  self.down.data), self.index, stream, self._ref, x.data_ptr(), ldx, T,
