@@ -76,11 +76,6 @@ def _launch(fn, what, tensors, index, stream, *args):
     Tensors used on a stream other than the current one are marked as in use there."""
     if stream is None:
         handle = _current_handle(index)
-        if index == _current_device():
-            rc = fn(*args, handle)
-            if rc != OK:
-                raise SgemmError(rc, what)
-            return
     else:
         handle = stream.cuda_stream
         for t in tensors:
@@ -114,6 +109,7 @@ class Q4Matrix:
         self.device = self.data.device
         self.index = self.device.index
         self._c.data = self.data.data_ptr()
+        self._matmul = lib().sgemm_q4_matmul
 
     @property
     def nbytes(self) -> int:
@@ -214,7 +210,14 @@ def q4_matmul(A, W: Q4Matrix, out=None, stream=None):
         if out.dtype != A.dtype or out.shape[0] != M or out.device != A.device:
             raise ValueError(f"out must be {M} x {W.K} of type {A.dtype} on {A.device}")
         ldc = _rows(out, "out", W.K)
-    _launch(lib().sgemm_q4_matmul, "sgemm_q4_matmul", (A, W.data, out), W.index, stream,
+    index = W.index
+    if stream is None and index == _current_device():  # the usual call, without a detour
+        rc = W._matmul(A.data_ptr(), code, lda, M, W._ref, out.data_ptr(), ldc,
+                       _current_handle(index))
+        if rc != OK:
+            raise SgemmError(rc, "sgemm_q4_matmul")
+        return out
+    _launch(W._matmul, "sgemm_q4_matmul", (A, W.data, out), index, stream,
             A.data_ptr(), code, lda, M, W._ref, out.data_ptr(), ldc)
     return out
 
@@ -257,6 +260,7 @@ class MoeLayer:
         self._c = _Moe(router.data_ptr(), _dtype_code(router, "router"), _DTYPES[self.dtype], D, F,
                        E, self.top_k, int(self.renormalize), gate._c, up._c, down._c)
         self._ref = ctypes.byref(self._c)
+        self._fn = lib().sgemm_moe
 
     def __call__(self, x, live=None, out=None, stream=None):
         _cuda_tensor(x, "x")
@@ -281,9 +285,15 @@ class MoeLayer:
             ldy = _rows(out, "out", self.D)
         ids = torch.empty((T, self.top_k), dtype=torch.int32, device=self.device)
         weights = torch.empty((T, self.top_k), dtype=torch.float32, device=self.device)
-        _launch(lib().sgemm_moe, "sgemm_moe",
-                (x, live, out, ids, weights, self.router, self.gate.data, self.up.data,
-                 self.down.data), self.index, stream, self._ref, x.data_ptr(), ldx, T,
-                None if live is None else live.data_ptr(), out.data_ptr(), ldy, ids.data_ptr(),
-                weights.data_ptr())
+        args = (self._ref, x.data_ptr(), ldx, T, None if live is None else live.data_ptr(),
+                out.data_ptr(), ldy, ids.data_ptr(), weights.data_ptr())
+        index = self.index
+        if stream is None and index == _current_device():
+            rc = self._fn(*args, _current_handle(index))
+            if rc != OK:
+                raise SgemmError(rc, "sgemm_moe")
+        else:
+            _launch(self._fn, "sgemm_moe",
+                    (x, live, out, ids, weights, self.router, self.gate.data, self.up.data,
+                     self.down.data), index, stream, *args)
         return out, ids, weights
