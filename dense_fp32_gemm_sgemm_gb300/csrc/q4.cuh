@@ -3,8 +3,9 @@
 //
 // With M of a few rows the bytes of B are the cost (2 M operations for half a byte), so the
 // format is built for few instructions a weight. The products run on the tensor core with B^T
-// as the 128-row operand, held in tensor memory: a thread owns one column of B (a row of
-// B^T), turns its codes into operand words in registers and stores them to its lane.
+// as the operand of many rows: 16 in a warp's registers for few columns (q4_warp.cuh), 128 in
+// tensor memory for more (q4_tensor.cu), where a thread owns one column of B (a row of B^T),
+// turns its codes into operand words and stores them to its lane.
 //
 // Operand words cost 5 instructions for 8 weights. The bfloat16 with the bit pattern of an
 // integer I in 0 .. 255 is I * 2^-133 exactly: its subnormals and its first binade lie on one
@@ -204,7 +205,7 @@ struct Magnitudes {
 };
 
 // The P pieces of 8 values (uint4: places 0 .. 7), for the plain form: times 2^96 and, at places
-// 2, 3, 6 and 7 (which meet 16 q), 2^92; and their sums, unscaled. Not for values that the plain
+// 2, 3, 6 and 7 (which meet 16 q), 2^92; and their sums, unscaled, added to `sum`. Not for values that the plain
 // form cannot take; those show in `magnitudes`.
 template <int P, class T>
 __device__ __forceinline__ void split_plain(const Raw8<T>& raw, Magnitudes& magnitudes,
