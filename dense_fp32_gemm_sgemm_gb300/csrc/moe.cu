@@ -54,6 +54,10 @@ constexpr int DEPTH = 2;        // stages of a warp's ring, a set of chunks each
 constexpr int SUM_COLUMNS = 32, SUM_TOKENS = 16;  // of a sum item
 constexpr int WARPS = 8, THREADS = WARPS * 32;
 constexpr int SMEM_LIMIT = 227 * 1024;
+constexpr int TILE = 8;  // the most tokens of a tile, and columns whose sums are exchanged
+constexpr int PITCH = TILE * 17;  // floats of a chunk's sums
+// Pieces of a hidden value, whatever the layer's type: all 24 significant bits.
+constexpr int H_PIECES = 3;
 
 struct MoeArgs {
     const void* x;
@@ -92,9 +96,7 @@ struct Stack {
 // How the expert kernel cuts its work.
 struct MoePlan {
     int capacity;                 // tokens of a tile
-    int x_pieces, x_columns_log;  // pieces of a token of x, and the columns that they take
-    int h_pieces, h_columns_log;  // and of a hidden row
-    int max_columns;              // of a tile
+    int x_pieces;                 // of a token of x
     int wn1, wn2;                 // warps that split n in first and second items
     int step1, step2;             // bytes from a warp's unit to its next
     ptrdiff_t gate_to_up;
@@ -280,19 +282,18 @@ __global__ void __launch_bounds__(ROUTE_THREADS) moe_route_kernel(const MoeArgs 
 struct MoeOffsets {
     int tiles;    // int4 each: expert, first member, members, whether the centred form is wanted
     int members;  // token and slot, by expert
-    int sums;     // [wn][set][chunk][column][17]
+    int sums;     // [wn][set][chunk][column, TILE of them][17]
     int masks;    // in the same place before: [expert][form][2], and [expert]
     int ring;
     int end;
 };
-__host__ __device__ constexpr MoeOffsets moe_offsets(int max_columns, int chunk, int tiles, int slots,
-                                                     int E) {
+__host__ __device__ constexpr MoeOffsets moe_offsets(int chunk, int tiles, int slots, int E) {
     MoeOffsets o{};
     o.tiles = 0;
     o.members = tiles * 16;
     o.sums = (o.members + slots * 2 + 15) / 16 * 16;
     o.masks = o.sums;
-    int most = WARPS * SET * max_columns * 17 * 4;
+    int most = WARPS * SET * PITCH * 4;
     if (most < E * 20) most = E * 20;
     o.ring = o.sums + (most + 15) / 16 * 16;
     o.end = o.ring + WARPS * DEPTH * SET * chunk;
@@ -322,11 +323,12 @@ __host__ __device__ constexpr int most_tiles(int E, int slots, int capacity) {
 
 // MT chunks (at stage, stage + chunk, ...) times NT tiles of 8 columns, added to total as in
 // q4_chunk. x(b, nt): the lane's 8 values of block b of column 8 nt + r, staged for the plain form;
-// sum(g, nt): the kept sums over group g of columns 8 nt + 2 c and + 1.
+// sum(g, nt): the kept sums over group g of columns 8 nt + 2 c and + 1. JOIN: joined(b) is multiplied
+// too, into the sums of the last tile of columns.
 // GROUP 0: the stack's own group size and zero points.
-template <int MT, int NT, int GROUP, bool ZEROS, class X, class Sum>
+template <int MT, int NT, bool JOIN, int GROUP, bool ZEROS, class X, class Joined, class Sum>
 __device__ __forceinline__ void chunk_set(const uint8_t* stage, int chunk, const Q4Geom& geom, int lane,
-                                          X&& x, Sum&& sum, float (*total)[NT][4]) {
+                                          X&& x, Joined&& joined, Sum&& sum, float (*total)[NT][4]) {
     const int r = lane >> 2;
     const int blocks = GROUP ? GROUP / 32 : geom.group / 32;
     const int groups = GROUP ? kQ4UnitN / (GROUP ? GROUP : 32) : kQ4UnitN / geom.group;
@@ -339,6 +341,8 @@ __device__ __forceinline__ void chunk_set(const uint8_t* stage, int chunk, const
             uint4 v[NT];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) v[nt] = x(b, nt);
+            uint4 more;
+            if constexpr (JOIN) more = joined(b);
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
                 const uint32_t* codes =
@@ -355,6 +359,10 @@ __device__ __forceinline__ void chunk_set(const uint8_t* stage, int chunk, const
                     else
                         mma_bf16(acc[m][nt], a0, v[nt].x, v[nt].y);
                     mma_bf16(acc[m][nt], a1, v[nt].z, v[nt].w);
+                }
+                if constexpr (JOIN) {
+                    mma_bf16(acc[m][NT - 1], a0, more.x, more.y);
+                    mma_bf16(acc[m][NT - 1], a1, more.z, more.w);
                 }
             }
         };
@@ -402,10 +410,10 @@ __device__ __forceinline__ float group_sum(const float* block, int g, int group)
     return s;
 }
 // The same in the centred form. Rarely run, so kept small rather than unrolled.
-template <int NT>
+template <int NT, bool JOIN>
 __device__ __forceinline__ void chunk_set_centred(const uint8_t* stage, int chunk, const Q4Geom& geom,
-                                                  int lane, const uint16_t* const (&col)[NT],
-                                                  float (&total)[SET][NT][4]) {
+                                                  int lane, const uint16_t* col, int padded,
+                                                  const uint16_t* joined, float (&total)[SET][NT][4]) {
     const int r = lane >> 2;
     const int blocks = geom.group / 32, groups = kQ4UnitN / geom.group;
 #pragma unroll
@@ -425,7 +433,7 @@ __device__ __forceinline__ void chunk_set_centred(const uint8_t* stage, int chun
                 }
                 const uint32_t* codes =
                     reinterpret_cast<const uint32_t*>(stage + m * chunk + b * 256) + lane;
-                const uint4 x = *reinterpret_cast<const uint4*>(col[nt] + b * 32);
+                const uint4 x = *reinterpret_cast<const uint4*>(col + nt * padded + b * 32);
                 uint32_t lo[4], hi[4];
                 q4_centred(codes[0], 0x43004300u | z0 * 0x00010001u, lo);
                 q4_centred(codes[32], 0x43004300u | z1 * 0x00010001u, hi);
@@ -433,6 +441,12 @@ __device__ __forceinline__ void chunk_set_centred(const uint8_t* stage, int chun
                 const uint32_t a1[4] = {lo[2], hi[2], lo[3], hi[3]};
                 mma_bf16(acc, a0, x.x, x.y);
                 mma_bf16(acc, a1, x.z, x.w);
+                if (JOIN && nt == NT - 1) {
+                    uint4 more = make_uint4(0, 0, 0, 0);
+                    if (joined) more = *reinterpret_cast<const uint4*>(joined + b * 32);
+                    mma_bf16(acc, a0, more.x, more.y);
+                    mma_bf16(acc, a1, more.z, more.w);
+                }
                 if (--left > 0) continue;
                 left = blocks;
                 const uint16_t* scales = reinterpret_cast<const uint16_t*>(side) + g * kQ4StripK + r;
@@ -447,6 +461,15 @@ __device__ __forceinline__ void chunk_set_centred(const uint8_t* stage, int chun
             }
         }
 }
+
+// The columns of A^T of a tile of tokens. Where tiles are of one or two tokens, a piece has a column
+// of its own (NT_MOST 1). With larger ones a token has two columns at most, and a third piece is
+// multiplied into the sums of the second: with a column of its own it would take eight tokens to 24
+// columns and more registers than there are (64 tokens: 430 us instead of 410). One tile of columns
+// holds all of them (column `columns` * m + p) where they fit; else there are two, and column m of
+// each is token m's: a thread then adds its tokens' sums before they are exchanged. So the order of
+// a token's sums does not depend on how many share the tile.
+__device__ __forceinline__ bool packed_columns(int tokens, int columns) { return tokens * columns <= TILE; }
 
 // NT_MOST: tiles of 8 columns that a tile of tokens may take.
 template <int NT_MOST, int GROUP, bool ZEROS>
@@ -463,7 +486,7 @@ __global__ void __launch_bounds__(THREADS, 2)
     const int slots = a.T * a.top;
     const int max_tiles = most_tiles(a.E, slots, plan.capacity);
     const MoeOffsets at =
-        moe_offsets(plan.max_columns, plan.chunk, max_tiles, slots, a.E);
+        moe_offsets(plan.chunk, max_tiles, slots, a.E);
     int4* tile_s = reinterpret_cast<int4*>(smem + at.tiles);
     uint16_t* member_s = reinterpret_cast<uint16_t*>(smem + at.members);
     float* sums = reinterpret_cast<float*>(smem + at.sums);
@@ -560,6 +583,7 @@ __global__ void __launch_bounds__(THREADS, 2)
         }
         __syncthreads();
     }
+    auto columns_of = [&](int pieces) { return NT_MOST == 1 ? pieces : min(pieces, 2); };
     const int tiles = tiles_s;
     const int first_items = tiles * groups1, second_items = tiles * groups2;
     const int items = first_items + second_items +
@@ -703,36 +727,36 @@ __global__ void __launch_bounds__(THREADS, 2)
     // Multiplies the warp's set of an item with the columns of its tile of tokens and puts the sums
     // to [wn][set][chunk][column][17]. One copy of this code serves both kinds of items: it is most
     // of the kernel, and where there are few items its instructions come from far.
-    const int pitch = plan.max_columns * 17;
     auto product = [&](const int4& tile, Walk& w) {
         const bool second = w.kind != 0;
         const Q4Geom& geom = second ? down.geom : gate.geom;
-        const int pieces = second ? plan.h_pieces : plan.x_pieces;
-        const int columns_log = second ? plan.h_columns_log : plan.x_columns_log;
+        const int pieces = second ? H_PIECES : plan.x_pieces;
+        const int token_columns = columns_of(pieces);
+        const bool packed = packed_columns(tile.z, token_columns);
         const int padded = second ? h_padded : x_padded, per_row = second ? 1 : a.top;
         const int place = second ? wn2 * sets2_item + wm2 : wn1 * sets1_item + wm1;
         const float* sum_rows = second ? a.h_sum : a.x_sum;
         const uint16_t* rows = second ? a.hp + (tile.w ? a.h_form : 0)
                                       : a.xp + (tile.w ? a.x_form : 0);
-        const int columns = tile.z << columns_log;
-        auto run = [&](auto nt_) {
+        auto run = [&](auto nt_, auto join_) {
             constexpr int NT = decltype(nt_)::value;
+            constexpr bool JOIN = decltype(join_)::value;
             // columns that do not exist repeat the first, and their sums are not used
-            const uint16_t* col[NT];
-            uint32_t sum_at[NT][2];  // of columns 2 c and 2 c + 1, in their units' first block
             auto row_of = [&](int j) {
-                const int m = j >> columns_log, p = j - (m << columns_log);
-                const bool is = m < tile.z && p < pieces;
+                const int apart = NT == 1 ? token_columns : 1;
+                const int m = apart == 1 ? j : apart == 2 ? j >> 1 : j * 11 >> 5, p = j - m * apart;
+                const bool is = m < tile.z;
                 const int row = member_s[tile.y + (is ? m : 0)] / per_row;
                 return uint32_t(row * pieces + (is ? p : 0));
             };
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                col[nt] = rows + size_t(row_of(nt * 8 + r)) * padded + c * 8;
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    sum_at[nt][i] = row_of(nt * 8 + 2 * c + i) * uint32_t(padded / 32);
-            }
+            // of the first tile of columns; the next piece's are `padded` further. The third
+            // piece of first columns is nothing.
+            const uint16_t* const col = rows + size_t(row_of(r)) * padded + c * 8;
+            const bool joins = NT == 2 || (r & 1);
+            const int join_at = NT * padded;
+            // of columns 2 c and 2 c + 1, in their units' first block
+            const uint32_t sum_at[2] = {row_of(2 * c) * uint32_t(padded / 32),
+                                        row_of(2 * c + 1) * uint32_t(padded / 32)};
             float total[SET][NT][4];
 #pragma unroll
             for (int m = 0; m < SET; ++m)
@@ -743,73 +767,109 @@ __global__ void __launch_bounds__(THREADS, 2)
 #pragma unroll 1
             while (w.left > 0) {
                 if (warp == 0 && w.left <= claim_at) claim_step();
-                const uint16_t* here[NT];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) here[nt] = col[nt] + w.unit * kQ4UnitN;
+                const uint16_t* here = col + w.unit * kQ4UnitN;
                 const float* here_sum = sum_rows + w.unit * (kQ4UnitN / 32);
+                auto third = [&](int b) {
+                    uint4 v = make_uint4(0, 0, 0, 0);
+                    if (joins) v = *reinterpret_cast<const uint4*>(here + join_at + b * 32);
+                    return v;
+                };
                 advance(w);
                 if (tile.w) {
                     acquire();
-                    chunk_set_centred<NT>(stage, plan.chunk, geom, lane, here, total);
+                    chunk_set_centred<NT, JOIN>(stage, plan.chunk, geom, lane, here, padded,
+                                                joins ? here + join_at : nullptr, total);
                 } else {
-                    if constexpr (NT == 1 && GROUP != 0) {
+                    if constexpr (NT == 1 && GROUP != 0 && !JOIN) {
                         // all four blocks' words at once, while the stage is waited for
                         uint4 x[4];
 #pragma unroll
                         for (int b = 0; b < 4; ++b)
-                            x[b] = *reinterpret_cast<const uint4*>(here[0] + b * 32);
+                            x[b] = *reinterpret_cast<const uint4*>(here + b * 32);
                         __align__(16) float block[2][4];
 #pragma unroll
                         for (int i = 0; i < 2; ++i)
                             *reinterpret_cast<float4*>(block[i]) =
-                                *reinterpret_cast<const float4*>(here_sum + sum_at[0][i]);
+                                *reinterpret_cast<const float4*>(here_sum + sum_at[i]);
                         acquire();
-                        chunk_set<SET, 1, GROUP, ZEROS>(
-                            stage, plan.chunk, geom, lane, [&](int b, int) { return x[b]; },
+                        chunk_set<SET, 1, false, GROUP, ZEROS>(
+                            stage, plan.chunk, geom, lane, [&](int b, int) { return x[b]; }, third,
                             [&](int g, int) {
                                 return make_float2(group_sum<GROUP>(block[0], g, GROUP),
                                                    group_sum<GROUP>(block[1], g, GROUP));
                             },
                             total);
                     } else {
-                        // with 16 columns, registers for two chunks at a time and no words ahead
+                        // no registers for words ahead, and with more columns for two chunks at a time
                         constexpr int MT = NT == 1 ? SET : 2;
                         acquire();
 #pragma unroll
                         for (int m = 0; m < SET; m += MT)
-                            chunk_set<MT, NT, GROUP, ZEROS>(
+                            chunk_set<MT, NT, JOIN, GROUP, ZEROS>(
                                 stage + m * plan.chunk, plan.chunk, geom, lane,
                                 [&](int b, int nt) {
-                                    return *reinterpret_cast<const uint4*>(here[nt] + b * 32);
+                                    return *reinterpret_cast<const uint4*>(here + nt * padded + b * 32);
                                 },
+                                third,
                                 [&](int g, int nt) {
-                                    return make_float2(
-                                        group_sum<GROUP>(here_sum + sum_at[nt][0], g, geom.group),
-                                        group_sum<GROUP>(here_sum + sum_at[nt][1], g, geom.group));
+                                    const float* block = here_sum + nt * (padded / 32);
+                                    float2 s = make_float2(
+                                        group_sum<GROUP>(block + sum_at[0], g, geom.group),
+                                        group_sum<GROUP>(block + sum_at[1], g, geom.group));
+                                    if (JOIN && nt == NT - 1) {
+                                        block += padded / 32;
+                                        if (NT == 2)
+                                            s.x += group_sum<GROUP>(block + sum_at[0], g, geom.group);
+                                        s.y += group_sum<GROUP>(block + sum_at[1], g, geom.group);
+                                    }
+                                    return s;
                                 },
                                 total + m);
                     }
                 }
                 release();
             }
-            float* mine = sums + place * SET * pitch + r;
+            float* mine = sums + place * SET * PITCH + r;
+            const int columns = NT == 1 ? tile.z * token_columns : tile.z;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int i = 0; i < 2; ++i) {
+                const int j = 2 * c + i;
+                if (j < columns)
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int j = nt * 8 + 2 * c + i;
-                    if (j < columns)
+                    for (int m = 0; m < SET; ++m) {
+                        float v = total[m][0][i], v8 = total[m][0][i + 2];
 #pragma unroll
-                        for (int m = 0; m < SET; ++m) {
-                            mine[m * pitch + j * 17] = total[m][nt][i];
-                            mine[m * pitch + j * 17 + 8] = total[m][nt][i + 2];
+                        for (int nt = 1; nt < NT; ++nt) {
+                            v += total[m][nt][i];
+                            v8 += total[m][nt][i + 2];
                         }
-                }
+                        mine[m * PITCH + j * 17] = v;
+                        mine[m * PITCH + j * 17 + 8] = v8;
+                    }
+            }
         };
-        if (NT_MOST == 1 || columns <= 8)
-            run(std::integral_constant<int, 1>());
-        else
-            run(std::integral_constant<int, NT_MOST>());
+        constexpr std::integral_constant<int, 1> one{};
+        constexpr std::integral_constant<int, 2> two{};
+        if constexpr (NT_MOST == 1) {
+            run(one, std::false_type());
+        } else if (pieces == 3) {
+            if (packed)
+                run(one, std::true_type());
+            else
+                run(two, std::true_type());
+        } else {
+            if (packed)
+                run(one, std::false_type());
+            else
+                run(two, std::false_type());
+        }
+    };
+    // A token's sum from one warp of those that split n: its pieces' that are there.
+    auto sum_of = [&](const float* from, int apart) {
+        float v = from[0];
+        if (apart > 1) v += from[17];
+        if (apart > 2) v += from[34];
+        return v;
     };
 
     // ---- the items
@@ -849,27 +909,24 @@ __global__ void __launch_bounds__(THREADS, 2)
         }
         if (item < first_items) {
             const int width = sets1_item * 32, f0 = (item - w.tile * groups1) * width;
+            const int token_columns = columns_of(plan.x_pieces);
+            const int apart = packed_columns(tile.z, token_columns) ? token_columns : 1;
             for (int i = tid; i < tile.z * width; i += threads) {
                 const int m = i / width, k = i - m * width;
                 const int f_at = f0 + k;
                 if (f_at >= plan.sets1 * 32) continue;
                 float g = 0.0f, u = 0.0f;
-                for (int p = 0; p < plan.x_pieces; ++p) {
-                    const float* from = sums + (k / kQ4StripK) * 2 * pitch +  // two of a set
-                                        ((m << plan.x_columns_log) + p) * 17 + k % kQ4StripK;
+                const float* from = sums + (k / kQ4StripK) * 2 * PITCH +  // two of a set
+                                    m * apart * 17 + k % kQ4StripK;
 #pragma unroll 4
-                    for (int q = 0; q < plan.wn1; ++q) {
-                        g += from[q * sets1_item * SET * pitch];
-                        u += from[q * sets1_item * SET * pitch + pitch];
-                    }
+                for (int q = 0; q < plan.wn1; ++q) {
+                    g += sum_of(from + q * sets1_item * SET * PITCH, apart);
+                    u += sum_of(from + q * sets1_item * SET * PITCH + PITCH, apart);
                 }
                 const int slot = member_s[tile.y + m];
                 const float h = f_at < a.F ? g / (1.0f + expf(-g)) * u * a.weights[slot] : 0.0f;
-                float piece[3];
-                split_pieces<3>(h, piece);
-                if (plan.h_pieces == 2 && fabsf(h) < 1e38f)
-                    // the second piece rounded to nearest: 2^-16 of the value at most
-                    piece[1] = __bfloat162float(__float2bfloat16_rn(h - piece[0]));
+                float piece[H_PIECES];
+                split_pieces<H_PIECES>(h, piece);
                 Magnitudes magnitude;
                 magnitude.add(__float_as_uint(h));
                 if (magnitude.special<float>()) {
@@ -877,13 +934,14 @@ __global__ void __launch_bounds__(THREADS, 2)
                     a.counters[2] = 1;
                 }
                 const float scale = (f_at & 2) ? kQ4Scale16 : kQ4Scale;  // by place, as in x
-                for (int p = 0; p < plan.h_pieces; ++p) {
+#pragma unroll
+                for (int p = 0; p < H_PIECES; ++p) {
                     float sum = piece[p];  // a warp's 32 values are one token's
                     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
                     if (lane == 0)
-                        a.h_sum[(size_t(slot) * plan.h_pieces + p) * (h_padded / 32) + f_at / 32] =
+                        a.h_sum[(size_t(slot) * H_PIECES + p) * (h_padded / 32) + f_at / 32] =
                             sum * a.h_factor;
-                    uint16_t* to = a.hp + (size_t(slot) * plan.h_pieces + p) * h_padded + f_at;
+                    uint16_t* to = a.hp + (size_t(slot) * H_PIECES + p) * h_padded + f_at;
                     to[0] = uint16_t(__float_as_uint(piece[p] * scale) >> 16);
                     to[a.h_form] = uint16_t(__float_as_uint(piece[p]) >> 16);
                 }
@@ -891,17 +949,12 @@ __global__ void __launch_bounds__(THREADS, 2)
             // past F: down's weights are zero there, but not whatever the scratch holds
             if (f0 + width >= plan.sets1 * 32) {
                 const int from = plan.sets1 * 32, rest = h_padded - from;
-                for (int i = tid; i < tile.z * plan.h_pieces * rest; i += threads) {
-                    const int line = i / rest, m = line / plan.h_pieces;
-                    uint16_t* to = a.hp +
-                                   (size_t(member_s[tile.y + m]) * plan.h_pieces +
-                                    line % plan.h_pieces) * h_padded +
-                                   from + i % rest;
+                for (int i = tid; i < tile.z * H_PIECES * rest; i += threads) {
+                    const int line = i / rest, m = line / H_PIECES;
+                    const size_t row = size_t(member_s[tile.y + m]) * H_PIECES + line % H_PIECES;
+                    uint16_t* to = a.hp + row * h_padded + from + i % rest;
                     to[0] = to[a.h_form] = 0;
-                    if (i % rest % 32 == 0)
-                        a.h_sum[(size_t(member_s[tile.y + m]) * plan.h_pieces +
-                                 line % plan.h_pieces) * (h_padded / 32) +
-                                (from + i % rest) / 32] = 0.0f;
+                    if (i % rest % 32 == 0) a.h_sum[row * (h_padded / 32) + (from + i % rest) / 32] = 0.0f;
                 }
             }
             __syncthreads();
@@ -909,16 +962,15 @@ __global__ void __launch_bounds__(THREADS, 2)
         } else if (item < first_items + second_items) {
             const int group = item - first_items - w.tile * groups2;
             const int width = sets2_item * 64;
+            const int token_columns = columns_of(H_PIECES);
+            const int apart = packed_columns(tile.z, token_columns) ? token_columns : 1;
             for (int i = tid; i < tile.z * width; i += threads) {
                 const int m = i / width, k = i - m * width, d = group * width + k;
                 if (d >= a.D) continue;
                 float v = 0.0f;
-                for (int p = 0; p < plan.h_pieces; ++p) {
-                    const float* from = sums + (k / kQ4StripK) * pitch +
-                                        ((m << plan.h_columns_log) + p) * 17 + k % kQ4StripK;
+                const float* from = sums + (k / kQ4StripK) * PITCH + m * apart * 17 + k % kQ4StripK;
 #pragma unroll 4
-                    for (int q = 0; q < plan.wn2; ++q) v += from[q * sets2_item * SET * pitch];
-                }
+                for (int q = 0; q < plan.wn2; ++q) v += sum_of(from + q * sets2_item * SET * PITCH, apart);
                 a.z[size_t(member_s[tile.y + m]) * a.D + d] = v;
             }
             __syncthreads();
@@ -1015,22 +1067,20 @@ int choose_split(double tiles, int sets, int units, int ctas) {
     return best;
 }
 
+// Whether tiles are of two tokens at most, all of whose pieces have columns of their own. Larger
+// ones save reading an expert's weights again, from L2, but take two matrix instructions or three
+// where these take one. 8 of 64 experts of 4096 x 2048, bfloat16: 3, 8, 16, 24 and 32 tokens take 87,
+// 141, 218, 264 and 344 us with small tiles, 110, 183, 232, 273 and 292 with large ones.
+bool small_tiles(const sgemm_moe_layer& m, int T) { return T <= 2 || T * m.top_k <= 3 * m.E; }
+
 MoePlan make_plan(const sgemm_moe_layer& m, const Q4Geom& g, const Q4Geom& gd, int T, int sm_count) {
     MoePlan p;
     const int slots = T * m.top_k;
     p.x_pieces = pieces_of(m.dtype);
-    p.x_columns_log = m.dtype == SGEMM_FLOAT32 ? 2 : p.x_pieces - 1;
-    // the hidden values: all 24 significant bits for float32, 16 for the 16-bit types
-    p.h_pieces = m.dtype == SGEMM_FLOAT32 ? 3 : 2;
-    p.h_columns_log = m.dtype == SGEMM_FLOAT32 ? 2 : 1;
-    // 16 columns at most: with 32, the matrix instructions take twice as long as reading the
-    // weights again from L2 for a second tile
-    p.capacity = 16 >> p.h_columns_log;
-    if (p.capacity > T) p.capacity = T;
-    p.max_columns = p.capacity << (p.x_columns_log > p.h_columns_log ? p.x_columns_log : p.h_columns_log);
+    p.capacity = small_tiles(m, T) ? (T < 2 ? T : 2) : TILE;
     const int chunk1 = q4_chunk_bytes(g.group, g.zeros), chunk2 = q4_chunk_bytes(gd.group, gd.zeros);
     p.chunk = chunk1 > chunk2 ? chunk1 : chunk2;
-    p.smem = moe_offsets(p.max_columns, p.chunk, most_tiles(m.E, slots, p.capacity), slots, m.E).end;
+    p.smem = moe_offsets(p.chunk, most_tiles(m.E, slots, p.capacity), slots, m.E).end;
     p.sets1 = (m.F + 31) / 32;
     p.sets2 = (m.D + 63) / 64;
     // tiles, about, if tokens picked experts at random
@@ -1110,12 +1160,12 @@ extern "C" int sgemm_moe(const sgemm_moe_layer* layer, const void* x, long long 
         return at;
     };
     const size_t at_xp = take(size_t(T) * plan.x_pieces * x_padded * 4);
-    const size_t at_hp = take(size_t(slots) * plan.h_pieces * h_padded * 4);
+    const size_t at_hp = take(size_t(slots) * H_PIECES * h_padded * 4);
     const size_t at_xs = take(size_t(T) * 4), at_hs = take(size_t(slots) * 4);
     const size_t at_counters = take(size_t(counters) * 4);
     const size_t at_z = take(size_t(slots) * m.D * 4);
     const size_t at_xsum = take(size_t(T) * plan.x_pieces * (x_padded / 32) * 4);
-    const size_t at_hsum = take(size_t(slots) * plan.h_pieces * (h_padded / 32) * 4);
+    const size_t at_hsum = take(size_t(slots) * H_PIECES * (h_padded / 32) * 4);
     const size_t at_ids = take(ids ? 0 : side), at_weights = take(weights ? 0 : side);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     Scratch ws;
@@ -1148,7 +1198,7 @@ extern "C" int sgemm_moe(const sgemm_moe_layer* layer, const void* x, long long 
     a.x_factor = g.zeros ? -1.0f : -8.0f;
     a.h_factor = gd.zeros ? -1.0f : -8.0f;
     a.x_form = size_t(T) * plan.x_pieces * x_padded;
-    a.h_form = size_t(slots) * plan.h_pieces * h_padded;
+    a.h_form = size_t(slots) * H_PIECES * h_padded;
     a.x_special = reinterpret_cast<int*>(base + at_xs);
     a.h_special = reinterpret_cast<int*>(base + at_hs);
     a.counters = reinterpret_cast<int*>(base + at_counters);
@@ -1179,7 +1229,7 @@ extern "C" int sgemm_moe(const sgemm_moe_layer* layer, const void* x, long long 
     config.numAttrs = 1;
     const Stack gate{static_cast<const uint8_t*>(m.gate.data), g};
     const Stack down{static_cast<const uint8_t*>(m.down.data), gd};
-    if (plan.max_columns <= 8)
+    if (small_tiles(m, T))
         err = launch_experts<1>(config, a, gate, down, plan);
     else
         err = launch_experts<2>(config, a, gate, down, plan);

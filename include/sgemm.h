@@ -434,11 +434,10 @@ typedef struct sgemm_moe_layer {
  *
  * 0 <= T <= 64 (T = 0 enqueues nothing), 1 <= D, F <= 16384, 1 <= E <= 256,
  * 1 <= top_k <= min(E, 16); gate and up have the same group and flags. Arithmetic as for
- * sgemm_q4_matmul; the hidden values are kept in FP32 and multiplied as two bfloat16
- * pieces (16 significant bits), three for float32 inputs (all 24). Results are bitwise
- * reproducible, and a token's do not depend on the other tokens, as long as T is the same
+ * sgemm_q4_matmul; the hidden values are kept in FP32 and multiplied as three bfloat16
+ * pieces (all 24 significant bits), whatever the type. Results are bitwise reproducible, and a token's do not depend on the other tokens, as long as T is the same
  * (T decides how sums are split). An expert that live tokens picked is read once for every
- * 8 of them (4 for float32), the others not at all. y, ids and weights must not overlap the
+ * 8 of them (for every 2 where T * top_k <= 3 E), the others not at all. y, ids and weights must not overlap the
  * inputs or each other. Two launches; workspace comes from the library's pool; the call can
  * be captured into a CUDA graph.
  */
