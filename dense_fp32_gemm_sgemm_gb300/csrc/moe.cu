@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(ROUTE_THREADS) moe_route_kernel(const MoeArgs 
 
 // Where the expert kernel's shared memory holds what, in bytes.
 struct MoeOffsets {
-    int tiles;    // int4 each: expert, first member, members, whether the centred form is wanted
+    int tiles;    // int4 each: expert, first member, members, which of them want the centred form
     int members;  // token and slot, by expert
     int sums;     // [wn][set][chunk][column, TILE of them][17]
     int masks;    // in the same place before: [expert][form][2], and [expert]
@@ -409,57 +409,90 @@ __device__ __forceinline__ float group_sum(const float* block, int g, int group)
     for (int k = 0; k < group / 32; ++k) s += block[g * (group / 32) + k];
     return s;
 }
-// The same in the centred form. Rarely run, so kept small rather than unrolled.
-template <int NT, bool JOIN>
-__device__ __forceinline__ void chunk_set_centred(const uint8_t* stage, int chunk, const Q4Geom& geom,
-                                                  int lane, const uint16_t* col, int padded,
-                                                  const uint16_t* joined, float (&total)[SET][NT][4]) {
-    const int r = lane >> 2;
-    const int blocks = geom.group / 32, groups = kQ4UnitN / geom.group;
-#pragma unroll
-    for (int m = 0; m < SET; ++m)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const uint8_t* side = stage + m * chunk + kQ4ChunkCodes;
-            float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            int left = blocks, g = 0;
+// What a product reads of a unit of its tile's columns, NT tiles of 8 of them.
+struct Columns {
+    const uint16_t* x;     // the lane's column of the first tile, staged for the plain form
+    const uint16_t* more;  // joined to the sums of the last tile's column, or null
+    int padded;            // from a tile's columns to the next one's, and from row to row
+    size_t form;           // to the same as they are, for the centred form
+    const float* sums;     // of 32 values each; those of columns 2 c and 2 c + 1 of the first tile:
+    uint32_t sum_at[2];
+    template <int NT, bool JOIN, int GROUP>
+    __device__ __forceinline__ float2 group_sums(int g, int nt, int group) const {
+        const float* block = sums + nt * (padded / 32);
+        float2 s = make_float2(group_sum<GROUP>(block + sum_at[0], g, group),
+                               group_sum<GROUP>(block + sum_at[1], g, group));
+        if (JOIN && nt == NT - 1) {
+            block += padded / 32;
+            if (NT == 2) s.x += group_sum<GROUP>(block + sum_at[0], g, group);
+            s.y += group_sum<GROUP>(block + sum_at[1], g, group);
+        }
+        return s;
+    }
+};
+
+// chunk_set of SET chunks where some columns want the centred form: both forms are multiplied, and
+// each column keeps the sums of its own, which are those that it has in a tile of one form. So a
+// token's bits do not depend on the others of its tile. special: of columns 2 c and 2 c + 1 (bits 0
+// and 1). Rarely run, so kept small and out of the way: totals in local memory, no loop unrolled.
+template <int NT, bool JOIN, int GROUP>
+__device__ __noinline__ void chunk_set_mixed(const uint8_t* stage, int chunk, int group, int zeros, int fp16,
+                                             const Columns col, int special, float* total) {
+    const int lane = threadIdx.x & 31, r = lane >> 2;
+    const int blocks = group / 32, groups = kQ4UnitN / group;
+    auto load = [](const uint16_t* p) { return *reinterpret_cast<const uint4*>(p); };
 #pragma unroll 1
-            for (int b = 0; b < 4; ++b) {
-                uint32_t z0 = 8, z1 = 8;
-                if (geom.zeros) {
-                    const uint8_t* z = side + groups * kQ4StripK * 2 + g * kQ4StripK + r;
-                    z0 = z[0];
-                    z1 = z[8];
-                }
-                const uint32_t* codes =
-                    reinterpret_cast<const uint32_t*>(stage + m * chunk + b * 256) + lane;
-                const uint4 x = *reinterpret_cast<const uint4*>(col + nt * padded + b * 32);
-                uint32_t lo[4], hi[4];
-                q4_centred(codes[0], 0x43004300u | z0 * 0x00010001u, lo);
-                q4_centred(codes[32], 0x43004300u | z1 * 0x00010001u, hi);
+    for (int i = 0; i < SET * NT; ++i, total += 4) {
+        const int m = i / NT, nt = i - m * NT;
+        const uint8_t* side = stage + m * chunk + kQ4ChunkCodes;
+        float plain[4] = {0.0f, 0.0f, 0.0f, 0.0f}, centred[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        int left = blocks, g = 0;
+#pragma unroll 1
+        for (int b = 0; b < 4; ++b) {
+            uint32_t z0 = 8, z1 = 8;
+            if (zeros) {
+                const uint8_t* z = side + groups * kQ4StripK * 2 + g * kQ4StripK + r;
+                z0 = z[0];
+                z1 = z[8];
+            }
+            const uint32_t* codes =
+                reinterpret_cast<const uint32_t*>(stage + m * chunk + b * 256) + lane;
+            auto multiply = [&](const uint32_t (&lo)[4], const uint32_t (&hi)[4], size_t at,
+                                float (&acc)[4]) {
                 const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]};
                 const uint32_t a1[4] = {lo[2], hi[2], lo[3], hi[3]};
+                const uint4 x = load(col.x + nt * col.padded + at);
                 mma_bf16(acc, a0, x.x, x.y);
                 mma_bf16(acc, a1, x.z, x.w);
                 if (JOIN && nt == NT - 1) {
                     uint4 more = make_uint4(0, 0, 0, 0);
-                    if (joined) more = *reinterpret_cast<const uint4*>(joined + b * 32);
+                    if (col.more) more = load(col.more + at);
                     mma_bf16(acc, a0, more.x, more.y);
                     mma_bf16(acc, a1, more.z, more.w);
                 }
-                if (--left > 0) continue;
-                left = blocks;
-                const uint16_t* scales = reinterpret_cast<const uint16_t*>(side) + g * kQ4StripK + r;
-                const float s0 = q4_scale(scales[0], geom.fp16);
-                const float s1 = q4_scale(scales[8], geom.fp16);
-                total[m][nt][0] = fmaf(s0, acc[0], total[m][nt][0]);
-                total[m][nt][1] = fmaf(s0, acc[1], total[m][nt][1]);
-                total[m][nt][2] = fmaf(s1, acc[2], total[m][nt][2]);
-                total[m][nt][3] = fmaf(s1, acc[3], total[m][nt][3]);
-                acc[0] = acc[1] = acc[2] = acc[3] = 0.0f;
-                ++g;
+            };
+            uint32_t lo[4], hi[4];
+            q4_plain(codes[0], lo);
+            q4_plain(codes[32], hi);
+            multiply(lo, hi, b * 32, plain);
+            q4_centred(codes[0], 0x43004300u | z0 * 0x00010001u, lo);
+            q4_centred(codes[32], 0x43004300u | z1 * 0x00010001u, hi);
+            multiply(lo, hi, b * 32 + col.form, centred);
+            if (--left > 0) continue;
+            left = blocks;
+            const uint16_t* scales = reinterpret_cast<const uint16_t*>(side) + g * kQ4StripK + r;
+            const float s0 = q4_scale(scales[0], fp16), s1 = q4_scale(scales[8], fp16);
+            const float f0 = zeros ? float(z0) : 1.0f, f1 = zeros ? float(z1) : 1.0f;
+            const float2 xs = col.group_sums<NT, JOIN, GROUP>(g, nt, group);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float d = fmaf(plain[j], kQ4Unscale, (j < 2 ? f0 : f1) * (j & 1 ? xs.y : xs.x));
+                total[j] = fmaf(j < 2 ? s0 : s1, special >> (j & 1) & 1 ? centred[j] : d, total[j]);
+                plain[j] = centred[j] = 0.0f;
             }
+            ++g;
         }
+    }
 }
 
 // The columns of A^T of a tile of tokens. Where tiles are of one or two tokens, a piece has a column
@@ -526,7 +559,7 @@ __global__ void __launch_bounds__(THREADS, 2)
     if (tid == 0) claimed = atomicAdd(a.counters, 1);
 
     // The tokens of each expert, in order, in tiles; the same in every CTA. Tokens that want the
-    // centred form have tiles of their own, so that they change nothing for the others. A token
+    // centred form have tiles of their own, so that the others need not take its time. A token
     // picks an expert once, so an expert's tokens are a 64-bit mask (one for each form).
     {
         for (int i = tid; i < slots; i += threads) {
@@ -563,7 +596,7 @@ __global__ void __launch_bounds__(THREADS, 2)
                 tile.x = tid;
                 tile.y = first + (other ? plain : 0) + from;
                 tile.z = min(plan.capacity, (other ? centred : plain) - from);
-                tile.w = other;
+                tile.w = other ? -1 : 0;
                 tile_s[first_tile + k] = tile;
             }
         }
@@ -736,15 +769,15 @@ __global__ void __launch_bounds__(THREADS, 2)
         const int padded = second ? h_padded : x_padded, per_row = second ? 1 : a.top;
         const int place = second ? wn2 * sets2_item + wm2 : wn1 * sets1_item + wm1;
         const float* sum_rows = second ? a.h_sum : a.x_sum;
-        const uint16_t* rows = second ? a.hp + (tile.w ? a.h_form : 0)
-                                      : a.xp + (tile.w ? a.x_form : 0);
+        const uint16_t* rows = second ? a.hp : a.xp;
         auto run = [&](auto nt_, auto join_) {
             constexpr int NT = decltype(nt_)::value;
             constexpr bool JOIN = decltype(join_)::value;
             // columns that do not exist repeat the first, and their sums are not used
+            const int apart = NT == 1 ? token_columns : 1;
+            auto token_of = [&](int j) { return apart == 1 ? j : apart == 2 ? j >> 1 : j * 11 >> 5; };
             auto row_of = [&](int j) {
-                const int apart = NT == 1 ? token_columns : 1;
-                const int m = apart == 1 ? j : apart == 2 ? j >> 1 : j * 11 >> 5, p = j - m * apart;
+                const int m = token_of(j), p = j - m * apart;
                 const bool is = m < tile.z;
                 const int row = member_s[tile.y + (is ? m : 0)] / per_row;
                 return uint32_t(row * pieces + (is ? p : 0));
@@ -753,7 +786,6 @@ __global__ void __launch_bounds__(THREADS, 2)
             // piece of first columns is nothing.
             const uint16_t* const col = rows + size_t(row_of(r)) * padded + c * 8;
             const bool joins = NT == 2 || (r & 1);
-            const int join_at = NT * padded;
             // of columns 2 c and 2 c + 1, in their units' first block
             const uint32_t sum_at[2] = {row_of(2 * c) * uint32_t(padded / 32),
                                         row_of(2 * c + 1) * uint32_t(padded / 32)};
@@ -767,33 +799,51 @@ __global__ void __launch_bounds__(THREADS, 2)
 #pragma unroll 1
             while (w.left > 0) {
                 if (warp == 0 && w.left <= claim_at) claim_step();
-                const uint16_t* here = col + w.unit * kQ4UnitN;
-                const float* here_sum = sum_rows + w.unit * (kQ4UnitN / 32);
-                auto third = [&](int b) {
+                Columns here;
+                here.x = col + w.unit * kQ4UnitN;
+                here.more = joins ? here.x + NT * padded : nullptr;
+                here.padded = padded;
+                here.form = second ? a.h_form : a.x_form;
+                here.sums = sum_rows + w.unit * (kQ4UnitN / 32);
+                here.sum_at[0] = sum_at[0];
+                here.sum_at[1] = sum_at[1];
+                auto more = [&](int b) {
                     uint4 v = make_uint4(0, 0, 0, 0);
-                    if (joins) v = *reinterpret_cast<const uint4*>(here + join_at + b * 32);
+                    if (joins) v = *reinterpret_cast<const uint4*>(here.more + b * 32);
                     return v;
                 };
                 advance(w);
                 if (tile.w) {
+                    const int special =
+                        (tile.w >> token_of(2 * c) & 1) | (tile.w >> token_of(2 * c + 1) & 1) << 1;
+                    float kept[SET * NT * 4];
+                    auto move = [&](bool back) {
+#pragma unroll
+                        for (int i = 0; i < SET * NT * 4; ++i) {
+                            float& t = total[i / (4 * NT)][i / 4 % NT][i % 4];
+                            back ? t = kept[i] : kept[i] = t;
+                        }
+                    };
                     acquire();
-                    chunk_set_centred<NT, JOIN>(stage, plan.chunk, geom, lane, here, padded,
-                                                joins ? here + join_at : nullptr, total);
+                    move(false);
+                    chunk_set_mixed<NT, JOIN, GROUP>(stage, plan.chunk, geom.group, geom.zeros, geom.fp16,
+                                                     here, special, kept);
+                    move(true);
                 } else {
                     if constexpr (NT == 1 && GROUP != 0 && !JOIN) {
                         // all four blocks' words at once, while the stage is waited for
                         uint4 x[4];
 #pragma unroll
                         for (int b = 0; b < 4; ++b)
-                            x[b] = *reinterpret_cast<const uint4*>(here + b * 32);
+                            x[b] = *reinterpret_cast<const uint4*>(here.x + b * 32);
                         __align__(16) float block[2][4];
 #pragma unroll
                         for (int i = 0; i < 2; ++i)
                             *reinterpret_cast<float4*>(block[i]) =
-                                *reinterpret_cast<const float4*>(here_sum + sum_at[i]);
+                                *reinterpret_cast<const float4*>(here.sums + sum_at[i]);
                         acquire();
                         chunk_set<SET, 1, false, GROUP, ZEROS>(
-                            stage, plan.chunk, geom, lane, [&](int b, int) { return x[b]; }, third,
+                            stage, plan.chunk, geom, lane, [&](int b, int) { return x[b]; }, more,
                             [&](int g, int) {
                                 return make_float2(group_sum<GROUP>(block[0], g, GROUP),
                                                    group_sum<GROUP>(block[1], g, GROUP));
@@ -808,21 +858,11 @@ __global__ void __launch_bounds__(THREADS, 2)
                             chunk_set<MT, NT, JOIN, GROUP, ZEROS>(
                                 stage + m * plan.chunk, plan.chunk, geom, lane,
                                 [&](int b, int nt) {
-                                    return *reinterpret_cast<const uint4*>(here + nt * padded + b * 32);
+                                    return *reinterpret_cast<const uint4*>(here.x + nt * padded + b * 32);
                                 },
-                                third,
+                                more,
                                 [&](int g, int nt) {
-                                    const float* block = here_sum + nt * (padded / 32);
-                                    float2 s = make_float2(
-                                        group_sum<GROUP>(block + sum_at[0], g, geom.group),
-                                        group_sum<GROUP>(block + sum_at[1], g, geom.group));
-                                    if (JOIN && nt == NT - 1) {
-                                        block += padded / 32;
-                                        if (NT == 2)
-                                            s.x += group_sum<GROUP>(block + sum_at[0], g, geom.group);
-                                        s.y += group_sum<GROUP>(block + sum_at[1], g, geom.group);
-                                    }
-                                    return s;
+                                    return here.template group_sums<NT, JOIN, GROUP>(g, nt, geom.group);
                                 },
                                 total + m);
                     }
@@ -888,14 +928,14 @@ __global__ void __launch_bounds__(THREADS, 2)
         }
         if (item >= first_items && item < first_items + second_items && !hidden_ready) {
             wait_count(a.counters + 1, first_items, &abort_s, a.err);
-            // tiles with a hidden value that the plain form cannot take
+            // members with a hidden value that the plain form cannot take
             const bool some = __ldcg(a.counters + 2) != 0;
             for (int k = tid; k < tiles; k += threads) {
                 const int4 tile = tile_s[k];
                 int special = 0;
                 if (some)
                     for (int i = 0; i < tile.z; ++i)
-                        special |= __ldcg(a.h_special + member_s[tile.y + i]);
+                        special |= (__ldcg(a.h_special + member_s[tile.y + i]) != 0) << i;
                 tile_s[k].w = special;
             }
             __syncthreads();
