@@ -71,6 +71,20 @@ _current_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
+def _result(shape, dtype, device, stream):
+    """An empty tensor for a call on ``stream``. It is allocated there: the current stream's
+    memory may still be in use by that stream's pending work, which the caller cannot order
+    before the call. The caller goes on with the tensor on the current stream, so it is marked
+    as in use there."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(current)
+    return t
+
+
 def _launch(fn, what, tensors, index, stream, *args):
     """Calls a library function with a stream as its last argument, on the tensors' device.
     Tensors used on a stream other than the current one are marked as in use there."""
@@ -95,7 +109,7 @@ class Q4Matrix:
     q4_pack. ``data`` is the packed buffer (uint8, one dimension)."""
 
     def __init__(self, N: int, K: int, group: int, zeros: bool, fp16_scales: bool, stack: bool,
-                 count: int, device):
+                 count: int, device, stream=None):
         self.N, self.K, self.group = int(N), int(K), int(group)
         self.zeros, self.count, self.stack = bool(zeros), int(count), bool(stack)
         self.scale_dtype = torch.float16 if fp16_scales else torch.bfloat16
@@ -105,7 +119,7 @@ class Q4Matrix:
         size = lib().sgemm_q4_bytes(self._ref)
         if size < 0:
             raise SgemmError(int(size), f"4-bit matrix {count} x {N} x {K}, group {group}")
-        self.data = torch.empty(size, dtype=torch.uint8, device=device)
+        self.data = _result(size, torch.uint8, device, stream)
         self.device = self.data.device
         self.index = self.device.index
         self._c.data = self.data.data_ptr()
@@ -124,13 +138,13 @@ class Q4Matrix:
                 f"scales={self.scale_dtype}, device={self.device})")
 
 
-def _packed_for(t, name, group, zeros, fp16_scales, transposed) -> Q4Matrix:
+def _packed_for(t, name, group, zeros, fp16_scales, transposed, stream) -> Q4Matrix:
     _cuda_tensor(t, name)
     if t.dim() not in (2, 3) or not t.is_contiguous() or t.numel() == 0:
         raise ValueError(f"{name} must be a contiguous, non-empty 2-D or 3-D tensor")
     N, K = (t.shape[-1], t.shape[-2]) if transposed else (t.shape[-2], t.shape[-1])
     count = t.shape[0] if t.dim() == 3 else 1
-    return Q4Matrix(N, K, group, zeros, fp16_scales, t.dim() == 3, count, t.device)
+    return Q4Matrix(N, K, group, zeros, fp16_scales, t.dim() == 3, count, t.device, stream)
 
 
 def q4_quantize(B, group: int = 128, zeros: bool = False, transposed: bool = False, stream=None):
@@ -139,7 +153,7 @@ def q4_quantize(B, group: int = 128, zeros: bool = False, transposed: bool = Fal
     one row for each output. Returns a Q4Matrix."""
     _cuda_tensor(B, "B")
     code = _dtype_code(B, "B")
-    W = _packed_for(B, "B", group, zeros, False, transposed)
+    W = _packed_for(B, "B", group, zeros, False, transposed, stream)
     _launch(lib().sgemm_q4_quantize, "sgemm_q4_quantize", (B, W.data), W.index, stream,
             B.data_ptr(), code, int(transposed), W._ref)
     return W
@@ -154,7 +168,7 @@ def q4_pack(codes, scales, zeros=None, group: int = 128, transposed: bool = Fals
     if codes.dtype != torch.uint8:
         raise ValueError("codes must be uint8")
     W = _packed_for(codes, "codes", group, zeros is not None,
-                    getattr(scales, "dtype", None) == torch.float16, transposed)
+                    getattr(scales, "dtype", None) == torch.float16, transposed, stream)
     groups = -(-W.N // W.group)
     shape = codes.shape[:-2] + ((W.K, groups) if transposed else (groups, W.K))
     for name, t, kinds in (("scales", scales, (torch.bfloat16, torch.float16)),
@@ -177,7 +191,7 @@ def q4_dequantize(W: Q4Matrix, out=None, stream=None):
     if not isinstance(W, Q4Matrix):
         raise TypeError("W must be a Q4Matrix")
     if out is None:
-        out = torch.empty(W.shape, dtype=torch.float32, device=W.device)
+        out = _result(W.shape, torch.float32, W.device, stream)
     else:
         _cuda_tensor(out, "out")
         if out.dtype != torch.float32 or tuple(out.shape) != W.shape or not out.is_contiguous() \
@@ -203,7 +217,7 @@ def q4_matmul(A, W: Q4Matrix, out=None, stream=None):
     if A.get_device() != W.index:
         raise ValueError(f"A is on {A.device}, W on {W.device}")
     if out is None:
-        out = torch.empty((M, W.K), dtype=A.dtype, device=W.device)
+        out = _result((M, W.K), A.dtype, W.device, stream)
         ldc = W.K
     else:
         _cuda_tensor(out, "out")
@@ -276,15 +290,15 @@ class MoeLayer:
                     not live.is_contiguous() or live.device != self.device:
                 raise ValueError(f"live must be {T} bool or uint8 values on {self.device}")
         if out is None:
-            out = torch.empty((T, self.D), dtype=self.dtype, device=self.device)
+            out = _result((T, self.D), self.dtype, self.device, stream)
             ldy = self.D
         else:
             _cuda_tensor(out, "out")
             if out.dtype != x.dtype or out.shape[0] != T or out.device != x.device:
                 raise ValueError(f"out must be {T} x {self.D} of type {x.dtype} on {x.device}")
             ldy = _rows(out, "out", self.D)
-        ids = torch.empty((T, self.top_k), dtype=torch.int32, device=self.device)
-        weights = torch.empty((T, self.top_k), dtype=torch.float32, device=self.device)
+        ids = _result((T, self.top_k), torch.int32, self.device, stream)
+        weights = _result((T, self.top_k), torch.float32, self.device, stream)
         args = (self._ref, x.data_ptr(), ldx, T, None if live is None else live.data_ptr(),
                 out.data_ptr(), ldy, ids.data_ptr(), weights.data_ptr())
         index = self.index
