@@ -112,10 +112,11 @@ constexpr float kQ4Unscale = 0x1p37f;      // 2^133 / 2^96
 // Splits x into P pieces whose sum it is: each takes the leading 8 significant bits of what
 // is left by truncation, so no piece overflows and the remainder is exact. An infinity or
 // NaN is its own first piece and leaves nothing (a difference of infinities would turn it
-// into NaN).
+// into NaN). A NaN is made quiet: one whose upper half is an infinity's would become one.
 template <int P>
 __device__ __forceinline__ void split_pieces(float x, float (&piece)[P]) {
     const bool finite = fabsf(x) <= 3.402823466e38f;
+    if (x != x) x = __uint_as_float(__float_as_uint(x) | 0x00400000u);
 #pragma unroll
     for (int p = 0; p < P; ++p) {
         const float hi =

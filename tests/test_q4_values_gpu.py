@@ -1,0 +1,64 @@
+"""The few-row product and the expert layer on every pattern of NaN. Bounds as in test_q4_gpu.py."""
+
+import pytest
+
+import dense_fp32_gemm_sgemm_gb300 as sg
+from tests.gpu_util import torch_cuda
+from tests.test_moe_gpu import Case
+from tests.test_q4_gpu import UNIT, dtypes, random_codes
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from dense_fp32_gemm_sgemm_gb300 import build
+    build.build()
+    torch_cuda()
+
+
+def matrix(key, N, K, group, zeros):
+    """A packed matrix and its values."""
+    codes, scales, z, values = random_codes(key, 1, N, K, group, zeros, False)
+    return sg.q4_pack(codes[0], scales[0], None if z is None else z[0], group=group), values[0]
+
+
+def check(C, A, values, tol=1e-5, kind="f32"):
+    ref, S = A.double() @ values, A.double().abs() @ values.abs()
+    bound = tol * S + UNIT[kind] * ref.abs() + (2.0 ** -25 if kind == "f16" else 0)
+    err = (C.cpu().double() - ref).abs()
+    assert (err <= bound).all(), f"{float((err / bound).max()):.3g} x the bound"
+
+
+@pytest.mark.parametrize("kind,bits", [("f32", [0x7f800001, 0x7f80ffff, -0x7fffff, 0x7fc00000]),
+                                       ("bf16", [0x7f81, 0x7fff, -0x7f]),
+                                       ("f16", [0x7c01, 0x7dff, -0x3ff])])
+@pytest.mark.parametrize("M", [5, 40])
+def test_any_nan_is_one(M, kind, bits):
+    torch = torch_cuda()
+    N, K = 200, 33
+    W, values = matrix("nan", N, K, 64, False)
+    A = torch.randn(M, N, generator=torch.Generator().manual_seed(M)).to(dtypes()[kind])
+    raw = A.view(torch.int32 if kind == "f32" else torch.int16)
+    for i, b in enumerate(bits):
+        raw[i, 17 * i + 3] = b
+    assert bool(torch.isnan(A[:len(bits)]).any(1).all())
+    C = sg.q4_matmul(A.cuda(), W)
+    assert bool(torch.isnan(C[:len(bits)]).all())
+    clean = A[len(bits):]
+    check(C[len(bits):], clean, values, kind=kind)
+
+
+@pytest.mark.parametrize("kind,bits", [("f32", 0x7f800001), ("bf16", 0x7f81), ("f16", 0x7c01)])
+@pytest.mark.parametrize("T", [3, 40])
+def test_any_nan_is_one_in_the_layer(T, kind, bits):
+    torch = torch_cuda()
+    c = Case(T, 100, 48, 4, 2, kind, key=85)
+    want, _, _ = c.check()
+    x = c.x.clone()
+    x.view(torch.int32 if kind == "f32" else torch.int16)[1, 9] = bits
+    y, ids, _ = c.layer(x.cuda())
+    assert ids[1].tolist() == [0, 1]
+    assert bool(torch.isnan(y[1]).all())
+    others = [t for t in range(T) if t != 1]
+    assert torch.equal(y.cpu().double()[others], want[others])
