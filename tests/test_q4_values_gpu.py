@@ -1,4 +1,6 @@
-"""The few-row product and the expert layer on every pattern of NaN. Bounds as in test_q4_gpu.py."""
+"""The few-row product and the expert layer on every pattern of NaN, rows of a product beside other
+rows, and reductions that are too long for the widest kernel. Bounds as in test_q4_gpu.py.
+"""
 
 import pytest
 
@@ -62,3 +64,40 @@ def test_any_nan_is_one_in_the_layer(T, kind, bits):
     assert bool(torch.isnan(y[1]).all())
     others = [t for t in range(T) if t != 1]
     assert torch.equal(y.cpu().double()[others], want[others])
+
+
+@pytest.mark.parametrize("kind,rows", [("f32", 3), ("bf16", 12), ("f32", 9)])
+def test_rows_do_not_depend_on_others(kind, rows):
+    """A row has the same bits whatever ordinary values the others hold, and an infinity or NaN
+    elsewhere leaves it within its bound."""
+    torch = torch_cuda()
+    N, K = 4096, 200
+    W, values = matrix("rows", N, K, 64, True)
+    gen = torch.Generator().manual_seed(rows)
+    A = torch.randn(rows, N, generator=gen).to(dtypes()[kind])
+    first = sg.q4_matmul(A.cuda(), W)
+    other = torch.randn(rows, N, generator=gen).to(dtypes()[kind])
+    other[1] = A[1]
+    assert torch.equal(sg.q4_matmul(other.cuda(), W)[1], first[1])
+    other[0, 5], other[rows - 1, 7] = float("inf"), float("nan")
+    check(sg.q4_matmul(other.cuda(), W)[1:2], A[1:2], values, kind=kind)
+
+
+@pytest.mark.parametrize("zeros", [False, True], ids=["sym", "zeros"])
+@pytest.mark.parametrize("group", [32, 128])
+@pytest.mark.parametrize("N", [20000, 40961, 65536])
+@pytest.mark.parametrize("kind,M", [("f32", 5), ("bf16", 17), ("f16", 9)])
+def test_long_reductions(kind, M, N, group, zeros):
+    """Reductions whose columns fit only 16 or 8 at a time. Up to 65536 n, a warpgroup of a
+    cluster of 8 adds the sums of 32 units of up to 4 groups one after another: 128 of 2^-24
+    each instead of 64, so 2e-5 S covers all."""
+    torch = torch_cuda()
+    K = 130
+    W, values = matrix("long", N, K, group, zeros)
+    A = torch.randn(M, N, generator=torch.Generator().manual_seed(N + M)).to(dtypes()[kind])
+    check(sg.q4_matmul(A.cuda(), W), A, values, tol=2e-5, kind=kind)
+    A[2, N - 1] = float("inf")
+    C = sg.q4_matmul(A.cuda(), W)
+    keep = [i for i in range(M) if i != 2]
+    check(C[keep], A[keep], values, tol=2e-5, kind=kind)
+    assert not bool(torch.isfinite(C[2]).any())
