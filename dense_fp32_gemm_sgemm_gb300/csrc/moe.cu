@@ -71,14 +71,15 @@ struct MoeArgs {
     size_t ldy;
     bool vec;  // rows of x and the router start on 16-byte boundaries
     // scratch
-    // pieces as bfloat16, first staged for the plain form, then, x_form and h_form further, as they
-    // are for the centred form
+    // pieces as bfloat16, first staged for the plain form, then, x_form and h_form further, for the
+    // centred form, each 32 n of a row with a power of two of their own
     uint16_t* xp;      // of x: [token][piece][D padded to units]
     uint16_t* hp;      // of the hidden values: [token and slot][piece][F padded]
     size_t x_form, h_form;
     // sums of 32 values of each piece, times -8 or, where the weights have zero points, -1
     float *x_sum, *h_sum;
     float x_factor, h_factor;
+    float *x_back, *h_back;  // what products of 32 values in the centred form are multiplied with
     int* x_special;    // [token]: nonzero where the plain form cannot take some value
     int* h_special;    // [token and slot]
     // 0: next item, 1: first items done, 2: whether some h_special is set, 3 ..: second items done
@@ -146,11 +147,20 @@ __device__ __forceinline__ bool write_pieces(const MoeArgs& a, int t, int rank, 
         float sums[P];
 #pragma unroll
         for (int p = 0; p < P; ++p) sums[p] = 0.0f;
+        Raw8<T> raw;
+        uint32_t most = 0;
         if (u < octets) {
-            const Raw8<T> raw = load_raw8(x, u * 8, a.D, a.vec);
+            raw = load_raw8(x, u * 8, a.D, a.vec);
+            most = largest_bits(raw);
+        }
+        most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
+        most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
+        const CentredScale scale(most);
+        if (u < octets) {
             uint4 plain[P], centred[P];
             split_plain<P>(raw, magnitudes, plain, sums);
-            split_centred<P>(raw, centred);
+            split_centred<P>(raw, scale.down, centred);
+            if (lane % 4 == 0) a.x_back[size_t(t) * (padded / 32) + u / 4] = scale.back;
 #pragma unroll
             for (int p = 0; p < P; ++p) {
                 uint16_t* to = a.xp + (size_t(t) * P + p) * padded;
@@ -417,6 +427,8 @@ struct Columns {
     size_t form;           // to the same as they are, for the centred form
     const float* sums;     // of 32 values each; those of columns 2 c and 2 c + 1 of the first tile:
     uint32_t sum_at[2];
+    const float* back;     // what products of 32 values in the centred form are multiplied with,
+    uint32_t back_at[2];   // for the same columns, in all tiles
     template <int NT, bool JOIN, int GROUP>
     __device__ __forceinline__ float2 group_sums(int g, int nt, int group) const {
         const float* block = sums + nt * (padded / 32);
@@ -433,7 +445,8 @@ struct Columns {
 
 // chunk_set of SET chunks where some columns want the centred form: both forms are multiplied, and
 // each column keeps the sums of its own, which are those that it has in a tile of one form. So a
-// token's bits do not depend on the others of its tile. special: of columns 2 c and 2 c + 1 (bits 0
+// token's bits do not depend on the others of its tile. The centred form's sums are of 32 n each.
+// special: of columns 2 c and 2 c + 1 (bits 0
 // and 1). Rarely run, so kept small and out of the way: totals in local memory, no loop unrolled.
 template <int NT, bool JOIN, int GROUP>
 __device__ __noinline__ void chunk_set_mixed(const uint8_t* stage, int chunk, int group, int zeros, int fp16,
@@ -445,7 +458,7 @@ __device__ __noinline__ void chunk_set_mixed(const uint8_t* stage, int chunk, in
     for (int i = 0; i < SET * NT; ++i, total += 4) {
         const int m = i / NT, nt = i - m * NT;
         const uint8_t* side = stage + m * chunk + kQ4ChunkCodes;
-        float plain[4] = {0.0f, 0.0f, 0.0f, 0.0f}, centred[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        float plain[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         int left = blocks, g = 0;
 #pragma unroll 1
         for (int b = 0; b < 4; ++b) {
@@ -475,20 +488,26 @@ __device__ __noinline__ void chunk_set_mixed(const uint8_t* stage, int chunk, in
             q4_plain(codes[0], lo);
             q4_plain(codes[32], hi);
             multiply(lo, hi, b * 32, plain);
+            float centred[4] = {0.0f, 0.0f, 0.0f, 0.0f};
             q4_centred(codes[0], 0x43004300u | z0 * 0x00010001u, lo);
             q4_centred(codes[32], 0x43004300u | z1 * 0x00010001u, hi);
             multiply(lo, hi, b * 32 + col.form, centred);
-            if (--left > 0) continue;
-            left = blocks;
             const uint16_t* scales = reinterpret_cast<const uint16_t*>(side) + g * kQ4StripK + r;
             const float s0 = q4_scale(scales[0], fp16), s1 = q4_scale(scales[8], fp16);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (special >> (j & 1) & 1)
+                    total[j] = add_centred(j < 2 ? s0 : s1, col.back[col.back_at[j & 1] + b], centred[j],
+                                           total[j]);
+            if (--left > 0) continue;
+            left = blocks;
             const float f0 = zeros ? float(z0) : 1.0f, f1 = zeros ? float(z1) : 1.0f;
             const float2 xs = col.group_sums<NT, JOIN, GROUP>(g, nt, group);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const float d = fmaf(plain[j], kQ4Unscale, (j < 2 ? f0 : f1) * (j & 1 ? xs.y : xs.x));
-                total[j] = fmaf(j < 2 ? s0 : s1, special >> (j & 1) & 1 ? centred[j] : d, total[j]);
-                plain[j] = centred[j] = 0.0f;
+                if (!(special >> (j & 1) & 1)) total[j] = fmaf(j < 2 ? s0 : s1, d, total[j]);
+                plain[j] = 0.0f;
             }
             ++g;
         }
@@ -766,7 +785,8 @@ __global__ void __launch_bounds__(THREADS, 2)
         const int pieces = second ? H_PIECES : plan.x_pieces;
         const int token_columns = columns_of(pieces);
         const bool packed = packed_columns(tile.z, token_columns);
-        const int padded = second ? h_padded : x_padded, per_row = second ? 1 : a.top;
+        const int padded = second ? h_padded : x_padded;
+        const uint32_t per_row = second ? 1 : a.top;
         const int place = second ? wn2 * sets2_item + wm2 : wn1 * sets1_item + wm1;
         const float* sum_rows = second ? a.h_sum : a.x_sum;
         const uint16_t* rows = second ? a.hp : a.xp;
@@ -776,11 +796,12 @@ __global__ void __launch_bounds__(THREADS, 2)
             // columns that do not exist repeat the first, and their sums are not used
             const int apart = NT == 1 ? token_columns : 1;
             auto token_of = [&](int j) { return apart == 1 ? j : apart == 2 ? j >> 1 : j * 11 >> 5; };
+            auto token_row = [&](int m) {
+                return uint32_t(member_s[tile.y + (m < tile.z ? m : 0)]) / per_row;
+            };
             auto row_of = [&](int j) {
                 const int m = token_of(j), p = j - m * apart;
-                const bool is = m < tile.z;
-                const int row = member_s[tile.y + (is ? m : 0)] / per_row;
-                return uint32_t(row * pieces + (is ? p : 0));
+                return token_row(m) * pieces + (m < tile.z ? p : 0);
             };
             // of the first tile of columns; the next piece's are `padded` further. The third
             // piece of first columns is nothing.
@@ -807,6 +828,7 @@ __global__ void __launch_bounds__(THREADS, 2)
                 here.sums = sum_rows + w.unit * (kQ4UnitN / 32);
                 here.sum_at[0] = sum_at[0];
                 here.sum_at[1] = sum_at[1];
+                const int unit = w.unit;
                 auto more = [&](int b) {
                     uint4 v = make_uint4(0, 0, 0, 0);
                     if (joins) v = *reinterpret_cast<const uint4*>(here.more + b * 32);
@@ -816,6 +838,9 @@ __global__ void __launch_bounds__(THREADS, 2)
                 if (tile.w) {
                     const int special =
                         (tile.w >> token_of(2 * c) & 1) | (tile.w >> token_of(2 * c + 1) & 1) << 1;
+                    here.back = (second ? a.h_back : a.x_back) + unit * (kQ4UnitN / 32);
+                    for (int i = 0; i < 2; ++i)
+                        here.back_at[i] = token_row(token_of(2 * c + i)) * uint32_t(padded / 32);
                     float kept[SET * NT * 4];
                     auto move = [&](bool back) {
 #pragma unroll
@@ -974,16 +999,22 @@ __global__ void __launch_bounds__(THREADS, 2)
                     a.counters[2] = 1;
                 }
                 const float scale = (f_at & 2) ? kQ4Scale16 : kQ4Scale;  // by place, as in x
+                // a warp's 32 values are one token's
+                const CentredScale centred(
+                    __reduce_max_sync(0xffffffffu, __float_as_uint(h) & 0x7fffffffu));
+                float centred_piece[H_PIECES];
+                split_pieces<H_PIECES>(h * centred.down, centred_piece);
+                if (lane == 0) a.h_back[size_t(slot) * (h_padded / 32) + f_at / 32] = centred.back;
 #pragma unroll
                 for (int p = 0; p < H_PIECES; ++p) {
-                    float sum = piece[p];  // a warp's 32 values are one token's
+                    float sum = piece[p];
                     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
                     if (lane == 0)
                         a.h_sum[(size_t(slot) * H_PIECES + p) * (h_padded / 32) + f_at / 32] =
                             sum * a.h_factor;
                     uint16_t* to = a.hp + (size_t(slot) * H_PIECES + p) * h_padded + f_at;
                     to[0] = uint16_t(__float_as_uint(piece[p] * scale) >> 16);
-                    to[a.h_form] = uint16_t(__float_as_uint(piece[p]) >> 16);
+                    to[a.h_form] = uint16_t(__float_as_uint(centred_piece[p]) >> 16);
                 }
             }
             // past F: down's weights are zero there, but not whatever the scratch holds
@@ -994,7 +1025,10 @@ __global__ void __launch_bounds__(THREADS, 2)
                     const size_t row = size_t(member_s[tile.y + m]) * H_PIECES + line % H_PIECES;
                     uint16_t* to = a.hp + row * h_padded + from + i % rest;
                     to[0] = to[a.h_form] = 0;
-                    if (i % rest % 32 == 0) a.h_sum[row * (h_padded / 32) + (from + i % rest) / 32] = 0.0f;
+                    if (i % rest % 32 == 0) {
+                        a.h_sum[row * (h_padded / 32) + (from + i % rest) / 32] = 0.0f;
+                        a.h_back[row / H_PIECES * (h_padded / 32) + (from + i % rest) / 32] = 1.0f;
+                    }
                 }
             }
             __syncthreads();
@@ -1206,6 +1240,8 @@ extern "C" int sgemm_moe(const sgemm_moe_layer* layer, const void* x, long long 
     const size_t at_z = take(size_t(slots) * m.D * 4);
     const size_t at_xsum = take(size_t(T) * plan.x_pieces * (x_padded / 32) * 4);
     const size_t at_hsum = take(size_t(slots) * H_PIECES * (h_padded / 32) * 4);
+    const size_t at_xback = take(size_t(T) * (x_padded / 32) * 4);
+    const size_t at_hback = take(size_t(slots) * (h_padded / 32) * 4);
     const size_t at_ids = take(ids ? 0 : side), at_weights = take(weights ? 0 : side);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     Scratch ws;
@@ -1235,6 +1271,8 @@ extern "C" int sgemm_moe(const sgemm_moe_layer* layer, const void* x, long long 
     a.hp = reinterpret_cast<uint16_t*>(base + at_hp);
     a.x_sum = reinterpret_cast<float*>(base + at_xsum);
     a.h_sum = reinterpret_cast<float*>(base + at_hsum);
+    a.x_back = reinterpret_cast<float*>(base + at_xback);
+    a.h_back = reinterpret_cast<float*>(base + at_hback);
     a.x_factor = g.zeros ? -1.0f : -8.0f;
     a.h_factor = gd.zeros ? -1.0f : -8.0f;
     a.x_form = size_t(T) * plan.x_pieces * x_padded;

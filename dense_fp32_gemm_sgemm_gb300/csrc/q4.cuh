@@ -15,9 +15,10 @@
 // staged times 2^96 to bring the products back into FP32's range, those that meet 16 q
 // times 2^92, and a group's sum is (sum of q x) - z (sum of x), the second sum taken once when
 // the columns are staged. Where a staged value is an infinity, a NaN or outside [2^-64, 2^24)
-// the scaled product could leave FP32's range; such columns are staged as they are and meet
-// the centred form: 0x4300 | q is the bfloat16 128 + q, and subtracting 128 + z leaves q - z
-// (eleven instructions).
+// the scaled product could leave FP32's range; such columns meet the centred form: 0x4300 | q
+// is the bfloat16 128 + q, and subtracting 128 + z leaves q - z (eleven instructions). They are
+// staged times a power of two that brings the largest of a group (of 32 n, in the expert layer)
+// near one, so that neither the sums overflow nor low pieces fall out of bfloat16's range.
 //
 // A unit is 128 columns of B times 128 n. In memory:
 //   codes: [block of 32 n][column][4 words]; word i of a column's block holds n = 8 i + e of the
@@ -255,13 +256,38 @@ __device__ __forceinline__ void split_plain(const Raw8<T>& raw, Magnitudes& magn
 #pragma unroll
     for (int p = 0; p < P; ++p) out[p] = make_uint4(word[p][0], word[p][1], word[p][2], word[p][3]);
 }
-// The pieces of 8 values as they are, for the centred form.
+// The power of two that values are staged with for the centred form, from the bits of the largest
+// magnitude among them (or an infinity's or NaN's), and its reciprocal, which their sums are
+// multiplied with. Within 2^100, which leaves both and what they are multiplied with normal.
+struct CentredScale {
+    float down, back;
+    __device__ __forceinline__ explicit CentredScale(uint32_t most) {
+        const int k = min(max(127 - int(most >> 23), -100), 100);
+        down = __uint_as_float(uint32_t(127 + k) << 23);
+        back = __uint_as_float(uint32_t(127 - k) << 23);
+    }
+};
+// total + s * back * acc, the factors in the order in which nothing overflows or is lost below
+// FP32's normal range that would not be in the result.
+__device__ __forceinline__ float add_centred(float s, float back, float acc, float total) {
+    return (back >= 1.0f) == (fabsf(s) < 1.0f) ? fmaf(s * back, acc, total)
+                                               : fmaf(s, back * acc, total);
+}
+template <class T>
+__device__ __forceinline__ uint32_t largest_bits(const Raw8<T>& raw) {
+    const T* e = reinterpret_cast<const T*>(&raw);
+    uint32_t most = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) most = max(most, __float_as_uint(float(e[i])) & 0x7fffffffu);
+    return most;
+}
+// The pieces of 8 values times a power of two, for the centred form.
 template <int P, class T>
-__device__ __forceinline__ void split_centred(const Raw8<T>& raw, uint4 (&out)[P]) {
+__device__ __forceinline__ void split_centred(const Raw8<T>& raw, float scale, uint4 (&out)[P]) {
     const T* e = reinterpret_cast<const T*>(&raw);
     float piece[8][P];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) split_pieces<P>(float(e[i]), piece[i]);
+    for (int i = 0; i < 8; ++i) split_pieces<P>(float(e[i]) * scale, piece[i]);
 #pragma unroll
     for (int p = 0; p < P; ++p)
         out[p] = make_uint4(pack_pieces(piece[0][p], piece[1][p]),

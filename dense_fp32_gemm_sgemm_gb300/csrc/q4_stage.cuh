@@ -43,8 +43,8 @@ struct Staging {
     int turn, turns;  // this CTA's number among those that stage the same rows
 };
 
-// Writes the pieces of the rows to their columns, and their sums (zeros for the centred form);
-// true where the plain form cannot take one of the thread's values. A group's octets lie in
+// Writes the pieces of the rows to their columns, and their sums (for the centred form, what their
+// products are to be multiplied with); true where the plain form cannot take one of the thread's values. A group's octets lie in
 // neighbouring lanes of a warp, so that shuffles add them.
 template <class T>
 __device__ __noinline__ bool stage_rows(const Staging s, bool plain) {
@@ -81,12 +81,21 @@ __device__ __noinline__ bool stage_rows(const Staging s, bool plain) {
             float sum[P];
 #pragma unroll
             for (int p = 0; p < P; ++p) sum[p] = 0.0f;
+            float back = 1.0f, down = 1.0f;
+            if (!plain && i + j * warps < bundles) {
+                uint32_t most = rows[j] >= 0 ? largest_bits(raw[j]) : 0;
+                for (int o = 1; o <= group_mask; o *= 2)
+                    most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+                const CentredScale scale(most);
+                back = scale.back;
+                down = scale.down;
+            }
             if (rows[j] >= 0) {
                 uint4 piece[P];
                 if (plain)
                     split_plain<P>(raw[j], magnitudes, piece, sum);
                 else
-                    split_centred<P>(raw[j], piece);
+                    split_centred<P>(raw[j], down, piece);
 #pragma unroll
                 for (int p = 0; p < P; ++p)
                     *reinterpret_cast<uint4*>(s.xs + octets[j] * s.octet_stride +
@@ -100,7 +109,7 @@ __device__ __noinline__ bool stage_rows(const Staging s, bool plain) {
                     sum[p] += __shfl_xor_sync(0xffffffffu, sum[p], o);
                 if (rows[j] >= 0 && (octets[j] & group_mask) == 0)
                     s.xsum[(octets[j] >> s.log_octets) * s.sum_pitch + rows[j] * COLS + p] =
-                        sum[p] * s.factor;
+                        plain ? sum[p] * s.factor : back;
             }
         }
     }

@@ -282,7 +282,6 @@ __global__ void __launch_bounds__(THREADS, 1) q4_matmul_kernel(const Q4Product a
             const int wg = (warp - WARP_GROUPS) >> 2;
             const int row = (warp & 3) * 32 + lane;  // of the tile, and lane of tensor memory
             const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
-            constexpr float unscale = CENTRED ? 1.0f : kQ4Unscale;
             float scale0[GROUPS], scale1[GROUPS];  // of the unit in buffer 0 and 1
             float zero0[GROUPS], zero1[GROUPS];
 #pragma unroll
@@ -389,9 +388,12 @@ __global__ void __launch_bounds__(THREADS, 1) q4_matmul_kernel(const Q4Product a
                                     const float x[4] = {x4.x, x4.y, x4.z, x4.w};
 #pragma unroll
                                     for (int e = 0; e < 4; ++e) {
-                                        const float t =
-                                            fmaf(acc[c + e], unscale, ZEROS ? z * x[e] : x[e]);
-                                        total[c0 + c + e] = fmaf(s, t, total[c0 + c + e]);
+                                        float& sum = total[c0 + c + e];
+                                        if constexpr (CENTRED)
+                                            sum = add_centred(s, x[e], acc[c + e], sum);
+                                        else
+                                            sum = fmaf(s, fmaf(acc[c + e], kQ4Unscale,
+                                                               ZEROS ? z * x[e] : x[e]), sum);
                                     }
                                 }
                             }

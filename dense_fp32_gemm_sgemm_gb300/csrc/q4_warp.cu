@@ -177,6 +177,7 @@ __global__ void __launch_bounds__(THREADS, MOST_RESIDENT)
             if (stage == ring_end) stage = ring;
         };
         auto word = [&](int b) { return *reinterpret_cast<const uint4*>(x + b * 64); };
+        auto sum = [&](int g) { return *reinterpret_cast<const float2*>(sums + g * COLUMNS); };
         if (special) {
 #pragma unroll 1
             for (int i = 0; i < my_units; ++i, next()) {
@@ -186,7 +187,7 @@ __global__ void __launch_bounds__(THREADS, MOST_RESIDENT)
 #pragma unroll
                 for (int m = 0; m < MT; ++m)
                     q4_chunk_centred<GROUP, ZEROS>(stage + m * CHUNK, geom.fp16, lane, word,
-                                                   total[m][0]);
+                                                   sum, total[m][0]);
             }
         } else {
 #pragma unroll 1
@@ -196,10 +197,7 @@ __global__ void __launch_bounds__(THREADS, MOST_RESIDENT)
                 fetch();
                 q4_chunk<MT, 1, GROUP, ZEROS>(
                     [&](int m) { return stage + m * CHUNK; }, geom.fp16, lane,
-                    [&](int b, int) { return word(b); },
-                    [&](int g, int) {
-                        return *reinterpret_cast<const float2*>(sums + g * COLUMNS);
-                    },
+                    [&](int b, int) { return word(b); }, [&](int g, int) { return sum(g); },
                     total);
             }
         }

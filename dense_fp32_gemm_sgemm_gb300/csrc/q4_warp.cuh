@@ -148,11 +148,11 @@ __device__ __forceinline__ void q4_chunk(Chunk&& chunk, int fp16, int lane, Load
 }
 
 // One chunk of one strip times a tile of 8 columns in the centred form, added to total. A(b): the
-// lane's word of block b of its column, staged as it is. Rarely run, so kept small rather than
-// unrolled.
-template <int GROUP, bool ZEROS, class LoadA>
+// lane's word of block b of its column, staged for that form; back(g): what the sums of group g are
+// to be multiplied with, for columns 2 c and 2 c + 1. Rarely run, so kept small rather than unrolled.
+template <int GROUP, bool ZEROS, class LoadA, class Back>
 __device__ __forceinline__ void q4_chunk_centred(const uint8_t* chunk, int fp16, int lane, LoadA&& A,
-                                                 float (&total)[4]) {
+                                                 Back&& back, float (&total)[4]) {
     constexpr int BLOCKS = GROUP / 32, GROUPS = kQ4UnitN / GROUP;
     const int r = lane >> 2;
     const uint8_t* side = chunk + kQ4ChunkCodes;
@@ -180,10 +180,11 @@ __device__ __forceinline__ void q4_chunk_centred(const uint8_t* chunk, int fp16,
         }
         const uint16_t* scales = reinterpret_cast<const uint16_t*>(side) + g * kQ4StripK + r;
         const float s0 = q4_scale(scales[0], fp16), s1 = q4_scale(scales[8], fp16);
-        total[0] = fmaf(s0, acc[0], total[0]);
-        total[1] = fmaf(s0, acc[1], total[1]);
-        total[2] = fmaf(s1, acc[2], total[2]);
-        total[3] = fmaf(s1, acc[3], total[3]);
+        const float2 f = back(g);
+        total[0] = add_centred(s0, f.x, acc[0], total[0]);
+        total[1] = add_centred(s0, f.y, acc[1], total[1]);
+        total[2] = add_centred(s1, f.x, acc[2], total[2]);
+        total[3] = add_centred(s1, f.y, acc[3], total[3]);
     }
 }
 

@@ -388,7 +388,9 @@ SGEMM_API int sgemm_q4_dequantize(const sgemm_q4* w, float* B, void* stream);
  * pieces (bfloat16, float16, float32) whose sum it is, the weights as the integers q, and
  * z times the group's sum of A is subtracted; where a row has an infinity, a NaN or a value
  * outside [2^-64, 2^24), the rows that are staged with it are multiplied by the integers
- * q - z instead. Sums are FP32, the scales are applied to each group's sum in FP32, and C is
+ * q - z instead, each group of a row times a power of two that is taken back with the scale:
+ * a finite A gives finite sums where the definition in FP32 does, and only values below 2^-110
+ * of the largest of their group may lose low bits. Sums are FP32, the scales are applied to each group's sum in FP32, and C is
  * rounded once. The order of summation depends on the sizes alone, so results are bitwise
  * reproducible. Elements of C's rows past K are not touched. C must not overlap A or w->data.
  * One launch, no workspace; the call can be captured into a CUDA graph.
