@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(ROUTE_THREADS) moe_route_kernel(const MoeArgs 
 
 // Where the expert kernel's shared memory holds what, in bytes.
 struct MoeOffsets {
-    int tiles;    // int4 each: expert, first member, members, which of them want the centred form
+    int tiles;    // int4 each: expert, first member, members, which of them want the centred form (-1: all)
     int members;  // token and slot, by expert
     int sums;     // [wn][set][chunk][column, TILE of them][17]
     int masks;    // in the same place before: [expert][form][2], and [expert]
@@ -441,75 +441,112 @@ struct Columns {
         }
         return s;
     }
+    // Adds a block's products with the tile nt of columns; at: where the block is in them.
+    template <int NT, bool JOIN>
+    __device__ __forceinline__ void multiply(const uint32_t (&a0)[4], const uint32_t (&a1)[4], int nt,
+                                             size_t at, float (&acc)[4]) const {
+        const uint4 v = *reinterpret_cast<const uint4*>(x + nt * padded + at);
+        mma_bf16(acc, a0, v.x, v.y);
+        mma_bf16(acc, a1, v.z, v.w);
+        if (JOIN && nt == NT - 1) {
+            uint4 w = make_uint4(0, 0, 0, 0);
+            if (more) w = *reinterpret_cast<const uint4*>(more + at);
+            mma_bf16(acc, a0, w.x, w.y);
+            mma_bf16(acc, a1, w.z, w.w);
+        }
+    }
 };
 
-// chunk_set of SET chunks where some columns want the centred form: both forms are multiplied, and
-// each column keeps the sums of its own, which are those that it has in a tile of one form. So a
-// token's bits do not depend on the others of its tile. The centred form's sums are of 32 n each.
-// special: of columns 2 c and 2 c + 1 (bits 0
-// and 1). Rarely run, so kept small and out of the way: totals in local memory, no loop unrolled.
+// A block of 32 n of a strip in the centred form, for the lane's columns r and r + 8 of it.
+struct CentredBlock {
+    float scale[2], zero[2];  // the zero points: 1 where there are none, for sums times -8
+    uint32_t a0[4], a1[4];
+    __device__ __forceinline__ CentredBlock(const uint8_t* strip, int b, int g, int group, int zeros,
+                                            int fp16) {
+        const int lane = threadIdx.x & 31, r = lane >> 2;
+        const uint8_t* side = strip + kQ4ChunkCodes;
+        const uint16_t* scales = reinterpret_cast<const uint16_t*>(side) + g * kQ4StripK + r;
+        const uint32_t* codes = reinterpret_cast<const uint32_t*>(strip + b * 256) + lane;
+        uint32_t word[2][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t z = 8;
+            if (zeros) z = side[kQ4UnitN / group * kQ4StripK * 2 + g * kQ4StripK + r + 8 * h];
+            scale[h] = q4_scale(scales[8 * h], fp16);
+            zero[h] = zeros ? float(z) : 1.0f;
+            q4_centred(codes[32 * h], 0x43004300u | z * 0x00010001u, word[h]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            a0[i] = word[i & 1][i >> 1];
+            a1[i] = word[i & 1][2 + (i >> 1)];
+        }
+    }
+};
+
+// chunk_set of SET chunks in the centred form, whose sums are of 32 n each. Rarely run, so kept small
+// rather than unrolled, and a function of its own, which leaves the plain form its registers.
+template <int NT, bool JOIN>
+__device__ __noinline__ void chunk_set_centred(const uint8_t* stage, int chunk, int group, int zeros, int fp16,
+                                               const Columns col, float* kept) {
+    const int group_log = 31 - __clz(group / 32);
+    float total[SET][NT][4];
+#pragma unroll
+    for (int i = 0; i < SET * NT * 4; ++i) total[i / (4 * NT)][i / 4 % NT][i % 4] = kept[i];
+#pragma unroll
+    for (int m = 0; m < SET; ++m)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll 1
+            for (int b = 0; b < 4; ++b) {
+                const CentredBlock w(stage + m * chunk, b, b >> group_log, group, zeros, fp16);
+                float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                col.multiply<NT, JOIN>(w.a0, w.a1, nt, col.form + b * 32, acc);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    total[m][nt][j] =
+                        add_centred(w.scale[j >> 1], col.back[col.back_at[j & 1] + b], acc[j], total[m][nt][j]);
+            }
+#pragma unroll
+    for (int i = 0; i < SET * NT * 4; ++i) kept[i] = total[i / (4 * NT)][i / 4 % NT][i % 4];
+}
+
+// The same where some columns want that form (special: bits 0 and 1 for columns 2 c and 2 c + 1) and
+// some the plain one: both are multiplied, and each column keeps the sums of its own, which are those
+// that it has in a tile of one form. So a token's bits do not depend on the others of its tile.
 template <int NT, bool JOIN, int GROUP>
 __device__ __noinline__ void chunk_set_mixed(const uint8_t* stage, int chunk, int group, int zeros, int fp16,
                                              const Columns col, int special, float* total) {
-    const int lane = threadIdx.x & 31, r = lane >> 2;
-    const int blocks = group / 32, groups = kQ4UnitN / group;
-    auto load = [](const uint16_t* p) { return *reinterpret_cast<const uint4*>(p); };
+    const int group_log = 31 - __clz(group / 32), lane = threadIdx.x & 31;
 #pragma unroll 1
     for (int i = 0; i < SET * NT; ++i, total += 4) {
         const int m = i / NT, nt = i - m * NT;
-        const uint8_t* side = stage + m * chunk + kQ4ChunkCodes;
+        const uint8_t* strip = stage + m * chunk;
         float plain[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        int left = blocks, g = 0;
 #pragma unroll 1
         for (int b = 0; b < 4; ++b) {
-            uint32_t z0 = 8, z1 = 8;
-            if (zeros) {
-                const uint8_t* z = side + groups * kQ4StripK * 2 + g * kQ4StripK + r;
-                z0 = z[0];
-                z1 = z[8];
-            }
-            const uint32_t* codes =
-                reinterpret_cast<const uint32_t*>(stage + m * chunk + b * 256) + lane;
-            auto multiply = [&](const uint32_t (&lo)[4], const uint32_t (&hi)[4], size_t at,
-                                float (&acc)[4]) {
-                const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]};
-                const uint32_t a1[4] = {lo[2], hi[2], lo[3], hi[3]};
-                const uint4 x = load(col.x + nt * col.padded + at);
-                mma_bf16(acc, a0, x.x, x.y);
-                mma_bf16(acc, a1, x.z, x.w);
-                if (JOIN && nt == NT - 1) {
-                    uint4 more = make_uint4(0, 0, 0, 0);
-                    if (col.more) more = load(col.more + at);
-                    mma_bf16(acc, a0, more.x, more.y);
-                    mma_bf16(acc, a1, more.z, more.w);
-                }
-            };
-            uint32_t lo[4], hi[4];
-            q4_plain(codes[0], lo);
-            q4_plain(codes[32], hi);
-            multiply(lo, hi, b * 32, plain);
-            float centred[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            q4_centred(codes[0], 0x43004300u | z0 * 0x00010001u, lo);
-            q4_centred(codes[32], 0x43004300u | z1 * 0x00010001u, hi);
-            multiply(lo, hi, b * 32 + col.form, centred);
-            const uint16_t* scales = reinterpret_cast<const uint16_t*>(side) + g * kQ4StripK + r;
-            const float s0 = q4_scale(scales[0], fp16), s1 = q4_scale(scales[8], fp16);
+            const int g = b >> group_log;
+            const CentredBlock w(strip, b, g, group, zeros, fp16);
+            float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            col.multiply<NT, JOIN>(w.a0, w.a1, nt, col.form + b * 32, acc);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 if (special >> (j & 1) & 1)
-                    total[j] = add_centred(j < 2 ? s0 : s1, col.back[col.back_at[j & 1] + b], centred[j],
-                                           total[j]);
-            if (--left > 0) continue;
-            left = blocks;
-            const float f0 = zeros ? float(z0) : 1.0f, f1 = zeros ? float(z1) : 1.0f;
+                    total[j] = add_centred(w.scale[j >> 1], col.back[col.back_at[j & 1] + b], acc[j], total[j]);
+            const uint32_t* codes = reinterpret_cast<const uint32_t*>(strip + b * 256) + lane;
+            uint32_t lo[4], hi[4];
+            q4_plain(codes[0], lo);
+            q4_plain(codes[32], hi);
+            const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]}, a1[4] = {lo[2], hi[2], lo[3], hi[3]};
+            col.multiply<NT, JOIN>(a0, a1, nt, b * 32, plain);
+            if ((b + 1) >> group_log == g) continue;
             const float2 xs = col.group_sums<NT, JOIN, GROUP>(g, nt, group);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float d = fmaf(plain[j], kQ4Unscale, (j < 2 ? f0 : f1) * (j & 1 ? xs.y : xs.x));
-                if (!(special >> (j & 1) & 1)) total[j] = fmaf(j < 2 ? s0 : s1, d, total[j]);
+                const float d = fmaf(plain[j], kQ4Unscale, w.zero[j >> 1] * (j & 1 ? xs.y : xs.x));
+                if (!(special >> (j & 1) & 1)) total[j] = fmaf(w.scale[j >> 1], d, total[j]);
                 plain[j] = 0.0f;
             }
-            ++g;
         }
     }
 }
@@ -851,8 +888,12 @@ __global__ void __launch_bounds__(THREADS, 2)
                     };
                     acquire();
                     move(false);
-                    chunk_set_mixed<NT, JOIN, GROUP>(stage, plan.chunk, geom.group, geom.zeros, geom.fp16,
-                                                     here, special, kept);
+                    if (tile.w == -1)
+                        chunk_set_centred<NT, JOIN>(stage, plan.chunk, geom.group, geom.zeros, geom.fp16,
+                                                    here, kept);
+                    else
+                        chunk_set_mixed<NT, JOIN, GROUP>(stage, plan.chunk, geom.group, geom.zeros,
+                                                         geom.fp16, here, special, kept);
                     move(true);
                 } else {
                     if constexpr (NT == 1 && GROUP != 0 && !JOIN) {
@@ -961,7 +1002,7 @@ __global__ void __launch_bounds__(THREADS, 2)
                 if (some)
                     for (int i = 0; i < tile.z; ++i)
                         special |= (__ldcg(a.h_special + member_s[tile.y + i]) != 0) << i;
-                tile_s[k].w = special;
+                tile_s[k].w = special == (1 << tile.z) - 1 ? -1 : special;
             }
             __syncthreads();
             hidden_ready = true;
