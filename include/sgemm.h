@@ -391,8 +391,10 @@ SGEMM_API int sgemm_q4_dequantize(const sgemm_q4* w, float* B, void* stream);
  * q - z instead, each group of a row times a power of two that is taken back with the scale:
  * a finite A gives finite sums where the definition in FP32 does, and only values below 2^-110
  * of the largest of their group may lose low bits. Sums are FP32, the scales are applied to each group's sum in FP32, and C is
- * rounded once. The order of summation depends on the sizes alone, so results are bitwise
- * reproducible. Elements of C's rows past K are not touched. C must not overlap A or w->data.
+ * rounded once. The matrix instructions align the products of 16 n to the largest |A| among
+ * them, whatever its weight: a group's sum is off by at most 2^-10 of its scale times its largest
+ * |A|, and by some 2^-16 as a rule. The order of summation depends on the sizes alone, so results
+ * are bitwise reproducible. Elements of C's rows past K are not touched. C must not overlap A or w->data.
  * One launch, no workspace; the call can be captured into a CUDA graph.
  */
 SGEMM_API int sgemm_q4_matmul(const void* A, int dtype, long long lda, int M, const sgemm_q4* w,

@@ -1,5 +1,6 @@
 """The few-row product and the expert layer on every pattern of NaN, rows of a product beside other
-rows, and reductions that are too long for the widest kernel. Bounds as in test_q4_gpu.py.
+rows, large values that meet zero weights, and reductions that are too long for the widest kernel.
+Bounds as in test_q4_gpu.py.
 """
 
 import pytest
@@ -81,6 +82,34 @@ def test_rows_do_not_depend_on_others(kind, rows):
     assert torch.equal(sg.q4_matmul(other.cuda(), W)[1], first[1])
     other[0, 5], other[rows - 1, 7] = float("inf"), float("nan")
     check(sg.q4_matmul(other.cuda(), W)[1:2], A[1:2], values, kind=kind)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("zeros", [False, True], ids=["sym", "zeros"])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("M", [1, 13])
+def test_large_values_that_meet_zero_weights(M, group, zeros, kind):
+    """S leaves them out, but the products are aligned to them: 2^-10 of the group's scale times its
+    largest |A| is added to the bound for each group, as the header states it."""
+    torch = torch_cuda()
+    N, K = 1000, 50
+    codes, scales, z, values = random_codes("zero", 1, N, K, group, zeros, False)
+    groups = -(-N // group)
+    gen = torch.Generator().manual_seed(group + M)
+    A = torch.randn(M, N, generator=gen)
+    for g in range(groups):
+        n = g * group + int(torch.randint(0, min(group, N - g * group), (1,), generator=gen))
+        codes[0, n] = z[0, g] if zeros else 8
+        values[0, n] = 0
+        A[:, n] *= 2.0 ** 13
+    A = A.to(dtypes()[kind])
+    W = sg.q4_pack(codes[0], scales[0], None if z is None else z[0], group=group)
+    ref, S = A.double() @ values[0], A.double().abs() @ values[0].abs()
+    padded = torch.nn.functional.pad(A.double().abs(), (0, groups * group - N))
+    largest = padded.view(M, groups, group).amax(-1)
+    bound = 1e-5 * S + 2.0 ** -10 * (largest @ scales[0].double().abs().cpu())
+    bound += UNIT[kind] * (ref.abs() + bound) + (2.0 ** -25 if kind == "f16" else 0)
+    assert ((sg.q4_matmul(A.cuda(), W).cpu().double() - ref).abs() <= bound).all()
 
 
 @pytest.mark.parametrize("zeros", [False, True], ids=["sym", "zeros"])
