@@ -21,8 +21,8 @@ constexpr int TILE_K = 64;
 constexpr int PITCH = TILE_K + 1;  // column and row walks of the tile are free of conflicts
 constexpr int THREADS = 256;
 
-// Quantisation: 32 n of so many columns a thread
-constexpr int Q_COLS = 1, Q_WIDTH = 32 * Q_COLS, Q_THREADS = 128, Q_CTAS = 7;
+// Quantisation: 32 n of a column a thread, 32 columns a CTA
+constexpr int Q_WIDTH = 32, Q_THREADS = 128, Q_CTAS = 7;
 
 // The nibble of a word that holds the e-th of its 8 codes.
 __device__ constexpr int nibble_of(int e) { return (e >> 1) + 4 * (e & 1); }
@@ -200,88 +200,66 @@ __global__ void __launch_bounds__(Q_THREADS, Q_CTAS)
     const int N = geom.N, K = geom.K;
     const T* mat = src + size_t(blockIdx.z) * N * K;
 
-    float v[Q_COLS][32];
+    const int k = k0 + lane;
+    float v[32];
     if constexpr (TRANSPOSED) {
         const char* begin = reinterpret_cast<const char*>(src);
-#pragma unroll
-        for (int j = 0; j < Q_COLS; ++j) {
-            const int k = k0 + lane + 32 * j;
-            load_along(mat + size_t(k) * N, n0, k < K ? N : 0, begin, begin + values * sizeof(T),
-                       v[j]);
-        }
+        load_along(mat + size_t(k) * N, n0, k < K ? N : 0, begin, begin + values * sizeof(T), v);
     } else if (n0 + 32 <= N && k0 + Q_WIDTH <= K) {
         // the CTA's corner and a 32-bit offset: one addition a load
         const T* corner = mat + size_t(blockIdx.y) * kQ4UnitN * K + k0;
         const uint32_t at = uint32_t(block * 32) * K + lane;
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-#pragma unroll
-            for (int j = 0; j < Q_COLS; ++j) v[j][i] = as_float(__ldcs(corner + (at + uint32_t(i) * K + 32 * j)));
+        for (int i = 0; i < 32; ++i) v[i] = as_float(__ldcs(corner + (at + uint32_t(i) * K)));
     } else {
 #pragma unroll
         for (int i = 0; i < 32; ++i)
-#pragma unroll
-            for (int j = 0; j < Q_COLS; ++j) {
-                const int k = k0 + lane + 32 * j;
-                v[j][i] = n0 + i < N && k < K ? as_float(mat[size_t(n0 + i) * K + k]) : 0.0f;
-            }
+            v[i] = n0 + i < N && k < K ? as_float(mat[size_t(n0 + i) * K + k]) : 0.0f;
     }
-    float lo[Q_COLS] = {}, hi[Q_COLS] = {};
+    float lo = 0.0f, hi = 0.0f;
 #pragma unroll
-    for (int j = 0; j < Q_COLS; ++j)
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            lo[j] = fminf(lo[j], v[j][i]);
-            hi[j] = fmaxf(hi[j], v[j][i]);
-        }
+    for (int i = 0; i < 32; ++i) {
+        lo = fminf(lo, v[i]);
+        hi = fmaxf(hi, v[i]);
+    }
     const int blocks = geom.group / 32, g = block / blocks;
     if (blocks > 1) {
-#pragma unroll
-        for (int j = 0; j < Q_COLS; ++j) {
-            lo_s[block][lane + 32 * j] = lo[j];
-            hi_s[block][lane + 32 * j] = hi[j];
-        }
+        lo_s[block][lane] = lo;
+        hi_s[block][lane] = hi;
         __syncthreads();
-        for (int b = g * blocks; b < (g + 1) * blocks; ++b)
-#pragma unroll
-            for (int j = 0; j < Q_COLS; ++j) {
-                lo[j] = fminf(lo[j], lo_s[b][lane + 32 * j]);
-                hi[j] = fmaxf(hi[j], hi_s[b][lane + 32 * j]);
-            }
+        for (int b = g * blocks; b < (g + 1) * blocks; ++b) {
+            lo = fminf(lo, lo_s[b][lane]);
+            hi = fmaxf(hi, hi_s[b][lane]);
+        }
     }
     uint8_t* unit = out + size_t(blockIdx.z) * geom.matrix_bytes() +
                     k0 / kQ4UnitK * geom.tile_bytes() + size_t(blockIdx.y) * geom.unit_bytes;
-#pragma unroll
-    for (int j = 0; j < Q_COLS; ++j) {
-        const int column = k0 % kQ4UnitK + lane + 32 * j;
-        float s = ZEROS ? __fsub_rn(__fdiv_rn(hi[j], 15.0f), __fdiv_rn(lo[j], 15.0f))
-                        : __fdiv_rn(fmaxf(hi[j], -lo[j]), 7.0f);
-        s = __bfloat162float(__float2bfloat16_rn(s));
-        float z = ZEROS ? 0.0f : 8.0f;
-        if (ZEROS && s > 0.0f) z = fminf(fmaxf(rintf(__fdiv_rn(-lo[j], s)), 0.0f), 15.0f);
-        if (block % blocks == 0) {
-            const int at = g * kQ4UnitK + column;
-            reinterpret_cast<uint16_t*>(unit + kQ4CodeBytes)[at] =
-                uint16_t(__float_as_uint(s) >> 16);
-            if (ZEROS)
-                unit[kQ4CodeBytes + kQ4UnitN / geom.group * kQ4UnitK * 2 + at] = uint8_t(z);
-        }
-        uint32_t word[4];
-        if (s > 0.0f) {
-            const float r = __fdiv_rn(1.0f, s);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float v8[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v8[e] = v[j][8 * i + e];
-                word[i] = quick_word<ZEROS>(v8, s, r, z);
-            }
-        } else {
-            word[0] = word[1] = word[2] = word[3] = uint32_t(z) * 0x11111111u;
-        }
-        reinterpret_cast<uint4*>(unit)[block * kQ4UnitK + column] =
-            make_uint4(word[0], word[1], word[2], word[3]);
+    const int column = k0 % kQ4UnitK + lane;
+    float s = ZEROS ? __fsub_rn(__fdiv_rn(hi, 15.0f), __fdiv_rn(lo, 15.0f))
+                    : __fdiv_rn(fmaxf(hi, -lo), 7.0f);
+    s = __bfloat162float(__float2bfloat16_rn(s));
+    float z = ZEROS ? 0.0f : 8.0f;
+    if (ZEROS && s > 0.0f) z = fminf(fmaxf(rintf(__fdiv_rn(-lo, s)), 0.0f), 15.0f);
+    if (block % blocks == 0) {
+        const int at = g * kQ4UnitK + column;
+        reinterpret_cast<uint16_t*>(unit + kQ4CodeBytes)[at] = uint16_t(__float_as_uint(s) >> 16);
+        if (ZEROS) unit[kQ4CodeBytes + kQ4UnitN / geom.group * kQ4UnitK * 2 + at] = uint8_t(z);
     }
+    uint32_t word[4];
+    if (s > 0.0f) {
+        const float r = __fdiv_rn(1.0f, s);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float v8[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v8[e] = v[8 * i + e];
+            word[i] = quick_word<ZEROS>(v8, s, r, z);
+        }
+    } else {
+        word[0] = word[1] = word[2] = word[3] = uint32_t(z) * 0x11111111u;
+    }
+    reinterpret_cast<uint4*>(unit)[block * kQ4UnitK + column] =
+        make_uint4(word[0], word[1], word[2], word[3]);
 }
 
 // Rows of 16-byte multiples are written 16 bytes at a time (VEC: a thread's four columns are
