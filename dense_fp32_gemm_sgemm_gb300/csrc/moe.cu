@@ -2,8 +2,8 @@
 // reading the weights of the experts that some token picked, once.
 //
 // moe_route_kernel: a cluster of 8 CTAs a token shares the router's rows, writes the token as
-// bfloat16 pieces (staged for the plain form of the weights and, once more, as they are for the
-// centred form), and its first CTA chooses the experts.
+// bfloat16 pieces (staged for the plain form of the weights and, once more, for the centred
+// form), and its first CTA chooses the experts.
 //
 // moe_expert_kernel: every CTA builds the same lists of the picked experts' tokens, cut into tiles
 // of so many tokens that an expert's weights are read once for each tile. Then the CTAs take work
@@ -20,17 +20,19 @@
 // HBM stays busy across items and across the waits.
 //
 // The inner product is that of q4_warp.cuh, on sets of four chunks (two strips of gate and of up, or
-// four of down), so that a column's words serve four strips (two gave 428 us instead of 338 at the
+// four of down), so that a column's words serve four strips (two gave 428 us instead of 338, with two pieces a hidden value, at the
 // largest case below). The sums of x that zero points take are kept beside the pieces, for each 32 n
 // (a group's hidden values may come from several CTAs, but 32 of them come from one). Taken by one
 // more matrix instruction on a constant operand, whose sums are truncated, they more than doubled the
 // error of float32 layers with zero points (5.8e-7 instead of 2.4e-7 of the result's norm).
 //
-// Measured, experts of 4096 x 2048, 8 of 64 picked, group 128, bfloat16: one token 43 us (its
-// weights take 15.6 at HBM's rate), 64 tokens 350 us (124). 8 experts of 512 x 512, one token: 17 us.
-// What bounds it: with few items, latencies, a third of them for instructions that come from far
-// (routing 6 us, lists 2, each phase 4 and its products); with many, the instructions of a set, some
-// 400 for one tile of columns, at 16 warps an SM.
+// Measured, experts of 4096 x 2048, 8 of 64 picked, group 128, bfloat16: one token 42 us (its
+// weights take 15.6 at HBM's rate), 64 tokens 410 us (124). 2 of 8 experts of 512 x 512, one token:
+// 17 us. What bounds it: with few items, latencies, a third of them for instructions that come from
+// far (routing 6 us, lists 2, each phase 4 and its products); with many, the instructions of a set,
+// some 400 for one tile of columns, at 16 warps an SM, and in the second product of tiles of more
+// than four tokens the matrix instructions, 96 a set at two cycles. A token whose input the centred
+// form takes costs more: 79 us instead of 42 for the one token, 580 instead of 410 for one of 64.
 #include <cmath>
 #include <type_traits>
 

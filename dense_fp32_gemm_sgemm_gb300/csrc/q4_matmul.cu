@@ -1,4 +1,9 @@
 // The few-row product with 4-bit weights: checks, and the choice of its kernel.
+//
+// Where a row wants the centred form of the weights (q4.cuh), the CTAs that meet its value stage
+// their columns again and convert. One such value in a row, against none: 1 x 8192 by 8192, bfloat16,
+// 19.7 us against 10.8; 1 x 6144 by 4096, float32, 11.4 against 7.4; 16 x 8192 by 6144, bfloat16, 26.4
+// against 18.3; 64 x 8192 by 65536 274 against 217.
 #include "q4_stage.cuh"
 
 using namespace sgemm;

@@ -5,7 +5,7 @@ the limits are those of the ``sgemm_q4_*`` and ``sgemm_moe`` entry points in the
 
     W = sg.q4_quantize(B, group=128)          # B: N x K (or E x N x K), any float type
     C = sg.q4_matmul(A, W)                    # A: M x N, a few rows; C has A's type
-    C = sg.matmul(A, sg.q4_dequantize(W))     # many rows: dequantise once, FP32 product
+    C = sg.matmul(A, sg.q4_dequantize(W))     # many float32 rows, N and K up to 8192
     layer = sg.MoeLayer(router, gate, up, down, top_k=2)
     y, ids, weights = layer(x)                # x: T x D, at most 64 tokens
 """
