@@ -87,6 +87,20 @@ def test_f32_magnitudes_that_change_along_a_row(M, group):
     check(sg.q4_matmul(A.cuda(), W), A, values)
 
 
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("group", GROUPS)
+@pytest.mark.parametrize("M", [2, 11, 40])
+def test_finite_special_values_beside_ordinary_rows(M, group, kind):
+    """Values outside the plain form's range in some rows, at both ends of n."""
+    torch = torch_cuda()
+    N, K = 700, 50
+    W, values = one("beside", N, K, group, True, [1.0] * -(-N // group))
+    A = torch.randn(M, N, generator=torch.Generator().manual_seed(M + group)).to(dtypes()[kind])
+    A[1, 3], A[1, N - 1] = 1e-25, 2.0 ** 26
+    A[M - 1, 350] = -(2.0 ** 24)
+    check(sg.q4_matmul(A.cuda(), W), A, values, kind)
+
+
 def layer_case(T, kind, group, zeros, e_in, e_down, key):
     """A case whose gate and up scales are times 2^e_in, its down scales times 2^e_down; the routing
     does not depend on the tokens."""
