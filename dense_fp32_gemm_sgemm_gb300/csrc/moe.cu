@@ -20,8 +20,8 @@
 // HBM stays busy across items and across the waits.
 //
 // The inner product is that of q4_warp.cuh, on sets of four chunks (two strips of gate and of up, or
-// four of down), so that a column's words serve four strips (two gave 428 us instead of 338, with two pieces a hidden value, at the
-// largest case below). The sums of x that zero points take are kept beside the pieces, for each 32 n
+// four of down), so that a column's words serve four strips (at the largest case below two gave 428 us
+// instead of 338, with two pieces a hidden value). The sums of x that zero points take are kept beside the pieces, for each 32 n
 // (a group's hidden values may come from several CTAs, but 32 of them come from one). Taken by one
 // more matrix instruction on a constant operand, whose sums are truncated, they more than doubled the
 // error of float32 layers with zero points (5.8e-7 instead of 2.4e-7 of the result's norm).

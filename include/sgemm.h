@@ -381,10 +381,10 @@ SGEMM_API int sgemm_q4_dequantize(const sgemm_q4* w, float* B, void* stream);
 /*
  * sgemm_q4_matmul - C[M x K] = A[M x N] . B with the 4-bit B of *w (count 1), for few rows:
  * the cost is reading B's codes once for every 32 columns (a row of A is one, two or, float32,
- * four of them). At 8192 x 8192, sgemm_q4_dequantize with solve_ex takes as long as 130 float32 or
- * some 650 16-bit rows here, and less from there on. A and C are device arrays of element type `dtype`
- * (SGEMM_FLOAT32, SGEMM_BFLOAT16 or SGEMM_FLOAT16), row-major with row pitches lda >= N
- * and ldc >= K in elements. 0 <= M <= 65536; M = 0 enqueues nothing.
+ * four of them). At 8192 x 8192, sgemm_q4_dequantize with solve_ex takes as long as 130 float32
+ * or some 650 16-bit rows here, and less from there on. A and C are device arrays of element
+ * type `dtype` (SGEMM_FLOAT32, SGEMM_BFLOAT16 or SGEMM_FLOAT16), row-major with row pitches
+ * lda >= N and ldc >= K in elements. 0 <= M <= 65536; M = 0 enqueues nothing.
  *
  * Neither A nor the weights are rounded: A is multiplied as one, two or three bfloat16
  * pieces (bfloat16, float16, float32) whose sum it is, the weights as the integers q, and
@@ -392,11 +392,13 @@ SGEMM_API int sgemm_q4_dequantize(const sgemm_q4* w, float* B, void* stream);
  * outside [2^-64, 2^24), the rows that are staged with it are multiplied by the integers
  * q - z instead, each group of a row times a power of two that is taken back with the scale:
  * a finite A gives finite sums where the definition in FP32 does, and only values below 2^-110
- * of the largest of their group may lose low bits. Sums are FP32, the scales are applied to each group's sum in FP32, and C is
- * rounded once. The matrix instructions align the products of 16 n to the largest |A| among
- * them, whatever its weight: a group's sum is off by at most 2^-10 of its scale times its largest
- * |A|, and by some 2^-16 as a rule. The order of summation depends on the sizes alone, so results
- * are bitwise reproducible. Elements of C's rows past K are not touched. C must not overlap A or w->data.
+ * of the largest of their group may lose low bits.
+ *
+ * Sums are FP32, the scales are applied to each group's sum in FP32, and C is rounded once. The
+ * matrix instructions align the products of 16 n to the largest |A| among them, whatever its
+ * weight: a group's sum is off by at most 2^-10 of its scale times its largest |A|, and by some
+ * 2^-16 as a rule. The order of summation depends on the sizes alone, so results are bitwise
+ * reproducible. Elements of C's rows past K are not touched. C must not overlap A or w->data.
  * One launch, no workspace; the call can be captured into a CUDA graph.
  */
 SGEMM_API int sgemm_q4_matmul(const void* A, int dtype, long long lda, int M, const sgemm_q4* w,
@@ -441,9 +443,10 @@ typedef struct sgemm_moe_layer {
  * 0 <= T <= 64 (T = 0 enqueues nothing), 1 <= D, F <= 16384, 1 <= E <= 256,
  * 1 <= top_k <= min(E, 16); gate and up have the same group and flags. Arithmetic as for
  * sgemm_q4_matmul; the hidden values are kept in FP32 and multiplied as three bfloat16
- * pieces (all 24 significant bits), whatever the type. Results are bitwise reproducible, and a token's do not depend on the other tokens, as long as T is the same
- * (T decides how sums are split). An expert that live tokens picked is read once for every
- * 8 of them (for every 2 where T * top_k <= 3 E), the others not at all. y, ids and weights must not overlap the
+ * pieces (all 24 significant bits), whatever the type. Results are bitwise reproducible, and
+ * a token's do not depend on the other tokens, as long as T is the same (T decides how sums
+ * are split). An expert that live tokens picked is read once for every 8 of them (for every 2
+ * where T * top_k <= 3 E), the others not at all. y, ids and weights must not overlap the
  * inputs or each other. Two launches; workspace comes from the library's pool; the call can
  * be captured into a CUDA graph.
  */
