@@ -10,6 +10,8 @@ missing, every call raises; there is no CPU fallback.
     C = sg.matmul(A, B, mode=sg.MODE_TF32)   # explicit 1xTF32
     C = sg.matmul(A, B, mode="3xfp16")       # scaled FP16 pieces (bound in the C header)
     W = sg.q4_quantize(B); C = sg.q4_matmul(A[:4].contiguous(), W)  # 4-bit weights (q4.py)
+    loss, losses, lse, dx, dw = sg.cross_entropy_grad(x, weight, target)  # (training.py)
+    update = sg.orthogonalize(gradient)
 """
 
 from __future__ import annotations
@@ -56,6 +58,9 @@ PROBE_F16_MMA = 3
 # the 4-bit operators live in q4.py, which needs torch; it is loaded at the first use of one
 _Q4_NAMES = ("Q4Matrix", "MoeLayer", "q4_quantize", "q4_pack", "q4_dequantize", "q4_matmul",
              "Q4_ZEROS", "Q4_SCALE_FP16", "MOE_MAX_TOKENS")
+# and the training operators in training.py
+_TRAINING_NAMES = ("CrossEntropy", "CrossEntropyGrad", "cross_entropy", "cross_entropy_grad",
+                   "orthogonalize", "ORTHOGONALIZE_COEFFICIENTS")
 
 _lock = threading.Lock()
 _lib = None
@@ -66,6 +71,11 @@ def __getattr__(name: str):
         from . import q4
         for n in _Q4_NAMES:
             globals()[n] = getattr(q4, n)
+        return globals()[name]
+    if name in _TRAINING_NAMES:
+        from . import training
+        for n in _TRAINING_NAMES:
+            globals()[n] = getattr(training, n)
         return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
@@ -143,6 +153,11 @@ def lib() -> ctypes.CDLL:
             L.sgemm_q4_matmul.restype = i
             L.sgemm_moe.argtypes = [vp, vp, ll, i, vp, vp, ll, vp, vp, vp]
             L.sgemm_moe.restype = i
+            L.sgemm_cross_entropy.argtypes = [vp, vp]
+            L.sgemm_cross_entropy.restype = i
+            L.sgemm_orthogonalize.argtypes = [vp, i, i, i, i, ll, ll, vp, ll, ll, i, vp,
+                                              ctypes.c_float, vp]
+            L.sgemm_orthogonalize.restype = i
             _lib = L
     return _lib
 

@@ -1,0 +1,573 @@
+// Matrix products of 16-bit operands on the tensor cores, with a fused epilogue: the core of
+// the cross entropy (cross_entropy.cu) and of the Newton-Schulz products (orthogonalize.cu).
+//
+// D[M x N] = sum over k of A[m][k] * B[k][n]; either operand may be stored with k or with its
+// other index contiguous, as one or more planes (pieces of a longer type) whose products are
+// added up in one accumulation. A pair of CTAs computes a tile of 256 x BN with
+// tcgen05.mma.cta_group::2; each CTA stages its 128 rows of A and its half of B's columns.
+//
+// Roles in a CTA: warp 0 issues the TMA loads (and, in the pair's first CTA, hands out units
+// of work), warp 1 of the first CTA issues the MMAs, warps 4-11 run the epilogue.
+//
+// Accumulation. The tensor core cuts off, rather than rounds, the bits that an addition to its
+// FP32 accumulator shifts out: some 2^-25 of the accumulator for each MMA, always towards zero.
+// After SEG_STEPS stages (32 MMAs, at most 2^-20 of a sum's size) the accumulator is therefore
+// added to FP32 registers, rounded to nearest, and starts again at zero. The two accumulators
+// of a CTA pair alternate, so the additions overlap the next stages' MMAs; 32 MMAs of 256 x 256
+// take 4096 cycles, the additions some 500.
+//
+// Units are claimed from a counter, so that long and short ones may be mixed in a launch. Which
+// pair computes a unit does not change what is computed.
+#pragma once
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "internal.cuh"
+#include "ptx.cuh"
+#include "wait.cuh"
+
+namespace sgemm {
+namespace hg {
+
+constexpr int BM = 256;       // rows of a tile (both CTAs)
+constexpr int HALF_M = 128;   // rows of one CTA
+constexpr int BK = 64;        // reduction elements in a stage: 128 bytes
+constexpr int STAGES = 6;
+constexpr int SEG_STEPS = 8;  // stages in an accumulator segment
+constexpr int SLOTS = 4;      // units handed out ahead
+constexpr int EPI_WARPS = 8;
+constexpr int EPI_WARP0 = 4;  // warps 2 and 3 only fill up the first warpgroup
+constexpr int THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
+// Registers: 168 a thread at launch (384 threads); the first warpgroup gives most of its own to
+// the epilogue's, whose threads hold 128 sums. 56 + 224 + 224 = 3 * 168.
+constexpr int REGS_FEW = 56;
+constexpr int REGS_MANY = 224;
+constexpr int A_BYTES = HALF_M * BK * 2;
+constexpr int CHUNK_BYTES = 64 * BK * 2;  // 64 elements of the other index by 64 of k
+constexpr int STAGING = 4096;             // bytes of one epilogue warp's staging block
+constexpr int NUM_BARS = 2 * STAGES + 4 + 1 + 2 * SLOTS;
+constexpr int MAX_PRODUCTS = 6;
+
+template <int BN>
+constexpr int B_BYTES = BN / 2 * BK * 2;
+template <int BN>
+constexpr int STAGE_BYTES = A_BYTES + B_BYTES<BN>;
+template <int BN>
+constexpr int SMEM_BYTES = STAGES * STAGE_BYTES<BN> + EPI_WARPS * STAGING + 512 + 1024;
+static_assert(SMEM_BYTES<256> <= 232448, "shared memory of an SM");
+
+// One product of a launch. Sizes are in elements; `live` may replace one of them on the device.
+struct Problem {
+    int M, N, K;
+    int batch;          // independent products, the maps' outermost coordinate / planes
+    int dyn;            // 0: as given; 1: M, 2: K is the number of live rows
+    int splits;         // parts of the reduction, each a unit
+    int group;          // tile rows that are worked through column by column
+    int symmetric;      // only tiles that reach the diagonal or lie below it (M == N)
+    int a_mn, b_mn;     // operand stored with its other index contiguous (else with k)
+    int a_row, b_row;   // added to the row coordinate (k or the other index, whichever is a row)
+    int planes_a, planes_b;
+    int products;       // pairs of planes, smallest products first
+    unsigned char pa[MAX_PRODUCTS], pb[MAX_PRODUCTS];
+    unsigned idesc;     // instruction descriptor without N
+};
+
+struct Args {
+    CUtensorMap a[2], b[2];  // 3-D: contiguous index, row, batch * planes + plane
+    Problem p[2];
+    int problems;
+    const int* live;  // number of rows in all, or null
+    int live0;        // rows before this launch's
+    int live_max;     // rows of this launch at most
+    int* counter;     // claimed units, zero before the launch
+    int* err;
+};
+
+// A unit of work.
+struct Unit {
+    int problem, batch, split;
+    int row0, col0;  // of the tile
+    int kb0, kb1;    // blocks of the reduction
+};
+
+__host__ __device__ inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// Tiles of a product of `tiles_m` tile rows; with `symmetric` tile row r has the tiles that
+// begin at or before its last row.
+template <int BN>
+__host__ __device__ inline int tile_count(const Problem& p, int tiles_m, int tiles_n) {
+    if (!p.symmetric) return tiles_m * tiles_n;
+    constexpr int R = BM / BN;
+    return R * (tiles_m - 1) * tiles_m / 2 + (tiles_m * R < tiles_n ? tiles_m * R : tiles_n);
+}
+
+template <int BN>
+__host__ __device__ inline int unit_count(const Problem& p, int live) {
+    const int m = p.dyn == 1 ? live : p.M;
+    if (m <= 0) return 0;
+    return p.batch * p.splits * tile_count<BN>(p, ceil_div(m, BM), ceil_div(p.N, BN));
+}
+
+// Unit u of the launch; u counts over all its problems.
+template <int BN>
+__device__ inline Unit unit_at(const Args& g, int u, int live) {
+    Unit t;
+    t.problem = 0;
+    if (g.problems > 1) {
+        const int first = unit_count<BN>(g.p[0], live);
+        if (u >= first) {
+            t.problem = 1;
+            u -= first;
+        }
+    }
+    const Problem& p = g.p[t.problem];
+    const int tiles_m = ceil_div(p.dyn == 1 ? live : p.M, BM), tiles_n = ceil_div(p.N, BN);
+    const int tiles = tile_count<BN>(p, tiles_m, tiles_n);
+    const int each = tiles * p.splits;
+    t.batch = u / each;
+    u -= t.batch * each;
+    t.split = u / tiles;
+    u -= t.split * tiles;
+    int tm, tn;
+    if (p.symmetric) {
+        constexpr int R = BM / BN;
+        tm = 0;
+        while (tm + 1 < tiles_m && u >= (tm + 1) * R) u -= ++tm * R;
+        tn = u;
+    } else {
+        const int grouped = p.group * tiles_n;
+        const int gi = u / grouped;
+        const int rows = min(p.group, tiles_m - gi * p.group);
+        u -= gi * grouped;
+        tm = gi * p.group + u % rows;
+        tn = u / rows;
+    }
+    t.row0 = tm * BM;
+    t.col0 = tn * BN;
+    const int kblocks = ceil_div(p.dyn == 2 ? live : p.K, BK);
+    const int each_k = ceil_div(kblocks, p.splits);
+    t.kb0 = min(t.split * each_k, kblocks);
+    t.kb1 = min(t.kb0 + each_k, kblocks);
+    return t;
+}
+
+// Instruction descriptor of kind::f16 without its N: FP32 accumulator, M = 256, operand types
+// FP16 (0) or bfloat16 (1), and the operands' major indices.
+inline unsigned instruction(bool bf16, bool a_mn, bool b_mn) {
+    const unsigned type = bf16 ? 1u : 0u;
+    return (1u << 4) | (type << 7) | (type << 10) | (unsigned(a_mn) << 15) |
+           (unsigned(b_mn) << 16) | (unsigned(BM >> 4) << 24);
+}
+
+// ---- shared memory --------------------------------------------------------------------
+// The same offsets in both CTAs. full, acc_empty, slot_empty, drain: used in the first CTA.
+struct Smem {
+    uint32_t ring, bar0, slots;
+    uint8_t* staging;
+    volatile int* slot_ptr;
+    uint32_t* tmem_slot;
+    volatile int* abort_flag;
+    __device__ uint32_t full(int s) const { return bar0 + 8u * s; }
+    __device__ uint32_t empty(int s) const { return bar0 + 8u * (STAGES + s); }
+    __device__ uint32_t acc_full(int b) const { return bar0 + 8u * (2 * STAGES + b); }
+    __device__ uint32_t acc_empty(int b) const { return bar0 + 8u * (2 * STAGES + 2 + b); }
+    __device__ uint32_t slot_full(int i) const { return bar0 + 8u * (2 * STAGES + 4 + i); }
+    __device__ uint32_t slot_empty(int i) const {
+        return bar0 + 8u * (2 * STAGES + 4 + SLOTS + i);
+    }
+    __device__ uint32_t drain() const { return bar0 + 8u * (2 * STAGES + 4 + 2 * SLOTS); }
+};
+
+template <int BN>
+__device__ __forceinline__ Smem carve(uint8_t* raw) {
+    uint8_t* base =
+        reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    Smem s;
+    s.ring = ptx::smem_u32(base);
+    s.staging = base + STAGES * STAGE_BYTES<BN>;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(s.staging + EPI_WARPS * STAGING);
+    s.bar0 = ptx::smem_u32(bars);
+    int* words = reinterpret_cast<int*>(bars + NUM_BARS);
+    s.slots = ptx::smem_u32(words);
+    s.slot_ptr = words;
+    s.tmem_slot = reinterpret_cast<uint32_t*>(words + SLOTS);
+    s.abort_flag = words + SLOTS + 1;
+    return s;
+}
+
+__device__ __forceinline__ bool wait_c(uint32_t bar, uint32_t parity, const Smem& sm, int* err) {
+    return wait_phase(bar, parity, sm.abort_flag, err, WAIT_LIMIT_NS, true);
+}
+
+// ---- operands in shared memory ----------------------------------------------------------
+// k contiguous: rows of 128 bytes (64 k), 8-row groups 1024 bytes apart; 16 k are 32 bytes.
+// Other index contiguous: chunks of 64 of it, 8192 bytes apart (the leading offset), each with
+// one 128-byte row for every k, 8 k 1024 bytes apart; 16 k are 2048 bytes. Both 128-byte
+// swizzled, as TMA writes them.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t saddr, bool mn, int k16) {
+    const uint32_t at = saddr + uint32_t(k16) * (mn ? 2048u : 32u);
+    uint64_t d = uint64_t((at >> 4) & 0x3FFFu);
+    d |= uint64_t(mn ? CHUNK_BYTES >> 4 : 1) << 16;
+    d |= uint64_t(1024 >> 4) << 32;
+    d |= uint64_t(1) << 46;
+    d |= uint64_t(2) << 61;
+    return d;
+}
+
+// ---- staging ------------------------------------------------------------------------------
+// A warp's 4 KiB block holds 32 rows of 128 bytes, 16-byte piece c of row r at c ^ (r % 8): both
+// a lane's own row and four whole rows at a time are free of bank conflicts.
+__device__ __forceinline__ uint4* staged(uint8_t* block, int row, int piece) {
+    return reinterpret_cast<uint4*>(block + row * 128 + ((piece ^ (row & 7)) << 4));
+}
+
+// Writes the staged block to global memory, 16 bytes a lane and four rows at a time. `row_at(r)`
+// gives the address of the block's row r, or null where there is none; `bytes` of a row count
+// (at most 128); `wide`: the addresses are 16-byte aligned, else elements of SIZE bytes are
+// stored.
+template <int SIZE, class RowAt>
+__device__ __forceinline__ void store_block(uint8_t* block, int bytes, bool wide, RowAt row_at) {
+    const int lane = threadIdx.x & 31, piece = lane & 7;
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = i * 4 + (lane >> 3);
+        char* to = reinterpret_cast<char*>(row_at(r));
+        if (to == nullptr || piece * 16 >= bytes) continue;
+        const uint4 v = *staged(block, r, piece);
+        if (wide && piece * 16 + 16 <= bytes) {
+            *reinterpret_cast<uint4*>(to + piece * 16) = v;
+        } else if (SIZE == 4) {
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (piece * 16 + j * 4 < bytes) reinterpret_cast<uint32_t*>(to)[piece * 4 + j] = w[j];
+        } else {
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (piece * 16 + j * 2 < bytes)
+                    reinterpret_cast<unsigned short*>(to)[piece * 8 + j] =
+                        static_cast<unsigned short>(w[j >> 1] >> (16 * (j & 1)));
+        }
+    }
+    __syncwarp();
+}
+
+// Two values as one word of bfloat16 or FP16, rounded to nearest.
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    if constexpr (BF16) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&v);
+    } else {
+        const __half2 v = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&v);
+    }
+}
+
+// ---- the kernel -----------------------------------------------------------------------------
+// EPI::BN, EPI::Params, and EPI(params, args, live, staging block) with
+//   void unit(const Unit&, int row (of the tile's first in this warp), int col, float (&acc)[BN / 2])
+// called by each epilogue warp once a unit: lane l holds row `row` + l, columns col .. col + BN / 2.
+template <class EPI>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+    half_gemm_kernel(const __grid_constant__ Args g, const __grid_constant__ typename EPI::Params ep) {
+    constexpr int BN = EPI::BN;
+    constexpr int COLS = BN / 2;  // columns of an epilogue warp
+    extern __shared__ uint8_t smem_raw[];
+    const Smem sm = carve<BN>(smem_raw);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = ptx::cluster_ctarank();
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            ptx::mbar_init(sm.full(s), 1);
+            ptx::mbar_init(sm.empty(s), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            ptx::mbar_init(sm.acc_full(b), 1);
+            ptx::mbar_init(sm.acc_empty(b), 2 * EPI_WARPS);
+        }
+        for (int i = 0; i < SLOTS; ++i) {
+            ptx::mbar_init(sm.slot_full(i), 1);
+            // the first CTA's MMA warp, the second's TMA warp, all epilogue warps
+            ptx::mbar_init(sm.slot_empty(i), 2 + 2 * EPI_WARPS);
+        }
+        ptx::mbar_init(sm.drain(), 1);
+        *sm.abort_flag = 0;
+        ptx::fence_mbar_init();
+        for (int i = 0; i < g.problems; ++i) {
+            ptx::prefetch_tensormap(&g.a[i]);
+            ptx::prefetch_tensormap(&g.b[i]);
+        }
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc_pair(ptx::smem_u32(sm.tmem_slot), 2 * BN);
+        ptx::tmem_relinquish_pair();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::cluster_sync();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *sm.tmem_slot;
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+
+    int live = 0;
+    if (g.live) live = min(max(*g.live - g.live0, 0), g.live_max);
+    // the unit in slot i, or -1 at the end or when a wait ran out
+    auto take = [&](int i) {
+        const int s = i % SLOTS;
+        if (!wait_c(sm.slot_full(s), (i / SLOTS) & 1, sm, g.err)) return -1;
+        return sm.slot_ptr[s];
+    };
+    auto taken = [&](int i) {
+        ptx::mbar_arrive_cluster(ptx::mapa_shared(sm.slot_empty(i % SLOTS), 0));
+    };
+
+    if (warp < EPI_WARP0) {
+      ptx::regs_give_up<REGS_FEW>();
+      if (warp == 0) {
+        if (lane == 0) {
+            int units = unit_count<BN>(g.p[0], live);
+            if (g.problems > 1) units += unit_count<BN>(g.p[1], live);
+            const int pairs = gridDim.x >> 1;
+            int next = blockIdx.x >> 1;
+            int s = 0;
+            uint32_t ph = 0;
+            for (int i = 0;; ++i) {
+                int u;
+                if (rank == 0) {
+                    u = next < units ? next : -1;
+                    if (u >= 0) next = pairs + atomicAdd(g.counter, 1);  // back by the next turn
+                    const int slot = i % SLOTS;
+                    if (!wait_c(sm.slot_empty(slot), ((i / SLOTS) & 1) ^ 1, sm, g.err)) u = -1;
+                    sm.slot_ptr[slot] = u;
+                    ptx::st_shared_cluster_f32(ptx::mapa_shared(sm.slots + 4u * slot, 1),
+                                               __int_as_float(u));
+                    ptx::mbar_arrive_cluster(ptx::mapa_shared(sm.slot_full(slot), 0));
+                    ptx::mbar_arrive_cluster(ptx::mapa_shared(sm.slot_full(slot), 1));
+                } else {
+                    u = take(i);
+                    if (u >= 0) taken(i);
+                }
+                if (u < 0) break;
+                const Unit t = unit_at<BN>(g, u, live);
+                const Problem& p = g.p[t.problem];
+                const CUtensorMap* ma = &g.a[t.problem];
+                const CUtensorMap* mb = &g.b[t.problem];
+                const int m0 = t.row0 + int(rank) * HALF_M;
+                const int n0 = t.col0 + int(rank) * (BN / 2);
+                bool ok = true;
+                for (int kb = t.kb0; ok && kb < t.kb1; ++kb) {
+                    const int k0 = kb * BK;
+                    for (int q = 0; q < p.products; ++q) {
+                        if (!wait_c(sm.empty(s), ph ^ 1u, sm, g.err)) {
+                            ok = false;
+                            break;
+                        }
+                        const uint32_t bar = ptx::mapa_shared(sm.full(s), 0);
+                        const uint32_t st = sm.ring + uint32_t(s) * STAGE_BYTES<BN>;
+                        if (rank == 0) ptx::mbar_arrive_expect_tx(sm.full(s), 2 * STAGE_BYTES<BN>);
+                        const int za = t.batch * p.planes_a + p.pa[q];
+                        const int zb = t.batch * p.planes_b + p.pb[q];
+                        if (p.a_mn) {
+                            ptx::tma_load_3d_pair(st, ma, bar, m0, p.a_row + k0, za);
+                            ptx::tma_load_3d_pair(st + CHUNK_BYTES, ma, bar, m0 + 64, p.a_row + k0,
+                                                  za);
+                        } else {
+                            ptx::tma_load_3d_pair(st, ma, bar, k0, p.a_row + m0, za);
+                        }
+                        const uint32_t sb = st + A_BYTES;
+                        if (p.b_mn) {
+                            ptx::tma_load_3d_pair(sb, mb, bar, n0, p.b_row + k0, zb);
+                            if (BN == 256)
+                                ptx::tma_load_3d_pair(sb + CHUNK_BYTES, mb, bar, n0 + 64,
+                                                      p.b_row + k0, zb);
+                        } else {
+                            ptx::tma_load_3d_pair(sb, mb, bar, k0, p.b_row + n0, zb);
+                        }
+                        if (++s == STAGES) {
+                            s = 0;
+                            ph ^= 1u;
+                        }
+                    }
+                }
+                if (!ok) {
+                    if (rank != 0) break;
+                    next = units;  // the others are told that there is nothing more
+                }
+            }
+            if (*sm.abort_flag) {  // copies in flight arrive before shared memory is given up
+                const unsigned long long t0 = ptx::globaltimer_ns();
+                while (ptx::globaltimer_ns() - t0 < 10000000ull) {
+                }
+            }
+        }
+      } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            int s = 0, seg = 0;
+            uint32_t ph = 0;
+            bool ok = true, issued = false;
+            for (int i = 0; ok; ++i) {
+                const int u = take(i);
+                if (u < 0) break;
+                taken(i);
+                const Unit t = unit_at<BN>(g, u, live);
+                const Problem& p = g.p[t.problem];
+                const uint32_t idesc = p.idesc | (uint32_t(BN >> 3) << 17);
+                const bool a_mn = p.a_mn, b_mn = p.b_mn;
+                int left = (t.kb1 - t.kb0) * p.products;
+                for (; ok && left > 0; left -= SEG_STEPS, ++seg) {
+                    const int b = seg & 1;
+                    if (!wait_c(sm.acc_empty(b), ((seg >> 1) & 1) ^ 1, sm, g.err)) {
+                        ok = false;
+                        break;
+                    }
+                    ptx::tc_fence_after();
+                    const uint32_t d = tmem + uint32_t(b * BN);
+                    const int steps = min(left, SEG_STEPS);
+                    for (int j = 0; j < steps; ++j) {
+                        if (!wait_c(sm.full(s), ph, sm, g.err)) {
+                            ok = false;
+                            break;
+                        }
+                        ptx::tc_fence_after();
+                        const uint32_t st = sm.ring + uint32_t(s) * STAGE_BYTES<BN>;
+#pragma unroll
+                        for (int k = 0; k < BK / 16; ++k)
+                            ptx::mma_pair<true>(d, operand_desc(st, a_mn, k),
+                                                operand_desc(st + A_BYTES, b_mn, k), idesc,
+                                                (j | k) ? 1u : 0u);
+                        issued = true;
+                        ptx::mma_commit_pair(sm.empty(s), 0x3);
+                        if (++s == STAGES) {
+                            s = 0;
+                            ph ^= 1u;
+                        }
+                    }
+                    if (!ok) break;
+                    ptx::mma_commit_pair(sm.acc_full(b), 0x3);
+                }
+            }
+            if (*sm.abort_flag && issued) {  // MMAs in flight end before TMEM is freed
+                ptx::mma_commit_pair(sm.drain(), 0x1);
+                const unsigned long long t0 = ptx::globaltimer_ns();
+                while (!ptx::mbar_try_wait(sm.drain(), 0) &&
+                       ptx::globaltimer_ns() - t0 < WAIT_LIMIT_NS) {
+                }
+            }
+        }
+      }
+    } else {
+        ptx::regs_take<REGS_MANY>();
+        // warp w reads TMEM lanes [32 (w % 4), +32) and the first or second half of the columns
+        const int q = warp & 3, h = (warp - EPI_WARP0) >> 2;
+        EPI epi(ep, g, live, sm.staging + (warp - EPI_WARP0) * STAGING);
+        float acc[COLS];
+        int seg = 0;
+        bool ok = true;
+        for (int i = 0; ok; ++i) {
+            const int u = take(i);
+            if (u < 0) break;
+            __syncwarp();
+            if (lane == 0) taken(i);
+            const Unit t = unit_at<BN>(g, u, live);
+            const int steps = (t.kb1 - t.kb0) * g.p[t.problem].products;
+            const int segs = (steps + SEG_STEPS - 1) / SEG_STEPS;
+            for (int sg = 0; sg < segs; ++sg, ++seg) {
+                const int b = seg & 1;
+                if (!wait_c(sm.acc_full(b), (seg >> 1) & 1, sm, g.err)) {
+                    ok = false;
+                    break;
+                }
+                ptx::tc_fence_after();
+                const uint32_t at = tmem + (uint32_t(q * 32) << 16) + uint32_t(b * BN + h * COLS);
+                if (sg == 0) {
+#pragma unroll
+                    for (int c = 0; c < COLS; c += 64) {
+                        uint32_t r[64];
+                        __syncwarp();
+                        ptx::tmem_ld_64(at + c, r);
+#pragma unroll
+                        for (int j = 0; j < 64; ++j) acc[c + j] = __uint_as_float(r[j]);
+                    }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < COLS; c += 16) {
+                        uint32_t r[16];
+                        __syncwarp();
+                        ptx::tmem_ld_16(at + c, r);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) acc[c + j] += __uint_as_float(r[j]);
+                    }
+                }
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(sm.acc_empty(b), 0));
+            }
+            if (!ok) break;
+            if (segs == 0) {
+#pragma unroll
+                for (int j = 0; j < COLS; ++j) acc[j] = 0.f;
+            }
+            epi.unit(t, t.row0 + int(rank) * HALF_M + q * 32, t.col0 + h * COLS, acc);
+        }
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::cluster_sync();
+    if (warp == 1) {
+        __syncwarp();
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc_pair(tmem, 2 * BN);
+    }
+}
+
+// ---- host -------------------------------------------------------------------------------------
+// A 3-D map over 16-bit elements: `inner` contiguous elements, `rows` of pitch `ld` elements (a
+// multiple of 8), `slabs` of `slab` elements apart; boxes of 64 x box_rows. Zeros are read outside.
+bool encode_operand(CUtensorMap* map, const void* base, bool bf16, long long inner, long long rows,
+                    long long ld, long long slabs, long long slab, int box_rows);
+
+// Launches `kernel`, allowed to start while the kernel before it on the stream ends (it waits
+// for that one by griddepcontrol.wait).
+template <typename... KArgs, typename... Args>
+cudaError_t launch(void (*kernel)(KArgs...), unsigned grid, unsigned block, size_t smem,
+                   cudaStream_t stream, const Args&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+    count_launch();
+    return e;
+}
+
+// Box rows of an operand: 64 k of a chunk, or its rows in a CTA.
+inline int box_rows(bool mn, int rows_of_cta) { return mn ? BK : rows_of_cta; }
+
+template <class EPI>
+cudaError_t launch_gemm(const Args& g, const typename EPI::Params& ep, int sm_count,
+                        cudaStream_t stream) {
+    constexpr int bytes = SMEM_BYTES<EPI::BN>;
+    cudaError_t e = set_smem_limit_once<half_gemm_kernel<EPI>>(bytes);
+    if (e != cudaSuccess) return e;
+    int units = 0;
+    for (int i = 0; i < g.problems; ++i) units += unit_count<EPI::BN>(g.p[i], g.live_max);
+    if (units == 0) return cudaSuccess;
+    const int pairs = sm_count / 2 > 0 ? sm_count / 2 : 1;
+    return launch(half_gemm_kernel<EPI>, 2u * unsigned(units < pairs ? units : pairs), THREADS,
+                  bytes, stream, g, ep);
+}
+
+}  // namespace hg
+}  // namespace sgemm

@@ -217,6 +217,16 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void* tmap,
         "l"(tmap), "r"(bar_cluster), "r"(c0), "r"(c1)
         : "memory");
 }
+// The same for a 3-D tensor map.
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const void* tmap,
+                                                 uint32_t bar_cluster, int32_t c0, int32_t c1,
+                                                 int32_t c2) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];\n" ::"r"(dst),
+        "l"(tmap), "r"(bar_cluster), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
 // Tensor-memory allocation shared by the CTA pair: one warp of EACH CTA executes it;
 // both receive the same base address.
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t dst_smem, uint32_t ncols) {
@@ -272,6 +282,17 @@ __device__ __forceinline__ void mma_commit_pair(uint32_t bar, uint16_t mask) {
         " [%0], %1;\n" ::"r"(bar),
         "h"(mask)
         : "memory");
+}
+
+// Registers of the calling warpgroup's threads from here on (all of its warps call it): fewer
+// than at the launch, or more, out of those that the block's other warpgroups gave up.
+template <int N>
+__device__ __forceinline__ void regs_give_up() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_take() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
 }
 
 // ---------------------------------------------------------------- single-CTA tcgen05 ------

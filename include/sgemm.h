@@ -454,6 +454,93 @@ SGEMM_API int sgemm_moe(const sgemm_moe_layer* layer, const void* x, long long l
                         const unsigned char* live, void* y, long long ldy, int* ids,
                         float* weights, void* stream);
 
+/* ==== training: the loss of an output head ============================================
+ *
+ * sgemm_ce describes one call; the struct is read during the call only. x holds T tokens'
+ * hidden states, weight the output head's V rows, target each token's row of it. All arrays
+ * are device arrays; rows have a pitch in elements and no alignment is required beyond the
+ * element type's (weights of 16 bits with 16-byte aligned rows are read in place, others are
+ * copied first).
+ */
+typedef struct sgemm_ce {
+    const void* x; /* T x D, row pitch ldx >= D */
+    long long ldx;
+    const void* weight; /* V x D, row pitch ldw >= D */
+    long long ldw;
+    const void* target; /* T integers */
+    int target_bits;    /* 32 or 64: their size */
+    int dtype;          /* of x, weight, dx, dweight: SGEMM_FLOAT32, _BFLOAT16 or _FLOAT16 */
+    int T;
+    int D;
+    int V;
+    const float* token_weights; /* T floats c, or null: 1 / (number of counted tokens) each */
+    float* loss;                /* one float, or null */
+    float* losses;              /* T floats */
+    float* lse;                 /* T floats */
+    void* dx;                   /* T x D, row pitch lddx, or null */
+    long long lddx;
+    void* dweight; /* V x D, row pitch lddw, or null */
+    long long lddw;
+} sgemm_ce;
+
+/*
+ * sgemm_cross_entropy - softmax cross entropy of the logits s[t][v] = x[t] . weight[v], which
+ * are not kept, and its gradients where dx or dweight is given. A token counts when
+ * 0 <= target < V; of the others nothing but the target is read.
+ *
+ *     lse[t] = log(sum over v of exp(s[t][v])),   losses[t] = lse[t] - s[t][target[t]],
+ *     loss = sum over t of c[t] * losses[t],
+ *     g[t][v] = c[t] * (exp(s[t][v] - lse[t]) - [v = target[t]]),
+ *     dx[t] = sum over v of g[t][v] * weight[v],   dweight[v] = sum over t of g[t][v] * x[t];
+ *
+ * losses, lse and dx are zero for tokens that do not count, and losses does not include c.
+ *
+ * 0 <= T <= 1048576, 1 <= D <= 65536, 1 <= V <= 1048576. T = 0 gives a loss of zero and a
+ * dweight of zeros. Sums are FP32; with bfloat16 and float16, g is rounded twice to that type
+ * (as exponentials relative to a maximum, and as g over the largest |c|) and each gradient
+ * once. float32 operands are multiplied as three bfloat16 pieces (all 24 bits; an infinity
+ * counts as a NaN). A counted token with an infinity or NaN may make all of dweight NaN, as
+ * the definition does. Results are bitwise reproducible: the order of sums depends on the
+ * sizes and on which tokens count. Outputs must not overlap the inputs or each other.
+ *
+ * Workspace comes from the library's pool: the counted rows of x; for gradients 2 bytes
+ * (float32: 10) for each logit of a chunk of tokens, 2 GiB at most or 256 tokens, and, where
+ * that makes several chunks, V x D floats. Everything is stream-ordered; the call can be
+ * captured into a CUDA graph after one call of the same kind outside.
+ */
+SGEMM_API int sgemm_cross_entropy(const sgemm_ce* args, void* stream);
+
+/* ==== training: orthogonalised updates =================================================
+ *
+ * sgemm_orthogonalize - `steps` Newton-Schulz steps towards the nearest matrix with
+ * orthonormal rows (or columns) for each of `count` matrices G of M x N:
+ *
+ *     X = G / (|G| + eps),  |G| the Frobenius norm;
+ *     for each step, with its a, b, c:   A = X X^T,  X = a X + (b A + c A A) X
+ *     (where M > N the same from the right: A = X^T X, X = a X + X (b A + c A A));
+ *
+ * and the last X is written to `out`. G and out are device arrays of type `dtype`
+ * (SGEMM_FLOAT32, SGEMM_BFLOAT16 or SGEMM_FLOAT16): element (i, j) of matrix e at
+ * e * stride + i * ld + j. They may be the same array with the same pitch and stride, else they
+ * must not overlap. coefficients: 3 * steps floats on the HOST, a, b, c of each step.
+ *
+ * 0 <= count <= 4096 (0 enqueues nothing), 1 <= M, N <= 32768, min(M, N) <= 16384,
+ * 1 <= steps <= 64, eps >= 0; ld >= N, and matrices of a stack do not overlap. X is kept in
+ * FP32 from step to step. The factors of the products are FP16 times 2^8, one piece (11 bits)
+ * for bfloat16 and two (22 bits) for the other types, so entries of X, A and b A + c A A must
+ * stay below 2^7 in size: with |G| at most 1 before the first step that holds for coefficients
+ * that keep singular values below some 10. A matrix with an infinity or NaN gives NaN; the
+ * others of its stack are not touched by it. Sums are FP32. Results are bitwise reproducible,
+ * and a matrix's do not depend on the others of its stack.
+ *
+ * Workspace comes from the library's pool. Everything is stream-ordered; the call can be
+ * captured into a CUDA graph after one call of the same kind outside.
+ */
+SGEMM_API int sgemm_orthogonalize(const void* G, int dtype, int count, int M, int N, long long ldg,
+                                  long long stride_g, void* out, long long ldo,
+                                  long long stride_o, int steps, const float* coefficients,
+                                  float eps, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
