@@ -244,6 +244,7 @@ struct CeForward {
     __device__ CeForward(const Params& p_, const hg::Args&, int live_, uint8_t* block_)
         : p(p_), block(block_), live(live_) {}
 
+    __device__ __forceinline__ void start(const hg::Unit&, int, int) {}
     __device__ __forceinline__ void unit(const hg::Unit&, int row, int col, float (&s)[COLS]) {
         const int lane = threadIdx.x & 31;
         const int cols = min(COLS, p.V - col);
@@ -640,6 +641,7 @@ struct CeGrad {
         });
     }
 
+    __device__ __forceinline__ void start(const hg::Unit&, int, int) {}
     __device__ __forceinline__ void unit(const hg::Unit& t, int row, int col, float (&s)[COLS]) {
         const GradOut& o = p.out[t.problem];
         if (!o.parts) {

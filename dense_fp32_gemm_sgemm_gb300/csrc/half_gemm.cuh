@@ -40,9 +40,9 @@ constexpr int EPI_WARPS = 8;
 constexpr int EPI_WARP0 = 4;  // warps 2 and 3 only fill up the first warpgroup
 constexpr int THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
 // Registers: 168 a thread at launch (384 threads); the first warpgroup gives most of its own to
-// the epilogue's, whose threads hold 128 sums. 56 + 224 + 224 = 3 * 168.
-constexpr int REGS_FEW = 56;
-constexpr int REGS_MANY = 224;
+// the epilogue's, whose threads hold 128 sums. 72 + 216 + 216 = 3 * 168.
+constexpr int REGS_FEW = 72;
+constexpr int REGS_MANY = 216;
 constexpr int A_BYTES = HALF_M * BK * 2;
 constexpr int CHUNK_BYTES = 64 * BK * 2;  // 64 elements of the other index by 64 of k
 constexpr int STAGING = 4096;             // bytes of one epilogue warp's staging block
@@ -196,8 +196,8 @@ __device__ __forceinline__ Smem carve(uint8_t* raw) {
     return s;
 }
 
-__device__ __forceinline__ bool wait_c(uint32_t bar, uint32_t parity, const Smem& sm, int* err) {
-    return wait_phase(bar, parity, sm.abort_flag, err, WAIT_LIMIT_NS, true);
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, const Smem& sm, int* err) {
+    return wait_phase(bar, parity, sm.abort_flag, err);
 }
 
 // ---- operands in shared memory ----------------------------------------------------------
@@ -205,15 +205,15 @@ __device__ __forceinline__ bool wait_c(uint32_t bar, uint32_t parity, const Smem
 // Other index contiguous: chunks of 64 of it, 8192 bytes apart (the leading offset), each with
 // one 128-byte row for every k, 8 k 1024 bytes apart; 16 k are 2048 bytes. Both 128-byte
 // swizzled, as TMA writes them.
-__device__ __forceinline__ uint64_t operand_desc(uint32_t saddr, bool mn, int k16) {
-    const uint32_t at = saddr + uint32_t(k16) * (mn ? 2048u : 32u);
-    uint64_t d = uint64_t((at >> 4) & 0x3FFFu);
-    d |= uint64_t(mn ? CHUNK_BYTES >> 4 : 1) << 16;
-    d |= uint64_t(1024 >> 4) << 32;
-    d |= uint64_t(1) << 46;
-    d |= uint64_t(2) << 61;
-    return d;
-}
+struct OperandDesc {
+    uint32_t lo, hi;  // of the operand in stage 0
+    uint32_t step;    // of `lo` to the next 16 k
+    __device__ __forceinline__ OperandDesc(uint32_t saddr, bool mn) {
+        lo = ((saddr >> 4) & 0x3FFFu) | uint32_t(mn ? CHUNK_BYTES >> 4 : 1) << 16;
+        hi = (1024u >> 4) | 1u << 14 | 2u << 29;
+        step = mn ? 2048u >> 4 : 32u >> 4;
+    }
+};
 
 // ---- staging ------------------------------------------------------------------------------
 // A warp's 4 KiB block holds 32 rows of 128 bytes, 16-byte piece c of row r at c ^ (r % 8): both
@@ -228,28 +228,35 @@ __device__ __forceinline__ uint4* staged(uint8_t* block, int row, int piece) {
 // stored.
 template <int SIZE, class RowAt>
 __device__ __forceinline__ void store_block(uint8_t* block, int bytes, bool wide, RowAt row_at) {
-    const int lane = threadIdx.x & 31, piece = lane & 7;
+    const int lane = threadIdx.x & 31, piece = lane & 7, r0 = lane >> 3;
     __syncwarp();
+    const int here = bytes - piece * 16;  // bytes of this lane's piece
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int r = i * 4 + (lane >> 3);
-        char* to = reinterpret_cast<char*>(row_at(r));
-        if (to == nullptr || piece * 16 >= bytes) continue;
-        const uint4 v = *staged(block, r, piece);
-        if (wide && piece * 16 + 16 <= bytes) {
-            *reinterpret_cast<uint4*>(to + piece * 16) = v;
-        } else if (SIZE == 4) {
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    for (int i0 = 0; i0 < 8; i0 += 4) {
+        uint4 v[4];  // read before the first store, which the compiler cannot tell apart
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (piece * 16 + j * 4 < bytes) reinterpret_cast<uint32_t*>(to)[piece * 4 + j] = w[j];
-        } else {
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        for (int i = 0; i < 4; ++i) v[i] = *staged(block, (i0 + i) * 4 + r0, piece);
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (piece * 16 + j * 2 < bytes)
-                    reinterpret_cast<unsigned short*>(to)[piece * 8 + j] =
-                        static_cast<unsigned short>(w[j >> 1] >> (16 * (j & 1)));
+        for (int i = 0; i < 4; ++i) {
+            char* to = reinterpret_cast<char*>(row_at((i0 + i) * 4 + r0));
+            if (to == nullptr || here <= 0) continue;
+            to += piece * 16;
+            if (wide && here >= 16) {
+                *reinterpret_cast<uint4*>(to) = v[i];
+                continue;
+            }
+            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+            if (SIZE == 4) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (j * 4 < here) reinterpret_cast<uint32_t*>(to)[j] = w[j];
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (j * 2 < here)
+                        reinterpret_cast<unsigned short*>(to)[j] =
+                            static_cast<unsigned short>(w[j >> 1] >> (16 * (j & 1)));
+            }
         }
     }
     __syncwarp();
@@ -269,8 +276,10 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 
 // ---- the kernel -----------------------------------------------------------------------------
 // EPI::BN, EPI::Params, and EPI(params, args, live, staging block) with
-//   void unit(const Unit&, int row (of the tile's first in this warp), int col, float (&acc)[BN / 2])
-// called by each epilogue warp once a unit: lane l holds row `row` + l, columns col .. col + BN / 2.
+//   void start(const Unit&, int row, int col)
+//   void unit(const Unit&, int row, int col, float (&acc)[BN / 2])
+// called by each epilogue warp at the beginning of a unit (to load what it will need) and with its
+// sums: lane l holds row `row` + l, columns col .. col + BN / 2.
 template <class EPI>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     half_gemm_kernel(const __grid_constant__ Args g, const __grid_constant__ typename EPI::Params ep) {
@@ -320,20 +329,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     // the unit in slot i, or -1 at the end or when a wait ran out
     auto take = [&](int i) {
         const int s = i % SLOTS;
-        if (!wait_c(sm.slot_full(s), (i / SLOTS) & 1, sm, g.err)) return -1;
-        return sm.slot_ptr[s];
+        // the slot is written by the first CTA's thread: the only data that ordinary stores hand
+        // to another CTA
+        const bool there = wait_phase(sm.slot_full(s), (i / SLOTS) & 1, sm.abort_flag, g.err,
+                                      WAIT_LIMIT_NS, true);
+        return __all_sync(~0u, there) ? sm.slot_ptr[s] : -1;
+    };
+    // a whole warp's wait, with the same answer for all lanes
+    auto wait_all = [&](uint32_t bar, uint32_t parity) {
+        return __all_sync(~0u, wait(bar, parity, sm, g.err)) != 0;
     };
     auto taken = [&](int i) {
-        ptx::mbar_arrive_cluster(ptx::mapa_shared(sm.slot_empty(i % SLOTS), 0));
+        ptx::mbar_arrive_remote(ptx::mapa_shared(sm.slot_empty(i % SLOTS), 0));
     };
 
     if (warp < EPI_WARP0) {
-      ptx::regs_give_up<REGS_FEW>();
-      if (warp == 0) {
-        if (lane == 0) {
+        ptx::regs_give_up<REGS_FEW>();
+        if (warp == 0) {
+            // all lanes go through the loop with equal values, one of them issues
             int units = unit_count<BN>(g.p[0], live);
             if (g.problems > 1) units += unit_count<BN>(g.p[1], live);
             const int pairs = gridDim.x >> 1;
+            const uint32_t full0 = ptx::mapa_shared(sm.full(0), 0);  // the first CTA's barriers
             int next = blockIdx.x >> 1;
             int s = 0;
             uint32_t ph = 0;
@@ -341,60 +358,65 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 int u;
                 if (rank == 0) {
                     u = next < units ? next : -1;
-                    if (u >= 0) next = pairs + atomicAdd(g.counter, 1);  // back by the next turn
                     const int slot = i % SLOTS;
-                    if (!wait_c(sm.slot_empty(slot), ((i / SLOTS) & 1) ^ 1, sm, g.err)) u = -1;
-                    sm.slot_ptr[slot] = u;
-                    ptx::st_shared_cluster_f32(ptx::mapa_shared(sm.slots + 4u * slot, 1),
-                                               __int_as_float(u));
-                    ptx::mbar_arrive_cluster(ptx::mapa_shared(sm.slot_full(slot), 0));
-                    ptx::mbar_arrive_cluster(ptx::mapa_shared(sm.slot_full(slot), 1));
+                    if (!wait_all(sm.slot_empty(slot), ((i / SLOTS) & 1) ^ 1)) u = -1;
+                    int claimed = 0;
+                    if (lane == 0) {
+                        sm.slot_ptr[slot] = u;
+                        ptx::st_shared_cluster_f32(ptx::mapa_shared(sm.slots + 4u * slot, 1),
+                                                   __int_as_float(u));
+                        ptx::mbar_arrive_cluster(ptx::mapa_shared(sm.slot_full(slot), 0));
+                        ptx::mbar_arrive_cluster(ptx::mapa_shared(sm.slot_full(slot), 1));
+                        if (u >= 0) claimed = atomicAdd(g.counter, 1);
+                    }
+                    next = pairs + claimed;  // lane 0's is passed on when it is needed
                 } else {
                     u = take(i);
-                    if (u >= 0) taken(i);
+                    __syncwarp();
+                    if (u >= 0 && lane == 0) taken(i);
                 }
                 if (u < 0) break;
                 const Unit t = unit_at<BN>(g, u, live);
                 const Problem& p = g.p[t.problem];
                 const CUtensorMap* ma = &g.a[t.problem];
                 const CUtensorMap* mb = &g.b[t.problem];
-                const int m0 = t.row0 + int(rank) * HALF_M;
-                const int n0 = t.col0 + int(rank) * (BN / 2);
+                const bool a_mn = p.a_mn, b_mn = p.b_mn;
+                const int products = p.products;
+                const int za = t.batch * p.planes_a, zb = t.batch * p.planes_b;
+                // coordinates of the first box, and how they move on
+                const int m0 = t.row0 + int(rank) * HALF_M, n0 = t.col0 + int(rank) * (BN / 2);
+                const int k0 = t.kb0 * BK;
+                int ax = a_mn ? m0 : k0, ay = p.a_row + (a_mn ? k0 : m0);
+                int bx = b_mn ? n0 : k0, by = p.b_row + (b_mn ? k0 : n0);
+                const int adx = a_mn ? 0 : BK, ady = a_mn ? BK : 0;
+                const int bdx = b_mn ? 0 : BK, bdy = b_mn ? BK : 0;
                 bool ok = true;
                 for (int kb = t.kb0; ok && kb < t.kb1; ++kb) {
-                    const int k0 = kb * BK;
-                    for (int q = 0; q < p.products; ++q) {
-                        if (!wait_c(sm.empty(s), ph ^ 1u, sm, g.err)) {
-                            ok = false;
-                            break;
-                        }
-                        const uint32_t bar = ptx::mapa_shared(sm.full(s), 0);
+                    for (int q = 0; q < products; ++q) {
+                        ok = wait_all(sm.empty(s), ph ^ 1u);
+                        if (!ok) break;
+                        const uint32_t bar = full0 + 8u * s;
                         const uint32_t st = sm.ring + uint32_t(s) * STAGE_BYTES<BN>;
-                        if (rank == 0) ptx::mbar_arrive_expect_tx(sm.full(s), 2 * STAGE_BYTES<BN>);
-                        const int za = t.batch * p.planes_a + p.pa[q];
-                        const int zb = t.batch * p.planes_b + p.pb[q];
-                        if (p.a_mn) {
-                            ptx::tma_load_3d_pair(st, ma, bar, m0, p.a_row + k0, za);
-                            ptx::tma_load_3d_pair(st + CHUNK_BYTES, ma, bar, m0 + 64, p.a_row + k0,
-                                                  za);
-                        } else {
-                            ptx::tma_load_3d_pair(st, ma, bar, k0, p.a_row + m0, za);
-                        }
-                        const uint32_t sb = st + A_BYTES;
-                        if (p.b_mn) {
-                            ptx::tma_load_3d_pair(sb, mb, bar, n0, p.b_row + k0, zb);
-                            if (BN == 256)
-                                ptx::tma_load_3d_pair(sb + CHUNK_BYTES, mb, bar, n0 + 64,
-                                                      p.b_row + k0, zb);
-                        } else {
-                            ptx::tma_load_3d_pair(sb, mb, bar, k0, p.b_row + n0, zb);
-                        }
+                        if (rank == 0)
+                            ptx::mbar_arrive_expect_tx_elect(sm.full(s), 2 * STAGE_BYTES<BN>);
+                        const int pa = za + p.pa[q], pb = zb + p.pb[q];
+                        ptx::tma_load_3d_pair(st, ma, bar, ax, ay, pa);
+                        if (a_mn) ptx::tma_load_3d_pair(st + CHUNK_BYTES, ma, bar, ax + 64, ay, pa);
+                        ptx::tma_load_3d_pair(st + A_BYTES, mb, bar, bx, by, pb);
+                        if (BN == 256 && b_mn)
+                            ptx::tma_load_3d_pair(st + A_BYTES + CHUNK_BYTES, mb, bar, bx + 64, by,
+                                                  pb);
                         if (++s == STAGES) {
                             s = 0;
                             ph ^= 1u;
                         }
                     }
+                    ax += adx;
+                    ay += ady;
+                    bx += bdx;
+                    by += bdy;
                 }
+                next = __shfl_sync(~0u, next, 0);
                 if (!ok) {
                     if (rank != 0) break;
                     next = units;  // the others are told that there is nothing more
@@ -405,62 +427,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 while (ptx::globaltimer_ns() - t0 < 10000000ull) {
                 }
             }
-        }
-      } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
+        } else if (warp == 1 && rank == 0) {
             int s = 0, seg = 0;
             uint32_t ph = 0;
             bool ok = true, issued = false;
             for (int i = 0; ok; ++i) {
                 const int u = take(i);
+                __syncwarp();
                 if (u < 0) break;
-                taken(i);
+                if (lane == 0) taken(i);
                 const Unit t = unit_at<BN>(g, u, live);
                 const Problem& p = g.p[t.problem];
                 const uint32_t idesc = p.idesc | (uint32_t(BN >> 3) << 17);
-                const bool a_mn = p.a_mn, b_mn = p.b_mn;
+                const OperandDesc a(sm.ring, p.a_mn), b(sm.ring + A_BYTES, p.b_mn);
                 int left = (t.kb1 - t.kb0) * p.products;
                 for (; ok && left > 0; left -= SEG_STEPS, ++seg) {
-                    const int b = seg & 1;
-                    if (!wait_c(sm.acc_empty(b), ((seg >> 1) & 1) ^ 1, sm, g.err)) {
-                        ok = false;
-                        break;
-                    }
+                    const int half = seg & 1;
+                    ok = wait_all(sm.acc_empty(half), ((seg >> 1) & 1) ^ 1);
+                    if (!ok) break;
                     ptx::tc_fence_after();
-                    const uint32_t d = tmem + uint32_t(b * BN);
+                    const uint32_t d = tmem + uint32_t(half * BN);
                     const int steps = min(left, SEG_STEPS);
                     for (int j = 0; j < steps; ++j) {
-                        if (!wait_c(sm.full(s), ph, sm, g.err)) {
-                            ok = false;
-                            break;
-                        }
+                        ok = wait_all(sm.full(s), ph);
+                        if (!ok) break;
                         ptx::tc_fence_after();
-                        const uint32_t st = sm.ring + uint32_t(s) * STAGE_BYTES<BN>;
-#pragma unroll
-                        for (int k = 0; k < BK / 16; ++k)
-                            ptx::mma_pair<true>(d, operand_desc(st, a_mn, k),
-                                                operand_desc(st + A_BYTES, b_mn, k), idesc,
-                                                (j | k) ? 1u : 0u);
+                        const uint32_t at = uint32_t(s) * (STAGE_BYTES<BN> >> 4);
+                        ptx::mma_pair_x4(d, a.lo + at, a.hi, a.step, b.lo + at, b.hi, b.step, idesc,
+                                         j);
                         issued = true;
-                        ptx::mma_commit_pair(sm.empty(s), 0x3);
+                        ptx::mma_commit_pair_elect(sm.empty(s), 0x3);
                         if (++s == STAGES) {
                             s = 0;
                             ph ^= 1u;
                         }
                     }
                     if (!ok) break;
-                    ptx::mma_commit_pair(sm.acc_full(b), 0x3);
+                    ptx::mma_commit_pair_elect(sm.acc_full(half), 0x3);
                 }
             }
-            if (*sm.abort_flag && issued) {  // MMAs in flight end before TMEM is freed
-                ptx::mma_commit_pair(sm.drain(), 0x1);
+            if (__any_sync(~0u, *sm.abort_flag != 0) && issued) {
+                // MMAs in flight end before TMEM is freed
+                ptx::mma_commit_pair_elect(sm.drain(), 0x1);
                 const unsigned long long t0 = ptx::globaltimer_ns();
                 while (!ptx::mbar_try_wait(sm.drain(), 0) &&
                        ptx::globaltimer_ns() - t0 < WAIT_LIMIT_NS) {
                 }
             }
         }
-      }
     } else {
         ptx::regs_take<REGS_MANY>();
         // warp w reads TMEM lanes [32 (w % 4), +32) and the first or second half of the columns
@@ -471,18 +485,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         bool ok = true;
         for (int i = 0; ok; ++i) {
             const int u = take(i);
+            __syncwarp();  // all lanes have read the slot
             if (u < 0) break;
-            __syncwarp();
             if (lane == 0) taken(i);
             const Unit t = unit_at<BN>(g, u, live);
             const int steps = (t.kb1 - t.kb0) * g.p[t.problem].products;
             const int segs = (steps + SEG_STEPS - 1) / SEG_STEPS;
+            const int row = t.row0 + int(rank) * HALF_M + q * 32, col = t.col0 + h * COLS;
+            epi.start(t, row, col);
             for (int sg = 0; sg < segs; ++sg, ++seg) {
                 const int b = seg & 1;
-                if (!wait_c(sm.acc_full(b), (seg >> 1) & 1, sm, g.err)) {
-                    ok = false;
-                    break;
-                }
+                ok = wait_all(sm.acc_full(b), (seg >> 1) & 1);
+                if (!ok) break;
                 ptx::tc_fence_after();
                 const uint32_t at = tmem + (uint32_t(q * 32) << 16) + uint32_t(b * BN + h * COLS);
                 if (sg == 0) {
@@ -506,14 +520,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 }
                 ptx::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(sm.acc_empty(b), 0));
+                if (lane == 0) ptx::mbar_arrive_remote(ptx::mapa_shared(sm.acc_empty(b), 0));
             }
             if (!ok) break;
             if (segs == 0) {
 #pragma unroll
                 for (int j = 0; j < COLS; ++j) acc[j] = 0.f;
             }
-            epi.unit(t, t.row0 + int(rank) * HALF_M + q * 32, t.col0 + h * COLS, acc);
+            epi.unit(t, row, col, acc);
         }
     }
     ptx::tc_fence_before();

@@ -142,26 +142,41 @@ __global__ void __launch_bounds__(CONVERT_THREADS)
 }
 
 // ---- epilogues ---------------------------------------------------------------------------------
-// A staged block of 32 rows x 64 FP16 (or 32 FP32) values, read from global memory: the reverse
-// of hg::store_block. Rows from `rows` on and bytes from `bytes` on are not read.
-__device__ __forceinline__ void load_block(uint8_t* block, const void* from, long long pitch_bytes,
-                                           int rows, int bytes) {
-    const int lane = threadIdx.x & 31, piece = lane & 7;
-    __syncwarp();
+// A block of 32 rows x 128 bytes on its way from global memory to a warp's rows: loaded into
+// registers well before it is needed (each lane four rows' pieces, eight loads in flight), then
+// passed through the staging block. Rows from `rows` on and bytes from `bytes` on are not read.
+struct Ahead {
+    uint4 v[8];
+    __device__ __forceinline__ void load(const void* from, long long pitch_bytes, int rows,
+                                         int bytes) {
+        const int lane = threadIdx.x & 31, piece = lane & 7;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int r = i * 4 + (lane >> 3);
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (r < rows && piece * 16 < bytes)
-            v = *reinterpret_cast<const uint4*>(static_cast<const char*>(from) + r * pitch_bytes +
-                                                piece * 16);
-        *hg::staged(block, r, piece) = v;
+        for (int i = 0; i < 8; ++i) {
+            const int r = i * 4 + (lane >> 3);
+            v[i] = make_uint4(0, 0, 0, 0);
+            if (r < rows && piece * 16 < bytes)
+                v[i] = *reinterpret_cast<const uint4*>(static_cast<const char*>(from) +
+                                                       r * pitch_bytes + piece * 16);
+        }
     }
-    __syncwarp();
+    __device__ __forceinline__ void stage(uint8_t* block) const {
+        const int lane = threadIdx.x & 31, piece = lane & 7;
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) *hg::staged(block, i * 4 + (lane >> 3), piece) = v[i];
+        __syncwarp();
+    }
+};
+
+// Bytes of `left` columns of SIZE bytes that a 128-byte row has, up to a multiple of 8 elements:
+// rows are padded that far.
+template <int SIZE>
+__device__ __forceinline__ int padded_bytes(int left) {
+    return min(128, ((left + 7) & ~7) * SIZE);
 }
 
-// 64 values from s[C] on, as piece k of the factors, to both triangles of a symmetric matrix (r x
-// r, row pitch ld) or, without MIRROR, to its place alone.
+// 64 values from s[C] on, as piece K of the factors, to their place; with MIRROR and `mirror`
+// also to the mirror image's. Rows have a pitch of ld, a multiple of 8, and zeros behind cols_n.
 template <int C, int K, int PIECES, bool MIRROR, int N>
 __device__ __forceinline__ void store_factor(uint8_t* block, const float (&s)[N], __half* to,
                                              long long ld, int row, int col, int rows_n, int cols_n,
@@ -169,31 +184,65 @@ __device__ __forceinline__ void store_factor(uint8_t* block, const float (&s)[N]
     const int lane = threadIdx.x & 31;
     const int left = cols_n - (col + C);
     if (left <= 0) return;
-    uint32_t w[32];
+    __syncwarp();
 #pragma unroll
-    for (int j = 0; j < 64; j += 2) {
-        __half a[PIECES], b[PIECES];
-        pieces_of<PIECES>(s[C + j], a);
-        pieces_of<PIECES>(s[C + j + 1], b);
-        w[j / 2] = uint32_t(__half_as_ushort(a[K])) | uint32_t(__half_as_ushort(b[K])) << 16;
-    }
+    for (int j = 0; j < 8; ++j) {
+        uint32_t w[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-        *hg::staged(block, lane, j) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-    __half* base = to + row * ld + col + C;
-    // rows are padded to 8 elements, whose tail holds zeros: whole pieces may be written
-    hg::store_block<2>(block, min(128, ((left + 7) & ~7) * 2), true, [&](int i) {
-        return row + i < rows_n ? base + i * ld : nullptr;
-    });
-    if (MIRROR && mirror) {
-        // row j of the mirror image: the warp's 32 rows are 64 consecutive bytes of it
-        if (row + lane < rows_n) {
-            __half* at = to + (col + C) * ld + row + lane;
-#pragma unroll
-            for (int j = 0; j < 64; ++j)
-                if (j < left)
-                    at[j * ld] = __ushort_as_half((unsigned short)(w[j / 2] >> (16 * (j & 1))));
+        for (int k = 0; k < 4; ++k) {
+            __half a[PIECES], b[PIECES];
+            pieces_of<PIECES>(s[C + 8 * j + 2 * k], a);
+            pieces_of<PIECES>(s[C + 8 * j + 2 * k + 1], b);
+            w[k] = uint32_t(__half_as_ushort(a[K])) | uint32_t(__half_as_ushort(b[K])) << 16;
         }
+        *hg::staged(block, lane, j) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    __half* base = to + row * ld + col + C;
+    hg::store_block<2>(block, padded_bytes<2>(left), true,
+                       [&](int i) { return row + i < rows_n ? base + i * ld : nullptr; });
+    if (MIRROR && mirror) {
+        // the block turned over: 64 rows of 32 values, 64 bytes each
+        unsigned short* turned = reinterpret_cast<unsigned short*>(block);
+#pragma unroll
+        for (int j = 0; j < 64; ++j) {
+            __half a[PIECES];
+            pieces_of<PIECES>(s[C + j], a);
+            turned[j * 32 + lane] = __half_as_ushort(a[K]);
+        }
+        __syncwarp();
+        const int piece = lane & 3;
+        __half* at = to + (col + C + (lane >> 2)) * ld + row + piece * 8;
+#pragma unroll
+        for (int i0 = 0; i0 < 8; i0 += 4) {
+            uint4 v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v[i] = reinterpret_cast<const uint4*>(block)[(i0 + i) * 32 + lane];
+            if (row + piece * 8 < rows_n) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if ((i0 + i) * 8 + (lane >> 2) < left)
+                        *reinterpret_cast<uint4*>(at + (i0 + i) * 8 * ld) = v[i];
+            }
+        }
+        __syncwarp();
+    }
+}
+
+// All of a thread's values as factors: C counts the columns done.
+template <int PIECES, bool MIRROR, int N>
+__device__ __forceinline__ void store_factors(uint8_t* block, const float (&s)[N], __half* to,
+                                              long long plane, long long ld, int row, int col,
+                                              int rows_n, int cols_n, bool mirror) {
+    store_factor<0, 0, PIECES, MIRROR>(block, s, to, ld, row, col, rows_n, cols_n, mirror);
+    if constexpr (PIECES == 2)
+        store_factor<0, 1, PIECES, MIRROR>(block, s, to + plane, ld, row, col, rows_n, cols_n,
+                                           mirror);
+    if constexpr (N == 128) {
+        store_factor<64, 0, PIECES, MIRROR>(block, s, to, ld, row, col, rows_n, cols_n, mirror);
+        if constexpr (PIECES == 2)
+            store_factor<64, 1, PIECES, MIRROR>(block, s, to + plane, ld, row, col, rows_n, cols_n,
+                                                mirror);
     }
 }
 
@@ -211,21 +260,14 @@ struct NsGram {
     uint8_t* block;
     __device__ NsGram(const Params& p_, const hg::Args&, int, uint8_t* block_)
         : p(p_), block(block_) {}
+    __device__ __forceinline__ void start(const hg::Unit&, int, int) {}
     __device__ __forceinline__ void unit(const hg::Unit& t, int row, int col, float (&s)[COLS]) {
         if (row >= p.r) return;
 #pragma unroll
         for (int j = 0; j < COLS; ++j) s[j] *= DOWN;
-        const bool mirror = t.col0 + BN <= t.row0;
         const long long plane = p.r * p.ld;
-        __half* to = p.out + t.batch * PIECES * plane;
-#define NS_STORE(C)                                                                              \
-    store_factor<C, 0, PIECES, true>(block, s, to, p.ld, row, col, p.r, p.r, mirror);            \
-    if constexpr (PIECES == 2)                                                                   \
-        store_factor<C, 1, PIECES, true>(block, s, to + plane, p.ld, row, col, p.r, p.r, mirror)
-        NS_STORE(0);
-        if constexpr (COLS == 128) {
-            NS_STORE(64);
-        }
+        store_factors<PIECES, true>(block, s, p.out + t.batch * PIECES * plane, plane, p.ld, row,
+                                    col, p.r, p.r, t.col0 + BN <= t.row0);
     }
 };
 
@@ -243,15 +285,25 @@ struct NsPoly {
     };
     const Params& p;
     uint8_t* block;
+    Ahead ahead;
     __device__ NsPoly(const Params& p_, const hg::Args&, int, uint8_t* block_)
         : p(p_), block(block_) {}
+    // piece K of A at 64 of the thread's columns
+    __device__ __forceinline__ void load(const hg::Unit& t, int row, int col, int c, int k) {
+        const __half* from = p.gram + (t.batch * PIECES + k) * (p.r * p.ld) + row * p.ld + col + c;
+        ahead.load(from, p.ld * 2, p.r - row, padded_bytes<2>(p.r - (col + c)));
+    }
+    __device__ __forceinline__ void start(const hg::Unit& t, int row, int col) {
+        load(t, row, col, 0, 0);
+    }
     template <int C, int K>
-    __device__ __forceinline__ void add(const __half* from, int row, int col, float (&s)[COLS]) {
+    __device__ __forceinline__ void add(const hg::Unit& t, int row, int col, float (&s)[COLS]) {
         const int lane = threadIdx.x & 31;
-        const int left = p.r - (col + C);
-        if (left <= 0) return;
-        load_block(block, from + row * p.ld + col + C, p.ld * 2, p.r - row,
-                   min(128, ((left + 7) & ~7) * 2));
+        ahead.stage(block);
+        if constexpr (K + 1 < PIECES)
+            load(t, row, col, C, K + 1);
+        else if constexpr (C + 64 < COLS)
+            load(t, row, col, C + 64, 0);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const uint4 v = *hg::staged(block, lane, j);
@@ -269,21 +321,15 @@ struct NsPoly {
         const float c = p.c * DOWN;
 #pragma unroll
         for (int j = 0; j < COLS; ++j) s[j] *= c;
-        const bool mirror = t.col0 + BN <= t.row0;
+        add<0, 0>(t, row, col, s);
+        if constexpr (PIECES == 2) add<0, 1>(t, row, col, s);
+        if constexpr (COLS == 128) {
+            add<64, 0>(t, row, col, s);
+            if constexpr (PIECES == 2) add<64, 1>(t, row, col, s);
+        }
         const long long plane = p.r * p.ld;
-        const __half* from = p.gram + t.batch * PIECES * plane;
-        __half* to = p.out + t.batch * PIECES * plane;
-        add<0, 0>(from, row, col, s);
-        if constexpr (PIECES == 2) add<0, 1>(from + plane, row, col, s);
-        if constexpr (COLS == 128) {
-            add<64, 0>(from, row, col, s);
-            if constexpr (PIECES == 2) add<64, 1>(from + plane, row, col, s);
-        }
-        NS_STORE(0);
-        if constexpr (COLS == 128) {
-            NS_STORE(64);
-        }
-#undef NS_STORE
+        store_factors<PIECES, true>(block, s, p.out + t.batch * PIECES * plane, plane, p.ld, row,
+                                    col, p.r, p.r, t.col0 + BN <= t.row0);
     }
 };
 
@@ -304,17 +350,26 @@ struct NsUpdate {
     };
     const Params& p;
     uint8_t* block;
+    Ahead ahead;
     __device__ NsUpdate(const Params& p_, const hg::Args&, int, uint8_t* block_)
         : p(p_), block(block_) {}
+
+    __device__ __forceinline__ float* x_at(const hg::Unit& t, int row, int col) const {
+        return p.x + t.batch * (p.M * p.ld) + row * p.ld + col;
+    }
+    __device__ __forceinline__ void start(const hg::Unit& t, int row, int col) {
+        ahead.load(x_at(t, row, col), p.ld * 4, p.M - row, padded_bytes<4>(p.N - col));
+    }
 
     template <int C>
     __device__ __forceinline__ void step32(const hg::Unit& t, int row, int col, float (&s)[COLS]) {
         const int lane = threadIdx.x & 31;
         const int left = p.N - (col + C);
         if (left <= 0) return;
-        float* x = p.x + t.batch * (p.M * p.ld) + row * p.ld + col + C;
-        const int bytes = min(128, ((left + 7) & ~7) * 4);
-        load_block(block, x, p.ld * 4, p.M - row, bytes);
+        float* x = x_at(t, row, col + C);
+        ahead.stage(block);
+        if constexpr (C + 32 < COLS)
+            ahead.load(x + 32, p.ld * 4, p.M - row, padded_bytes<4>(left - 32));
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const uint4 v = *hg::staged(block, lane, j);
@@ -325,14 +380,13 @@ struct NsUpdate {
         }
         const bool inner = p.out != nullptr;
         if (!inner && p.dtype != SGEMM_FLOAT32) return;
-        __syncwarp();
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
+        for (int j = 0; j < 8; ++j)  // over the values that this lane has just read
             *hg::staged(block, lane, j) =
                 make_uint4(__float_as_uint(s[C + 4 * j]), __float_as_uint(s[C + 4 * j + 1]),
                            __float_as_uint(s[C + 4 * j + 2]), __float_as_uint(s[C + 4 * j + 3]));
         if (inner) {
-            hg::store_block<4>(block, bytes, true, [&](int i) {
+            hg::store_block<4>(block, padded_bytes<4>(left), true, [&](int i) {
                 return row + i < p.M ? x + i * p.ld : nullptr;
             });
         } else {
@@ -373,21 +427,11 @@ struct NsUpdate {
             step32<96>(t, row, col, s);
         }
         if (p.out) {
-            const long long plane = p.M * p.ld;
-            __half* to = p.out + t.batch * PIECES * plane;
 #pragma unroll
             for (int j = 0; j < COLS; ++j) s[j] *= UP;
-            __syncwarp();
-            store_factor<0, 0, PIECES, false>(block, s, to, p.ld, row, col, p.M, p.N, false);
-            if constexpr (PIECES == 2)
-                store_factor<0, 1, PIECES, false>(block, s, to + plane, p.ld, row, col, p.M, p.N,
-                                                  false);
-            if constexpr (COLS == 128) {
-                store_factor<64, 0, PIECES, false>(block, s, to, p.ld, row, col, p.M, p.N, false);
-                if constexpr (PIECES == 2)
-                    store_factor<64, 1, PIECES, false>(block, s, to + plane, p.ld, row, col, p.M,
-                                                       p.N, false);
-            }
+            const long long plane = p.M * p.ld;
+            store_factors<PIECES, false>(block, s, p.out + t.batch * PIECES * plane, plane, p.ld,
+                                         row, col, p.M, p.N, false);
         } else if (p.dtype == SGEMM_BFLOAT16) {
             result64<0, true>(t, row, col, s);
             if constexpr (COLS == 128) result64<64, true>(t, row, col, s);

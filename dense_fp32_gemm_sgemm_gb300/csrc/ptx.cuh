@@ -193,6 +193,11 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
                      cluster_addr)
                  : "memory");
 }
+// The same without ordering this thread's memory operations at cluster scope, which would wait
+// for its stores to global memory: for handing on tensor memory or a slot that was read.
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];\n" ::"r"(cluster_addr) : "memory");
+}
 // try_wait with acquire at cluster scope, for barriers that other CTAs arrive on.
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
     uint32_t done;
@@ -217,14 +222,24 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void* tmap,
         "l"(tmap), "r"(bar_cluster), "r"(c0), "r"(c1)
         : "memory");
 }
-// The same for a 3-D tensor map.
+// The same for a 3-D tensor map. The whole warp calls it with equal arguments and one elected lane
+// issues it, so that the operands stay in uniform registers (as in mma_ts below).
 __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const void* tmap,
                                                  uint32_t bar_cluster, int32_t c0, int32_t c1,
                                                  int32_t c2) {
     asm volatile(
-        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5}], [%2];\n" ::"r"(dst),
+        "{\n.reg .pred q;\nelect.sync _|q, 0xffffffff;\n"
+        "@q cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];\n}\n" ::"r"(dst),
         "l"(tmap), "r"(bar_cluster), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
+// mbar_arrive_expect_tx by one elected lane of the calling warp.
+__device__ __forceinline__ void mbar_arrive_expect_tx_elect(uint32_t bar, uint32_t bytes) {
+    asm volatile(
+        "{\n.reg .pred q;\nelect.sync _|q, 0xffffffff;\n"
+        "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n}\n" ::"r"(bar),
+        "r"(bytes)
         : "memory");
 }
 // Tensor-memory allocation shared by the CTA pair: one warp of EACH CTA executes it;
@@ -273,6 +288,36 @@ __device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t a_desc, uint6
             SGEMM_MMA_ASM("tcgen05.mma.cta_group::2.kind::tf32");
     }
 #undef SGEMM_MMA_ASM
+}
+// Four pair MMAs of kind::f16 along the reduction, issued by one elected lane of the calling warp
+// (all lanes have equal arguments): the descriptors' low words move on by a_step and b_step, their
+// high words are constant. The first MMA overwrites D unless `accumulate` is set.
+__device__ __forceinline__ void mma_pair_x4(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi,
+                                            uint32_t a_step, uint32_t b_lo, uint32_t b_hi,
+                                            uint32_t b_step, uint32_t idesc, uint32_t accumulate) {
+#define SGEMM_MMA_NEXT                                                                    \
+    "add.u32 al, al, %3;\nadd.u32 bl, bl, %6;\nmov.b64 da, {al, %2};\nmov.b64 db, {bl, %5};\n" \
+    "@q tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %7, t;\n"
+    asm volatile(
+        "{\n.reg .pred p, q, t;\n.reg .b32 al, bl;\n.reg .b64 da, db;\n"
+        "elect.sync _|q, 0xffffffff;\n"
+        "setp.ne.b32 p, %8, 0;\nsetp.eq.b32 t, 0, 0;\n"
+        "mov.b32 al, %1;\nmov.b32 bl, %4;\nmov.b64 da, {al, %2};\nmov.b64 db, {bl, %5};\n"
+        "@q tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %7, p;\n" SGEMM_MMA_NEXT SGEMM_MMA_NEXT
+            SGEMM_MMA_NEXT "}\n" ::"r"(d_tmem),
+        "r"(a_lo), "r"(a_hi), "r"(a_step), "r"(b_lo), "r"(b_hi), "r"(b_step), "r"(idesc),
+        "r"(accumulate)
+        : "memory");
+#undef SGEMM_MMA_NEXT
+}
+// mma_commit_pair (below) by the elected lane, which is the same each time.
+__device__ __forceinline__ void mma_commit_pair_elect(uint32_t bar, uint16_t mask) {
+    asm volatile(
+        "{\n.reg .pred q;\nelect.sync _|q, 0xffffffff;\n"
+        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+        " [%0], %1;\n}\n" ::"r"(bar),
+        "h"(mask)
+        : "memory");
 }
 // Arrive on the mbarrier at the same offset in every CTA of `mask` once all previously
 // issued pair MMAs of this thread finish.
