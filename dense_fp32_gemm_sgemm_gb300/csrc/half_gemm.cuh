@@ -6,8 +6,9 @@
 // added up in one accumulation. A pair of CTAs computes a tile of 256 x BN with
 // tcgen05.mma.cta_group::2; each CTA stages its 128 rows of A and its half of B's columns.
 //
-// Roles in a CTA: warp 0 issues the TMA loads (and, in the pair's first CTA, hands out units
-// of work), warp 1 of the first CTA issues the MMAs, warps 4-11 run the epilogue.
+// Roles in a CTA: warp 0 issues A's TMA loads (and, in the pair's first CTA, hands out units of
+// work), warp 2 B's (a step takes one warp some 450 cycles for both, the MMAs 512), warp 1 of the
+// first CTA issues the MMAs, warps 4-11 run the epilogue.
 //
 // Accumulation. The tensor core cuts off, rather than rounds, the bits that an addition to its
 // FP32 accumulator shifts out: some 2^-25 of the accumulator for each MMA, always towards zero.
@@ -37,7 +38,7 @@ constexpr int STAGES = 6;
 constexpr int SEG_STEPS = 8;  // stages in an accumulator segment
 constexpr int SLOTS = 4;      // units handed out ahead
 constexpr int EPI_WARPS = 8;
-constexpr int EPI_WARP0 = 4;  // warps 2 and 3 only fill up the first warpgroup
+constexpr int EPI_WARP0 = 4;  // warp 3 only fills up the first warpgroup
 constexpr int THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
 // Registers: 168 a thread at launch (384 threads); the first warpgroup gives most of its own to
 // the epilogue's, whose threads hold 128 sums. 72 + 216 + 216 = 3 * 168.
@@ -301,8 +302,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
         for (int i = 0; i < SLOTS; ++i) {
             ptx::mbar_init(sm.slot_full(i), 1);
-            // the first CTA's MMA warp, the second's TMA warp, all epilogue warps
-            ptx::mbar_init(sm.slot_empty(i), 2 + 2 * EPI_WARPS);
+            // the first CTA's MMA warp, the TMA warps but the one that hands out, all epilogue warps
+            ptx::mbar_init(sm.slot_empty(i), 4 + 2 * EPI_WARPS);
         }
         ptx::mbar_init(sm.drain(), 1);
         *sm.abort_flag = 0;
@@ -345,8 +346,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 
     if (warp < EPI_WARP0) {
         ptx::regs_give_up<REGS_FEW>();
-        if (warp == 0) {
+        if (warp == 0 || warp == 2) {
             // all lanes go through the loop with equal values, one of them issues
+            const bool is_a = warp == 0;
+            const bool hands_out = is_a && rank == 0;
             int units = unit_count<BN>(g.p[0], live);
             if (g.problems > 1) units += unit_count<BN>(g.p[1], live);
             const int pairs = gridDim.x >> 1;
@@ -356,7 +359,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             uint32_t ph = 0;
             for (int i = 0;; ++i) {
                 int u;
-                if (rank == 0) {
+                if (hands_out) {
                     u = next < units ? next : -1;
                     const int slot = i % SLOTS;
                     if (!wait_all(sm.slot_empty(slot), ((i / SLOTS) & 1) ^ 1)) u = -1;
@@ -378,47 +381,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 if (u < 0) break;
                 const Unit t = unit_at<BN>(g, u, live);
                 const Problem& p = g.p[t.problem];
-                const CUtensorMap* ma = &g.a[t.problem];
-                const CUtensorMap* mb = &g.b[t.problem];
-                const bool a_mn = p.a_mn, b_mn = p.b_mn;
+                const CUtensorMap* map = is_a ? &g.a[t.problem] : &g.b[t.problem];
+                const bool mn = is_a ? p.a_mn : p.b_mn;
                 const int products = p.products;
-                const int za = t.batch * p.planes_a, zb = t.batch * p.planes_b;
+                const unsigned char* planes = is_a ? p.pa : p.pb;
+                const int z0 = t.batch * (is_a ? p.planes_a : p.planes_b);
+                const int z1 = z0 + planes[0];
                 // coordinates of the first box, and how they move on
-                const int m0 = t.row0 + int(rank) * HALF_M, n0 = t.col0 + int(rank) * (BN / 2);
-                const int k0 = t.kb0 * BK;
-                int ax = a_mn ? m0 : k0, ay = p.a_row + (a_mn ? k0 : m0);
-                int bx = b_mn ? n0 : k0, by = p.b_row + (b_mn ? k0 : n0);
-                const int adx = a_mn ? 0 : BK, ady = a_mn ? BK : 0;
-                const int bdx = b_mn ? 0 : BK, bdy = b_mn ? BK : 0;
+                const int o = is_a ? t.row0 + int(rank) * HALF_M : t.col0 + int(rank) * (BN / 2);
+                const int k0 = t.kb0 * BK, first = is_a ? p.a_row : p.b_row;
+                int x = mn ? o : k0, y = first + (mn ? k0 : o);
+                const int dx = mn ? 0 : BK, dy = mn ? BK : 0;
+                const bool two = mn && (is_a || BN == 256);
+                const uint32_t to = sm.ring + (is_a ? 0 : A_BYTES);
                 bool ok = true;
                 for (int kb = t.kb0; ok && kb < t.kb1; ++kb) {
                     for (int q = 0; q < products; ++q) {
+                        const int z = products == 1 ? z1 : z0 + planes[q];
                         ok = wait_all(sm.empty(s), ph ^ 1u);
                         if (!ok) break;
                         const uint32_t bar = full0 + 8u * s;
-                        const uint32_t st = sm.ring + uint32_t(s) * STAGE_BYTES<BN>;
-                        if (rank == 0)
+                        const uint32_t st = to + uint32_t(s) * STAGE_BYTES<BN>;
+                        // the bytes of both CTAs; some may have arrived already
+                        if (hands_out)
                             ptx::mbar_arrive_expect_tx_elect(sm.full(s), 2 * STAGE_BYTES<BN>);
-                        const int pa = za + p.pa[q], pb = zb + p.pb[q];
-                        ptx::tma_load_3d_pair(st, ma, bar, ax, ay, pa);
-                        if (a_mn) ptx::tma_load_3d_pair(st + CHUNK_BYTES, ma, bar, ax + 64, ay, pa);
-                        ptx::tma_load_3d_pair(st + A_BYTES, mb, bar, bx, by, pb);
-                        if (BN == 256 && b_mn)
-                            ptx::tma_load_3d_pair(st + A_BYTES + CHUNK_BYTES, mb, bar, bx + 64, by,
-                                                  pb);
+                        ptx::tma_load_3d_pair(st, map, bar, x, y, z);
+                        if (two) ptx::tma_load_3d_pair(st + CHUNK_BYTES, map, bar, x + 64, y, z);
                         if (++s == STAGES) {
                             s = 0;
                             ph ^= 1u;
                         }
                     }
-                    ax += adx;
-                    ay += ady;
-                    bx += bdx;
-                    by += bdy;
+                    x += dx;
+                    y += dy;
                 }
                 next = __shfl_sync(~0u, next, 0);
                 if (!ok) {
-                    if (rank != 0) break;
+                    if (!hands_out) break;
                     next = units;  // the others are told that there is nothing more
                 }
             }
