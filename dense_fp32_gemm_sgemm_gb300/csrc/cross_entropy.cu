@@ -233,16 +233,23 @@ struct CeForward {
         float2* stats;   // [block of COLS columns][row of the chunk]: maximum, sum
         float* picked;   // [row of the chunk]
         const int* label;  // of the chunk's rows
-        void* kept;
-        long long pitch;  // elements of a row of `kept`, a multiple of 64
+        CUtensorMap kept;  // blocks of 64 columns (16 bits) or 32 (logits)
         int stats_pitch;
         int V;
     };
     const Params& p;
-    uint8_t* block;
+    hg::WarpIo& io;
     int live;
-    __device__ CeForward(const Params& p_, const hg::Args&, int live_, uint8_t* block_)
-        : p(p_), block(block_), live(live_) {}
+    __device__ CeForward(const Params& p_, const hg::Args&, int live_, hg::WarpIo& io_)
+        : p(p_), io(io_), live(live_) {}
+
+    // 32 words of every lane as block B's rows to columns `col` on of `kept`
+    template <int C, int B>
+    __device__ __forceinline__ void keep(const float (&s)[COLS], int row, int col) {
+        io.acquire(B);
+        hg::stage_words<C>(io.block(B), s);
+        io.store(B, &p.kept, col, row, 0);
+    }
 
     __device__ __forceinline__ void start(const hg::Unit&, int, int) {}
     __device__ __forceinline__ void unit(const hg::Unit&, int row, int col, float (&s)[COLS]) {
@@ -268,42 +275,26 @@ struct CeForward {
         const float from = m == -INFINITY ? 0.f : m;
         float sum = 0.f;
         if constexpr (KEEP == Keep::logits) {
-#pragma unroll
-            for (int c = 0; c < COLS; c += 32) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    *hg::staged(block, lane, j) =
-                        make_uint4(__float_as_uint(s[c + 4 * j]), __float_as_uint(s[c + 4 * j + 1]),
-                                   __float_as_uint(s[c + 4 * j + 2]),
-                                   __float_as_uint(s[c + 4 * j + 3]));
-                float* base = static_cast<float*>(p.kept) + (long long)row * p.pitch + col + c;
-                hg::store_block<4>(block, 128, true,
-                                   [&](int i) { return base + (long long)i * p.pitch; });
+            keep<0, 0>(s, row, col);
+            keep<32, 1>(s, row, col + 32);
+            if constexpr (COLS == 128) {
+                keep<64, 0>(s, row, col + 64);
+                keep<96, 1>(s, row, col + 96);
             }
         }
+        constexpr bool HALF = KEEP == Keep::bf16 || KEEP == Keep::fp16;
         constexpr float BIAS = KEEP == Keep::fp16 ? float(FP16_EXP_BITS) : 0.f;
 #pragma unroll
-        for (int c = 0; c < COLS; c += 64) {
-#pragma unroll
-            for (int j = 0; j < 64; j += 2) {
-                const float a = exp2_fast((s[c + j] - from) * LOG2E + BIAS);
-                const float b = exp2_fast((s[c + j + 1] - from) * LOG2E + BIAS);
-                sum += a + b;
-                if constexpr (KEEP == Keep::bf16 || KEEP == Keep::fp16)
-                    s[c + j / 2] = __uint_as_float(hg::pack2<KEEP == Keep::bf16>(a, b));
-            }
-            if constexpr (KEEP == Keep::bf16 || KEEP == Keep::fp16) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    *hg::staged(block, lane, j) =
-                        make_uint4(__float_as_uint(s[c + 4 * j]), __float_as_uint(s[c + 4 * j + 1]),
-                                   __float_as_uint(s[c + 4 * j + 2]),
-                                   __float_as_uint(s[c + 4 * j + 3]));
-                unsigned short* base =
-                    static_cast<unsigned short*>(p.kept) + (long long)row * p.pitch + col + c;
-                hg::store_block<2>(block, 128, true,
-                                   [&](int i) { return base + (long long)i * p.pitch; });
-            }
+        for (int j = 0; j < COLS; j += 2) {
+            const float a = exp2_fast((s[j] - from) * LOG2E + BIAS);
+            const float b = exp2_fast((s[j + 1] - from) * LOG2E + BIAS);
+            sum += a + b;
+            if constexpr (HALF)
+                s[j / 2] = __uint_as_float(hg::pack2<KEEP == Keep::bf16>(a, b));
+        }
+        if constexpr (HALF) {
+            keep<0, 0>(s, row, col);
+            if constexpr (COLS == 128) keep<32, 1>(s, row, col + 64);
         }
         if constexpr (KEEP == Keep::fp16) sum *= 1.f / float(1 << FP16_EXP_BITS);
         p.stats[(long long)(col / COLS) * p.stats_pitch + r] = make_float2(m, sum);
@@ -521,16 +512,17 @@ __global__ void __launch_bounds__(FINISH_THREADS) ce_finish(const FinishArgs a) 
 
 // ---- the second launch's epilogue ------------------------------------------------------------------
 struct GradOut {
+    CUtensorMap map;  // of the output (blocks of 128 bytes a row) or, FP32, of the parts
     void* out;
     long long ld;
     int dtype;        // SGEMM_FLOAT32, SGEMM_BFLOAT16 or SGEMM_FLOAT16
-    int wide;         // 16-byte aligned rows
+    int tma;          // stored through the map; else row by row
+    int wide;         // rows are 16-byte aligned
     int rows_n, cols_n;
     const int* rows;  // output row of each row, or null
     float* sums;      // FP32 sums over chunks (pitch cols_n rounded up to 4), or null
     int first, last;  // chunk of those
-    float* parts;     // FP32 parts of a split reduction, or null
-    long long part;   // floats of one
+    int part_rows;    // rows of a part of a split reduction, or 0
 };
 
 template <bool SUMS>
@@ -543,39 +535,16 @@ struct CeGrad {
         float down;  // 2^-FP16_GRAD_BITS or 1
     };
     const Params& p;
-    const hg::Args& args;
-    uint8_t* block;
+    hg::WarpIo& io;
     int live;
     float scale;
-    __device__ CeGrad(const Params& p_, const hg::Args& args_, int live_, uint8_t* block_)
-        : p(p_), args(args_), block(block_), live(live_) {
+    __device__ CeGrad(const Params& p_, const hg::Args&, int live_, hg::WarpIo& io_)
+        : p(p_), io(io_), live(live_) {
         scale = p.info->c_max * p.down;
     }
 
-    // 32 columns from c on as FP32 into the staging block
-    template <int C>
-    __device__ __forceinline__ void stage32(const float (&s)[COLS]) {
-        const int lane = threadIdx.x & 31;
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            *hg::staged(block, lane, j) =
-                make_uint4(__float_as_uint(s[C + 4 * j]), __float_as_uint(s[C + 4 * j + 1]),
-                           __float_as_uint(s[C + 4 * j + 2]), __float_as_uint(s[C + 4 * j + 3]));
-    }
-    template <int C, bool BF16>
-    __device__ __forceinline__ void stage64(const float (&s)[COLS]) {
-        const int lane = threadIdx.x & 31;
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            *hg::staged(block, lane, j) = make_uint4(
-                hg::pack2<BF16>(s[C + 8 * j], s[C + 8 * j + 1]),
-                hg::pack2<BF16>(s[C + 8 * j + 2], s[C + 8 * j + 3]),
-                hg::pack2<BF16>(s[C + 8 * j + 4], s[C + 8 * j + 5]),
-                hg::pack2<BF16>(s[C + 8 * j + 6], s[C + 8 * j + 7]));
-    }
-
     // the staged FP32 block added to the sums; with the last chunk the result goes out
-    __device__ __forceinline__ void add_block(const GradOut& o, int row, int col) {
+    __device__ __forceinline__ void add_block(uint8_t* block, const GradOut& o, int row, int col) {
         const int lane = threadIdx.x & 31;
         const long long pitch = (o.cols_n + 3) & ~3;
         __syncwarp();
@@ -603,63 +572,57 @@ struct CeGrad {
         __syncwarp();
     }
 
-    template <int C>
-    __device__ __forceinline__ void part32(const hg::Unit& t, const GradOut& o, int row, int col,
-                                           const float (&s)[COLS]) {
-        const int left = o.cols_n - col - C;
-        if (left <= 0) return;
-        stage32<C>(s);
-        if (o.parts) {
-            const long long pitch = (o.cols_n + 3) & ~3;
-            float* base = o.parts + t.split * o.part + col + C;
-            hg::store_block<4>(block, min(128, left * 4), true, [&](int i) {
-                return row + i < live ? base + (row + i) * pitch : nullptr;
-            });
-        } else if (SUMS && o.sums) {
-            add_block(o, row, col + C);
+    // 32 words of every lane, from word C on, through block B to columns `col` on
+    template <int C, int B, int SIZE>
+    __device__ __forceinline__ void part(const hg::Unit& t, const GradOut& o, int row, int col,
+                                         int index, const float (&s)[COLS]) {
+        if (col >= o.cols_n) return;
+        io.acquire(B);
+        hg::stage_words<C>(io.block(B), s);
+        if (o.tma) {
+            io.store(B, &o.map, col, t.split * o.part_rows + row, 0);
+        } else if (SUMS && SIZE == 4 && o.sums) {
+            add_block(io.block(B), o, row, col);
         } else {
-            float* base = static_cast<float*>(o.out) + col + C;
-            const int rows_n = o.rows ? live : o.rows_n;
-            hg::store_block<4>(block, min(128, left * 4), o.wide, [&](int i) {
-                const int r = row + i;
-                return r < rows_n ? base + (o.rows ? o.rows[r] : r) * o.ld : nullptr;
-            });
+            const int bytes = min(128, (o.cols_n - col) * SIZE);
+            char* base = static_cast<char*>(o.out) + (long long)col * SIZE;
+            if (!o.rows) base += row * (o.ld * SIZE);
+            const hg::Rows to = {base, o.ld * SIZE, (o.rows ? live : o.rows_n) - row, bytes,
+                                 o.wide && bytes % 16 == 0};
+            if (o.rows)
+                hg::store_block<SIZE, true>(io.block(B), to, index);
+            else
+                hg::store_block<SIZE>(io.block(B), to);
         }
-    }
-
-    template <int C, bool BF16>
-    __device__ __forceinline__ void part64(const GradOut& o, int row, int col,
-                                           const float (&s)[COLS]) {
-        const int left = o.cols_n - col - C;
-        if (left <= 0) return;
-        stage64<C, BF16>(s);
-        unsigned short* base = static_cast<unsigned short*>(o.out) + col + C;
-        const int rows_n = o.rows ? live : o.rows_n;
-        hg::store_block<2>(block, min(128, left * 2), o.wide, [&](int i) {
-            const int r = row + i;
-            return r < rows_n ? base + (o.rows ? o.rows[r] : r) * o.ld : nullptr;
-        });
     }
 
     __device__ __forceinline__ void start(const hg::Unit&, int, int) {}
     __device__ __forceinline__ void unit(const hg::Unit& t, int row, int col, float (&s)[COLS]) {
         const GradOut& o = p.out[t.problem];
-        if (!o.parts) {
+        const int lane = threadIdx.x & 31;
+        const int index = o.rows && row + lane < live ? o.rows[row + lane] : 0;
+        if (!o.part_rows) {
 #pragma unroll
             for (int j = 0; j < COLS; ++j) s[j] *= scale;
         }
-        if (o.parts || (SUMS && o.sums) || o.dtype == SGEMM_FLOAT32) {
-            part32<0>(t, o, row, col, s);
-            part32<32>(t, o, row, col, s);
-            part32<64>(t, o, row, col, s);
-            part32<96>(t, o, row, col, s);
-        } else if (o.dtype == SGEMM_BFLOAT16) {
-            part64<0, true>(o, row, col, s);
-            part64<64, true>(o, row, col, s);
-        } else {
-            part64<0, false>(o, row, col, s);
-            part64<64, false>(o, row, col, s);
+        if (o.part_rows || (SUMS && o.sums) || o.dtype == SGEMM_FLOAT32) {
+            part<0, 0, 4>(t, o, row, col, index, s);
+            part<32, 1, 4>(t, o, row, col + 32, index, s);
+            part<64, 0, 4>(t, o, row, col + 64, index, s);
+            part<96, 1, 4>(t, o, row, col + 96, index, s);
+            return;
         }
+        if (o.dtype == SGEMM_BFLOAT16) {
+#pragma unroll
+            for (int j = 0; j < COLS; j += 2)
+                s[j / 2] = __uint_as_float(hg::pack2<true>(s[j], s[j + 1]));
+        } else {
+#pragma unroll
+            for (int j = 0; j < COLS; j += 2)
+                s[j / 2] = __uint_as_float(hg::pack2<false>(s[j], s[j + 1]));
+        }
+        part<0, 0, 2>(t, o, row, col, index, s);
+        part<32, 1, 2>(t, o, row, col + 64, index, s);
     }
 };
 
@@ -768,29 +731,20 @@ int check(const sgemm_ce& a) {
 
 template <int BN>
 cudaError_t forward(Keep keep, const hg::Args& g, float2* stats, float* picked, const int* label,
-                    void* kept, long long pitch, int stats_pitch, int V, int sm_count,
-                    cudaStream_t s) {
+                    const CUtensorMap& kept, int stats_pitch, int V, int sm_count, cudaStream_t s) {
     switch (keep) {
-        case Keep::none: {
-            using E = CeForward<BN, Keep::none>;
-            return hg::launch_gemm<E>(g, {stats, picked, label, kept, pitch, stats_pitch, V},
-                                      sm_count, s);
-        }
-        case Keep::bf16: {
-            using E = CeForward<BN, Keep::bf16>;
-            return hg::launch_gemm<E>(g, {stats, picked, label, kept, pitch, stats_pitch, V},
-                                      sm_count, s);
-        }
-        case Keep::fp16: {
-            using E = CeForward<BN, Keep::fp16>;
-            return hg::launch_gemm<E>(g, {stats, picked, label, kept, pitch, stats_pitch, V},
-                                      sm_count, s);
-        }
-        default: {
-            using E = CeForward<BN, Keep::logits>;
-            return hg::launch_gemm<E>(g, {stats, picked, label, kept, pitch, stats_pitch, V},
-                                      sm_count, s);
-        }
+        case Keep::none:
+            return hg::launch_gemm<CeForward<BN, Keep::none>>(
+                g, {stats, picked, label, kept, stats_pitch, V}, sm_count, s);
+        case Keep::bf16:
+            return hg::launch_gemm<CeForward<BN, Keep::bf16>>(
+                g, {stats, picked, label, kept, stats_pitch, V}, sm_count, s);
+        case Keep::fp16:
+            return hg::launch_gemm<CeForward<BN, Keep::fp16>>(
+                g, {stats, picked, label, kept, stats_pitch, V}, sm_count, s);
+        default:
+            return hg::launch_gemm<CeForward<BN, Keep::logits>>(
+                g, {stats, picked, label, kept, stats_pitch, V}, sm_count, s);
     }
 }
 
@@ -893,6 +847,11 @@ cudaError_t run(const sgemm_ce& a, const DeviceInfo& info, int dev, cudaStream_t
     fwd.live_max = bwd.live_max = chunk;
     fwd.err = bwd.err = info.error_word;
 
+    CUtensorMap kept_map;
+    std::memset(&kept_map, 0, sizeof kept_map);
+    if (grad && !hg::encode_block(&kept_map, kept, f32 ? 4 : 2, pitch, chunk, pitch, 1, pitch,
+                                  f32 ? 32 : 64, 32))
+        return cudaErrorInvalidValue;
     GradOut outs[2];
     std::memset(outs, 0, sizeof outs);
     int n = 0, dx_at = -1;
@@ -920,8 +879,11 @@ cudaError_t run(const sgemm_ce& a, const DeviceInfo& info, int dev, cudaStream_t
         outs[n].rows_n = chunk;
         outs[n].cols_n = a.D;
         if (splits > 1) {
-            outs[n].parts = parts;
-            outs[n].part = (long long)part;
+            outs[n].tma = 1;
+            outs[n].part_rows = chunk;
+            if (!hg::encode_block(&outs[n].map, parts, 4, d4, (long long)splits * chunk, d4, 1, d4,
+                                  32, 32))
+                return cudaErrorInvalidValue;
         }
         dx_at = n++;
     }
@@ -948,6 +910,10 @@ cudaError_t run(const sgemm_ce& a, const DeviceInfo& info, int dev, cudaStream_t
         outs[n].rows_n = a.V;
         outs[n].cols_n = a.D;
         outs[n].sums = sums ? sum : nullptr;
+        outs[n].tma = !sums && outs[n].wide;
+        if (outs[n].tma && !hg::encode_block(&outs[n].map, a.dweight, size, a.D, a.V, a.lddw, 1,
+                                             a.lddw, 128 / size, 32))
+            return cudaErrorInvalidValue;
         dw_at = n++;
     }
     bwd.problems = n;
@@ -981,10 +947,10 @@ cudaError_t run(const sgemm_ce& a, const DeviceInfo& info, int dev, cudaStream_t
         fwd.p[0].a_row = live0;
         fwd.counter = counters + 2 * c;
         const int stats_pitch = chunk;
-        e = narrow ? forward<128>(keep, fwd, stats, picked, label + live0, kept, pitch, stats_pitch,
-                                  a.V, info.sm_count, s)
-                   : forward<256>(keep, fwd, stats, picked, label + live0, kept, pitch, stats_pitch,
-                                  a.V, info.sm_count, s);
+        e = narrow ? forward<128>(keep, fwd, stats, picked, label + live0, kept_map, stats_pitch, a.V,
+                                  info.sm_count, s)
+                   : forward<256>(keep, fwd, stats, picked, label + live0, kept_map, stats_pitch, a.V,
+                                  info.sm_count, s);
         if (e != cudaSuccess) return e;
         FinishArgs fa = {stats, stats_pitch, blocks, cols, picked, rows + live0, label + live0, ci,
                          live0, chunk, a.token_weights, a.loss, a.losses, a.lse, kept, g_planes,

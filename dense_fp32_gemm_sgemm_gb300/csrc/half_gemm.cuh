@@ -34,7 +34,7 @@ namespace hg {
 constexpr int BM = 256;       // rows of a tile (both CTAs)
 constexpr int HALF_M = 128;   // rows of one CTA
 constexpr int BK = 64;        // reduction elements in a stage: 128 bytes
-constexpr int STAGES = 6;
+constexpr int STAGES = 5;
 constexpr int SEG_STEPS = 8;  // stages in an accumulator segment
 constexpr int SLOTS = 4;      // units handed out ahead
 constexpr int EPI_WARPS = 8;
@@ -46,8 +46,8 @@ constexpr int REGS_FEW = 72;
 constexpr int REGS_MANY = 216;
 constexpr int A_BYTES = HALF_M * BK * 2;
 constexpr int CHUNK_BYTES = 64 * BK * 2;  // 64 elements of the other index by 64 of k
-constexpr int STAGING = 4096;             // bytes of one epilogue warp's staging block
-constexpr int NUM_BARS = 2 * STAGES + 4 + 1 + 2 * SLOTS;
+constexpr int STAGING = 4096;             // bytes of a staging block, two for an epilogue warp
+constexpr int NUM_BARS = 2 * STAGES + 4 + 1 + 2 * SLOTS + 2 * EPI_WARPS;
 constexpr int MAX_PRODUCTS = 6;
 
 template <int BN>
@@ -55,7 +55,7 @@ constexpr int B_BYTES = BN / 2 * BK * 2;
 template <int BN>
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES<BN>;
 template <int BN>
-constexpr int SMEM_BYTES = STAGES * STAGE_BYTES<BN> + EPI_WARPS * STAGING + 512 + 1024;
+constexpr int SMEM_BYTES = STAGES * STAGE_BYTES<BN> + 2 * EPI_WARPS * STAGING + 512 + 1024;
 static_assert(SMEM_BYTES<256> <= 232448, "shared memory of an SM");
 
 // One product of a launch. Sizes are in elements; `live` may replace one of them on the device.
@@ -178,6 +178,7 @@ struct Smem {
         return bar0 + 8u * (2 * STAGES + 4 + SLOTS + i);
     }
     __device__ uint32_t drain() const { return bar0 + 8u * (2 * STAGES + 4 + 2 * SLOTS); }
+    __device__ uint32_t loaded(int i) const { return bar0 + 8u * (2 * STAGES + 5 + 2 * SLOTS + i); }
 };
 
 template <int BN>
@@ -187,7 +188,7 @@ __device__ __forceinline__ Smem carve(uint8_t* raw) {
     Smem s;
     s.ring = ptx::smem_u32(base);
     s.staging = base + STAGES * STAGE_BYTES<BN>;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(s.staging + EPI_WARPS * STAGING);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(s.staging + 2 * EPI_WARPS * STAGING);
     s.bar0 = ptx::smem_u32(bars);
     int* words = reinterpret_cast<int*>(bars + NUM_BARS);
     s.slots = ptx::smem_u32(words);
@@ -217,46 +218,123 @@ struct OperandDesc {
 };
 
 // ---- staging ------------------------------------------------------------------------------
-// A warp's 4 KiB block holds 32 rows of 128 bytes, 16-byte piece c of row r at c ^ (r % 8): both
-// a lane's own row and four whole rows at a time are free of bank conflicts.
+// A staging block holds 32 rows of 128 bytes, 16-byte piece c of row r at c ^ (r % 8), which is
+// TMA's 128-byte swizzle: both a lane's own row and four whole rows at a time are free of bank
+// conflicts.
 __device__ __forceinline__ uint4* staged(uint8_t* block, int row, int piece) {
     return reinterpret_cast<uint4*>(block + row * 128 + ((piece ^ (row & 7)) << 4));
 }
 
-// Writes the staged block to global memory, 16 bytes a lane and four rows at a time. `row_at(r)`
-// gives the address of the block's row r, or null where there is none; `bytes` of a row count
-// (at most 128); `wide`: the addresses are 16-byte aligned, else elements of SIZE bytes are
-// stored.
-template <int SIZE, class RowAt>
-__device__ __forceinline__ void store_block(uint8_t* block, int bytes, bool wide, RowAt row_at) {
-    const int lane = threadIdx.x & 31, piece = lane & 7, r0 = lane >> 3;
+// An epilogue warp's two staging blocks and its TMA traffic through them, which its first lane
+// issues. A block is written again once the store that last used it has read it.
+struct WarpIo {
+    uint8_t* blocks;
+    uint32_t bar;  // of block 0's loads; block 1's is 8 bytes on
+    volatile int* abort_flag;
+    int* err;
+    uint32_t parity = 0;  // bit i: of block i's next load
+    int last = 0;         // block of the latest store
+    bool first;           // this lane issues
+    __device__ __forceinline__ uint8_t* block(int i) const { return blocks + i * STAGING; }
+    __device__ __forceinline__ void acquire(int i) {
+        if (first) {
+            if (last == i)
+                ptx::bulk_wait_read0();
+            else
+                ptx::bulk_wait_read<1>();
+        }
+        __syncwarp();
+    }
+    // The block's 4096 bytes from a map whose boxes have as many.
+    __device__ __forceinline__ void load(int i, const CUtensorMap* map, int x, int y, int z) {
+        acquire(i);
+        if (first) {
+            ptx::mbar_arrive_expect_tx(bar + 8u * i, STAGING);
+            ptx::tma_load_3d(ptx::smem_u32(block(i)), map, bar + 8u * i, x, y, z);
+        }
+    }
+    __device__ __forceinline__ void wait_load(int i) {
+        wait_phase(bar + 8u * i, parity >> i & 1u, abort_flag, err);
+        parity ^= 1u << i;
+        __syncwarp();
+    }
+    // What the lanes wrote to the block goes out.
+    __device__ __forceinline__ void store(int i, const CUtensorMap* map, int x, int y, int z) {
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (first) {
+            ptx::tma_store_3d(map, ptx::smem_u32(block(i)), x, y, z);
+            ptx::bulk_commit();
+        }
+        last = i;
+    }
+    __device__ __forceinline__ void finish() {
+        if (first) ptx::bulk_wait0();
+    }
+};
+
+// A lane's row of a staging block from 32 registers.
+template <int C, int N>
+__device__ __forceinline__ void stage_words(uint8_t* block, const float (&s)[N]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        *staged(block, lane, j) =
+            make_uint4(__float_as_uint(s[C + 4 * j]), __float_as_uint(s[C + 4 * j + 1]),
+                       __float_as_uint(s[C + 4 * j + 2]), __float_as_uint(s[C + 4 * j + 3]));
+}
+
+// Where a block's rows go. The code that follows is kept short: an epilogue passes through it once
+// a unit, and instructions that are fetched for one use cost more than they compute.
+struct Rows {
+    char* base;        // of row 0's first byte
+    long long pitch;   // bytes
+    int count;         // rows from here on are not written
+    int bytes;         // of a row, at most 128
+    bool wide;         // 16-byte aligned rows of whole 16-byte pieces; else element by element
+};
+
+// Writes the staged block to global memory, 16 bytes a lane and four rows at a time. MAPPED: lane
+// l's `index` is the row that row l goes to. SIZE: bytes of an element.
+template <int SIZE, bool MAPPED = false>
+__device__ __forceinline__ void store_block(uint8_t* block, const Rows& to, int index = 0) {
+    const int lane = threadIdx.x & 31;
     __syncwarp();
-    const int here = bytes - piece * 16;  // bytes of this lane's piece
+    if (to.wide) {
+        const int piece = lane & 7, r0 = lane >> 3;
+        const bool here = piece * 16 < to.bytes;
+        char* at = to.base + piece * 16;
+        if (!MAPPED) at += r0 * to.pitch;
+        const long long step = 4 * to.pitch;
 #pragma unroll
-    for (int i0 = 0; i0 < 8; i0 += 4) {
-        uint4 v[4];  // read before the first store, which the compiler cannot tell apart
+        for (int i0 = 0; i0 < 8; i0 += 4) {
+            uint4 v[4];  // read before the first store, which the compiler cannot tell apart
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = *staged(block, (i0 + i) * 4 + r0, piece);
+            for (int i = 0; i < 4; ++i) v[i] = *staged(block, (i0 + i) * 4 + r0, piece);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            char* to = reinterpret_cast<char*>(row_at((i0 + i) * 4 + r0));
-            if (to == nullptr || here <= 0) continue;
-            to += piece * 16;
-            if (wide && here >= 16) {
-                *reinterpret_cast<uint4*>(to) = v[i];
-                continue;
+            for (int i = 0; i < 4; ++i) {
+                const int r = (i0 + i) * 4 + r0;
+                char* p = at;
+                if (MAPPED) p += __shfl_sync(~0u, index, r) * to.pitch;
+                if (here && r < to.count) *reinterpret_cast<uint4*>(p) = v[i];
+                if (!MAPPED) at += step;
             }
-            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-            if (SIZE == 4) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (j * 4 < here) reinterpret_cast<uint32_t*>(to)[j] = w[j];
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (j * 2 < here)
-                        reinterpret_cast<unsigned short*>(to)[j] =
-                            static_cast<unsigned short>(w[j >> 1] >> (16 * (j & 1)));
+        }
+    } else {
+        constexpr int PER = 16 / SIZE;  // elements of a piece
+        const int count = min(to.count, 32), elements = to.bytes / SIZE;
+#pragma unroll 1
+        for (int r = 0; r < count; ++r) {
+            const int row = MAPPED ? __shfl_sync(~0u, index, r) : r;
+            char* p = to.base + row * to.pitch;
+#pragma unroll 1
+            for (int e = lane; e < elements; e += 32) {
+                const uint4* q = staged(block, r, e / PER);
+                if (SIZE == 4)
+                    reinterpret_cast<uint32_t*>(p)[e] = reinterpret_cast<const uint32_t*>(q)[e % PER];
+                else
+                    reinterpret_cast<unsigned short*>(p)[e] =
+                        reinterpret_cast<const unsigned short*>(q)[e % PER];
             }
         }
     }
@@ -276,7 +354,7 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 }
 
 // ---- the kernel -----------------------------------------------------------------------------
-// EPI::BN, EPI::Params, and EPI(params, args, live, staging block) with
+// EPI::BN, EPI::Params, and EPI(params, args, live, warp's io) with
 //   void start(const Unit&, int row, int col)
 //   void unit(const Unit&, int row, int col, float (&acc)[BN / 2])
 // called by each epilogue warp at the beginning of a unit (to load what it will need) and with its
@@ -306,6 +384,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             ptx::mbar_init(sm.slot_empty(i), 4 + 2 * EPI_WARPS);
         }
         ptx::mbar_init(sm.drain(), 1);
+        for (int i = 0; i < 2 * EPI_WARPS; ++i) ptx::mbar_init(sm.loaded(i), 1);
         *sm.abort_flag = 0;
         ptx::fence_mbar_init();
         for (int i = 0; i < g.problems; ++i) {
@@ -478,7 +557,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         ptx::regs_take<REGS_MANY>();
         // warp w reads TMEM lanes [32 (w % 4), +32) and the first or second half of the columns
         const int q = warp & 3, h = (warp - EPI_WARP0) >> 2;
-        EPI epi(ep, g, live, sm.staging + (warp - EPI_WARP0) * STAGING);
+        WarpIo io;
+        io.blocks = sm.staging + 2 * (warp - EPI_WARP0) * STAGING;
+        io.bar = sm.loaded(2 * (warp - EPI_WARP0));
+        io.abort_flag = sm.abort_flag;
+        io.err = g.err;
+        io.first = lane == 0;
+        EPI epi(ep, g, live, io);
         float acc[COLS];
         int seg = 0;
         bool ok = true;
@@ -528,6 +613,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             }
             epi.unit(t, row, col, acc);
         }
+        io.finish();
     }
     ptx::tc_fence_before();
     __syncthreads();
@@ -544,6 +630,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 // multiple of 8), `slabs` of `slab` elements apart; boxes of 64 x box_rows. Zeros are read outside.
 bool encode_operand(CUtensorMap* map, const void* base, bool bf16, long long inner, long long rows,
                     long long ld, long long slabs, long long slab, int box_rows);
+
+// The same for the epilogue's blocks: elements of `size` bytes (2, FP16; 4, FP32), boxes of box_cols
+// x box_rows, 128-byte swizzled where a row has 128 bytes. Nothing is written outside.
+bool encode_block(CUtensorMap* map, const void* base, int size, long long cols, long long rows,
+                  long long ld, long long slabs, long long slab, int box_cols, int box_rows);
 
 // Launches `kernel`, allowed to start while the kernel before it on the stream ends (it waits
 // for that one by griddepcontrol.wait).

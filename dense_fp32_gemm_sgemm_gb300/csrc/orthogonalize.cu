@@ -142,107 +142,71 @@ __global__ void __launch_bounds__(CONVERT_THREADS)
 }
 
 // ---- epilogues ---------------------------------------------------------------------------------
-// A block of 32 rows x 128 bytes on its way from global memory to a warp's rows: loaded into
-// registers well before it is needed (each lane four rows' pieces, eight loads in flight), then
-// passed through the staging block. Rows from `rows` on and bytes from `bytes` on are not read.
-struct Ahead {
-    uint4 v[8];
-    __device__ __forceinline__ void load(const void* from, long long pitch_bytes, int rows,
-                                         int bytes) {
-        const int lane = threadIdx.x & 31, piece = lane & 7;
+// Turns a thread's values into factors in place: words 2 j and 2 j + 1 get the first and the second
+// pieces of values 2 j and 2 j + 1. (A conversion instruction for each value and use would cost
+// more than everything else here: they go at 16 a clock and SM.)
+template <int PIECES, int N>
+__device__ __forceinline__ void pack_factors(float (&s)[N]) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int r = i * 4 + (lane >> 3);
-            v[i] = make_uint4(0, 0, 0, 0);
-            if (r < rows && piece * 16 < bytes)
-                v[i] = *reinterpret_cast<const uint4*>(static_cast<const char*>(from) +
-                                                       r * pitch_bytes + piece * 16);
+    for (int j = 0; j < N; j += 2) {
+        const __half2 high = __floats2half2_rn(s[j], s[j + 1]);
+        if constexpr (PIECES == 2) {
+            const float2 h = __half22float2(high);
+            const __half2 low = __floats2half2_rn(s[j] - h.x, s[j + 1] - h.y);
+            s[j + 1] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&low));
         }
+        s[j] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&high));
     }
-    __device__ __forceinline__ void stage(uint8_t* block) const {
-        const int lane = threadIdx.x & 31, piece = lane & 7;
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 8; ++i) *hg::staged(block, i * 4 + (lane >> 3), piece) = v[i];
-        __syncwarp();
-    }
+}
+
+// Where factors go: blocks of 64 columns x 32 rows, and blocks turned over (32 x 64).
+struct FactorMaps {
+    CUtensorMap straight, turned;
 };
 
-// Bytes of `left` columns of SIZE bytes that a 128-byte row has, up to a multiple of 8 elements:
-// rows are padded that far.
-template <int SIZE>
-__device__ __forceinline__ int padded_bytes(int left) {
-    return min(128, ((left + 7) & ~7) * SIZE);
-}
-
-// 64 values from s[C] on, as piece K of the factors, to their place; with MIRROR and `mirror`
-// also to the mirror image's. Rows have a pitch of ld, a multiple of 8, and zeros behind cols_n.
-template <int C, int K, int PIECES, bool MIRROR, int N>
-__device__ __forceinline__ void store_factor(uint8_t* block, const float (&s)[N], __half* to,
-                                             long long ld, int row, int col, int rows_n, int cols_n,
-                                             bool mirror) {
+// Piece K of 64 packed values from s[C] on, through block B, to `slab` at (row, col); with MIRROR
+// and `mirror` also, turned over, through the other block, to (col, row).
+template <int C, int K, int B, bool MIRROR, int N>
+__device__ __forceinline__ void store_factor(hg::WarpIo& io, const FactorMaps& to,
+                                             const float (&s)[N], int slab, int row, int col,
+                                             int cols_n, bool mirror) {
     const int lane = threadIdx.x & 31;
-    const int left = cols_n - (col + C);
-    if (left <= 0) return;
-    __syncwarp();
+    if (col >= cols_n) return;
+    io.acquire(B);
+    uint8_t* block = io.block(B);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        uint32_t w[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            __half a[PIECES], b[PIECES];
-            pieces_of<PIECES>(s[C + 8 * j + 2 * k], a);
-            pieces_of<PIECES>(s[C + 8 * j + 2 * k + 1], b);
-            w[k] = uint32_t(__half_as_ushort(a[K])) | uint32_t(__half_as_ushort(b[K])) << 16;
-        }
-        *hg::staged(block, lane, j) = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-    __half* base = to + row * ld + col + C;
-    hg::store_block<2>(block, padded_bytes<2>(left), true,
-                       [&](int i) { return row + i < rows_n ? base + i * ld : nullptr; });
+    for (int j = 0; j < 8; ++j)
+        *hg::staged(block, lane, j) = make_uint4(
+            __float_as_uint(s[C + 8 * j + K]), __float_as_uint(s[C + 8 * j + 2 + K]),
+            __float_as_uint(s[C + 8 * j + 4 + K]), __float_as_uint(s[C + 8 * j + 6 + K]));
+    io.store(B, &to.straight, col, row, slab);
     if (MIRROR && mirror) {
-        // the block turned over: 64 rows of 32 values, 64 bytes each
-        unsigned short* turned = reinterpret_cast<unsigned short*>(block);
+        io.acquire(B ^ 1);
+        // 64 rows of 32 values, 64 bytes each
+        unsigned short* turned = reinterpret_cast<unsigned short*>(io.block(B ^ 1)) + lane;
 #pragma unroll
-        for (int j = 0; j < 64; ++j) {
-            __half a[PIECES];
-            pieces_of<PIECES>(s[C + j], a);
-            turned[j * 32 + lane] = __half_as_ushort(a[K]);
+        for (int j = 0; j < 64; j += 2) {
+            const uint32_t w = __float_as_uint(s[C + j + K]);
+            turned[j * 32] = (unsigned short)w;
+            turned[j * 32 + 32] = (unsigned short)(w >> 16);
         }
-        __syncwarp();
-        const int piece = lane & 3;
-        __half* at = to + (col + C + (lane >> 2)) * ld + row + piece * 8;
-#pragma unroll
-        for (int i0 = 0; i0 < 8; i0 += 4) {
-            uint4 v[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                v[i] = reinterpret_cast<const uint4*>(block)[(i0 + i) * 32 + lane];
-            if (row + piece * 8 < rows_n) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if ((i0 + i) * 8 + (lane >> 2) < left)
-                        *reinterpret_cast<uint4*>(at + (i0 + i) * 8 * ld) = v[i];
-            }
-        }
-        __syncwarp();
+        io.store(B ^ 1, &to.turned, row, col, slab);
     }
 }
 
-// All of a thread's values as factors: C counts the columns done.
+// All of a thread's values as factors (and so packed).
 template <int PIECES, bool MIRROR, int N>
-__device__ __forceinline__ void store_factors(uint8_t* block, const float (&s)[N], __half* to,
-                                              long long plane, long long ld, int row, int col,
-                                              int rows_n, int cols_n, bool mirror) {
-    store_factor<0, 0, PIECES, MIRROR>(block, s, to, ld, row, col, rows_n, cols_n, mirror);
+__device__ __forceinline__ void store_factors(hg::WarpIo& io, const FactorMaps& to, float (&s)[N],
+                                              int batch, int row, int col, int cols_n, bool mirror) {
+    pack_factors<PIECES>(s);
+    const int slab = batch * PIECES;
+    store_factor<0, 0, 0, MIRROR>(io, to, s, slab, row, col, cols_n, mirror);
     if constexpr (PIECES == 2)
-        store_factor<0, 1, PIECES, MIRROR>(block, s, to + plane, ld, row, col, rows_n, cols_n,
-                                           mirror);
+        store_factor<0, 1, 1, MIRROR>(io, to, s, slab + 1, row, col, cols_n, mirror);
     if constexpr (N == 128) {
-        store_factor<64, 0, PIECES, MIRROR>(block, s, to, ld, row, col, rows_n, cols_n, mirror);
+        store_factor<64, 0, PIECES == 1, MIRROR>(io, to, s, slab, row, col + 64, cols_n, mirror);
         if constexpr (PIECES == 2)
-            store_factor<64, 1, PIECES, MIRROR>(block, s, to + plane, ld, row, col, rows_n, cols_n,
-                                                mirror);
+            store_factor<64, 1, 1, MIRROR>(io, to, s, slab + 1, row, col + 64, cols_n, mirror);
     }
 }
 
@@ -252,22 +216,18 @@ struct NsGram {
     static constexpr int BN = BN_;
     static constexpr int COLS = BN / 2;
     struct Params {
-        __half* out;
+        FactorMaps out;
         int r;
-        long long ld;
     };
     const Params& p;
-    uint8_t* block;
-    __device__ NsGram(const Params& p_, const hg::Args&, int, uint8_t* block_)
-        : p(p_), block(block_) {}
+    hg::WarpIo& io;
+    __device__ NsGram(const Params& p_, const hg::Args&, int, hg::WarpIo& io_) : p(p_), io(io_) {}
     __device__ __forceinline__ void start(const hg::Unit&, int, int) {}
     __device__ __forceinline__ void unit(const hg::Unit& t, int row, int col, float (&s)[COLS]) {
         if (row >= p.r) return;
 #pragma unroll
         for (int j = 0; j < COLS; ++j) s[j] *= DOWN;
-        const long long plane = p.r * p.ld;
-        store_factors<PIECES, true>(block, s, p.out + t.batch * PIECES * plane, plane, p.ld, row,
-                                    col, p.r, p.r, t.col0 + BN <= t.row0);
+        store_factors<PIECES, true>(io, p.out, s, t.batch, row, col, p.r, t.col0 + BN <= t.row0);
     }
 };
 
@@ -277,43 +237,47 @@ struct NsPoly {
     static constexpr int BN = BN_;
     static constexpr int COLS = BN / 2;
     struct Params {
-        const __half* gram;
-        __half* out;
+        CUtensorMap gram;  // blocks of 64 columns
+        FactorMaps out;
         int r;
-        long long ld;
         float b, c;
     };
     const Params& p;
-    uint8_t* block;
-    Ahead ahead;
-    __device__ NsPoly(const Params& p_, const hg::Args&, int, uint8_t* block_)
-        : p(p_), block(block_) {}
-    // piece K of A at 64 of the thread's columns
-    __device__ __forceinline__ void load(const hg::Unit& t, int row, int col, int c, int k) {
-        const __half* from = p.gram + (t.batch * PIECES + k) * (p.r * p.ld) + row * p.ld + col + c;
-        ahead.load(from, p.ld * 2, p.r - row, padded_bytes<2>(p.r - (col + c)));
+    hg::WarpIo& io;
+    __device__ NsPoly(const Params& p_, const hg::Args&, int, hg::WarpIo& io_) : p(p_), io(io_) {}
+    // piece I % PIECES of A at columns I / PIECES * 64 of the thread's, into block I % 2
+    template <int I>
+    __device__ __forceinline__ void load(const hg::Unit& t, int row, int col) {
+        if constexpr (I < COLS / 64 * PIECES) {
+            constexpr int C = I / PIECES * 64;
+            if (col + C < p.r) io.load(I % 2, &p.gram, col + C, row, t.batch * PIECES + I % PIECES);
+        }
     }
     __device__ __forceinline__ void start(const hg::Unit& t, int row, int col) {
-        load(t, row, col, 0, 0);
+        if (row >= p.r) return;
+        load<0>(t, row, col);
+        load<1>(t, row, col);
     }
-    template <int C, int K>
+    template <int I>
     __device__ __forceinline__ void add(const hg::Unit& t, int row, int col, float (&s)[COLS]) {
-        const int lane = threadIdx.x & 31;
-        ahead.stage(block);
-        if constexpr (K + 1 < PIECES)
-            load(t, row, col, C, K + 1);
-        else if constexpr (C + 64 < COLS)
-            load(t, row, col, C + 64, 0);
+        if constexpr (I < COLS / 64 * PIECES) {
+            constexpr int C = I / PIECES * 64;
+            const int lane = threadIdx.x & 31;
+            if (col + C >= p.r) return;
+            io.wait_load(I % 2);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint4 v = *hg::staged(block, lane, j);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            for (int j = 0; j < 8; ++j) {
+                const uint4 v = *hg::staged(io.block(I % 2), lane, j);
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
-                s[C + 8 * j + 2 * k] = fmaf(p.b, f.x, s[C + 8 * j + 2 * k]);
-                s[C + 8 * j + 2 * k + 1] = fmaf(p.b, f.y, s[C + 8 * j + 2 * k + 1]);
+                for (int k = 0; k < 4; ++k) {
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+                    s[C + 8 * j + 2 * k] = fmaf(p.b, f.x, s[C + 8 * j + 2 * k]);
+                    s[C + 8 * j + 2 * k + 1] = fmaf(p.b, f.y, s[C + 8 * j + 2 * k + 1]);
+                }
             }
+            __syncwarp();  // read by all lanes
+            load<I + 2>(t, row, col);
         }
     }
     __device__ __forceinline__ void unit(const hg::Unit& t, int row, int col, float (&s)[COLS]) {
@@ -321,15 +285,11 @@ struct NsPoly {
         const float c = p.c * DOWN;
 #pragma unroll
         for (int j = 0; j < COLS; ++j) s[j] *= c;
-        add<0, 0>(t, row, col, s);
-        if constexpr (PIECES == 2) add<0, 1>(t, row, col, s);
-        if constexpr (COLS == 128) {
-            add<64, 0>(t, row, col, s);
-            if constexpr (PIECES == 2) add<64, 1>(t, row, col, s);
-        }
-        const long long plane = p.r * p.ld;
-        store_factors<PIECES, true>(block, s, p.out + t.batch * PIECES * plane, plane, p.ld, row,
-                                    col, p.r, p.r, t.col0 + BN <= t.row0);
+        add<0>(t, row, col, s);
+        add<1>(t, row, col, s);
+        add<2>(t, row, col, s);
+        add<3>(t, row, col, s);
+        store_factors<PIECES, true>(io, p.out, s, t.batch, row, col, p.r, t.col0 + BN <= t.row0);
     }
 };
 
@@ -339,83 +299,60 @@ struct NsUpdate {
     static constexpr int BN = BN_;
     static constexpr int COLS = BN / 2;
     struct Params {
-        float* x;           // FP32, in place
-        __half* out;        // factors, or null with the last step
+        CUtensorMap x;      // FP32, in place: blocks of 32 columns
+        FactorMaps out;
         int M, N;
-        long long ld;       // of x and the factors
         float a;
+        int last;           // the result goes out instead
         void* result;
         long long ldo, stride;
         int dtype, wide;
     };
     const Params& p;
-    uint8_t* block;
-    Ahead ahead;
-    __device__ NsUpdate(const Params& p_, const hg::Args&, int, uint8_t* block_)
-        : p(p_), block(block_) {}
+    hg::WarpIo& io;
+    __device__ NsUpdate(const Params& p_, const hg::Args&, int, hg::WarpIo& io_) : p(p_), io(io_) {}
 
-    __device__ __forceinline__ float* x_at(const hg::Unit& t, int row, int col) const {
-        return p.x + t.batch * (p.M * p.ld) + row * p.ld + col;
-    }
     __device__ __forceinline__ void start(const hg::Unit& t, int row, int col) {
-        ahead.load(x_at(t, row, col), p.ld * 4, p.M - row, padded_bytes<4>(p.N - col));
+        if (row >= p.M) return;
+        if (col < p.N) io.load(0, &p.x, col, row, t.batch);
+        if (col + 32 < p.N) io.load(1, &p.x, col + 32, row, t.batch);
     }
 
     template <int C>
     __device__ __forceinline__ void step32(const hg::Unit& t, int row, int col, float (&s)[COLS]) {
+        constexpr int B = C / 32 % 2;
         const int lane = threadIdx.x & 31;
-        const int left = p.N - (col + C);
-        if (left <= 0) return;
-        float* x = x_at(t, row, col + C);
-        ahead.stage(block);
-        if constexpr (C + 32 < COLS)
-            ahead.load(x + 32, p.ld * 4, p.M - row, padded_bytes<4>(left - 32));
+        if (col + C >= p.N) return;
+        io.wait_load(B);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const uint4 v = *hg::staged(block, lane, j);
+            const uint4 v = *hg::staged(io.block(B), lane, j);
             s[C + 4 * j] = fmaf(p.a, __uint_as_float(v.x), s[C + 4 * j] * DOWN2);
             s[C + 4 * j + 1] = fmaf(p.a, __uint_as_float(v.y), s[C + 4 * j + 1] * DOWN2);
             s[C + 4 * j + 2] = fmaf(p.a, __uint_as_float(v.z), s[C + 4 * j + 2] * DOWN2);
             s[C + 4 * j + 3] = fmaf(p.a, __uint_as_float(v.w), s[C + 4 * j + 3] * DOWN2);
         }
-        const bool inner = p.out != nullptr;
-        if (!inner && p.dtype != SGEMM_FLOAT32) return;
-#pragma unroll
-        for (int j = 0; j < 8; ++j)  // over the values that this lane has just read
-            *hg::staged(block, lane, j) =
-                make_uint4(__float_as_uint(s[C + 4 * j]), __float_as_uint(s[C + 4 * j + 1]),
-                           __float_as_uint(s[C + 4 * j + 2]), __float_as_uint(s[C + 4 * j + 3]));
-        if (inner) {
-            hg::store_block<4>(block, padded_bytes<4>(left), true, [&](int i) {
-                return row + i < p.M ? x + i * p.ld : nullptr;
-            });
+        if (!p.last) {
+            hg::stage_words<C>(io.block(B), s);  // over the values that this lane has just read
+            io.store(B, &p.x, col + C, row, t.batch);
         } else {
-            float* base = static_cast<float*>(p.result) + t.batch * p.stride + row * p.ldo + col + C;
-            hg::store_block<4>(block, min(128, left * 4), p.wide, [&](int i) {
-                return row + i < p.M ? base + i * p.ldo : nullptr;
-            });
+            __syncwarp();  // read by all lanes
         }
+        if constexpr (C + 64 < COLS)
+            if (col + C + 64 < p.N) io.load(B, &p.x, col + C + 64, row, t.batch);
     }
 
-    template <int C, bool BF16>
-    __device__ __forceinline__ void result64(const hg::Unit& t, int row, int col,
-                                             const float (&s)[COLS]) {
-        const int lane = threadIdx.x & 31;
-        const int left = p.N - (col + C);
-        if (left <= 0) return;
-        __syncwarp();
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            *hg::staged(block, lane, j) = make_uint4(
-                hg::pack2<BF16>(s[C + 8 * j], s[C + 8 * j + 1]),
-                hg::pack2<BF16>(s[C + 8 * j + 2], s[C + 8 * j + 3]),
-                hg::pack2<BF16>(s[C + 8 * j + 4], s[C + 8 * j + 5]),
-                hg::pack2<BF16>(s[C + 8 * j + 6], s[C + 8 * j + 7]));
-        unsigned short* base =
-            static_cast<unsigned short*>(p.result) + t.batch * p.stride + row * p.ldo + col + C;
-        hg::store_block<2>(block, min(128, left * 2), p.wide, [&](int i) {
-            return row + i < p.M ? base + i * p.ldo : nullptr;
-        });
+    // 32 words from word C on, through block B, to the result's columns `col` on
+    template <int C, int B, int SIZE>
+    __device__ __forceinline__ void result(const hg::Unit& t, int row, int col,
+                                           const float (&s)[COLS]) {
+        if (col >= p.N) return;
+        io.acquire(B);
+        hg::stage_words<C>(io.block(B), s);
+        const int bytes = min(128, (p.N - col) * SIZE);
+        char* base = static_cast<char*>(p.result) + (t.batch * p.stride + row * p.ldo + col) * SIZE;
+        hg::store_block<SIZE>(io.block(B),
+                              {base, p.ldo * SIZE, p.M - row, bytes, p.wide && bytes % 16 == 0});
     }
 
     __device__ __forceinline__ void unit(const hg::Unit& t, int row, int col, float (&s)[COLS]) {
@@ -426,19 +363,28 @@ struct NsUpdate {
             step32<64>(t, row, col, s);
             step32<96>(t, row, col, s);
         }
-        if (p.out) {
+        if (!p.last) {
 #pragma unroll
             for (int j = 0; j < COLS; ++j) s[j] *= UP;
-            const long long plane = p.M * p.ld;
-            store_factors<PIECES, false>(block, s, p.out + t.batch * PIECES * plane, plane, p.ld,
-                                         row, col, p.M, p.N, false);
-        } else if (p.dtype == SGEMM_BFLOAT16) {
-            result64<0, true>(t, row, col, s);
-            if constexpr (COLS == 128) result64<64, true>(t, row, col, s);
-        } else if (p.dtype == SGEMM_FLOAT16) {
-            result64<0, false>(t, row, col, s);
-            if constexpr (COLS == 128) result64<64, false>(t, row, col, s);
+            store_factors<PIECES, false>(io, p.out, s, t.batch, row, col, p.N, false);
+            return;
         }
+        if (p.dtype == SGEMM_FLOAT32) {
+            result<0, 0, 4>(t, row, col, s);
+            result<32, 1, 4>(t, row, col + 32, s);
+            if constexpr (COLS == 128) {
+                result<64, 0, 4>(t, row, col + 64, s);
+                result<96, 1, 4>(t, row, col + 96, s);
+            }
+            return;
+        }
+        const bool bf16 = p.dtype == SGEMM_BFLOAT16;
+#pragma unroll
+        for (int j = 0; j < COLS; j += 2)
+            s[j / 2] = __uint_as_float(bf16 ? hg::pack2<true>(s[j], s[j + 1])
+                                            : hg::pack2<false>(s[j], s[j + 1]));
+        result<0, 0, 2>(t, row, col, s);
+        if constexpr (COLS == 128) result<32, 1, 2>(t, row, col + 64, s);
     }
 };
 
@@ -530,6 +476,19 @@ cudaError_t iterate(const Call& a, const DeviceInfo& info, float* x, __half* (&f
     pp.M = pp.N = pp.K = r;
     pp.symmetric = 1;
     pp.idesc = hg::instruction(false, false, false);
+    // the epilogues' blocks
+    auto factor_maps = [&](FactorMaps& m, const __half* base, int cols, int rows, int ld) {
+        const long long plane = (long long)rows * ld;
+        return hg::encode_block(&m.straight, base, 2, cols, rows, ld, slabs, plane, 64, 32) &&
+               hg::encode_block(&m.turned, base, 2, cols, rows, ld, slabs, plane, 32, 64);
+    };
+    FactorMaps gram_out, poly_out, x_out[2];
+    CUtensorMap x_map;
+    if (!factor_maps(gram_out, gram, r, r, rp) || !factor_maps(poly_out, poly, r, r, rp) ||
+        !factor_maps(x_out[0], factors[0], a.N, a.M, Np) ||
+        !factor_maps(x_out[1], factors[1], a.N, a.M, Np) ||
+        !hg::encode_block(&x_map, x, 4, a.N, a.M, Np, a.count, x_plane, 32, 32))
+        return cudaErrorInvalidValue;
     const int size = a.dtype == SGEMM_FLOAT32 ? 4 : 2;
     const int wide = aligned16(a.out) && a.ldo * size % 16 == 0 && a.stride_o * size % 16 == 0;
     for (int i = 0; i < a.steps; ++i) {
@@ -539,15 +498,15 @@ cudaError_t iterate(const Call& a, const DeviceInfo& info, float* x, __half* (&f
         poly_args.counter = counters + 3 * i + 1;
         u.counter = counters + 3 * i + 2;
         cudaError_t e =
-            hg::launch_gemm<NsGram<BN, PIECES>>(g, {gram, r, rp}, info.sm_count, s);
+            hg::launch_gemm<NsGram<BN, PIECES>>(g, {gram_out, r}, info.sm_count, s);
         if (e != cudaSuccess) return e;
-        e = hg::launch_gemm<NsPoly<BN, PIECES>>(poly_args, {gram, poly, r, rp, c[1], c[2]},
-                                                info.sm_count, s);
+        e = hg::launch_gemm<NsPoly<BN, PIECES>>(
+            poly_args, {gram_out.straight, poly_out, r, c[1], c[2]}, info.sm_count, s);
         if (e != cudaSuccess) return e;
         const bool last = i == a.steps - 1;
         e = hg::launch_gemm<NsUpdate<BN, PIECES>>(
-            u, {x, last ? nullptr : factors[(i + 1) & 1], a.M, a.N, Np, c[0], a.out, a.ldo,
-                a.stride_o, a.dtype, wide},
+            u, {x_map, x_out[(i + 1) & 1], a.M, a.N, c[0], last, a.out, a.ldo, a.stride_o, a.dtype,
+                wide},
             info.sm_count, s);
         if (e != cudaSuccess) return e;
     }
