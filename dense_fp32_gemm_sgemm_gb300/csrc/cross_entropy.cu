@@ -229,6 +229,8 @@ template <int BN_, Keep KEEP>
 struct CeForward {
     static constexpr int BN = BN_;
     static constexpr int COLS = BN / 2;
+    static constexpr int PROBLEMS = 1;
+    static constexpr bool CHAIN = false;
     struct Params {
         float2* stats;   // [block of COLS columns][row of the chunk]: maximum, sum
         float* picked;   // [row of the chunk]
@@ -240,7 +242,7 @@ struct CeForward {
     const Params& p;
     hg::WarpIo& io;
     int live;
-    __device__ CeForward(const Params& p_, const hg::Args&, int live_, hg::WarpIo& io_)
+    __device__ CeForward(const Params& p_, int live_, hg::WarpIo& io_)
         : p(p_), io(io_), live(live_) {}
 
     // 32 words of every lane as block B's rows to columns `col` on of `kept`
@@ -529,6 +531,8 @@ template <bool SUMS>
 struct CeGrad {
     static constexpr int BN = 256;
     static constexpr int COLS = BN / 2;
+    static constexpr int PROBLEMS = 2;
+    static constexpr bool CHAIN = false;
     struct Params {
         GradOut out[2];
         const CeInfo* info;
@@ -538,7 +542,7 @@ struct CeGrad {
     hg::WarpIo& io;
     int live;
     float scale;
-    __device__ CeGrad(const Params& p_, const hg::Args&, int live_, hg::WarpIo& io_)
+    __device__ CeGrad(const Params& p_, int live_, hg::WarpIo& io_)
         : p(p_), io(io_), live(live_) {
         scale = p.info->c_max * p.down;
     }
@@ -730,7 +734,7 @@ int check(const sgemm_ce& a) {
 }
 
 template <int BN>
-cudaError_t forward(Keep keep, const hg::Args& g, float2* stats, float* picked, const int* label,
+cudaError_t forward(Keep keep, const hg::Args<1>& g, float2* stats, float* picked, const int* label,
                     const CUtensorMap& kept, int stats_pitch, int V, int sm_count, cudaStream_t s) {
     switch (keep) {
         case Keep::none:
@@ -823,7 +827,8 @@ cudaError_t run(const sgemm_ce& a, const DeviceInfo& info, int dev, cudaStream_t
 
     // operands as tensors
     const void* g_of = f32 ? static_cast<const void*>(g_planes) : kept;
-    hg::Args fwd, bwd;
+    hg::Args<1> fwd;
+    hg::Args<2> bwd;
     std::memset(&fwd, 0, sizeof fwd);
     std::memset(&bwd, 0, sizeof bwd);
     const int half = narrow ? 64 : 128;
@@ -846,6 +851,10 @@ cudaError_t run(const sgemm_ce& a, const DeviceInfo& info, int dev, cudaStream_t
     fwd.live = bwd.live = &ci->count;
     fwd.live_max = bwd.live_max = chunk;
     fwd.err = bwd.err = info.error_word;
+    // losses are FP32 whatever the inputs (16 stages: off by 2^-19 of a sum at most, 3 to 4e-7
+    // of lse measured; 8: 1.5e-7, and a large product 1 % slower); 16-bit gradients bear 2^-18
+    fwd.seg_steps = f32 ? 8 : 16;
+    bwd.seg_steps = f32 ? 8 : 32;
 
     CUtensorMap kept_map;
     std::memset(&kept_map, 0, sizeof kept_map);

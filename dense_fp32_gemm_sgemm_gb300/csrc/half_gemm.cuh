@@ -12,10 +12,11 @@
 //
 // Accumulation. The tensor core cuts off, rather than rounds, the bits that an addition to its
 // FP32 accumulator shifts out: some 2^-25 of the accumulator for each MMA, always towards zero.
-// After SEG_STEPS stages (32 MMAs, at most 2^-20 of a sum's size) the accumulator is therefore
-// added to FP32 registers, rounded to nearest, and starts again at zero. The two accumulators
-// of a CTA pair alternate, so the additions overlap the next stages' MMAs; 32 MMAs of 256 x 256
-// take 4096 cycles, the additions some 500.
+// After seg_steps stages (4 MMAs each) the accumulator is therefore added to FP32 registers, rounded
+// to nearest, and starts again at zero. The two accumulators of a CTA pair alternate, so the
+// additions overlap the next stages' MMAs, and so does the epilogue as far as two segments reach
+// (a stage of 256 columns takes 512 cycles): short segments are for results in FP32, long ones let
+// a long epilogue pass unnoticed.
 //
 // Units are claimed from a counter, so that long and short ones may be mixed in a launch. Which
 // pair computes a unit does not change what is computed.
@@ -35,7 +36,6 @@ constexpr int BM = 256;       // rows of a tile (both CTAs)
 constexpr int HALF_M = 128;   // rows of one CTA
 constexpr int BK = 64;        // reduction elements in a stage: 128 bytes
 constexpr int STAGES = 5;
-constexpr int SEG_STEPS = 8;  // stages in an accumulator segment
 constexpr int SLOTS = 4;      // units handed out ahead
 constexpr int EPI_WARPS = 8;
 constexpr int EPI_WARP0 = 4;  // warp 3 only fills up the first warpgroup
@@ -69,20 +69,27 @@ struct Problem {
     int a_mn, b_mn;     // operand stored with its other index contiguous (else with k)
     int a_row, b_row;   // added to the row coordinate (k or the other index, whichever is a row)
     int planes_a, planes_b;
-    int products;       // pairs of planes, smallest products first
+    int products;       // pairs of planes, each staged for itself
     unsigned char pa[MAX_PRODUCTS], pb[MAX_PRODUCTS];
     unsigned idesc;     // instruction descriptor without N
 };
 
+template <int PROBLEMS>
 struct Args {
-    CUtensorMap a[2], b[2];  // 3-D: contiguous index, row, batch * planes + plane
-    Problem p[2];
+    CUtensorMap a[PROBLEMS], b[PROBLEMS];  // 3-D: contiguous index, row, batch * planes + plane
+    Problem p[PROBLEMS];
     int problems;
     const int* live;  // number of rows in all, or null
     int live0;        // rows before this launch's
     int live_max;     // rows of this launch at most
     int* counter;     // claimed units, zero before the launch
     int* err;
+    // A chain of products that build on one another: rounds of three problems, the odd rounds with
+    // the last three. done[i * batch + e] counts the epilogue warps' finished units of product e of
+    // phase i = 3 round + problem, zero before the launch.
+    int rounds;
+    int* done;
+    int seg_steps;  // stages in an accumulator segment
 };
 
 // A unit of work.
@@ -90,6 +97,7 @@ struct Unit {
     int problem, batch, split;
     int row0, col0;  // of the tile
     int kb0, kb1;    // blocks of the reduction
+    int phase;       // of a chain
 };
 
 __host__ __device__ inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
@@ -110,17 +118,45 @@ __host__ __device__ inline int unit_count(const Problem& p, int live) {
     return p.batch * p.splits * tile_count<BN>(p, ceil_div(m, BM), ceil_div(p.N, BN));
 }
 
+// Units of the launch's problems, and of all together.
+struct Units {
+    int first, second, third, all;
+    template <int BN, bool CHAIN, class ARGS>
+    static __device__ __forceinline__ Units of(const ARGS& g, int live) {
+        Units n;
+        n.first = unit_count<BN>(g.p[0], live);
+        n.second = n.third = 0;
+        if (CHAIN || g.problems > 1) n.second = unit_count<BN>(g.p[1], live);
+        if constexpr (CHAIN) n.third = unit_count<BN>(g.p[2], live);
+        n.all = n.first + n.second + n.third;
+        if (CHAIN) n.all *= g.rounds;
+        return n;
+    }
+};
+
 // Unit u of the launch; u counts over all its problems.
-template <int BN>
-__device__ inline Unit unit_at(const Args& g, int u, int live) {
+template <int BN, bool CHAIN, class ARGS>
+__device__ inline Unit unit_at(const ARGS& g, const Units& n, int u, int live) {
     Unit t;
     t.problem = 0;
-    if (g.problems > 1) {
-        const int first = unit_count<BN>(g.p[0], live);
-        if (u >= first) {
+    t.phase = 0;
+    if constexpr (CHAIN) {
+        const int each = n.first + n.second + n.third;
+        const int round = u / each;
+        u -= round * each;
+        if (u >= n.first) {
+            u -= n.first;
             t.problem = 1;
-            u -= first;
+            if (u >= n.second) {
+                u -= n.second;
+                t.problem = 2;
+            }
         }
+        t.phase = 3 * round + t.problem;
+        t.problem += 3 * (round & 1);
+    } else if (u >= n.first) {
+        t.problem = 1;
+        u -= n.first;
     }
     const Problem& p = g.p[t.problem];
     const int tiles_m = ceil_div(p.dyn == 1 ? live : p.M, BM), tiles_n = ceil_div(p.N, BN);
@@ -169,16 +205,15 @@ struct Smem {
     volatile int* slot_ptr;
     uint32_t* tmem_slot;
     volatile int* abort_flag;
-    __device__ uint32_t full(int s) const { return bar0 + 8u * s; }
-    __device__ uint32_t empty(int s) const { return bar0 + 8u * (STAGES + s); }
-    __device__ uint32_t acc_full(int b) const { return bar0 + 8u * (2 * STAGES + b); }
-    __device__ uint32_t acc_empty(int b) const { return bar0 + 8u * (2 * STAGES + 2 + b); }
-    __device__ uint32_t slot_full(int i) const { return bar0 + 8u * (2 * STAGES + 4 + i); }
-    __device__ uint32_t slot_empty(int i) const {
-        return bar0 + 8u * (2 * STAGES + 4 + SLOTS + i);
-    }
-    __device__ uint32_t drain() const { return bar0 + 8u * (2 * STAGES + 4 + 2 * SLOTS); }
-    __device__ uint32_t loaded(int i) const { return bar0 + 8u * (2 * STAGES + 5 + 2 * SLOTS + i); }
+    __device__ uint32_t at(int i) const { return bar0 + 8u * i; }
+    __device__ uint32_t full(int s) const { return at(s); }
+    __device__ uint32_t empty(int s) const { return at(STAGES + s); }
+    __device__ uint32_t acc_full(int b) const { return at(2 * STAGES + b); }
+    __device__ uint32_t acc_empty(int b) const { return at(2 * STAGES + 2 + b); }
+    __device__ uint32_t slot_full(int i) const { return at(2 * STAGES + 4 + i); }
+    __device__ uint32_t slot_empty(int i) const { return at(2 * STAGES + 4 + SLOTS + i); }
+    __device__ uint32_t drain() const { return at(2 * STAGES + 4 + 2 * SLOTS); }
+    __device__ uint32_t loaded(int i) const { return at(2 * STAGES + 5 + 2 * SLOTS + i); }
 };
 
 template <int BN>
@@ -354,15 +389,22 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 }
 
 // ---- the kernel -----------------------------------------------------------------------------
-// EPI::BN, EPI::Params, and EPI(params, args, live, warp's io) with
+// EPI::BN, EPI::Params, and EPI(params, live, warp's io) with
+//   bool reads(const Unit&): whether start reads what the phase before wrote (a chain's alone)
 //   void start(const Unit&, int row, int col)
 //   void unit(const Unit&, int row, int col, float (&acc)[BN / 2])
 // called by each epilogue warp at the beginning of a unit (to load what it will need) and with its
 // sums: lane l holds row `row` + l, columns col .. col + BN / 2.
+// EPI::PROBLEMS: of the launch at most. EPI::CHAIN: units are done in order, and one of a phase
+// waits until all of the phase before that belong to the same product have been stored. Every earlier unit was claimed by a CTA
+// that runs, and waits for still earlier ones only, so that all waits end however many CTAs the
+// GPU runs at a time.
 template <class EPI>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
-    half_gemm_kernel(const __grid_constant__ Args g, const __grid_constant__ typename EPI::Params ep) {
+    half_gemm_kernel(const __grid_constant__ Args<EPI::PROBLEMS> g,
+                     const __grid_constant__ typename EPI::Params ep) {
     constexpr int BN = EPI::BN;
+    constexpr bool CHAIN = EPI::CHAIN;
     constexpr int COLS = BN / 2;  // columns of an epilogue warp
     extern __shared__ uint8_t smem_raw[];
     const Smem sm = carve<BN>(smem_raw);
@@ -370,10 +412,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const uint32_t rank = ptx::cluster_ctarank();
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < STAGES; ++s) {
-            ptx::mbar_init(sm.full(s), 1);
-            ptx::mbar_init(sm.empty(s), 1);
-        }
+        for (int s = 0; s < 2 * STAGES; ++s) ptx::mbar_init(sm.at(s), 1);  // full, empty
         for (int b = 0; b < 2; ++b) {
             ptx::mbar_init(sm.acc_full(b), 1);
             ptx::mbar_init(sm.acc_empty(b), 2 * EPI_WARPS);
@@ -406,6 +445,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 
     int live = 0;
     if (g.live) live = min(max(*g.live - g.live0, 0), g.live_max);
+    const Units n_units = Units::of<BN, CHAIN>(g, live);
+    // chain: what the phase before this unit's computes of its product has been stored, for TMA to
+    // read
+    auto wait_before = [&](const Unit& t) {
+        if (t.phase == 0) return true;
+        const int type = (t.phase - 1) % 3, batch = g.p[0].batch;
+        const int units =
+            type == 0 ? n_units.first : type == 1 ? n_units.second : n_units.third;
+        bool ok = true;
+        if (lane == 0)
+            ok = wait_count(g.done + (t.phase - 1) * batch + t.batch, 2 * EPI_WARPS * (units / batch),
+                            sm.abort_flag, g.err);
+        ok = __all_sync(~0u, ok) != 0;
+        ptx::fence_proxy_async_global();
+        return ok;
+    };
     // the unit in slot i, or -1 at the end or when a wait ran out
     auto take = [&](int i) {
         const int s = i % SLOTS;
@@ -429,11 +484,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             // all lanes go through the loop with equal values, one of them issues
             const bool is_a = warp == 0;
             const bool hands_out = is_a && rank == 0;
-            int units = unit_count<BN>(g.p[0], live);
-            if (g.problems > 1) units += unit_count<BN>(g.p[1], live);
-            const int pairs = gridDim.x >> 1;
-            const uint32_t full0 = ptx::mapa_shared(sm.full(0), 0);  // the first CTA's barriers
+            const int units = n_units.all;
+            const uint32_t full0 = sm.full(0), empty0 = sm.empty(0);
+            const uint32_t signal0 = ptx::mapa_shared(full0, 0);  // the first CTA's barriers
+            const bool expects = is_a && rank == 0;
+            const uint32_t ring = sm.ring + (is_a ? 0 : A_BYTES);
+            // the first units are given out by the pairs' numbers, in a chain claimed like all
+            // others: a pair may not be running yet
+            const int pairs = CHAIN ? 0 : gridDim.x >> 1;
             int next = blockIdx.x >> 1;
+            if (CHAIN && hands_out) {
+                if (lane == 0) next = atomicAdd(g.counter, 1);
+                next = __shfl_sync(~0u, next, 0);
+            }
             int s = 0;
             uint32_t ph = 0;
             for (int i = 0;; ++i) {
@@ -458,32 +521,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                     if (u >= 0 && lane == 0) taken(i);
                 }
                 if (u < 0) break;
-                const Unit t = unit_at<BN>(g, u, live);
+                const Unit t = unit_at<BN, CHAIN>(g, n_units, u, live);
                 const Problem& p = g.p[t.problem];
                 const CUtensorMap* map = is_a ? &g.a[t.problem] : &g.b[t.problem];
                 const bool mn = is_a ? p.a_mn : p.b_mn;
-                const int products = p.products;
                 const unsigned char* planes = is_a ? p.pa : p.pb;
                 const int z0 = t.batch * (is_a ? p.planes_a : p.planes_b);
-                const int z1 = z0 + planes[0];
+                const int products = p.products;
+                unsigned order = 0;  // the products' planes, four bits each
+                for (int q = 0; q < products; ++q) order |= unsigned(planes[q]) << (4 * q);
                 // coordinates of the first box, and how they move on
                 const int o = is_a ? t.row0 + int(rank) * HALF_M : t.col0 + int(rank) * (BN / 2);
                 const int k0 = t.kb0 * BK, first = is_a ? p.a_row : p.b_row;
                 int x = mn ? o : k0, y = first + (mn ? k0 : o);
                 const int dx = mn ? 0 : BK, dy = mn ? BK : 0;
                 const bool two = mn && (is_a || BN == 256);
-                const uint32_t to = sm.ring + (is_a ? 0 : A_BYTES);
-                bool ok = true;
+                bool ok = !CHAIN || wait_before(t);
                 for (int kb = t.kb0; ok && kb < t.kb1; ++kb) {
+                    unsigned planes_left = order;
                     for (int q = 0; q < products; ++q) {
-                        const int z = products == 1 ? z1 : z0 + planes[q];
-                        ok = wait_all(sm.empty(s), ph ^ 1u);
+                        const int z = z0 + int(planes_left & 15u);
+                        planes_left >>= 4;
+                        ok = wait_all(empty0 + 8u * s, ph ^ 1u);
                         if (!ok) break;
-                        const uint32_t bar = full0 + 8u * s;
-                        const uint32_t st = to + uint32_t(s) * STAGE_BYTES<BN>;
+                        const uint32_t bar = signal0 + 8u * s;
+                        const uint32_t st = ring + uint32_t(s) * STAGE_BYTES<BN>;
                         // the bytes of both CTAs; some may have arrived already
-                        if (hands_out)
-                            ptx::mbar_arrive_expect_tx_elect(sm.full(s), 2 * STAGE_BYTES<BN>);
+                        if (expects)
+                            ptx::mbar_arrive_expect_tx_elect(full0 + 8u * s, 2 * STAGE_BYTES<BN>);
                         ptx::tma_load_3d_pair(st, map, bar, x, y, z);
                         if (two) ptx::tma_load_3d_pair(st + CHUNK_BYTES, map, bar, x + 64, y, z);
                         if (++s == STAGES) {
@@ -514,18 +579,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 __syncwarp();
                 if (u < 0) break;
                 if (lane == 0) taken(i);
-                const Unit t = unit_at<BN>(g, u, live);
+                const Unit t = unit_at<BN, CHAIN>(g, n_units, u, live);
                 const Problem& p = g.p[t.problem];
                 const uint32_t idesc = p.idesc | (uint32_t(BN >> 3) << 17);
                 const OperandDesc a(sm.ring, p.a_mn), b(sm.ring + A_BYTES, p.b_mn);
                 int left = (t.kb1 - t.kb0) * p.products;
-                for (; ok && left > 0; left -= SEG_STEPS, ++seg) {
+                for (; ok && left > 0; left -= g.seg_steps, ++seg) {
                     const int half = seg & 1;
                     ok = wait_all(sm.acc_empty(half), ((seg >> 1) & 1) ^ 1);
                     if (!ok) break;
                     ptx::tc_fence_after();
                     const uint32_t d = tmem + uint32_t(half * BN);
-                    const int steps = min(left, SEG_STEPS);
+                    const int steps = min(left, g.seg_steps);
                     for (int j = 0; j < steps; ++j) {
                         ok = wait_all(sm.full(s), ph);
                         if (!ok) break;
@@ -563,7 +628,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         io.abort_flag = sm.abort_flag;
         io.err = g.err;
         io.first = lane == 0;
-        EPI epi(ep, g, live, io);
+        EPI epi(ep, live, io);
         float acc[COLS];
         int seg = 0;
         bool ok = true;
@@ -572,10 +637,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             __syncwarp();  // all lanes have read the slot
             if (u < 0) break;
             if (lane == 0) taken(i);
-            const Unit t = unit_at<BN>(g, u, live);
+            const Unit t = unit_at<BN, CHAIN>(g, n_units, u, live);
             const int steps = (t.kb1 - t.kb0) * g.p[t.problem].products;
-            const int segs = (steps + SEG_STEPS - 1) / SEG_STEPS;
+            const int segs = (steps + g.seg_steps - 1) / g.seg_steps;
             const int row = t.row0 + int(rank) * HALF_M + q * 32, col = t.col0 + h * COLS;
+            if constexpr (CHAIN) {
+                if (epi.reads(t) && !wait_before(t)) break;
+            }
             epi.start(t, row, col);
             for (int sg = 0; sg < segs; ++sg, ++seg) {
                 const int b = seg & 1;
@@ -612,6 +680,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 for (int j = 0; j < COLS; ++j) acc[j] = 0.f;
             }
             epi.unit(t, row, col, acc);
+            if constexpr (CHAIN) {
+                __syncwarp();
+                if (lane == 0) {
+                    ptx::bulk_wait0();  // its stores are in global memory
+                    ptx::fence_proxy_async_global();
+                    __threadfence();
+                    ptx::red_release_gpu_add(g.done + t.phase * g.p[0].batch + t.batch, 1);
+                }
+            }
         }
         io.finish();
     }
@@ -660,13 +737,17 @@ cudaError_t launch(void (*kernel)(KArgs...), unsigned grid, unsigned block, size
 inline int box_rows(bool mn, int rows_of_cta) { return mn ? BK : rows_of_cta; }
 
 template <class EPI>
-cudaError_t launch_gemm(const Args& g, const typename EPI::Params& ep, int sm_count,
+cudaError_t launch_gemm(const Args<EPI::PROBLEMS>& g, const typename EPI::Params& ep, int sm_count,
                         cudaStream_t stream) {
     constexpr int bytes = SMEM_BYTES<EPI::BN>;
     cudaError_t e = set_smem_limit_once<half_gemm_kernel<EPI>>(bytes);
     if (e != cudaSuccess) return e;
+    // pairs for all units, in a chain for those of its largest phase
     int units = 0;
-    for (int i = 0; i < g.problems; ++i) units += unit_count<EPI::BN>(g.p[i], g.live_max);
+    for (int i = 0; i < g.problems; ++i) {
+        const int n = unit_count<EPI::BN>(g.p[i], g.live_max);
+        units = !EPI::CHAIN ? units + n : units > n ? units : n;
+    }
     if (units == 0) return cudaSuccess;
     const int pairs = sm_count / 2 > 0 ? sm_count / 2 : 1;
     return launch(half_gemm_kernel<EPI>, 2u * unsigned(units < pairs ? units : pairs), THREADS,

@@ -7,14 +7,15 @@
 // r r q + r r r + 2 r r q operations.
 //
 // Precision. The iteration multiplies small singular values by a (3.4) each step, and with them
-// whatever rounding put there. So X itself is kept in FP32, and only the factors of the products
-// are rounded: the term a X, which carries the small values, is exact, and (b A + c A A) X adds
-// little to them. With the factors in FP16 (11 bits) the result is off by 0.5 to 1.7e-3 of its
-// RMS for normal, low-rank and graded matrices, about as much as by the rounding of a bfloat16
-// result (1.7e-3); factors in bfloat16 give 0.5 to 1.3e-2, and 1 to 20e-2 where X itself is rounded too.
-// float16 and float32 results take two FP16 pieces of each factor (22 bits) and three products:
-// 3e-7 to 4e-6, as much as FP32 arithmetic's. (CPU simulations of 256 x 256 to 512 x 1024.)
-// Factors are held times 2^8, so that entries down to 2^-22 keep all their bits.
+// whatever rounding put there. So X itself is kept in two FP16 pieces, 22 bits, and only the factors
+// of the products are rounded further: the term a X, which carries the small values, keeps its
+// bits, and (b A + c A A) X adds little to them. With factors of one FP16 piece (11 bits) the
+// result is off by 0.5 to 1.7e-3 of its RMS for normal, low-rank and graded matrices, about as much
+// as by the rounding of a bfloat16 result (1.7e-3); bfloat16 factors give 0.5 to 1.3e-2, and 1 to
+// 20e-2 where X is rounded to them too. float16 and float32 results take both pieces of each factor
+// and three products: 0.3 to 6e-6, where FP32 arithmetic throughout gives 0.2 to 3e-6. (CPU
+// simulations of 256 x 256 to 512 x 1024.) The pieces are of values times a power of two, so that
+// small entries stay in FP16's normal range: 2^13 for X, 2^12 for A, 2^10 for the polynomial.
 #include <algorithm>
 #include <cstring>
 
@@ -24,12 +25,11 @@
 namespace sgemm {
 namespace {
 
-constexpr float UP = 256.f;             // scale of the factors
-constexpr float DOWN = 1.f / UP;
-constexpr float DOWN2 = DOWN * DOWN;    // of their products
+constexpr float UP_X = 0x1p13f, UP_A = 0x1p12f, UP_P = 0x1p10f;  // scales of the pieces
 constexpr int NORM_THREADS = 256;
 constexpr int MAX_NORM_CTAS = 304;      // for one matrix
 constexpr int CONVERT_THREADS = 256;
+constexpr int MAX_STEPS = 64;
 
 __device__ __forceinline__ float load(const float* p) { return *p; }
 __device__ __forceinline__ float load(const __nv_bfloat16* p) { return __bfloat162float(*p); }
@@ -80,19 +80,12 @@ __global__ void __launch_bounds__(NORM_THREADS)
     }
 }
 
-// One or two FP16 pieces of v.
-template <int PIECES>
-__device__ __forceinline__ void pieces_of(float v, __half (&p)[PIECES]) {
-    p[0] = __float2half_rn(v);
-    if constexpr (PIECES == 2) p[1] = __float2half_rn(v - __half2float(p[0]));
-}
-
-// X = G / (norm + eps), in FP32 and as factors. Rows of Np elements, zeros behind N.
-template <class T_IN, int PIECES>
+// X = G / (norm + eps) in two pieces. Rows of Np elements, zeros behind N.
+template <class T_IN>
 __global__ void __launch_bounds__(CONVERT_THREADS)
     ns_convert(const T_IN* __restrict__ g, long long ld, long long stride, int M, int N, int Np,
-               const double* __restrict__ partial, int partials, float eps, float* __restrict__ x,
-               __half* __restrict__ planes) {
+               const double* __restrict__ partial, int partials, float eps,
+               __half* __restrict__ x) {
     __shared__ double sums[CONVERT_THREADS / 32];
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
@@ -107,37 +100,35 @@ __global__ void __launch_bounds__(CONVERT_THREADS)
     for (int w = 0; w < CONVERT_THREADS / 32; ++w) sum += sums[w];
     const double norm = sqrt(sum) + double(eps);
     const float by = float(norm);
-    // a norm outside FP32's range is divided by in two steps
+    // a norm outside FP32's range is divided by in FP64
     const bool plain = by > 0x1p-100f && by < 0x1p100f;
     const T_IN* from = g + blockIdx.y * stride;
     const long long plane = (long long)M * Np;
-    float* to = x + blockIdx.y * plane;
-    __half* pl = planes + blockIdx.y * PIECES * plane;
+    __half* to = x + blockIdx.y * 2 * plane;
     const int groups = Np / 8;
     const long long all = (long long)M * groups;
     for (long long i = (long long)blockIdx.x * CONVERT_THREADS + threadIdx.x; i < all;
          i += (long long)gridDim.x * CONVERT_THREADS) {
         const int row = int(i / groups), c0 = int(i - (long long)row * groups) * 8;
         const T_IN* p = from + row * ld + c0;
-        float v[8];
-        __half q[PIECES][8];
+        __half2 high[4], low[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            v[j] = c0 + j < N ? load(p + j) : 0.f;
-            // columns behind N stay zero, whatever the norm is
-            if (c0 + j < N) v[j] = plain ? v[j] / by : float(double(v[j]) / norm);
-            __half w[PIECES];
-            pieces_of<PIECES>(v[j] * UP, w);
+        for (int j = 0; j < 8; j += 2) {
+            float v[2];
 #pragma unroll
-            for (int k = 0; k < PIECES; ++k) q[k][j] = w[k];
+            for (int k = 0; k < 2; ++k) {
+                const int c = c0 + j + k;
+                v[k] = c < N ? load(p + j + k) : 0.f;
+                // columns behind N stay zero, whatever the norm is
+                if (c < N) v[k] = (plain ? v[k] / by : float(double(v[k]) / norm)) * UP_X;
+            }
+            high[j / 2] = __floats2half2_rn(v[0], v[1]);
+            const float2 h = __half22float2(high[j / 2]);
+            low[j / 2] = __floats2half2_rn(v[0] - h.x, v[1] - h.y);
         }
-        float4* o = reinterpret_cast<float4*>(to + row * (long long)Np + c0);
-        o[0] = make_float4(v[0], v[1], v[2], v[3]);
-        o[1] = make_float4(v[4], v[5], v[6], v[7]);
-#pragma unroll
-        for (int k = 0; k < PIECES; ++k)
-            *reinterpret_cast<uint4*>(pl + k * plane + row * (long long)Np + c0) =
-                *reinterpret_cast<const uint4*>(q[k]);
+        __half* o = to + row * (long long)Np + c0;
+        *reinterpret_cast<uint4*>(o) = *reinterpret_cast<const uint4*>(high);
+        *reinterpret_cast<uint4*>(o + plane) = *reinterpret_cast<const uint4*>(low);
     }
 }
 
@@ -210,6 +201,59 @@ __device__ __forceinline__ void store_factors(hg::WarpIo& io, const FactorMaps& 
     }
 }
 
+// s = s + f * (the pieces' sum) over a thread's columns: PIECES pieces of a matrix in blocks of 64
+// columns, through the two staging blocks in turn, the next two on their way.
+template <int COLS, int PIECES>
+struct Adder {
+    static constexpr int BLOCKS = COLS / 64 * PIECES;
+    // piece I % PIECES of columns I / PIECES * 64 on, into staging block I % 2
+    template <int I>
+    static __device__ __forceinline__ void load(hg::WarpIo& io, const CUtensorMap* from, int slab,
+                                                int row, int col, int cols_n) {
+        if constexpr (I < BLOCKS) {
+            constexpr int C = I / PIECES * 64;
+            if (col + C < cols_n) io.load(I % 2, from, col + C, row, slab + I % PIECES);
+        }
+    }
+    static __device__ __forceinline__ void start(hg::WarpIo& io, const CUtensorMap* from, int slab,
+                                                 int row, int col, int cols_n) {
+        load<0>(io, from, slab, row, col, cols_n);
+        load<1>(io, from, slab, row, col, cols_n);
+    }
+    template <int I>
+    static __device__ __forceinline__ void add(hg::WarpIo& io, const CUtensorMap* from, int slab,
+                                               int row, int col, int cols_n, float f,
+                                               float (&s)[COLS]) {
+        if constexpr (I < BLOCKS) {
+            constexpr int C = I / PIECES * 64;
+            if (col + C >= cols_n) return;
+            const int lane = threadIdx.x & 31;
+            io.wait_load(I % 2);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint4 v = *hg::staged(io.block(I % 2), lane, j);
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+                    s[C + 8 * j + 2 * k] = fmaf(f, x.x, s[C + 8 * j + 2 * k]);
+                    s[C + 8 * j + 2 * k + 1] = fmaf(f, x.y, s[C + 8 * j + 2 * k + 1]);
+                }
+            }
+            __syncwarp();  // read by all lanes
+            load<I + 2>(io, from, slab, row, col, cols_n);
+        }
+    }
+    static __device__ __forceinline__ void run(hg::WarpIo& io, const CUtensorMap* from, int slab,
+                                               int row, int col, int cols_n, float f,
+                                               float (&s)[COLS]) {
+        add<0>(io, from, slab, row, col, cols_n, f, s);
+        add<1>(io, from, slab, row, col, cols_n, f, s);
+        add<2>(io, from, slab, row, col, cols_n, f, s);
+        add<3>(io, from, slab, row, col, cols_n, f, s);
+    }
+};
+
 // A = X X^T: the factors of A, from the tiles at and below the diagonal.
 template <int BN_, int PIECES>
 struct NsGram {
@@ -221,12 +265,11 @@ struct NsGram {
     };
     const Params& p;
     hg::WarpIo& io;
-    __device__ NsGram(const Params& p_, const hg::Args&, int, hg::WarpIo& io_) : p(p_), io(io_) {}
-    __device__ __forceinline__ void start(const hg::Unit&, int, int) {}
+    __device__ NsGram(const Params& p_, hg::WarpIo& io_) : p(p_), io(io_) {}
     __device__ __forceinline__ void unit(const hg::Unit& t, int row, int col, float (&s)[COLS]) {
         if (row >= p.r) return;
 #pragma unroll
-        for (int j = 0; j < COLS; ++j) s[j] *= DOWN;
+        for (int j = 0; j < COLS; ++j) s[j] *= UP_A / (UP_X * UP_X);
         store_factors<PIECES, true>(io, p.out, s, t.batch, row, col, p.r, t.col0 + BN <= t.row0);
     }
 };
@@ -236,110 +279,47 @@ template <int BN_, int PIECES>
 struct NsPoly {
     static constexpr int BN = BN_;
     static constexpr int COLS = BN / 2;
+    using Add = Adder<COLS, PIECES>;
     struct Params {
-        CUtensorMap gram;  // blocks of 64 columns
+        CUtensorMap gram;
         FactorMaps out;
         int r;
-        float b, c;
     };
     const Params& p;
     hg::WarpIo& io;
-    __device__ NsPoly(const Params& p_, const hg::Args&, int, hg::WarpIo& io_) : p(p_), io(io_) {}
-    // piece I % PIECES of A at columns I / PIECES * 64 of the thread's, into block I % 2
-    template <int I>
-    __device__ __forceinline__ void load(const hg::Unit& t, int row, int col) {
-        if constexpr (I < COLS / 64 * PIECES) {
-            constexpr int C = I / PIECES * 64;
-            if (col + C < p.r) io.load(I % 2, &p.gram, col + C, row, t.batch * PIECES + I % PIECES);
-        }
-    }
+    __device__ NsPoly(const Params& p_, hg::WarpIo& io_) : p(p_), io(io_) {}
     __device__ __forceinline__ void start(const hg::Unit& t, int row, int col) {
-        if (row >= p.r) return;
-        load<0>(t, row, col);
-        load<1>(t, row, col);
+        if (row < p.r) Add::start(io, &p.gram, t.batch * PIECES, row, col, p.r);
     }
-    template <int I>
-    __device__ __forceinline__ void add(const hg::Unit& t, int row, int col, float (&s)[COLS]) {
-        if constexpr (I < COLS / 64 * PIECES) {
-            constexpr int C = I / PIECES * 64;
-            const int lane = threadIdx.x & 31;
-            if (col + C >= p.r) return;
-            io.wait_load(I % 2);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const uint4 v = *hg::staged(io.block(I % 2), lane, j);
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
-                    s[C + 8 * j + 2 * k] = fmaf(p.b, f.x, s[C + 8 * j + 2 * k]);
-                    s[C + 8 * j + 2 * k + 1] = fmaf(p.b, f.y, s[C + 8 * j + 2 * k + 1]);
-                }
-            }
-            __syncwarp();  // read by all lanes
-            load<I + 2>(t, row, col);
-        }
-    }
-    __device__ __forceinline__ void unit(const hg::Unit& t, int row, int col, float (&s)[COLS]) {
+    __device__ __forceinline__ void unit(const hg::Unit& t, int row, int col, float b, float c,
+                                         float (&s)[COLS]) {
         if (row >= p.r) return;
-        const float c = p.c * DOWN;
+        c *= UP_P / (UP_A * UP_A);
 #pragma unroll
         for (int j = 0; j < COLS; ++j) s[j] *= c;
-        add<0>(t, row, col, s);
-        add<1>(t, row, col, s);
-        add<2>(t, row, col, s);
-        add<3>(t, row, col, s);
+        Add::run(io, &p.gram, t.batch * PIECES, row, col, p.r, b * (UP_P / UP_A), s);
         store_factors<PIECES, true>(io, p.out, s, t.batch, row, col, p.r, t.col0 + BN <= t.row0);
     }
 };
 
-// X = a X + (product): in FP32 and as factors for the next step, or as the result.
-template <int BN_, int PIECES>
+// X = a X + (product), in pieces for the next step or as the result. X always has two pieces.
+template <int BN_>
 struct NsUpdate {
     static constexpr int BN = BN_;
     static constexpr int COLS = BN / 2;
+    using Add = Adder<COLS, 2>;
     struct Params {
-        CUtensorMap x;      // FP32, in place: blocks of 32 columns
-        FactorMaps out;
+        FactorMaps x[2];  // of X before a step and after it, by the step's parity
         int M, N;
-        float a;
-        int last;           // the result goes out instead
         void* result;
         long long ldo, stride;
         int dtype, wide;
     };
     const Params& p;
     hg::WarpIo& io;
-    __device__ NsUpdate(const Params& p_, const hg::Args&, int, hg::WarpIo& io_) : p(p_), io(io_) {}
-
-    __device__ __forceinline__ void start(const hg::Unit& t, int row, int col) {
-        if (row >= p.M) return;
-        if (col < p.N) io.load(0, &p.x, col, row, t.batch);
-        if (col + 32 < p.N) io.load(1, &p.x, col + 32, row, t.batch);
-    }
-
-    template <int C>
-    __device__ __forceinline__ void step32(const hg::Unit& t, int row, int col, float (&s)[COLS]) {
-        constexpr int B = C / 32 % 2;
-        const int lane = threadIdx.x & 31;
-        if (col + C >= p.N) return;
-        io.wait_load(B);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint4 v = *hg::staged(io.block(B), lane, j);
-            s[C + 4 * j] = fmaf(p.a, __uint_as_float(v.x), s[C + 4 * j] * DOWN2);
-            s[C + 4 * j + 1] = fmaf(p.a, __uint_as_float(v.y), s[C + 4 * j + 1] * DOWN2);
-            s[C + 4 * j + 2] = fmaf(p.a, __uint_as_float(v.z), s[C + 4 * j + 2] * DOWN2);
-            s[C + 4 * j + 3] = fmaf(p.a, __uint_as_float(v.w), s[C + 4 * j + 3] * DOWN2);
-        }
-        if (!p.last) {
-            hg::stage_words<C>(io.block(B), s);  // over the values that this lane has just read
-            io.store(B, &p.x, col + C, row, t.batch);
-        } else {
-            __syncwarp();  // read by all lanes
-        }
-        if constexpr (C + 64 < COLS)
-            if (col + C + 64 < p.N) io.load(B, &p.x, col + C + 64, row, t.batch);
+    __device__ NsUpdate(const Params& p_, hg::WarpIo& io_) : p(p_), io(io_) {}
+    __device__ __forceinline__ void start(const hg::Unit& t, int row, int col, int odd) {
+        if (row < p.M) Add::start(io, &p.x[odd].straight, t.batch * 2, row, col, p.N);
     }
 
     // 32 words from word C on, through block B, to the result's columns `col` on
@@ -355,18 +335,15 @@ struct NsUpdate {
                               {base, p.ldo * SIZE, p.M - row, bytes, p.wide && bytes % 16 == 0});
     }
 
-    __device__ __forceinline__ void unit(const hg::Unit& t, int row, int col, float (&s)[COLS]) {
+    __device__ __forceinline__ void unit(const hg::Unit& t, int row, int col, int odd, float a,
+                                         bool last, float (&s)[COLS]) {
         if (row >= p.M) return;
-        step32<0>(t, row, col, s);
-        step32<32>(t, row, col, s);
-        if constexpr (COLS == 128) {
-            step32<64>(t, row, col, s);
-            step32<96>(t, row, col, s);
-        }
-        if (!p.last) {
+        const float down = last ? 1.f / (UP_P * UP_X) : 1.f / UP_P;
 #pragma unroll
-            for (int j = 0; j < COLS; ++j) s[j] *= UP;
-            store_factors<PIECES, false>(io, p.out, s, t.batch, row, col, p.N, false);
+        for (int j = 0; j < COLS; ++j) s[j] *= down;
+        Add::run(io, &p.x[odd].straight, t.batch * 2, row, col, p.N, last ? a / UP_X : a, s);
+        if (!last) {
+            store_factors<2, false>(io, p.x[odd ^ 1], s, t.batch, row, col, p.N, false);
             return;
         }
         if (p.dtype == SGEMM_FLOAT32) {
@@ -385,6 +362,52 @@ struct NsUpdate {
                                             : hg::pack2<false>(s[j], s[j + 1]));
         result<0, 0, 2>(t, row, col, s);
         if constexpr (COLS == 128) result<32, 1, 2>(t, row, col + 64, s);
+    }
+};
+
+// The whole iteration as a chain of phases: three for each step. Launching them one by one costs
+// some 6 us each where they are small (a launch, barriers and TMEM set up, the code fetched anew).
+template <int BN_, int PIECES>
+struct NsChain {
+    static constexpr int BN = BN_;
+    static constexpr int COLS = BN / 2;
+    static constexpr int PROBLEMS = 6;
+    static constexpr bool CHAIN = true;
+    using Gram = NsGram<BN, PIECES>;
+    using Poly = NsPoly<BN, PIECES>;
+    using Update = NsUpdate<BN>;
+    struct Params {
+        typename Gram::Params gram;
+        typename Poly::Params poly;
+        typename Update::Params update;
+        int steps;
+        float coefficients[3 * MAX_STEPS];
+    };
+    const Params& p;
+    Gram gram;
+    Poly poly;
+    Update update;
+    __device__ NsChain(const Params& p_, int, hg::WarpIo& io)
+        : p(p_), gram(p_.gram, io), poly(p_.poly, io), update(p_.update, io) {}
+    // (the update reads an X that was stored three phases before, but the phases between may not
+    // have begun when a unit is handed out)
+    __device__ __forceinline__ bool reads(const hg::Unit& t) const { return t.phase % 3 != 0; }
+    __device__ __forceinline__ void start(const hg::Unit& t, int row, int col) {
+        const int type = t.phase % 3;
+        if (type == 1)
+            poly.start(t, row, col);
+        else if (type == 2)
+            update.start(t, row, col, t.problem == 5);
+    }
+    __device__ __forceinline__ void unit(const hg::Unit& t, int row, int col, float (&s)[COLS]) {
+        const int step = t.phase / 3, type = t.phase - 3 * step;
+        const float* c = p.coefficients + 3 * step;
+        if (type == 0)
+            gram.unit(t, row, col, s);
+        else if (type == 1)
+            poly.unit(t, row, col, c[1], c[2], s);
+        else
+            update.unit(t, row, col, t.problem == 5, c[0], step == p.steps - 1, s);
     }
 };
 
@@ -409,108 +432,99 @@ struct Layout {
     }
 };
 
-template <int PIECES>
-void set_planes(hg::Problem& p) {
-    p.planes_a = p.planes_b = PIECES;
-    p.products = PIECES == 1 ? 1 : 3;
-    if (PIECES == 2) {  // low.high, high.low, high.high
-        p.pa[0] = 1;
-        p.pb[1] = 1;
-    }
+// Products of one piece each, or of low.high, high.low and high.high pieces.
+void set_products(hg::Problem& p, int pieces) {
+    p.planes_a = p.planes_b = pieces;
+    p.products = pieces == 1 ? 1 : 3;
+    if (pieces == 2) p.pa[0] = p.pb[1] = 1;
 }
 
+// counters: of claimed units, then of each phase's finished ones
 template <int BN, int PIECES>
-cudaError_t iterate(const Call& a, const DeviceInfo& info, float* x, __half* (&factors)[2],
-                    __half* gram, __half* poly, int* counters, int Np, int rp, cudaStream_t s) {
+cudaError_t iterate(const Call& a, const DeviceInfo& info, __half* (&x)[2], __half* gram,
+                    __half* poly, int* counters, int Np, int rp, cudaStream_t s) {
     const bool tall = a.M > a.N;
     const int r = std::min(a.M, a.N), q = std::max(a.M, a.N);
     const long long x_plane = (long long)a.M * Np, r_plane = (long long)r * rp;
     const int slabs = a.count * PIECES;
-    hg::Args base;
-    std::memset(&base, 0, sizeof base);
-    base.problems = 1;
-    base.err = info.error_word;
-    hg::Problem& p = base.p[0];
-    p.batch = a.count;
-    p.splits = 1;
-    p.group = 8;
-    set_planes<PIECES>(p);
-    // maps of X with k and with the other index contiguous (wide: k is a column), of A and of the
-    // polynomial, with k contiguous (they are symmetric)
-    hg::Args gram_args[2] = {base, base}, poly_args = base, update_args[2] = {base, base};
-    for (int i = 0; i < 2; ++i) {
-        hg::Args& g = gram_args[i];
-        // A = X X^T: both operands along the columns; tall, X^T X: both along the rows
-        if (!hg::encode_operand(&g.a[0], factors[i], false, a.N, a.M, Np, slabs, x_plane,
-                                hg::box_rows(tall, hg::HALF_M)) ||
-            !hg::encode_operand(&g.b[0], factors[i], false, a.N, a.M, Np, slabs, x_plane,
-                                hg::box_rows(tall, BN / 2)))
-            return cudaErrorInvalidValue;
-        hg::Problem& gp = g.p[0];
-        gp.M = gp.N = r;
-        gp.K = q;
-        gp.symmetric = 1;
-        gp.a_mn = gp.b_mn = tall;
-        gp.idesc = hg::instruction(false, tall, tall);
-        // wide: P (r x r) times X, whose columns are contiguous; tall: X times P
-        hg::Args& u = update_args[i];
-        hg::Problem& up = u.p[0];
-        up.M = a.M;
-        up.N = a.N;
-        up.K = r;
-        up.b_mn = !tall;
-        up.idesc = hg::instruction(false, false, !tall);
-        const bool ok =
-            tall ? hg::encode_operand(&u.a[0], factors[i], false, a.N, a.M, Np, slabs, x_plane,
-                                      hg::HALF_M) &&
-                       hg::encode_operand(&u.b[0], poly, false, r, r, rp, slabs, r_plane, BN / 2)
-                 : hg::encode_operand(&u.a[0], poly, false, r, r, rp, slabs, r_plane, hg::HALF_M) &&
-                       hg::encode_operand(&u.b[0], factors[i], false, a.N, a.M, Np, slabs, x_plane,
-                                          hg::BK);
-        if (!ok) return cudaErrorInvalidValue;
-    }
-    if (!hg::encode_operand(&poly_args.a[0], gram, false, r, r, rp, slabs, r_plane, hg::HALF_M) ||
-        !hg::encode_operand(&poly_args.b[0], gram, false, r, r, rp, slabs, r_plane, BN / 2))
-        return cudaErrorInvalidValue;
-    hg::Problem& pp = poly_args.p[0];
-    pp.M = pp.N = pp.K = r;
-    pp.symmetric = 1;
-    pp.idesc = hg::instruction(false, false, false);
-    // the epilogues' blocks
-    auto factor_maps = [&](FactorMaps& m, const __half* base, int cols, int rows, int ld) {
-        const long long plane = (long long)rows * ld;
-        return hg::encode_block(&m.straight, base, 2, cols, rows, ld, slabs, plane, 64, 32) &&
-               hg::encode_block(&m.turned, base, 2, cols, rows, ld, slabs, plane, 32, 64);
+    using Chain = NsChain<BN, PIECES>;
+    hg::Args<6> g;
+    std::memset(&g, 0, sizeof g);
+    g.problems = 3;
+    g.rounds = a.steps;
+    g.counter = counters;
+    g.done = counters + 1;
+    g.err = info.error_word;
+    // 16-bit results bear an accumulator that is cut off 4 * 256 times (2^-15 of a sum, at most)
+    g.seg_steps = a.dtype == SGEMM_FLOAT32 ? 8 : 256;
+    // operand maps: k contiguous, or the other index
+    auto x_operand = [&](CUtensorMap& m, int i, bool mn, int rows_of_cta) {
+        return hg::encode_operand(&m, x[i], false, a.N, a.M, Np, 2 * a.count, x_plane,
+                                  hg::box_rows(mn, rows_of_cta));
     };
-    FactorMaps gram_out, poly_out, x_out[2];
-    CUtensorMap x_map;
-    if (!factor_maps(gram_out, gram, r, r, rp) || !factor_maps(poly_out, poly, r, r, rp) ||
-        !factor_maps(x_out[0], factors[0], a.N, a.M, Np) ||
-        !factor_maps(x_out[1], factors[1], a.N, a.M, Np) ||
-        !hg::encode_block(&x_map, x, 4, a.N, a.M, Np, a.count, x_plane, 32, 32))
+    auto r_operand = [&](CUtensorMap& m, const __half* base, int rows_of_cta) {
+        return hg::encode_operand(&m, base, false, r, r, rp, slabs, r_plane, rows_of_cta);
+    };
+    for (int i = 0; i < 2; ++i) {
+        hg::Problem* p = g.p + 3 * i;
+        for (int j = 0; j < 3; ++j) {
+            p[j].batch = a.count;
+            p[j].splits = 1;
+            p[j].group = 8;
+            set_products(p[j], PIECES);
+        }
+        p[0].planes_a = p[0].planes_b = 2;
+        (tall ? p[2].planes_a : p[2].planes_b) = 2;
+        // A = X X^T: both operands along the columns; tall, X^T X: both along the rows
+        p[0].M = p[0].N = r;
+        p[0].K = q;
+        p[0].symmetric = 1;
+        p[0].a_mn = p[0].b_mn = tall;
+        p[0].idesc = hg::instruction(false, tall, tall);
+        // A A, symmetric both
+        p[1].M = p[1].N = p[1].K = r;
+        p[1].symmetric = 1;
+        p[1].idesc = hg::instruction(false, false, false);
+        // the polynomial P times X, whose columns are contiguous; tall: X times P
+        p[2].M = a.M;
+        p[2].N = a.N;
+        p[2].K = r;
+        p[2].b_mn = !tall;
+        p[2].idesc = hg::instruction(false, false, !tall);
+        CUtensorMap *ma = g.a + 3 * i, *mb = g.b + 3 * i;
+        if (!x_operand(ma[0], i, tall, hg::HALF_M) || !x_operand(mb[0], i, tall, BN / 2) ||
+            !r_operand(ma[1], gram, hg::HALF_M) || !r_operand(mb[1], gram, BN / 2))
+            return cudaErrorInvalidValue;
+        if (tall ? !x_operand(ma[2], i, false, hg::HALF_M) || !r_operand(mb[2], poly, BN / 2)
+                 : !r_operand(ma[2], poly, hg::HALF_M) || !x_operand(mb[2], i, true, 0))
+            return cudaErrorInvalidValue;
+    }
+    // the epilogues' blocks
+    typename Chain::Params p;
+    auto factor_maps = [&](FactorMaps& m, const __half* base, int cols, int rows, int ld, int n) {
+        const long long plane = (long long)rows * ld;
+        return hg::encode_block(&m.straight, base, 2, cols, rows, ld, n, plane, 64, 32) &&
+               hg::encode_block(&m.turned, base, 2, cols, rows, ld, n, plane, 32, 64);
+    };
+    if (!factor_maps(p.gram.out, gram, r, r, rp, slabs) ||
+        !factor_maps(p.poly.out, poly, r, r, rp, slabs) ||
+        !factor_maps(p.update.x[0], x[0], a.N, a.M, Np, 2 * a.count) ||
+        !factor_maps(p.update.x[1], x[1], a.N, a.M, Np, 2 * a.count))
         return cudaErrorInvalidValue;
     const int size = a.dtype == SGEMM_FLOAT32 ? 4 : 2;
-    const int wide = aligned16(a.out) && a.ldo * size % 16 == 0 && a.stride_o * size % 16 == 0;
-    for (int i = 0; i < a.steps; ++i) {
-        const float* c = a.coefficients + 3 * i;
-        hg::Args g = gram_args[i & 1], u = update_args[i & 1];
-        g.counter = counters + 3 * i;
-        poly_args.counter = counters + 3 * i + 1;
-        u.counter = counters + 3 * i + 2;
-        cudaError_t e =
-            hg::launch_gemm<NsGram<BN, PIECES>>(g, {gram_out, r}, info.sm_count, s);
-        if (e != cudaSuccess) return e;
-        e = hg::launch_gemm<NsPoly<BN, PIECES>>(
-            poly_args, {gram_out.straight, poly_out, r, c[1], c[2]}, info.sm_count, s);
-        if (e != cudaSuccess) return e;
-        const bool last = i == a.steps - 1;
-        e = hg::launch_gemm<NsUpdate<BN, PIECES>>(
-            u, {x_map, x_out[(i + 1) & 1], a.M, a.N, c[0], last, a.out, a.ldo, a.stride_o, a.dtype,
-                wide},
-            info.sm_count, s);
-        if (e != cudaSuccess) return e;
-    }
-    return cudaSuccess;
+    p.gram.r = p.poly.r = r;
+    p.poly.gram = p.gram.out.straight;
+    p.update.M = a.M;
+    p.update.N = a.N;
+    p.update.result = a.out;
+    p.update.ldo = a.ldo;
+    p.update.stride = a.stride_o;
+    p.update.dtype = a.dtype;
+    p.update.wide = aligned16(a.out) && a.ldo * size % 16 == 0 && a.stride_o * size % 16 == 0;
+    p.steps = a.steps;
+    std::memset(p.coefficients, 0, sizeof p.coefficients);
+    std::memcpy(p.coefficients, a.coefficients, size_t(3) * a.steps * sizeof(float));
+    return hg::launch_gemm<Chain>(g, p, info.sm_count, s);
 }
 
 template <class T_IN, int PIECES>
@@ -522,11 +536,11 @@ cudaError_t run(const Call& a, const DeviceInfo& info, int dev, cudaStream_t s) 
     const int most = std::max(1, std::min(MAX_NORM_CTAS, 2048 / a.count + 1));
     const int ctas = int(std::min<long long>(most, (groups + NORM_THREADS - 1) / NORM_THREADS));
     Layout lay;
-    const size_t at_counters = lay.add(size_t(3) * a.steps * sizeof(int));
+    const int n_counters = 1 + 3 * a.steps * a.count;
+    const size_t at_counters = lay.add(size_t(n_counters) * sizeof(int));
     const size_t at_norm = lay.add(size_t(a.count) * ctas * sizeof(double));
-    const size_t at_x = lay.add(x_plane * 4 * a.count);
-    const size_t at_f0 = lay.add(x_plane * 2 * PIECES * a.count);
-    const size_t at_f1 = lay.add(a.steps > 1 ? x_plane * 2 * PIECES * a.count : 0);
+    const size_t at_x0 = lay.add(x_plane * 4 * a.count);
+    const size_t at_x1 = a.steps > 1 ? lay.add(x_plane * 4 * a.count) : at_x0;
     const size_t at_gram = lay.add(r_plane * 2 * PIECES * a.count);
     const size_t at_poly = lay.add(r_plane * 2 * PIECES * a.count);
     Scratch scratch;
@@ -535,9 +549,8 @@ cudaError_t run(const Call& a, const DeviceInfo& info, int dev, cudaStream_t s) 
     uint8_t* base = static_cast<uint8_t*>(scratch.ptr);
     int* counters = reinterpret_cast<int*>(base + at_counters);
     double* partial = reinterpret_cast<double*>(base + at_norm);
-    float* x = reinterpret_cast<float*>(base + at_x);
-    __half* factors[2] = {reinterpret_cast<__half*>(base + at_f0),
-                          reinterpret_cast<__half*>(base + (a.steps > 1 ? at_f1 : at_f0))};
+    __half* x[2] = {reinterpret_cast<__half*>(base + at_x0),
+                    reinterpret_cast<__half*>(base + at_x1)};
     __half* gram = reinterpret_cast<__half*>(base + at_gram);
     __half* poly = reinterpret_cast<__half*>(base + at_poly);
     const T_IN* G = static_cast<const T_IN*>(a.G);
@@ -557,16 +570,16 @@ cudaError_t run(const Call& a, const DeviceInfo& info, int dev, cudaStream_t s) 
         return cudaLaunchKernelEx(&cfg, kernel, args...);
     };
     e = launch2(ns_norm<T_IN>, NORM_THREADS, G, a.ldg, a.stride_g, a.M, a.N, partial, counters,
-                3 * a.steps);
+                n_counters);
     if (e != cudaSuccess) return e;
-    e = launch2(ns_convert<T_IN, PIECES>, CONVERT_THREADS, G, a.ldg, a.stride_g, a.M, a.N, Np,
-                static_cast<const double*>(partial), ctas, a.eps, x, factors[0]);
+    e = launch2(ns_convert<T_IN>, CONVERT_THREADS, G, a.ldg, a.stride_g, a.M, a.N, Np,
+                static_cast<const double*>(partial), ctas, a.eps, x[0]);
     if (e != cudaSuccess) return e;
     // 128 columns a tile where 256 would leave pairs without one
     const int tiles = ((a.M + 255) / 256) * ((a.N + 255) / 256) * a.count;
     return tiles < std::max(info.sm_count / 2, 1)
-               ? iterate<128, PIECES>(a, info, x, factors, gram, poly, counters, Np, rp, s)
-               : iterate<256, PIECES>(a, info, x, factors, gram, poly, counters, Np, rp, s);
+               ? iterate<128, PIECES>(a, info, x, gram, poly, counters, Np, rp, s)
+               : iterate<256, PIECES>(a, info, x, gram, poly, counters, Np, rp, s);
 }
 
 // Bytes from the first to behind the last element.
@@ -586,7 +599,7 @@ extern "C" int sgemm_orthogonalize(const void* G, int dtype, int count, int M, i
                                    float eps, void* stream) {
     if (dtype < SGEMM_FLOAT32 || dtype > SGEMM_FLOAT16) return SGEMM_ERR_ARG;
     if (count < 0 || count > 4096 || M < 1 || N < 1 || M > 32768 || N > 32768) return SGEMM_ERR_ARG;
-    if (std::min(M, N) > 16384 || steps < 1 || steps > 64 || !coefficients) return SGEMM_ERR_ARG;
+    if (std::min(M, N) > 16384 || steps < 1 || steps > MAX_STEPS || !coefficients) return SGEMM_ERR_ARG;
     if (!(eps >= 0.f) || ldg < N || ldo < N) return SGEMM_ERR_ARG;
     if (count == 0) return SGEMM_OK;
     const int size = dtype == SGEMM_FLOAT32 ? 4 : 2;

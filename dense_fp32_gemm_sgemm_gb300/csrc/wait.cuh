@@ -33,4 +33,23 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volati
     }
 }
 
+// Waits until the count at p (global memory, added to with release semantics) is at least
+// `target`, with the same limit and answers.
+__device__ __forceinline__ bool wait_count(const int* p, int target, volatile int* abort_flag,
+                                           int* err) {
+    if (ptx::ld_acquire_gpu(p) >= target) return true;
+    const unsigned long long t0 = ptx::globaltimer_ns();
+    while (true) {
+#pragma unroll 1
+        for (int i = 0; i < 32; ++i)
+            if (ptx::ld_acquire_gpu(p) >= target) return true;
+        if (*abort_flag) return false;
+        if (ptx::globaltimer_ns() - t0 > WAIT_LIMIT_NS) {
+            *abort_flag = 1;
+            atomicExch(err, kErrWaitTimeout);
+            return false;
+        }
+    }
+}
+
 }  // namespace sgemm
