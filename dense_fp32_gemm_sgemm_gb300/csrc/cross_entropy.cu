@@ -245,14 +245,21 @@ struct CeForward {
     __device__ CeForward(const Params& p_, int live_, hg::WarpIo& io_)
         : p(p_), io(io_), live(live_) {}
 
-    // 32 words of every lane as block B's rows to columns `col` on of `kept`
-    template <int C, int B>
-    __device__ __forceinline__ void keep(const float (&s)[COLS], int row, int col) {
-        io.acquire(B);
-        hg::stage_words<C>(io.block(B), s);
-        io.store(B, &p.kept, col, row, 0);
+    // `words` words of every lane, 32 at a time, to columns `col` on of `kept`, which a word has
+    // 32 / `each` of. (Loops, as the code is fetched anew in every launch: see hg::Rows.)
+    __device__ __forceinline__ void keep(float (&s)[COLS], int words, int each, int row, int col) {
+        int block = 0;
+#pragma unroll 1
+        for (int at = 0; at < words; at += 32) {
+            io.acquire(block);
+            hg::stage_words<0>(io.block(block), s);
+            io.store(block, &p.kept, col, row, 0);
+            col += each;
+            block ^= 1;
+#pragma unroll
+            for (int j = 0; j + 32 < COLS; ++j) s[j] = s[j + 32];
+        }
     }
-
     __device__ __forceinline__ void start(const hg::Unit&, int, int) {}
     __device__ __forceinline__ void unit(const hg::Unit&, int row, int col, float (&s)[COLS]) {
         const int lane = threadIdx.x & 31;
@@ -276,14 +283,6 @@ struct CeForward {
         for (int j = 1; j < COLS; ++j) m = fmaxf(m, s[j]);
         const float from = m == -INFINITY ? 0.f : m;
         float sum = 0.f;
-        if constexpr (KEEP == Keep::logits) {
-            keep<0, 0>(s, row, col);
-            keep<32, 1>(s, row, col + 32);
-            if constexpr (COLS == 128) {
-                keep<64, 0>(s, row, col + 64);
-                keep<96, 1>(s, row, col + 96);
-            }
-        }
         constexpr bool HALF = KEEP == Keep::bf16 || KEEP == Keep::fp16;
         constexpr float BIAS = KEEP == Keep::fp16 ? float(FP16_EXP_BITS) : 0.f;
 #pragma unroll
@@ -294,10 +293,8 @@ struct CeForward {
             if constexpr (HALF)
                 s[j / 2] = __uint_as_float(hg::pack2<KEEP == Keep::bf16>(a, b));
         }
-        if constexpr (HALF) {
-            keep<0, 0>(s, row, col);
-            if constexpr (COLS == 128) keep<32, 1>(s, row, col + 64);
-        }
+        if constexpr (HALF) keep(s, COLS / 2, 64, row, col);
+        if constexpr (KEEP == Keep::logits) keep(s, COLS, 32, row, col);
         if constexpr (KEEP == Keep::fp16) sum *= 1.f / float(1 << FP16_EXP_BITS);
         p.stats[(long long)(col / COLS) * p.stats_pitch + r] = make_float2(m, sum);
     }
@@ -576,17 +573,16 @@ struct CeGrad {
         __syncwarp();
     }
 
-    // 32 words of every lane, from word C on, through block B to columns `col` on
-    template <int C, int B, int SIZE>
-    __device__ __forceinline__ void part(const hg::Unit& t, const GradOut& o, int row, int col,
+    // The first 32 words of every lane through a staging block to columns `col` on.
+    template <int SIZE>
+    __device__ __forceinline__ void part(const hg::Unit& t, const GradOut& o, int b, int row, int col,
                                          int index, const float (&s)[COLS]) {
-        if (col >= o.cols_n) return;
-        io.acquire(B);
-        hg::stage_words<C>(io.block(B), s);
+        io.acquire(b);
+        hg::stage_words<0>(io.block(b), s);
         if (o.tma) {
-            io.store(B, &o.map, col, t.split * o.part_rows + row, 0);
+            io.store(b, &o.map, col, t.split * o.part_rows + row, 0);
         } else if (SUMS && SIZE == 4 && o.sums) {
-            add_block(io.block(B), o, row, col);
+            add_block(io.block(b), o, row, col);
         } else {
             const int bytes = min(128, (o.cols_n - col) * SIZE);
             char* base = static_cast<char*>(o.out) + (long long)col * SIZE;
@@ -594,9 +590,9 @@ struct CeGrad {
             const hg::Rows to = {base, o.ld * SIZE, (o.rows ? live : o.rows_n) - row, bytes,
                                  o.wide && bytes % 16 == 0};
             if (o.rows)
-                hg::store_block<SIZE, true>(io.block(B), to, index);
+                hg::store_block<SIZE, true>(io.block(b), to, index);
             else
-                hg::store_block<SIZE>(io.block(B), to);
+                hg::store_block<SIZE>(io.block(b), to);
         }
     }
 
@@ -609,24 +605,26 @@ struct CeGrad {
 #pragma unroll
             for (int j = 0; j < COLS; ++j) s[j] *= scale;
         }
-        if (o.part_rows || (SUMS && o.sums) || o.dtype == SGEMM_FLOAT32) {
-            part<0, 0, 4>(t, o, row, col, index, s);
-            part<32, 1, 4>(t, o, row, col + 32, index, s);
-            part<64, 0, 4>(t, o, row, col + 64, index, s);
-            part<96, 1, 4>(t, o, row, col + 96, index, s);
-            return;
-        }
-        if (o.dtype == SGEMM_BFLOAT16) {
+        const bool wide = o.part_rows || (SUMS && o.sums) || o.dtype == SGEMM_FLOAT32;
+        if (!wide) {
+            const bool bf16 = o.dtype == SGEMM_BFLOAT16;
 #pragma unroll
             for (int j = 0; j < COLS; j += 2)
-                s[j / 2] = __uint_as_float(hg::pack2<true>(s[j], s[j + 1]));
-        } else {
-#pragma unroll
-            for (int j = 0; j < COLS; j += 2)
-                s[j / 2] = __uint_as_float(hg::pack2<false>(s[j], s[j + 1]));
+                s[j / 2] = __uint_as_float(bf16 ? hg::pack2<true>(s[j], s[j + 1])
+                                                : hg::pack2<false>(s[j], s[j + 1]));
         }
-        part<0, 0, 2>(t, o, row, col, index, s);
-        part<32, 1, 2>(t, o, row, col + 64, index, s);
+        const int each = wide ? 32 : 64, end = min(col + COLS, o.cols_n);
+        int b = 0;
+#pragma unroll 1
+        for (int at = col; at < end; at += each) {
+            if (wide)
+                part<4>(t, o, b, row, at, index, s);
+            else
+                part<2>(t, o, b, row, at, index, s);
+            b ^= 1;
+#pragma unroll
+            for (int j = 0; j + 32 < COLS; ++j) s[j] = s[j + 32];
+        }
     }
 };
 

@@ -132,282 +132,220 @@ __global__ void __launch_bounds__(CONVERT_THREADS)
     }
 }
 
-// ---- epilogues ---------------------------------------------------------------------------------
-// Turns a thread's values into factors in place: words 2 j and 2 j + 1 get the first and the second
-// pieces of values 2 j and 2 j + 1. (A conversion instruction for each value and use would cost
-// more than everything else here: they go at 16 a clock and SM.)
-template <int PIECES, int N>
-__device__ __forceinline__ void pack_factors(float (&s)[N]) {
-#pragma unroll
-    for (int j = 0; j < N; j += 2) {
-        const __half2 high = __floats2half2_rn(s[j], s[j + 1]);
-        if constexpr (PIECES == 2) {
-            const float2 h = __half22float2(high);
-            const __half2 low = __floats2half2_rn(s[j] - h.x, s[j + 1] - h.y);
-            s[j + 1] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&low));
-        }
-        s[j] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&high));
-    }
-}
-
+// ---- the epilogue -------------------------------------------------------------------------------
 // Where factors go: blocks of 64 columns x 32 rows, and blocks turned over (32 x 64).
 struct FactorMaps {
     CUtensorMap straight, turned;
 };
 
-// Piece K of 64 packed values from s[C] on, through block B, to `slab` at (row, col); with MIRROR
-// and `mirror` also, turned over, through the other block, to (col, row).
-template <int C, int K, int B, bool MIRROR, int N>
-__device__ __forceinline__ void store_factor(hg::WarpIo& io, const FactorMaps& to,
-                                             const float (&s)[N], int slab, int row, int col,
-                                             int cols_n, bool mirror) {
-    const int lane = threadIdx.x & 31;
-    if (col >= cols_n) return;
-    io.acquire(B);
-    uint8_t* block = io.block(B);
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        *hg::staged(block, lane, j) = make_uint4(
-            __float_as_uint(s[C + 8 * j + K]), __float_as_uint(s[C + 8 * j + 2 + K]),
-            __float_as_uint(s[C + 8 * j + 4 + K]), __float_as_uint(s[C + 8 * j + 6 + K]));
-    io.store(B, &to.straight, col, row, slab);
-    if (MIRROR && mirror) {
-        io.acquire(B ^ 1);
-        // 64 rows of 32 values, 64 bytes each
-        unsigned short* turned = reinterpret_cast<unsigned short*>(io.block(B ^ 1)) + lane;
-#pragma unroll
-        for (int j = 0; j < 64; j += 2) {
-            const uint32_t w = __float_as_uint(s[C + j + K]);
-            turned[j * 32] = (unsigned short)w;
-            turned[j * 32 + 32] = (unsigned short)(w >> 16);
-        }
-        io.store(B ^ 1, &to.turned, row, col, slab);
-    }
-}
-
-// All of a thread's values as factors (and so packed).
-template <int PIECES, bool MIRROR, int N>
-__device__ __forceinline__ void store_factors(hg::WarpIo& io, const FactorMaps& to, float (&s)[N],
-                                              int batch, int row, int col, int cols_n, bool mirror) {
-    pack_factors<PIECES>(s);
-    const int slab = batch * PIECES;
-    store_factor<0, 0, 0, MIRROR>(io, to, s, slab, row, col, cols_n, mirror);
-    if constexpr (PIECES == 2)
-        store_factor<0, 1, 1, MIRROR>(io, to, s, slab + 1, row, col, cols_n, mirror);
-    if constexpr (N == 128) {
-        store_factor<64, 0, PIECES == 1, MIRROR>(io, to, s, slab, row, col + 64, cols_n, mirror);
-        if constexpr (PIECES == 2)
-            store_factor<64, 1, 1, MIRROR>(io, to, s, slab + 1, row, col + 64, cols_n, mirror);
-    }
-}
-
-// s = s + f * (the pieces' sum) over a thread's columns: PIECES pieces of a matrix in blocks of 64
-// columns, through the two staging blocks in turn, the next two on their way.
-template <int COLS, int PIECES>
-struct Adder {
-    static constexpr int BLOCKS = COLS / 64 * PIECES;
-    // piece I % PIECES of columns I / PIECES * 64 on, into staging block I % 2
-    template <int I>
-    static __device__ __forceinline__ void load(hg::WarpIo& io, const CUtensorMap* from, int slab,
-                                                int row, int col, int cols_n) {
-        if constexpr (I < BLOCKS) {
-            constexpr int C = I / PIECES * 64;
-            if (col + C < cols_n) io.load(I % 2, from, col + C, row, slab + I % PIECES);
-        }
-    }
-    static __device__ __forceinline__ void start(hg::WarpIo& io, const CUtensorMap* from, int slab,
-                                                 int row, int col, int cols_n) {
-        load<0>(io, from, slab, row, col, cols_n);
-        load<1>(io, from, slab, row, col, cols_n);
-    }
-    template <int I>
-    static __device__ __forceinline__ void add(hg::WarpIo& io, const CUtensorMap* from, int slab,
-                                               int row, int col, int cols_n, float f,
-                                               float (&s)[COLS]) {
-        if constexpr (I < BLOCKS) {
-            constexpr int C = I / PIECES * 64;
-            if (col + C >= cols_n) return;
-            const int lane = threadIdx.x & 31;
-            io.wait_load(I % 2);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const uint4 v = *hg::staged(io.block(I % 2), lane, j);
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
-                    s[C + 8 * j + 2 * k] = fmaf(f, x.x, s[C + 8 * j + 2 * k]);
-                    s[C + 8 * j + 2 * k + 1] = fmaf(f, x.y, s[C + 8 * j + 2 * k + 1]);
-                }
-            }
-            __syncwarp();  // read by all lanes
-            load<I + 2>(io, from, slab, row, col, cols_n);
-        }
-    }
-    static __device__ __forceinline__ void run(hg::WarpIo& io, const CUtensorMap* from, int slab,
-                                               int row, int col, int cols_n, float f,
-                                               float (&s)[COLS]) {
-        add<0>(io, from, slab, row, col, cols_n, f, s);
-        add<1>(io, from, slab, row, col, cols_n, f, s);
-        add<2>(io, from, slab, row, col, cols_n, f, s);
-        add<3>(io, from, slab, row, col, cols_n, f, s);
-    }
-};
-
-// A = X X^T: the factors of A, from the tiles at and below the diagonal.
-template <int BN_, int PIECES>
-struct NsGram {
-    static constexpr int BN = BN_;
-    static constexpr int COLS = BN / 2;
-    struct Params {
-        FactorMaps out;
-        int r;
-    };
-    const Params& p;
-    hg::WarpIo& io;
-    __device__ NsGram(const Params& p_, hg::WarpIo& io_) : p(p_), io(io_) {}
-    __device__ __forceinline__ void unit(const hg::Unit& t, int row, int col, float (&s)[COLS]) {
-        if (row >= p.r) return;
-#pragma unroll
-        for (int j = 0; j < COLS; ++j) s[j] *= UP_A / (UP_X * UP_X);
-        store_factors<PIECES, true>(io, p.out, s, t.batch, row, col, p.r, t.col0 + BN <= t.row0);
-    }
-};
-
-// b A + c A A, from the tiles at and below the diagonal.
-template <int BN_, int PIECES>
-struct NsPoly {
-    static constexpr int BN = BN_;
-    static constexpr int COLS = BN / 2;
-    using Add = Adder<COLS, PIECES>;
-    struct Params {
-        CUtensorMap gram;
-        FactorMaps out;
-        int r;
-    };
-    const Params& p;
-    hg::WarpIo& io;
-    __device__ NsPoly(const Params& p_, hg::WarpIo& io_) : p(p_), io(io_) {}
-    __device__ __forceinline__ void start(const hg::Unit& t, int row, int col) {
-        if (row < p.r) Add::start(io, &p.gram, t.batch * PIECES, row, col, p.r);
-    }
-    __device__ __forceinline__ void unit(const hg::Unit& t, int row, int col, float b, float c,
-                                         float (&s)[COLS]) {
-        if (row >= p.r) return;
-        c *= UP_P / (UP_A * UP_A);
-#pragma unroll
-        for (int j = 0; j < COLS; ++j) s[j] *= c;
-        Add::run(io, &p.gram, t.batch * PIECES, row, col, p.r, b * (UP_P / UP_A), s);
-        store_factors<PIECES, true>(io, p.out, s, t.batch, row, col, p.r, t.col0 + BN <= t.row0);
-    }
-};
-
-// X = a X + (product), in pieces for the next step or as the result. X always has two pieces.
-template <int BN_>
-struct NsUpdate {
-    static constexpr int BN = BN_;
-    static constexpr int COLS = BN / 2;
-    using Add = Adder<COLS, 2>;
-    struct Params {
-        FactorMaps x[2];  // of X before a step and after it, by the step's parity
-        int M, N;
-        void* result;
-        long long ldo, stride;
-        int dtype, wide;
-    };
-    const Params& p;
-    hg::WarpIo& io;
-    __device__ NsUpdate(const Params& p_, hg::WarpIo& io_) : p(p_), io(io_) {}
-    __device__ __forceinline__ void start(const hg::Unit& t, int row, int col, int odd) {
-        if (row < p.M) Add::start(io, &p.x[odd].straight, t.batch * 2, row, col, p.N);
-    }
-
-    // 32 words from word C on, through block B, to the result's columns `col` on
-    template <int C, int B, int SIZE>
-    __device__ __forceinline__ void result(const hg::Unit& t, int row, int col,
-                                           const float (&s)[COLS]) {
-        if (col >= p.N) return;
-        io.acquire(B);
-        hg::stage_words<C>(io.block(B), s);
-        const int bytes = min(128, (p.N - col) * SIZE);
-        char* base = static_cast<char*>(p.result) + (t.batch * p.stride + row * p.ldo + col) * SIZE;
-        hg::store_block<SIZE>(io.block(B),
-                              {base, p.ldo * SIZE, p.M - row, bytes, p.wide && bytes % 16 == 0});
-    }
-
-    __device__ __forceinline__ void unit(const hg::Unit& t, int row, int col, int odd, float a,
-                                         bool last, float (&s)[COLS]) {
-        if (row >= p.M) return;
-        const float down = last ? 1.f / (UP_P * UP_X) : 1.f / UP_P;
-#pragma unroll
-        for (int j = 0; j < COLS; ++j) s[j] *= down;
-        Add::run(io, &p.x[odd].straight, t.batch * 2, row, col, p.N, last ? a / UP_X : a, s);
-        if (!last) {
-            store_factors<2, false>(io, p.x[odd ^ 1], s, t.batch, row, col, p.N, false);
-            return;
-        }
-        if (p.dtype == SGEMM_FLOAT32) {
-            result<0, 0, 4>(t, row, col, s);
-            result<32, 1, 4>(t, row, col + 32, s);
-            if constexpr (COLS == 128) {
-                result<64, 0, 4>(t, row, col + 64, s);
-                result<96, 1, 4>(t, row, col + 96, s);
-            }
-            return;
-        }
-        const bool bf16 = p.dtype == SGEMM_BFLOAT16;
-#pragma unroll
-        for (int j = 0; j < COLS; j += 2)
-            s[j / 2] = __uint_as_float(bf16 ? hg::pack2<true>(s[j], s[j + 1])
-                                            : hg::pack2<false>(s[j], s[j + 1]));
-        result<0, 0, 2>(t, row, col, s);
-        if constexpr (COLS == 128) result<32, 1, 2>(t, row, col + 64, s);
-    }
-};
-
-// The whole iteration as a chain of phases: three for each step. Launching them one by one costs
-// some 6 us each where they are small (a launch, barriers and TMEM set up, the code fetched anew).
+// The whole iteration is a chain of phases, three for each step, in one launch (one by one they
+// cost some 6 us each where they are small: a launch, barriers and TMEM set up). The phases share
+// one epilogue:
+//
+//     s = f s + h (the pieces of a matrix at the tile's place), stored as pieces,
+//
+// for A without the second term, for the polynomial with that of A (the products of symmetric
+// matrices from the tiles at and below the diagonal, the others as mirror images), for the new X
+// with that of X. It is written as loops over 64 columns and over pieces with the values moved to
+// where the next turn expects them: an SM fetches instructions for the first time at some 100 ns
+// for each 128 bytes, and fully unrolled the three epilogues took 20 us each at their first use, a
+// whole phase 5.
 template <int BN_, int PIECES>
 struct NsChain {
     static constexpr int BN = BN_;
     static constexpr int COLS = BN / 2;
     static constexpr int PROBLEMS = 6;
     static constexpr bool CHAIN = true;
-    using Gram = NsGram<BN, PIECES>;
-    using Poly = NsPoly<BN, PIECES>;
-    using Update = NsUpdate<BN>;
     struct Params {
-        typename Gram::Params gram;
-        typename Poly::Params poly;
-        typename Update::Params update;
+        FactorMaps gram, poly;
+        FactorMaps x[2];  // X before a step and after it, by the step's parity; two pieces
+        int r, M, N;
+        void* result;     // of the last step
+        long long ldo, stride;
+        int dtype, wide;
         int steps;
         float coefficients[3 * MAX_STEPS];
     };
     const Params& p;
-    Gram gram;
-    Poly poly;
-    Update update;
-    __device__ NsChain(const Params& p_, int, hg::WarpIo& io)
-        : p(p_), gram(p_.gram, io), poly(p_.poly, io), update(p_.update, io) {}
-    // (the update reads an X that was stored three phases before, but the phases between may not
-    // have begun when a unit is handed out)
+    hg::WarpIo& io;
+    __device__ NsChain(const Params& p_, int, hg::WarpIo& io_) : p(p_), io(io_) {}
+
+    // The matrix of the second term.
+    struct Second {
+        const CUtensorMap* map;
+        int pieces, slab, rows, cols;
+    };
+    __device__ __forceinline__ Second second(const hg::Unit& t, int type) const {
+        if (type == 1) return {&p.gram.straight, PIECES, t.batch * PIECES, p.r, p.r};
+        return {&p.x[t.problem == 5].straight, 2, t.batch * 2, p.M, p.N};
+    }
+    // Block n of the second term: 64 columns, piece by piece; into staging block n % 2.
+    __device__ __forceinline__ void load(const Second& m, int n, int row, int col) {
+        const int c = m.pieces == 2 ? n >> 1 : n;
+        if (c * 64 < COLS && col + c * 64 < m.cols)
+            io.load(n & 1, m.map, col + c * 64, row, m.slab + (m.pieces == 2 ? n & 1 : 0));
+    }
     __device__ __forceinline__ bool reads(const hg::Unit& t) const { return t.phase % 3 != 0; }
     __device__ __forceinline__ void start(const hg::Unit& t, int row, int col) {
         const int type = t.phase % 3;
-        if (type == 1)
-            poly.start(t, row, col);
-        else if (type == 2)
-            update.start(t, row, col, t.problem == 5);
+        if (type == 0) return;
+        const Second m = second(t, type);
+        if (row >= m.rows) return;
+        load(m, 0, row, col);
+        load(m, 1, row, col);
     }
+
+    // The next 64 columns to the front.
+    static __device__ __forceinline__ void turn(float (&s)[COLS]) {
+        if constexpr (COLS == 128) {
+#pragma unroll
+            for (int j = 0; j < 64; ++j) {
+                const float v = s[j];
+                s[j] = s[j + 64];
+                s[j + 64] = v;
+            }
+        }
+    }
+
+    // The first 32 words of every lane to columns `col` on of the result.
+    template <int SIZE>
+    __device__ __forceinline__ void store_result(const hg::Unit& t, int block, int row, int col,
+                                                 const float (&s)[COLS]) {
+        io.acquire(block);
+        hg::stage_words<0>(io.block(block), s);
+        const int bytes = min(128, (p.N - col) * SIZE);
+        char* base = static_cast<char*>(p.result) + (t.batch * p.stride + row * p.ldo + col) * SIZE;
+        hg::store_block<SIZE>(io.block(block),
+                              {base, p.ldo * SIZE, p.M - row, bytes, p.wide && bytes % 16 == 0});
+    }
+
     __device__ __forceinline__ void unit(const hg::Unit& t, int row, int col, float (&s)[COLS]) {
+        const int lane = threadIdx.x & 31;
         const int step = t.phase / 3, type = t.phase - 3 * step;
         const float* c = p.coefficients + 3 * step;
-        if (type == 0)
-            gram.unit(t, row, col, s);
-        else if (type == 1)
-            poly.unit(t, row, col, c[1], c[2], s);
+        const bool last = type == 2 && step == p.steps - 1;
+        const int rows_n = type == 2 ? p.M : p.r, cols_n = type == 2 ? p.N : p.r;
+        if (row >= rows_n || col >= cols_n) return;
+        float f, h = 0.f;
+        if (type == 0) {
+            f = UP_A / (UP_X * UP_X);
+        } else if (type == 1) {
+            f = c[2] * (UP_P / (UP_A * UP_A));
+            h = c[1] * (UP_P / UP_A);
+        } else {
+            f = last ? 1.f / (UP_P * UP_X) : 1.f / UP_P;
+            h = last ? c[0] / UP_X : c[0];
+        }
+#pragma unroll
+        for (int j = 0; j < COLS; ++j) s[j] *= f;
+        if (type != 0) {
+            const Second m = second(t, type);
+            int n = 0;
+#pragma unroll 1
+            for (int at = 0; at < COLS; at += 64) {
+#pragma unroll 1
+                for (int k = 0; k < m.pieces && col + at < cols_n; ++k, ++n) {
+                    io.wait_load(n & 1);
+                    uint8_t* block = io.block(n & 1);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const uint4 v = *hg::staged(block, lane, j);
+                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float2 x =
+                                __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+                            s[8 * j + 2 * i] = fmaf(h, x.x, s[8 * j + 2 * i]);
+                            s[8 * j + 2 * i + 1] = fmaf(h, x.y, s[8 * j + 2 * i + 1]);
+                        }
+                    }
+                    __syncwarp();  // read by all lanes
+                    load(m, n + 2, row, col);
+                }
+                turn(s);
+            }
+        }
+        if (!last)
+            store_pieces(t, type, row, col, cols_n, s);
         else
-            update.unit(t, row, col, t.problem == 5, c[0], step == p.steps - 1, s);
+            store_last(t, row, col, s);
+    }
+
+    // All values as pieces of the next factor. The words 2 j and 2 j + 1 get the first and second
+    // pieces of values 2 j and 2 j + 1: one conversion for two values and each piece.
+    __device__ __forceinline__ void store_pieces(const hg::Unit& t, int type, int row, int col,
+                                                 int cols_n, float (&s)[COLS]) {
+        const int lane = threadIdx.x & 31;
+        const int pieces = type == 2 ? 2 : PIECES;
+        const FactorMaps& to =
+            type == 0 ? p.gram : type == 1 ? p.poly : p.x[t.problem != 5];
+        const int slab = t.batch * pieces;
+        const bool mirror = type != 2 && t.col0 + BN <= t.row0;
+        int block = 0;
+#pragma unroll 1
+        for (int at = col; at < min(col + COLS, cols_n); at += 64) {
+#pragma unroll
+            for (int j = 0; j < 64; j += 2) {
+                const __half2 high = __floats2half2_rn(s[j], s[j + 1]);
+                const float2 v = __half22float2(high);
+                const __half2 low = __floats2half2_rn(s[j] - v.x, s[j + 1] - v.y);
+                s[j] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&high));
+                s[j + 1] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&low));
+            }
+#pragma unroll 1
+            for (int k = 0; k < pieces; ++k) {
+                io.acquire(block);
+                uint8_t* straight = io.block(block);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    *hg::staged(straight, lane, j) =
+                        make_uint4(__float_as_uint(s[8 * j]), __float_as_uint(s[8 * j + 2]),
+                                   __float_as_uint(s[8 * j + 4]), __float_as_uint(s[8 * j + 6]));
+                io.store(block, &to.straight, at, row, slab + k);
+                block ^= 1;
+                if (mirror) {
+                    // turned over: 64 rows of 32 values, 64 bytes each
+                    io.acquire(block);
+                    unsigned short* turned =
+                        reinterpret_cast<unsigned short*>(io.block(block)) + lane;
+#pragma unroll
+                    for (int j = 0; j < 64; j += 2) {
+                        const uint32_t w = __float_as_uint(s[j]);
+                        turned[j * 32] = (unsigned short)w;
+                        turned[j * 32 + 32] = (unsigned short)(w >> 16);
+                    }
+                    io.store(block, &to.turned, row, at, slab + k);
+                    block ^= 1;
+                }
+#pragma unroll
+                for (int j = 0; j < 64; j += 2) s[j] = s[j + 1];
+            }
+            turn(s);
+        }
+    }
+
+    __device__ __forceinline__ void store_last(const hg::Unit& t, int row, int col,
+                                               float (&s)[COLS]) {
+        const bool f32 = p.dtype == SGEMM_FLOAT32;
+        if (!f32) {
+            const bool bf16 = p.dtype == SGEMM_BFLOAT16;
+#pragma unroll
+            for (int j = 0; j < COLS; j += 2)
+                s[j / 2] = __uint_as_float(bf16 ? hg::pack2<true>(s[j], s[j + 1])
+                                                : hg::pack2<false>(s[j], s[j + 1]));
+        }
+        const int each = f32 ? 32 : 64, end = min(col + COLS, p.N);
+        int block = 0;
+#pragma unroll 1
+        for (int at = col; at < end; at += each) {
+            if (f32)
+                store_result<4>(t, block, row, at, s);
+            else
+                store_result<2>(t, block, row, at, s);
+            block ^= 1;
+#pragma unroll
+            for (int j = 0; j + 32 < COLS; ++j) s[j] = s[j + 32];
+        }
     }
 };
 
@@ -499,28 +437,26 @@ cudaError_t iterate(const Call& a, const DeviceInfo& info, __half* (&x)[2], __ha
                  : !r_operand(ma[2], poly, hg::HALF_M) || !x_operand(mb[2], i, true, 0))
             return cudaErrorInvalidValue;
     }
-    // the epilogues' blocks
+    // the epilogue's blocks
     typename Chain::Params p;
     auto factor_maps = [&](FactorMaps& m, const __half* base, int cols, int rows, int ld, int n) {
         const long long plane = (long long)rows * ld;
         return hg::encode_block(&m.straight, base, 2, cols, rows, ld, n, plane, 64, 32) &&
                hg::encode_block(&m.turned, base, 2, cols, rows, ld, n, plane, 32, 64);
     };
-    if (!factor_maps(p.gram.out, gram, r, r, rp, slabs) ||
-        !factor_maps(p.poly.out, poly, r, r, rp, slabs) ||
-        !factor_maps(p.update.x[0], x[0], a.N, a.M, Np, 2 * a.count) ||
-        !factor_maps(p.update.x[1], x[1], a.N, a.M, Np, 2 * a.count))
+    if (!factor_maps(p.gram, gram, r, r, rp, slabs) || !factor_maps(p.poly, poly, r, r, rp, slabs) ||
+        !factor_maps(p.x[0], x[0], a.N, a.M, Np, 2 * a.count) ||
+        !factor_maps(p.x[1], x[1], a.N, a.M, Np, 2 * a.count))
         return cudaErrorInvalidValue;
     const int size = a.dtype == SGEMM_FLOAT32 ? 4 : 2;
-    p.gram.r = p.poly.r = r;
-    p.poly.gram = p.gram.out.straight;
-    p.update.M = a.M;
-    p.update.N = a.N;
-    p.update.result = a.out;
-    p.update.ldo = a.ldo;
-    p.update.stride = a.stride_o;
-    p.update.dtype = a.dtype;
-    p.update.wide = aligned16(a.out) && a.ldo * size % 16 == 0 && a.stride_o * size % 16 == 0;
+    p.r = r;
+    p.M = a.M;
+    p.N = a.N;
+    p.result = a.out;
+    p.ldo = a.ldo;
+    p.stride = a.stride_o;
+    p.dtype = a.dtype;
+    p.wide = aligned16(a.out) && a.ldo * size % 16 == 0 && a.stride_o * size % 16 == 0;
     p.steps = a.steps;
     std::memset(p.coefficients, 0, sizeof p.coefficients);
     std::memcpy(p.coefficients, a.coefficients, size_t(3) * a.steps * sizeof(float));
