@@ -146,8 +146,54 @@ __global__ void __launch_bounds__(PLAN_THREADS)
     }
 }
 
-// Packs row rows[r] of x as row r of xc (one plane, or three for float32), zeros up to the next
-// multiple of 256 rows; gives token r, where it does not count, its zeros. A CTA a row.
+// One row of D elements as Dp elements, zeros behind D (all zeros where `from` is null): 16 bits as
+// they are, float32 as three planes. Eight elements a thread and turn; `wide`: 16-byte aligned rows
+// of a multiple of 8 elements.
+template <class T_IN>
+__device__ __forceinline__ void pack_row(const T_IN* from, int D, int Dp, long long plane, bool wide,
+                                         unsigned short* to) {
+    for (int d = threadIdx.x * 8; d < Dp; d += blockDim.x * 8) {
+        if constexpr (sizeof(T_IN) == 4) {
+            float v[8];
+            if (from && wide && d < D) {
+                const float4 a = *reinterpret_cast<const float4*>(from + d);
+                const float4 b = *reinterpret_cast<const float4*>(from + d + 4);
+                v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+                v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = from && d + j < D ? from[d + j] : 0.f;
+            }
+            __align__(16) __nv_bfloat16 p[3][8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                __nv_bfloat16 q[3];
+                split3(v[j], q);
+#pragma unroll
+                for (int i = 0; i < 3; ++i) p[i][j] = q[i];
+            }
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+                *reinterpret_cast<uint4*>(to + i * plane + d) = *reinterpret_cast<const uint4*>(p[i]);
+        } else {
+            const unsigned short* f = reinterpret_cast<const unsigned short*>(from);
+            uint4 w = make_uint4(0, 0, 0, 0);
+            if (f && wide && d < D) {
+                w = *reinterpret_cast<const uint4*>(f + d);
+            } else if (f) {
+                uint32_t h[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) h[j] = d + j < D ? f[d + j] : 0u;
+                w = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16,
+                               h[6] | h[7] << 16);
+            }
+            *reinterpret_cast<uint4*>(to + d) = w;
+        }
+    }
+}
+
+// Packs row rows[r] of x as row r of xc, zeros up to the next multiple of 256 rows; gives token r,
+// where it does not count, its zeros. A CTA a row.
 template <class T_IN>
 __global__ void __launch_bounds__(128)
     ce_gather(const T_IN* __restrict__ x, long long ldx, int T, int D, int Dp, long long plane,
@@ -159,27 +205,9 @@ __global__ void __launch_bounds__(128)
     ptx::griddep_launch_dependents();
     const int r = blockIdx.x;
     const int n = info->count;
-    if (r < ((n + 255) & ~255)) {
-        const T_IN* from = r < n ? x + (long long)rows[r] * ldx : nullptr;
-        unsigned short* to = xc + (long long)r * Dp;
-        if constexpr (sizeof(T_IN) == 4) {
-            for (int d = threadIdx.x; d < Dp; d += blockDim.x) {
-                __nv_bfloat16 p[3];
-                split3(from && d < D ? from[d] : 0.f, p);
-#pragma unroll
-                for (int i = 0; i < 3; ++i)
-                    to[i * plane + d] = *reinterpret_cast<const unsigned short*>(&p[i]);
-            }
-        } else if (wide) {  // 16-byte aligned rows of a multiple of 8
-            for (int d = threadIdx.x * 8; d < Dp; d += blockDim.x * 8)
-                *reinterpret_cast<uint4*>(to + d) =
-                    from ? *reinterpret_cast<const uint4*>(from + d) : make_uint4(0, 0, 0, 0);
-        } else {
-            const unsigned short* f = reinterpret_cast<const unsigned short*>(from);
-            for (int d = threadIdx.x; d < Dp; d += blockDim.x)
-                to[d] = f && d < D ? f[d] : (unsigned short)0;
-        }
-    }
+    if (r < ((n + 255) & ~255))
+        pack_row(r < n ? x + (long long)rows[r] * ldx : nullptr, D, Dp, plane, wide,
+                 xc + (long long)r * Dp);
     if (r < T) {
         const long long y = target64 ? reinterpret_cast<const long long*>(target)[r]
                                      : (long long)reinterpret_cast<const int*>(target)[r];
@@ -195,27 +223,14 @@ __global__ void __launch_bounds__(128)
     }
 }
 
-// Weights that TMA cannot read as they are: copied to rows of Dp elements, float32 as three
-// planes. A CTA a row.
+// Weights that TMA cannot read as they are. A CTA a row.
 template <class T_IN>
 __global__ void __launch_bounds__(128)
-    ce_weights(const T_IN* __restrict__ w, long long ldw, int D, int Dp, long long plane,
+    ce_weights(const T_IN* __restrict__ w, long long ldw, int D, int Dp, long long plane, int wide,
                unsigned short* __restrict__ wc) {
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
-    const T_IN* from = w + (long long)blockIdx.x * ldw;
-    unsigned short* to = wc + (long long)blockIdx.x * Dp;
-    for (int d = threadIdx.x; d < Dp; d += blockDim.x) {
-        if constexpr (sizeof(T_IN) == 4) {
-            __nv_bfloat16 p[3];
-            split3(d < D ? from[d] : 0.f, p);
-#pragma unroll
-            for (int i = 0; i < 3; ++i)
-                to[i * plane + d] = *reinterpret_cast<const unsigned short*>(&p[i]);
-        } else {
-            to[d] = d < D ? reinterpret_cast<const unsigned short*>(from)[d] : (unsigned short)0;
-        }
-    }
+    pack_row(w + (long long)blockIdx.x * ldw, D, Dp, plane, wide, wc + (long long)blockIdx.x * Dp);
 }
 
 // ---- the first product's epilogue -------------------------------------------------------------
@@ -765,7 +780,7 @@ cudaError_t run(const sgemm_ce& a, const DeviceInfo& info, int dev, cudaStream_t
     const int size = element_size(a.dtype);
     const Planes& planes = f32 ? THREE : ONE;
     const bool grad = a.dx || a.dweight;
-    const int Dp = round_up(a.D, 8);
+    const int Dp = round_up(a.D, 64);  // rows of whole 128-byte lines
     const long long pitch = round_up(a.V, 128);
     const int Tp = round_up(a.T, 256);
     // rows of a chunk: what is kept of their logits, and statistics of 64 columns at least
@@ -935,7 +950,8 @@ cudaError_t run(const sgemm_ce& a, const DeviceInfo& info, int dev, cudaStream_t
         e = hg::launch(ce_plan<int>, 1, PLAN_THREADS, 0, s, static_cast<const int*>(a.target),
                        a.token_weights, a.T, a.V, rows, label, ci, counters, 2 * chunks);
     if (e != cudaSuccess) return e;
-    const int wide_x = size == 2 && aligned16(a.x) && a.ldx % 8 == 0 && a.D % 8 == 0;
+    const int wide_x = aligned16(a.x) && a.ldx * size % 16 == 0 && a.D % 8 == 0;
+    const int wide_w = aligned16(a.weight) && a.ldw * size % 16 == 0 && a.D % 8 == 0;
     e = hg::launch(ce_gather<T_IN>, Tp, 128, 0, s, static_cast<const T_IN*>(a.x), a.ldx, a.T, a.D,
                    Dp, (long long)x_plane, static_cast<const int*>(rows),
                    static_cast<const CeInfo*>(ci), xc, a.target, int(a.target_bits == 64), a.V,
@@ -943,7 +959,7 @@ cudaError_t run(const sgemm_ce& a, const DeviceInfo& info, int dev, cudaStream_t
     if (e != cudaSuccess) return e;
     if (!direct) {
         e = hg::launch(ce_weights<T_IN>, a.V, 128, 0, s, static_cast<const T_IN*>(a.weight), a.ldw,
-                       a.D, Dp, (long long)w_plane, wc);
+                       a.D, Dp, (long long)w_plane, wide_w, wc);
         if (e != cudaSuccess) return e;
     }
     const int finish_ctas = chunk / FINISH_ROWS;

@@ -466,7 +466,8 @@ cudaError_t iterate(const Call& a, const DeviceInfo& info, __half* (&x)[2], __ha
 template <class T_IN, int PIECES>
 cudaError_t run(const Call& a, const DeviceInfo& info, int dev, cudaStream_t s) {
     const int r = std::min(a.M, a.N);
-    const int Np = (a.N + 7) / 8 * 8, rp = (r + 7) / 8 * 8;
+    // rows of whole 128-byte lines, so that TMA's boxes do not straddle them
+    const int Np = (a.N + 63) / 64 * 64, rp = (r + 63) / 64 * 64;
     const size_t x_plane = size_t(a.M) * Np, r_plane = size_t(r) * rp;
     const long long groups = (long long)a.M * ((a.N + 7) / 8);
     const int most = std::max(1, std::min(MAX_NORM_CTAS, 2048 / a.count + 1));
