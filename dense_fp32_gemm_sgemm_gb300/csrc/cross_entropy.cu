@@ -34,7 +34,6 @@ namespace sgemm {
 namespace {
 
 constexpr long long CE_CHUNK_BYTES = 1ll << 31;
-constexpr int FINISH_ROWS = 4;
 constexpr int FINISH_THREADS = 256;
 constexpr int PLAN_THREADS = 1024;
 constexpr int PLAN_ITEMS = 4;
@@ -192,8 +191,8 @@ __device__ __forceinline__ void pack_row(const T_IN* from, int D, int Dp, long l
     }
 }
 
-// Packs row rows[r] of x as row r of xc, zeros up to the next multiple of 256 rows; gives token r,
-// where it does not count, its zeros. A CTA a row.
+// Packs row rows[r] of x as row r of xc, zeros up to the next multiple of 64 rows (the reduction over
+// tokens reads them); gives token r, where it does not count, its zeros. A CTA a row.
 template <class T_IN>
 __global__ void __launch_bounds__(128)
     ce_gather(const T_IN* __restrict__ x, long long ldx, int T, int D, int Dp, long long plane,
@@ -205,7 +204,7 @@ __global__ void __launch_bounds__(128)
     ptx::griddep_launch_dependents();
     const int r = blockIdx.x;
     const int n = info->count;
-    if (r < ((n + 255) & ~255))
+    if (r < ((n + 63) & ~63))
         pack_row(r < n ? x + (long long)rows[r] * ldx : nullptr, D, Dp, plane, wide,
                  xc + (long long)r * Dp);
     if (r < T) {
@@ -244,7 +243,7 @@ template <int BN_, Keep KEEP>
 struct CeForward {
     static constexpr int BN = BN_;
     static constexpr int COLS = BN / 2;
-    static constexpr int PROBLEMS = 1;
+    static constexpr int PROBLEMS = 1, PLANES = 1;
     static constexpr bool CHAIN = false;
     struct Params {
         float2* stats;   // [block of COLS columns][row of the chunk]: maximum, sum
@@ -334,14 +333,14 @@ struct FinishArgs {
     int V, T, last_finished;  // CTAs of this kernel in the whole call
 };
 
-// FINISH_ROWS rows a CTA; 16 or 32 bytes of a row a thread and turn. Bound by the memory it
-// reads and writes.
-template <Keep KEEP>
+// ROWS rows a CTA, with the same columns of all of them in flight together; 8 columns a thread and
+// turn. Bound by the memory it reads and writes: at 8192 x 65536, 16 bits, 4 rows a CTA move
+// FINISH_GBS GB/s. Where that leaves SMs without a CTA, one row each.
+template <Keep KEEP, int ROWS>
 __global__ void __launch_bounds__(FINISH_THREADS) ce_finish(const FinishArgs a) {
-    __shared__ float2 part[FINISH_THREADS / 32][FINISH_ROWS];
-    __shared__ float row_from[FINISH_ROWS], row_log[FINISH_ROWS], row_scale[FINISH_ROWS],
-        row_label[FINISH_ROWS];
-    __shared__ int row_y[FINISH_ROWS];
+    __shared__ float2 part[FINISH_THREADS / 32][ROWS];
+    __shared__ float row_from[ROWS], row_log[ROWS], row_scale[ROWS], row_label[ROWS];
+    __shared__ int row_y[ROWS];
     __shared__ double sums[FINISH_THREADS / 32];
     __shared__ int is_last;
     ptx::griddep_wait();
@@ -349,11 +348,11 @@ __global__ void __launch_bounds__(FINISH_THREADS) ce_finish(const FinishArgs a) 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int count = a.info->count;
     const int live = min(max(count - a.live0, 0), a.live_max);
-    const int r0 = blockIdx.x * FINISH_ROWS;
+    const int r0 = blockIdx.x * ROWS;
     if (r0 < live) {
-        float m[FINISH_ROWS], l[FINISH_ROWS];
+        float m[ROWS], l[ROWS];
 #pragma unroll
-        for (int i = 0; i < FINISH_ROWS; ++i) {
+        for (int i = 0; i < ROWS; ++i) {
             m[i] = -INFINITY;
             l[i] = 0.f;
         }
@@ -365,16 +364,15 @@ __global__ void __launch_bounds__(FINISH_THREADS) ce_finish(const FinishArgs a) 
             m0 = top;
         };
         for (int b = tid; b < a.blocks; b += FINISH_THREADS) {
-            const float4* at = reinterpret_cast<const float4*>(
-                a.stats + (long long)b * a.stats_pitch + r0);
-            const float4 v0 = at[0], v1 = at[1];
-            join(m[0], l[0], v0.x, v0.y);
-            join(m[1], l[1], v0.z, v0.w);
-            join(m[2], l[2], v1.x, v1.y);
-            join(m[3], l[3], v1.z, v1.w);
+            const float2* at = a.stats + (long long)b * a.stats_pitch + r0;
+            float2 v[ROWS];
+#pragma unroll
+            for (int i = 0; i < ROWS; ++i) v[i] = at[i];
+#pragma unroll
+            for (int i = 0; i < ROWS; ++i) join(m[i], l[i], v[i].x, v[i].y);
         }
 #pragma unroll
-        for (int i = 0; i < FINISH_ROWS; ++i) {
+        for (int i = 0; i < ROWS; ++i) {
 #pragma unroll
             for (int o = 16; o; o >>= 1) {
                 const float m1 = __shfl_xor_sync(~0u, m[i], o), l1 = __shfl_xor_sync(~0u, l[i], o);
@@ -391,89 +389,105 @@ __global__ void __launch_bounds__(FINISH_THREADS) ce_finish(const FinishArgs a) 
             if (lane == 0) part[warp][i] = make_float2(m[i], l[i]);
         }
         __syncthreads();
-        if (tid < FINISH_ROWS) {
+    }
+    if (tid < ROWS) {
+        const int r = r0 + tid;
+        float from = 0.f, logl = 0.f, scale = 0.f, at_label = 0.f;
+        int y = -1;
+        if (r < live) {
             float2 t = part[0][tid];
             for (int w = 1; w < FINISH_THREADS / 32; ++w) {
                 const float2 u = part[w][tid];
-                join(t.x, t.y, u.x, u.y);
+                const float top = fmaxf(t.x, u.x);
+                t.y = (t.x == -INFINITY ? t.y : t.y * expf(t.x - top)) +
+                      (u.x == -INFINITY ? u.y : u.y * expf(u.x - top));
+                t.x = top;
             }
-            const int r = r0 + tid;
-            float scale = 0.f;
-            int y = -1;
-            if (r < live) {
-                const int token = a.rows[r];
-                y = a.label[r];
-                const float logl = logf(t.y);
-                const float picked = a.picked[r];
-                a.lse[token] = t.x + logl;
-                a.losses[token] = (t.x - picked) + logl;
-                const float c = a.c ? a.c[token] : a.info->c_mean;
-                scale = c / a.info->c_max;
-                row_from[tid] = t.x;
-                row_log[tid] = logl;
-                row_label[tid] = expm1f((picked - t.x) - logl) * scale;
-            }
-            row_scale[tid] = scale;
-            row_y[tid] = y;
+            const int token = a.rows[r];
+            y = a.label[r];
+            from = t.x;
+            logl = logf(t.y);
+            const float picked = a.picked[r];
+            a.lse[token] = from + logl;
+            a.losses[token] = (from - picked) + logl;
+            const float c = a.c ? a.c[token] : a.info->c_mean;
+            scale = c / a.info->c_max;
+            at_label = expm1f((picked - from) - logl) * scale;
         }
-        __syncthreads();
+        row_from[tid] = from;
+        row_log[tid] = logl;
+        row_scale[tid] = scale;
+        row_label[tid] = at_label;
+        row_y[tid] = y;
     }
+    __syncthreads();
     if constexpr (KEEP != Keep::none) {
-        const int padded = (live + 63) & ~63;
-        for (int i = 0; i < FINISH_ROWS; ++i) {
-            const int r = r0 + i;
-            if (r >= padded) break;
-            const bool there = r < live;
-            const float from = there ? row_from[i] : 0.f, logl = there ? row_log[i] : 0.f;
-            const float scale = there ? row_scale[i] : 0.f;
-            const int y = there ? row_y[i] : -1;
+        const int padded = (live + 63) & ~63;  // zeros up to here: the reduction over tokens reads them
+        const int n = min(ROWS, padded - r0);
+        if (n > 0) {
             for (int v0 = tid * 8; v0 < a.V; v0 += FINISH_THREADS * 8) {
-                const bool labelled = y >= v0 && y < v0 + 8;
-                float g[8];
                 if constexpr (KEEP == Keep::logits) {
-                    const float4* at = reinterpret_cast<const float4*>(
-                        static_cast<const float*>(a.kept) + (long long)r * a.pitch + v0);
-                    if (there) {
-                        const float4 u = at[0], w = at[1];
-                        const float s[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) g[j] = expf((s[j] - from) - logl) * scale;
-                    } else {
+#pragma unroll 1
+                    for (int i = 0; i < n; ++i) {
+                        const int r = r0 + i, y = row_y[i];
+                        const float* at =
+                            static_cast<const float*>(a.kept) + (long long)r * a.pitch + v0;
+                        float g[8];
 #pragma unroll
                         for (int j = 0; j < 8; ++j) g[j] = 0.f;
-                    }
-                    if (labelled) {
+                        if (r < live) {
+                            const float4 u = *reinterpret_cast<const float4*>(at);
+                            const float4 w = *reinterpret_cast<const float4*>(at + 4);
+                            const float s[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) g[j] = y == v0 + j ? row_label[i] : g[j];
-                    }
-                    uint32_t w[3][4];
+                            for (int j = 0; j < 8; ++j)
+                                g[j] = expf((s[j] - row_from[i]) - row_log[i]) * row_scale[i];
+                        }
+                        if (y >= v0 && y < v0 + 8) {
 #pragma unroll
-                    for (int j = 0; j < 8; j += 2) {
-                        __nv_bfloat16 p[3], q[3];
-                        split3(g[j], p);
-                        split3(g[j + 1], q);
+                            for (int j = 0; j < 8; ++j) g[j] = y == v0 + j ? row_label[i] : g[j];
+                        }
+                        uint32_t w[3][4];
+#pragma unroll
+                        for (int j = 0; j < 8; j += 2) {
+                            __nv_bfloat16 p[3], q[3];
+                            split3(g[j], p);
+                            split3(g[j + 1], q);
+#pragma unroll
+                            for (int k = 0; k < 3; ++k)
+                                w[k][j / 2] =
+                                    uint32_t(*reinterpret_cast<unsigned short*>(&p[k])) |
+                                    uint32_t(*reinterpret_cast<unsigned short*>(&q[k])) << 16;
+                        }
 #pragma unroll
                         for (int k = 0; k < 3; ++k)
-                            w[k][j / 2] = uint32_t(*reinterpret_cast<unsigned short*>(&p[k])) |
-                                          uint32_t(*reinterpret_cast<unsigned short*>(&q[k])) << 16;
+                            *reinterpret_cast<uint4*>(a.planes + k * a.plane +
+                                                      (long long)r * a.pitch + v0) =
+                                make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
                     }
-#pragma unroll
-                    for (int k = 0; k < 3; ++k)
-                        *reinterpret_cast<uint4*>(a.planes + k * a.plane + (long long)r * a.pitch +
-                                                  v0) = make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
                 } else {
                     constexpr bool BF = KEEP == Keep::bf16;
-                    constexpr float UP = BF ? 1.f : float(1 << FP16_GRAD_BITS);
-                    constexpr float UNIT = BF ? 1.f : UP / float(1 << FP16_EXP_BITS);
-                    uint4* at = reinterpret_cast<uint4*>(
-                        static_cast<unsigned short*>(a.kept) + (long long)r * a.pitch + v0);
-                    uint4 out = make_uint4(0, 0, 0, 0);
-                    if (there) {
-                        const uint4 e = *at;
-                        const float2 st =
-                            a.stats[(long long)(v0 / a.cols) * a.stats_pitch + r];
-                        const float f = expf((st.x - from) - logl) * scale * UNIT;
-                        const uint32_t in[4] = {e.x, e.y, e.z, e.w};
+                    constexpr float GRAD_UP = BF ? 1.f : float(1 << FP16_GRAD_BITS);
+                    constexpr float UNIT = BF ? 1.f : GRAD_UP / float(1 << FP16_EXP_BITS);
+                    unsigned short* at =
+                        static_cast<unsigned short*>(a.kept) + (long long)r0 * a.pitch + v0;
+                    const float2* stats = a.stats + (long long)(v0 / a.cols) * a.stats_pitch + r0;
+                    uint4 e[ROWS];
+                    float top[ROWS];
+#pragma unroll
+                    for (int i = 0; i < ROWS; ++i) {
+                        e[i] = make_uint4(0, 0, 0, 0);
+                        top[i] = 0.f;
+                        if (r0 + i < live) {
+                            e[i] = *reinterpret_cast<const uint4*>(at + i * a.pitch);
+                            top[i] = stats[i].x;
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < ROWS; ++i) {
+                        const float f = expf((top[i] - row_from[i]) - row_log[i]) * row_scale[i] * UNIT;
+                        const uint32_t in[4] = {e[i].x, e[i].y, e[i].z, e[i].w};
+                        float g[8];
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             float2 v;
@@ -486,15 +500,17 @@ __global__ void __launch_bounds__(FINISH_THREADS) ce_finish(const FinishArgs a) 
                             g[2 * j] = v.x * f;
                             g[2 * j + 1] = v.y * f;
                         }
-                        if (labelled) {
+                        const int y = row_y[i];
+                        if (y >= v0 && y < v0 + 8) {
 #pragma unroll
                             for (int j = 0; j < 8; ++j)
-                                g[j] = y == v0 + j ? row_label[i] * UP : g[j];
+                                g[j] = y == v0 + j ? row_label[i] * GRAD_UP : g[j];
                         }
-                        out = make_uint4(hg::pack2<BF>(g[0], g[1]), hg::pack2<BF>(g[2], g[3]),
-                                         hg::pack2<BF>(g[4], g[5]), hg::pack2<BF>(g[6], g[7]));
+                        uint4 out = make_uint4(hg::pack2<BF>(g[0], g[1]), hg::pack2<BF>(g[2], g[3]),
+                                               hg::pack2<BF>(g[4], g[5]), hg::pack2<BF>(g[6], g[7]));
+                        if (r0 + i >= live) out = make_uint4(0, 0, 0, 0);
+                        if (i < n) *reinterpret_cast<uint4*>(at + i * a.pitch) = out;
                     }
-                    *at = out;
                 }
             }
         }
@@ -543,7 +559,7 @@ template <bool SUMS>
 struct CeGrad {
     static constexpr int BN = 256;
     static constexpr int COLS = BN / 2;
-    static constexpr int PROBLEMS = 2;
+    static constexpr int PROBLEMS = 2, PLANES = 1;
     static constexpr bool CHAIN = false;
     struct Params {
         GradOut out[2];
@@ -765,6 +781,12 @@ cudaError_t forward(Keep keep, const hg::Args<1>& g, float2* stats, float* picke
     }
 }
 
+template <Keep KEEP>
+cudaError_t finish(const FinishArgs& a, int rows, int ctas, cudaStream_t s) {
+    return rows == 4 ? hg::launch(ce_finish<KEEP, 4>, ctas, FINISH_THREADS, 0, s, a)
+                     : hg::launch(ce_finish<KEEP, 1>, ctas, FINISH_THREADS, 0, s, a);
+}
+
 // Parts of dx's reduction: a unit should take no more than half of a pair's share of the launch,
 // so that the shares come out even.
 int dx_splits(int tiles_dx, int kblocks_dx, int tiles_dw, int kblocks_dw, int pairs) {
@@ -952,7 +974,7 @@ cudaError_t run(const sgemm_ce& a, const DeviceInfo& info, int dev, cudaStream_t
     if (e != cudaSuccess) return e;
     const int wide_x = aligned16(a.x) && a.ldx * size % 16 == 0 && a.D % 8 == 0;
     const int wide_w = aligned16(a.weight) && a.ldw * size % 16 == 0 && a.D % 8 == 0;
-    e = hg::launch(ce_gather<T_IN>, Tp, 128, 0, s, static_cast<const T_IN*>(a.x), a.ldx, a.T, a.D,
+    e = hg::launch(ce_gather<T_IN>, round_up(a.T, 64), 128, 0, s, static_cast<const T_IN*>(a.x), a.ldx, a.T, a.D,
                    Dp, (long long)x_plane, static_cast<const int*>(rows),
                    static_cast<const CeInfo*>(ci), xc, a.target, int(a.target_bits == 64), a.V,
                    a.losses, a.lse, static_cast<T_IN*>(a.dx), a.lddx, wide_x);
@@ -962,7 +984,10 @@ cudaError_t run(const sgemm_ce& a, const DeviceInfo& info, int dev, cudaStream_t
                        a.D, Dp, (long long)w_plane, wide_w, wc);
         if (e != cudaSuccess) return e;
     }
-    const int finish_ctas = chunk / FINISH_ROWS;
+    // rows that ce_finish has something to do for: those of tokens, for gradients 64 at a time
+    const int finish_n = std::min(chunk, grad ? round_up(a.T, 64) : a.T);
+    const int finish_rows = finish_n >= 8 * info.sm_count ? 4 : 1;
+    const int finish_ctas = (finish_n + finish_rows - 1) / finish_rows;
     for (int c = 0; c < chunks; ++c) {
         const int live0 = c * chunk;
         const Keep keep = !grad ? Keep::none : f32 ? Keep::logits : bf16 ? Keep::bf16 : Keep::fp16;
@@ -978,19 +1003,10 @@ cudaError_t run(const sgemm_ce& a, const DeviceInfo& info, int dev, cudaStream_t
         FinishArgs fa = {stats, stats_pitch, blocks, cols, picked, rows + live0, label + live0, ci,
                          live0, chunk, a.token_weights, a.loss, a.losses, a.lse, kept, g_planes,
                          pitch, (long long)g_plane, a.V, a.T, finish_ctas * chunks};
-        switch (keep) {
-            case Keep::none:
-                e = hg::launch(ce_finish<Keep::none>, finish_ctas, FINISH_THREADS, 0, s, fa);
-                break;
-            case Keep::bf16:
-                e = hg::launch(ce_finish<Keep::bf16>, finish_ctas, FINISH_THREADS, 0, s, fa);
-                break;
-            case Keep::fp16:
-                e = hg::launch(ce_finish<Keep::fp16>, finish_ctas, FINISH_THREADS, 0, s, fa);
-                break;
-            default:
-                e = hg::launch(ce_finish<Keep::logits>, finish_ctas, FINISH_THREADS, 0, s, fa);
-        }
+        e = keep == Keep::none   ? finish<Keep::none>(fa, finish_rows, finish_ctas, s)
+            : keep == Keep::bf16 ? finish<Keep::bf16>(fa, finish_rows, finish_ctas, s)
+            : keep == Keep::fp16 ? finish<Keep::fp16>(fa, finish_rows, finish_ctas, s)
+                                 : finish<Keep::logits>(fa, finish_rows, finish_ctas, s);
         if (e != cudaSuccess) return e;
         if (!grad) continue;
         bwd.counter = counters + 2 * c + 1;

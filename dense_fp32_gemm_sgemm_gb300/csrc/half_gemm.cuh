@@ -35,7 +35,7 @@ namespace hg {
 constexpr int BM = 256;       // rows of a tile (both CTAs)
 constexpr int HALF_M = 128;   // rows of one CTA
 constexpr int BK = 64;        // reduction elements in a stage: 128 bytes
-constexpr int STAGES = 5;
+constexpr int MAX_STAGES = 6;
 constexpr int SLOTS = 4;      // units handed out ahead
 constexpr int EPI_WARPS = 8;
 constexpr int EPI_WARP0 = 4;  // warp 3 only fills up the first warpgroup
@@ -47,16 +47,27 @@ constexpr int REGS_MANY = 216;
 constexpr int A_BYTES = HALF_M * BK * 2;
 constexpr int CHUNK_BYTES = 64 * BK * 2;  // 64 elements of the other index by 64 of k
 constexpr int STAGING = 4096;             // bytes of a staging block, two for an epilogue warp
-constexpr int NUM_BARS = 2 * STAGES + 4 + 1 + 2 * SLOTS + 2 * EPI_WARPS;
+constexpr int NUM_BARS = 2 * MAX_STAGES + 4 + 1 + 2 * SLOTS + 2 * EPI_WARPS;
 constexpr int MAX_PRODUCTS = 6;
 
 template <int BN>
 constexpr int B_BYTES = BN / 2 * BK * 2;
-template <int BN>
-constexpr int STAGE_BYTES = A_BYTES + B_BYTES<BN>;
-template <int BN>
-constexpr int SMEM_BYTES = STAGES * STAGE_BYTES<BN> + 2 * EPI_WARPS * STAGING + 512 + 1024;
-static_assert(SMEM_BYTES<256> <= 232448, "shared memory of an SM");
+// A stage: 64 k of both operands, of one plane each (then every product has a stage to itself), or
+// of all PLANES of them, which all products of those k share. A stage of one product and 128 columns
+// takes some 430 cycles to wait for, issue and hand on where its MMAs take 256, and its 24 KiB 384 to
+// arrive; with two planes three products share 48 KiB, a wait and a commit. (Of 256 columns the MMAs
+// take 512, and three stages of 64 KiB would leave the epilogue too little.)
+template <class EPI>
+struct Ring {
+    static constexpr int BN = EPI::BN, PLANES = EPI::PLANES;
+    static constexpr int B_AT = PLANES * A_BYTES;  // of B in a stage
+    static constexpr int STAGE_BYTES = PLANES * (A_BYTES + B_BYTES<BN>);
+    static constexpr int STAGES = BN == 256 ? 5 : PLANES == 1 ? 6 : 3;
+    static constexpr int SMEM_BYTES =
+        STAGES * STAGE_BYTES + 2 * EPI_WARPS * STAGING + 512 + 1024;
+    static_assert(SMEM_BYTES <= 232448, "shared memory of an SM");
+    static_assert(STAGES <= MAX_STAGES && (PLANES == 1 || (PLANES == 2 && BN == 128)), "see above");
+};
 
 // One product of a launch. Sizes are in elements; `live` may replace one of them on the device.
 struct Problem {
@@ -69,7 +80,7 @@ struct Problem {
     int a_mn, b_mn;     // operand stored with its other index contiguous (else with k)
     int a_row, b_row;   // added to the row coordinate (k or the other index, whichever is a row)
     int planes_a, planes_b;
-    int products;       // pairs of planes, each staged for itself
+    int products;       // pairs of planes, smallest products first
     unsigned char pa[MAX_PRODUCTS], pb[MAX_PRODUCTS];
     unsigned idesc;     // instruction descriptor without N
 };
@@ -89,7 +100,7 @@ struct Args {
     // phase i = 3 round + problem, zero before the launch.
     int rounds;
     int* done;
-    int seg_steps;  // stages in an accumulator segment
+    int seg_steps;  // stages in an accumulator segment (see Ring)
 };
 
 // A unit of work.
@@ -207,22 +218,22 @@ struct Smem {
     volatile int* abort_flag;
     __device__ uint32_t at(int i) const { return bar0 + 8u * i; }
     __device__ uint32_t full(int s) const { return at(s); }
-    __device__ uint32_t empty(int s) const { return at(STAGES + s); }
-    __device__ uint32_t acc_full(int b) const { return at(2 * STAGES + b); }
-    __device__ uint32_t acc_empty(int b) const { return at(2 * STAGES + 2 + b); }
-    __device__ uint32_t slot_full(int i) const { return at(2 * STAGES + 4 + i); }
-    __device__ uint32_t slot_empty(int i) const { return at(2 * STAGES + 4 + SLOTS + i); }
-    __device__ uint32_t drain() const { return at(2 * STAGES + 4 + 2 * SLOTS); }
-    __device__ uint32_t loaded(int i) const { return at(2 * STAGES + 5 + 2 * SLOTS + i); }
+    __device__ uint32_t empty(int s) const { return at(MAX_STAGES + s); }
+    __device__ uint32_t acc_full(int b) const { return at(2 * MAX_STAGES + b); }
+    __device__ uint32_t acc_empty(int b) const { return at(2 * MAX_STAGES + 2 + b); }
+    __device__ uint32_t slot_full(int i) const { return at(2 * MAX_STAGES + 4 + i); }
+    __device__ uint32_t slot_empty(int i) const { return at(2 * MAX_STAGES + 4 + SLOTS + i); }
+    __device__ uint32_t drain() const { return at(2 * MAX_STAGES + 4 + 2 * SLOTS); }
+    __device__ uint32_t loaded(int i) const { return at(2 * MAX_STAGES + 5 + 2 * SLOTS + i); }
 };
 
-template <int BN>
+template <class R>
 __device__ __forceinline__ Smem carve(uint8_t* raw) {
     uint8_t* base =
         reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     Smem s;
     s.ring = ptx::smem_u32(base);
-    s.staging = base + STAGES * STAGE_BYTES<BN>;
+    s.staging = base + R::STAGES * R::STAGE_BYTES;
     uint64_t* bars = reinterpret_cast<uint64_t*>(s.staging + 2 * EPI_WARPS * STAGING);
     s.bar0 = ptx::smem_u32(bars);
     int* words = reinterpret_cast<int*>(bars + NUM_BARS);
@@ -395,7 +406,7 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 //   void unit(const Unit&, int row, int col, float (&acc)[BN / 2])
 // called by each epilogue warp at the beginning of a unit (to load what it will need) and with its
 // sums: lane l holds row `row` + l, columns col .. col + BN / 2.
-// EPI::PROBLEMS: of the launch at most. EPI::CHAIN: units are done in order, and one of a phase
+// EPI::PROBLEMS: of the launch at most. EPI::PLANES: staged together (see Ring). EPI::CHAIN: units are done in order, and one of a phase
 // waits until all of the phase before that belong to the same product have been stored. Every earlier unit was claimed by a CTA
 // that runs, and waits for still earlier ones only, so that all waits end however many CTAs the
 // GPU runs at a time.
@@ -406,13 +417,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     constexpr int BN = EPI::BN;
     constexpr bool CHAIN = EPI::CHAIN;
     constexpr int COLS = BN / 2;  // columns of an epilogue warp
+    using R = Ring<EPI>;
+    constexpr int STAGES = R::STAGES;
     extern __shared__ uint8_t smem_raw[];
-    const Smem sm = carve<BN>(smem_raw);
+    const Smem sm = carve<R>(smem_raw);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = ptx::cluster_ctarank();
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < 2 * STAGES; ++s) ptx::mbar_init(sm.at(s), 1);  // full, empty
+        for (int s = 0; s < 2 * MAX_STAGES; ++s) ptx::mbar_init(sm.at(s), 1);  // full, empty
         for (int b = 0; b < 2; ++b) {
             ptx::mbar_init(sm.acc_full(b), 1);
             ptx::mbar_init(sm.acc_empty(b), 2 * EPI_WARPS);
@@ -488,7 +501,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             const uint32_t full0 = sm.full(0), empty0 = sm.empty(0);
             const uint32_t signal0 = ptx::mapa_shared(full0, 0);  // the first CTA's barriers
             const bool expects = is_a && rank == 0;
-            const uint32_t ring = sm.ring + (is_a ? 0 : A_BYTES);
+            const uint32_t ring = sm.ring + (is_a ? 0 : R::B_AT);
+            const uint32_t plane_bytes = is_a ? A_BYTES : B_BYTES<BN>;
             // the first units are given out by the pairs' numbers, in a chain claimed like all
             // others: a pair may not be running yet
             const int pairs = CHAIN ? 0 : gridDim.x >> 1;
@@ -539,18 +553,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 bool ok = !CHAIN || wait_before(t);
                 for (int kb = t.kb0; ok && kb < t.kb1; ++kb) {
                     unsigned planes_left = order;
-                    for (int q = 0; q < products; ++q) {
+                    const int stages = R::PLANES == 1 ? products : 1;
+                    for (int q = 0; q < stages; ++q) {
                         const int z = z0 + int(planes_left & 15u);
                         planes_left >>= 4;
                         ok = wait_all(empty0 + 8u * s, ph ^ 1u);
                         if (!ok) break;
                         const uint32_t bar = signal0 + 8u * s;
-                        const uint32_t st = ring + uint32_t(s) * STAGE_BYTES<BN>;
+                        uint32_t st = ring + uint32_t(s) * R::STAGE_BYTES;
                         // the bytes of both CTAs; some may have arrived already
                         if (expects)
-                            ptx::mbar_arrive_expect_tx_elect(full0 + 8u * s, 2 * STAGE_BYTES<BN>);
-                        ptx::tma_load_3d_pair(st, map, bar, x, y, z);
-                        if (two) ptx::tma_load_3d_pair(st + CHUNK_BYTES, map, bar, x + 64, y, z);
+                            ptx::mbar_arrive_expect_tx_elect(full0 + 8u * s, 2 * R::STAGE_BYTES);
+#pragma unroll
+                        for (int i = 0; i < R::PLANES; ++i) {
+                            const int zi = R::PLANES == 1 ? z : z0 + i;
+                            ptx::tma_load_3d_pair(st, map, bar, x, y, zi);
+                            if (two)
+                                ptx::tma_load_3d_pair(st + CHUNK_BYTES, map, bar, x + 64, y, zi);
+                            st += plane_bytes;
+                        }
                         if (++s == STAGES) {
                             s = 0;
                             ph ^= 1u;
@@ -582,8 +603,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 const Unit t = unit_at<BN, CHAIN>(g, n_units, u, live);
                 const Problem& p = g.p[t.problem];
                 const uint32_t idesc = p.idesc | (uint32_t(BN >> 3) << 17);
-                const OperandDesc a(sm.ring, p.a_mn), b(sm.ring + A_BYTES, p.b_mn);
-                int left = (t.kb1 - t.kb0) * p.products;
+                const OperandDesc a(sm.ring, p.a_mn), b(sm.ring + R::B_AT, p.b_mn);
+                // the products' planes within a stage, four bits each
+                const int products = p.products;
+                unsigned order_a = 0, order_b = 0;
+                if constexpr (R::PLANES > 1) {
+                    for (int q = 0; q < products; ++q) {
+                        order_a |= unsigned(p.pa[q]) << (4 * q);
+                        order_b |= unsigned(p.pb[q]) << (4 * q);
+                    }
+                }
+                int left = (t.kb1 - t.kb0) * (R::PLANES == 1 ? products : 1);
                 for (; ok && left > 0; left -= g.seg_steps, ++seg) {
                     const int half = seg & 1;
                     ok = wait_all(sm.acc_empty(half), ((seg >> 1) & 1) ^ 1);
@@ -595,9 +625,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                         ok = wait_all(sm.full(s), ph);
                         if (!ok) break;
                         ptx::tc_fence_after();
-                        const uint32_t at = uint32_t(s) * (STAGE_BYTES<BN> >> 4);
-                        ptx::mma_pair_x4(d, a.lo + at, a.hi, a.step, b.lo + at, b.hi, b.step, idesc,
-                                         j);
+                        const uint32_t at = uint32_t(s) * (R::STAGE_BYTES >> 4);
+                        if constexpr (R::PLANES == 1) {
+                            ptx::mma_pair_x4(d, a.lo + at, a.hi, a.step, b.lo + at, b.hi, b.step,
+                                             idesc, j);
+                        } else {
+                            unsigned oa = order_a, ob = order_b;
+                            for (int q = 0; q < products; ++q) {
+                                ptx::mma_pair_x4(d, a.lo + at + (oa & 15u) * (A_BYTES >> 4), a.hi,
+                                                 a.step, b.lo + at + (ob & 15u) * (B_BYTES<BN> >> 4),
+                                                 b.hi, b.step, idesc, j | q);
+                                oa >>= 4;
+                                ob >>= 4;
+                            }
+                        }
                         issued = true;
                         ptx::mma_commit_pair_elect(sm.empty(s), 0x3);
                         if (++s == STAGES) {
@@ -638,7 +679,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             if (u < 0) break;
             if (lane == 0) taken(i);
             const Unit t = unit_at<BN, CHAIN>(g, n_units, u, live);
-            const int steps = (t.kb1 - t.kb0) * g.p[t.problem].products;
+            const int steps = (t.kb1 - t.kb0) * (R::PLANES == 1 ? g.p[t.problem].products : 1);
             const int segs = (steps + g.seg_steps - 1) / g.seg_steps;
             const int row = t.row0 + int(rank) * HALF_M + q * 32, col = t.col0 + h * COLS;
             if constexpr (CHAIN) {
@@ -739,7 +780,7 @@ inline int box_rows(bool mn, int rows_of_cta) { return mn ? BK : rows_of_cta; }
 template <class EPI>
 cudaError_t launch_gemm(const Args<EPI::PROBLEMS>& g, const typename EPI::Params& ep, int sm_count,
                         cudaStream_t stream) {
-    constexpr int bytes = SMEM_BYTES<EPI::BN>;
+    constexpr int bytes = Ring<EPI>::SMEM_BYTES;
     cudaError_t e = set_smem_limit_once<half_gemm_kernel<EPI>>(bytes);
     if (e != cudaSuccess) return e;
     // pairs for all units, in a chain for those of its largest phase

@@ -17,6 +17,7 @@
 // simulations of 256 x 256 to 512 x 1024.) The pieces are of values times a power of two, so that
 // small entries stay in FP16's normal range: 2^13 for X, 2^12 for A, 2^10 for the polynomial.
 #include <algorithm>
+#include <cmath>
 #include <cstring>
 
 #include "half_gemm.cuh"
@@ -155,6 +156,7 @@ struct NsChain {
     static constexpr int BN = BN_;
     static constexpr int COLS = BN / 2;
     static constexpr int PROBLEMS = 6;
+    static constexpr int PLANES = BN == 128 ? PIECES : 1;
     static constexpr bool CHAIN = true;
     struct Params {
         FactorMaps gram, poly;
@@ -394,7 +396,7 @@ cudaError_t iterate(const Call& a, const DeviceInfo& info, __half* (&x)[2], __ha
     g.done = counters + 1;
     g.err = info.error_word;
     // 16-bit results bear an accumulator that is cut off 4 * 256 times (2^-15 of a sum, at most)
-    g.seg_steps = a.dtype == SGEMM_FLOAT32 ? 8 : 256;
+    g.seg_steps = a.dtype == SGEMM_FLOAT32 ? (Chain::PLANES == 1 ? 8 : 3) : 256;
     // operand maps: k contiguous, or the other index
     auto x_operand = [&](CUtensorMap& m, int i, bool mn, int rows_of_cta) {
         return hg::encode_operand(&m, x[i], false, a.N, a.M, Np, 2 * a.count, x_plane,
@@ -463,6 +465,35 @@ cudaError_t iterate(const Call& a, const DeviceInfo& info, __half* (&x)[2], __ha
     return hg::launch_gemm<Chain>(g, p, info.sm_count, s);
 }
 
+// Columns of a tile: whatever gives the shorter step by what was measured: 522 cycles for a stage
+// of 256 columns, 430 for one of 128, or 270 for each product where three share a stage; and what
+// the last unit's epilogue adds to a phase, 6000 or 3000. A phase of one matrix takes whole rounds
+// of units; the phases of several overlap.
+template <int BN>
+double step_cycles(const Call& a, int pieces, int pairs) {
+    const int r = std::min(a.M, a.N), q = std::max(a.M, a.N);
+    const int products = pieces == 1 ? 1 : 3;
+    const double stage = BN == 256 ? 522. : pieces == 1 ? 430. : 270.;
+    hg::Problem square = {}, whole = {};
+    square.symmetric = 1;
+    const int tiles_r = hg::ceil_div(r, hg::BM);
+    const double units_r =
+        double(a.count) * hg::tile_count<BN>(square, tiles_r, hg::ceil_div(r, BN));
+    const double units_x = double(a.count) * hg::tile_count<BN>(whole, hg::ceil_div(a.M, hg::BM),
+                                                                hg::ceil_div(a.N, BN));
+    auto rounds = [&](double units) {
+        const double n = units / pairs;
+        return a.count == 1 ? std::ceil(n) : std::max(n, 1.);
+    };
+    const double k_q = hg::ceil_div(q, hg::BK), k_r = hg::ceil_div(r, hg::BK);
+    return (rounds(units_r) * (k_q + k_r) + rounds(units_x) * k_r) * products * stage +
+           3 * (BN == 256 ? 6000. : 3000.);
+}
+
+int tile_columns(const Call& a, int pieces, int pairs) {
+    return step_cycles<128>(a, pieces, pairs) < step_cycles<256>(a, pieces, pairs) ? 128 : 256;
+}
+
 template <class T_IN, int PIECES>
 cudaError_t run(const Call& a, const DeviceInfo& info, int dev, cudaStream_t s) {
     const int r = std::min(a.M, a.N);
@@ -512,9 +543,7 @@ cudaError_t run(const Call& a, const DeviceInfo& info, int dev, cudaStream_t s) 
     e = launch2(ns_convert<T_IN>, CONVERT_THREADS, G, a.ldg, a.stride_g, a.M, a.N, Np,
                 static_cast<const double*>(partial), ctas, a.eps, x[0]);
     if (e != cudaSuccess) return e;
-    // 128 columns a tile where 256 would leave pairs without one
-    const int tiles = ((a.M + 255) / 256) * ((a.N + 255) / 256) * a.count;
-    return tiles < std::max(info.sm_count / 2, 1)
+    return tile_columns(a, PIECES, std::max(info.sm_count / 2, 1)) == 128
                ? iterate<128, PIECES>(a, info, x, gram, poly, counters, Np, rp, s)
                : iterate<256, PIECES>(a, info, x, gram, poly, counters, Np, rp, s);
 }
