@@ -367,20 +367,28 @@ __device__ __forceinline__ void store_block(uint8_t* block, const Rows& to, int 
             }
         }
     } else {
-        constexpr int PER = 16 / SIZE;  // elements of a piece
-        const int count = min(to.count, 32), elements = to.bytes / SIZE;
+        // four rows in flight, 32 consecutive elements a store
+        constexpr int PER = 16 / SIZE, TURNS = SIZE == 4 ? 1 : 2;
+        const int elements = to.bytes / SIZE;
 #pragma unroll 1
-        for (int r = 0; r < count; ++r) {
-            const int row = MAPPED ? __shfl_sync(~0u, index, r) : r;
-            char* p = to.base + row * to.pitch;
-#pragma unroll 1
-            for (int e = lane; e < elements; e += 32) {
-                const uint4* q = staged(block, r, e / PER);
-                if (SIZE == 4)
-                    reinterpret_cast<uint32_t*>(p)[e] = reinterpret_cast<const uint32_t*>(q)[e % PER];
-                else
-                    reinterpret_cast<unsigned short*>(p)[e] =
-                        reinterpret_cast<const unsigned short*>(q)[e % PER];
+        for (int r0 = 0; r0 < 32 && r0 < to.count; r0 += 4) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = r0 + i, row = MAPPED ? __shfl_sync(~0u, index, r) : r;
+                char* p = to.base + row * to.pitch;
+#pragma unroll
+                for (int j = 0; j < TURNS; ++j) {
+                    const int e = lane + 32 * j;
+                    const uint4* q = staged(block, r, e / PER);
+                    const bool here = e < elements && r < to.count;
+                    if (SIZE == 4) {
+                        const uint32_t v = reinterpret_cast<const uint32_t*>(q)[e % PER];
+                        if (here) reinterpret_cast<uint32_t*>(p)[e] = v;
+                    } else {
+                        const unsigned short v = reinterpret_cast<const unsigned short*>(q)[e % PER];
+                        if (here) reinterpret_cast<unsigned short*>(p)[e] = v;
+                    }
+                }
             }
         }
     }
