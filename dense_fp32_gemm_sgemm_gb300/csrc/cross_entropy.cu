@@ -6,7 +6,8 @@
 // over the tokens that count (0 <= y < V). Three products of T V D multiply-adds, the least that
 // the gradients take; the logits exist in the tensor core's accumulators only.
 //
-//  1. ce_plan lists the counted tokens in order, ce_gather packs their rows of x. Uncounted rows
+//  1. ce_plan lists the counted tokens in order, ce_gather packs their rows of x (ce_select does
+//     both for few). Uncounted rows
 //     are never read again: whatever they hold stays out of dW, and costs no products.
 //  2. The first product's epilogue has a row's 64 or 128 columns in a thread: their maximum m and
 //     sum of exp(s - m) (FP32) go to `stats`, the target's logit (FP32) is picked out, and, for
@@ -37,6 +38,7 @@ constexpr long long CE_CHUNK_BYTES = 1ll << 31;
 constexpr int FINISH_THREADS = 256;
 constexpr int PLAN_THREADS = 1024;
 constexpr int PLAN_ITEMS = 4;
+constexpr int SELECT_TOKENS = 1024;  // up to which ce_select does the work of both
 constexpr float LOG2E = 1.4426950408889634f;
 
 // What ce_plan leaves on the device.
@@ -219,6 +221,92 @@ __global__ void __launch_bounds__(128)
                 for (int d = threadIdx.x; d < D; d += blockDim.x)
                     dx[(long long)r * lddx + d] = T_IN(0.f);
         }
+    }
+}
+
+// ce_plan and ce_gather in one launch, for few tokens: every CTA goes through all targets itself to
+// find the one that its row is for (1 token: 16 us a call in two launches, SELECT_US in one).
+template <class T_IN>
+__global__ void __launch_bounds__(128)
+    ce_select(const T_IN* __restrict__ x, long long ldx, int T, int D, int Dp, long long plane,
+              const void* __restrict__ target, int target64, int V, const float* __restrict__ c,
+              int* __restrict__ rows, int* __restrict__ label, CeInfo* info, int* counters,
+              int n_counters, unsigned short* __restrict__ xc, float* __restrict__ losses,
+              float* __restrict__ lse, T_IN* __restrict__ dx, long long lddx, int wide) {
+    __shared__ int warp_sum[4];
+    __shared__ float warp_max[4];
+    __shared__ int my_token;
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = blockIdx.x;
+    auto target_of = [&](int t) {
+        const long long y = target64 ? reinterpret_cast<const long long*>(target)[t]
+                                     : (long long)reinterpret_cast<const int*>(target)[t];
+        return y >= 0 && y < V ? int(y) : -1;
+    };
+    const int each = (T + 127) / 128, t0 = tid * each, t1 = min(t0 + each, T);
+    int mine = 0;
+    float top = 0.f;
+    for (int t = t0; t < t1; ++t) {
+        if (target_of(t) < 0) continue;
+        ++mine;
+        if (c && r == 0) {
+            const float a = fabsf(c[t]);
+            if (finite(a)) top = fmaxf(top, a);
+        }
+    }
+    int scan = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(~0u, scan, o);
+        if (lane >= o) scan += up;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+    if (lane == 31) warp_sum[warp] = scan;
+    if (lane == 0) warp_max[warp] = top;
+    __syncthreads();
+    int first = scan - mine, n = 0;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        if (w < warp) first += warp_sum[w];
+        n += warp_sum[w];
+    }
+    if (r >= first && r < first + mine) {
+        int at = first, t = t0;
+        while (true) {
+            const int y = target_of(t);
+            if (y >= 0 && at++ == r) {
+                my_token = t;
+                rows[r] = t;
+                label[r] = y;
+                break;
+            }
+            ++t;
+        }
+    }
+    if (r == 0) {
+        for (int i = tid; i < n_counters; i += 128) counters[i] = 0;
+        if (tid == 0) {
+#pragma unroll
+            for (int w = 1; w < 4; ++w) top = fmaxf(top, warp_max[w]);
+            info->count = n;
+            info->finished = 0;
+            info->c_mean = n > 0 ? 1.f / float(n) : 0.f;
+            info->c_max = c ? (top > 0.f ? top : 1.f) : (n > 0 ? info->c_mean : 1.f);
+        }
+    }
+    __syncthreads();
+    if (r < ((n + 63) & ~63))
+        pack_row(r < n ? x + (long long)my_token * ldx : nullptr, D, Dp, plane, wide,
+                 xc + (long long)r * Dp);
+    if (r < T && target_of(r) < 0) {
+        if (tid == 0) {
+            losses[r] = 0.f;
+            lse[r] = 0.f;
+        }
+        if (dx)
+            for (int d = tid; d < D; d += 128) dx[(long long)r * lddx + d] = T_IN(0.f);
     }
 }
 
@@ -964,20 +1052,29 @@ cudaError_t run(const sgemm_ce& a, const DeviceInfo& info, int dev, cudaStream_t
     const float down = a.dtype == SGEMM_FLOAT16 ? 1.f / float(1 << FP16_GRAD_BITS) : 1.f;
 
     // launches
-    if (a.target_bits == 64)
-        e = hg::launch(ce_plan<long long>, 1, PLAN_THREADS, 0, s,
-                       static_cast<const long long*>(a.target), a.token_weights, a.T, a.V, rows,
-                       label, ci, counters, 2 * chunks);
-    else
-        e = hg::launch(ce_plan<int>, 1, PLAN_THREADS, 0, s, static_cast<const int*>(a.target),
-                       a.token_weights, a.T, a.V, rows, label, ci, counters, 2 * chunks);
-    if (e != cudaSuccess) return e;
     const int wide_x = aligned16(a.x) && a.ldx * size % 16 == 0 && a.D % 8 == 0;
     const int wide_w = aligned16(a.weight) && a.ldw * size % 16 == 0 && a.D % 8 == 0;
-    e = hg::launch(ce_gather<T_IN>, round_up(a.T, 64), 128, 0, s, static_cast<const T_IN*>(a.x), a.ldx, a.T, a.D,
-                   Dp, (long long)x_plane, static_cast<const int*>(rows),
-                   static_cast<const CeInfo*>(ci), xc, a.target, int(a.target_bits == 64), a.V,
-                   a.losses, a.lse, static_cast<T_IN*>(a.dx), a.lddx, wide_x);
+    const T_IN* x = static_cast<const T_IN*>(a.x);
+    T_IN* dx = static_cast<T_IN*>(a.dx);
+    const int packed_rows = round_up(a.T, 64), target64 = a.target_bits == 64;
+    if (a.T <= SELECT_TOKENS) {
+        e = hg::launch(ce_select<T_IN>, packed_rows, 128, 0, s, x, a.ldx, a.T, a.D, Dp,
+                       (long long)x_plane, a.target, target64, a.V, a.token_weights, rows, label, ci,
+                       counters, 2 * chunks, xc, a.losses, a.lse, dx, a.lddx, wide_x);
+    } else {
+        if (target64)
+            e = hg::launch(ce_plan<long long>, 1, PLAN_THREADS, 0, s,
+                           static_cast<const long long*>(a.target), a.token_weights, a.T, a.V, rows,
+                           label, ci, counters, 2 * chunks);
+        else
+            e = hg::launch(ce_plan<int>, 1, PLAN_THREADS, 0, s, static_cast<const int*>(a.target),
+                           a.token_weights, a.T, a.V, rows, label, ci, counters, 2 * chunks);
+        if (e != cudaSuccess) return e;
+        e = hg::launch(ce_gather<T_IN>, packed_rows, 128, 0, s, x, a.ldx, a.T, a.D, Dp,
+                       (long long)x_plane, static_cast<const int*>(rows),
+                       static_cast<const CeInfo*>(ci), xc, a.target, target64, a.V, a.losses, a.lse,
+                       dx, a.lddx, wide_x);
+    }
     if (e != cudaSuccess) return e;
     if (!direct) {
         e = hg::launch(ce_weights<T_IN>, a.V, 128, 0, s, static_cast<const T_IN*>(a.weight), a.ldw,
