@@ -32,17 +32,34 @@ constexpr int MAX_NORM_CTAS = 304;      // for one matrix
 constexpr int CONVERT_THREADS = 256;
 constexpr int MAX_STEPS = 64;
 
-__device__ __forceinline__ float load(const float* p) { return *p; }
-__device__ __forceinline__ float load(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-__device__ __forceinline__ float load(const __half* p) { return __half2float(*p); }
+// Eight elements of a row from column c on, zeros from N on. wide: 16-byte aligned rows.
+template <class T_IN>
+__device__ __forceinline__ void load8(const T_IN* p, int c, int N, bool wide, float (&v)[8]) {
+    if (wide && c + 8 <= N) {
+        if constexpr (sizeof(T_IN) == 4) {
+            const float4 a = reinterpret_cast<const float4*>(p)[0];
+            const float4 b = reinterpret_cast<const float4*>(p)[1];
+            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+            v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        } else {
+            const uint4 a = *reinterpret_cast<const uint4*>(p);
+            const T_IN* e = reinterpret_cast<const T_IN*>(&a);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = float(e[j]);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = c + j < N ? float(p[j]) : 0.f;
+    }
+}
 
 // ---- the norm ------------------------------------------------------------------------------
-// Sums of squares of the rows that a CTA takes, one partial sum for each CTA. Eight elements are
-// squared and added in FP32 where that neither overflows nor loses them (their largest between
-// 2^-50 and 2^50, or all zero), else in FP64; a thread's sums are FP64.
+// Sums of squares of what a CTA takes, one partial sum for each CTA. Eight elements are squared and
+// added in FP32, after a power of two where their largest is not between 2^-50 and 2^50; a thread's
+// sums are FP64.
 template <class T_IN>
 __global__ void __launch_bounds__(NORM_THREADS)
-    ns_norm(const T_IN* __restrict__ g, long long ld, long long stride, int M, int N,
+    ns_norm(const T_IN* __restrict__ g, long long ld, long long stride, int M, int N, int wide,
             double* __restrict__ partial, int* counters, int n_counters) {
     __shared__ double sums[NORM_THREADS / 32];
     ptx::griddep_wait();
@@ -56,20 +73,22 @@ __global__ void __launch_bounds__(NORM_THREADS)
     for (long long i = (long long)blockIdx.x * NORM_THREADS + threadIdx.x; i < all;
          i += (long long)gridDim.x * NORM_THREADS) {
         const int row = int(i / groups), c0 = int(i - (long long)row * groups) * 8;
-        const T_IN* p = from + row * ld + c0;
         float v[8], top = 0.f, s = 0.f;
+        load8(from + row * ld + c0, c0, N, wide, v);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            v[j] = c0 + j < N ? load(p + j) : 0.f;
-            top = fmaxf(top, fabsf(v[j]));
-            s = fmaf(v[j], v[j], s);
+        for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(v[j]));
+        float f = 1.f;
+        double back = 1.0;
+        if (top >= 0x1p50f) {
+            f = 0x1p-78f;
+            back = 0x1p156;
+        } else if (top <= 0x1p-50f) {
+            f = 0x1p76f;
+            back = 0x1p-152;
         }
-        if (top == 0.f || (top > 0x1p-50f && top < 0x1p50f)) {
-            sum += double(s);  // NaN where one of them is
-        } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sum += double(v[j]) * double(v[j]);
-        }
+        for (int j = 0; j < 8; ++j) s = fmaf(v[j] * f, v[j] * f, s);
+        sum += double(s) * back;  // NaN where one of them is
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
@@ -81,11 +100,13 @@ __global__ void __launch_bounds__(NORM_THREADS)
     }
 }
 
-// X = G / (norm + eps) in two pieces. Rows of Np elements, zeros behind N.
+// X = G / (norm + eps) in two pieces. Rows of Np elements, zeros behind N. The divisor is taken as a
+// power of two, in two exact factors, times a number of [1, 2), whose reciprocal is rounded once for
+// all elements.
 template <class T_IN>
 __global__ void __launch_bounds__(CONVERT_THREADS)
     ns_convert(const T_IN* __restrict__ g, long long ld, long long stride, int M, int N, int Np,
-               const double* __restrict__ partial, int partials, float eps,
+               int wide, const double* __restrict__ partial, int partials, float eps,
                __half* __restrict__ x) {
     __shared__ double sums[CONVERT_THREADS / 32];
     ptx::griddep_wait();
@@ -100,9 +121,13 @@ __global__ void __launch_bounds__(CONVERT_THREADS)
     sum = 0.0;
     for (int w = 0; w < CONVERT_THREADS / 32; ++w) sum += sums[w];
     const double norm = sqrt(sum) + double(eps);
-    const float by = float(norm);
-    // a norm outside FP32's range is divided by in FP64
-    const bool plain = by > 0x1p-100f && by < 0x1p100f;
+    float f0 = 1.f, f1 = 1.f, f2 = float(1.0 / norm) * UP_X;  // of a norm that is 0, inf or NaN
+    if (norm > 0.0 && norm < 0x1p300) {
+        const int k = ilogb(norm);
+        f0 = float(scalbn(1.0, -(k / 2)));
+        f1 = float(scalbn(1.0, -(k - k / 2)));
+        f2 = float(1.0 / scalbn(norm, -k)) * UP_X;
+    }
     const T_IN* from = g + blockIdx.y * stride;
     const long long plane = (long long)M * Np;
     __half* to = x + blockIdx.y * 2 * plane;
@@ -111,21 +136,18 @@ __global__ void __launch_bounds__(CONVERT_THREADS)
     for (long long i = (long long)blockIdx.x * CONVERT_THREADS + threadIdx.x; i < all;
          i += (long long)gridDim.x * CONVERT_THREADS) {
         const int row = int(i / groups), c0 = int(i - (long long)row * groups) * 8;
-        const T_IN* p = from + row * ld + c0;
-        __half2 high[4], low[4];
+        float v[8];
+        load8(from + row * ld + c0, c0, N, wide, v);
+        __align__(16) __half2 high[4];
+        __align__(16) __half2 low[4];
 #pragma unroll
         for (int j = 0; j < 8; j += 2) {
-            float v[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int c = c0 + j + k;
-                v[k] = c < N ? load(p + j + k) : 0.f;
-                // columns behind N stay zero, whatever the norm is
-                if (c < N) v[k] = (plain ? v[k] / by : float(double(v[k]) / norm)) * UP_X;
-            }
-            high[j / 2] = __floats2half2_rn(v[0], v[1]);
+            // columns behind N stay zero, whatever the norm is
+            const float a = c0 + j < N ? ((v[j] * f0) * f1) * f2 : 0.f;
+            const float b = c0 + j + 1 < N ? ((v[j + 1] * f0) * f1) * f2 : 0.f;
+            high[j / 2] = __floats2half2_rn(a, b);
             const float2 h = __half22float2(high[j / 2]);
-            low[j / 2] = __floats2half2_rn(v[0] - h.x, v[1] - h.y);
+            low[j / 2] = __floats2half2_rn(a - h.x, b - h.y);
         }
         __half* o = to + row * (long long)Np + c0;
         *reinterpret_cast<uint4*>(o) = *reinterpret_cast<const uint4*>(high);
@@ -537,10 +559,12 @@ cudaError_t run(const Call& a, const DeviceInfo& info, int dev, cudaStream_t s) 
         count_launch();
         return cudaLaunchKernelEx(&cfg, kernel, args...);
     };
-    e = launch2(ns_norm<T_IN>, NORM_THREADS, G, a.ldg, a.stride_g, a.M, a.N, partial, counters,
+    const int size = sizeof(T_IN);
+    const int wide = aligned16(G) && a.ldg * size % 16 == 0 && a.stride_g * size % 16 == 0;
+    e = launch2(ns_norm<T_IN>, NORM_THREADS, G, a.ldg, a.stride_g, a.M, a.N, wide, partial, counters,
                 n_counters);
     if (e != cudaSuccess) return e;
-    e = launch2(ns_convert<T_IN>, CONVERT_THREADS, G, a.ldg, a.stride_g, a.M, a.N, Np,
+    e = launch2(ns_convert<T_IN>, CONVERT_THREADS, G, a.ldg, a.stride_g, a.M, a.N, Np, wide,
                 static_cast<const double*>(partial), ctas, a.eps, x[0]);
     if (e != cudaSuccess) return e;
     return tile_columns(a, PIECES, std::max(info.sm_count / 2, 1)) == 128

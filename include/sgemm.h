@@ -525,15 +525,18 @@ SGEMM_API int sgemm_cross_entropy(const sgemm_ce* args, void* stream);
  * must not overlap. coefficients: 3 * steps floats on the HOST, a, b, c of each step.
  *
  * 0 <= count <= 4096 (0 enqueues nothing), 1 <= M, N <= 32768, min(M, N) <= 16384,
- * 1 <= steps <= 64, eps >= 0; ld >= N, and matrices of a stack do not overlap. X is kept in
- * FP32 from step to step. The factors of the products are FP16 times 2^8, one piece (11 bits)
- * for bfloat16 and two (22 bits) for the other types, so entries of X, A and b A + c A A must
- * stay below 2^7 in size: with |G| at most 1 before the first step that holds for coefficients
- * that keep singular values below some 10. A matrix with an infinity or NaN gives NaN; the
- * others of its stack are not touched by it. Sums are FP32. Results are bitwise reproducible,
- * and a matrix's do not depend on the others of its stack.
+ * 1 <= steps <= 64, eps >= 0; ld >= N, and matrices of a stack do not overlap. X is kept in two
+ * FP16 pieces (22 bits) from step to step; the factors of the products are one piece (11 bits)
+ * for bfloat16 and two for the other types; sums are FP32. The pieces are of values times 2^13
+ * (X), 2^12 (A) and 2^10 (the polynomial): entries of X must stay below 8, of A below 16, of
+ * b A + c A A below 64 in size, else the result is NaN. As |X| <= 1 at first, that holds for any
+ * coefficients meant to bring singular values near one. A matrix with an infinity or NaN gives
+ * NaN; the others of its stack are not touched by it. A zero matrix gives zeros (with eps = 0, NaN).
+ * Results are bitwise reproducible, and a matrix's do not depend on the others of its stack (but
+ * on their number, which decides how sums are split).
  *
- * Workspace comes from the library's pool. Everything is stream-ordered; the call can be
+ * Workspace comes from the library's pool: 8 bytes for each element and, with r = min(M, N), 4 (or
+ * 8) times r * r for each matrix. Three launches. Everything is stream-ordered; the call can be
  * captured into a CUDA graph after one call of the same kind outside.
  */
 SGEMM_API int sgemm_orthogonalize(const void* G, int dtype, int count, int M, int N, long long ldg,
