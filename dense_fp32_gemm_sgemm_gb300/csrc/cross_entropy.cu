@@ -341,10 +341,11 @@ struct CeForward {
         int stats_pitch;
         int V;
     };
+    using Io = hg::WarpIo<hg::Ring<CeForward>::BLOCKS>;
     const Params& p;
-    hg::WarpIo& io;
+    Io& io;
     int live;
-    __device__ CeForward(const Params& p_, int live_, hg::WarpIo& io_)
+    __device__ CeForward(const Params& p_, int live_, Io& io_)
         : p(p_), io(io_), live(live_) {}
 
     // `words` words of every lane, 32 at a time, to columns `col` on of `kept`, which a word has
@@ -357,7 +358,7 @@ struct CeForward {
             hg::stage_words<0>(io.block(block), s);
             io.store(block, &p.kept, col, row, 0);
             col += each;
-            block ^= 1;
+            block = Io::of(block + 1);
 #pragma unroll
             for (int j = 0; j + 32 < COLS; ++j) s[j] = s[j + 32];
         }
@@ -654,11 +655,12 @@ struct CeGrad {
         const CeInfo* info;
         float down;  // 2^-FP16_GRAD_BITS or 1
     };
+    using Io = hg::WarpIo<hg::Ring<CeGrad>::BLOCKS>;
     const Params& p;
-    hg::WarpIo& io;
+    Io& io;
     int live;
     float scale;
-    __device__ CeGrad(const Params& p_, int live_, hg::WarpIo& io_)
+    __device__ CeGrad(const Params& p_, int live_, Io& io_)
         : p(p_), io(io_), live(live_) {
         scale = p.info->c_max * p.down;
     }
@@ -740,7 +742,7 @@ struct CeGrad {
                 part<4>(t, o, b, row, at, index, s);
             else
                 part<2>(t, o, b, row, at, index, s);
-            b ^= 1;
+            b = Io::of(b + 1);
 #pragma unroll
             for (int j = 0; j + 32 < COLS; ++j) s[j] = s[j + 32];
         }

@@ -6,9 +6,10 @@
 // added up in one accumulation. A pair of CTAs computes a tile of 256 x BN with
 // tcgen05.mma.cta_group::2; each CTA stages its 128 rows of A and its half of B's columns.
 //
-// Roles in a CTA: warp 0 issues A's TMA loads (and, in the pair's first CTA, hands out units of
-// work), warp 2 B's (a step takes one warp some 450 cycles for both, the MMAs 512), warp 1 of the
-// first CTA issues the MMAs, warps 4-11 run the epilogue.
+// Roles in a CTA: warp 0 issues A's TMA loads, warp 2 B's (a step takes one warp some 450 cycles for
+// both, the MMAs 512); in the pair's first CTA warp 1 issues the MMAs and warp 3 hands out units of
+// work, each shortly before the loads of the one before end (after them that cost 3 us a unit); warps
+// 4-11 run the epilogue.
 //
 // Accumulation. The tensor core cuts off, rather than rounds, the bits that an addition to its
 // FP32 accumulator shifts out: some 2^-25 of the accumulator for each MMA, always towards zero.
@@ -36,9 +37,9 @@ constexpr int BM = 256;       // rows of a tile (both CTAs)
 constexpr int HALF_M = 128;   // rows of one CTA
 constexpr int BK = 64;        // reduction elements in a stage: 128 bytes
 constexpr int MAX_STAGES = 6;
-constexpr int SLOTS = 4;      // units handed out ahead
+constexpr int SLOTS = 2;      // units handed out and not yet taken by all
 constexpr int EPI_WARPS = 8;
-constexpr int EPI_WARP0 = 4;  // warp 3 only fills up the first warpgroup
+constexpr int EPI_WARP0 = 4;
 constexpr int THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
 // Registers: 168 a thread at launch (384 threads); the first warpgroup gives most of its own to
 // the epilogue's, whose threads hold 128 sums. 72 + 216 + 216 = 3 * 168.
@@ -46,8 +47,9 @@ constexpr int REGS_FEW = 72;
 constexpr int REGS_MANY = 216;
 constexpr int A_BYTES = HALF_M * BK * 2;
 constexpr int CHUNK_BYTES = 64 * BK * 2;  // 64 elements of the other index by 64 of k
-constexpr int STAGING = 4096;             // bytes of a staging block, two for an epilogue warp
-constexpr int NUM_BARS = 2 * MAX_STAGES + 4 + 1 + 2 * SLOTS + 2 * EPI_WARPS;
+constexpr int STAGING = 4096;             // bytes of a staging block
+constexpr int NUM_BARS = 2 * MAX_STAGES + 6 + 2 * SLOTS + 2 * EPI_WARPS;
+constexpr int CLAIM_AHEAD = 4;  // blocks of k before a unit's end at which the next one is claimed
 constexpr int MAX_PRODUCTS = 6;
 
 template <int BN>
@@ -56,15 +58,17 @@ constexpr int B_BYTES = BN / 2 * BK * 2;
 // of all PLANES of them, which all products of those k share. A stage of one product and 128 columns
 // takes some 430 cycles to wait for, issue and hand on where its MMAs take 256, and its 24 KiB 384 to
 // arrive; with two planes three products share 48 KiB, a wait and a commit. (Of 256 columns the MMAs
-// take 512, and three stages of 64 KiB would leave the epilogue too little.)
+// take 512, and three stages of 64 KiB would look ahead no further.)
 template <class EPI>
 struct Ring {
     static constexpr int BN = EPI::BN, PLANES = EPI::PLANES;
     static constexpr int B_AT = PLANES * A_BYTES;  // of B in a stage
     static constexpr int STAGE_BYTES = PLANES * (A_BYTES + B_BYTES<BN>);
-    static constexpr int STAGES = BN == 256 ? 5 : PLANES == 1 ? 6 : 3;
+    static constexpr int STAGES = PLANES == 1 ? 6 : 3;
+    // staging blocks of an epilogue warp
+    static constexpr int BLOCKS = BN == 256 ? 1 : 2;
     static constexpr int SMEM_BYTES =
-        STAGES * STAGE_BYTES + 2 * EPI_WARPS * STAGING + 512 + 1024;
+        STAGES * STAGE_BYTES + BLOCKS * EPI_WARPS * STAGING + 512 + 1024;
     static_assert(SMEM_BYTES <= 232448, "shared memory of an SM");
     static_assert(STAGES <= MAX_STAGES && (PLANES == 1 || (PLANES == 2 && BN == 128)), "see above");
 };
@@ -224,7 +228,8 @@ struct Smem {
     __device__ uint32_t slot_full(int i) const { return at(2 * MAX_STAGES + 4 + i); }
     __device__ uint32_t slot_empty(int i) const { return at(2 * MAX_STAGES + 4 + SLOTS + i); }
     __device__ uint32_t drain() const { return at(2 * MAX_STAGES + 4 + 2 * SLOTS); }
-    __device__ uint32_t loaded(int i) const { return at(2 * MAX_STAGES + 5 + 2 * SLOTS + i); }
+    __device__ uint32_t claim() const { return at(2 * MAX_STAGES + 5 + 2 * SLOTS); }
+    __device__ uint32_t loaded(int i) const { return at(2 * MAX_STAGES + 6 + 2 * SLOTS + i); }
 };
 
 template <class R>
@@ -234,7 +239,7 @@ __device__ __forceinline__ Smem carve(uint8_t* raw) {
     Smem s;
     s.ring = ptx::smem_u32(base);
     s.staging = base + R::STAGES * R::STAGE_BYTES;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(s.staging + 2 * EPI_WARPS * STAGING);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(s.staging + R::BLOCKS * EPI_WARPS * STAGING);
     s.bar0 = ptx::smem_u32(bars);
     int* words = reinterpret_cast<int*>(bars + NUM_BARS);
     s.slots = ptx::smem_u32(words);
@@ -271,11 +276,14 @@ __device__ __forceinline__ uint4* staged(uint8_t* block, int row, int piece) {
     return reinterpret_cast<uint4*>(block + row * 128 + ((piece ^ (row & 7)) << 4));
 }
 
-// An epilogue warp's two staging blocks and its TMA traffic through them, which its first lane
-// issues. A block is written again once the store that last used it has read it.
+// An epilogue warp's staging blocks (one or two) and its TMA traffic through them, which its first
+// lane issues. A block is written again once the store that last used it has read it.
+template <int BLOCKS>
 struct WarpIo {
     uint8_t* blocks;
     uint32_t bar;  // of block 0's loads; block 1's is 8 bytes on
+    // the block of the n-th use
+    static __device__ __forceinline__ int of(int n) { return n & (BLOCKS - 1); }
     volatile int* abort_flag;
     int* err;
     uint32_t parity = 0;  // bit i: of block i's next load
@@ -284,7 +292,7 @@ struct WarpIo {
     __device__ __forceinline__ uint8_t* block(int i) const { return blocks + i * STAGING; }
     __device__ __forceinline__ void acquire(int i) {
         if (first) {
-            if (last == i)
+            if (BLOCKS == 1 || last == i)
                 ptx::bulk_wait_read0();
             else
                 ptx::bulk_wait_read<1>();
@@ -440,10 +448,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
         for (int i = 0; i < SLOTS; ++i) {
             ptx::mbar_init(sm.slot_full(i), 1);
-            // the first CTA's MMA warp, the TMA warps but the one that hands out, all epilogue warps
-            ptx::mbar_init(sm.slot_empty(i), 4 + 2 * EPI_WARPS);
+            // the first CTA's MMA warp, the TMA and the epilogue warps of both
+            ptx::mbar_init(sm.slot_empty(i), 5 + 2 * EPI_WARPS);
         }
         ptx::mbar_init(sm.drain(), 1);
+        ptx::mbar_init(sm.claim(), 1);
         for (int i = 0; i < 2 * EPI_WARPS; ++i) ptx::mbar_init(sm.loaded(i), 1);
         *sm.abort_flag = 0;
         ptx::fence_mbar_init();
@@ -469,8 +478,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const Units n_units = Units::of<BN, CHAIN>(g, live);
     // chain: what the phase before this unit's computes of its product has been stored, for TMA to
     // read
+    int ready_phase = 0, ready_batch = -1;  // that this warp has found complete
     auto wait_before = [&](const Unit& t) {
-        if (t.phase == 0) return true;
+        if (t.phase == 0 || (t.phase == ready_phase && t.batch == ready_batch)) return true;
         const int type = (t.phase - 1) % 3, batch = g.p[0].batch;
         const int units =
             type == 0 ? n_units.first : type == 1 ? n_units.second : n_units.third;
@@ -480,6 +490,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                             sm.abort_flag, g.err);
         ok = __all_sync(~0u, ok) != 0;
         ptx::fence_proxy_async_global();
+        ready_phase = t.phase;
+        ready_batch = t.batch;
         return ok;
     };
     // the unit in slot i, or -1 at the end or when a wait ran out
@@ -504,46 +516,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         if (warp == 0 || warp == 2) {
             // all lanes go through the loop with equal values, one of them issues
             const bool is_a = warp == 0;
-            const bool hands_out = is_a && rank == 0;
-            const int units = n_units.all;
             const uint32_t full0 = sm.full(0), empty0 = sm.empty(0);
             const uint32_t signal0 = ptx::mapa_shared(full0, 0);  // the first CTA's barriers
             const bool expects = is_a && rank == 0;
             const uint32_t ring = sm.ring + (is_a ? 0 : R::B_AT);
             const uint32_t plane_bytes = is_a ? A_BYTES : B_BYTES<BN>;
-            // the first units are given out by the pairs' numbers, in a chain claimed like all
-            // others: a pair may not be running yet
-            const int pairs = CHAIN ? 0 : gridDim.x >> 1;
-            int next = blockIdx.x >> 1;
-            if (CHAIN && hands_out) {
-                if (lane == 0) next = atomicAdd(g.counter, 1);
-                next = __shfl_sync(~0u, next, 0);
-            }
+            const bool tells = is_a && rank == 0 && lane == 0;  // when to claim the next unit
             int s = 0;
             uint32_t ph = 0;
-            for (int i = 0;; ++i) {
-                int u;
-                if (hands_out) {
-                    u = next < units ? next : -1;
-                    const int slot = i % SLOTS;
-                    if (!wait_all(sm.slot_empty(slot), ((i / SLOTS) & 1) ^ 1)) u = -1;
-                    int claimed = 0;
-                    if (lane == 0) {
-                        sm.slot_ptr[slot] = u;
-                        ptx::st_shared_cluster_f32(ptx::mapa_shared(sm.slots + 4u * slot, 1),
-                                                   __int_as_float(u));
-                        ptx::mbar_arrive_cluster(ptx::mapa_shared(sm.slot_full(slot), 0));
-                        ptx::mbar_arrive_cluster(ptx::mapa_shared(sm.slot_full(slot), 1));
-                        if (u >= 0) claimed = atomicAdd(g.counter, 1);
-                    }
-                    next = pairs + claimed;  // lane 0's is passed on when it is needed
-                } else {
-                    u = take(i);
-                    __syncwarp();
-                    if (u >= 0 && lane == 0) taken(i);
-                }
+            bool ok = true;
+            for (int i = 0; ok; ++i) {
+                const int u = take(i);
+                __syncwarp();
                 if (u < 0) break;
+                if (lane == 0) taken(i);
                 const Unit t = unit_at<BN, CHAIN>(g, n_units, u, live);
+                const int claim_kb = max(t.kb0, t.kb1 - CLAIM_AHEAD);
+                if (tells && t.kb0 >= t.kb1) ptx::mbar_arrive(sm.claim());
                 const Problem& p = g.p[t.problem];
                 const CUtensorMap* map = is_a ? &g.a[t.problem] : &g.b[t.problem];
                 const bool mn = is_a ? p.a_mn : p.b_mn;
@@ -558,8 +547,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 int x = mn ? o : k0, y = first + (mn ? k0 : o);
                 const int dx = mn ? 0 : BK, dy = mn ? BK : 0;
                 const bool two = mn && (is_a || BN == 256);
-                bool ok = !CHAIN || wait_before(t);
+                ok = !CHAIN || wait_before(t);
                 for (int kb = t.kb0; ok && kb < t.kb1; ++kb) {
+                    if (tells && kb == claim_kb) ptx::mbar_arrive(sm.claim());
                     unsigned planes_left = order;
                     const int stages = R::PLANES == 1 ? products : 1;
                     for (int q = 0; q < stages; ++q) {
@@ -588,15 +578,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                     x += dx;
                     y += dy;
                 }
-                next = __shfl_sync(~0u, next, 0);
-                if (!ok) {
-                    if (!hands_out) break;
-                    next = units;  // the others are told that there is nothing more
-                }
             }
             if (*sm.abort_flag) {  // copies in flight arrive before shared memory is given up
                 const unsigned long long t0 = ptx::globaltimer_ns();
                 while (ptx::globaltimer_ns() - t0 < 10000000ull) {
+                }
+            }
+        } else if (warp == 3 && rank == 0) {
+            // the first units are given out by the pairs' numbers, in a chain claimed like all
+            // others: a pair may not be running yet
+            const int pairs = CHAIN ? 0 : gridDim.x >> 1;
+            if (lane == 0) {
+                int next = CHAIN ? atomicAdd(g.counter, 1) : blockIdx.x >> 1;
+                for (int i = 0;; ++i) {
+                    const int slot = i % SLOTS;
+                    int u = next < n_units.all ? next : -1;
+                    if (!wait(sm.slot_empty(slot), ((i / SLOTS) & 1) ^ 1, sm, g.err)) u = -1;
+                    sm.slot_ptr[slot] = u;
+                    ptx::st_shared_cluster_f32(ptx::mapa_shared(sm.slots + 4u * slot, 1),
+                                               __int_as_float(u));
+                    ptx::mbar_arrive_cluster(ptx::mapa_shared(sm.slot_full(slot), 0));
+                    ptx::mbar_arrive_cluster(ptx::mapa_shared(sm.slot_full(slot), 1));
+                    if (u < 0) break;
+                    // not before the unit is nearly done: another pair may be free earlier
+                    if (!wait(sm.claim(), i & 1, sm, g.err)) next = n_units.all;
+                    else next = pairs + atomicAdd(g.counter, 1);
                 }
             }
         } else if (warp == 1 && rank == 0) {
@@ -671,8 +677,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         ptx::regs_take<REGS_MANY>();
         // warp w reads TMEM lanes [32 (w % 4), +32) and the first or second half of the columns
         const int q = warp & 3, h = (warp - EPI_WARP0) >> 2;
-        WarpIo io;
-        io.blocks = sm.staging + 2 * (warp - EPI_WARP0) * STAGING;
+        WarpIo<R::BLOCKS> io;
+        io.blocks = sm.staging + R::BLOCKS * (warp - EPI_WARP0) * STAGING;
         io.bar = sm.loaded(2 * (warp - EPI_WARP0));
         io.abort_flag = sm.abort_flag;
         io.err = g.err;

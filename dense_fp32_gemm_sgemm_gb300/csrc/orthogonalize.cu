@@ -190,9 +190,11 @@ struct NsChain {
         int steps;
         float coefficients[3 * MAX_STEPS];
     };
+    using Io = hg::WarpIo<hg::Ring<NsChain>::BLOCKS>;
+    static constexpr int AHEAD = hg::Ring<NsChain>::BLOCKS;  // blocks loaded ahead
     const Params& p;
-    hg::WarpIo& io;
-    __device__ NsChain(const Params& p_, int, hg::WarpIo& io_) : p(p_), io(io_) {}
+    Io& io;
+    __device__ NsChain(const Params& p_, int, Io& io_) : p(p_), io(io_) {}
 
     // The matrix of the second term.
     struct Second {
@@ -203,11 +205,11 @@ struct NsChain {
         if (type == 1) return {&p.gram.straight, PIECES, t.batch * PIECES, p.r, p.r};
         return {&p.x[t.problem == 5].straight, 2, t.batch * 2, p.M, p.N};
     }
-    // Block n of the second term: 64 columns, piece by piece; into staging block n % 2.
+    // Block n of the second term: 64 columns, piece by piece.
     __device__ __forceinline__ void load(const Second& m, int n, int row, int col) {
         const int c = m.pieces == 2 ? n >> 1 : n;
         if (c * 64 < COLS && col + c * 64 < m.cols)
-            io.load(n & 1, m.map, col + c * 64, row, m.slab + (m.pieces == 2 ? n & 1 : 0));
+            io.load(Io::of(n), m.map, col + c * 64, row, m.slab + (m.pieces == 2 ? n & 1 : 0));
     }
     __device__ __forceinline__ bool reads(const hg::Unit& t) const { return t.phase % 3 != 0; }
     __device__ __forceinline__ void start(const hg::Unit& t, int row, int col) {
@@ -216,7 +218,7 @@ struct NsChain {
         const Second m = second(t, type);
         if (row >= m.rows) return;
         load(m, 0, row, col);
-        load(m, 1, row, col);
+        if (AHEAD > 1) load(m, 1, row, col);
     }
 
     // The next 64 columns to the front.
@@ -269,8 +271,8 @@ struct NsChain {
             for (int at = 0; at < COLS; at += 64) {
 #pragma unroll 1
                 for (int k = 0; k < m.pieces && col + at < cols_n; ++k, ++n) {
-                    io.wait_load(n & 1);
-                    uint8_t* block = io.block(n & 1);
+                    io.wait_load(Io::of(n));
+                    uint8_t* block = io.block(Io::of(n));
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         const uint4 v = *hg::staged(block, lane, j);
@@ -284,7 +286,7 @@ struct NsChain {
                         }
                     }
                     __syncwarp();  // read by all lanes
-                    load(m, n + 2, row, col);
+                    load(m, n + AHEAD, row, col);
                 }
                 turn(s);
             }
@@ -326,7 +328,7 @@ struct NsChain {
                         make_uint4(__float_as_uint(s[8 * j]), __float_as_uint(s[8 * j + 2]),
                                    __float_as_uint(s[8 * j + 4]), __float_as_uint(s[8 * j + 6]));
                 io.store(block, &to.straight, at, row, slab + k);
-                block ^= 1;
+                block = Io::of(block + 1);
                 if (mirror) {
                     // turned over: 64 rows of 32 values, 64 bytes each
                     io.acquire(block);
@@ -339,7 +341,7 @@ struct NsChain {
                         turned[j * 32 + 32] = (unsigned short)(w >> 16);
                     }
                     io.store(block, &to.turned, row, at, slab + k);
-                    block ^= 1;
+                    block = Io::of(block + 1);
                 }
 #pragma unroll
                 for (int j = 0; j < 64; j += 2) s[j] = s[j + 1];
@@ -366,7 +368,7 @@ struct NsChain {
                 store_result<4>(t, block, row, at, s);
             else
                 store_result<2>(t, block, row, at, s);
-            block ^= 1;
+            block = Io::of(block + 1);
 #pragma unroll
             for (int j = 0; j + 32 < COLS; ++j) s[j] = s[j + 32];
         }
