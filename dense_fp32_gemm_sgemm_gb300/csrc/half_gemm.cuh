@@ -8,7 +8,7 @@
 //
 // Roles in a CTA: warp 0 issues A's TMA loads, warp 2 B's (a step takes one warp some 450 cycles for
 // both, the MMAs 512); in the pair's first CTA warp 1 issues the MMAs and warp 3 hands out units of
-// work, each shortly before the loads of the one before end (after them that cost 3 us a unit); warps
+// work, each when the loads of the one before begin (when they ended that cost 3 us a unit); warps
 // 4-11 run the epilogue.
 //
 // Accumulation. The tensor core cuts off, rather than rounds, the bits that an addition to its
@@ -37,7 +37,7 @@ constexpr int BM = 256;       // rows of a tile (both CTAs)
 constexpr int HALF_M = 128;   // rows of one CTA
 constexpr int BK = 64;        // reduction elements in a stage: 128 bytes
 constexpr int MAX_STAGES = 6;
-constexpr int SLOTS = 2;      // units handed out and not yet taken by all
+constexpr int SLOTS = 4;      // units handed out and not yet taken by all
 constexpr int EPI_WARPS = 8;
 constexpr int EPI_WARP0 = 4;
 constexpr int THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
@@ -49,7 +49,6 @@ constexpr int A_BYTES = HALF_M * BK * 2;
 constexpr int CHUNK_BYTES = 64 * BK * 2;  // 64 elements of the other index by 64 of k
 constexpr int STAGING = 4096;             // bytes of a staging block
 constexpr int NUM_BARS = 2 * MAX_STAGES + 6 + 2 * SLOTS + 2 * EPI_WARPS;
-constexpr int CLAIM_AHEAD = 4;  // blocks of k before a unit's end at which the next one is claimed
 constexpr int MAX_PRODUCTS = 6;
 
 template <int BN>
@@ -521,7 +520,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             const bool expects = is_a && rank == 0;
             const uint32_t ring = sm.ring + (is_a ? 0 : R::B_AT);
             const uint32_t plane_bytes = is_a ? A_BYTES : B_BYTES<BN>;
-            const bool tells = is_a && rank == 0 && lane == 0;  // when to claim the next unit
+            const bool tells = is_a && rank == 0 && lane == 0;  // that the next unit may be claimed
             int s = 0;
             uint32_t ph = 0;
             bool ok = true;
@@ -530,9 +529,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 __syncwarp();
                 if (u < 0) break;
                 if (lane == 0) taken(i);
+                if (tells) ptx::mbar_arrive(sm.claim());
                 const Unit t = unit_at<BN, CHAIN>(g, n_units, u, live);
-                const int claim_kb = max(t.kb0, t.kb1 - CLAIM_AHEAD);
-                if (tells && t.kb0 >= t.kb1) ptx::mbar_arrive(sm.claim());
                 const Problem& p = g.p[t.problem];
                 const CUtensorMap* map = is_a ? &g.a[t.problem] : &g.b[t.problem];
                 const bool mn = is_a ? p.a_mn : p.b_mn;
@@ -549,7 +547,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 const bool two = mn && (is_a || BN == 256);
                 ok = !CHAIN || wait_before(t);
                 for (int kb = t.kb0; ok && kb < t.kb1; ++kb) {
-                    if (tells && kb == claim_kb) ptx::mbar_arrive(sm.claim());
                     unsigned planes_left = order;
                     const int stages = R::PLANES == 1 ? products : 1;
                     for (int q = 0; q < stages; ++q) {
@@ -600,9 +597,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                     ptx::mbar_arrive_cluster(ptx::mapa_shared(sm.slot_full(slot), 0));
                     ptx::mbar_arrive_cluster(ptx::mapa_shared(sm.slot_full(slot), 1));
                     if (u < 0) break;
-                    // not before the unit is nearly done: another pair may be free earlier
-                    if (!wait(sm.claim(), i & 1, sm, g.err)) next = n_units.all;
-                    else next = pairs + atomicAdd(g.counter, 1);
+                    // when the unit's loads begin; earlier, other pairs would run out of units
+                    const bool go = wait(sm.claim(), i & 1, sm, g.err);
+                    next = go ? pairs + atomicAdd(g.counter, 1) : n_units.all;
                 }
             }
         } else if (warp == 1 && rank == 0) {
