@@ -421,10 +421,10 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 //   void unit(const Unit&, int row, int col, float (&acc)[BN / 2])
 // called by each epilogue warp at the beginning of a unit (to load what it will need) and with its
 // sums: lane l holds row `row` + l, columns col .. col + BN / 2.
-// EPI::PROBLEMS: of the launch at most. EPI::PLANES: staged together (see Ring). EPI::CHAIN: units are done in order, and one of a phase
-// waits until all of the phase before that belong to the same product have been stored. Every earlier unit was claimed by a CTA
-// that runs, and waits for still earlier ones only, so that all waits end however many CTAs the
-// GPU runs at a time.
+// EPI::PROBLEMS: of the launch at most. EPI::PLANES: staged together (see Ring). EPI::CHAIN: units
+// are claimed in order, and one waits until all units of the phase before that belong to the same
+// product have been stored. Every earlier unit was claimed by a CTA that runs, and waits for still
+// earlier ones only, so that all waits end however many CTAs the GPU runs at a time.
 template <class EPI>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     half_gemm_kernel(const __grid_constant__ Args<EPI::PROBLEMS> g,
@@ -737,7 +737,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 if (lane == 0) {
                     ptx::bulk_wait0();  // its stores are in global memory
                     ptx::fence_proxy_async_global();
-                    __threadfence();
                     ptx::red_release_gpu_add(g.done + t.phase * g.p[0].batch + t.batch, 1);
                 }
             }
@@ -788,11 +787,27 @@ cudaError_t launch(void (*kernel)(KArgs...), unsigned grid, unsigned block, size
 // Box rows of an operand: 64 k of a chunk, or its rows in a CTA.
 inline int box_rows(bool mn, int rows_of_cta) { return mn ? BK : rows_of_cta; }
 
+// Raises the kernel's shared-memory limit, once per device, and makes sure that its threads start
+// with the registers that its warpgroups share out among themselves: with fewer, the second of them
+// would wait for registers that nobody gives up.
+template <class EPI>
+cudaError_t prepare_gemm() {
+    const cudaError_t e = set_smem_limit_once<half_gemm_kernel<EPI>>(Ring<EPI>::SMEM_BYTES);
+    if (e != cudaSuccess) return e;
+    static const cudaError_t enough = [] {
+        cudaFuncAttributes attr;
+        const cudaError_t f = cudaFuncGetAttributes(&attr, half_gemm_kernel<EPI>);
+        if (f != cudaSuccess) return f;
+        return 3 * attr.numRegs < REGS_FEW + 2 * REGS_MANY ? cudaErrorLaunchOutOfResources
+                                                           : cudaSuccess;
+    }();
+    return enough;
+}
+
 template <class EPI>
 cudaError_t launch_gemm(const Args<EPI::PROBLEMS>& g, const typename EPI::Params& ep, int sm_count,
                         cudaStream_t stream) {
-    constexpr int bytes = Ring<EPI>::SMEM_BYTES;
-    cudaError_t e = set_smem_limit_once<half_gemm_kernel<EPI>>(bytes);
+    const cudaError_t e = prepare_gemm<EPI>();
     if (e != cudaSuccess) return e;
     // pairs for all units, in a chain for those of its largest phase
     int units = 0;
@@ -803,7 +818,7 @@ cudaError_t launch_gemm(const Args<EPI::PROBLEMS>& g, const typename EPI::Params
     if (units == 0) return cudaSuccess;
     const int pairs = sm_count / 2 > 0 ? sm_count / 2 : 1;
     return launch(half_gemm_kernel<EPI>, 2u * unsigned(units < pairs ? units : pairs), THREADS,
-                  bytes, stream, g, ep);
+                  Ring<EPI>::SMEM_BYTES, stream, g, ep);
 }
 
 }  // namespace hg
