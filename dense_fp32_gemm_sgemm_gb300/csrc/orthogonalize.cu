@@ -28,8 +28,7 @@ namespace {
 
 constexpr float UP_X = 0x1p13f, UP_A = 0x1p12f, UP_P = 0x1p10f;  // scales of the pieces
 constexpr int NORM_THREADS = 256;
-constexpr int MAX_NORM_CTAS = 304;      // for one matrix
-constexpr int CONVERT_THREADS = 256;
+constexpr int MAX_NORM_CTAS = 1216;     // for one matrix: eight an SM
 constexpr int MAX_STEPS = 64;
 
 // Eight elements of a row from column c on, zeros from N on. wide: 16-byte aligned rows.
@@ -53,89 +52,88 @@ __device__ __forceinline__ void load8(const T_IN* p, int c, int N, bool wide, fl
     }
 }
 
-// ---- the norm ------------------------------------------------------------------------------
-// Sums of squares of what a CTA takes, one partial sum for each CTA. Eight elements are squared and
-// added in FP32, after a power of two where their largest is not between 2^-50 and 2^50; a thread's
-// sums are FP64.
-template <class T_IN>
-__global__ void __launch_bounds__(NORM_THREADS)
-    ns_norm(const T_IN* __restrict__ g, long long ld, long long stride, int M, int N, int wide,
-            double* __restrict__ partial, int* counters, int n_counters) {
-    __shared__ double sums[NORM_THREADS / 32];
-    ptx::griddep_wait();
-    ptx::griddep_launch_dependents();
-    if (blockIdx.x == 0 && blockIdx.y == 0)
-        for (int i = threadIdx.x; i < n_counters; i += NORM_THREADS) counters[i] = 0;
-    const T_IN* from = g + blockIdx.y * stride;
-    const int groups = (N + 7) / 8;
-    const long long all = (long long)M * groups;
-    double sum = 0.0;
-    for (long long i = (long long)blockIdx.x * NORM_THREADS + threadIdx.x; i < all;
-         i += (long long)gridDim.x * NORM_THREADS) {
-        const int row = int(i / groups), c0 = int(i - (long long)row * groups) * 8;
-        float v[8], top = 0.f, s = 0.f;
+// ---- the norm and the first X --------------------------------------------------------------
+// FP32 sum with what its additions rounded off.
+struct Compensated {
+    float sum = 0.f, rest = 0.f;
+    __device__ __forceinline__ void add(float s) {
+        const float t = sum + s, u = t - sum;
+        rest += (sum - (t - u)) + (s - u);
+        sum = t;
+    }
+    // of all lanes' sums, in the first lane
+    __device__ __forceinline__ double of_warp() {
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            const float other = __shfl_down_sync(~0u, sum, o);
+            rest += __shfl_down_sync(~0u, rest, o);
+            add(other);
+        }
+        return (threadIdx.x & 31) == 0 ? double(sum) + double(rest) : 0.0;
+    }
+};
+
+// The sum of a CTA's squares over groups of eight elements i0, i0 + step, ... of a matrix, in its
+// first thread. Groups are squared and added in FP32, those whose largest element is not between
+// 2^-50 and 2^50 after a power of two and for themselves; a warp's sums are compensated, and joined in
+// FP64, of which an SM does two operations a clock.
+template <int THREADS, class T_IN>
+__device__ __forceinline__ double sum_squares(const T_IN* from, long long ld, int M, int N, bool wide,
+                                              unsigned i0, unsigned step) {
+    __shared__ double sums[THREADS / 32];
+    const unsigned groups = (N + 7) / 8, all = M * groups;  // at most 2^27
+    Compensated small, middle, large;
+    for (unsigned i = i0; i < all; i += step) {
+        const unsigned row = i / groups;
+        const int c0 = int(i - row * groups) * 8;
+        float v[8], top = 0.f;
         load8(from + row * ld + c0, c0, N, wide, v);
 #pragma unroll
         for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(v[j]));
-        float f = 1.f;
-        double back = 1.0;
-        if (top >= 0x1p50f) {
-            f = 0x1p-78f;
-            back = 0x1p156;
-        } else if (top <= 0x1p-50f) {
-            f = 0x1p76f;
-            back = 0x1p-152;
-        }
+        auto squares = [&](float f) {
+            float s = 0.f;  // NaN where one of them is
 #pragma unroll
-        for (int j = 0; j < 8; ++j) s = fmaf(v[j] * f, v[j] * f, s);
-        sum += double(s) * back;  // NaN where one of them is
+            for (int j = 0; j < 8; ++j) s = fmaf(v[j] * f, v[j] * f, s);
+            return s;
+        };
+        if (top >= 0x1p50f)
+            large.add(squares(0x1p-78f));
+        else if (top <= 0x1p-50f)
+            small.add(squares(0x1p76f));
+        else
+            middle.add(squares(1.f));
     }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+    double sum = middle.of_warp();
+    if (__any_sync(~0u, small.sum != 0.f || large.sum != 0.f))
+        sum += small.of_warp() * 0x1p-152 + large.of_warp() * 0x1p156;
     if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = sum;
     __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int w = 1; w < NORM_THREADS / 32; ++w) sum += sums[w];
-        partial[(long long)blockIdx.y * gridDim.x + blockIdx.x] = sum;
-    }
+    if (threadIdx.x == 0)
+        for (int w = 1; w < THREADS / 32; ++w) sum += sums[w];
+    return sum;
 }
 
-// X = G / (norm + eps) in two pieces. Rows of Np elements, zeros behind N. The divisor is taken as a
-// power of two, in two exact factors, times a number of [1, 2), whose reciprocal is rounded once for
-// all elements.
-template <class T_IN>
-__global__ void __launch_bounds__(CONVERT_THREADS)
-    ns_convert(const T_IN* __restrict__ g, long long ld, long long stride, int M, int N, int Np,
-               int wide, const double* __restrict__ partial, int partials, float eps,
-               __half* __restrict__ x) {
-    __shared__ double sums[CONVERT_THREADS / 32];
-    ptx::griddep_wait();
-    ptx::griddep_launch_dependents();
-    double sum = 0.0;
-    const double* mine = partial + (long long)blockIdx.y * partials;
-    for (int i = threadIdx.x; i < partials; i += CONVERT_THREADS) sum += mine[i];
-#pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-    if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = sum;
-    __syncthreads();
-    sum = 0.0;
-    for (int w = 0; w < CONVERT_THREADS / 32; ++w) sum += sums[w];
+// 1 / (sqrt(sum) + eps) as a power of two, in two exact factors, times a number of (1/2, 1], rounded
+// once for all elements. For one thread: FP64 arithmetic of a whole CTA takes microseconds.
+__device__ __forceinline__ float4 divisor(double sum, float eps) {
     const double norm = sqrt(sum) + double(eps);
-    float f0 = 1.f, f1 = 1.f, f2 = float(1.0 / norm) * UP_X;  // of a norm that is 0, inf or NaN
-    if (norm > 0.0 && norm < 0x1p300) {
-        const int k = ilogb(norm);
-        f0 = float(scalbn(1.0, -(k / 2)));
-        f1 = float(scalbn(1.0, -(k - k / 2)));
-        f2 = float(1.0 / scalbn(norm, -k)) * UP_X;
-    }
-    const T_IN* from = g + blockIdx.y * stride;
+    if (!(norm > 0.0 && norm < 0x1p300))  // 0, infinity or NaN
+        return make_float4(1.f, 1.f, float(1.0 / norm) * UP_X, 0.f);
+    const int k = ilogb(norm);
+    return make_float4(float(scalbn(1.0, -(k / 2))), float(scalbn(1.0, -(k - k / 2))),
+                       float(1.0 / scalbn(norm, -k)) * UP_X, 0.f);
+}
+
+// X = G / norm in two pieces, the same groups. Rows of Np elements, zeros behind N.
+template <class T_IN>
+__device__ __forceinline__ void first_x(const T_IN* from, long long ld, int M, int N, int Np, bool wide,
+                                        float4 by, __half* to, unsigned i0, unsigned step) {
+    const float f0 = by.x, f1 = by.y, f2 = by.z;
     const long long plane = (long long)M * Np;
-    __half* to = x + blockIdx.y * 2 * plane;
-    const int groups = Np / 8;
-    const long long all = (long long)M * groups;
-    for (long long i = (long long)blockIdx.x * CONVERT_THREADS + threadIdx.x; i < all;
-         i += (long long)gridDim.x * CONVERT_THREADS) {
-        const int row = int(i / groups), c0 = int(i - (long long)row * groups) * 8;
+    const unsigned groups = Np / 8, all = M * groups;
+    for (unsigned i = i0; i < all; i += step) {
+        const unsigned row = i / groups;
+        const int c0 = int(i - row * groups) * 8;
         float v[8];
         load8(from + row * ld + c0, c0, N, wide, v);
         __align__(16) __half2 high[4];
@@ -153,6 +151,45 @@ __global__ void __launch_bounds__(CONVERT_THREADS)
         *reinterpret_cast<uint4*>(o) = *reinterpret_cast<const uint4*>(high);
         *reinterpret_cast<uint4*>(o + plane) = *reinterpret_cast<const uint4*>(low);
     }
+}
+
+// Partial sums of squares, one for each CTA of a matrix (grid row).
+template <class T_IN>
+__global__ void __launch_bounds__(NORM_THREADS)
+    ns_norm(const T_IN* __restrict__ g, long long ld, long long stride, int M, int N, int wide,
+            double* __restrict__ partial, int* counters, int n_counters) {
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    const int cta = blockIdx.y * gridDim.x + blockIdx.x;
+    for (int i = cta * NORM_THREADS + threadIdx.x; i < n_counters;
+         i += gridDim.x * gridDim.y * NORM_THREADS)
+        counters[i] = 0;
+    const double sum = sum_squares<NORM_THREADS>(
+        g + blockIdx.y * stride, ld, M, N, wide,
+        blockIdx.x * NORM_THREADS + threadIdx.x, gridDim.x * NORM_THREADS);
+    if (threadIdx.x == 0) partial[cta] = sum;
+}
+
+template <class T_IN>
+__global__ void __launch_bounds__(NORM_THREADS)
+    ns_convert(const T_IN* __restrict__ g, long long ld, long long stride, int M, int N, int Np,
+               int wide, const double* __restrict__ partial, int partials, float eps,
+               __half* __restrict__ x) {
+    __shared__ float4 by;
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    if (threadIdx.x < 32) {
+        double sum = 0.0;
+        const double* mine = partial + (long long)blockIdx.y * partials;
+        for (int i = threadIdx.x; i < partials; i += 32) sum += mine[i];
+#pragma unroll
+        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+        if (threadIdx.x == 0) by = divisor(sum, eps);
+    }
+    __syncthreads();
+    first_x(g + blockIdx.y * stride, ld, M, N, Np, wide, by,
+            x + blockIdx.y * 2 * ((long long)M * Np),
+            blockIdx.x * NORM_THREADS + threadIdx.x, gridDim.x * NORM_THREADS);
 }
 
 // ---- the epilogue -------------------------------------------------------------------------------
@@ -525,7 +562,7 @@ cudaError_t run(const Call& a, const DeviceInfo& info, int dev, cudaStream_t s) 
     const int Np = (a.N + 63) / 64 * 64, rp = (r + 63) / 64 * 64;
     const size_t x_plane = size_t(a.M) * Np, r_plane = size_t(r) * rp;
     const long long groups = (long long)a.M * ((a.N + 7) / 8);
-    const int most = std::max(1, std::min(MAX_NORM_CTAS, 2048 / a.count + 1));
+    const int most = std::max(1, std::min(MAX_NORM_CTAS, 4096 / a.count + 1));
     const int ctas = int(std::min<long long>(most, (groups + NORM_THREADS - 1) / NORM_THREADS));
     Layout lay;
     const int n_counters = 1 + 3 * a.steps * a.count;
@@ -546,12 +583,13 @@ cudaError_t run(const Call& a, const DeviceInfo& info, int dev, cudaStream_t s) 
     __half* gram = reinterpret_cast<__half*>(base + at_gram);
     __half* poly = reinterpret_cast<__half*>(base + at_poly);
     const T_IN* G = static_cast<const T_IN*>(a.G);
-    const dim3 grid(ctas, a.count);
+    const int size = sizeof(T_IN);
+    const int wide = aligned16(G) && a.ldg * size % 16 == 0 && a.stride_g * size % 16 == 0;
     // both kernels have one grid row for each matrix
-    auto launch2 = [&](auto kernel, unsigned threads, auto... args) {
+    auto launch2 = [&](auto kernel, auto... args) {
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = grid;
-        cfg.blockDim = dim3(threads);
+        cfg.gridDim = dim3(ctas, a.count);
+        cfg.blockDim = dim3(NORM_THREADS);
         cfg.stream = s;
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -561,12 +599,9 @@ cudaError_t run(const Call& a, const DeviceInfo& info, int dev, cudaStream_t s) 
         count_launch();
         return cudaLaunchKernelEx(&cfg, kernel, args...);
     };
-    const int size = sizeof(T_IN);
-    const int wide = aligned16(G) && a.ldg * size % 16 == 0 && a.stride_g * size % 16 == 0;
-    e = launch2(ns_norm<T_IN>, NORM_THREADS, G, a.ldg, a.stride_g, a.M, a.N, wide, partial, counters,
-                n_counters);
+    e = launch2(ns_norm<T_IN>, G, a.ldg, a.stride_g, a.M, a.N, wide, partial, counters, n_counters);
     if (e != cudaSuccess) return e;
-    e = launch2(ns_convert<T_IN>, CONVERT_THREADS, G, a.ldg, a.stride_g, a.M, a.N, Np, wide,
+    e = launch2(ns_convert<T_IN>, G, a.ldg, a.stride_g, a.M, a.N, Np, wide,
                 static_cast<const double*>(partial), ctas, a.eps, x[0]);
     if (e != cudaSuccess) return e;
     return tile_columns(a, PIECES, std::max(info.sm_count / 2, 1)) == 128
