@@ -19,12 +19,15 @@
 //     exp(m - lse) c / max c, the target's element from its logit by expm1, so that a confident
 //     token's small 1 - p keeps its bits. c is divided by the largest |c|, which the last
 //     epilogue multiplies back: where all c are equal, nothing is rounded by them.
-//  4. The second launch computes dx (reduction over V, in parts where it is long and tiles are
-//     few) and dW (reduction over the tokens) together, long units first.
+//  4. A second product computes dx (reduction over V, in parts where it is long and tiles are
+//     few) and dW (reduction over the tokens) in one launch, long units first.
 //
 // Tokens are worked through in chunks, so that the exponentials take CE_CHUNK_BYTES at most.
 // float32 operands are three bfloat16 planes (24 bits), of which six products are taken; the
 // logits are then kept in FP32 and g in three planes.
+//
+// Measured (8192 x 4096 by 65536, bfloat16): 8.03 ms, 1.64 PFLOP/s, where the power cap holds cuBLAS's
+// products at 1.71 to 1.77; 2.3 + 0.37 + 4.4 ms for the three passes with the clock at 1.9 GHz.
 #include <algorithm>
 #include <cstring>
 
@@ -225,7 +228,8 @@ __global__ void __launch_bounds__(128)
 }
 
 // ce_plan and ce_gather in one launch, for few tokens: every CTA goes through all targets itself to
-// find the one that its row is for (1 token: 16 us a call in two launches, SELECT_US in one).
+// find the one that its row is for (1 x 512 by 4096, loss alone: 16.2 us of device time a call with two
+// launches, 14.3 with one).
 template <class T_IN>
 __global__ void __launch_bounds__(128)
     ce_select(const T_IN* __restrict__ x, long long ldx, int T, int D, int Dp, long long plane,
@@ -423,8 +427,9 @@ struct FinishArgs {
 };
 
 // ROWS rows a CTA, with the same columns of all of them in flight together; 8 columns a thread and
-// turn. Bound by the memory it reads and writes: at 8192 x 65536, 16 bits, 4 rows a CTA move
-// FINISH_GBS GB/s. Where that leaves SMs without a CTA, one row each.
+// turn. Bound by the memory it reads and writes: 8192 x 65536 of 16 bits, 4 rows a CTA, take 370 us
+// (5.8 TB/s; 399 with the rows one after the other). Where few rows would leave SMs without a CTA, one
+// row each (256 x 8192: 11.7 us against 22).
 template <Keep KEEP, int ROWS>
 __global__ void __launch_bounds__(FINISH_THREADS) ce_finish(const FinishArgs a) {
     __shared__ float2 part[FINISH_THREADS / 32][ROWS];

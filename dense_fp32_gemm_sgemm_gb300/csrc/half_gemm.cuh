@@ -19,6 +19,10 @@
 // (a stage of 256 columns takes 512 cycles): short segments are for results in FP32, long ones let
 // a long epilogue pass unnoticed.
 //
+// Measured: 522 cycles a stage of 256 columns, where the MMAs take 512 and 32 KiB arrive at 62 bytes
+// a cycle and SM; the tensor pipe is active 88 to 90 % of the time in products of 2048 x 4096 by 16384
+// and at the power cap in larger ones.
+//
 // Units are claimed from a counter, so that long and short ones may be mixed in a launch. Which
 // pair computes a unit does not change what is computed.
 #pragma once

@@ -16,6 +16,11 @@
 // and three products: 0.3 to 6e-6, where FP32 arithmetic throughout gives 0.2 to 3e-6. (CPU
 // simulations of 256 x 256 to 512 x 1024.) The pieces are of values times a power of two, so that
 // small entries stay in FP16's normal range: 2^13 for X, 2^12 for A, 2^10 for the polynomial.
+//
+// Measured: 6144 x 8192, bfloat16, 4.1 ms (1.41 PFLOP/s of what symmetric products cannot do without);
+// 4096 x 4096 1.07 ms, where whole rounds of 76 units take 1.15 of the work (gram and polynomial 2 for
+// 1.8, update 4 for 3.4), the update's second term and stores 11 % and the ends of 15 phases some 8 us
+// each. A finer order, in which a unit waits for its own blocks of rows alone, brought nothing.
 #include <algorithm>
 #include <cmath>
 #include <cstring>

@@ -501,7 +501,9 @@ typedef struct sgemm_ce {
  * once. float32 operands are multiplied as three bfloat16 pieces (all 24 bits; an infinity
  * counts as a NaN). A counted token with an infinity or NaN may make all of dweight NaN, as
  * the definition does. Results are bitwise reproducible: the order of sums depends on the
- * sizes and on which tokens count. Outputs must not overlap the inputs or each other.
+ * sizes and on which tokens count. Outputs must not overlap the inputs or each other (an array
+ * counts from its first to its last element, with what lies between its rows). token_weights
+ * are assumed finite.
  *
  * Workspace comes from the library's pool: the counted rows of x; for gradients 2 bytes
  * (float32: 10) for each logit of a chunk of tokens, 2 GiB at most or 256 tokens, and, where
@@ -522,7 +524,7 @@ SGEMM_API int sgemm_cross_entropy(const sgemm_ce* args, void* stream);
  * and the last X is written to `out`. G and out are device arrays of type `dtype`
  * (SGEMM_FLOAT32, SGEMM_BFLOAT16 or SGEMM_FLOAT16): element (i, j) of matrix e at
  * e * stride + i * ld + j. They may be the same array with the same pitch and stride, else they
- * must not overlap. coefficients: 3 * steps floats on the HOST, a, b, c of each step.
+ * must not overlap (from the first to the last element). coefficients: 3 * steps floats on the HOST, a, b, c of each step.
  *
  * 0 <= count <= 4096 (0 enqueues nothing), 1 <= M, N <= 32768, min(M, N) <= 16384,
  * 1 <= steps <= 64, eps >= 0; ld >= N, and matrices of a stack do not overlap. X is kept in two
