@@ -423,7 +423,7 @@ struct FinishArgs {
     void* kept;        // exponentials (16 bits, in place) or logits; null without gradients
     unsigned short* planes;  // of g for float32
     long long pitch, plane;
-    int V, T, last_finished;  // CTAs of this kernel in the whole call
+    int V, last_finished;  // CTAs of this kernel in the whole call
 };
 
 // ROWS rows a CTA, with the same columns of all of them in flight together; 8 columns a thread and
@@ -1106,7 +1106,7 @@ cudaError_t run(const sgemm_ce& a, const DeviceInfo& info, int dev, cudaStream_t
         if (e != cudaSuccess) return e;
         FinishArgs fa = {stats, stats_pitch, blocks, cols, picked, rows + live0, label + live0, ci,
                          live0, chunk, a.token_weights, a.loss, a.losses, a.lse, kept, g_planes,
-                         pitch, (long long)g_plane, a.V, a.T, finish_ctas * chunks};
+                         pitch, (long long)g_plane, a.V, finish_ctas * chunks};
         e = keep == Keep::none   ? finish<Keep::none>(fa, finish_rows, finish_ctas, s)
             : keep == Keep::bf16 ? finish<Keep::bf16>(fa, finish_rows, finish_ctas, s)
             : keep == Keep::fp16 ? finish<Keep::fp16>(fa, finish_rows, finish_ctas, s)

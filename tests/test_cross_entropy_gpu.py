@@ -314,6 +314,26 @@ def test_chunks_of_tokens_without_gradients():
     assert abs(float(out.loss) - float(mean)) <= 2 ** -22 * abs(float(mean))
 
 
+def test_offsets_beyond_31_bits():
+    """2.4e9 elements of x: the last rows' gradients, and a class of their own at the end."""
+    torch = torch_cuda()
+    T, D, V = 600001, 4096, 256
+    gen = torch.Generator(device="cuda").manual_seed(30)
+    x = torch.empty(T, D, device="cuda", dtype=torch.bfloat16)
+    x.view(-1, 4096)[:] = 0
+    x[-700:] = torch.randn(700, D, device="cuda", generator=gen).to(torch.bfloat16)
+    w = (torch.randn(V, D, device="cuda", generator=gen) * D ** -0.5).to(torch.bfloat16)
+    y = torch.full((T,), -100, device="cuda")
+    y[-700:] = torch.randint(V, (700,), device="cuda", generator=gen)
+    y[:100000] = 3  # rows of zeros: equal logits, no gradient of the weights
+    out = sg.cross_entropy_grad(x, w, y)
+    tail = Reference(x[-700:], w, y[-700:], torch.full((700,), 1 / 100700, device="cuda"))
+    tail.check((out.losses[-700:], out.lse[-700:], out.dx[-700:], out.dweight),
+               ("losses", "lse", "dx", "dw"))
+    assert (out.lse[:100000] - 8 * 0.6931471805599453).abs().max() <= 2 ** -16
+    assert not out.dx[100000:-700].any()
+
+
 def test_gradient_against_differences():
     """Central differences of the float32 loss along random directions against the gradients. Each
     loss is off by 2^-18 at most here; what the step itself costs (h^2 / 6 of the third derivative) is
