@@ -981,9 +981,11 @@ cudaError_t run(const sgemm_ce& a, const DeviceInfo& info, int dev, cudaStream_t
     fwd.live = bwd.live = &ci->count;
     fwd.live_max = bwd.live_max = chunk;
     fwd.err = bwd.err = info.error_word;
-    // losses are FP32 whatever the inputs (16 stages: off by 2^-19 of a sum at most, 3 to 4e-7
-    // of lse measured; 8: 1.5e-7, and a large product 1 % slower); 16-bit gradients bear 2^-18
-    fwd.seg_steps = f32 ? 8 : 16;
+    // Losses are FP32 whatever the inputs: 16 stages are off by 2^-19 of a sum at most, 3 to 4e-7 of
+    // lse measured; 8 by 1.5e-7, and a large product takes 1 % longer, as the epilogue has only two
+    // segments' time. Where a pair has one unit at most, whose end nothing follows, 2.
+    fwd.seg_steps = narrow ? 2 : f32 ? 8 : 16;
+    // 16-bit gradients bear 2^-18
     bwd.seg_steps = f32 ? 8 : 32;
 
     CUtensorMap kept_map;
