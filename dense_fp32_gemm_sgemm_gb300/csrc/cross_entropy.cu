@@ -42,6 +42,7 @@ constexpr int FINISH_THREADS = 256;
 constexpr int PLAN_THREADS = 1024;
 constexpr int PLAN_ITEMS = 4;
 constexpr int SELECT_TOKENS = 1024;  // up to which ce_select does the work of both
+constexpr long long MAX_TMA_PITCH = 1ll << 37;  // elements; a map's pitch ends at 2^40 bytes
 constexpr float LOG2E = 1.4426950408889634f;
 
 // What ce_plan leaves on the device.
@@ -779,16 +780,6 @@ __global__ void __launch_bounds__(256)
 }
 
 // ---- host ---------------------------------------------------------------------------------------------
-// Regions of one allocation, each 256-byte aligned.
-struct Layout {
-    size_t total = 0;
-    size_t add(size_t bytes) {
-        const size_t at = total;
-        total += (bytes + 255) & ~size_t(255);
-        return at;
-    }
-};
-
 int round_up(int n, int to) { return (n + to - 1) / to * to; }
 
 struct Planes {
@@ -911,7 +902,8 @@ cudaError_t run(const sgemm_ce& a, const DeviceInfo& info, int dev, cudaStream_t
     const bool narrow = chunk / 256 * ((a.V + 255) / 256) < pairs;
     const int cols = narrow ? 64 : 128;
     const int blocks = (a.V + cols - 1) / cols;
-    const bool direct = !f32 && aligned16(a.weight) && a.ldw % 8 == 0;
+    const bool direct =
+        !f32 && aligned16(a.weight) && a.ldw % 8 == 0 && a.ldw < MAX_TMA_PITCH;
     const int tiles_d = (a.D + 255) / 256;
     const int splits =
         a.dx ? dx_splits(chunk / 256 * tiles_d, (a.V + 63) / 64,
@@ -919,7 +911,7 @@ cudaError_t run(const sgemm_ce& a, const DeviceInfo& info, int dev, cudaStream_t
              : 1;
     const bool sums = a.dweight && chunks > 1;
 
-    Layout lay;
+    hg::Layout lay;
     const size_t at_info = lay.add(sizeof(CeInfo));
     const size_t at_counters = lay.add(size_t(chunks) * 2 * sizeof(int));
     const size_t at_rows = lay.add(size_t(Tp) * 4);
@@ -1051,7 +1043,7 @@ cudaError_t run(const sgemm_ce& a, const DeviceInfo& info, int dev, cudaStream_t
         outs[n].rows_n = a.V;
         outs[n].cols_n = a.D;
         outs[n].sums = sums ? sum : nullptr;
-        outs[n].tma = !sums && outs[n].wide;
+        outs[n].tma = !sums && outs[n].wide && a.lddw < MAX_TMA_PITCH;
         if (outs[n].tma && !hg::encode_block(&outs[n].map, a.dweight, size, a.D, a.V, a.lddw, 1,
                                              a.lddw, 128 / size, 32))
             return cudaErrorInvalidValue;

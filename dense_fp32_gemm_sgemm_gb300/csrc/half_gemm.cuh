@@ -788,6 +788,16 @@ cudaError_t launch(void (*kernel)(KArgs...), unsigned grid, unsigned block, size
     return e;
 }
 
+// Regions of one allocation, each 256-byte aligned.
+struct Layout {
+    size_t total = 0;
+    size_t add(size_t bytes) {
+        const size_t at = total;
+        total += (bytes + 255) & ~size_t(255);
+        return at;
+    }
+};
+
 // Box rows of an operand: 64 k of a chunk, or its rows in a CTA.
 inline int box_rows(bool mn, int rows_of_cta) { return mn ? BK : rows_of_cta; }
 

@@ -429,15 +429,6 @@ struct Call {
     float eps;
 };
 
-struct Layout {
-    size_t total = 0;
-    size_t add(size_t bytes) {
-        const size_t at = total;
-        total += (bytes + 255) & ~size_t(255);
-        return at;
-    }
-};
-
 // Products of one piece each, or of low.high, high.low and high.high pieces.
 void set_products(hg::Problem& p, int pieces) {
     p.planes_a = p.planes_b = pieces;
@@ -574,7 +565,7 @@ cudaError_t run(const Call& a, const DeviceInfo& info, int dev, cudaStream_t s) 
     const long long groups = (long long)a.M * ((a.N + 7) / 8);
     const int most = std::max(1, std::min(MAX_NORM_CTAS, 4096 / a.count + 1));
     const int ctas = int(std::min<long long>(most, (groups + NORM_THREADS - 1) / NORM_THREADS));
-    Layout lay;
+    hg::Layout lay;
     const int n_counters = 1 + 3 * a.steps * a.count;
     const size_t at_counters = lay.add(size_t(n_counters) * sizeof(int));
     const size_t at_norm = lay.add(size_t(a.count) * ctas * sizeof(double));
