@@ -334,6 +334,23 @@ def test_offsets_beyond_31_bits():
     assert not out.dx[100000:-700].any()
 
 
+def test_rows_gigabytes_apart():
+    """Weights and their gradient with rows 2^31 bytes apart; without tokens, the zeros there too."""
+    torch = torch_cuda()
+    T, D, V, pitch = 70, 96, 3, 2 ** 30 + 64
+    x, w, y, _ = inputs(T, D, V, "bf16")
+    expected = sg.cross_entropy_grad(x, w, y)
+    wide = torch.empty_strided((V, D), (pitch, 1), device="cuda", dtype=torch.bfloat16)
+    wide.copy_(w)
+    dw = torch.empty_strided((V, D), (pitch, 1), device="cuda", dtype=torch.bfloat16)
+    out = sg.cross_entropy_grad(x, wide, y, dweight=dw)
+    for got, want in zip(out, expected):
+        assert torch.equal(got, want)
+    dw.fill_(float("nan"))
+    sg.cross_entropy_grad(x[:0], wide, y[:0], dweight=dw)
+    assert not dw.any()
+
+
 def test_gradient_against_differences():
     """Central differences of the float32 loss along random directions against the gradients. Each
     loss is off by 2^-18 at most here; what the step itself costs (h^2 / 6 of the third derivative) is
