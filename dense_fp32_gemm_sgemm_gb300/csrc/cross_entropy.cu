@@ -9,16 +9,18 @@
 //  1. ce_plan lists the counted tokens in order, ce_gather packs their rows of x (ce_select does
 //     both for few). Uncounted rows
 //     are never read again: whatever they hold stays out of dW, and costs no products.
-//  2. The first product's epilogue has a row's 64 or 128 columns in a thread: their maximum m and
-//     sum of exp(s - m) (FP32) go to `stats`, the target's logit (FP32) is picked out, and, for
-//     gradients, exp(s - m) is stored in 16 bits. That rounding (2^-9 of each value, bfloat16;
+//  2. The first product's epilogue has a row's 64 or 128 columns in a thread: the target's logit (FP32)
+//     is picked out, the maximum m and the sum of exp(s - m) (FP32) of the other columns go to `stats`,
+//     and, for gradients, exp(s - m) is stored in 16 bits. That rounding (2^-9 of each value, bfloat16;
 //     2^-12, FP16, which holds them times 2^15 so that small ones keep their bits) and the one
 //     of g average out in the sums over tokens and vocabulary; s itself in 16 bits would be off
 //     by 2^-9 |s| in the exponent.
-//  3. ce_finish joins the stats of a row to lse and turns the exponentials into g in place: times
-//     exp(m - lse) c / max c, the target's element from its logit by expm1, so that a confident
-//     token's small 1 - p keeps its bits. c is divided by the largest |c|, which the last
-//     epilogue multiplies back: where all c are equal, nothing is rounded by them.
+//  3. ce_finish joins the stats of a row to the others' sum, `rest`, and with the target's exponential e
+//     to lse, and turns the exponentials into g in place: times exp(m - lse) c / max c. The target's
+//     loss and element are log1p(rest / e) and -rest / (e + rest): a confident token's, whose rest may
+//     be below 2^-24 of e, keep their bits, which a sum of all exponentials has dropped. c is divided
+//     by the largest |c|, which the last epilogue multiplies back: where all c are equal, nothing is
+//     rounded by them.
 //  4. A second product computes dx (reduction over V, in parts where it is long and tiles are
 //     few) and dW (reduction over the tokens) in one launch, long units first.
 //
@@ -339,7 +341,7 @@ struct CeForward {
     static constexpr int PROBLEMS = 1, PLANES = 1;
     static constexpr bool CHAIN = false;
     struct Params {
-        float2* stats;   // [block of COLS columns][row of the chunk]: maximum, sum
+        float2* stats;   // [block of COLS columns][row of the chunk]: maximum, sum without the target
         float* picked;   // [row of the chunk]
         const int* label;  // of the chunk's rows
         CUtensorMap kept;  // blocks of 64 columns (16 bits) or 32 (logits)
@@ -383,7 +385,10 @@ struct CeForward {
         if (__any_sync(~0u, y >= 0 && y < cols)) {
             float v = 0.f;
 #pragma unroll
-            for (int j = 0; j < COLS; ++j) v = y == j ? s[j] : v;
+            for (int j = 0; j < COLS; ++j) {
+                v = y == j ? s[j] : v;
+                s[j] = y == j ? -INFINITY : s[j];  // the statistics are of the others
+            }
             if (y >= 0 && y < cols) p.picked[r] = v;
         }
         float m = s[0];
@@ -500,14 +505,17 @@ __global__ void __launch_bounds__(FINISH_THREADS) ce_finish(const FinishArgs a) 
             }
             const int token = a.rows[r];
             y = a.label[r];
-            from = t.x;
-            logl = logf(t.y);
             const float picked = a.picked[r];
+            from = fmaxf(t.x, picked);  // t: of all but the target
+            const float rest = t.x == -INFINITY ? t.y : t.y * expf(t.x - from);
+            const float e = picked == -INFINITY ? 0.f : expf(picked - from);
+            const float total = e + rest;
+            logl = logf(total);
             a.lse[token] = from + logl;
-            a.losses[token] = (from - picked) + logl;
+            a.losses[token] = rest <= e ? log1pf(rest / e) : (from - picked) + logl;
             const float c = a.c ? a.c[token] : a.info->c_mean;
             scale = c / a.info->c_max;
-            at_label = expm1f((picked - from) - logl) * scale;
+            at_label = -(rest / total) * scale;
         }
         row_from[tid] = from;
         row_log[tid] = logl;
