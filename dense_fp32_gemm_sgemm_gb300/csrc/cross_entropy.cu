@@ -981,11 +981,14 @@ cudaError_t run(const sgemm_ce& a, const DeviceInfo& info, int dev, cudaStream_t
     fwd.live = bwd.live = &ci->count;
     fwd.live_max = bwd.live_max = chunk;
     fwd.err = bwd.err = info.error_word;
-    // Losses are FP32 whatever the inputs: 16 stages are off by 2^-19 of a sum at most, 3 to 4e-7 of
-    // lse measured; 8 by 1.5e-7, and a large product takes 1 % longer, as the epilogue has only two
-    // segments' time. Where a pair has one unit at most, whose end nothing follows, 2.
-    fwd.seg_steps = narrow ? 2 : f32 ? 8 : 16;
-    // 16-bit gradients bear 2^-18
+    // Losses are FP32 whatever the inputs, so segments are short (relative error of the losses, against
+    // 64 bits): 16 stages 7 to 9e-7, 8 stages 3 to 5e-7, 4 stages 2 to 3e-7, 2 stages 1e-7. With several
+    // rows of tiles the epilogue has only two segments' time: 8 stages take as long as 16 (2048 x 4096 by
+    // 65536, bfloat16: 652 and 655 us; 4 stages 685, 2 stages 740). A single row of tiles waits for its
+    // weights, and 4 stages cost nothing (256 x 4096 by 65536: 133.3 and 133.2 us with 16, float32 901 and
+    // 897 with 8; 2 stages 139 and 961). Tiles of 128 columns, of which a pair has two at most: 2 stages.
+    fwd.seg_steps = narrow ? 2 : chunk == 256 ? 4 : 8;
+    // 128 MMAs cut off 2^-16 of a sum of one sign, which is far below a 16-bit gradient's rounding
     bwd.seg_steps = f32 ? 8 : 32;
 
     CUtensorMap kept_map;
