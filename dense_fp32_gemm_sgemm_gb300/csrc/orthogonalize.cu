@@ -452,11 +452,12 @@ cudaError_t iterate(const Call& a, const DeviceInfo& info, __half* (&x)[2], __ha
     g.counter = counters;
     g.done = counters + 1;
     g.err = info.error_word;
-    // 16-bit results bear an accumulator that is cut off 4 * 256 times (2^-15 of a sum, at most).
+    // 16-bit results: 128 MMAs at most between two additions in FP32, which cut off 2^-16 of a sum of one
+    // sign. (A float16 sum of 3072 lost 1.3e-4, a quarter of its rounding and always towards zero.)
     // float32: 32 or 36 MMAs, or 8 or 12 where the smaller side is below 512 and FP32 arithmetic itself
     // is good to 1 to 2e-6 (64 x 999 to 350 x 542: 2.0 to 3.7e-6 against 1.2 to 2e-6, 8 to 15 % of the
     // time; 2304 x 2560: 0.9e-6 against 0.6e-6 and FP32's 2.6e-6, 27 %).
-    g.seg_steps = a.dtype != SGEMM_FLOAT32 ? 256
+    g.seg_steps = a.dtype != SGEMM_FLOAT32 ? 128 / (Chain::PLANES == 1 ? 4 : 12)
                   : r < 512                ? (Chain::PLANES == 1 ? 2 : 1)
                                            : (Chain::PLANES == 1 ? 8 : 3);
     // operand maps: k contiguous, or the other index
