@@ -15,11 +15,15 @@
 // FP32 accumulator shifts out, always towards zero. Measured in sums of one sign, FP16 operands: 0.8 ulps of
 // the accumulator (an ulp is 2^-23 of it at most) an MMA in sums of 4 MMAs, 1.9 in sums of 32, 2.2 in the worst
 // sum; bfloat16 products have fewer bits to lose, 0.3. So n MMAs cost up to n 2^-23 of an evenly growing sum.
-// After seg_steps stages (4 MMAs each, 12 with two planes) the accumulator is therefore added to FP32
-// registers, rounded to nearest, and starts again at zero. The two accumulators of a CTA pair alternate, so
-// the additions overlap the next stages' MMAs, and so does the epilogue as far as two segments reach (a
-// stage of 256 columns takes 512 cycles): short segments are for results in FP32, long ones let a long
-// epilogue pass unnoticed.
+// After seg_steps stages (4 MMAs each) the accumulator is therefore added to FP32 registers, rounded to
+// nearest, and starts again at zero. The two accumulators of a CTA pair alternate, so the additions overlap
+// the next stages' MMAs, and so does the epilogue as far as two segments reach (a stage of 256 columns
+// takes 512 cycles): short segments are for results in FP32, long ones let a long epilogue pass unnoticed.
+//
+// Where two planes share a stage (Ring), the second is what the first leaves of a value, times 2^11: an FP16
+// piece of it then has its 11 bits down to 2^-38 of the first's unit instead of 2^-14. Both products that
+// have a second plane are summed in accumulators of their own, a unit's whole reduction in one, and added with
+// 2^-11 to the unit's last segment; what these cut off is 2^-11 of the other's.
 //
 // Measured: 522 cycles a stage of 256 columns, where the MMAs take 512 and 32 KiB arrive at 62 bytes
 // a cycle and SM; the tensor pipe is active 88 to 90 % of the time in products of 2048 x 4096 by 16384
@@ -56,14 +60,15 @@ constexpr int CHUNK_BYTES = 64 * BK * 2;  // 64 elements of the other index by 6
 constexpr int STAGING = 4096;             // bytes of a staging block
 constexpr int NUM_BARS = 2 * MAX_STAGES + 6 + 2 * SLOTS + 2 * EPI_WARPS;
 constexpr int MAX_PRODUCTS = 6;
+constexpr float SECOND_UP = 0x1p11f, SECOND_DOWN = 0x1p-11f;  // of the second of two planes in a stage
 
 template <int BN>
 constexpr int B_BYTES = BN / 2 * BK * 2;
 // A stage: 64 k of both operands, of one plane each (then every product has a stage to itself), or
-// of all PLANES of them, which all products of those k share. A stage of one product and 128 columns
-// takes some 430 cycles to wait for, issue and hand on where its MMAs take 256, and its 24 KiB 384 to
-// arrive; with two planes three products share 48 KiB, a wait and a commit. (Of 256 columns the MMAs
-// take 512, and three stages of 64 KiB would look ahead no further.)
+// of both planes of them (a value and 2^11 times what that leaves), which three products share: all but
+// the one of the second planes. A stage of one product and 128 columns takes some 430 cycles to wait for,
+// issue and hand on where its MMAs take 256, and its 24 KiB 384 to arrive; with two planes three products
+// share 48 KiB, a wait and a commit.
 template <class EPI>
 struct Ring {
     static constexpr int BN = EPI::BN, PLANES = EPI::PLANES;
@@ -76,6 +81,8 @@ struct Ring {
         STAGES * STAGE_BYTES + BLOCKS * EPI_WARPS * STAGING + 512 + 1024;
     static_assert(SMEM_BYTES <= 232448, "shared memory of an SM");
     static_assert(STAGES <= MAX_STAGES && (PLANES == 1 || (PLANES == 2 && BN == 128)), "see above");
+    // of tensor memory: two accumulators, and with two planes two more
+    static constexpr int TMEM_COLUMNS = 2 * PLANES * BN;
 };
 
 // One product of a launch. Sizes are in elements; `live` may replace one of them on the device.
@@ -89,7 +96,7 @@ struct Problem {
     int a_mn, b_mn;     // operand stored with its other index contiguous (else with k)
     int a_row, b_row;   // added to the row coordinate (k or the other index, whichever is a row)
     int planes_a, planes_b;
-    int products;       // pairs of planes, smallest products first
+    int products;       // pairs of planes, smallest products first (1 where a stage holds two planes)
     unsigned char pa[MAX_PRODUCTS], pb[MAX_PRODUCTS];
     unsigned idesc;     // instruction descriptor without N
 };
@@ -427,7 +434,8 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 //   void unit(const Unit&, int row, int col, float (&acc)[BN / 2])
 // called by each epilogue warp at the beginning of a unit (to load what it will need) and with its
 // sums: lane l holds row `row` + l, columns col .. col + BN / 2.
-// EPI::PROBLEMS: of the launch at most. EPI::PLANES: staged together (see Ring). EPI::CHAIN: units
+// EPI::PROBLEMS: of the launch at most. EPI::PLANES: staged together (see Ring); with two, every unit has
+// some of the reduction. EPI::CHAIN: units
 // are claimed in order, and one waits until all units of the phase before that belong to the same
 // product have been stored. Every earlier unit was claimed by a CTA that runs, and waits for still
 // earlier ones only, so that all waits end however many CTAs the GPU runs at a time.
@@ -467,7 +475,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
     }
     if (warp == 1) {
-        ptx::tmem_alloc_pair(ptx::smem_u32(sm.tmem_slot), 2 * BN);
+        ptx::tmem_alloc_pair(ptx::smem_u32(sm.tmem_slot), R::TMEM_COLUMNS);
         ptx::tmem_relinquish_pair();
     }
     ptx::tc_fence_before();
@@ -554,8 +562,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 ok = !CHAIN || wait_before(t);
                 for (int kb = t.kb0; ok && kb < t.kb1; ++kb) {
                     unsigned planes_left = order;
-                    const int stages = R::PLANES == 1 ? products : 1;
-                    for (int q = 0; q < stages; ++q) {
+                    for (int q = 0; q < products; ++q) {
                         const int z = z0 + int(planes_left & 15u);
                         planes_left >>= 4;
                         ok = wait_all(empty0 + 8u * s, ph ^ 1u);
@@ -621,16 +628,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 const Problem& p = g.p[t.problem];
                 const uint32_t idesc = p.idesc | (uint32_t(BN >> 3) << 17);
                 const OperandDesc a(sm.ring, p.a_mn), b(sm.ring + R::B_AT, p.b_mn);
-                // the products' planes within a stage, four bits each
-                const int products = p.products;
-                unsigned order_a = 0, order_b = 0;
-                if constexpr (R::PLANES > 1) {
-                    for (int q = 0; q < products; ++q) {
-                        order_a |= unsigned(p.pa[q]) << (4 * q);
-                        order_b |= unsigned(p.pb[q]) << (4 * q);
-                    }
-                }
-                int left = (t.kb1 - t.kb0) * (R::PLANES == 1 ? products : 1);
+                // Two planes: the unit's sum of the products that have a second one. The unit before the
+                // last had this accumulator, and its last segment, read with it, was waited for at the
+                // latest with this unit's first: the unit between has one at least.
+                const uint32_t d_low = tmem + uint32_t(2 * BN + (i & 1) * BN);
+                uint32_t started = 0;
+                int left = (t.kb1 - t.kb0) * p.products;
                 for (; ok && left > 0; left -= g.seg_steps, ++seg) {
                     const int half = seg & 1;
                     ok = wait_all(sm.acc_empty(half), ((seg >> 1) & 1) ^ 1);
@@ -647,14 +650,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                             ptx::mma_pair_x4(d, a.lo + at, a.hi, a.step, b.lo + at, b.hi, b.step,
                                              idesc, j);
                         } else {
-                            unsigned oa = order_a, ob = order_b;
-                            for (int q = 0; q < products; ++q) {
-                                ptx::mma_pair_x4(d, a.lo + at + (oa & 15u) * (A_BYTES >> 4), a.hi,
-                                                 a.step, b.lo + at + (ob & 15u) * (B_BYTES<BN> >> 4),
-                                                 b.hi, b.step, idesc, j | q);
-                                oa >>= 4;
-                                ob >>= 4;
-                            }
+                            constexpr uint32_t A1 = A_BYTES >> 4, B1 = B_BYTES<BN> >> 4;
+                            ptx::mma_pair_x4(d_low, a.lo + at + A1, a.hi, a.step, b.lo + at, b.hi,
+                                             b.step, idesc, started);
+                            started = 1;
+                            ptx::mma_pair_x4(d_low, a.lo + at, a.hi, a.step, b.lo + at + B1, b.hi,
+                                             b.step, idesc, 1);
+                            ptx::mma_pair_x4(d, a.lo + at, a.hi, a.step, b.lo + at, b.hi, b.step,
+                                             idesc, j);
                         }
                         issued = true;
                         ptx::mma_commit_pair_elect(sm.empty(s), 0x3);
@@ -696,7 +699,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             if (u < 0) break;
             if (lane == 0) taken(i);
             const Unit t = unit_at<BN, CHAIN>(g, n_units, u, live);
-            const int steps = (t.kb1 - t.kb0) * (R::PLANES == 1 ? g.p[t.problem].products : 1);
+            const int steps = (t.kb1 - t.kb0) * g.p[t.problem].products;
             const int segs = (steps + g.seg_steps - 1) / g.seg_steps;
             const int row = t.row0 + int(rank) * HALF_M + q * 32, col = t.col0 + h * COLS;
             if constexpr (CHAIN) {
@@ -728,6 +731,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                         for (int j = 0; j < 16; ++j) acc[c + j] += __uint_as_float(r[j]);
                     }
                 }
+                if constexpr (R::PLANES == 2) {
+                    if (sg == segs - 1) {
+                        const uint32_t low =
+                            tmem + (uint32_t(q * 32) << 16) + uint32_t((2 + (i & 1)) * BN + h * COLS);
+#pragma unroll
+                        for (int c = 0; c < COLS; c += 16) {
+                            uint32_t r[16];
+                            __syncwarp();
+                            ptx::tmem_ld_16(low + c, r);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                acc[c + j] = fmaf(__uint_as_float(r[j]), SECOND_DOWN, acc[c + j]);
+                        }
+                    }
+                }
                 ptx::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive_remote(ptx::mapa_shared(sm.acc_empty(b), 0));
@@ -755,7 +773,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     if (warp == 1) {
         __syncwarp();
         ptx::tc_fence_after();
-        ptx::tmem_dealloc_pair(tmem, 2 * BN);
+        ptx::tmem_dealloc_pair(tmem, R::TMEM_COLUMNS);
     }
 }
 

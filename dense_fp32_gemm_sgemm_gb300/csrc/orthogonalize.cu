@@ -14,8 +14,12 @@
 // as by the rounding of a bfloat16 result (1.7e-3); bfloat16 factors give 0.5 to 1.3e-2, and 1 to
 // 20e-2 where X is rounded to them too. float16 and float32 results take both pieces of each factor
 // and three products: 0.3 to 6e-6, where FP32 arithmetic throughout gives 0.2 to 3e-6. (CPU
-// simulations of 256 x 256 to 512 x 1024.) The pieces are of values times a power of two, so that
-// small entries stay in FP16's normal range: 2^13 for X, 2^12 for A, 2^10 for the polynomial.
+// simulations of 256 x 256 to 512 x 1024.) The first pieces are of values times a power of two, so that
+// small entries stay in FP16's normal range: 2^13 for X, 2^12 for A, 2^10 for the polynomial; the second
+// of what they leave, times 2^11 more, so that a value has 22 bits down to 2^-27 (X), 2^-26 and 2^-24 and
+// steps of 2^-48, 2^-47 and 2^-45 below. Rows of small entries keep their own precision: one 1e-5 times as
+// large as the others of 256 x 256 or 256 x 1024 is good to 1 to 5e-7, 1e-7 to 3 to 5e-6 (without the 2^11
+// 0.5 to 1e-4 and 0.4 to 1e-2; FP32 0.4 to 2e-6).
 //
 // Measured: 6144 x 8192, bfloat16, 4.1 ms (1.41 PFLOP/s of what symmetric products cannot do without);
 // 4096 x 4096 1.07 ms, where whole rounds of 76 units take 1.15 of the work (gram and polynomial 2 for
@@ -150,7 +154,7 @@ __device__ __forceinline__ void first_x(const T_IN* from, long long ld, int M, i
             const float b = c0 + j + 1 < N ? ((v[j + 1] * f0) * f1) * f2 : 0.f;
             high[j / 2] = __floats2half2_rn(a, b);
             const float2 h = __half22float2(high[j / 2]);
-            low[j / 2] = __floats2half2_rn(a - h.x, b - h.y);
+            low[j / 2] = __floats2half2_rn((a - h.x) * hg::SECOND_UP, (b - h.y) * hg::SECOND_UP);
         }
         __half* o = to + row * (long long)Np + c0;
         *reinterpret_cast<uint4*>(o) = *reinterpret_cast<const uint4*>(high);
@@ -220,7 +224,7 @@ struct NsChain {
     static constexpr int BN = BN_;
     static constexpr int COLS = BN / 2;
     static constexpr int PROBLEMS = 6;
-    static constexpr int PLANES = BN == 128 ? PIECES : 1;
+    static constexpr int PLANES = PIECES;
     static constexpr bool CHAIN = true;
     struct Params {
         FactorMaps gram, poly;
@@ -313,6 +317,7 @@ struct NsChain {
             for (int at = 0; at < COLS; at += 64) {
 #pragma unroll 1
                 for (int k = 0; k < m.pieces && col + at < cols_n; ++k, ++n) {
+                    const float times = k == 0 ? h : h * hg::SECOND_DOWN;
                     io.wait_load(Io::of(n));
                     uint8_t* block = io.block(Io::of(n));
 #pragma unroll
@@ -323,8 +328,8 @@ struct NsChain {
                         for (int i = 0; i < 4; ++i) {
                             const float2 x =
                                 __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-                            s[8 * j + 2 * i] = fmaf(h, x.x, s[8 * j + 2 * i]);
-                            s[8 * j + 2 * i + 1] = fmaf(h, x.y, s[8 * j + 2 * i + 1]);
+                            s[8 * j + 2 * i] = fmaf(times, x.x, s[8 * j + 2 * i]);
+                            s[8 * j + 2 * i + 1] = fmaf(times, x.y, s[8 * j + 2 * i + 1]);
                         }
                     }
                     __syncwarp();  // read by all lanes
@@ -356,7 +361,8 @@ struct NsChain {
             for (int j = 0; j < 64; j += 2) {
                 const __half2 high = __floats2half2_rn(s[j], s[j + 1]);
                 const float2 v = __half22float2(high);
-                const __half2 low = __floats2half2_rn(s[j] - v.x, s[j + 1] - v.y);
+                const __half2 low = __floats2half2_rn((s[j] - v.x) * hg::SECOND_UP,
+                                                      (s[j + 1] - v.y) * hg::SECOND_UP);
                 s[j] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&high));
                 s[j + 1] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&low));
             }
@@ -429,11 +435,10 @@ struct Call {
     float eps;
 };
 
-// Products of one piece each, or of low.high, high.low and high.high pieces.
+// Factors of one piece each, or of two that a stage holds together (all but the product of the second ones).
 void set_products(hg::Problem& p, int pieces) {
     p.planes_a = p.planes_b = pieces;
-    p.products = pieces == 1 ? 1 : 3;
-    if (pieces == 2) p.pa[0] = p.pb[1] = 1;
+    p.products = 1;
 }
 
 // counters: of claimed units, then of each phase's finished ones
@@ -453,13 +458,13 @@ cudaError_t iterate(const Call& a, const DeviceInfo& info, __half* (&x)[2], __ha
     g.done = counters + 1;
     g.err = info.error_word;
     // 16-bit results: 128 MMAs at most between two additions in FP32, which cut off 2^-16 of a sum of one
-    // sign. (A float16 sum of 3072 lost 1.3e-4, a quarter of its rounding and always towards zero.)
-    // float32: 32 or 36 MMAs, or 8 or 12 where the smaller side is below 512 and FP32 arithmetic itself
-    // is good to 1 to 2e-6 (64 x 999 to 350 x 542: 2.0 to 3.7e-6 against 1.2 to 2e-6, 8 to 15 % of the
-    // time; 2304 x 2560: 0.9e-6 against 0.6e-6 and FP32's 2.6e-6, 27 %).
-    g.seg_steps = a.dtype != SGEMM_FLOAT32 ? 128 / (Chain::PLANES == 1 ? 4 : 12)
-                  : r < 512                ? (Chain::PLANES == 1 ? 2 : 1)
-                                           : (Chain::PLANES == 1 ? 8 : 3);
+    // sign.
+    // float32 (MMAs of the first pieces): 12, or 4 where the smaller side is below 512 and FP32 arithmetic
+    // itself is good to 1 to 2e-6 (350 x 542: 3.2e-6 with 12, 2.4e-6 with 8, 1.5e-6 with 4, FP32 2.1e-6;
+    // 64 x 20000 takes 980 us instead of 755; 1001 x 2731: 3.2e-6 with 36, 1.3e-6 with 12, 0.7e-6 with 4, FP32
+    // 2.5e-6, 367, 384 and 430 us), or 24 from 2048 on (2304 x 2560: 0.9e-6 against 0.6e-6 with 12 and FP32's
+    // 2.6e-6; 6144 x 8192 11.8 and 12.4 ms).
+    g.seg_steps = a.dtype != SGEMM_FLOAT32 ? 32 : r < 512 ? 1 : r < 2048 ? 3 : 6;
     // operand maps: k contiguous, or the other index
     auto x_operand = [&](CUtensorMap& m, int i, bool mn, int rows_of_cta) {
         return hg::encode_operand(&m, x[i], false, a.N, a.M, Np, 2 * a.count, x_plane,
@@ -528,15 +533,13 @@ cudaError_t iterate(const Call& a, const DeviceInfo& info, __half* (&x)[2], __ha
     return hg::launch_gemm<Chain>(g, p, info.sm_count, s);
 }
 
-// Columns of a tile: whatever gives the shorter step by what was measured: 522 cycles for a stage
-// of 256 columns, 430 for one of 128, or 270 for each product where three share a stage; and what
-// the last unit's epilogue adds to a phase, 6000 or 3000. A phase of one matrix takes whole rounds
-// of units; the phases of several overlap.
+// Columns of a tile with factors of one piece: whatever gives the shorter step by what was measured, 522
+// cycles for a stage of 256 columns and 430 for one of 128, and what the last unit's epilogue adds to a
+// phase, 6000 or 3000. A phase of one matrix takes whole rounds of units; the phases of several overlap.
+// (Two pieces have 128: their second accumulators take the rest of the tensor memory.)
 template <int BN>
-double step_cycles(const Call& a, int pieces, int pairs) {
+double step_cycles(const Call& a, int pairs) {
     const int r = std::min(a.M, a.N), q = std::max(a.M, a.N);
-    const int products = pieces == 1 ? 1 : 3;
-    const double stage = BN == 256 ? 522. : pieces == 1 ? 430. : 270.;
     hg::Problem square = {}, whole = {};
     square.symmetric = 1;
     const int tiles_r = hg::ceil_div(r, hg::BM);
@@ -549,12 +552,8 @@ double step_cycles(const Call& a, int pieces, int pairs) {
         return a.count == 1 ? std::ceil(n) : std::max(n, 1.);
     };
     const double k_q = hg::ceil_div(q, hg::BK), k_r = hg::ceil_div(r, hg::BK);
-    return (rounds(units_r) * (k_q + k_r) + rounds(units_x) * k_r) * products * stage +
+    return (rounds(units_r) * (k_q + k_r) + rounds(units_x) * k_r) * (BN == 256 ? 522. : 430.) +
            3 * (BN == 256 ? 6000. : 3000.);
-}
-
-int tile_columns(const Call& a, int pieces, int pairs) {
-    return step_cycles<128>(a, pieces, pairs) < step_cycles<256>(a, pieces, pairs) ? 128 : 256;
 }
 
 template <class T_IN, int PIECES>
@@ -606,9 +605,12 @@ cudaError_t run(const Call& a, const DeviceInfo& info, int dev, cudaStream_t s) 
     e = launch2(ns_convert<T_IN>, G, a.ldg, a.stride_g, a.M, a.N, Np, wide,
                 static_cast<const double*>(partial), ctas, a.eps, x[0]);
     if (e != cudaSuccess) return e;
-    return tile_columns(a, PIECES, std::max(info.sm_count / 2, 1)) == 128
-               ? iterate<128, PIECES>(a, info, x, gram, poly, counters, Np, rp, s)
-               : iterate<256, PIECES>(a, info, x, gram, poly, counters, Np, rp, s);
+    if constexpr (PIECES == 1) {
+        const int pairs = std::max(info.sm_count / 2, 1);
+        if (step_cycles<256>(a, pairs) <= step_cycles<128>(a, pairs))
+            return iterate<256, 1>(a, info, x, gram, poly, counters, Np, rp, s);
+    }
+    return iterate<128, PIECES>(a, info, x, gram, poly, counters, Np, rp, s);
 }
 
 // Bytes from the first to behind the last element.

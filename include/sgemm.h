@@ -529,16 +529,22 @@ SGEMM_API int sgemm_cross_entropy(const sgemm_ce* args, void* stream);
  * 0 <= count <= 4096 (0 enqueues nothing), 1 <= M, N <= 32768, min(M, N) <= 16384,
  * 1 <= steps <= 64, eps >= 0; ld >= N, and matrices of a stack do not overlap. X is kept in two
  * FP16 pieces (22 bits) from step to step; the factors of the products are one piece (11 bits)
- * for bfloat16 and two for the other types; sums are FP32. The pieces are of values times 2^13
- * (X), 2^12 (A) and 2^10 (the polynomial): entries of X must stay below 8, of A below 16, of
- * b A + c A A below 64 in size, else the result is NaN. As |X| <= 1 at first, that holds for any
- * coefficients meant to bring singular values near one. A matrix with an infinity or NaN gives
+ * for bfloat16 and two for the other types; sums are FP32. The first pieces are of values times
+ * 2^13 (X), 2^12 (A) and 2^10 (the polynomial b A + c A A), the second of what these leave, times
+ * 2^11 more. So 22 bits are kept of entries from 2^-27 (X), 2^-26 and 2^-24 on, 11 bits of one
+ * piece from 2^-26 (A) and 2^-24 on; below that steps are 2^-48, 2^-47 and 2^-45, or 2^-36 and
+ * 2^-34: float32 rows or columns down to some 1e-6 of the others' size are as near as FP32
+ * arithmetic, smaller ones lose a bit for each factor of two. Entries of X must stay below 8,
+ * of A below 16, of the polynomial below 64 in size; a larger one is an infinity or NaN in all
+ * that follows from it. As |X| <= 1 at first, that holds for any coefficients meant to bring
+ * singular values near one. A matrix with an infinity or NaN gives
  * NaN; the others of its stack are not touched by it. A zero matrix gives zeros (with eps = 0, NaN).
  * Results are bitwise reproducible, and a matrix's do not depend on the others of its stack (but
  * on their number, which decides how sums are split).
  *
- * Workspace comes from the library's pool: 8 bytes for each element and, with r = min(M, N), 4 (or
- * 8) times r * r for each matrix. Three launches. Everything is stream-ordered; the call can be
+ * Workspace comes from the library's pool: 8 bytes for each element (one step: 4) and, with
+ * r = min(M, N), 4 (bfloat16) or 8 times r * r for each matrix, rows rounded up to 64 elements.
+ * Three launches. Everything is stream-ordered; the call can be
  * captured into a CUDA graph after one call of the same kind outside.
  */
 SGEMM_API int sgemm_orthogonalize(const void* G, int dtype, int count, int M, int N, long long ldg,
