@@ -12,6 +12,7 @@ those of ``sgemm_cross_entropy`` and ``sgemm_orthogonalize`` in the C header.
 from __future__ import annotations
 
 import ctypes
+import operator
 import struct
 from typing import NamedTuple
 
@@ -136,7 +137,8 @@ def _layout(t, name):
     count = t.shape[0] if t.dim() == 3 else 1
     stride = t.stride(0) if count > 1 else 0
     if count > 1 and stride < (M - 1) * pitch + N:
-        raise ValueError(f"{name}'s matrices must not overlap (strides {t.stride()})")
+        raise ValueError(f"each of {name}'s matrices must begin behind the last element of the one "
+                         f"before (strides {t.stride()})")
     return count, M, N, pitch, stride
 
 
@@ -146,10 +148,10 @@ def orthogonalize(G, steps: int = 5, coefficients=ORTHOGONALIZE_COEFFICIENTS, ep
     towards the nearest matrix with orthonormal rows (columns where M > N): X = G / (|G| + eps),
     then ``X = a X + (b A + c A A) X`` with ``A = X X^T`` for each step. ``coefficients``: a, b, c
     for all steps or a sequence of one such triple for each. ``out`` may be G itself."""
+    steps = operator.index(steps)
     _cuda_tensor(G, "G")
     code = _dtype_code(G, "G")
     count, M, N, ldg, stride_g = _layout(G, "G")
-    steps = int(steps)
     triples = [tuple(c) if isinstance(c, (tuple, list)) else c for c in coefficients]
     if triples and not isinstance(triples[0], tuple):
         triples = [tuple(triples)] * steps

@@ -527,8 +527,8 @@ SGEMM_API int sgemm_cross_entropy(const sgemm_ce* args, void* stream);
  * must not overlap (from the first to the last element). coefficients: 3 * steps floats on the HOST, a, b, c of each step.
  *
  * 0 <= count <= 4096 (0 enqueues nothing), 1 <= M, N <= 32768, min(M, N) <= 16384,
- * 1 <= steps <= 64, eps >= 0; ld >= N, and matrices of a stack do not overlap. X is kept in two
- * FP16 pieces (22 bits) from step to step; the factors of the products are one piece (11 bits)
+ * 1 <= steps <= 64, eps >= 0; ld >= N, and each matrix of a stack begins behind the last element
+ * of the one before. X is kept in two FP16 pieces (22 bits) from step to step; the factors of the products are one piece (11 bits)
  * for bfloat16 and two for the other types; sums are FP32. The first pieces are of values times
  * 2^13 (X), 2^12 (A) and 2^10 (the polynomial b A + c A A), the second of what these leave, times
  * 2^11 more. So 22 bits are kept of entries from 2^-27 (X), 2^-26 and 2^-24 on, 11 bits of one
