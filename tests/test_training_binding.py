@@ -22,4 +22,4 @@ def test_a_stack_whose_rows_alternate():
     assert _layout(t, "G") == (6, 3, 8, 8, 24)
     with pytest.raises(ValueError, match="begin behind the last element of the one before"):
         _layout(t.transpose(0, 1), "G")
-    assert _layout(t[:1].transpose(0, 1)[:1], "G") == (1, 1, 8, 8, 0)
+    assert _layout(t[:1].transpose(0, 1)[:1], "G") == (1, 1, 8, 24, 0)  # the pitch of one row counts for nothing
