@@ -2,7 +2,9 @@
 output head, with its gradients, and orthogonalised updates.
 
 Like the rest of the binding this marshals arguments only; the definitions and the limits are
-those of ``sgemm_cross_entropy`` and ``sgemm_orthogonalize`` in the C header.
+those of ``sgemm_cross_entropy`` and ``sgemm_orthogonalize`` in the C header. As everywhere in the
+binding, results are not part of autograd's graph, also where inputs require gradients: a loss that
+is to be differentiated needs cross_entropy_grad, whose gradients the caller passes on.
 
     loss, losses, lse = sg.cross_entropy(x, weight, target)             # x: T x D, weight: V x D
     loss, losses, lse, dx, dweight = sg.cross_entropy_grad(x, weight, target)
@@ -106,7 +108,7 @@ def cross_entropy(x, weight, target, token_weights=None, stream=None) -> CrossEn
     V x D (float32, bfloat16 or float16; rows may be slices of wider ones), target T integers.
     Tokens whose target is not in 0 .. V - 1 do not count; of them nothing is read.
     ``token_weights`` (T, float32): each token's share of ``loss``; without, one over the number
-    of tokens that count."""
+    of tokens that count. The results are values alone, without a graph for ``backward``."""
     return CrossEntropy(*_cross_entropy(x, weight, target, token_weights, False, False, None, None,
                                         stream)[:3])
 
@@ -115,7 +117,7 @@ def cross_entropy_grad(x, weight, target, token_weights=None, need_dx=True, need
                        dx=None, dweight=None, stream=None) -> CrossEntropyGrad:
     """cross_entropy and the gradients of its ``loss`` with respect to x and weight, written to
     ``dx`` and ``dweight`` where they are given. With need_dx or need_dweight false that gradient
-    is neither computed nor written."""
+    is neither computed nor written. ``loss`` has no graph for ``backward``: the gradients are here."""
     for name, t, need in (("dx", dx, need_dx), ("dweight", dweight, need_dweight)):
         if t is not None and not need:
             raise ValueError(f"{name} is given but not needed")

@@ -497,17 +497,22 @@ typedef struct sgemm_ce {
  *
  * 0 <= T <= 1048576, 1 <= D <= 65536, 1 <= V <= 1048576. T = 0 gives a loss of zero and a
  * dweight of zeros. Sums are FP32; with bfloat16 and float16, g is rounded twice to that type
- * (as exponentials relative to a maximum, and as g over the largest |c|) and each gradient
- * once. float32 operands are multiplied as three bfloat16 pieces (all 24 bits; an infinity
- * counts as a NaN). A counted token with an infinity or NaN may make all of dweight NaN, as
- * the definition does. Results are bitwise reproducible: the order of sums depends on the
- * sizes and on which tokens count. Outputs must not overlap the inputs or each other (an array
- * counts from its first to its last element, with what lies between its rows). token_weights
- * are assumed finite.
+ * (as exponentials relative to a maximum, and as g over the largest |c|), the target's once, and
+ * each gradient once. float16 holds g over the largest |c| times 2^14: with 11 bits from 2^-28 on,
+ * in steps of 2^-38 below, so that a token whose |c| is below 2^-16 of the largest loses bits of
+ * its dx (up to 1 % at 2^-24). float32 operands are multiplied as three bfloat16 pieces (all 24 bits; an infinity
+ * counts as a NaN). A token with a logit of +infinity or NaN has NaN for its loss, lse and dx, and
+ * may make all of dweight NaN, as the definition does; logits of -infinity have no weight.
+ * Results are bitwise reproducible: the order of sums depends on the sizes and on which tokens
+ * count. Outputs must not overlap the inputs or each other (an array counts from its first to its
+ * last element, with what lies between its rows). token_weights are assumed finite.
  *
- * Workspace comes from the library's pool: the counted rows of x; for gradients 2 bytes
- * (float32: 10) for each logit of a chunk of tokens, 2 GiB at most or 256 tokens, and, where
- * that makes several chunks, V x D floats. Everything is stream-ordered; the call can be
+ * Workspace comes from the library's pool: T rows of x (D rounded up to 64 elements, 2 bytes each,
+ * float32: 6); the same of V rows for float32 weights and those of 16 bits that are not read in
+ * place; for gradients 2 bytes (float32: 10) for each logit of a chunk of tokens, 2 GiB at most or
+ * 256 tokens; where the reduction of dx is split, a chunk of tokens times D floats for each part
+ * (1024 classes or more, and not more parts than SMs); where there are several chunks, V x D floats for the sums of
+ * dweight; 8 bytes for 64 (or 128) logits of a chunk. Everything is stream-ordered; the call can be
  * captured into a CUDA graph after one call of the same kind outside.
  */
 SGEMM_API int sgemm_cross_entropy(const sgemm_ce* args, void* stream);
@@ -524,7 +529,8 @@ SGEMM_API int sgemm_cross_entropy(const sgemm_ce* args, void* stream);
  * and the last X is written to `out`. G and out are device arrays of type `dtype`
  * (SGEMM_FLOAT32, SGEMM_BFLOAT16 or SGEMM_FLOAT16): element (i, j) of matrix e at
  * e * stride + i * ld + j. They may be the same array with the same pitch and stride, else they
- * must not overlap (from the first to the last element). coefficients: 3 * steps floats on the HOST, a, b, c of each step.
+ * must not overlap (from the first to the last element). coefficients: 3 * steps floats on the
+ * HOST, a, b, c of each step.
  *
  * 0 <= count <= 4096 (0 enqueues nothing), 1 <= M, N <= 32768, min(M, N) <= 16384,
  * 1 <= steps <= 64, eps >= 0; ld >= N, and each matrix of a stack begins behind the last element
