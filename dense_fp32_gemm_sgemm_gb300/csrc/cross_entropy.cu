@@ -43,7 +43,10 @@ constexpr long long CE_CHUNK_BYTES = 1ll << 31;
 constexpr int FINISH_THREADS = 256;
 constexpr int PLAN_THREADS = 1024;
 constexpr int PLAN_ITEMS = 4;
-constexpr int SELECT_TOKENS = 1024;  // up to which ce_select does the work of both
+// Up to which ce_select does the work of both, in which every CTA goes through all targets. Loss of T x 512
+// by 1000 on the device: T = 64 22.7 us against 24.7 with two launches, 512 24.7 and 26.7, 1024 28 and 27,
+// 2048 49 and 38, 8192 289 and 68.
+constexpr int SELECT_TOKENS = 1024;
 constexpr long long MAX_TMA_PITCH = 1ll << 37;  // elements; a map's pitch ends at 2^40 bytes
 constexpr float LOG2E = 1.4426950408889634f;
 
@@ -1012,6 +1015,7 @@ cudaError_t run(const sgemm_ce& a, const DeviceInfo& info, int dev, cudaStream_t
         p.batch = 1;
         p.splits = splits;
         p.dyn = 1;
+        // 8192 x 4096 by 65536 takes 7.0 ms with 8 tile rows together, 7.2 with 2, 7.7 with 32
         p.group = 8;
         p.b_mn = 1;
         set_planes(p, planes);
@@ -1043,6 +1047,7 @@ cudaError_t run(const sgemm_ce& a, const DeviceInfo& info, int dev, cudaStream_t
         p.K = chunk;
         p.batch = p.splits = 1;
         p.dyn = 2;
+        // the same call takes 7.0 ms with 4, 7.3 with 1, 7.1 with 16
         p.group = 4;
         p.a_mn = p.b_mn = 1;
         set_planes(p, planes);

@@ -478,7 +478,7 @@ cudaError_t iterate(const Call& a, const DeviceInfo& info, __half* (&x)[2], __ha
         for (int j = 0; j < 3; ++j) {
             p[j].batch = a.count;
             p[j].splits = 1;
-            p[j].group = 8;
+            p[j].group = 8;  // 6144 x 8192, bfloat16: 3.50 ms, with 2 3.61, with 32 3.57
             set_products(p[j], PIECES);
         }
         p[0].planes_a = p[0].planes_b = 2;
