@@ -21,6 +21,12 @@
 // large as the others of 256 x 256 or 256 x 1024 is good to 1 to 5e-7, 1e-7 to 3 to 5e-6 (without the 2^11
 // 0.5 to 1e-4 and 0.4 to 1e-2; FP32 0.4 to 2e-6).
 //
+// With two pieces, E = A - I/2 is stored in A's place, and the polynomial is c E E + (b + c) E + (b/2 + c/4) I.
+// Once singular values are near one, A's diagonal holds most of its size, and a sum of A A one product, its
+// square, from which the accumulator cuts all others: 2^-22 of it, which the later steps multiply by up to 20
+// (64 x 999 of normal entries: 3.4e-6, with E 1.7e-6; 71 x 6384 with strong directions 1.4 and 0.6e-6). One
+// half is between the squares of 0 and 1.2; with zero or one 1.3 to 4 times the error in simulations.
+//
 // Measured: 6144 x 8192, bfloat16, 4.1 ms (1.41 PFLOP/s of what symmetric products cannot do without);
 // 4096 x 4096 1.07 ms, where whole rounds of 76 units take 1.15 of the work (gram and polynomial 2 for
 // 1.8, update 4 for 3.4), the update's second term and stores 11 % and the ends of 15 phases some 8 us
@@ -226,6 +232,7 @@ struct NsChain {
     static constexpr int PROBLEMS = 6;
     static constexpr int PLANES = PIECES;
     static constexpr bool CHAIN = true;
+    static constexpr float MIDDLE = PIECES == 2 ? 0.5f : 0.f;  // see above
     struct Params {
         FactorMaps gram, poly;
         FactorMaps x[2];  // X before a step and after it, by the step's parity; two pieces
@@ -298,12 +305,14 @@ struct NsChain {
         const bool last = type == 2 && step == p.steps - 1;
         const int rows_n = type == 2 ? p.M : p.r, cols_n = type == 2 ? p.N : p.r;
         if (row >= rows_n || col >= cols_n) return;
-        float f, h = 0.f;
+        float f, h = 0.f, unit = 0.f;  // unit: times the identity
         if (type == 0) {
             f = UP_A / (UP_X * UP_X);
+            unit = -MIDDLE * UP_A;
         } else if (type == 1) {
             f = c[2] * (UP_P / (UP_A * UP_A));
-            h = c[1] * (UP_P / UP_A);
+            h = (c[1] + 2.f * MIDDLE * c[2]) * (UP_P / UP_A);
+            unit = (c[1] + MIDDLE * c[2]) * MIDDLE * UP_P;
         } else {
             f = last ? 1.f / (UP_P * UP_X) : 1.f / UP_P;
             h = last ? c[0] / UP_X : c[0];
@@ -337,6 +346,11 @@ struct NsChain {
                 }
                 turn(s);
             }
+        }
+        if (MIDDLE != 0.f && type != 2 && row + 32 > col && row < col + COLS) {
+            const int diagonal = row + lane - col;
+#pragma unroll
+            for (int j = 0; j < COLS; ++j) s[j] = j == diagonal ? s[j] + unit : s[j];
         }
         if (!last)
             store_pieces(t, type, row, col, cols_n, s);
@@ -459,12 +473,11 @@ cudaError_t iterate(const Call& a, const DeviceInfo& info, __half* (&x)[2], __ha
     g.err = info.error_word;
     // 16-bit results: 128 MMAs at most between two additions in FP32, which cut off 2^-16 of a sum of one
     // sign.
-    // float32 (MMAs of the first pieces): 12, or 4 where the smaller side is below 512 and FP32 arithmetic
-    // itself is good to 1 to 2e-6 (350 x 542: 3.2e-6 with 12, 2.4e-6 with 8, 1.5e-6 with 4, FP32 2.1e-6;
-    // 64 x 20000 takes 980 us instead of 755; 1001 x 2731: 3.2e-6 with 36, 1.3e-6 with 12, 0.7e-6 with 4, FP32
-    // 2.5e-6, 367, 384 and 430 us), or 24 from 2048 on (2304 x 2560: 0.9e-6 against 0.6e-6 with 12 and FP32's
-    // 2.6e-6; 6144 x 8192 11.8 and 12.4 ms).
-    g.seg_steps = a.dtype != SGEMM_FLOAT32 ? 32 : r < 512 ? 1 : r < 2048 ? 3 : 6;
+    // float32 (MMAs of the first pieces): 8 where the smaller side is below 512 and FP32 arithmetic itself is
+    // good to 1 to 2e-6 (150 x 1408: 1.2e-6, with 4 0.8, with 12 1.7, FP32 1.4; 64 x 20000 769 us, with 4 980);
+    // 12 below 2048 (1210 x 5480: 1.5e-6, with 8 1.1, with 16 2.0, FP32 2.7; 550 us, 543 and 532); then 24
+    // (2102 x 3552: 1.9e-6, with 12 1.1, FP32 2.5; 6144 x 8192 12.1 and 12.5 ms).
+    g.seg_steps = a.dtype != SGEMM_FLOAT32 ? 32 : r < 512 ? 2 : r < 2048 ? 3 : 6;
     // operand maps: k contiguous, or the other index
     auto x_operand = [&](CUtensorMap& m, int i, bool mn, int rows_of_cta) {
         return hg::encode_operand(&m, x[i], false, a.N, a.M, Np, 2 * a.count, x_plane,

@@ -537,7 +537,7 @@ SGEMM_API int sgemm_cross_entropy(const sgemm_ce* args, void* stream);
  * of the one before. X is kept in two FP16 pieces (22 bits) from step to step; the factors of the products are one piece (11 bits)
  * for bfloat16 and two for the other types; sums are FP32. The first pieces are of values times
  * 2^13 (X), 2^12 (A) and 2^10 (the polynomial b A + c A A), the second of what these leave, times
- * 2^11 more. So 22 bits are kept of entries from 2^-27 (X), 2^-26 and 2^-24 on, 11 bits of one
+ * 2^11 more (of A - I/2 in A's place). So 22 bits are kept of entries from 2^-27 (X), 2^-26 and 2^-24 on, 11 bits of one
  * piece from 2^-26 (A) and 2^-24 on; below that steps are 2^-48, 2^-47 and 2^-45, or 2^-36 and
  * 2^-34: float32 rows or columns down to some 1e-6 of the others' size are as near as FP32
  * arithmetic, smaller ones lose a bit for each factor of two. Entries of X must stay below 8,
