@@ -28,8 +28,8 @@
 // float32 operands are three bfloat16 planes (24 bits), of which six products are taken; the
 // logits are then kept in FP32 and g in three planes.
 //
-// Measured (8192 x 4096 by 65536, bfloat16): 8.03 ms, 1.64 PFLOP/s, where the power cap holds cuBLAS's
-// products at 1.71 to 1.77; 2.3 + 0.37 + 4.4 ms for the three passes with the clock at 1.9 GHz.
+// Measured (8192 x 4096 by 65536, bfloat16): 8.0 to 8.3 ms, 1.59 to 1.65 PFLOP/s, where the power cap holds
+// cuBLAS at 1.71 to 1.77; 2.3 + 0.37 + 4.4 ms for the three passes with the clock at 1.9 GHz.
 #include <algorithm>
 #include <cstring>
 

@@ -27,8 +27,8 @@
 // (64 x 999 of normal entries: 3.4e-6, with E 1.7e-6; 71 x 6384 with strong directions 1.4 and 0.6e-6). One
 // half is between the squares of 0 and 1.2; with zero or one 1.3 to 4 times the error in simulations.
 //
-// Measured: 6144 x 8192, bfloat16, 4.1 ms (1.41 PFLOP/s of what symmetric products cannot do without);
-// 4096 x 4096 1.07 ms, where whole rounds of 76 units take 1.15 of the work (gram and polynomial 2 for
+// Measured: 6144 x 8192, bfloat16, 4.1 to 4.2 ms (1.4 PFLOP/s of what symmetric products cannot do without);
+// 4096 x 4096 1.08 to 1.11 ms, where whole rounds of 76 units take 1.15 of the work (gram and polynomial 2 for
 // 1.8, update 4 for 3.4), the update's second term and stores 11 % and the ends of 15 phases some 8 us
 // each. A finer order, in which a unit waits for its own blocks of rows alone, brought nothing.
 #include <algorithm>
