@@ -21,9 +21,9 @@
 // takes 512 cycles): short segments are for results in FP32, long ones let a long epilogue pass unnoticed.
 //
 // Where two planes share a stage (Ring), the second is what the first leaves of a value, times 2^11: an FP16
-// piece of it then has its 11 bits down to 2^-38 of the first's unit instead of 2^-14. Both products that
-// have a second plane are summed in accumulators of their own, a unit's whole reduction in one, and added with
-// 2^-11 to the unit's last segment; what these cut off is 2^-11 of the other's.
+// piece of it then is a normal number down to 2^-25 in the first one's scale instead of 2^-14, with steps of
+// 2^-35 below. Both products that have a second plane are summed in accumulators of their own, a unit's whole
+// reduction in one, and added with 2^-11 to the unit's last segment; what these cut off is 2^-11 of the other's.
 //
 // Measured: 522 cycles a stage of 256 columns, where the MMAs take 512 and 32 KiB arrive at 62 bytes
 // a cycle and SM; the tensor pipe is active 88 to 90 % of the time in products of 2048 x 4096 by 16384
@@ -435,10 +435,9 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 // called by each epilogue warp at the beginning of a unit (to load what it will need) and with its
 // sums: lane l holds row `row` + l, columns col .. col + BN / 2.
 // EPI::PROBLEMS: of the launch at most. EPI::PLANES: staged together (see Ring); with two, every unit has
-// some of the reduction. EPI::CHAIN: units
-// are claimed in order, and one waits until all units of the phase before that belong to the same
-// product have been stored. Every earlier unit was claimed by a CTA that runs, and waits for still
-// earlier ones only, so that all waits end however many CTAs the GPU runs at a time.
+// some of the reduction. EPI::CHAIN: units are claimed in order, and one waits until all units of the phase
+// before that belong to the same product have been stored. Every earlier unit was claimed by a CTA that runs,
+// and waits for still earlier ones only, so that all waits end however many CTAs the GPU runs at a time.
 template <class EPI>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     half_gemm_kernel(const __grid_constant__ Args<EPI::PROBLEMS> g,

@@ -495,25 +495,25 @@ typedef struct sgemm_ce {
  *
  * losses, lse and dx are zero for tokens that do not count, and losses does not include c.
  *
- * 0 <= T <= 1048576, 1 <= D <= 65536, 1 <= V <= 1048576. T = 0 gives a loss of zero and a
- * dweight of zeros. Sums are FP32; with bfloat16 and float16, g is rounded twice to that type
- * (as exponentials relative to a maximum, and as g over the largest |c|), the target's once, and
- * each gradient once. float16 holds g over the largest |c| times 2^14: with 11 bits from 2^-28 on,
- * in steps of 2^-38 below, so that a token whose |c| is below 2^-16 of the largest loses bits of
- * its dx (up to 1 % at 2^-24). float32 operands are multiplied as three bfloat16 pieces (all 24 bits; an infinity
- * counts as a NaN). A token with a logit of +infinity or NaN has NaN for its loss, lse and dx, and
- * may make all of dweight NaN, as the definition does; logits of -infinity have no weight.
- * Results are bitwise reproducible: the order of sums depends on the sizes and on which tokens
- * count. Outputs must not overlap the inputs or each other (an array counts from its first to its
- * last element, with what lies between its rows). token_weights are assumed finite.
+ * 0 <= T <= 1048576, 1 <= D <= 65536, 1 <= V <= 1048576. T = 0 gives a loss of zero and a dweight
+ * of zeros. Sums are FP32; with bfloat16 and float16, g is rounded twice to that type (as
+ * exponentials relative to a maximum, and as g over the largest |c|), the target's once, and each
+ * gradient once. float16 holds g over the largest |c| times 2^14: with 11 bits from 2^-28 on, in
+ * steps of 2^-38 below, so that a token whose |c| is below 2^-16 of the largest loses bits of its
+ * dx (up to 1 % at 2^-24). float32 operands are multiplied as three bfloat16 pieces (all 24 bits;
+ * an infinity counts as a NaN). A token with a logit of +infinity or NaN has NaN for its loss, lse
+ * and dx, and may make all of dweight NaN, as the definition does; logits of -infinity have no
+ * weight. Results are bitwise reproducible: the order of sums depends on the sizes and on which
+ * tokens count. Outputs must not overlap the inputs or each other (an array counts from its first
+ * to its last element, with what lies between its rows). token_weights are assumed finite.
  *
  * Workspace comes from the library's pool: T rows of x (D rounded up to 64 elements, 2 bytes each,
  * float32: 6); the same of V rows for float32 weights and those of 16 bits that are not read in
  * place; for gradients 2 bytes (float32: 10) for each logit of a chunk of tokens, 2 GiB at most or
  * 256 tokens; where the reduction of dx is split, a chunk of tokens times D floats for each part
- * (1024 classes or more, and not more parts than SMs); where there are several chunks, V x D floats for the sums of
- * dweight; 8 bytes for 64 (or 128) logits of a chunk. Everything is stream-ordered; the call can be
- * captured into a CUDA graph after one call of the same kind outside.
+ * (1024 classes or more, and not more parts than SMs); where there are several chunks, V x D
+ * floats for the sums of dweight; 8 bytes for 64 (or 128) logits of a chunk. Everything is stream-
+ * ordered; the call can be captured into a CUDA graph after one call of the same kind outside.
  */
 SGEMM_API int sgemm_cross_entropy(const sgemm_ce* args, void* stream);
 
@@ -532,26 +532,27 @@ SGEMM_API int sgemm_cross_entropy(const sgemm_ce* args, void* stream);
  * must not overlap (from the first to the last element). coefficients: 3 * steps floats on the
  * HOST, a, b, c of each step.
  *
- * 0 <= count <= 4096 (0 enqueues nothing), 1 <= M, N <= 32768, min(M, N) <= 16384,
- * 1 <= steps <= 64, eps >= 0; ld >= N, and each matrix of a stack begins behind the last element
- * of the one before. X is kept in two FP16 pieces (22 bits) from step to step; the factors of the products are one piece (11 bits)
- * for bfloat16 and two for the other types; sums are FP32. The first pieces are of values times
- * 2^13 (X), 2^12 (A) and 2^10 (the polynomial b A + c A A), the second of what these leave, times
- * 2^11 more (of A - I/2 in A's place). So 22 bits are kept of entries from 2^-27 (X), 2^-26 and 2^-24 on, 11 bits of one
- * piece from 2^-26 (A) and 2^-24 on; below that steps are 2^-48, 2^-47 and 2^-45, or 2^-36 and
- * 2^-34: float32 rows or columns down to some 1e-6 of the others' size are as near as FP32
- * arithmetic, smaller ones lose a bit for each factor of two. Entries of X must stay below 8,
- * of A below 16, of the polynomial below 64 in size; a larger one is an infinity or NaN in all
- * that follows from it. As |X| <= 1 at first, that holds for any coefficients meant to bring
- * singular values near one. A matrix with an infinity or NaN gives
- * NaN; the others of its stack are not touched by it. A zero matrix gives zeros (with eps = 0, NaN).
- * Results are bitwise reproducible, and a matrix's do not depend on the others of its stack (but
- * on their number, which decides how sums are split).
+ * 0 <= count <= 4096 (0 enqueues nothing), 1 <= M, N <= 32768, min(M, N) <= 16384, 1 <= steps <=
+ * 64, eps >= 0; ld >= N, and each matrix of a stack begins behind the last element of the one
+ * before. X is kept in two FP16 pieces (22 bits) from step to step; the factors of the products
+ * are one piece (11 bits) for bfloat16 and two for the other types; sums are FP32. The first
+ * pieces are of values times 2^13 (X), 2^12 (A) and 2^10 (the polynomial b A + c A A), the second
+ * of what these leave, times 2^11 more (of A - I/2 in A's place). So 22 bits are kept of entries
+ * from 2^-27 (X), 2^-26 and 2^-24 on, 11 bits of one piece from 2^-26 (A) and 2^-24 on; below that
+ * steps are 2^-48, 2^-47 and 2^-45, or 2^-36 and 2^-34: float32 rows or columns whose entries of
+ * X are above some 2^-32 (1e-6 of the others in 256 x 256, 1e-5 in 4096 x 4096) are as near as
+ * FP32 arithmetic, smaller ones lose a bit for each factor of
+ * two. Entries of X must stay below 8, of A below 16, of the polynomial below 64 in size; a larger
+ * one is an infinity or NaN in all that follows from it. As |X| <= 1 at first, that holds for any
+ * coefficients meant to bring singular values near one. A matrix with an infinity or NaN gives
+ * NaN; the others of its stack are not touched by it. A zero matrix gives zeros (with eps = 0,
+ * NaN). Results are bitwise reproducible, and a matrix's do not depend on the others of its stack
+ * (but on their number, which decides how sums are split).
  *
- * Workspace comes from the library's pool: 8 bytes for each element (one step: 4) and, with
- * r = min(M, N), 4 (bfloat16) or 8 times r * r for each matrix, rows rounded up to 64 elements.
- * Three launches. Everything is stream-ordered; the call can be
- * captured into a CUDA graph after one call of the same kind outside.
+ * Workspace comes from the library's pool: 8 bytes for each element (one step: 4) and, with r =
+ * min(M, N), 4 (bfloat16) or 8 times r * r for each matrix, rows rounded up to 64 elements. Three
+ * launches. Everything is stream-ordered; the call can be captured into a CUDA graph after one
+ * call of the same kind outside.
  */
 SGEMM_API int sgemm_orthogonalize(const void* G, int dtype, int count, int M, int N, long long ldg,
                                   long long stride_g, void* out, long long ldo,
